@@ -20,9 +20,11 @@ F32, BF16 = 0, 1
 
 OK = 0
 ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_ALIGNMENT, ERR_WORKSPACE, ERR_LAUNCH, ERR_DEVICE_TIMEOUT = -1, -2, -3, -4, -5, -6
+ERR_CACHE_RANGE = -7
 
 # Every entry point the header declares, with its ctypes signature.
 _VP, _I, _SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+_LL, _F, _D = ctypes.c_longlong, ctypes.c_float, ctypes.c_double
 SIGNATURES = {
     "gsdpa_workspace_bytes": (_SZ, [_I] * 10),
     "gated_sdpa_fwd": (_I, [_VP] * 7 + [_I] * 10 + [_VP, _SZ, _VP]),
@@ -42,6 +44,14 @@ SIGNATURES = {
     "gsdpa_wait_self_test": (_I, [_VP]),
     "gated_sdpa_decode_noalloc": (_I, [_VP] * 7 + [_I] * 7 + [_VP]),
     "gsdpa_decode_noalloc_max_scratch": (_SZ, []),
+    "gsdpa_rope_init": (_I, [_VP, _I, _I, _D, _I] + [_D] * 5),
+    "gsdpa_rope_init_freqs": (_I, [_VP, _I, _I, _VP, _D]),
+    "gsdpa_qk_norm_rope": (_I, [_VP] * 7 + [_LL] * 4 + [_I] * 6 + [_F, _VP, _I, _VP]),
+    "gsdpa_qk_norm_rope_bwd_workspace_bytes": (_SZ, [_I] * 4),
+    "gsdpa_qk_norm_rope_bwd": (_I, [_VP] * 11 + [_LL] * 6 + [_I] * 6 + [_F, _VP, _I, _VP, _SZ, _VP]),
+    "gsdpa_cache8_append": (_I, [_VP] * 3 + [_LL] * 2 + [_VP] * 2 + [_I, _VP]),
+    "gsdpa_cache8_workspace_bytes": (_SZ, [_VP] + [_I] * 4),
+    "gated_sdpa_cache8": (_I, [_VP] * 7 + [_I] * 4 + [_VP, _SZ, _VP]),
 }
 
 _lock = threading.Lock()
@@ -492,3 +502,304 @@ def decode_noalloc(X, Q, K, V, W_g=None, *, gate="elementwise", out=None, sink=N
     if st != OK:
         raise GsdpaError(st, "gated_sdpa_decode_noalloc")
     return out, sink
+
+
+# ---- per-head norm and rotary positions (gsdpa_qk_norm_rope), and the 8-bit K/V cache (gsdpa_cache8)
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "parts": 3}
+
+
+class _RopePlan(ctypes.Structure):
+    _fields_ = [("rotary_dim", _I), ("layout", _I), ("attn_scale", _F), ("reserved", _I),
+                ("turn", ctypes.c_ulonglong * 64)]
+
+
+class Rope:
+    """The plan of the rotary positions (gsdpa_rope), made once on the host.
+
+    rotary_dim: columns of each head that are rotated, a multiple of 16; layout
+    "half" (pairs i, i + rotary_dim / 2) or "interleaved" (2i, 2i + 1). Frequencies
+    theta^(-2i / rotary_dim) under ``scaling``: "none", "linear" (divided by
+    factor), "base" (theta enlarged) or "parts" (slow pairs divided by factor,
+    those that turn more than beta_fast times in orig_len kept); or ``inv_freq``,
+    rotary_dim / 2 of the caller's own. attn_scale multiplies cosine and sine
+    (None: 1, or 0.1 ln(factor) + 1 with "parts")."""
+
+    def __init__(self, rotary_dim, *, layout="half", theta=10000.0, scaling="none", factor=1.0, orig_len=0,
+                 beta_fast=32.0, beta_slow=1.0, attn_scale=None, inv_freq=None):
+        self.plan = _RopePlan()
+        self.ref = ctypes.addressof(self.plan)
+        if attn_scale is not None and attn_scale == 0:
+            raise ValueError("attn_scale must not be 0")
+        if inv_freq is not None:
+            w = [float(x) for x in inv_freq]
+            if len(w) != rotary_dim // 2:
+                raise ValueError(f"inv_freq has {len(w)} frequencies, rotary_dim = {rotary_dim} needs {rotary_dim // 2}")
+            st = load().gsdpa_rope_init_freqs(self.ref, rotary_dim, ROPE_LAYOUTS[layout], (_D * len(w))(*w),
+                                              1.0 if attn_scale is None else attn_scale)
+            where = "gsdpa_rope_init_freqs"
+        else:
+            st = load().gsdpa_rope_init(self.ref, rotary_dim, ROPE_LAYOUTS[layout], theta, ROPE_SCALINGS[scaling],
+                                        factor, orig_len, beta_fast, beta_slow, attn_scale or 0.0)
+            where = "gsdpa_rope_init"
+        if st != OK:
+            raise GsdpaError(int(st), where)
+
+
+def _head_rows(t, name, shape, dtype, device):
+    """The row length in elements of t, [B, L, H, d_k] with contiguous heads and
+    evenly spaced token rows (a contiguous tensor, or a column block of one)."""
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if not t.is_cuda or t.device != device:
+        raise ValueError(f"{name} must be a CUDA tensor on {device}, not on {t.device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, the problem needs {tuple(shape)}")
+    B, L, H, d = shape
+    s0, s1, s2, s3 = t.stride()
+    ld = s1 if L > 1 else (s0 if B > 1 else H * d)
+    if (s3 != 1 and d > 1) or (H > 1 and s2 != d) or (L > 1 and B > 1 and s0 != L * ld):
+        raise ValueError(f"{name}: heads must be contiguous and token rows evenly spaced (strides {tuple(t.stride())})")
+    if ld < H * d and B * L > 1:
+        raise ValueError(f"{name}: its token rows overlap (strides {tuple(t.stride())})")
+    return ld
+
+
+def _vector(t, name, n, dtype, device):
+    """The address of an optional contiguous vector of n elements."""
+    if t is None:
+        return None
+    _expect(t, name, n, dtype, device)
+    return t.data_ptr()
+
+
+_DTYPES = {}
+
+
+def _dtype_code(dt):
+    if not _DTYPES:
+        import torch
+        _DTYPES.update({torch.bfloat16: BF16, torch.float32: F32})
+    if dt not in _DTYPES:
+        raise TypeError(f"unsupported dtype {dt}")
+    return _DTYPES[dt]
+
+
+def _qk_dims(Q, K):
+    if Q.dim() != 4 or K.dim() != 4:
+        raise ValueError("Q and K must be 4-D: [B, L, H, d_k]")
+    B, L, H_q, d_k = Q.shape
+    if K.shape[0] != B or K.shape[1] != L or K.shape[3] != d_k:
+        raise ValueError(f"K {tuple(K.shape)} must be [B={B}, L={L}, H_kv, d_k={d_k}]")
+    return B, L, H_q, K.shape[2], d_k
+
+
+def qk_norm_rope(Q, K, *, gamma_q=None, gamma_k=None, norm=True, eps=1e-6, rope=None, positions=None, out_q=None,
+                 out_k=None, stream=None):
+    """Per-head RMS norm of Q [B, L, H_q, d_k] and K [B, L, H_kv, d_k] and their
+    rotary positions in one pass (gsdpa_qk_norm_rope); float32 or bfloat16.
+
+    Q and K (and out_q, out_k) may be column blocks of a packed projection's
+    output, and out_q, out_k may be Q, K themselves. gamma_q, gamma_k [d_k] or
+    None for 1; ``rope`` a Rope or None for no rotation; positions int32 [B, L] or
+    None for 0 .. L - 1. Returns (Q', K')."""
+    import torch
+    dt, dev = Q.dtype, Q.device
+    code = _dtype_code(dt)
+    B, L, H_q, H_kv, d_k = _qk_dims(Q, K)
+    ld_q, ld_k = _head_rows(Q, "Q", Q.shape, dt, dev), _head_rows(K, "K", K.shape, dt, dev)
+    if out_q is None:
+        out_q, ld_qo = torch.empty((B, L, H_q, d_k), dtype=dt, device=dev), H_q * d_k
+    else:
+        ld_qo = _head_rows(out_q, "out_q", Q.shape, dt, dev)
+    if out_k is None:
+        out_k, ld_ko = torch.empty((B, L, H_kv, d_k), dtype=dt, device=dev), H_kv * d_k
+    else:
+        ld_ko = _head_rows(out_k, "out_k", K.shape, dt, dev)
+    gq, gk = _vector(gamma_q, "gamma_q", d_k, dt, dev), _vector(gamma_k, "gamma_k", d_k, dt, dev)
+    pos = _vector(positions, "positions", B * L, torch.int32, dev)
+    s = _stream(stream, dev)
+    st = load().gsdpa_qk_norm_rope(Q.data_ptr(), K.data_ptr(), gq, gk, pos, out_q.data_ptr(), out_k.data_ptr(), ld_q,
+                                   ld_k, ld_qo, ld_ko, B, L, H_q, H_kv, d_k, 1 if norm else 0, eps,
+                                   None if rope is None else rope.ref, code, s.cuda_stream)
+    if st != OK:
+        raise GsdpaError(st, "gsdpa_qk_norm_rope")
+    return out_q, out_k
+
+
+def qk_norm_rope_bwd_workspace_bytes(B, L, d_k, norm=True) -> int:
+    n = load().gsdpa_qk_norm_rope_bwd_workspace_bytes(B, L, d_k, 1 if norm else 0)
+    if n == ctypes.c_size_t(-1).value:
+        raise GsdpaError(ERR_INVALID_ARG, "gsdpa_qk_norm_rope_bwd_workspace_bytes")
+    return n
+
+
+def qk_norm_rope_bwd(Q, K, dQo, dKo, *, gamma_q=None, gamma_k=None, norm=True, eps=1e-6, rope=None, positions=None,
+                     out_dq=None, out_dk=None, workspace=None, stream=None):
+    """Backward of qk_norm_rope: from dQo, dKo (gradients of its outputs) and its
+    inputs, a dict with dQ, dK and, with the norm, dgamma_q and dgamma_k (with
+    respect to a gamma of 1 where none was given). out_dq, out_dk may be dQo, dKo
+    or column blocks of the packed projection's gradient."""
+    import torch
+    dt, dev = Q.dtype, Q.device
+    code = _dtype_code(dt)
+    B, L, H_q, H_kv, d_k = _qk_dims(Q, K)
+    ld_q, ld_k = _head_rows(Q, "Q", Q.shape, dt, dev), _head_rows(K, "K", K.shape, dt, dev)
+    ld_dqo, ld_dko = _head_rows(dQo, "dQo", Q.shape, dt, dev), _head_rows(dKo, "dKo", K.shape, dt, dev)
+    if out_dq is None:
+        out_dq, ld_dq = torch.empty((B, L, H_q, d_k), dtype=dt, device=dev), H_q * d_k
+    else:
+        ld_dq = _head_rows(out_dq, "out_dq", Q.shape, dt, dev)
+    if out_dk is None:
+        out_dk, ld_dk = torch.empty((B, L, H_kv, d_k), dtype=dt, device=dev), H_kv * d_k
+    else:
+        ld_dk = _head_rows(out_dk, "out_dk", K.shape, dt, dev)
+    gq, gk = _vector(gamma_q, "gamma_q", d_k, dt, dev), _vector(gamma_k, "gamma_k", d_k, dt, dev)
+    pos = _vector(positions, "positions", B * L, torch.int32, dev)
+    out = {"dQ": out_dq, "dK": out_dk}
+    need, dgq, dgk = 0, None, None
+    if norm:
+        # (no rows: the library enqueues nothing, and the sums are zero)
+        make = torch.empty if B * L > 0 else torch.zeros
+        out["dgamma_q"], out["dgamma_k"] = make(d_k, dtype=dt, device=dev), make(d_k, dtype=dt, device=dev)
+        dgq, dgk = out["dgamma_q"].data_ptr(), out["dgamma_k"].data_ptr()
+        need = qk_norm_rope_bwd_workspace_bytes(B, L, d_k)
+    workspace, ws_bytes = _workspace(workspace, need, dev)
+    s = _stream(stream, dev)
+    st = load().gsdpa_qk_norm_rope_bwd(
+        Q.data_ptr(), K.data_ptr(), gq, gk, pos, dQo.data_ptr(), dKo.data_ptr(), out_dq.data_ptr(), out_dk.data_ptr(),
+        dgq, dgk, ld_q, ld_k, ld_dqo, ld_dko, ld_dq, ld_dk, B, L, H_q, H_kv, d_k, 1 if norm else 0, eps,
+        None if rope is None else rope.ref, code, _ptr(workspace), ws_bytes, s.cuda_stream)
+    if st != OK:
+        raise GsdpaError(st, "gsdpa_qk_norm_rope_bwd")
+    return out
+
+
+CACHE_BLOCK = 64   # tokens that share a scale
+CACHE_KINDS = {"int8": 0, "e4m3": 1}
+
+
+class _Cache8Plan(ctypes.Structure):
+    _fields_ = [("kind", _I), ("B", _I), ("H_kv", _I), ("d_k", _I), ("capacity", _I), ("k8", _VP), ("v8", _VP),
+                ("k_scale", _VP), ("v_scale", _VP), ("k_tail", _VP), ("v_tail", _VP)]
+
+
+class Cache8:
+    """A K/V cache held in 8 bits (gsdpa_cache8) over the caller's tensors:
+
+    k8 [B, H_kv, n, 64, d_k] and v8 [B, H_kv, n, d_k, 64], int8 or float8_e4m3fn;
+    k_scale, v_scale float32 [B, H_kv, n]; k_tail [B, H_kv, 2, 64, d_k] and v_tail
+    [B, H_kv, 2, d_k, 64] bfloat16 (the tokens of a block that is not full yet).
+    The capacity is 64 n tokens per sequence. Lengths are the caller's."""
+
+    def __init__(self, k8, v8, k_scale, v_scale, k_tail, v_tail):
+        import torch
+        kinds = {torch.int8: 0, torch.float8_e4m3fn: 1}
+        if k8.dtype not in kinds:
+            raise TypeError(f"k8 must be int8 or float8_e4m3fn, not {k8.dtype}")
+        if k8.dim() != 5 or k8.shape[3] != CACHE_BLOCK:
+            raise ValueError(f"k8 {tuple(k8.shape)} must be [B, H_kv, n, {CACHE_BLOCK}, d_k]")
+        B, H, n, _, d = k8.shape
+        want = {"k8": (k8, (B, H, n, CACHE_BLOCK, d), k8.dtype), "v8": (v8, (B, H, n, d, CACHE_BLOCK), k8.dtype),
+                "k_scale": (k_scale, (B, H, n), torch.float32), "v_scale": (v_scale, (B, H, n), torch.float32),
+                "k_tail": (k_tail, (B, H, 2, CACHE_BLOCK, d), torch.bfloat16),
+                "v_tail": (v_tail, (B, H, 2, d, CACHE_BLOCK), torch.bfloat16)}
+        for name, (t, shape, dtype) in want.items():
+            if t is not None and tuple(t.shape) != shape:
+                raise ValueError(f"{name} has shape {tuple(t.shape)}, the cache needs {shape}")
+            numel = 1
+            for v in shape:
+                numel *= v
+            _expect(t, name, numel, dtype, k8.device)
+        self.k8, self.v8, self.k_scale, self.v_scale, self.k_tail, self.v_tail = k8, v8, k_scale, v_scale, k_tail, v_tail
+        self.B, self.H_kv, self.d_k, self.capacity, self.device = B, H, d, n * CACHE_BLOCK, k8.device
+        self.plan = _Cache8Plan(kinds[k8.dtype], B, H, d, n * CACHE_BLOCK, k8.data_ptr(), v8.data_ptr(),
+                                k_scale.data_ptr(), v_scale.data_ptr(), k_tail.data_ptr(), v_tail.data_ptr())
+        self.ref = ctypes.addressof(self.plan)
+
+
+def cache8_alloc(B, capacity, H_kv, d_k, kind="int8", device="cuda") -> Cache8:
+    """An empty Cache8 of ``capacity`` tokens (rounded up to a multiple of 64) per sequence."""
+    import torch
+    n = (capacity + CACHE_BLOCK - 1) // CACHE_BLOCK
+    dt = {"int8": torch.int8, "e4m3": torch.float8_e4m3fn}[kind]
+
+    def make(*shape, dtype):
+        return torch.empty(shape, dtype=dtype, device=device)
+    return Cache8(make(B, H_kv, n, CACHE_BLOCK, d_k, dtype=dt), make(B, H_kv, n, d_k, CACHE_BLOCK, dtype=dt),
+                  make(B, H_kv, n, dtype=torch.float32), make(B, H_kv, n, dtype=torch.float32),
+                  make(B, H_kv, 2, CACHE_BLOCK, d_k, dtype=torch.bfloat16),
+                  make(B, H_kv, 2, d_k, CACHE_BLOCK, dtype=torch.bfloat16))
+
+
+def cache8_append(cache, K, V, lens, n_new=None, *, stream=None) -> None:
+    """Appends K, V [B, L, H_kv, d_k] bfloat16 to the cache (gsdpa_cache8_append):
+    row i < n_new[b] becomes token lens[b] + i of sequence b. lens and n_new (None:
+    L each) are int32 [B] on the device and are not changed."""
+    import torch
+    dev = cache.device
+    if K.dim() != 4:
+        raise ValueError("K must be [B, L, H_kv, d_k]")
+    shape = (cache.B, K.shape[1], cache.H_kv, cache.d_k)
+    ld_k = _head_rows(K, "K", shape, torch.bfloat16, dev)
+    ld_v = _head_rows(V, "V", shape, torch.bfloat16, dev)
+    if lens is None:
+        raise ValueError("lens is required")
+    at = _vector(lens, "lens", cache.B, torch.int32, dev)
+    new = _vector(n_new, "n_new", cache.B, torch.int32, dev)
+    s = _stream(stream, dev)
+    st = load().gsdpa_cache8_append(cache.ref, K.data_ptr(), V.data_ptr(), ld_k, ld_v, at, new, shape[1],
+                                    s.cuda_stream)
+    if st != OK:
+        raise GsdpaError(st, "gsdpa_cache8_append")
+
+
+def cache8_workspace_bytes(cache, L_q, H_q, d_model=0, gate="elementwise") -> int:
+    n = load().gsdpa_cache8_workspace_bytes(cache.ref, L_q, d_model, H_q, GATE_CODES[gate])
+    if n == ctypes.c_size_t(-1).value:
+        raise GsdpaError(ERR_UNSUPPORTED, "gsdpa_cache8_workspace_bytes")
+    return n
+
+
+def gated_sdpa_cache8(X, Q, cache, lens, W_g=None, *, gate="elementwise", n_new=None, out=None, workspace=None,
+                      stream=None):
+    """Gated attention of a step's tokens against the 8-bit cache (gated_sdpa_cache8),
+    after cache8_append of their keys and values with the same lens and n_new: row i
+    of Q [B, L_q, H_q, d_k] sees tokens 0 .. lens[b] + i. X [B, L_q, d_model] and W_g
+    as for gated_sdpa_fwd (None for gate="none"). Rows i >= n_new[b] of the result
+    are zero. Returns O, like Q."""
+    import torch
+    dev, bf = cache.device, torch.bfloat16
+    gm = GATE_CODES[gate]
+    if Q.dim() != 4 or Q.shape[0] != cache.B or Q.shape[3] != cache.d_k:
+        raise ValueError(f"Q {tuple(Q.shape)} must be [B={cache.B}, L_q, H_q, d_k={cache.d_k}]")
+    B, L_q, H_q, d_k = Q.shape
+    n = B * L_q * H_q * d_k
+    _expect(Q, "Q", n, bf, dev)
+    d_model, x, w = 0, None, None
+    if gm != GATE_NONE:
+        d_model = _x_dim(X, B, L_q)
+        _expect(X, "X", B * L_q * d_model, bf, dev)
+        _expect(W_g, "W_g", d_model * _gate_cols(gm, H_q, d_k), bf, dev)
+        x, w = X.data_ptr(), W_g.data_ptr()
+    if out is None:
+        out = torch.empty((B, L_q, H_q, d_k), dtype=bf, device=dev)
+    else:
+        _expect(out, "out", n, bf, dev)
+    if lens is None:
+        raise ValueError("lens is required")
+    at = _vector(lens, "lens", B, torch.int32, dev)
+    new = _vector(n_new, "n_new", B, torch.int32, dev)
+    lib = load()
+    need = lib.gsdpa_cache8_workspace_bytes(cache.ref, L_q, d_model, H_q, gm)
+    if need == ctypes.c_size_t(-1).value:
+        need = 0   # (the call itself says why)
+    workspace, ws_bytes = _workspace(workspace, need, dev)
+    s = _stream(stream, dev)
+    st = lib.gated_sdpa_cache8(x, Q.data_ptr(), cache.ref, at, new, w, out.data_ptr(), L_q, d_model, H_q, gm,
+                               None if workspace is None else workspace.data_ptr(), ws_bytes, s.cuda_stream)
+    if st != OK:
+        raise GsdpaError(st, "gated_sdpa_cache8")
+    return out

@@ -14,7 +14,8 @@
 
 namespace gsdpa {
 
-// Set by a kernel's bounded wait when it runs out; read and cleared by
+// Set by a kernel's bounded wait when it runs out, or by a length outside its
+// cache (the bits of sm103_ptx.cuh); read and cleared by
 // gsdpa_check_device_error().
 __device__ uint32_t g_error_word;
 
@@ -100,6 +101,18 @@ bool current_runtime(Runtime* rt, int* cc_major, int* cc_minor) {
 
 int plan_sms() { return kPlanSms; }
 
+void plan_gate_rows(const Problem& p, int num_sms, WorkspacePlan* w) {
+    w->gate_rows = p.B * p.Lq;
+    w->gate_cols = gate_cols(p);
+    const int nt = gate_col_tile(w->gate_cols);
+    const int tiles = ((w->gate_rows + 127) / 128) * ((w->gate_cols + nt - 1) / nt);
+    const int nkc = (p.d_model + 63) / 64;
+    int splits = (num_sms + tiles - 1) / tiles;
+    const int max_splits = nkc / 4 > 0 ? nkc / 4 : 1;
+    if (splits > max_splits) splits = max_splits;
+    w->gate_splits = splits < 1 ? 1 : splits;
+}
+
 WorkspacePlan plan_workspace(const Problem& p, int num_sms) {
     WorkspacePlan w;
     size_t off = 0;
@@ -123,19 +136,10 @@ WorkspacePlan plan_workspace(const Problem& p, int num_sms) {
         // less than a short one on all of them (measured on GQA 32/4 L4096:
         // 120.0 -> 113.8 us per call). Decode: the rows are few, and the
         // splits spread the W_g read over the SMs.
-        int splits = 1;   // (head-shared headwise: one row-dot kernel, no split)
-        if (p.gate_mode != GSDPA_GATE_HEADWISE_SHARED && decode) {
-            const int nt = gate_col_tile(w.gate_cols);
-            const int tiles = ((w.gate_rows + 127) / 128) * ((w.gate_cols + nt - 1) / nt);
-            const int nkc = (p.d_model + 63) / 64;
-            splits = (num_sms + tiles - 1) / tiles;
-            int max_splits = nkc / 4 > 0 ? nkc / 4 : 1;
-            if (splits > max_splits) splits = max_splits;
-            if (splits < 1) splits = 1;
-        }
-        w.gate_splits = splits;
+        w.gate_splits = 1;   // (head-shared headwise: one row-dot kernel, no split)
+        if (p.gate_mode != GSDPA_GATE_HEADWISE_SHARED && decode) plan_gate_rows(p, num_sms, &w);
         w.gate_part = off;
-        off = align256(off + sizeof(float) * (size_t)splits * w.gate_rows * w.gate_cols);
+        off = align256(off + sizeof(float) * (size_t)w.gate_splits * w.gate_rows * w.gate_cols);
     }
     // bf16 prefill: the counter from which the CTAs of the attention kernel
     // claim their units (dynamic schedule) and, with the first-token share, one
@@ -216,6 +220,10 @@ __global__ void state_zero_kernel(int* __restrict__ p, int n) {
     __threadfence();
     __syncthreads();
     pdl_trigger();
+}
+
+cudaError_t launch_state_zero(const ZeroJob& zero, cudaStream_t s) {
+    return launch_dependent(state_zero_kernel, dim3(1), dim3(256), 0, s, zero.p, zero.n);
 }
 
 __global__ void sink_finalize_kernel(const float* __restrict__ part, float* __restrict__ sink, int n, int tiles,
@@ -480,8 +488,7 @@ int fwd_impl(const void* X, const void* Q, const void* K, const void* V, const v
         if (decode) {
             if (e == cudaSuccess) e = launch_decode_bf16(p, w, ws, rt, s, gate_launched);
         } else {
-            if (e == cudaSuccess && zero.n > 0)
-                e = launch_dependent(state_zero_kernel, dim3(1), dim3(256), 0, s, zero.p, zero.n);
+            if (e == cudaSuccess && zero.n > 0) e = launch_state_zero(zero, s);
             // (the prefill kernel also finishes the first-token share)
             if (e == cudaSuccess) e = launch_prefill_bf16(p, w, ws, rt, s);
         }
@@ -706,7 +713,7 @@ int gsdpa_check_device_error(void* stream) {
     if (v != 0) {
         const uint32_t zero = 0;
         cudaMemcpyToSymbol(g_error_word, &zero, sizeof(zero));
-        return GSDPA_ERR_DEVICE_TIMEOUT;
+        return (v & ERR_WAIT_TIMEOUT) ? GSDPA_ERR_DEVICE_TIMEOUT : GSDPA_ERR_CACHE_RANGE;
     }
     return GSDPA_OK;
 }
@@ -720,6 +727,7 @@ const char* gsdpa_status_string(int status) {
         case GSDPA_ERR_WORKSPACE: return "GSDPA_ERR_WORKSPACE";
         case GSDPA_ERR_LAUNCH: return "GSDPA_ERR_LAUNCH";
         case GSDPA_ERR_DEVICE_TIMEOUT: return "GSDPA_ERR_DEVICE_TIMEOUT";
+        case GSDPA_ERR_CACHE_RANGE: return "GSDPA_ERR_CACHE_RANGE";
         default: return "GSDPA_ERR_UNKNOWN";
     }
 }

@@ -13,9 +13,11 @@ namespace gsdpa {
 
 // ---------------------------------------------------------------- device error word
 // Bits a kernel ORs into the error word (a __device__ global owned by the
-// host API) when one of its bounded waits runs out.
+// host API): one of its bounded waits ran out; a sequence's length or token
+// count, read on the device, lies outside its cache.
 enum : uint32_t {
     ERR_WAIT_TIMEOUT = 1u,
+    ERR_CACHE_RANGE = 2u,
 };
 
 struct WaitCtl {

@@ -109,7 +109,8 @@ typedef enum {
     GSDPA_ERR_ALIGNMENT = -3,        /* a pointer is not 16-byte aligned        */
     GSDPA_ERR_WORKSPACE = -4,        /* workspace NULL or smaller than needed   */
     GSDPA_ERR_LAUNCH = -5,           /* the CUDA runtime refused a launch       */
-    GSDPA_ERR_DEVICE_TIMEOUT = -6    /* a kernel wait ran out (see below)       */
+    GSDPA_ERR_DEVICE_TIMEOUT = -6,   /* a kernel wait ran out (see below)       */
+    GSDPA_ERR_CACHE_RANGE = -7       /* a length on the device lay outside its cache (see below) */
 } gsdpa_status;
 
 /*
@@ -340,10 +341,179 @@ GSDPA_API int gated_sdpa_bwd_saved_gate(const void* X, const void* Q, const void
                    void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * Per-head RMS norm of queries and keys, and rotary positions, in one pass:
+ * what stands between the projection and the attention ("GatedAttention
+ * [2025]", sec. 1.2.1 takes Q and K as given). For one head's row x at
+ * position p:
+ *     y_c = x_c gamma_c / sqrt(mean_c x_c^2 + eps)      (norm; else y = x)
+ *     (y_a, y_b) -> t (y_a cos(p w_i) - y_b sin(p w_i),
+ *                      y_b cos(p w_i) + y_a sin(p w_i))  for each pair i < rotary_dim / 2
+ * with (a, b) = (i, i + rotary_dim / 2) (half layout) or (2i, 2i + 1)
+ * (interleaved), w_i the pair's frequency and t = attn_scale; the columns from
+ * rotary_dim on are not rotated. Everything in float32, rounded once; the angle
+ * p w_i is exact to about |p| 2^-52 rad for every 32-bit position.
+ *
+ * gsdpa_rope is the plan, made once on the host by one of the two init
+ * functions and passed to every call (its contents are copied at the call).
+ *   rotary_dim : a multiple of 16, 16 .. 128 (and at most the call's d_k).
+ *   theta      : > 1; w_i = theta^(-2i / rotary_dim).
+ *   scaling    : PLAIN; LINEAR, w_i / factor; BASE, theta replaced by
+ *                theta factor^(rotary_dim / (rotary_dim - 2)); PARTS (the
+ *                "NTK-by-parts" interpolation of the YaRN paper), pairs that
+ *                turn more than beta_fast times in orig_len positions keep
+ *                their frequency, those under beta_slow turns are divided by
+ *                factor, a linear ramp over the pair's index between. factor
+ *                >= 1 (unused with PLAIN), orig_len >= 1 and beta_fast >=
+ *                beta_slow > 0 with PARTS.
+ *   attn_scale : t; 0 for the default, 1 (PARTS: 0.1 ln(factor) + 1).
+ * gsdpa_rope_init_freqs takes any finite frequencies (rotary_dim / 2 of them,
+ * radians per position) and t as it is.
+ */
+typedef enum { GSDPA_ROPE_HALF = 0, GSDPA_ROPE_INTERLEAVED = 1 } gsdpa_rope_layout;
+typedef enum {
+    GSDPA_ROPE_PLAIN = 0,
+    GSDPA_ROPE_LINEAR = 1,
+    GSDPA_ROPE_BASE = 2,
+    GSDPA_ROPE_PARTS = 3
+} gsdpa_rope_scaling;
+typedef struct {
+    int rotary_dim, layout;
+    float attn_scale;
+    int reserved;
+    unsigned long long turn[64];   /* each pair's frequency in turns per position, times 2^64, modulo 2^64 */
+} gsdpa_rope;
+GSDPA_API int gsdpa_rope_init(gsdpa_rope* rope, int rotary_dim, int layout, double theta, int scaling, double factor,
+                              double orig_len, double beta_fast, double beta_slow, double attn_scale);
+GSDPA_API int gsdpa_rope_init_freqs(gsdpa_rope* rope, int rotary_dim, int layout, const double* inv_freq,
+                                    double attn_scale);
+
+/*
+ * The forward. Q [B, L, H_q, d_k] and K [B, L, H_kv, d_k], heads contiguous in
+ * a token's row, rows ld elements apart (ld_q >= H_q d_k, ...), so that Q and K
+ * may be column blocks of one projection's output; likewise the outputs Qo, Ko.
+ *   gamma_q, gamma_k : [d_k], same dtype, or NULL for 1 (NULL without norm).
+ *   positions        : device int32 [B, L] (any values), or NULL for 0 .. L - 1.
+ *   norm             : 1 or 0.    eps : finite, >= 0 (norm only).
+ *   rope             : the plan (host pointer), or NULL for no rotation.
+ *   dtype            : GSDPA_F32 or GSDPA_BF16 (Q, K, gammas and outputs).
+ * d_k 64 or 128 (GSDPA_ERR_UNSUPPORTED otherwise); any H_q, H_kv >= 1. In place
+ * (Qo == Q with ld_qo == ld_q, the same for K) is allowed, other overlaps are
+ * not. Tensors 16-byte aligned, row lengths a multiple of 16 bytes. sm_103
+ * device. No workspace. B or L == 0: nothing is enqueued, GSDPA_OK.
+ */
+GSDPA_API int gsdpa_qk_norm_rope(const void* Q, const void* K, const void* gamma_q, const void* gamma_k,
+                   const int* positions, void* Qo, void* Ko,
+                   long long ld_q, long long ld_k, long long ld_qo, long long ld_ko,
+                   int B, int L, int H_q, int H_kv, int d_k, int norm, float eps, const gsdpa_rope* rope, int dtype,
+                   void* stream);
+
+/*
+ * The backward of gsdpa_qk_norm_rope: from dQo, dKo (the loss's gradients with
+ * respect to its outputs: gated_sdpa_bwd's dQ and dK) and the forward's inputs,
+ * the gradients with respect to Q, K, gamma_q and gamma_k.
+ *   Q, K             : the forward's inputs; not read (may be NULL) without norm.
+ *   dQ, dK           : out, each may be dQo, dKo (same row length).
+ *   dgamma_q, dgamma_k : out, [d_k] in the call's dtype, 16-byte aligned, summed in
+ *                      float32 over all rows in a fixed order (repeated calls give
+ *                      the same bits), or NULL for one that is not wanted; NULL
+ *                      without norm. With gamma NULL they are the gradients at 1.
+ *   workspace        : gsdpa_qk_norm_rope_bwd_workspace_bytes(...) bytes, 256-byte
+ *                      aligned (0 without norm).
+ * Other arguments, alignment and errors as for the forward. An empty problem
+ * enqueues nothing and leaves dgamma_q and dgamma_k as they are.
+ */
+GSDPA_API size_t gsdpa_qk_norm_rope_bwd_workspace_bytes(int B, int L, int d_k, int norm);
+GSDPA_API int gsdpa_qk_norm_rope_bwd(const void* Q, const void* K, const void* gamma_q, const void* gamma_k,
+                   const int* positions, const void* dQo, const void* dKo, void* dQ, void* dK,
+                   void* dgamma_q, void* dgamma_k,
+                   long long ld_q, long long ld_k, long long ld_dqo, long long ld_dko, long long ld_dq,
+                   long long ld_dk, int B, int L, int H_q, int H_kv, int d_k, int norm, float eps,
+                   const gsdpa_rope* rope, int dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * A K/V cache held in 8 bits, with one scale per block of 64 tokens and head
+ * ("GatedAttention [2025]", sec. 1.3.1: the grouped-query cache is what decode
+ * reads). The caller owns every buffer; the struct (on the host) describes them
+ * and its contents are copied at each call.
+ *   k8      : [B, H_kv, capacity / 64, 64, d_k] codes of the keys
+ *   v8      : [B, H_kv, capacity / 64, d_k, 64] codes of the values (transposed)
+ *   k_scale, v_scale : float32 [B, H_kv, capacity / 64], >= 0 (or NaN): a code stands
+ *             for code * scale
+ *   k_tail  : bf16 [B, H_kv, 2, 64, d_k], v_tail : bf16 [B, H_kv, 2, d_k, 64]: the
+ *             tokens of a block that is not full yet wait here unrounded, block j in
+ *             buffer j % 2. Token p is token p % 64 of block p / 64.
+ *   kind    : GSDPA_CACHE_INT8 (signed integers) or GSDPA_CACHE_E4M3 (8-bit floating
+ *             point, 4 exponent and 3 mantissa bits, no infinities).
+ *   capacity: tokens per sequence, a multiple of 64.   d_k : 64 or 128.
+ * A sequence of T tokens has T / 64 full blocks in 8 bits and T % 64 tokens in its
+ * open block's buffer; the lengths belong to the caller (one array serves every
+ * layer of a model). Nothing needs to be initialised for T = 0. Codes and scales
+ * written elsewhere in this format may be used as well. Tensors 16-byte aligned,
+ * scales 4-byte aligned.
+ */
+typedef enum { GSDPA_CACHE_INT8 = 0, GSDPA_CACHE_E4M3 = 1 } gsdpa_cache_kind;
+typedef struct {
+    int kind, B, H_kv, d_k, capacity;
+    void *k8, *v8;
+    float *k_scale, *v_scale;
+    void *k_tail, *v_tail;
+} gsdpa_cache8;
+
+/*
+ * Appends a step's keys and values. Sequence b holds lens[b] tokens before the
+ * call; its first n_new[b] rows of K and V become tokens lens[b] .. (rows past
+ * them are not read). lens is not changed: add n_new to it once, after the last
+ * layer's attention.
+ *   K, V   : device bf16 [B, L, H_kv, d_k], heads contiguous, rows ld_k, ld_v elements
+ *            apart (multiples of 8, >= H_kv d_k).
+ *   lens   : device int32 [B].    n_new : device int32 [B], or NULL for L each.
+ * A block that becomes full is written in 8 bits: with amax its largest |x|,
+ *   int8: scale = amax (1 / 127), reciprocal and product rounded to float32, code =
+ *         x / scale to nearest, ties to even (+-127 at most);
+ *   e4m3: scale = 2^e, the least e >= -126 with amax <= 448 scale, code = x / scale
+ *         to nearest, ties to even.
+ * amax = 0: scale and codes 0. A block that holds a NaN or an infinity: scale NaN,
+ * codes 0 (every row that sees one of its tokens becomes NaN). Each token is rounded
+ * once: the contents do not depend on how tokens were split over calls. Up to 64
+ * tokens may be taken back (drafts that were not accepted) by lowering lens.
+ * A sequence with lens[b] < 0, n_new[b] outside 0 .. L or more tokens than capacity
+ * is left as it was, and the next gsdpa_check_device_error returns
+ * GSDPA_ERR_CACHE_RANGE. Asynchronous on `stream`; sm_103 device.
+ */
+GSDPA_API int gsdpa_cache8_append(const gsdpa_cache8* cache, const void* K, const void* V, long long ld_k,
+                   long long ld_v, const int* lens, const int* n_new, int L, void* stream);
+
+/*
+ * The gated attention of a step's tokens against the cache, after their keys and
+ * values have been appended: query row i of sequence b sees tokens 0 .. lens[b] + i.
+ *   Q, O   : device bf16 [B, L_q, H_q, d_k].   X : bf16 [B, L_q, d_model].
+ *   W_g    : as for gated_sdpa_fwd; gate_mode NONE, HEADWISE or ELEMENTWISE.
+ *   lens   : device int32 [B], the tokens BEFORE this step (as passed to the append).
+ *   n_new  : device int32 [B], rows of this step, or NULL for L_q each. Rows i >=
+ *            n_new[b] of O are zero.
+ * H_q a multiple of H_kv with (H_q / H_kv) L_q <= 128 (a decoding step, or a few
+ * drafted tokens; GSDPA_ERR_UNSUPPORTED otherwise); d_model and the headwise gate's
+ * H_q multiples of 8. A sequence that does not fit its cache (as above) gives zero
+ * rows and GSDPA_ERR_CACHE_RANGE from the next gsdpa_check_device_error. Tokens past
+ * a sequence's end are not seen whatever their bytes; a NaN or infinity among the
+ * step's own keys is seen by the rows that may see it, one among its values in the
+ * open block by every row of the step.
+ * workspace: gsdpa_cache8_workspace_bytes(...) bytes, 256-byte aligned; calls that
+ * share one must not overlap on the device. Asynchronous on `stream`; other errors
+ * as for gated_sdpa_fwd.
+ */
+GSDPA_API size_t gsdpa_cache8_workspace_bytes(const gsdpa_cache8* cache, int L_q, int d_model, int H_q,
+                   int gate_mode);
+GSDPA_API int gated_sdpa_cache8(const void* X, const void* Q, const gsdpa_cache8* cache, const int* lens,
+                   const int* n_new, const void* W_g, void* O, int L_q, int d_model, int H_q, int gate_mode,
+                   void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Synchronises `stream`, then reads and clears the device error word that
- * bounded waits inside the kernels set when they run out. Returns GSDPA_OK,
- * GSDPA_ERR_DEVICE_TIMEOUT, or GSDPA_ERR_LAUNCH if the stream itself reports
- * a CUDA error.
+ * bounded waits inside the kernels set when they run out, and the 8-bit
+ * cache's kernels when a sequence's length or token count does not fit its
+ * cache. Returns GSDPA_OK, GSDPA_ERR_DEVICE_TIMEOUT, GSDPA_ERR_CACHE_RANGE, or
+ * GSDPA_ERR_LAUNCH if the stream itself reports a CUDA error.
  */
 GSDPA_API int gsdpa_check_device_error(void* stream);
 

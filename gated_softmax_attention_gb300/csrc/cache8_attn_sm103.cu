@@ -10,15 +10,23 @@
 // 2 d_k bytes a token and K/V head. 8-bit elements arrive twice as fast as
 // 16-bit ones, and four or eight query heads' products per element are then
 // more than the CUDA cores do in that time, so both products run on the tensor
-// cores with mma.sync: 16 query rows (heads of the group x new tokens) against
-// 8 tokens or columns, fp16 operands, fp32 sums. (tcgen05 needs 64 or 128
-// rows on one side, operands in shared memory in one of its own types, and
-// leaves the scores in tensor memory; here the rows are few and the 8-bit codes
-// have to pass through registers anyway, to become fp16.) int8 and e4m3 codes
-// are exact in fp16; q, a bf16 row scaled by a power of two to below 1, too
-// (elements under 2^-14 of the row's largest lose bits that weigh less than
-// 2^-24 of it). The weights are rounded to fp16 (11 bits) for the second product, to
-// bf16 for the open block's, whose values may exceed fp16's range.
+// cores with mma.sync, fp16 operands and fp32 sums: 16 tokens (then 16 value
+// columns) on the wide side, 8 query rows (heads of the group x new tokens) on
+// the narrow one. (tcgen05 wants 64 or 128 rows, operands in shared memory in
+// one of its own types, and leaves the scores in tensor memory; here the 8-bit
+// codes have to pass through registers anyway, to become fp16.) What is left
+// to the ordinary pipes is turning codes into fp16, 5 instructions for 4 int8
+// codes, and it sets the shape: a code is converted once for up to 16 query
+// rows, and with 16 x 8 products the unused part of the narrow side is small
+// for a decoding step (the first build put the query rows on the side of 16: twice the
+// products, sums and registers, 2010 instructions a tile, and 64 sequences of
+// 2048 tokens took 88 us instead of the 40 us of their bytes).
+//
+// int8 and e4m3 codes are exact in fp16; q, a bf16 row scaled by a power of two
+// to below 1, too (elements under 2^-14 of the row's largest lose bits that
+// weigh less than 2^-24 of it). The weights are rounded to fp16 (11 bits) for
+// the second product; the open block's, whose values may exceed fp16's range,
+// to two bf16 parts (16 bits).
 //
 // Two running references, both only for range: m for the sum of weights, and
 // M for the outputs, which carry the value scales: a block adds
@@ -28,19 +36,23 @@
 //
 // Tile = one block: K8 [64][d_k] and V8 [d_k][64], each 64 d_k contiguous bytes,
 // brought by cp.async.bulk. The tiles of all sequences and K/V heads form one
-// sequence of tiles that is cut evenly over the CTAs (lengths are read on the
-// device: no length, however uneven, leaves SMs idle). In a CTA, 8 warps work on 8 / R tiles at a
-// time, R warps to a tile (R = 1 up to 16 query rows, then 2, 4, 8); each such
-// team streams its own tiles through a ring of its own. At the end of a K/V
-// head's tiles the warps merge in shared memory; a head whose tiles are split
-// over CTAs is merged by the CTA that arrives last (an atomic counter; the
-// partial results are added in a fixed order). No CTA waits for another.
+// sequence of tiles that is cut evenly over the CTAs, and a CTA's share again
+// over its teams of warps (lengths are read on the device: no length, however
+// uneven, leaves SMs idle): up to 8 query rows, 8 teams of two warps that have
+// 32 of a tile's tokens each; beyond, teams of one, two, four or eight warps
+// with 16 query rows each. A team streams its tiles through a ring of its own
+// (one warp issues all copies) and needs no other team until its share is done: a
+// K/V head that lies within the share is finished by the team, the two heads
+// that its ends cut are left as parts (outputs, m, l, M) and merged at the end of
+// the CTA, and heads that the CTA's ends cut by the CTA that arrives last (an
+// atomic counter; parts are added in a fixed order). No CTA waits for another.
+// (With the tiles dealt to the teams in turn, and all warps merging at the end of
+// every head, the same 64 sequences took 90 us.)
 //
-// The order of the tokens inside a tile's products is chosen so that no
-// element moves between lanes: lane (g, t) of a warp holds, after the first
-// product, the scores of tokens 16 t .. 16 t + 15, which is what it needs as
-// the second product's weights, and 16 consecutive bytes of a value column are
-// its share of that product's other operand.
+// The order of the tokens inside a tile's products is chosen so that 16
+// consecutive bytes of a value column are one lane's share of the second
+// product's wide operand; the weights reach their place in its narrow operand
+// by one 8 x 8 transposition (movmatrix) for each 8 tokens.
 #include "cache8_internal.h"
 
 #include <cuda_fp16.h>
@@ -48,13 +60,14 @@
 namespace gsdpa {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
+constexpr int kSlots = 8;            // warps' parts in the merge buffer
 constexpr int kMaxRows = 128;        // query rows (heads of a group x new tokens) per K/V head
 constexpr int kMaxStages = 16;       // ring stages per team
+constexpr int kMaxCtas = 160;        // most CTAs (plan_sms)
 constexpr int kMinTiles = 8;         // fewest tiles worth a CTA
-constexpr int kBars = 64;            // ring stages of all teams
-constexpr uint32_t kSmemMax = 232448 - 1536;   // dynamic: what a CTA may have, less barriers and a few words
+constexpr int kWholeTiles = 32;      // most tiles of a head for one CTA to take it alone (see below)
+constexpr int kBars = 48;            // ring stages of all teams
+constexpr uint32_t kSmemMax = 232448 - 1984;   // dynamic: what a CTA may have, less barriers, parts and a few words
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kMove = 8.0f;
 
@@ -68,15 +81,23 @@ struct Cache8Args {
     int B, Lq, Hq, Hkv, G;           // G = Hq / Hkv
     int rows;                        // G * Lq
     int blocks, capacity;
-    int R, stages;                   // warps to a tile; ring stages per team
-    int merge_rows;                  // rows of a warp's part of the merge buffer
+    int R, stages;                   // groups of query rows (of 8 NT) to a team; ring stages per team
     const float* gate_part;          // [gate_splits, B * Lq, gate_cols] or null
     int gate_splits, gate_cols, gate_mode;
-    float* part_o;                   // [CTAs][2][rows][D]
-    float* part_s;                   // [CTAs][2][rows][4]: m, l, M
+    float* piece;                    // [CTAs][teams][rows][D + 4]: a team's first head, where its share goes on
+    float* part;                     // [CTAs][2][rows][D + 4]: a CTA's first and last head
     int* counters;                   // [B * Hkv]
+    int wait_first;                  // no gate kernel: everything before this kernel is waited for at once
     WaitCtl ctl;
 };
+
+// Zeroes the arrival counters where no gate kernel does. The attention kernel is
+// let start at once and waits for this one to end.
+__global__ void zero_counters_kernel(int* __restrict__ p, int n) {
+    pdl_trigger();
+    pdl_wait();
+    for (int k = blockIdx.x * blockDim.x + threadIdx.x; k < n; k += gridDim.x * blockDim.x) p[k] = 0;
+}
 
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
@@ -97,25 +118,47 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], 
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// 4 codes -> two fp16 pairs (codes 0, 1 and codes 2, 3), exactly.
+// 4 codes -> two fp16 pairs, exactly: int8 codes 0, 2 and 1, 3; e4m3 codes 0, 1
+// and 2, 3. pair_first() and pair_step() say which: code k of pair h is the
+// word's code h * pair_first + k * pair_step.
 template <bool E4M3>
-__device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t& p01, uint32_t& p23) {
+__device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
     if constexpr (E4M3) {
-        asm("{\n\t.reg .b16 lo, hi;\n\t"
-            "mov.b32 {lo, hi}, %2;\n\t"
-            "cvt.rn.f16x2.e4m3x2 %0, lo;\n\t"
-            "cvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
-            : "=r"(p01), "=r"(p23)
+        asm("{\n\t.reg .b16 a, b;\n\t"
+            "mov.b32 {a, b}, %2;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+            : "=r"(lo), "=r"(hi)
             : "r"(w));
     } else {
         // code + 128 in the low bits of the fp16 number 1024, then 1152 taken off
-        const uint32_t u = w ^ 0x80808080u;
         const __half2 off = __half2half2(__ushort_as_half(0x6480));   // 1152
-        uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
-        __half2 x = __hsub2(*reinterpret_cast<__half2*>(&a), off), y = __hsub2(*reinterpret_cast<__half2*>(&b), off);
-        p01 = *reinterpret_cast<uint32_t*>(&x);
-        p23 = *reinterpret_cast<uint32_t*>(&y);
+        const uint32_t a = (w & 0x00ff00ffu) ^ 0x64806480u, b = ((w >> 8) & 0x00ff00ffu) ^ 0x64806480u;
+        const __half2 x = __hsub2(*reinterpret_cast<const __half2*>(&a), off);
+        const __half2 y = __hsub2(*reinterpret_cast<const __half2*>(&b), off);
+        lo = *reinterpret_cast<const uint32_t*>(&x);
+        hi = *reinterpret_cast<const uint32_t*>(&y);
     }
+}
+template <bool E4M3>
+__device__ constexpr int pair_first() { return E4M3 ? 2 : 1; }
+template <bool E4M3>
+__device__ constexpr int pair_step() { return E4M3 ? 1 : 2; }
+// the same order for 4 16-bit elements in two words
+template <bool E4M3>
+__device__ __forceinline__ void pair_up(uint32_t& a, uint32_t& b) {
+    if constexpr (!E4M3) {
+        const uint32_t lo = __byte_perm(a, b, 0x5410), hi = __byte_perm(a, b, 0x7632);
+        a = lo;
+        b = hi;
+    }
+}
+
+// An 8 x 8 matrix of 16-bit elements, row g columns 2 t, 2 t + 1 in lane (g, t), transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
 }
 
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
@@ -143,11 +186,11 @@ struct SeqTiles {
 // the walk instead of leading it out of the batch.)
 struct Cursor {
     int b, kvh, j, tiles;
-    long long left;   // tiles of the CTA's range from here on
-    __device__ __forceinline__ void skip(const Cache8Args& a, long long n) {
+    int left;   // tiles of the share from here on
+    __device__ __forceinline__ void skip(const Cache8Args& a, int n) {
         left -= n;
         if (left <= 0) return;
-        long long at = j + n;
+        int at = j + n;
         while (at >= tiles) {
             at -= tiles;
             if (++kvh == a.Hkv) {
@@ -161,44 +204,65 @@ struct Cursor {
                 } while (tiles == 0);
             }
         }
-        j = (int)at;
+        j = at;
     }
 };
 
-// What a warp keeps of its 16 query rows; lane (g, t) has rows g and g + 8.
-template <int D>
+// n things dealt to k takers in order, each as many as the next or one more:
+// where a taker's share begins, and whose share holds thing x.
+struct Deal {
+    int each, more;
+    __device__ __forceinline__ Deal(int n, int k) : each(n / k), more(n % k) {}
+    __device__ __forceinline__ int from(int c) const { return c * each + min(c, more); }
+    __device__ __forceinline__ int taker(int x) const {
+        const int fat = more * (each + 1);
+        return x < fat ? x / (each + 1) : more + (x - fat) / each;
+    }
+};
+
+// What a warp keeps of its 8 NT query rows; lane (g, t) has rows 8 n + 2 t + e.
+template <int D, int NT>
 struct RowState {
-    float o[D / 8][4];   // columns 8 i + 2 t, + 1 of rows g, g + 8
-    float m[2], l[2], M[2];
+    float o[NT][D / 16][4];   // element 2 x + e: column 16 i + 8 x + g of row 8 n + 2 t + e
+    float m[NT][2], l[NT][2], M[NT][2];
     __device__ __forceinline__ void clear() {
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i)
+        for (int n = 0; n < NT; ++n) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
+            for (int i = 0; i < D / 16; ++i)
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            m[r] = M[r] = -INFINITY;
-            l[r] = 0.f;
+                for (int e = 0; e < 4; ++e) o[n][i][e] = 0.f;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                m[n][e] = M[n][e] = -INFINITY;
+                l[n][e] = 0.f;
+            }
         }
     }
 };
 
-// The scores of a tile (log2 units, tokens masked past lim) become weights:
-// s holds p c on return, l and the references are brought up to date. vs is
-// the tile's value scale.
-template <int D>
-__device__ __forceinline__ void soften(float (&s)[8][4], const float (&f)[2], bool mask, int base, const int (&lim)[2],
-                                       float vs, int t, RowState<D>& st) {
-    float top[2] = {-INFINITY, -INFINITY};
+// The scores of a warp's 16 MT tokens of a tile become weights: element 2 x + e
+// of s[n][i] is token at + 4 i + x * pair_first and row 8 n + 2 t + e, seen up
+// to token lim. f turns products into scores (log2 units), vs is the tile's
+// value scale. On return s holds p c, and l and the references are up to date.
+template <int D, int NT, int MT, bool E4M3, bool MASK>
+__device__ __forceinline__ void soften(float (&s)[NT][MT][4], const float (&f)[NT][2], float ks, int at,
+                                       const int (&lim)[NT][2], float vs, RowState<D, NT>& st) {
+    float top[NT][2];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int n = 0; n < NT; ++n) {
+        top[n][0] = top[n][1] = -INFINITY;
+        const float k[2] = {f[n][0] * ks, f[n][1] * ks};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            s[i][e] *= f[e >> 1];
-            if (mask && base + 16 * t + 2 * i + (e & 1) > lim[e >> 1]) s[i][e] = -INFINITY;
-            top[e >> 1] = fmaxf(top[e >> 1], s[i][e]);
-        }
-    // vs = frac 2^e
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                s[n][i][e] *= k[e & 1];
+                if (MASK && at + 4 * i + (e >> 1) * pair_first<E4M3>() > lim[n][e & 1]) s[n][i][e] = -INFINITY;
+                top[n][e & 1] = fmaxf(top[n][e & 1], s[n][i][e]);
+            }
+    }
+    // vs = frac 2^ev
     float frac = vs, ev = 0.f;
     if (vs < 8.6736174e-19f) {   // 2^-60: out of the subnormal numbers
         frac *= 1.152921504606847e18f;
@@ -210,110 +274,118 @@ __device__ __forceinline__ void soften(float (&s)[8][4], const float (&f)[2], bo
         frac = __uint_as_float((bits & 0x7fffffu) | 0x3f800000u);
     }
     bool need = false;
-    float tv[2];
+    float tv[NT][2];
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
-        top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
-        tv[r] = vs > 0.f ? top[r] + ev + 1.f : -INFINITY;
-        need = need || top[r] > st.m[r] + kMove || tv[r] > st.M[r] + kMove;
-    }
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+#pragma unroll
+            for (int sh = 4; sh < 32; sh <<= 1)
+                top[n][e] = fmaxf(top[n][e], __shfl_xor_sync(0xffffffffu, top[n][e], sh));
+            tv[n][e] = vs > 0.f ? top[n][e] + ev + 1.f : -INFINITY;
+            need = need || top[n][e] > st.m[n][e] + kMove || tv[n][e] > st.M[n][e] + kMove;
+        }
     if (__any_sync(0xffffffffu, need)) {
-        float fo[2];
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const float m = fmaxf(st.m[r], top[r]), M = fmaxf(st.M[r], tv[r]);
-            st.l[r] *= st.m[r] == -INFINITY ? 0.f : ex2_approx(st.m[r] - m);
-            fo[r] = st.M[r] == -INFINITY ? 0.f : ex2_approx(st.M[r] - M);
-            st.m[r] = m;
-            st.M[r] = M;
+        for (int n = 0; n < NT; ++n) {
+            float fo[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float m = fmaxf(st.m[n][e], top[n][e]), M = fmaxf(st.M[n][e], tv[n][e]);
+                st.l[n][e] *= st.m[n][e] == -INFINITY ? 0.f : ex2_approx(st.m[n][e] - m);
+                fo[e] = st.M[n][e] == -INFINITY ? 0.f : ex2_approx(st.M[n][e] - M);
+                st.m[n][e] = m;
+                st.M[n][e] = M;
+            }
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) st.o[n][i][e] *= fo[e & 1];
+        }
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        float c[2], m[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            // (a row that has seen no token yet has no reference; a scale of zero adds nothing)
+            m[e] = st.m[n][e] == -INFINITY ? 0.f : st.m[n][e];
+            c[e] = vs == 0.f ? 0.f : frac * (st.M[n][e] == -INFINITY ? 1.f : ex2_approx(m[e] + ev - st.M[n][e]));
         }
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i)
+        for (int i = 0; i < MT; ++i)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) st.o[i][e] *= fo[e >> 1];
-    }
-    float c[2], m[2];
+            for (int e = 0; e < 4; ++e) {
+                const float p = ex2_approx(s[n][i][e] - m[e & 1]);
+                st.l[n][e & 1] += p;
+                s[n][i][e] = p * c[e & 1];
+            }
+        if constexpr (MASK) {   // a block with a NaN scale must not reach the rows that see none of it
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        // (a row that has seen no token yet has no reference; a scale of zero adds nothing)
-        m[r] = st.m[r] == -INFINITY ? 0.f : st.m[r];
-        c[r] = vs == 0.f ? 0.f : frac * (st.M[r] == -INFINITY ? 1.f : ex2_approx(m[r] + ev - st.M[r]));
-    }
+            for (int i = 0; i < MT; ++i)
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float p = ex2_approx(s[i][e] - m[e >> 1]);
-            st.l[e >> 1] += p;
-            s[i][e] = p * c[e >> 1];
+                for (int e = 0; e < 4; ++e)
+                    if (at + 4 * i + (e >> 1) * pair_first<E4M3>() > lim[n][e & 1]) s[n][i][e] = 0.f;
         }
-    if (mask) {   // a block with a NaN scale must not reach the rows that see none of it
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (base + 16 * t + 2 * i + (e & 1) > lim[e >> 1]) s[i][e] = 0.f;
     }
 }
 
-// Query rows as the first product's operand: k step (c, q) of lane t covers
-// columns 16 c + 4 q .. + 3 of its piece c (t, then t + 4 when d_k = 128).
+// A query row as the first product's narrow operand: k step 4 c + q of lane t
+// covers columns 16 (t + 4 c) + 4 q .. + 3.
 template <int D>
-__device__ __forceinline__ void load_rows(const __nv_bfloat16* const (&src)[2], int t, uint32_t (&w)[D / 16][4]) {
+__device__ __forceinline__ void load_row(const __nv_bfloat16* src, int t, uint32_t (&w)[D / 16][2]) {
 #pragma unroll
-    for (int r = 0; r < 2; ++r)
+    for (int c = 0; c < D / 64; ++c)
 #pragma unroll
-        for (int c = 0; c < D / 64; ++c)
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (src[r]) v = *reinterpret_cast<const uint4*>(src[r] + 16 * (t + 4 * c) + 8 * half);
-                w[4 * c + 2 * half][r] = v.x;
-                w[4 * c + 2 * half][2 + r] = v.y;
-                w[4 * c + 2 * half + 1][r] = v.z;
-                w[4 * c + 2 * half + 1][2 + r] = v.w;
-            }
+        for (int half = 0; half < 2; ++half) {
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (src) v = *reinterpret_cast<const uint4*>(src + 16 * (t + 4 * c) + 8 * half);
+            w[4 * c + 2 * half][0] = v.x;
+            w[4 * c + 2 * half][1] = v.y;
+            w[4 * c + 2 * half + 1][0] = v.z;
+            w[4 * c + 2 * half + 1][1] = v.w;
+        }
 }
 
-// bf16 rows -> fp16 rows scaled by a power of two to below 1; back[r] undoes it.
-template <int D>
-__device__ __forceinline__ void rows_to_f16(uint32_t (&w)[D / 16][4], float (&back)[2]) {
+// A bf16 row -> fp16 scaled by a power of two to below 1, its pairs in the order
+// of the codes'; returns the factor that undoes the scale.
+template <int D, bool E4M3>
+__device__ __forceinline__ float row_to_f16(uint32_t (&w)[D / 16][2]) {
+    uint32_t top = 0;
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        uint32_t top = 0;
+    for (int k = 0; k < D / 16; ++k)
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k)
+        for (int h = 0; h < 2; ++h) top = max(top, max(w[k][h] & 0x7fffu, (w[k][h] >> 16) & 0x7fffu));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    const uint32_t e = min(max(top >> 7, 1u), 252u);   // the largest element's exponent field
+    const float scale = __uint_as_float((253u - e) << 23);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const uint32_t v = w[k][2 * h + r];
-                top = max(top, max(v & 0x7fffu, (v >> 16) & 0x7fffu));
-            }
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const uint32_t e = min(max(top >> 7, 1u), 252u);   // the largest element's exponent field
-        const float scale = __uint_as_float((253u - e) << 23);
-        back[r] = __uint_as_float((e + 1u) << 23);
+    for (int k = 0; k < D / 16; ++k) {
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const uint32_t v = w[k][2 * h + r];
-                w[k][2 * h + r] = pack_f16x2(__uint_as_float(v << 16) * scale, __uint_as_float(v & 0xffff0000u) * scale);
-            }
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t v = w[k][h];
+            w[k][h] = pack_f16x2(__uint_as_float(v << 16) * scale, __uint_as_float(v & 0xffff0000u) * scale);
+        }
+        pair_up<E4M3>(w[k][0], w[k][1]);
     }
+    return __uint_as_float((e + 1u) << 23);
 }
 
-// Output columns [col, col + 4) of query row `row`: the sums become the
-// attention's output, gated and stored.
+// What turns a row's summed outputs into the attention's (a row whose weights
+// leave nothing is zero).
+__device__ __forceinline__ float out_scale(float m, float l, float M) {
+    return l > 0.f || l != l ? (M == -INFINITY ? 0.f : ex2_approx(M - m)) / l : 0.f;
+}
+
+// Output columns [col, col + 4) of query row `row`: the sums o, scaled by k,
+// gated and stored.
 template <int D>
-__device__ __forceinline__ void finish(const Cache8Args& a, int b, int kvh, int n, int row, int col, float m, float l,
-                                       float M, const float4& o) {
+__device__ __forceinline__ void finish(const Cache8Args& a, int b, int kvh, int n, int row, int col, float k,
+                                       const float4& o) {
     const int i = row / a.G;
     if (i >= n) return;
     const int h = kvh * a.G + row % a.G;
-    // (a row whose weights leave nothing is zero)
-    const float k = l > 0.f || l != l ? (M == -INFINITY ? 0.f : ex2_approx(M - m)) / l : 0.f;
     float y[4] = {o.x * k, o.y * k, o.z * k, o.w * k};
     const long long token = (long long)b * a.Lq + i;
     if (a.gate_mode != GSDPA_GATE_NONE) {
@@ -333,414 +405,758 @@ __device__ __forceinline__ void finish(const Cache8Args& a, int b, int kvh, int 
         make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
 }
 
-// One more (m, l, M, o) into a running merge.
-__device__ __forceinline__ void merge(float& m, float& l, float& M, float4& o, float m2, float l2, float M2,
-                                      const float4& o2) {
-    const float mn = fmaxf(m, m2), Mn = fmaxf(M, M2);
-    const float a = m == -INFINITY ? 0.f : ex2_approx(m - mn), b = m2 == -INFINITY ? 0.f : ex2_approx(m2 - mn);
-    const float c = M == -INFINITY ? 0.f : ex2_approx(M - Mn), d = M2 == -INFINITY ? 0.f : ex2_approx(M2 - Mn);
-    l = l * a + l2 * b;
-    o.x = o.x * c + o2.x * d;
-    o.y = o.y * c + o2.y * d;
-    o.z = o.z * c + o2.z * d;
-    o.w = o.w * c + o2.w * d;
-    m = mn;
-    M = Mn;
+// 2^(x - top), 0 for a part that saw nothing.
+__device__ __forceinline__ float part_weight(float x, float top) { return x == -INFINITY ? 0.f : ex2_approx(x - top); }
+
+template <int D, bool E4M3, int NT>
+struct Config {
+    static constexpr int KS = NT == 1 ? 2 : 1;          // warps that share a tile's tokens
+    static constexpr int WARPS = kSlots * KS;           // ... that compute
+    static constexpr int CONSUMERS = WARPS * 32;
+    static constexpr int THREADS = CONSUMERS + 128;     // one more warp issues the copies, in a group of four of its own:
+    // its registers go to the others (at launch 640 threads have 96 each, 384 have 168: 61440 and 64512 in
+    // all, which is 512 x 112 + 128 x 32 and 256 x 232 + 128 x 40)
+    static constexpr int REGS = NT == 1 ? 112 : 232, COPY_REGS = NT == 1 ? 32 : 40;
+    static constexpr int MT = 4 / KS;                   // groups of 16 tokens to a warp
+    static constexpr int STRIDE = D + 4;                // floats of a row's part: D columns, then m, l, M
+    static constexpr uint32_t STAGE = kCacheBlock * D;  // bytes: an 8-bit tile's K or V, or half the open block's
+};
+
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
 }
 
-template <int D, bool E4M3>
-__global__ void __launch_bounds__(kThreads, 1) cache8_attn_kernel(const Cache8Args a) {
-    constexpr uint32_t STAGE = kCacheBlock * D;   // bytes: an 8-bit tile's K or V, or half the open block's
+// A part of a cut head: where it is and whose.
+struct Piece {
+    const float *rows, *rows2;   // [rows][STRIDE], in shared or global memory; what a second warp adds, or null
+    int u0;                      // the head's first tile in the sequence of all tiles
+    int b, kvh;
+};
+
+template <int D, bool E4M3, int NT>
+__global__ void __launch_bounds__(Config<D, E4M3, NT>::THREADS, 1)
+cache8_attn_kernel(const __grid_constant__ Cache8Args a) {
+    using C = Config<D, E4M3, NT>;
+    constexpr uint32_t STAGE = C::STAGE;
+    constexpr int kThreads = C::THREADS, kConsumers = C::CONSUMERS, MT = C::MT, STRIDE = C::STRIDE;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ uint64_t s_full[kBars], s_empty[kBars];
-    __shared__ long long s_scan[kWarps];
-    __shared__ int s_b, s_rem, s_last;
+    __shared__ int s_scan[kThreads / 32], s_longest[kThreads / 32];
+    __shared__ Piece s_piece[2 * kSlots];   // in the order of the tiles; rows null: none
+    __shared__ int s_b[kSlots], s_rem[kSlots];
+    __shared__ int s_last[2];
     __shared__ int s_abort;
     volatile int* abort_flag = &s_abort;
 
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const int g = lane >> 2, t = lane & 3;
-    const int teams = kWarps / a.R, team = warp / a.R, rt = warp % a.R;
-    const bool leader = rt == 0 && lane == 0;
-    uint8_t* ring = smem + (size_t)team * a.stages * STAGE;
-    float* red_o = reinterpret_cast<float*>(smem + (size_t)teams * a.stages * STAGE);   // [8 warps][merge_rows][D]
-    float* red_s = red_o + kWarps * a.merge_rows * D;                                   // [8 warps][merge_rows][4]
-    uint64_t* full = s_full + team * a.stages;
-    uint64_t* empty = s_empty + team * a.stages;
-    if (leader) {
-        for (int k = 0; k < a.stages; ++k) {
-            mbar_init(&full[k], 1);
-            mbar_init(&empty[k], a.R);
-        }
-        mbar_fence_init();
+    const int team_warps = C::KS * a.R, teams = kSlots / a.R;
+    const int team = warp / team_warps, in_team = warp % team_warps;   // (the copying warp: neither)
+    float* slots = reinterpret_cast<float*>(smem + (size_t)teams * a.stages * STAGE);   // [teams][rows][STRIDE]
+    if (tid < teams * a.stages) {
+        mbar_init(&s_full[tid], 1);
+        mbar_init(&s_empty[tid], team_warps);
     }
+    mbar_fence_init();
+    if (tid < 2 * kSlots) s_piece[tid].rows = s_piece[tid].rows2 = nullptr;
     if (tid == 0) s_abort = 0;
+    if (a.wait_first) pdl_wait();
 
-    // ---- the CTA's share of all tiles: [lo, hi) of N
+    // ---- the CTA's share of all tiles, [lo, hi) of N, and the teams' shares of that
     const int per = (a.B + kThreads - 1) / kThreads;
-    long long mine = 0;
-    for (int b = tid * per; b < min(a.B, (tid + 1) * per); ++b) mine += SeqTiles(a, b).tiles;
+    int mine = 0, longest = 0;
+    for (int b = tid * per; b < min(a.B, (tid + 1) * per); ++b) {
+        const int n = SeqTiles(a, b).tiles;
+        mine += n;
+        longest = max(longest, n);
+    }
     mine *= a.Hkv;
-    long long scan = mine;
+    int scan = mine;
 #pragma unroll
     for (int sh = 1; sh < 32; sh <<= 1) {
-        const long long up = __shfl_up_sync(0xffffffffu, scan, sh);
+        const int up = __shfl_up_sync(0xffffffffu, scan, sh);
         if (lane >= sh) scan += up;
     }
+    longest = __reduce_max_sync(0xffffffffu, longest);
     if (lane == 31) s_scan[warp] = scan;
+    if (lane == 0) s_longest[warp] = longest;
     __syncthreads();
-    long long N = 0, before = scan - mine;
+    int N = 0, before = scan - mine;   // (fits: the host checks the cache's number of tiles)
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
+    for (int w = 0; w < kThreads / 32; ++w) {
         if (w < warp) before += s_scan[w];
         N += s_scan[w];
+        longest = max(longest, s_longest[w]);
     }
-    long long ctas = (N + kMinTiles - 1) / kMinTiles;
-    ctas = ctas < 1 ? 1 : (ctas > (long long)gridDim.x ? (long long)gridDim.x : ctas);
-    const long long me = blockIdx.x;
-    const long long lo = me < ctas ? N * me / ctas : N, hi = me < ctas ? N * (me + 1) / ctas : N;
-    if (lo < hi && lo >= before && lo < before + mine) {
-        long long at = lo - before;
-        int b = tid * per;
-        long long in_seq = (long long)SeqTiles(a, b).tiles * a.Hkv;
-        while (at >= in_seq && b + 1 < a.B) {
-            at -= in_seq;
-            in_seq = (long long)SeqTiles(a, ++b).tiles * a.Hkv;
+    const int me = blockIdx.x;
+    const int ctas = max(1, min((int)gridDim.x, (N + kMinTiles - 1) / kMinTiles));
+    const Deal deal(N, ctas);
+    int lo = me < ctas ? deal.from(me) : N, hi = me < ctas ? deal.from(me + 1) : N;
+    // Short sequences, a CTA for each head: no head is cut between CTAs, whose
+    // merge would take longer than the tiles (the CTA's own head is then all there is).
+    const bool by_head = longest <= kWholeTiles && a.B * (long long)a.Hkv <= gridDim.x;
+    if (by_head) {
+        lo = 0;
+        hi = me < a.B * a.Hkv ? SeqTiles(a, me / a.Hkv).tiles : 0;
+    }
+    const Deal team_deal(hi - lo, teams);
+    const auto team_lo = [&](int k) { return lo + team_deal.from(k); };
+    if (by_head) {
+        if (tid < teams) {
+            s_b[tid] = me / a.Hkv;
+            s_rem[tid] = me % a.Hkv * hi + team_lo(tid);
         }
-        s_b = b;
-        s_rem = (int)at;   // (below H_kv * capacity / 64, checked on the host)
+    } else if (mine > 0) {
+        for (int k = 0; k < teams; ++k) {
+            const int from = team_lo(k);
+            if (from < before || from >= before + mine || from == team_lo(k + 1)) continue;
+            int at = from - before;
+            int b = tid * per;
+            int in_seq = SeqTiles(a, b).tiles * a.Hkv;
+            while (at >= in_seq && b + 1 < a.B) {
+                at -= in_seq;
+                in_seq = SeqTiles(a, ++b).tiles * a.Hkv;
+            }
+            s_b[k] = b;
+            s_rem[k] = at;
+        }
     }
+    __syncthreads();
+    const auto start_of = [&](int k) {
+        Cursor c;
+        c.left = team_lo(k + 1) - team_lo(k);
+        c.b = c.kvh = c.j = c.tiles = 0;
+        if (c.left > 0) {
+            c.b = s_b[k];
+            c.tiles = SeqTiles(a, c.b).tiles;
+            if (c.tiles == 0) {
+                c.left = 0;
+            } else {
+                c.kvh = s_rem[k] / c.tiles;
+                c.j = s_rem[k] % c.tiles;
+            }
+        }
+        return c;
+    };
+    if (warp >= C::WARPS) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::COPY_REGS));
+        if (warp > C::WARPS) return;
+        // ---- copies: lane k serves team k, in the order the team consumes them
+        Cursor next;
+        next.left = 0;
+        if (lane < teams) next = start_of(lane);
+        uint8_t* ring = smem + (size_t)lane * a.stages * STAGE;
+        uint64_t *full = s_full + lane * a.stages, *empty = s_empty + lane * a.stages;
+        uint32_t stage = 0, phase = 0, armed = 0, armed_phase = 0;
+        int part = 0;   // copy of the tile at `next`: 8 bits K, V; open block K, K, V, V
+        long long unit = 0;
+        int T = 0;
+        const auto enter = [&]() {
+            unit = (long long)next.b * a.Hkv + next.kvh;
+            T = SeqTiles(a, next.b).T;
+        };
+        if (next.left > 0) enter();
+        unsigned long long idle_since = 0;
+        while (__any_sync(0xffffffffu, next.left > 0)) {
+            bool did = false;
+            if (next.left > 0 && mbar_test(&empty[stage], phase ^ 1u)) {
+                did = true;
+                mbar_arrive_expect_tx(&full[stage], STAGE);
+                armed |= 1u << stage;
+                armed_phase = (armed_phase & ~(1u << stage)) | (phase << stage);
+                const bool open = (next.j + 1) * kCacheBlock > T;
+                const uint8_t* src;
+                if (!open) {
+                    src = (part == 0 ? a.k8 : a.v8) + (unit * a.blocks + next.j) * STAGE;
+                } else {
+                    const __nv_bfloat16* tail = part < 2 ? a.k_tail : a.v_tail;
+                    src = reinterpret_cast<const uint8_t*>(tail) +
+                          ((unit * 2 + (next.j & 1)) * 2 + (part & 1)) * STAGE;
+                }
+                bulk_load(ring + stage * STAGE, src, STAGE, &full[stage]);
+                if (++part == (open ? 4 : 2)) {
+                    part = 0;
+                    if (next.j + 1 < next.tiles) {
+                        ++next.j;
+                        --next.left;
+                    } else {
+                        next.skip(a, 1);
+                        if (next.left > 0) enter();
+                    }
+                }
+                if (++stage == (uint32_t)a.stages) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+            if (__any_sync(0xffffffffu, did)) {
+                idle_since = 0;
+                continue;
+            }
+            // every team's ring is full: look again shortly, but not for ever
+            if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
+            const unsigned long long now = globaltimer_ns();
+            if (idle_since == 0) idle_since = now;
+            if (__any_sync(0xffffffffu, now - idle_since > a.ctl.limit_ns)) {
+                if (lane == 0) {
+                    atomicOr(a.ctl.err, ERR_WAIT_TIMEOUT);
+                    *abort_flag = 1;
+                }
+                break;
+            }
+            __nanosleep(40);
+        }
+        if (!__all_sync(0xffffffffu, next.left <= 0)) {
+            // let copies in flight land before the CTA exits
+            volatile int never = 0;
+            WaitCtl c2 = a.ctl;
+            if (c2.limit_ns < 1000000000ull) c2.limit_ns = 1000000000ull;
+            for (int k = 0; k < a.stages; ++k)
+                if (armed & (1u << k)) mbar_wait(&full[k], (armed_phase >> k) & 1u, &never, c2);
+        }
+        return;
+    }
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS));
+    bool ok = true;
+    {
+        // ---- the team's tiles
+        const uint8_t* ring = smem + (size_t)team * a.stages * STAGE;
+        uint64_t *full = s_full + team * a.stages, *empty = s_empty + team * a.stages;
+        const int rt = in_team / C::KS, kh = in_team % C::KS;   // the warp's query rows and part of a tile's tokens
+        const int team_threads = 32 * team_warps, team_tid = 32 * in_team + lane;
+        float* slot = slots + (size_t)team * a.rows * STRIDE;
+        uint32_t c_stage = 0, c_phase = 0, r_stage = 0;
+        const auto wait_full = [&]() -> const uint8_t* {
+            if (!__all_sync(0xffffffffu, mbar_wait(&full[c_stage], c_phase, abort_flag, a.ctl))) {
+                ok = false;
+                return nullptr;
+            }
+            const uint8_t* p = ring + c_stage * STAGE;
+            if (++c_stage == (uint32_t)a.stages) {
+                c_stage = 0;
+                c_phase ^= 1u;
+            }
+            return p;
+        };
+        const auto release = [&]() {   // the oldest stage that is still held
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&empty[r_stage]);
+            if (++r_stage == (uint32_t)a.stages) r_stage = 0;
+        };
+        RowState<D, NT> st;
+        // (the lane's tokens of a tile's first 16: see soften)
+        const int key0 = 16 * (g >> 1) + 4 * MT * kh + (g & 1) * pair_step<E4M3>();
+        const float unscaled = kLog2e * rsqrtf((float)D);
+        Cursor at = start_of(team);
+        int here = team_lo(team);   // the cursor's place in the sequence of all tiles
+        while (at.left > 0) {
+            const SeqTiles q(a, at.b);
+            const long long unit = (long long)at.b * a.Hkv + at.kvh;
+            const int j1 = min(at.tiles, at.j + at.left);   // segment: tiles [at.j, j1) of the head
+            uint32_t qf[NT][D / 16][2];
+            float f[NT][2];
+            int lim[NT][2];
+            const auto row_of = [&](int n, int* last) -> const __nv_bfloat16* {
+                const int row = 8 * (NT * rt + n) + g, i = row / a.G;
+                const bool real = row < a.rows && i < q.n;
+                *last = real ? q.len + i : -1;
+                return real ? a.Q + (((long long)at.b * a.Lq + i) * a.Hq + at.kvh * a.G + row % a.G) * D : nullptr;
+            };
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                int last;
+                load_row<D>(row_of(n, &last), t, qf[n]);
+                const float back = row_to_f16<D, E4M3>(qf[n]) * unscaled;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    f[n][e] = __shfl_sync(0xffffffffu, back, 4 * (2 * t + e));
+                    lim[n][e] = __shfl_sync(0xffffffffu, last, 4 * (2 * t + e));
+                }
+            }
+            st.clear();
+            // the segment's scales, 32 tiles at a time, one batch ahead
+            const float *ksp = a.k_scale + unit * a.blocks, *vsp = a.v_scale + unit * a.blocks;
+            const auto scale_of = [&](const float* p, int from) {
+                const int k = from + lane;
+                return k < j1 && !q.open(k) ? p[k] : 0.f;
+            };
+            float ks_now = scale_of(ksp, at.j), vs_now = scale_of(vsp, at.j);
+            float ks_next = scale_of(ksp, at.j + 32), vs_next = scale_of(vsp, at.j + 32);
+            for (int j = at.j, it = 0; ok && j < j1; ++j, ++it) {
+                if (it == 32) {
+                    it = 0;
+                    ks_now = ks_next;
+                    vs_now = vs_next;
+                    ks_next = scale_of(ksp, j + 32);
+                    vs_next = scale_of(vsp, j + 32);
+                }
+                const int base = j * kCacheBlock;
+                float s[NT][MT][4];
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int i = 0; i < MT; ++i)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) s[n][i][e] = 0.f;
+                if (!q.open(j)) {
+                    const float ks = __shfl_sync(0xffffffffu, ks_now, it), vs = __shfl_sync(0xffffffffu, vs_now, it);
+                    const uint8_t* kt = wait_full();
+                    if (!kt) break;
+#pragma unroll
+                    for (int i = 0; i < MT; ++i) {
+                        const uint8_t* r0 = kt + (key0 + 4 * i) * D + 16 * t;
+                        const uint8_t* r1 = r0 + pair_first<E4M3>() * D;
+#pragma unroll
+                        for (int c = 0; c < D / 64; ++c) {
+                            const uint4 x = *reinterpret_cast<const uint4*>(r0 + 64 * c);
+                            const uint4 y = *reinterpret_cast<const uint4*>(r1 + 64 * c);
+                            const uint32_t x4[4] = {x.x, x.y, x.z, x.w}, y4[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                uint32_t w[4];
+                                codes_to_f16<E4M3>(x4[k], w[0], w[2]);
+                                codes_to_f16<E4M3>(y4[k], w[1], w[3]);
+#pragma unroll
+                                for (int n = 0; n < NT; ++n)
+                                    mma_f16(s[n][i], w, qf[n][4 * c + k][0], qf[n][4 * c + k][1]);
+                            }
+                        }
+                    }
+                    release();
+                    // (the first query row sees tokens up to len: tiles before need no mask)
+                    if (base + kCacheBlock - 1 > q.len)
+                        soften<D, NT, MT, E4M3, true>(s, f, ks, base + key0, lim, vs, st);
+                    else
+                        soften<D, NT, MT, E4M3, false>(s, f, ks, base + key0, lim, vs, st);
+                    uint32_t pf[NT][MT][2];
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int i = 0; i < MT; ++i)
+#pragma unroll
+                            for (int x = 0; x < 2; ++x)
+                                pf[n][i][x] = transpose8(pack_f16x2(s[n][i][2 * x], s[n][i][2 * x + 1]));
+                    const uint8_t* vt = wait_full();
+                    if (!vt) break;
+#pragma unroll
+                    for (int i = 0; i < D / 16; ++i) {
+                        const uint8_t* r = vt + (16 * i + g) * kCacheBlock + 16 * t + 4 * MT * kh;
+                        uint32_t x4[MT], y4[MT];
+                        if constexpr (MT == 4) {
+                            *reinterpret_cast<uint4*>(x4) = *reinterpret_cast<const uint4*>(r);
+                            *reinterpret_cast<uint4*>(y4) = *reinterpret_cast<const uint4*>(r + 8 * kCacheBlock);
+                        } else {
+                            *reinterpret_cast<uint2*>(x4) = *reinterpret_cast<const uint2*>(r);
+                            *reinterpret_cast<uint2*>(y4) = *reinterpret_cast<const uint2*>(r + 8 * kCacheBlock);
+                        }
+#pragma unroll
+                        for (int k = 0; k < MT; ++k) {
+                            uint32_t w[4];
+                            codes_to_f16<E4M3>(x4[k], w[0], w[2]);
+                            codes_to_f16<E4M3>(y4[k], w[1], w[3]);
+#pragma unroll
+                            for (int n = 0; n < NT; ++n) mma_f16(st.o[n][i], w, pf[n][k][0], pf[n][k][1]);
+                        }
+                    }
+                    release();
+                } else {
+                    // the open block, in bf16: keys [64][D], values [D][64], each in two stages
+                    uint32_t qb[NT][D / 16][2];
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        int last;
+                        load_row<D>(row_of(n, &last), t, qb[n]);
+                    }
+                    const uint8_t* k0 = wait_full();
+                    if (!k0) break;
+                    const uint8_t* k1 = wait_full();
+                    if (!k1) break;
+                    const uint8_t* half = g < 4 ? k0 : k1 - 32 * D * 2;   // tokens 16 (g / 2) ..: first or second 32
+#pragma unroll
+                    for (int i = 0; i < MT; ++i) {
+                        const uint8_t* r0 = half + (key0 + 4 * i) * D * 2 + 32 * t;
+                        const uint8_t* r1 = r0 + pair_first<E4M3>() * D * 2;
+#pragma unroll
+                        for (int c = 0; c < D / 64; ++c)
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                const uint4 x = *reinterpret_cast<const uint4*>(r0 + 128 * c + 16 * k);
+                                const uint4 y = *reinterpret_cast<const uint4*>(r1 + 128 * c + 16 * k);
+                                const uint32_t w0[4] = {x.x, y.x, x.y, y.y}, w1[4] = {x.z, y.z, x.w, y.w};
+#pragma unroll
+                                for (int n = 0; n < NT; ++n) {
+                                    const int ko = 4 * c + 2 * k;
+                                    mma_bf16(s[n][i], w0, qb[n][ko][0], qb[n][ko][1]);
+                                    mma_bf16(s[n][i], w1, qb[n][ko + 1][0], qb[n][ko + 1][1]);
+                                }
+                            }
+                    }
+                    release();
+                    release();
+                    float fo[NT][2];
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) fo[n][0] = fo[n][1] = unscaled;
+                    soften<D, NT, MT, E4M3, true>(s, fo, 1.f, base + key0, lim, 1.f, st);
+                    // each weight as two bf16 parts
+                    uint32_t wh[NT][MT][2], wl[NT][MT][2];
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int i = 0; i < MT; ++i)
+#pragma unroll
+                            for (int x = 0; x < 2; ++x) {
+                                const float p0 = s[n][i][2 * x], p1 = s[n][i][2 * x + 1];
+                                const uint32_t h = pack_bf16x2(p0, p1);
+                                wh[n][i][x] = transpose8(h);
+                                wl[n][i][x] = transpose8(pack_bf16x2(p0 - __uint_as_float(h << 16),
+                                                                     p1 - __uint_as_float(h & 0xffff0000u)));
+                            }
+                    // slots past the sequence's end hold whatever was there before: zero, not 0 * NaN
+                    uint32_t keep[2 * MT];
+#pragma unroll
+                    for (int k = 0; k < 2 * MT; ++k) {
+                        const int over = q.T - (base + 16 * t + 4 * MT * kh + 2 * k);
+                        keep[k] = over > 1 ? 0xffffffffu : (over == 1 ? 0x0000ffffu : 0u);
+                    }
+                    const uint8_t* v0 = wait_full();
+                    if (!v0) break;
+                    const uint8_t* v1 = wait_full();
+                    if (!v1) break;
+#pragma unroll
+                    for (int i = 0; i < D / 16; ++i) {
+                        const uint8_t* r = (i < D / 32 ? v0 : v1) + (16 * (i % (D / 32)) + g) * kCacheBlock * 2 +
+                                           32 * t + 8 * MT * kh;
+#pragma unroll
+                        for (int k = 0; k < MT / 2; ++k) {
+                            uint4 x = *reinterpret_cast<const uint4*>(r + 16 * k);
+                            uint4 y = *reinterpret_cast<const uint4*>(r + 8 * kCacheBlock * 2 + 16 * k);
+                            x.x &= keep[4 * k];
+                            x.y &= keep[4 * k + 1];
+                            x.z &= keep[4 * k + 2];
+                            x.w &= keep[4 * k + 3];
+                            y.x &= keep[4 * k];
+                            y.y &= keep[4 * k + 1];
+                            y.z &= keep[4 * k + 2];
+                            y.w &= keep[4 * k + 3];
+                            pair_up<E4M3>(x.x, x.y);
+                            pair_up<E4M3>(x.z, x.w);
+                            pair_up<E4M3>(y.x, y.y);
+                            pair_up<E4M3>(y.z, y.w);
+                            const uint32_t w0[4] = {x.x, y.x, x.y, y.y}, w1[4] = {x.z, y.z, x.w, y.w};
+#pragma unroll
+                            for (int n = 0; n < NT; ++n) {
+                                mma_bf16(st.o[n][i], w0, wh[n][2 * k][0], wh[n][2 * k][1]);
+                                mma_bf16(st.o[n][i], w0, wl[n][2 * k][0], wl[n][2 * k][1]);
+                                mma_bf16(st.o[n][i], w1, wh[n][2 * k + 1][0], wh[n][2 * k + 1][1]);
+                                mma_bf16(st.o[n][i], w1, wl[n][2 * k + 1][0], wl[n][2 * k + 1][1]);
+                            }
+                        }
+                    }
+                    release();
+                    release();
+                }
+            }
+
+            // ---- the segment's rows into the team's slot, merged where two warps shared the tokens
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+#pragma unroll
+                    for (int sh = 4; sh < 32; sh <<= 1)
+                        st.l[n][e] += __shfl_xor_sync(0xffffffffu, st.l[n][e], sh);
+            const auto put = [&](float* base) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int row = 8 * (NT * rt + n) + 2 * t + e;
+                        if (row >= a.rows) continue;
+                        float* to = base + row * STRIDE;
+#pragma unroll
+                        for (int i = 0; i < D / 16; ++i) {
+                            to[16 * i + g] = st.o[n][i][e];
+                            to[16 * i + 8 + g] = st.o[n][i][2 + e];
+                        }
+                        if (g == 0)
+                            *reinterpret_cast<float4*>(to + D) = make_float4(st.m[n][e], st.l[n][e], st.M[n][e], 0.f);
+                    }
+            };
+            const bool whole = at.j == 0 && j1 == at.tiles, final = j1 - at.j == at.left;
+            // (the share's last part: the ring is empty and holds the second warp's rows)
+            float* spare = reinterpret_cast<float*>(smem + (size_t)team * a.stages * STAGE);
+            const bool apart = C::KS == 2 && final && !whole;
+            if (C::KS == 2 && !apart && kh == 1) put(slot);
+            if (C::KS == 1 || (apart && kh == 0)) put(slot);
+            ok = named_bar_and(1 + team, team_threads, ok && !*abort_flag);
+            if (!ok) break;
+            if (apart) {
+                if (kh == 1) put(spare);
+            } else if constexpr (C::KS == 2) {
+                if (kh == 0) {
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int row = 8 * (NT * rt + n) + 2 * t + e;
+                            if (row >= a.rows) continue;
+                            const float* from = slot + row * STRIDE;
+                            const float4 x = *reinterpret_cast<const float4*>(from + D);
+                            const float m = fmaxf(st.m[n][e], x.x), M = fmaxf(st.M[n][e], x.z);
+                            const float oa = part_weight(st.M[n][e], M), ob = part_weight(x.z, M);
+                            st.l[n][e] = st.l[n][e] * part_weight(st.m[n][e], m) + x.y * part_weight(x.x, m);
+                            st.m[n][e] = m;
+                            st.M[n][e] = M;
+#pragma unroll
+                            for (int i = 0; i < D / 16; ++i) {
+                                st.o[n][i][e] = st.o[n][i][e] * oa + from[16 * i + g] * ob;
+                                st.o[n][i][2 + e] = st.o[n][i][2 + e] * oa + from[16 * i + 8 + g] * ob;
+                            }
+                        }
+                    __syncwarp();
+                    put(slot);
+                }
+                named_bar_sync(1 + team, team_threads);
+            }
+            const float* kept = slot;   // the last head's rows stay here
+            if (whole) {
+                if (a.gate_mode != GSDPA_GATE_NONE) pdl_wait();   // the gate logits
+                for (int idx = team_tid; idx < a.rows * (D / 4); idx += team_threads) {
+                    const int row = idx / (D / 4), col = 4 * (idx % (D / 4));
+                    const float* from = slot + row * STRIDE;
+                    const float4 x = *reinterpret_cast<const float4*>(from + D);
+                    finish<D>(a, at.b, at.kvh, q.n, row, col, out_scale(x.x, x.y, x.z),
+                              *reinterpret_cast<const float4*>(from + col));
+                }
+            } else if (!final) {
+                float* to = a.piece + ((long long)blockIdx.x * teams + team) * a.rows * STRIDE;
+                for (int idx = team_tid; idx < a.rows * (STRIDE / 4); idx += team_threads)
+                    reinterpret_cast<float4*>(to)[idx] = reinterpret_cast<const float4*>(slot)[idx];
+                kept = to;
+            }
+            if (!whole && team_tid == 0) {
+                Piece& p = s_piece[2 * team + (final ? 1 : 0)];
+                p.rows = kept;
+                p.rows2 = apart ? spare : nullptr;
+                p.u0 = here - at.j;
+                p.b = at.b;
+                p.kvh = at.kvh;
+            }
+            if (!final) named_bar_sync(1 + team, team_threads);   // the slot may be written again
+            here += j1 - at.j;
+            at.skip(a, j1 - at.j);
+        }
+    }
+
+    // ---- the heads that the teams' shares cut
+    const auto sync_all = [&]() { named_bar_sync(kSlots + 1, kConsumers); };
+    if (!named_bar_and(kSlots + 1, kConsumers, ok && !*abort_flag)) {
+        pdl_wait();
+        return;
+    }
+    // Neighbouring parts of one head are a group. Every warp finds the groups for
+    // itself: a lane stands for a source of rows (lane % 16: the part, upper
+    // half: its second warp's rows), heads has the bit of each group's first part.
+    const int piece = lane % (2 * kSlots);
+    const float* rows_at = lane < 2 * kSlots ? s_piece[piece].rows : s_piece[piece].rows2;
+    const uint32_t sources = __ballot_sync(0xffffffffu, rows_at != nullptr);
+    const uint32_t parts = sources & 0xffffu, below = parts & ((1u << piece) - 1);
+    const int u0_here = s_piece[piece].u0;
+    const int u0_below = __shfl_sync(0xffffffffu, u0_here, below ? 31 - __clz(below) : piece);
+    const uint32_t heads = __ballot_sync(0xffffffffu, lane < 2 * kSlots && rows_at && (!below || u0_below != u0_here));
+    const int groups = __popc(heads), items = a.rows * (D / 4);
+    const auto part_of = [&](int c, int u0) {   // CTA c's part of the head at u0
+        return a.part + (long long)(2 * c + (u0 <= deal.from(c) ? 0 : 1)) * a.rows * STRIDE;
+    };
+    // The parts' weights and the sums' state of each (group, row), a warp to each;
+    // kept in the ring behind the second warp's rows of the first team.
+    float* weight = reinterpret_cast<float*>(smem) + (C::KS == 2 ? a.rows * STRIDE : 0);   // [groups][rows][32]
+    float4* state = reinterpret_cast<float4*>(weight + groups * a.rows * 32);              // m, l, M, output scale
+    for (int k = warp; k < groups * a.rows; k += C::WARPS) {
+        const int gr = k / a.rows, row = k % a.rows;
+        const bool in = rows_at && __popc(heads & ((2u << piece) - 1)) == gr + 1;
+        float4 x = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
+        if (in) x = *reinterpret_cast<const float4*>(rows_at + row * STRIDE + D);
+        float m = x.x, M = x.z;
+#pragma unroll
+        for (int sh = 1; sh < 32; sh <<= 1) {
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, sh));
+            M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, sh));
+        }
+        float l = x.y * part_weight(x.x, m);
+        weight[k * 32 + lane] = part_weight(x.z, M);
+#pragma unroll
+        for (int sh = 1; sh < 32; sh <<= 1) l += __shfl_xor_sync(0xffffffffu, l, sh);
+        if (lane == 0) state[k] = make_float4(m, l, M, out_scale(m, l, M));
+    }
+    pdl_wait();   // the gate logits; and the next kernel on the stream may rely on the gate kernel having ended
+    sync_all();
+    for (int idx = tid; idx < groups * items; idx += kConsumers) {
+        const int gr = idx / items, row = idx % items / (D / 4), col = 4 * (idx % (D / 4));
+        uint32_t rest = heads;
+        for (int k = 0; k < gr; ++k) rest &= rest - 1;
+        const uint32_t after = rest & (rest - 1);
+        const uint32_t range = (after ? (after & (0u - after)) - 1 : 0xffffu) & ~((rest & (0u - rest)) - 1);
+        uint32_t todo = sources & (range | (range << 16));
+        const float* w = weight + (gr * a.rows + row) * 32;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        while (todo) {   // four sources at a time
+            float4 v[4];
+            float f[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int i = todo ? __ffs(todo) - 1 : -1;
+                f[k] = 0.f;
+                v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (i >= 0) {
+                    const float* from = i < 2 * kSlots ? s_piece[i].rows : s_piece[i - 2 * kSlots].rows2;
+                    v[k] = *reinterpret_cast<const float4*>(from + row * STRIDE + col);
+                    f[k] = w[i];
+                }
+                todo &= todo - 1;
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                o.x += v[k].x * f[k];
+                o.y += v[k].y * f[k];
+                o.z += v[k].z * f[k];
+                o.w += v[k].w * f[k];
+            }
+        }
+        const float4 x = state[gr * a.rows + row];
+        const Piece& p = s_piece[__ffs(rest) - 1];
+        const SeqTiles q(a, p.b);
+        if (p.u0 >= lo && p.u0 + q.tiles <= hi) {
+            finish<D>(a, p.b, p.kvh, q.n, row, col, x.w, o);
+        } else {
+            float* to = part_of(me, p.u0) + row * STRIDE;
+            *reinterpret_cast<float4*>(to + col) = o;
+            if (col == 0) *reinterpret_cast<float4*>(to + D) = x;
+        }
+    }
+    // ---- the heads that the CTA's ends cut: the first and the last group
+    sync_all();   // (and the ring and the slots are free from here on)
+    const int ends[2] = {__ffs(heads) - 1, 31 - __clz(heads)};
+    if (tid < 2) {
+        int last = 0;
+        if (groups > tid) {
+            const Piece& p = s_piece[ends[tid]];
+            const int u1 = p.u0 + SeqTiles(a, p.b).tiles;
+            if (p.u0 < lo || u1 > hi) {
+                __threadfence();   // (after the barrier: covers what every thread has written)
+                last = atomicAdd(a.counters + (long long)p.b * a.Hkv + p.kvh, 1) == deal.taker(u1 - 1) - deal.taker(p.u0);
+                __threadfence();
+            }
+        }
+        s_last[tid] = last;
+    }
+    sync_all();
+    for (int e = 0; e < 2; ++e) {
+        if (!s_last[e]) continue;
+        const Piece& p = s_piece[ends[e]];
+        const SeqTiles q(a, p.b);
+        const int c0 = deal.taker(p.u0), count = deal.taker(p.u0 + q.tiles - 1) - c0 + 1;
+        // each part's weight and each row's scale, a warp to a row
+        float* weight = reinterpret_cast<float*>(smem);            // [rows][count]
+        float* scale = weight + a.rows * count;                    // [rows]
+        float* sums = weight + ((a.rows * (count + 1) + 3) & ~3);  // [split][items] of 4 floats
+        for (int row = warp; row < a.rows; row += C::WARPS) {
+            float m = -INFINITY, M = -INFINITY, l = 0.f;
+            float4 x[(kMaxCtas + 31) / 32];
+#pragma unroll
+            for (int k = 0; k < (kMaxCtas + 31) / 32; ++k) {
+                const int c = 32 * k + lane;
+                x[k] = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
+                if (c < count) x[k] = __ldcg(reinterpret_cast<const float4*>(part_of(c0 + c, p.u0) + row * STRIDE + D));
+                m = fmaxf(m, x[k].x);
+                M = fmaxf(M, x[k].z);
+            }
+#pragma unroll
+            for (int sh = 1; sh < 32; sh <<= 1) {
+                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, sh));
+                M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, sh));
+            }
+#pragma unroll
+            for (int k = 0; k < (kMaxCtas + 31) / 32; ++k) {
+                const int c = 32 * k + lane;
+                l += x[k].y * part_weight(x[k].x, m);
+                if (c < count) weight[row * count + c] = part_weight(x[k].z, M);
+            }
+#pragma unroll
+            for (int sh = 1; sh < 32; sh <<= 1) l += __shfl_xor_sync(0xffffffffu, l, sh);
+            if (lane == 0) scale[row] = out_scale(m, l, M);
+        }
+        sync_all();
+        // the weighted sum, the parts split over the threads that would be idle
+        const int split = items < kConsumers ? kConsumers / items : 1;
+        for (int idx = tid; idx < split * items; idx += kConsumers) {
+            const int sub = idx / items, row = idx % items / (D / 4), col = 4 * (idx % (D / 4));
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+            for (int c = sub; c < count; c += split) {
+                const float4 v = __ldcg(reinterpret_cast<const float4*>(part_of(c0 + c, p.u0) + row * STRIDE + col));
+                const float w = weight[row * count + c];
+                o.x += v.x * w;
+                o.y += v.y * w;
+                o.z += v.z * w;
+                o.w += v.w * w;
+            }
+            if (split == 1) finish<D>(a, p.b, p.kvh, q.n, row, col, scale[row], o);
+            else reinterpret_cast<float4*>(sums)[idx] = o;
+        }
+        sync_all();
+        if (split > 1) {
+            for (int idx = tid; idx < items; idx += kConsumers) {
+                const int row = idx / (D / 4), col = 4 * (idx % (D / 4));
+                float4 o = reinterpret_cast<const float4*>(sums)[idx];
+                for (int k = 1; k < split; ++k) {
+                    const float4 v = reinterpret_cast<const float4*>(sums)[k * items + idx];
+                    o.x += v.x;
+                    o.y += v.y;
+                    o.z += v.z;
+                    o.w += v.w;
+                }
+                finish<D>(a, p.b, p.kvh, q.n, row, col, scale[row], o);
+            }
+            sync_all();   // (the next head's sums may be written)
+        }
+    }
+
     // rows that no sequence has a token for are zero
     for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
         const SeqRange r = seq_range(a.lens, a.n_new, b, a.Lq, a.capacity);
         if (!r.ok && tid == 0) atomicOr(a.ctl.err, ERR_CACHE_RANGE);
         const long long from = ((long long)b * a.Lq + r.n) * a.Hq * D / 8, to = ((long long)b + 1) * a.Lq * a.Hq * D / 8;
-        for (long long i = from + tid; i < to; i += kThreads)
+        for (long long i = from + tid; i < to; i += kConsumers)
             reinterpret_cast<uint4*>(a.O)[i] = make_uint4(0, 0, 0, 0);
-    }
-    __syncthreads();
-    Cursor at;   // the CTA's place: start of the current segment
-    at.b = lo < hi ? s_b : 0;
-    at.tiles = SeqTiles(a, at.b).tiles;
-    if (lo >= hi || at.tiles == 0) {
-        pdl_wait();
-        return;
-    }
-    at.kvh = s_rem / at.tiles;
-    at.j = s_rem % at.tiles;
-    at.left = hi - lo;
-
-    // ---- producer (the team's leader): copies in the order the team consumes them
-    Cursor next = at;
-    int part = 0;               // copy of the tile at `next`: 8 bits K, V; open block K, K, V, V
-    bool more = leader && team < next.left;
-    if (more) next.skip(a, team);
-    uint32_t p_stage = 0, p_phase = 0, armed = 0, armed_phase = 0;
-    auto produce = [&]() -> bool {
-        if (!mbar_wait(&empty[p_stage], p_phase ^ 1u, abort_flag, a.ctl)) return false;
-        mbar_arrive_expect_tx(&full[p_stage], STAGE);
-        armed |= 1u << p_stage;
-        armed_phase = (armed_phase & ~(1u << p_stage)) | (p_phase << p_stage);
-        const long long unit = (long long)next.b * a.Hkv + next.kvh;
-        const bool open = SeqTiles(a, next.b).open(next.j);
-        const uint8_t* src;
-        if (!open) {
-            src = (part == 0 ? a.k8 : a.v8) + (unit * a.blocks + next.j) * STAGE;
-        } else {
-            const __nv_bfloat16* tail = part < 2 ? a.k_tail : a.v_tail;
-            src = reinterpret_cast<const uint8_t*>(tail) + ((unit * 2 + (next.j & 1)) * 2 + (part & 1)) * STAGE;
-        }
-        bulk_load(ring + p_stage * STAGE, src, STAGE, &full[p_stage]);
-        if (++part == (open ? 4 : 2)) {
-            part = 0;
-            more = teams < next.left;
-            next.skip(a, teams);
-        }
-        if (++p_stage == (uint32_t)a.stages) {
-            p_stage = 0;
-            p_phase ^= 1u;
-        }
-        return true;
-    };
-    bool ok = true;
-    if (leader)
-        for (int k = 0; k < a.stages && more && ok; ++k) ok = produce();
-    ok = __all_sync(0xffffffffu, ok);
-
-    // ---- consumer
-    uint32_t c_stage = 0, c_phase = 0;
-    auto wait_full = [&]() -> const uint8_t* {
-        if (!__all_sync(0xffffffffu, mbar_wait(&full[c_stage], c_phase, abort_flag, a.ctl))) {
-            ok = false;
-            return nullptr;
-        }
-        const uint8_t* p = ring + c_stage * STAGE;
-        if (++c_stage == (uint32_t)a.stages) {
-            c_stage = 0;
-            c_phase ^= 1u;
-        }
-        return p;
-    };
-    uint32_t r_stage = 0;
-    auto release = [&]() {   // the oldest stage that is still held
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&empty[r_stage]);
-        if (++r_stage == (uint32_t)a.stages) r_stage = 0;
-        if (leader && more && !produce()) *abort_flag = 1;
-        __syncwarp();
-    };
-
-    RowState<D> st;
-    long long done = 0;   // tiles of the CTA's range before the current segment
-    while (at.left > 0) {
-        const SeqTiles q(a, at.b);
-        const long long unit = (long long)at.b * a.Hkv + at.kvh;
-        const int j1 = (int)min((long long)at.tiles, at.j + at.left);   // segment: tiles [at.j, j1) of the unit
-        const __nv_bfloat16* src[2];
-        int lim[2];
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const int row = 16 * rt + g + 8 * r, i = row / a.G;
-            const bool real = row < a.rows && i < q.n;
-            src[r] = real ? a.Q + (((long long)at.b * a.Lq + i) * a.Hq + at.kvh * a.G + row % a.G) * D : nullptr;
-            lim[r] = real ? q.len + i : -1;
-        }
-        uint32_t qf[D / 16][4];
-        float f[2];
-        load_rows<D>(src, t, qf);
-        rows_to_f16<D>(qf, f);
-        const float unscaled = kLog2e * rsqrtf((float)D);
-        f[0] *= unscaled;
-        f[1] *= unscaled;
-        st.clear();
-        // the team's tiles of the segment: every teams-th of the CTA's range; their
-        // scales come 32 tiles at a time, one batch ahead
-        int j = at.j + (int)((team - done % teams + teams) % teams);
-        const float *ksp = a.k_scale + unit * a.blocks, *vsp = a.v_scale + unit * a.blocks;
-        auto scale_of = [&](const float* p, int from) {
-            const int k = from + lane * teams;
-            return k < j1 && !q.open(k) ? p[k] : 0.f;
-        };
-        float ks_now = scale_of(ksp, j), vs_now = scale_of(vsp, j);
-        float ks_next = scale_of(ksp, j + 32 * teams), vs_next = scale_of(vsp, j + 32 * teams);
-        for (int it = 0; ok && j < j1; j += teams, ++it) {
-            if (it == 32) {
-                it = 0;
-                ks_now = ks_next;
-                vs_now = vs_next;
-                ks_next = scale_of(ksp, j + 32 * teams);
-                vs_next = scale_of(vsp, j + 32 * teams);
-            }
-            const int base = j * kCacheBlock;
-            const bool mask = base + kCacheBlock - 1 > q.len;   // (the first query row sees tokens up to len)
-            float s[8][4];
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) s[i][e] = 0.f;
-            // tokens of the first product's columns: column n of step i is token 16 (n / 2) + 2 i + n % 2
-            if (!q.open(j)) {
-                const float ks = __shfl_sync(0xffffffffu, ks_now, it), vs = __shfl_sync(0xffffffffu, vs_now, it);
-                const uint8_t* kt = wait_full();
-                if (!kt) break;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const uint8_t* row = kt + (16 * (g >> 1) + 2 * i + (g & 1)) * D + 16 * t;
-#pragma unroll
-                    for (int c = 0; c < D / 64; ++c) {
-                        const uint4 w = *reinterpret_cast<const uint4*>(row + 64 * c);
-                        const uint32_t w4[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            uint32_t b0, b1;
-                            codes_to_f16<E4M3>(w4[k], b0, b1);
-                            mma_f16(s[i], qf[4 * c + k], b0, b1);
-                        }
-                    }
-                }
-                release();
-                const float fk[2] = {f[0] * ks, f[1] * ks};
-                soften<D>(s, fk, mask, base, lim, vs, t, st);
-                uint32_t pf[4][4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    pf[k][0] = pack_f16x2(s[2 * k][0], s[2 * k][1]);
-                    pf[k][1] = pack_f16x2(s[2 * k][2], s[2 * k][3]);
-                    pf[k][2] = pack_f16x2(s[2 * k + 1][0], s[2 * k + 1][1]);
-                    pf[k][3] = pack_f16x2(s[2 * k + 1][2], s[2 * k + 1][3]);
-                }
-                const uint8_t* vt = wait_full();
-                if (!vt) break;
-#pragma unroll
-                for (int i = 0; i < D / 8; ++i) {
-                    const uint4 w = *reinterpret_cast<const uint4*>(vt + (8 * i + g) * kCacheBlock + 16 * t);
-                    const uint32_t w4[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        uint32_t b0, b1;
-                        codes_to_f16<E4M3>(w4[k], b0, b1);
-                        mma_f16(st.o[i], pf[k], b0, b1);
-                    }
-                }
-                release();
-            } else {
-                // the open block, in bf16: keys [64][D], values [D][64], each in two stages
-                uint32_t qb[D / 16][4];
-                load_rows<D>(src, t, qb);
-                const uint8_t* k0 = wait_full();
-                if (!k0) break;
-                const uint8_t* k1 = wait_full();
-                if (!k1) break;
-                const uint8_t* half = g < 4 ? k0 : k1;   // tokens 16 (g / 2) ..: the first or second 32
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const uint8_t* row = half + (16 * ((g >> 1) & 1) + 2 * i + (g & 1)) * D * 2 + 32 * t;
-#pragma unroll
-                    for (int c = 0; c < D / 64; ++c)
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const uint4 w = *reinterpret_cast<const uint4*>(row + 128 * c + 16 * k);
-                            mma_bf16(s[i], qb[4 * c + 2 * k], w.x, w.y);
-                            mma_bf16(s[i], qb[4 * c + 2 * k + 1], w.z, w.w);
-                        }
-                }
-                release();
-                release();
-                const float fk[2] = {unscaled, unscaled};
-                soften<D>(s, fk, true, base, lim, 1.f, t, st);
-                uint32_t pf[4][4], keep[8];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    pf[k][0] = pack_bf16x2(s[2 * k][0], s[2 * k][1]);
-                    pf[k][1] = pack_bf16x2(s[2 * k][2], s[2 * k][3]);
-                    pf[k][2] = pack_bf16x2(s[2 * k + 1][0], s[2 * k + 1][1]);
-                    pf[k][3] = pack_bf16x2(s[2 * k + 1][2], s[2 * k + 1][3]);
-                }
-                // slots past the sequence's end hold whatever was there before: zero, not 0 * NaN
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const int over = q.T - (base + 16 * t + 2 * k);
-                    keep[k] = over > 1 ? 0xffffffffu : (over == 1 ? 0x0000ffffu : 0u);
-                }
-                const uint8_t* v0 = wait_full();
-                if (!v0) break;
-                const uint8_t* v1 = wait_full();
-                if (!v1) break;
-#pragma unroll
-                for (int i = 0; i < D / 8; ++i) {
-                    const uint8_t* row = (i < D / 16 ? v0 : v1) + (8 * (i % (D / 16)) + g) * kCacheBlock * 2 + 32 * t;
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const uint4 w = *reinterpret_cast<const uint4*>(row + 16 * k);
-                        mma_bf16(st.o[i], pf[2 * k], w.x & keep[4 * k], w.y & keep[4 * k + 1]);
-                        mma_bf16(st.o[i], pf[2 * k + 1], w.z & keep[4 * k + 2], w.w & keep[4 * k + 3]);
-                    }
-                }
-                release();
-                release();
-            }
-        }
-
-        // ---- merge the teams
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            st.l[r] += __shfl_xor_sync(0xffffffffu, st.l[r], 1);
-            st.l[r] += __shfl_xor_sync(0xffffffffu, st.l[r], 2);
-            const int row = g + 8 * r;
-            if (16 * rt + row < a.rows) {
-                float* to = red_o + ((long long)warp * a.merge_rows + row) * D + 2 * t;
-#pragma unroll
-                for (int i = 0; i < D / 8; ++i)
-                    *reinterpret_cast<float2*>(to + 8 * i) = make_float2(st.o[i][2 * r], st.o[i][2 * r + 1]);
-                if (t == 0)
-                    *reinterpret_cast<float4*>(red_s + (warp * a.merge_rows + row) * 4) =
-                        make_float4(st.m[r], st.l[r], st.M[r], 0.f);
-            }
-        }
-        if (!__syncthreads_and(ok && !*abort_flag)) {
-            ok = false;
-            break;
-        }
-        const bool whole = at.j == 0 && j1 == at.tiles;
-        // the unit's place in the sequence of all tiles, and the CTAs it is split over
-        const long long u0 = lo + done - at.j, u1 = u0 + at.tiles - 1;
-        long long c0 = u0 * ctas / N, c1 = u1 * ctas / N;
-        while (N * (c0 + 1) / ctas <= u0) ++c0;
-        while (N * (c1 + 1) / ctas <= u1) ++c1;
-        const auto slot = [&](long long c) { return 2 * c + (c > c0 || u0 == N * c0 / ctas ? 0 : 1); };
-        if (whole && a.gate_mode != GSDPA_GATE_NONE) pdl_wait();   // the gate logits
-        for (int idx = tid; idx < a.rows * (D / 4); idx += kThreads) {
-            const int row = idx / (D / 4), col = 4 * (idx % (D / 4));
-            float m = -INFINITY, l = 0.f, M = -INFINITY;
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int w = row / 16; w < kWarps; w += a.R) {
-                const float4 x = *reinterpret_cast<const float4*>(red_s + (w * a.merge_rows + row % 16) * 4);
-                merge(m, l, M, o, x.x, x.y, x.z,
-                      *reinterpret_cast<const float4*>(red_o + ((long long)w * a.merge_rows + row % 16) * D + col));
-            }
-            if (whole) {
-                finish<D>(a, at.b, at.kvh, q.n, row, col, m, l, M, o);
-            } else {
-                const long long to = slot(me) * a.rows + row;
-                *reinterpret_cast<float4*>(a.part_o + to * D + col) = o;
-                if (col == 0) *reinterpret_cast<float4*>(a.part_s + to * 4) = make_float4(m, l, M, 0.f);
-            }
-        }
-        if (!whole) {
-            __threadfence();
-            __syncthreads();
-            if (tid == 0) s_last = atomicAdd(a.counters + unit, 1) == (int)(c1 - c0);
-            __syncthreads();
-            if (s_last) {
-                __threadfence();
-                if (a.gate_mode != GSDPA_GATE_NONE) pdl_wait();
-                for (int idx = tid; idx < a.rows * (D / 4); idx += kThreads) {
-                    const int row = idx / (D / 4), col = 4 * (idx % (D / 4));
-                    float m = -INFINITY, l = 0.f, M = -INFINITY;
-                    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-                    for (long long c = c0; c <= c1; ++c) {
-                        const long long from = slot(c) * a.rows + row;
-                        const float4 x = __ldcg(reinterpret_cast<const float4*>(a.part_s + from * 4));
-                        merge(m, l, M, o, x.x, x.y, x.z, __ldcg(reinterpret_cast<const float4*>(a.part_o + from * D + col)));
-                    }
-                    finish<D>(a, at.b, at.kvh, q.n, row, col, m, l, M, o);
-                }
-            }
-        }
-        __syncthreads();   // the merge buffer may be written again
-        const int took = j1 - at.j;
-        done += took;
-        at.skip(a, took);
-    }
-    pdl_wait();   // (the next kernel on the stream may rely on the gate kernel having ended too)
-    if (!ok && leader) {
-        // let copies in flight land before the CTA exits
-        volatile int never = 0;
-        WaitCtl c2 = a.ctl;
-        if (c2.limit_ns < 1000000000ull) c2.limit_ns = 1000000000ull;
-        for (int k = 0; k < a.stages; ++k)
-            if (armed & (1u << k)) mbar_wait(&full[k], (armed_phase >> k) & 1u, &never, c2);
     }
 }
 
 // Shared memory and ring of one problem.
 struct Shape {
-    int R, stages, merge_rows;
+    int NT, R, stages;
     uint32_t smem;
 };
 Shape shape_of(int rows, int D) {
     Shape s;
+    s.NT = rows <= 8 ? 1 : 2;
     s.R = rows <= 16 ? 1 : (rows <= 32 ? 2 : (rows <= 64 ? 4 : 8));
-    s.merge_rows = rows < 16 ? rows : 16;
-    const uint32_t merge = kWarps * (uint32_t)(s.merge_rows * (D + 4)) * 4;
-    const uint32_t per_stage = (uint32_t)(kWarps / s.R) * kCacheBlock * D;
+    const uint32_t merge = (uint32_t)(kSlots / s.R * rows * (D + 4)) * 4;
+    const uint32_t per_stage = (uint32_t)(kSlots / s.R) * kCacheBlock * D;
     // as many copies in flight as fit, up to 192 KB (an open block holds two stages at once)
     s.stages = (int)((kSmemMax - merge) / per_stage);
     const int most = (int)(196608 / per_stage);
     if (s.stages > most) s.stages = most;
     if (s.stages > kMaxStages) s.stages = kMaxStages;
-    if (s.stages > kBars * s.R / kWarps) s.stages = kBars * s.R / kWarps;
+    if (s.stages > kBars * s.R / kSlots) s.stages = kBars * s.R / kSlots;
     s.smem = (uint32_t)s.stages * per_stage + merge;
     return s;
 }
@@ -748,7 +1164,7 @@ Shape shape_of(int rows, int D) {
 struct Cache8Plan {
     Problem p{};
     WorkspacePlan w;   // the gate kernel's part
-    size_t part_o = 0, part_s = 0, counters = 0, total = 0;
+    size_t piece = 0, part = 0, counters = 0, total = 0;
     int n_counters = 0;
 };
 
@@ -762,7 +1178,8 @@ int plan_cache8(const gsdpa_cache8* c, int Lq, int d_model, int Hq, int gate_mod
     if (gate_mode == GSDPA_GATE_HEADWISE && Hq % 8 != 0) return GSDPA_ERR_UNSUPPORTED;
     const long long rows = (long long)(Hq / c->H_kv) * Lq;
     if (rows > kMaxRows) return GSDPA_ERR_UNSUPPORTED;
-    if ((long long)c->H_kv * (c->capacity / kCacheBlock) > 0x7fffffffLL) return GSDPA_ERR_UNSUPPORTED;
+    // (tiles are counted in 32 bits)
+    if ((long long)c->B * c->H_kv * (c->capacity / kCacheBlock) > 0x7fffffffLL) return GSDPA_ERR_UNSUPPORTED;
     if ((long long)c->B * Lq > 0x7fffffffLL / 8) return GSDPA_ERR_UNSUPPORTED;
     if (c->B == 0 || Lq == 0) return GSDPA_OK;   // an empty problem: nothing to plan
     Cache8Plan& o = *out;
@@ -785,23 +1202,29 @@ int plan_cache8(const gsdpa_cache8* c, int Lq, int d_model, int Hq, int gate_mod
     };
     if (gate_mode != GSDPA_GATE_NONE) plan_gate_rows(p, plan_sms(), &o.w);
     o.w.gate_part = take(sizeof(float) * (size_t)o.w.gate_splits * o.w.gate_rows * o.w.gate_cols);
-    o.part_o = take(sizeof(float) * 2 * plan_sms() * (size_t)rows * c->d_k);
-    o.part_s = take(sizeof(float) * 2 * plan_sms() * (size_t)rows * 4);
+    const size_t part = sizeof(float) * (size_t)rows * (c->d_k + 4);
+    o.piece = take(part * plan_sms() * (kSlots / shape_of((int)rows, c->d_k).R));
+    o.part = take(part * plan_sms() * 2);
     o.n_counters = c->B * c->H_kv;
     o.counters = take(sizeof(int) * (size_t)o.n_counters);
     o.total = off;
     return GSDPA_OK;
 }
 
-template <int D, bool E4M3>
+template <int D, bool E4M3, int NT>
 cudaError_t launch(const Cache8Args& a, const Shape& sh, unsigned grid, cudaStream_t s) {
     static PerDeviceSetup setup;
     const cudaError_t e = setup_once_per_device(setup, [](int&) {
-        return cudaFuncSetAttribute(cache8_attn_kernel<D, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        return cudaFuncSetAttribute(cache8_attn_kernel<D, E4M3, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     (int)kSmemMax);
     });
     if (e != cudaSuccess) return e;
-    return launch_dependent(cache8_attn_kernel<D, E4M3>, dim3(grid), dim3(kThreads), sh.smem, s, a);
+    return launch_dependent(cache8_attn_kernel<D, E4M3, NT>, dim3(grid), dim3(Config<D, E4M3, NT>::THREADS), sh.smem, s,
+                            a);
+}
+template <int D, bool E4M3>
+cudaError_t launch(const Cache8Args& a, const Shape& sh, unsigned grid, cudaStream_t s) {
+    return sh.NT == 1 ? launch<D, E4M3, 1>(a, sh, grid, s) : launch<D, E4M3, 2>(a, sh, grid, s);
 }
 
 }  // namespace
@@ -843,16 +1266,18 @@ int gated_sdpa_cache8(const void* X, const void* Q, const gsdpa_cache8* cache, c
     pl.p.X = X;
     pl.p.Wg = W_g;
 
-    // The arrival counters are zeroed by the kernel that runs first: the gate
-    // logits' or, without a gate, state_zero_kernel. Both wait for the kernels
-    // before them, so the attention, their programmatic dependent, finds the
-    // cache and the queries written; it waits for the logits where it reads them.
+    // The arrival counters are zeroed by the kernel that runs first. The gate
+    // logits' kernel does it after waiting for the kernels before it, and then lets
+    // the attention, its programmatic dependent, start: that finds the cache and
+    // the queries written and waits for the logits where it reads them. Without a
+    // gate zero_counters_kernel does it, and the attention waits for its end.
     ZeroJob zero;
     zero.p = reinterpret_cast<int*>(ws + pl.counters);
     zero.n = pl.n_counters;
     bool launched = false;
     cudaError_t e = launch_gate_logits_bf16(pl.p, pl.w, ws, rt, s, &launched, zero);
-    if (e == cudaSuccess && !launched) e = launch_state_zero(zero, s);
+    if (e == cudaSuccess && !launched)
+        e = launch_dependent(zero_counters_kernel, dim3((zero.n + 255) / 256), dim3(256), 0, s, zero.p, zero.n);
     if (e == cudaErrorInvalidValue) return GSDPA_ERR_INVALID_ARG;
     if (e != cudaSuccess) return GSDPA_ERR_LAUNCH;
 
@@ -878,20 +1303,21 @@ int gated_sdpa_cache8(const void* X, const void* Q, const gsdpa_cache8* cache, c
     const Shape sh = shape_of(a.rows, cache->d_k);
     a.R = sh.R;
     a.stages = sh.stages;
-    a.merge_rows = sh.merge_rows;
     a.gate_part = gated ? reinterpret_cast<const float*>(ws + pl.w.gate_part) : nullptr;
     a.gate_splits = pl.w.gate_splits;
     a.gate_cols = pl.w.gate_cols;
     a.gate_mode = gate_mode;
-    a.part_o = reinterpret_cast<float*>(ws + pl.part_o);
-    a.part_s = reinterpret_cast<float*>(ws + pl.part_s);
+    a.piece = reinterpret_cast<float*>(ws + pl.piece);
+    a.part = reinterpret_cast<float*>(ws + pl.part);
     a.counters = zero.p;
+    a.wait_first = launched ? 0 : 1;
     a.ctl.err = rt.err;
     a.ctl.limit_ns = rt.limit_ns;
     // one CTA per SM, fewer where a full cache would not give each its tiles
     const long long most = ((long long)a.B * a.Hkv * a.blocks + kMinTiles - 1) / kMinTiles;
     long long grid = rt.num_sms < plan_sms() ? rt.num_sms : plan_sms();
     if (grid > most) grid = most;
+    if (grid > kMaxCtas) grid = kMaxCtas;
     const bool e4m3 = cache->kind == GSDPA_CACHE_E4M3;
     if (cache->d_k == 128)
         e = e4m3 ? launch<128, true>(a, sh, (unsigned)grid, s) : launch<128, false>(a, sh, (unsigned)grid, s);

@@ -222,10 +222,6 @@ __global__ void state_zero_kernel(int* __restrict__ p, int n) {
     pdl_trigger();
 }
 
-cudaError_t launch_state_zero(const ZeroJob& zero, cudaStream_t s) {
-    return launch_dependent(state_zero_kernel, dim3(1), dim3(256), 0, s, zero.p, zero.n);
-}
-
 __global__ void sink_finalize_kernel(const float* __restrict__ part, float* __restrict__ sink, int n, int tiles,
                                      float inv_lq) {
     const int idx = blockIdx.x * blockDim.x + threadIdx.x;
@@ -488,7 +484,8 @@ int fwd_impl(const void* X, const void* Q, const void* K, const void* V, const v
         if (decode) {
             if (e == cudaSuccess) e = launch_decode_bf16(p, w, ws, rt, s, gate_launched);
         } else {
-            if (e == cudaSuccess && zero.n > 0) e = launch_state_zero(zero, s);
+            if (e == cudaSuccess && zero.n > 0)
+                e = launch_dependent(state_zero_kernel, dim3(1), dim3(256), 0, s, zero.p, zero.n);
             // (the prefill kernel also finishes the first-token share)
             if (e == cudaSuccess) e = launch_prefill_bf16(p, w, ws, rt, s);
         }

@@ -160,9 +160,6 @@ struct ZeroJob {
     int* p = nullptr;
     int n = 0;
 };
-// zero.n ints zeroed by a kernel of their own, a programmatic dependent of the
-// kernel before it that lets its own dependent start when they are (gsdpa_api.cu).
-cudaError_t launch_state_zero(const ZeroJob& zero, cudaStream_t s);
 cudaError_t launch_gate_logits_bf16(const Problem& p, const WorkspacePlan& w, char* ws, const Runtime& rt,
                                     cudaStream_t s, bool* launched, ZeroJob zero = ZeroJob());
 // Elementwise bf16 prefill: sigma(X W_g) as fp16 into the workspace (gate_sigmoid_sm103.cu).

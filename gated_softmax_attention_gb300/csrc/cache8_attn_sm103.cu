@@ -64,8 +64,8 @@ constexpr int kSlots = 8;            // warps' parts in the merge buffer
 constexpr int kMaxRows = 128;        // query rows (heads of a group x new tokens) per K/V head
 constexpr int kMaxStages = 16;       // ring stages per team
 constexpr int kMaxCtas = 160;        // most CTAs (plan_sms)
-constexpr int kMinTiles = 8;         // fewest tiles worth a CTA
-constexpr int kWholeTiles = 32;      // most tiles of a head for one CTA to take it alone (see below)
+constexpr int kTeamParts = 12;       // most teams to a head (about) for them to merge it without their CTAs
+constexpr int kWholeTiles = 16;      // most tiles of a head for one CTA to take it alone (see below)
 constexpr int kBars = 48;            // ring stages of all teams
 constexpr uint32_t kSmemMax = 232448 - 1984;   // dynamic: what a CTA may have, less barriers, parts and a few words
 constexpr float kLog2e = 1.4426950408889634f;
@@ -84,7 +84,7 @@ struct Cache8Args {
     int R, stages;                   // groups of query rows (of 8 NT) to a team; ring stages per team
     const float* gate_part;          // [gate_splits, B * Lq, gate_cols] or null
     int gate_splits, gate_cols, gate_mode;
-    float* piece;                    // [CTAs][teams][rows][D + 4]: a team's first head, where its share goes on
+    float* piece;                    // [CTAs][teams][2][rows][D + 4]: a team's first and last head
     float* part;                     // [CTAs][2][rows][D + 4]: a CTA's first and last head
     int* counters;                   // [B * Hkv]
     int wait_first;                  // no gate kernel: everything before this kernel is waited for at once
@@ -133,7 +133,11 @@ __device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t& lo, uint32_t&
     } else {
         // code + 128 in the low bits of the fp16 number 1024, then 1152 taken off
         const __half2 off = __half2half2(__ushort_as_half(0x6480));   // 1152
-        const uint32_t a = (w & 0x00ff00ffu) ^ 0x64806480u, b = ((w >> 8) & 0x00ff00ffu) ^ 0x64806480u;
+        // (as one three-input operation: left to itself the compiler makes two of it, and the integer pipe
+        // is what the conversion is bound by)
+        uint32_t a, b;
+        asm("lop3.b32 %0, %1, %2, %3, 0x6a;" : "=r"(a) : "r"(w), "r"(0x00ff00ffu), "r"(0x64806480u));
+        asm("lop3.b32 %0, %1, %2, %3, 0x6a;" : "=r"(b) : "r"(w >> 8), "r"(0x00ff00ffu), "r"(0x64806480u));
         const __half2 x = __hsub2(*reinterpret_cast<const __half2*>(&a), off);
         const __half2 y = __hsub2(*reinterpret_cast<const __half2*>(&b), off);
         lo = *reinterpret_cast<const uint32_t*>(&x);
@@ -241,29 +245,10 @@ struct RowState {
     }
 };
 
-// The scores of a warp's 16 MT tokens of a tile become weights: element 2 x + e
-// of s[n][i] is token at + 4 i + x * pair_first and row 8 n + 2 t + e, seen up
-// to token lim. f turns products into scores (log2 units), vs is the tile's
-// value scale. On return s holds p c, and l and the references are up to date.
-template <int D, int NT, int MT, bool E4M3, bool MASK>
-__device__ __forceinline__ void soften(float (&s)[NT][MT][4], const float (&f)[NT][2], float ks, int at,
-                                       const int (&lim)[NT][2], float vs, RowState<D, NT>& st) {
-    float top[NT][2];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        top[n][0] = top[n][1] = -INFINITY;
-        const float k[2] = {f[n][0] * ks, f[n][1] * ks};
-#pragma unroll
-        for (int i = 0; i < MT; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                s[n][i][e] *= k[e & 1];
-                if (MASK && at + 4 * i + (e >> 1) * pair_first<E4M3>() > lim[n][e & 1]) s[n][i][e] = -INFINITY;
-                top[n][e & 1] = fmaxf(top[n][e & 1], s[n][i][e]);
-            }
-    }
-    // vs = frac 2^ev
-    float frac = vs, ev = 0.f;
+// A value scale as frac 2^ev, frac in [1, 2) (0, NaN and infinity stay what they are).
+__device__ __forceinline__ void split_scale(float vs, float& frac, float& ev) {
+    frac = vs;
+    ev = 0.f;
     if (vs < 8.6736174e-19f) {   // 2^-60: out of the subnormal numbers
         frac *= 1.152921504606847e18f;
         ev = -60.f;
@@ -272,26 +257,50 @@ __device__ __forceinline__ void soften(float (&s)[NT][MT][4], const float (&f)[N
     if (vs > 0.f && (bits >> 23) < 255u) {
         ev += (float)((int)(bits >> 23) - 127);
         frac = __uint_as_float((bits & 0x7fffffu) | 0x3f800000u);
+    } else {
+        ev = -INFINITY;   // (nothing that M should follow)
     }
+}
+
+// The products of a warp's 16 MT tokens of a tile become weights: element
+// 2 x + e of s[n][i] is token at + 4 i + x * pair_first and row 8 n + 2 t + e,
+// seen up to token lim. f ks turns products into scores (log2 units), frac 2^ev
+// is the tile's value scale. On return s holds p c, and l and the references
+// are up to date. The references are compared with the lane's own largest score
+// only; the row's is found when one of them has to move.
+template <int D, int NT, int MT, bool E4M3, bool MASK>
+__device__ __forceinline__ void soften(float (&s)[NT][MT][4], const float (&f)[NT][2], float ks, int at,
+                                       const int (&lim)[NT][2], float frac, float ev, RowState<D, NT>& st) {
+    float k[NT][2], top[NT][2];
     bool need = false;
-    float tv[NT][2];
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int n = 0; n < NT; ++n) {
+        top[n][0] = top[n][1] = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (MASK && at + 4 * i + (e >> 1) * pair_first<E4M3>() > lim[n][e & 1]) s[n][i][e] = -INFINITY;
+                top[n][e & 1] = fmaxf(top[n][e & 1], s[n][i][e]);
+            }
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-#pragma unroll
-            for (int sh = 4; sh < 32; sh <<= 1)
-                top[n][e] = fmaxf(top[n][e], __shfl_xor_sync(0xffffffffu, top[n][e], sh));
-            tv[n][e] = vs > 0.f ? top[n][e] + ev + 1.f : -INFINITY;
-            need = need || top[n][e] > st.m[n][e] + kMove || tv[n][e] > st.M[n][e] + kMove;
+            k[n][e] = f[n][e] * ks;
+            // (a score that is no number is not above anything: the weights show it)
+            top[n][e] = top[n][e] == -INFINITY ? -INFINITY : top[n][e] * k[n][e];
+            need = need || top[n][e] > st.m[n][e] + kMove || top[n][e] + ev + 1.f > st.M[n][e] + kMove;
         }
+    }
     if (__any_sync(0xffffffffu, need)) {
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             float fo[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const float m = fmaxf(st.m[n][e], top[n][e]), M = fmaxf(st.M[n][e], tv[n][e]);
+                float x = top[n][e];
+#pragma unroll
+                for (int sh = 4; sh < 32; sh <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, sh));
+                const float m = fmaxf(st.m[n][e], x), M = fmaxf(st.M[n][e], x + ev + 1.f);
                 st.l[n][e] *= st.m[n][e] == -INFINITY ? 0.f : ex2_approx(st.m[n][e] - m);
                 fo[e] = st.M[n][e] == -INFINITY ? 0.f : ex2_approx(st.M[n][e] - M);
                 st.m[n][e] = m;
@@ -310,23 +319,21 @@ __device__ __forceinline__ void soften(float (&s)[NT][MT][4], const float (&f)[N
         for (int e = 0; e < 2; ++e) {
             // (a row that has seen no token yet has no reference; a scale of zero adds nothing)
             m[e] = st.m[n][e] == -INFINITY ? 0.f : st.m[n][e];
-            c[e] = vs == 0.f ? 0.f : frac * (st.M[n][e] == -INFINITY ? 1.f : ex2_approx(m[e] + ev - st.M[n][e]));
+            c[e] = ev == -INFINITY || st.M[n][e] == -INFINITY ? frac : frac * ex2_approx(m[e] + ev - st.M[n][e]);
         }
 #pragma unroll
         for (int i = 0; i < MT; ++i)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const float p = ex2_approx(s[n][i][e] - m[e & 1]);
-                st.l[n][e & 1] += p;
-                s[n][i][e] = p * c[e & 1];
+                float p = ex2_approx(fmaf(s[n][i][e], k[n][e & 1], -m[e & 1]));
+                // masked: nothing, whatever the scales are (0 * -inf and NaN scales among them)
+                if (MASK && at + 4 * i + (e >> 1) * pair_first<E4M3>() > lim[n][e & 1]) {
+                    s[n][i][e] = 0.f;
+                } else {
+                    st.l[n][e & 1] += p;
+                    s[n][i][e] = p * c[e & 1];
+                }
             }
-        if constexpr (MASK) {   // a block with a NaN scale must not reach the rows that see none of it
-#pragma unroll
-            for (int i = 0; i < MT; ++i)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (at + 4 * i + (e >> 1) * pair_first<E4M3>() > lim[n][e & 1]) s[n][i][e] = 0.f;
-        }
     }
 }
 
@@ -441,6 +448,11 @@ struct Piece {
     int b, kvh;
 };
 
+// Sources of one head, up to the next group's first.
+struct Group {
+    int first, u0, b, kvh;
+};
+
 template <int D, bool E4M3, int NT>
 __global__ void __launch_bounds__(Config<D, E4M3, NT>::THREADS, 1)
 cache8_attn_kernel(const __grid_constant__ Cache8Args a) {
@@ -451,8 +463,10 @@ cache8_attn_kernel(const __grid_constant__ Cache8Args a) {
     __shared__ uint64_t s_full[kBars], s_empty[kBars];
     __shared__ int s_scan[kThreads / 32], s_longest[kThreads / 32];
     __shared__ Piece s_piece[2 * kSlots];   // in the order of the tiles; rows null: none
+    __shared__ Group s_group[2 * kSlots + 1];
+    __shared__ int s_groups;
     __shared__ int s_b[kSlots], s_rem[kSlots];
-    __shared__ int s_last[2];
+    __shared__ int s_last[kSlots];
     __shared__ int s_abort;
     volatile int* abort_flag = &s_abort;
 
@@ -497,9 +511,9 @@ cache8_attn_kernel(const __grid_constant__ Cache8Args a) {
         longest = max(longest, s_longest[w]);
     }
     const int me = blockIdx.x;
-    const int ctas = max(1, min((int)gridDim.x, (N + kMinTiles - 1) / kMinTiles));
-    const Deal deal(N, ctas);
-    int lo = me < ctas ? deal.from(me) : N, hi = me < ctas ? deal.from(me + 1) : N;
+    const int ctas = max(1, min((int)gridDim.x, N / teams));   // every team has a tile (or there is one CTA)
+    const Deal deal(N, ctas * teams);
+    int lo = me < ctas ? deal.from(me * teams) : N, hi = me < ctas ? deal.from((me + 1) * teams) : N;
     // Short sequences, a CTA for each head: no head is cut between CTAs, whose
     // merge would take longer than the tiles (the CTA's own head is then all there is).
     const bool by_head = longest <= kWholeTiles && a.B * (long long)a.Hkv <= gridDim.x;
@@ -507,8 +521,12 @@ cache8_attn_kernel(const __grid_constant__ Cache8Args a) {
         lo = 0;
         hi = me < a.B * a.Hkv ? SeqTiles(a, me / a.Hkv).tiles : 0;
     }
-    const Deal team_deal(hi - lo, teams);
-    const auto team_lo = [&](int k) { return lo + team_deal.from(k); };
+    // Where a head is cut into few parts the teams merge it themselves, the last to
+    // arrive; else first each CTA what its teams have.
+    const bool by_team = !by_head && longest <= kTeamParts * deal.each;
+    const auto team_lo = [&](int k) {
+        return by_head ? Deal(hi, teams).from(k) : (me < ctas ? deal.from(me * teams + k) : N);
+    };
     if (by_head) {
         if (tid < teams) {
             s_b[tid] = me / a.Hkv;
@@ -633,23 +651,29 @@ cache8_attn_kernel(const __grid_constant__ Cache8Args a) {
         const int rt = in_team / C::KS, kh = in_team % C::KS;   // the warp's query rows and part of a tile's tokens
         const int team_threads = 32 * team_warps, team_tid = 32 * in_team + lane;
         float* slot = slots + (size_t)team * a.rows * STRIDE;
-        uint32_t c_stage = 0, c_phase = 0, r_stage = 0;
-        const auto wait_full = [&]() -> const uint8_t* {
-            if (!__all_sync(0xffffffffu, mbar_wait(&full[c_stage], c_phase, abort_flag, a.ctl))) {
+        uint32_t stage = 0, phase = 0;   // the oldest stage that is not released
+        const auto wait_full = [&](uint32_t ahead = 0) -> const uint8_t* {   // that stage, or the next
+            uint32_t k = stage + ahead, ph = phase;
+            if (k >= (uint32_t)a.stages) {
+                k -= a.stages;
+                ph ^= 1u;
+            }
+            if (!__all_sync(0xffffffffu, mbar_wait(&full[k], ph, abort_flag, a.ctl))) {
                 ok = false;
                 return nullptr;
             }
-            const uint8_t* p = ring + c_stage * STAGE;
-            if (++c_stage == (uint32_t)a.stages) {
-                c_stage = 0;
-                c_phase ^= 1u;
-            }
-            return p;
+            return ring + k * STAGE;
         };
-        const auto release = [&]() {   // the oldest stage that is still held
+        const auto release = [&]() {
             __syncwarp();
-            if (lane == 0) mbar_arrive(&empty[r_stage]);
-            if (++r_stage == (uint32_t)a.stages) r_stage = 0;
+            if (lane == 0) mbar_arrive(&empty[stage]);
+            if (++stage == (uint32_t)a.stages) {
+                stage = 0;
+                phase ^= 1u;
+            }
+        };
+        const auto team_part = [&](int n, int u0) {   // team n's part of the head at u0: its first head's or its last's
+            return a.piece + (long long)(2 * n + (u0 <= deal.from(n) ? 0 : 1)) * a.rows * STRIDE;
         };
         RowState<D, NT> st;
         // (the lane's tokens of a tile's first 16: see soften)
@@ -663,40 +687,50 @@ cache8_attn_kernel(const __grid_constant__ Cache8Args a) {
             const int j1 = min(at.tiles, at.j + at.left);   // segment: tiles [at.j, j1) of the head
             uint32_t qf[NT][D / 16][2];
             float f[NT][2];
-            int lim[NT][2];
-            const auto row_of = [&](int n, int* last) -> const __nv_bfloat16* {
+            const auto row_of = [&](int n) -> const __nv_bfloat16* {
                 const int row = 8 * (NT * rt + n) + g, i = row / a.G;
-                const bool real = row < a.rows && i < q.n;
-                *last = real ? q.len + i : -1;
-                return real ? a.Q + (((long long)at.b * a.Lq + i) * a.Hq + at.kvh * a.G + row % a.G) * D : nullptr;
+                return row < a.rows && i < q.n
+                           ? a.Q + (((long long)at.b * a.Lq + i) * a.Hq + at.kvh * a.G + row % a.G) * D : nullptr;
+            };
+            const auto limits = [&](int (&lim)[NT][2]) {   // the last token that each of the lane's rows sees
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int row = 8 * (NT * rt + n) + 2 * t + e, i = row / a.G;
+                        lim[n][e] = row < a.rows && i < q.n ? q.len + i : -1;
+                    }
             };
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                int last;
-                load_row<D>(row_of(n, &last), t, qf[n]);
+                load_row<D>(row_of(n), t, qf[n]);
                 const float back = row_to_f16<D, E4M3>(qf[n]) * unscaled;
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    f[n][e] = __shfl_sync(0xffffffffu, back, 4 * (2 * t + e));
-                    lim[n][e] = __shfl_sync(0xffffffffu, last, 4 * (2 * t + e));
-                }
+                for (int e = 0; e < 2; ++e) f[n][e] = __shfl_sync(0xffffffffu, back, 4 * (2 * t + e));
             }
             st.clear();
-            // the segment's scales, 32 tiles at a time, one batch ahead
-            const float *ksp = a.k_scale + unit * a.blocks, *vsp = a.v_scale + unit * a.blocks;
-            const auto scale_of = [&](const float* p, int from) {
-                const int k = from + lane;
-                return k < j1 && !q.open(k) ? p[k] : 0.f;
+            // the segment's scales, 16 tiles at a time, one batch ahead: the keys' in lanes
+            // 0 .. 15, the values' (split) in lanes 16 .. 31
+            const float* scales = (lane < 16 ? a.k_scale : a.v_scale) + unit * a.blocks;
+            const auto scale_of = [&](int from) {
+                const int k = from + (lane & 15);
+                return k < j1 && !q.open(k) ? scales[k] : 0.f;
             };
-            float ks_now = scale_of(ksp, at.j), vs_now = scale_of(vsp, at.j);
-            float ks_next = scale_of(ksp, at.j + 32), vs_next = scale_of(vsp, at.j + 32);
-            for (int j = at.j, it = 0; ok && j < j1; ++j, ++it) {
-                if (it == 32) {
+            float sc_next = scale_of(at.j + 16), sc = scale_of(at.j), ev_of;
+            {
+                float frac;
+                split_scale(sc, frac, ev_of);
+                if (lane >= 16) sc = frac;
+            }
+            const int full_end = min(j1, q.T / kCacheBlock);   // (the open block, if any, is the head's last)
+            for (int j = at.j, it = 0; ok && j < full_end; ++j, ++it) {
+                if (it == 16) {
                     it = 0;
-                    ks_now = ks_next;
-                    vs_now = vs_next;
-                    ks_next = scale_of(ksp, j + 32);
-                    vs_next = scale_of(vsp, j + 32);
+                    sc = sc_next;
+                    float frac;
+                    split_scale(sc, frac, ev_of);
+                    if (lane >= 16) sc = frac;
+                    sc_next = scale_of(j + 16);
                 }
                 const int base = j * kCacheBlock;
                 float s[NT][MT][4];
@@ -706,163 +740,176 @@ cache8_attn_kernel(const __grid_constant__ Cache8Args a) {
                     for (int i = 0; i < MT; ++i)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) s[n][i][e] = 0.f;
-                if (!q.open(j)) {
-                    const float ks = __shfl_sync(0xffffffffu, ks_now, it), vs = __shfl_sync(0xffffffffu, vs_now, it);
-                    const uint8_t* kt = wait_full();
-                    if (!kt) break;
+                const float ks = __shfl_sync(0xffffffffu, sc, it);
+                const float frac = __shfl_sync(0xffffffffu, sc, 16 + it), ev = __shfl_sync(0xffffffffu, ev_of, 16 + it);
+                const uint8_t* kt = wait_full();
+                if (!kt) break;
 #pragma unroll
-                    for (int i = 0; i < MT; ++i) {
-                        const uint8_t* r0 = kt + (key0 + 4 * i) * D + 16 * t;
-                        const uint8_t* r1 = r0 + pair_first<E4M3>() * D;
+                for (int i = 0; i < MT; ++i) {
+                    const uint8_t* r0 = kt + (key0 + 4 * i) * D + 16 * t;
+                    const uint8_t* r1 = r0 + pair_first<E4M3>() * D;
 #pragma unroll
-                        for (int c = 0; c < D / 64; ++c) {
-                            const uint4 x = *reinterpret_cast<const uint4*>(r0 + 64 * c);
-                            const uint4 y = *reinterpret_cast<const uint4*>(r1 + 64 * c);
-                            const uint32_t x4[4] = {x.x, x.y, x.z, x.w}, y4[4] = {y.x, y.y, y.z, y.w};
+                    for (int c = 0; c < D / 64; ++c) {
+                        const uint4 x = *reinterpret_cast<const uint4*>(r0 + 64 * c);
+                        const uint4 y = *reinterpret_cast<const uint4*>(r1 + 64 * c);
+                        const uint32_t x4[4] = {x.x, x.y, x.z, x.w}, y4[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                uint32_t w[4];
-                                codes_to_f16<E4M3>(x4[k], w[0], w[2]);
-                                codes_to_f16<E4M3>(y4[k], w[1], w[3]);
-#pragma unroll
-                                for (int n = 0; n < NT; ++n)
-                                    mma_f16(s[n][i], w, qf[n][4 * c + k][0], qf[n][4 * c + k][1]);
-                            }
-                        }
-                    }
-                    release();
-                    // (the first query row sees tokens up to len: tiles before need no mask)
-                    if (base + kCacheBlock - 1 > q.len)
-                        soften<D, NT, MT, E4M3, true>(s, f, ks, base + key0, lim, vs, st);
-                    else
-                        soften<D, NT, MT, E4M3, false>(s, f, ks, base + key0, lim, vs, st);
-                    uint32_t pf[NT][MT][2];
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int i = 0; i < MT; ++i)
-#pragma unroll
-                            for (int x = 0; x < 2; ++x)
-                                pf[n][i][x] = transpose8(pack_f16x2(s[n][i][2 * x], s[n][i][2 * x + 1]));
-                    const uint8_t* vt = wait_full();
-                    if (!vt) break;
-#pragma unroll
-                    for (int i = 0; i < D / 16; ++i) {
-                        const uint8_t* r = vt + (16 * i + g) * kCacheBlock + 16 * t + 4 * MT * kh;
-                        uint32_t x4[MT], y4[MT];
-                        if constexpr (MT == 4) {
-                            *reinterpret_cast<uint4*>(x4) = *reinterpret_cast<const uint4*>(r);
-                            *reinterpret_cast<uint4*>(y4) = *reinterpret_cast<const uint4*>(r + 8 * kCacheBlock);
-                        } else {
-                            *reinterpret_cast<uint2*>(x4) = *reinterpret_cast<const uint2*>(r);
-                            *reinterpret_cast<uint2*>(y4) = *reinterpret_cast<const uint2*>(r + 8 * kCacheBlock);
-                        }
-#pragma unroll
-                        for (int k = 0; k < MT; ++k) {
+                        for (int k = 0; k < 4; ++k) {
                             uint32_t w[4];
                             codes_to_f16<E4M3>(x4[k], w[0], w[2]);
                             codes_to_f16<E4M3>(y4[k], w[1], w[3]);
 #pragma unroll
-                            for (int n = 0; n < NT; ++n) mma_f16(st.o[n][i], w, pf[n][k][0], pf[n][k][1]);
+                            for (int n = 0; n < NT; ++n)
+                                mma_f16(s[n][i], w, qf[n][4 * c + k][0], qf[n][4 * c + k][1]);
                         }
                     }
-                    release();
+                }
+                release();
+                // (the first query row sees tokens up to len: tiles before need no mask)
+                int lim[NT][2] = {};
+                if (base + kCacheBlock - 1 > q.len) {
+                    limits(lim);
+                    soften<D, NT, MT, E4M3, true>(s, f, ks, base + key0, lim, frac, ev, st);
                 } else {
-                    // the open block, in bf16: keys [64][D], values [D][64], each in two stages
-                    uint32_t qb[NT][D / 16][2];
+                    soften<D, NT, MT, E4M3, false>(s, f, ks, base + key0, lim, frac, ev, st);
+                }
+                uint32_t pf[NT][MT][2];
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        int last;
-                        load_row<D>(row_of(n, &last), t, qb[n]);
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int i = 0; i < MT; ++i)
+#pragma unroll
+                        for (int x = 0; x < 2; ++x)
+                            pf[n][i][x] = transpose8(pack_f16x2(s[n][i][2 * x], s[n][i][2 * x + 1]));
+                const uint8_t* vt = wait_full();
+                if (!vt) break;
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) {
+                    const uint8_t* r = vt + (16 * i + g) * kCacheBlock + 16 * t + 4 * MT * kh;
+                    uint32_t x4[MT], y4[MT];
+                    if constexpr (MT == 4) {
+                        *reinterpret_cast<uint4*>(x4) = *reinterpret_cast<const uint4*>(r);
+                        *reinterpret_cast<uint4*>(y4) = *reinterpret_cast<const uint4*>(r + 8 * kCacheBlock);
+                    } else {
+                        *reinterpret_cast<uint2*>(x4) = *reinterpret_cast<const uint2*>(r);
+                        *reinterpret_cast<uint2*>(y4) = *reinterpret_cast<const uint2*>(r + 8 * kCacheBlock);
                     }
-                    const uint8_t* k0 = wait_full();
-                    if (!k0) break;
-                    const uint8_t* k1 = wait_full();
-                    if (!k1) break;
-                    const uint8_t* half = g < 4 ? k0 : k1 - 32 * D * 2;   // tokens 16 (g / 2) ..: first or second 32
 #pragma unroll
-                    for (int i = 0; i < MT; ++i) {
-                        const uint8_t* r0 = half + (key0 + 4 * i) * D * 2 + 32 * t;
-                        const uint8_t* r1 = r0 + pair_first<E4M3>() * D * 2;
+                    for (int k = 0; k < MT; ++k) {
+                        uint32_t w[4];
+                        codes_to_f16<E4M3>(x4[k], w[0], w[2]);
+                        codes_to_f16<E4M3>(y4[k], w[1], w[3]);
 #pragma unroll
-                        for (int c = 0; c < D / 64; ++c)
-#pragma unroll
-                            for (int k = 0; k < 2; ++k) {
-                                const uint4 x = *reinterpret_cast<const uint4*>(r0 + 128 * c + 16 * k);
-                                const uint4 y = *reinterpret_cast<const uint4*>(r1 + 128 * c + 16 * k);
-                                const uint32_t w0[4] = {x.x, y.x, x.y, y.y}, w1[4] = {x.z, y.z, x.w, y.w};
-#pragma unroll
-                                for (int n = 0; n < NT; ++n) {
-                                    const int ko = 4 * c + 2 * k;
-                                    mma_bf16(s[n][i], w0, qb[n][ko][0], qb[n][ko][1]);
-                                    mma_bf16(s[n][i], w1, qb[n][ko + 1][0], qb[n][ko + 1][1]);
-                                }
-                            }
+                        for (int n = 0; n < NT; ++n) mma_f16(st.o[n][i], w, pf[n][k][0], pf[n][k][1]);
                     }
-                    release();
-                    release();
-                    float fo[NT][2];
+                }
+                release();
+            }
+            while (ok && j1 > full_end) {   // (once: `break` where a wait ran out)
+                const int base = full_end * kCacheBlock;
+                float s[NT][MT][4];
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) fo[n][0] = fo[n][1] = unscaled;
-                    soften<D, NT, MT, E4M3, true>(s, fo, 1.f, base + key0, lim, 1.f, st);
-                    // each weight as two bf16 parts
-                    uint32_t wh[NT][MT][2], wl[NT][MT][2];
+                for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int n = 0; n < NT; ++n)
+                    for (int i = 0; i < MT; ++i)
 #pragma unroll
-                        for (int i = 0; i < MT; ++i)
+                        for (int e = 0; e < 4; ++e) s[n][i][e] = 0.f;
+                // the open block, in bf16: keys [64][D], values [D][64], each in two stages
+                uint32_t qb[NT][D / 16][2];
 #pragma unroll
-                            for (int x = 0; x < 2; ++x) {
-                                const float p0 = s[n][i][2 * x], p1 = s[n][i][2 * x + 1];
-                                const uint32_t h = pack_bf16x2(p0, p1);
-                                wh[n][i][x] = transpose8(h);
-                                wl[n][i][x] = transpose8(pack_bf16x2(p0 - __uint_as_float(h << 16),
-                                                                     p1 - __uint_as_float(h & 0xffff0000u)));
-                            }
-                    // slots past the sequence's end hold whatever was there before: zero, not 0 * NaN
-                    uint32_t keep[2 * MT];
+                for (int n = 0; n < NT; ++n) {
+                    load_row<D>(row_of(n), t, qb[n]);
+                }
+                const uint8_t* k0 = wait_full();
+                if (!k0) break;
+                const uint8_t* k1 = wait_full(1);
+                if (!k1) break;
+                const uint8_t* half = g < 4 ? k0 : k1 - 32 * D * 2;   // tokens 16 (g / 2) ..: first or second 32
 #pragma unroll
-                    for (int k = 0; k < 2 * MT; ++k) {
-                        const int over = q.T - (base + 16 * t + 4 * MT * kh + 2 * k);
-                        keep[k] = over > 1 ? 0xffffffffu : (over == 1 ? 0x0000ffffu : 0u);
-                    }
-                    const uint8_t* v0 = wait_full();
-                    if (!v0) break;
-                    const uint8_t* v1 = wait_full();
-                    if (!v1) break;
+                for (int i = 0; i < MT; ++i) {
+                    const uint8_t* r0 = half + (key0 + 4 * i) * D * 2 + 32 * t;
+                    const uint8_t* r1 = r0 + pair_first<E4M3>() * D * 2;
 #pragma unroll
-                    for (int i = 0; i < D / 16; ++i) {
-                        const uint8_t* r = (i < D / 32 ? v0 : v1) + (16 * (i % (D / 32)) + g) * kCacheBlock * 2 +
-                                           32 * t + 8 * MT * kh;
+                    for (int c = 0; c < D / 64; ++c)
 #pragma unroll
-                        for (int k = 0; k < MT / 2; ++k) {
-                            uint4 x = *reinterpret_cast<const uint4*>(r + 16 * k);
-                            uint4 y = *reinterpret_cast<const uint4*>(r + 8 * kCacheBlock * 2 + 16 * k);
-                            x.x &= keep[4 * k];
-                            x.y &= keep[4 * k + 1];
-                            x.z &= keep[4 * k + 2];
-                            x.w &= keep[4 * k + 3];
-                            y.x &= keep[4 * k];
-                            y.y &= keep[4 * k + 1];
-                            y.z &= keep[4 * k + 2];
-                            y.w &= keep[4 * k + 3];
-                            pair_up<E4M3>(x.x, x.y);
-                            pair_up<E4M3>(x.z, x.w);
-                            pair_up<E4M3>(y.x, y.y);
-                            pair_up<E4M3>(y.z, y.w);
+                        for (int k = 0; k < 2; ++k) {
+                            const uint4 x = *reinterpret_cast<const uint4*>(r0 + 128 * c + 16 * k);
+                            const uint4 y = *reinterpret_cast<const uint4*>(r1 + 128 * c + 16 * k);
                             const uint32_t w0[4] = {x.x, y.x, x.y, y.y}, w1[4] = {x.z, y.z, x.w, y.w};
 #pragma unroll
                             for (int n = 0; n < NT; ++n) {
-                                mma_bf16(st.o[n][i], w0, wh[n][2 * k][0], wh[n][2 * k][1]);
-                                mma_bf16(st.o[n][i], w0, wl[n][2 * k][0], wl[n][2 * k][1]);
-                                mma_bf16(st.o[n][i], w1, wh[n][2 * k + 1][0], wh[n][2 * k + 1][1]);
-                                mma_bf16(st.o[n][i], w1, wl[n][2 * k + 1][0], wl[n][2 * k + 1][1]);
+                                const int ko = 4 * c + 2 * k;
+                                mma_bf16(s[n][i], w0, qb[n][ko][0], qb[n][ko][1]);
+                                mma_bf16(s[n][i], w1, qb[n][ko + 1][0], qb[n][ko + 1][1]);
                             }
                         }
-                    }
-                    release();
-                    release();
                 }
+                release();
+                release();
+                float fo[NT][2];
+#pragma unroll
+                for (int n = 0; n < NT; ++n) fo[n][0] = fo[n][1] = unscaled;
+                int lim[NT][2];
+                limits(lim);
+                soften<D, NT, MT, E4M3, true>(s, fo, 1.f, base + key0, lim, 1.f, 0.f, st);
+                // each weight as two bf16 parts
+                uint32_t wh[NT][MT][2], wl[NT][MT][2];
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int i = 0; i < MT; ++i)
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            const float p0 = s[n][i][2 * x], p1 = s[n][i][2 * x + 1];
+                            const uint32_t h = pack_bf16x2(p0, p1);
+                            wh[n][i][x] = transpose8(h);
+                            wl[n][i][x] = transpose8(pack_bf16x2(p0 - __uint_as_float(h << 16),
+                                                                 p1 - __uint_as_float(h & 0xffff0000u)));
+                        }
+                // slots past the sequence's end hold whatever was there before: zero, not 0 * NaN
+                uint32_t keep[2 * MT];
+#pragma unroll
+                for (int k = 0; k < 2 * MT; ++k) {
+                    const int over = q.T - (base + 16 * t + 4 * MT * kh + 2 * k);
+                    keep[k] = over > 1 ? 0xffffffffu : (over == 1 ? 0x0000ffffu : 0u);
+                }
+                const uint8_t* v0 = wait_full();
+                if (!v0) break;
+                const uint8_t* v1 = wait_full(1);
+                if (!v1) break;
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) {
+                    const uint8_t* r = (i < D / 32 ? v0 : v1) + (16 * (i % (D / 32)) + g) * kCacheBlock * 2 +
+                                       32 * t + 8 * MT * kh;
+#pragma unroll
+                    for (int k = 0; k < MT / 2; ++k) {
+                        uint4 x = *reinterpret_cast<const uint4*>(r + 16 * k);
+                        uint4 y = *reinterpret_cast<const uint4*>(r + 8 * kCacheBlock * 2 + 16 * k);
+                        x.x &= keep[4 * k];
+                        x.y &= keep[4 * k + 1];
+                        x.z &= keep[4 * k + 2];
+                        x.w &= keep[4 * k + 3];
+                        y.x &= keep[4 * k];
+                        y.y &= keep[4 * k + 1];
+                        y.z &= keep[4 * k + 2];
+                        y.w &= keep[4 * k + 3];
+                        pair_up<E4M3>(x.x, x.y);
+                        pair_up<E4M3>(x.z, x.w);
+                        pair_up<E4M3>(y.x, y.y);
+                        pair_up<E4M3>(y.z, y.w);
+                        const uint32_t w0[4] = {x.x, y.x, x.y, y.y}, w1[4] = {x.z, y.z, x.w, y.w};
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            mma_bf16(st.o[n][i], w0, wh[n][2 * k][0], wh[n][2 * k][1]);
+                            mma_bf16(st.o[n][i], w0, wl[n][2 * k][0], wl[n][2 * k][1]);
+                            mma_bf16(st.o[n][i], w1, wh[n][2 * k + 1][0], wh[n][2 * k + 1][1]);
+                            mma_bf16(st.o[n][i], w1, wl[n][2 * k + 1][0], wl[n][2 * k + 1][1]);
+                        }
+                    }
+                }
+                release();
+                release();
+                break;
             }
 
             // ---- the segment's rows into the team's slot, merged where two warps shared the tokens
@@ -893,7 +940,7 @@ cache8_attn_kernel(const __grid_constant__ Cache8Args a) {
             const bool whole = at.j == 0 && j1 == at.tiles, final = j1 - at.j == at.left;
             // (the share's last part: the ring is empty and holds the second warp's rows)
             float* spare = reinterpret_cast<float*>(smem + (size_t)team * a.stages * STAGE);
-            const bool apart = C::KS == 2 && final && !whole;
+            const bool apart = C::KS == 2 && final && !whole && !by_team;
             if (C::KS == 2 && !apart && kh == 1) put(slot);
             if (C::KS == 1 || (apart && kh == 0)) put(slot);
             ok = named_bar_and(1 + team, team_threads, ok && !*abort_flag);
@@ -936,13 +983,50 @@ cache8_attn_kernel(const __grid_constant__ Cache8Args a) {
                     finish<D>(a, at.b, at.kvh, q.n, row, col, out_scale(x.x, x.y, x.z),
                               *reinterpret_cast<const float4*>(from + col));
                 }
-            } else if (!final) {
-                float* to = a.piece + ((long long)blockIdx.x * teams + team) * a.rows * STRIDE;
+            } else if (by_team) {
+                const int u0 = here - at.j, n = me * teams + team;
+                float4* to = reinterpret_cast<float4*>(team_part(n, u0));
                 for (int idx = team_tid; idx < a.rows * (STRIDE / 4); idx += team_threads)
-                    reinterpret_cast<float4*>(to)[idx] = reinterpret_cast<const float4*>(slot)[idx];
-                kept = to;
+                    to[idx] = reinterpret_cast<const float4*>(slot)[idx];
+                named_bar_sync(1 + team, team_threads);
+                const int n0 = deal.taker(u0), n1 = deal.taker(u0 + at.tiles - 1);
+                if (team_tid == 0) {
+                    __threadfence();   // (after the barrier: covers what every thread of the team has written)
+                    s_last[team] = atomicAdd(a.counters + unit, 1) == n1 - n0;
+                    __threadfence();
+                }
+                named_bar_sync(1 + team, team_threads);
+                if (s_last[team]) {
+                    if (a.gate_mode != GSDPA_GATE_NONE) pdl_wait();
+                    for (int idx = team_tid; idx < a.rows * (D / 4); idx += team_threads) {
+                        const int row = idx / (D / 4), col = 4 * (idx % (D / 4));
+                        float m = -INFINITY, l = 0.f, M = -INFINITY;
+                        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+                        for (int k = n0; k <= n1; ++k) {
+                            const float* from = team_part(k, u0) + row * STRIDE;
+                            const float4 x = __ldcg(reinterpret_cast<const float4*>(from + D));
+                            const float4 v = __ldcg(reinterpret_cast<const float4*>(from + col));
+                            const float mn = fmaxf(m, x.x), Mn = fmaxf(M, x.z);
+                            const float oa = part_weight(M, Mn), ob = part_weight(x.z, Mn);
+                            l = l * part_weight(m, mn) + x.y * part_weight(x.x, mn);
+                            m = mn;
+                            M = Mn;
+                            o.x = o.x * oa + v.x * ob;
+                            o.y = o.y * oa + v.y * ob;
+                            o.z = o.z * oa + v.z * ob;
+                            o.w = o.w * oa + v.w * ob;
+                        }
+                        finish<D>(a, at.b, at.kvh, q.n, row, col, out_scale(m, l, M), o);
+                    }
+                }
+            } else if (!final) {
+                float4* to = reinterpret_cast<float4*>(team_part(me * teams + team, here));
+                for (int idx = team_tid; idx < a.rows * (STRIDE / 4); idx += team_threads)
+                    to[idx] = reinterpret_cast<const float4*>(slot)[idx];
+                kept = reinterpret_cast<const float*>(to);
             }
-            if (!whole && team_tid == 0) {
+            if (!whole && !by_team && team_tid == 0) {
                 Piece& p = s_piece[2 * team + (final ? 1 : 0)];
                 p.rows = kept;
                 p.rows2 = apart ? spare : nullptr;
@@ -962,122 +1046,60 @@ cache8_attn_kernel(const __grid_constant__ Cache8Args a) {
         pdl_wait();
         return;
     }
-    // Neighbouring parts of one head are a group. Every warp finds the groups for
-    // itself: a lane stands for a source of rows (lane % 16: the part, upper
-    // half: its second warp's rows), heads has the bit of each group's first part.
-    const int piece = lane % (2 * kSlots);
-    const float* rows_at = lane < 2 * kSlots ? s_piece[piece].rows : s_piece[piece].rows2;
-    const uint32_t sources = __ballot_sync(0xffffffffu, rows_at != nullptr);
-    const uint32_t parts = sources & 0xffffu, below = parts & ((1u << piece) - 1);
-    const int u0_here = s_piece[piece].u0;
-    const int u0_below = __shfl_sync(0xffffffffu, u0_here, below ? 31 - __clz(below) : piece);
-    const uint32_t heads = __ballot_sync(0xffffffffu, lane < 2 * kSlots && rows_at && (!below || u0_below != u0_here));
-    const int groups = __popc(heads), items = a.rows * (D / 4);
-    const auto part_of = [&](int c, int u0) {   // CTA c's part of the head at u0
-        return a.part + (long long)(2 * c + (u0 <= deal.from(c) ? 0 : 1)) * a.rows * STRIDE;
-    };
-    // The parts' weights and the sums' state of each (group, row), a warp to each;
-    // kept in the ring behind the second warp's rows of the first team.
-    float* weight = reinterpret_cast<float*>(smem) + (C::KS == 2 ? a.rows * STRIDE : 0);   // [groups][rows][32]
-    float4* state = reinterpret_cast<float4*>(weight + groups * a.rows * 32);              // m, l, M, output scale
-    for (int k = warp; k < groups * a.rows; k += C::WARPS) {
-        const int gr = k / a.rows, row = k % a.rows;
-        const bool in = rows_at && __popc(heads & ((2u << piece) - 1)) == gr + 1;
-        float4 x = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
-        if (in) x = *reinterpret_cast<const float4*>(rows_at + row * STRIDE + D);
-        float m = x.x, M = x.z;
-#pragma unroll
-        for (int sh = 1; sh < 32; sh <<= 1) {
-            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, sh));
-            M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, sh));
-        }
-        float l = x.y * part_weight(x.x, m);
-        weight[k * 32 + lane] = part_weight(x.z, M);
-#pragma unroll
-        for (int sh = 1; sh < 32; sh <<= 1) l += __shfl_xor_sync(0xffffffffu, l, sh);
-        if (lane == 0) state[k] = make_float4(m, l, M, out_scale(m, l, M));
-    }
+    // Merged twice by the same code: first the CTA's parts, then the parts of the
+    // heads that its ends cut, where it is the last to arrive. Sources (pointers
+    // to rows) of one head are a group; all of it in the ring, behind the second
+    // warp's rows of the first team.
     pdl_wait();   // the gate logits; and the next kernel on the stream may rely on the gate kernel having ended
-    sync_all();
-    for (int idx = tid; idx < groups * items; idx += kConsumers) {
-        const int gr = idx / items, row = idx % items / (D / 4), col = 4 * (idx % (D / 4));
-        uint32_t rest = heads;
-        for (int k = 0; k < gr; ++k) rest &= rest - 1;
-        const uint32_t after = rest & (rest - 1);
-        const uint32_t range = (after ? (after & (0u - after)) - 1 : 0xffffu) & ~((rest & (0u - rest)) - 1);
-        uint32_t todo = sources & (range | (range << 16));
-        const float* w = weight + (gr * a.rows + row) * 32;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        while (todo) {   // four sources at a time
-            float4 v[4];
-            float f[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int i = todo ? __ffs(todo) - 1 : -1;
-                f[k] = 0.f;
-                v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (i >= 0) {
-                    const float* from = i < 2 * kSlots ? s_piece[i].rows : s_piece[i - 2 * kSlots].rows2;
-                    v[k] = *reinterpret_cast<const float4*>(from + row * STRIDE + col);
-                    f[k] = w[i];
-                }
-                todo &= todo - 1;
-            }
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                o.x += v[k].x * f[k];
-                o.y += v[k].y * f[k];
-                o.z += v[k].z * f[k];
-                o.w += v[k].w * f[k];
-            }
+    const int items = a.rows * (D / 4);
+    const auto part_of = [&](int c, int u0) {   // CTA c's part of the head at u0
+        return a.part + (long long)(2 * c + (u0 <= deal.from(c * teams) ? 0 : 1)) * a.rows * STRIDE;
+    };
+    const float** source = reinterpret_cast<const float**>(smem + (C::KS == 2 ? a.rows * STRIDE * 4 : 0));
+    float* weight = reinterpret_cast<float*>(source + kMaxCtas + 2);                          // [sources][rows]
+    int groups = 0;
+    if (warp == 0) {
+        // a lane stands for a source (lane % 16: the part, upper half: its second warp's rows)
+        const int piece = lane % (2 * kSlots);
+        const bool upper = lane >= 2 * kSlots;
+        const float* at = upper ? s_piece[piece].rows2 : s_piece[piece].rows;
+        const uint32_t there = __ballot_sync(0xffffffffu, at != nullptr);
+        const uint32_t lower = there & 0xffffu, under = (1u << piece) - 1;
+        const int u0 = s_piece[piece].u0, before_me = (lower & under) ? 31 - __clz(lower & under) : piece;
+        const int u0_before = __shfl_sync(0xffffffffu, u0, before_me);
+        const bool head = !upper && at && (!(lower & under) || u0_before != u0);
+        const uint32_t heads = __ballot_sync(0xffffffffu, head);
+        const int place = __popc(lower & under) + __popc((there >> 16) & under) + (upper ? (int)((lower >> piece) & 1u) : 0);
+        if (at) source[place] = at;
+        if (head) {
+            Group& gr = s_group[__popc(heads & under)];
+            gr.first = place;
+            gr.u0 = u0;
+            gr.b = s_piece[piece].b;
+            gr.kvh = s_piece[piece].kvh;
         }
-        const float4 x = state[gr * a.rows + row];
-        const Piece& p = s_piece[__ffs(rest) - 1];
-        const SeqTiles q(a, p.b);
-        if (p.u0 >= lo && p.u0 + q.tiles <= hi) {
-            finish<D>(a, p.b, p.kvh, q.n, row, col, x.w, o);
-        } else {
-            float* to = part_of(me, p.u0) + row * STRIDE;
-            *reinterpret_cast<float4*>(to + col) = o;
-            if (col == 0) *reinterpret_cast<float4*>(to + D) = x;
+        if (lane == 0) {
+            s_groups = __popc(heads);
+            s_group[__popc(heads)].first = __popc(there);
         }
     }
-    // ---- the heads that the CTA's ends cut: the first and the last group
-    sync_all();   // (and the ring and the slots are free from here on)
-    const int ends[2] = {__ffs(heads) - 1, 31 - __clz(heads)};
-    if (tid < 2) {
-        int last = 0;
-        if (groups > tid) {
-            const Piece& p = s_piece[ends[tid]];
-            const int u1 = p.u0 + SeqTiles(a, p.b).tiles;
-            if (p.u0 < lo || u1 > hi) {
-                __threadfence();   // (after the barrier: covers what every thread has written)
-                last = atomicAdd(a.counters + (long long)p.b * a.Hkv + p.kvh, 1) == deal.taker(u1 - 1) - deal.taker(p.u0);
-                __threadfence();
-            }
-        }
-        s_last[tid] = last;
-    }
-    sync_all();
-    for (int e = 0; e < 2; ++e) {
-        if (!s_last[e]) continue;
-        const Piece& p = s_piece[ends[e]];
-        const SeqTiles q(a, p.b);
-        const int c0 = deal.taker(p.u0), count = deal.taker(p.u0 + q.tiles - 1) - c0 + 1;
-        // each part's weight and each row's scale, a warp to a row
-        float* weight = reinterpret_cast<float*>(smem);            // [rows][count]
-        float* scale = weight + a.rows * count;                    // [rows]
-        float* sums = weight + ((a.rows * (count + 1) + 3) & ~3);  // [split][items] of 4 floats
-        for (int row = warp; row < a.rows; row += C::WARPS) {
+    for (int pass = 0;; ++pass) {
+        sync_all();
+        groups = s_groups;
+        const int total = s_group[groups].first;
+        float4* state = reinterpret_cast<float4*>(weight + ((total * a.rows + 3) & ~3));   // [groups][rows]: m, l, M, scale
+        // the sources' weights and each row's sums, a warp to a row
+        for (int k = warp; k < groups * a.rows; k += C::WARPS) {
+            const int gr = k / a.rows, row = k % a.rows, i0 = s_group[gr].first, i1 = s_group[gr + 1].first;
             float m = -INFINITY, M = -INFINITY, l = 0.f;
             float4 x[(kMaxCtas + 31) / 32];
 #pragma unroll
-            for (int k = 0; k < (kMaxCtas + 31) / 32; ++k) {
-                const int c = 32 * k + lane;
-                x[k] = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
-                if (c < count) x[k] = __ldcg(reinterpret_cast<const float4*>(part_of(c0 + c, p.u0) + row * STRIDE + D));
-                m = fmaxf(m, x[k].x);
-                M = fmaxf(M, x[k].z);
+            for (int c = 0; c < (kMaxCtas + 31) / 32; ++c) {
+                const int i = i0 + 32 * c + lane;
+                x[c] = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
+                if (i < i1) x[c] = *reinterpret_cast<const float4*>(source[i] + row * STRIDE + D);
+                m = fmaxf(m, x[c].x);
+                M = fmaxf(M, x[c].z);
             }
 #pragma unroll
             for (int sh = 1; sh < 32; sh <<= 1) {
@@ -1085,48 +1107,90 @@ cache8_attn_kernel(const __grid_constant__ Cache8Args a) {
                 M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, sh));
             }
 #pragma unroll
-            for (int k = 0; k < (kMaxCtas + 31) / 32; ++k) {
-                const int c = 32 * k + lane;
-                l += x[k].y * part_weight(x[k].x, m);
-                if (c < count) weight[row * count + c] = part_weight(x[k].z, M);
+            for (int c = 0; c < (kMaxCtas + 31) / 32; ++c) {
+                const int i = i0 + 32 * c + lane;
+                l += x[c].y * part_weight(x[c].x, m);
+                if (i < i1) weight[i * a.rows + row] = part_weight(x[c].z, M);
             }
 #pragma unroll
             for (int sh = 1; sh < 32; sh <<= 1) l += __shfl_xor_sync(0xffffffffu, l, sh);
-            if (lane == 0) scale[row] = out_scale(m, l, M);
+            if (lane == 0) state[k] = make_float4(m, l, M, out_scale(m, l, M));
         }
         sync_all();
-        // the weighted sum, the parts split over the threads that would be idle
-        const int split = items < kConsumers ? kConsumers / items : 1;
-        for (int idx = tid; idx < split * items; idx += kConsumers) {
-            const int sub = idx / items, row = idx % items / (D / 4), col = 4 * (idx % (D / 4));
+        // the weighted sums; a column's sources are split over lanes that would be idle
+        int split = 1;
+        while (split < 8 && 2 * split * groups * items <= kConsumers) split *= 2;
+        for (int idx = tid; idx < groups * items * split; idx += kConsumers) {
+            const int sub = idx % split, item = idx / split;
+            const int gr = item / items, row = item % items / (D / 4), col = 4 * (item % (D / 4));
+            const int i1 = s_group[gr + 1].first;
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
-            for (int c = sub; c < count; c += split) {
-                const float4 v = __ldcg(reinterpret_cast<const float4*>(part_of(c0 + c, p.u0) + row * STRIDE + col));
-                const float w = weight[row * count + c];
+            for (int i = s_group[gr].first + sub; i < i1; i += split) {
+                const float4 v = *reinterpret_cast<const float4*>(source[i] + row * STRIDE + col);
+                const float w = weight[i * a.rows + row];
                 o.x += v.x * w;
                 o.y += v.y * w;
                 o.z += v.z * w;
                 o.w += v.w * w;
             }
-            if (split == 1) finish<D>(a, p.b, p.kvh, q.n, row, col, scale[row], o);
-            else reinterpret_cast<float4*>(sums)[idx] = o;
+            for (int sh = 1; sh < split; sh <<= 1) {   // (a whole warp: items come in sixteens)
+                o.x += __shfl_xor_sync(0xffffffffu, o.x, sh);
+                o.y += __shfl_xor_sync(0xffffffffu, o.y, sh);
+                o.z += __shfl_xor_sync(0xffffffffu, o.z, sh);
+                o.w += __shfl_xor_sync(0xffffffffu, o.w, sh);
+            }
+            if (sub != 0) continue;
+            const Group& gp = s_group[gr];
+            const float4 x = state[gr * a.rows + row];
+            const SeqTiles q(a, gp.b);
+            if (pass == 1 || (gp.u0 >= lo && gp.u0 + q.tiles <= hi)) {
+                finish<D>(a, gp.b, gp.kvh, q.n, row, col, x.w, o);
+            } else {
+                float* to = part_of(me, gp.u0) + row * STRIDE;
+                *reinterpret_cast<float4*>(to + col) = o;
+                if (col == 0) *reinterpret_cast<float4*>(to + D) = x;
+            }
+        }
+        if (pass == 1) break;
+        // the heads that the CTA's ends cut are the first and the last group
+        sync_all();
+        if (tid < 2) {
+            int last = 0;
+            if (groups > tid) {
+                const Group& gp = s_group[tid == 0 ? 0 : groups - 1];
+                const int u1 = gp.u0 + SeqTiles(a, gp.b).tiles;
+                if (gp.u0 < lo || u1 > hi) {
+                    __threadfence();   // (after the barrier: covers what every thread has written)
+                    last = atomicAdd(a.counters + (long long)gp.b * a.Hkv + gp.kvh, 1) ==
+                           deal.taker(u1 - 1) / teams - deal.taker(gp.u0) / teams;
+                    __threadfence();
+                }
+            }
+            s_last[tid] = last;
         }
         sync_all();
-        if (split > 1) {
-            for (int idx = tid; idx < items; idx += kConsumers) {
-                const int row = idx / (D / 4), col = 4 * (idx % (D / 4));
-                float4 o = reinterpret_cast<const float4*>(sums)[idx];
-                for (int k = 1; k < split; ++k) {
-                    const float4 v = reinterpret_cast<const float4*>(sums)[k * items + idx];
-                    o.x += v.x;
-                    o.y += v.y;
-                    o.z += v.z;
-                    o.w += v.w;
-                }
-                finish<D>(a, p.b, p.kvh, q.n, row, col, scale[row], o);
+        const bool first = s_last[0], second = s_last[1];
+        if (!first && !second) break;
+        const Group g0 = s_group[0], g1 = s_group[groups - 1];
+        const auto cta_of = [&](int x) { return deal.taker(x) / teams; };
+        const int c0 = cta_of(g0.u0), n0 = first ? cta_of(g0.u0 + SeqTiles(a, g0.b).tiles - 1) - c0 + 1 : 0;
+        const int c1 = cta_of(g1.u0), n1 = second ? cta_of(g1.u0 + SeqTiles(a, g1.b).tiles - 1) - c1 + 1 : 0;
+        sync_all();   // (everyone has read the groups)
+        for (int i = tid; i < n0 + n1; i += kConsumers)
+            source[i] = i < n0 ? part_of(c0 + i, g0.u0) : part_of(c1 + i - n0, g1.u0);
+        if (tid == 0) {
+            int n = 0;
+            if (first) {
+                s_group[n] = g0;
+                s_group[n++].first = 0;
             }
-            sync_all();   // (the next head's sums may be written)
+            if (second) {
+                s_group[n] = g1;
+                s_group[n++].first = n0;
+            }
+            s_group[n].first = n0 + n1;
+            s_groups = n;
         }
     }
 
@@ -1203,7 +1267,7 @@ int plan_cache8(const gsdpa_cache8* c, int Lq, int d_model, int Hq, int gate_mod
     if (gate_mode != GSDPA_GATE_NONE) plan_gate_rows(p, plan_sms(), &o.w);
     o.w.gate_part = take(sizeof(float) * (size_t)o.w.gate_splits * o.w.gate_rows * o.w.gate_cols);
     const size_t part = sizeof(float) * (size_t)rows * (c->d_k + 4);
-    o.piece = take(part * plan_sms() * (kSlots / shape_of((int)rows, c->d_k).R));
+    o.piece = take(part * plan_sms() * 2 * (kSlots / shape_of((int)rows, c->d_k).R));
     o.part = take(part * plan_sms() * 2);
     o.n_counters = c->B * c->H_kv;
     o.counters = take(sizeof(int) * (size_t)o.n_counters);
@@ -1314,7 +1378,7 @@ int gated_sdpa_cache8(const void* X, const void* Q, const gsdpa_cache8* cache, c
     a.ctl.err = rt.err;
     a.ctl.limit_ns = rt.limit_ns;
     // one CTA per SM, fewer where a full cache would not give each its tiles
-    const long long most = ((long long)a.B * a.Hkv * a.blocks + kMinTiles - 1) / kMinTiles;
+    const long long most = (long long)a.B * a.Hkv * ((a.blocks + kSlots / a.R - 1) / (kSlots / a.R));
     long long grid = rt.num_sms < plan_sms() ? rt.num_sms : plan_sms();
     if (grid > most) grid = most;
     if (grid > kMaxCtas) grid = kMaxCtas;

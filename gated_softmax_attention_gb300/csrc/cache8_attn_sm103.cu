@@ -64,6 +64,11 @@ constexpr int kSlots = 8;            // warps' parts in the merge buffer
 constexpr int kMaxRows = 128;        // query rows (heads of a group x new tokens) per K/V head
 constexpr int kMaxStages = 16;       // ring stages per team
 constexpr int kMaxCtas = 160;        // most CTAs (plan_sms)
+constexpr int kFanOne = 16;          // most CTAs whose parts of a head are merged at once
+constexpr int kFan = 8;              // ... else this many neighbours' at first
+constexpr int kMaxSources = 64;      // 2 heads' parts: of a CTA's warps, of kFanOne CTAs, or of kMaxCtas / kFan groups
+constexpr int kMaxGroups = 18;       // heads that a CTA has parts of, and one more; an even number
+static_assert((kMaxCtas + kFan - 1) / kFan <= 32 && kFanOne <= 32, "a lane to a source");
 constexpr int kTeamParts = 12;       // most teams to a head (about) for them to merge it without their CTAs
 constexpr int kWholeTiles = 16;      // most tiles of a head for one CTA to take it alone (see below)
 constexpr int kBars = 48;            // ring stages of all teams
@@ -79,14 +84,16 @@ struct Cache8Args {
     const float *k_scale, *v_scale;
     const __nv_bfloat16 *k_tail, *v_tail;
     int B, Lq, Hq, Hkv, G;           // G = Hq / Hkv
+    int g_inverse;                   // 65536 / G, rounded up: row / G is row * g_inverse >> 16 for the rows there are
     int rows;                        // G * Lq
     int blocks, capacity;
+    int lg_teams;                    // teams of a CTA, 2^lg_teams = 8 / R
     int R, stages;                   // groups of query rows (of 8 NT) to a team; ring stages per team
     const float* gate_part;          // [gate_splits, B * Lq, gate_cols] or null
     int gate_splits, gate_cols, gate_mode;
     float* piece;                    // [CTAs][teams][2][rows][D + 4]: a team's first and last head
     float* part;                     // [CTAs][2][rows][D + 4]: a CTA's first and last head
-    int* counters;                   // [B * Hkv]
+    int* counters;                   // [B * Hkv], then [2 * CTAs]
     int wait_first;                  // no gate kernel: everything before this kernel is waited for at once
     WaitCtl ctl;
 };
@@ -390,9 +397,9 @@ __device__ __forceinline__ float out_scale(float m, float l, float M) {
 template <int D>
 __device__ __forceinline__ void finish(const Cache8Args& a, int b, int kvh, int n, int row, int col, float k,
                                        const float4& o) {
-    const int i = row / a.G;
+    const int i = row * a.g_inverse >> 16;
     if (i >= n) return;
-    const int h = kvh * a.G + row % a.G;
+    const int h = (kvh - i) * a.G + row;   // kvh G + row % G
     float y[4] = {o.x * k, o.y * k, o.z * k, o.w * k};
     const long long token = (long long)b * a.Lq + i;
     if (a.gate_mode != GSDPA_GATE_NONE) {
@@ -448,9 +455,21 @@ struct Piece {
     int b, kvh;
 };
 
-// Sources of one head, up to the next group's first.
+// Sources of one head, up to the next group's first; where the merged rows go
+// (null: they are the output), n tokens of the step.
 struct Group {
-    int first, u0, b, kvh;
+    float* dest;
+    int first, b, kvh, n;
+};
+static_assert(sizeof(Group) * kMaxGroups % 16 == 0 && kMaxGroups > 2 * kSlots, "what follows is 16-byte aligned");
+
+// An end of a CTA's share that cuts a head: the head, the CTAs that have parts
+// of it, how far its merge is (0 nothing to do, 1 among neighbours, 2 of all), and
+// what to merge next.
+struct End {
+    int u0, unit, b, kvh, n, c0, parts, level;
+    int first, step, take;
+    bool final;
 };
 
 template <int D, bool E4M3, int NT>
@@ -463,7 +482,7 @@ cache8_attn_kernel(const __grid_constant__ Cache8Args a) {
     __shared__ uint64_t s_full[kBars], s_empty[kBars];
     __shared__ int s_scan[kThreads / 32], s_longest[kThreads / 32];
     __shared__ Piece s_piece[2 * kSlots];   // in the order of the tiles; rows null: none
-    __shared__ Group s_group[2 * kSlots + 1];
+    __shared__ End s_end[2];
     __shared__ int s_groups;
     __shared__ int s_b[kSlots], s_rem[kSlots];
     __shared__ int s_last[kSlots];
@@ -472,7 +491,7 @@ cache8_attn_kernel(const __grid_constant__ Cache8Args a) {
 
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const int g = lane >> 2, t = lane & 3;
-    const int team_warps = C::KS * a.R, teams = kSlots / a.R;
+    const int team_warps = C::KS * a.R, teams = 1 << a.lg_teams;
     const int team = warp / team_warps, in_team = warp % team_warps;   // (the copying warp: neither)
     float* slots = reinterpret_cast<float*>(smem + (size_t)teams * a.stages * STAGE);   // [teams][rows][STRIDE]
     if (tid < teams * a.stages) {
@@ -511,7 +530,7 @@ cache8_attn_kernel(const __grid_constant__ Cache8Args a) {
         longest = max(longest, s_longest[w]);
     }
     const int me = blockIdx.x;
-    const int ctas = max(1, min((int)gridDim.x, N / teams));   // every team has a tile (or there is one CTA)
+    const int ctas = max(1, min((int)gridDim.x, N >> a.lg_teams));   // every team has a tile (or there is one CTA)
     const Deal deal(N, ctas * teams);
     int lo = me < ctas ? deal.from(me * teams) : N, hi = me < ctas ? deal.from((me + 1) * teams) : N;
     // Short sequences, a CTA for each head: no head is cut between CTAs, whose
@@ -688,16 +707,16 @@ cache8_attn_kernel(const __grid_constant__ Cache8Args a) {
             uint32_t qf[NT][D / 16][2];
             float f[NT][2];
             const auto row_of = [&](int n) -> const __nv_bfloat16* {
-                const int row = 8 * (NT * rt + n) + g, i = row / a.G;
+                const int row = 8 * (NT * rt + n) + g, i = row * a.g_inverse >> 16;
                 return row < a.rows && i < q.n
-                           ? a.Q + (((long long)at.b * a.Lq + i) * a.Hq + at.kvh * a.G + row % a.G) * D : nullptr;
+                           ? a.Q + (((long long)at.b * a.Lq + i) * a.Hq + (at.kvh - i) * a.G + row) * D : nullptr;
             };
             const auto limits = [&](int (&lim)[NT][2]) {   // the last token that each of the lane's rows sees
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const int row = 8 * (NT * rt + n) + 2 * t + e, i = row / a.G;
+                        const int row = 8 * (NT * rt + n) + 2 * t + e, i = row * a.g_inverse >> 16;
                         lim[n][e] = row < a.rows && i < q.n ? q.len + i : -1;
                     }
             };
@@ -1046,18 +1065,21 @@ cache8_attn_kernel(const __grid_constant__ Cache8Args a) {
         pdl_wait();
         return;
     }
-    // Merged twice by the same code: first the CTA's parts, then the parts of the
-    // heads that its ends cut, where it is the last to arrive. Sources (pointers
-    // to rows) of one head are a group; all of it in the ring, behind the second
-    // warp's rows of the first team.
+    // One code merges at every level: the CTA's parts first; then, where this CTA
+    // is the last to arrive, the parts of a head that its ends cut, of up to
+    // kFanOne CTAs at once, else of kFan neighbouring CTAs and then of those groups
+    // (one CTA reading all parts of a head cut over half the GPU took 15 us).
+    // Sources (pointers to rows) of one head are a group of the merge; all of it in
+    // the ring, behind the second warp's rows of the first team.
     pdl_wait();   // the gate logits; and the next kernel on the stream may rely on the gate kernel having ended
     const int items = a.rows * (D / 4);
+    const auto part_index = [&](int c, int u0) { return 2 * c + (u0 <= deal.from(c << a.lg_teams) ? 0 : 1); };
     const auto part_of = [&](int c, int u0) {   // CTA c's part of the head at u0
-        return a.part + (long long)(2 * c + (u0 <= deal.from(c * teams) ? 0 : 1)) * a.rows * STRIDE;
+        return a.part + (long long)part_index(c, u0) * a.rows * STRIDE;
     };
     const float** source = reinterpret_cast<const float**>(smem + (C::KS == 2 ? a.rows * STRIDE * 4 : 0));
-    float* weight = reinterpret_cast<float*>(source + kMaxCtas + 2);                          // [sources][rows]
-    int groups = 0;
+    Group* s_group = reinterpret_cast<Group*>(source + kMaxSources);  // [groups + 1]
+    float* weight = reinterpret_cast<float*>(s_group + kMaxGroups);   // [sources][rows]
     if (warp == 0) {
         // a lane stands for a source (lane % 16: the part, upper half: its second warp's rows)
         const int piece = lane % (2 * kSlots);
@@ -1073,68 +1095,95 @@ cache8_attn_kernel(const __grid_constant__ Cache8Args a) {
         if (at) source[place] = at;
         if (head) {
             Group& gr = s_group[__popc(heads & under)];
+            const SeqTiles q(a, s_piece[piece].b);
             gr.first = place;
-            gr.u0 = u0;
             gr.b = s_piece[piece].b;
             gr.kvh = s_piece[piece].kvh;
+            gr.n = q.n;
+            gr.dest = u0 >= lo && u0 + q.tiles <= hi ? nullptr : part_of(me, u0);
+            // an end of the CTA's share that cuts a head: its first group or its last
+            const bool first = !(heads & under), last = !(heads >> (piece + 1));
+            if (gr.dest) {
+                End& e = s_end[first ? 0 : 1];
+                e.c0 = deal.taker(u0) >> a.lg_teams;
+                e.parts = (deal.taker(u0 + q.tiles - 1) >> a.lg_teams) - e.c0 + 1;
+                e.u0 = u0;
+                e.unit = gr.b * a.Hkv + gr.kvh;
+                e.b = gr.b;
+                e.kvh = gr.kvh;
+                e.n = gr.n;
+                e.level = e.parts > kFanOne ? 1 : 2;
+            }
+            if (first && !gr.dest) s_end[0].level = 0;
+            if (last && (first || !gr.dest)) s_end[1].level = 0;
         }
         if (lane == 0) {
             s_groups = __popc(heads);
             s_group[__popc(heads)].first = __popc(there);
+            if (!heads) s_end[0].level = s_end[1].level = 0;
         }
     }
-    for (int pass = 0;; ++pass) {
+    for (;;) {
         sync_all();
-        groups = s_groups;
-        const int total = s_group[groups].first;
+        const int groups = s_groups, total = s_group[groups].first;
         float4* state = reinterpret_cast<float4*>(weight + ((total * a.rows + 3) & ~3));   // [groups][rows]: m, l, M, scale
-        // the sources' weights and each row's sums, a warp to a row
-        for (int k = warp; k < groups * a.rows; k += C::WARPS) {
-            const int gr = k / a.rows, row = k % a.rows, i0 = s_group[gr].first, i1 = s_group[gr + 1].first;
-            float m = -INFINITY, M = -INFINITY, l = 0.f;
-            float4 x[(kMaxCtas + 31) / 32];
-#pragma unroll
-            for (int c = 0; c < (kMaxCtas + 31) / 32; ++c) {
-                const int i = i0 + 32 * c + lane;
-                x[c] = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
-                if (i < i1) x[c] = *reinterpret_cast<const float4*>(source[i] + row * STRIDE + D);
-                m = fmaxf(m, x[c].x);
-                M = fmaxf(M, x[c].z);
+        // the sources' weights and each row's sums, a warp to a row, a lane to a source
+        for (int k = warp, gr = 0, row = warp; k < groups * a.rows; k += C::WARPS, row += C::WARPS) {
+            while (row >= a.rows) {
+                row -= a.rows;
+                ++gr;
             }
+            const int i = s_group[gr].first + lane;
+            const bool in = i < s_group[gr + 1].first;
+            float4 x = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
+            if (in) x = *reinterpret_cast<const float4*>(source[i] + row * STRIDE + D);
+            float m = x.x, M = x.z;
 #pragma unroll
             for (int sh = 1; sh < 32; sh <<= 1) {
                 m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, sh));
                 M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, sh));
             }
-#pragma unroll
-            for (int c = 0; c < (kMaxCtas + 31) / 32; ++c) {
-                const int i = i0 + 32 * c + lane;
-                l += x[c].y * part_weight(x[c].x, m);
-                if (i < i1) weight[i * a.rows + row] = part_weight(x[c].z, M);
-            }
+            float l = x.y * part_weight(x.x, m);
+            if (in) weight[i * a.rows + row] = part_weight(x.z, M);
 #pragma unroll
             for (int sh = 1; sh < 32; sh <<= 1) l += __shfl_xor_sync(0xffffffffu, l, sh);
             if (lane == 0) state[k] = make_float4(m, l, M, out_scale(m, l, M));
         }
         sync_all();
         // the weighted sums; a column's sources are split over lanes that would be idle
-        int split = 1;
-        while (split < 8 && 2 * split * groups * items <= kConsumers) split *= 2;
-        for (int idx = tid; idx < groups * items * split; idx += kConsumers) {
-            const int sub = idx % split, item = idx / split;
-            const int gr = item / items, row = item % items / (D / 4), col = 4 * (item % (D / 4));
-            const int i1 = s_group[gr + 1].first;
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-            for (int i = s_group[gr].first + sub; i < i1; i += split) {
-                const float4 v = *reinterpret_cast<const float4*>(source[i] + row * STRIDE + col);
-                const float w = weight[i * a.rows + row];
-                o.x += v.x * w;
-                o.y += v.y * w;
-                o.z += v.z * w;
-                o.w += v.w * w;
+        int lg = 0;
+        while (lg < 3 && ((groups * items) << (lg + 1)) <= kConsumers) ++lg;
+        for (int idx = tid; idx < (groups * items) << lg; idx += kConsumers) {
+            const int sub = idx & ((1 << lg) - 1);
+            int item = idx >> lg, gr = 0;
+            while (item >= items) {
+                item -= items;
+                ++gr;
             }
-            for (int sh = 1; sh < split; sh <<= 1) {   // (a whole warp: items come in sixteens)
+            const int row = item / (D / 4), col = 4 * (item % (D / 4)), i1 = s_group[gr + 1].first;
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int i0 = s_group[gr].first + sub; i0 < i1; i0 += 8 << lg) {   // eight loads under way
+                float4 v[8];
+                float w[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const int i = i0 + (k << lg);
+                    v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    w[k] = 0.f;
+                    if (i < i1) {
+                        v[k] = *reinterpret_cast<const float4*>(source[i] + row * STRIDE + col);
+                        w[k] = weight[i * a.rows + row];
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    o.x += v[k].x * w[k];
+                    o.y += v[k].y * w[k];
+                    o.z += v[k].z * w[k];
+                    o.w += v[k].w * w[k];
+                }
+            }
+            for (int sh = 1; sh < 1 << lg; sh <<= 1) {   // (whole warps: items come in sixteens)
                 o.x += __shfl_xor_sync(0xffffffffu, o.x, sh);
                 o.y += __shfl_xor_sync(0xffffffffu, o.y, sh);
                 o.z += __shfl_xor_sync(0xffffffffu, o.z, sh);
@@ -1143,51 +1192,50 @@ cache8_attn_kernel(const __grid_constant__ Cache8Args a) {
             if (sub != 0) continue;
             const Group& gp = s_group[gr];
             const float4 x = state[gr * a.rows + row];
-            const SeqTiles q(a, gp.b);
-            if (pass == 1 || (gp.u0 >= lo && gp.u0 + q.tiles <= hi)) {
-                finish<D>(a, gp.b, gp.kvh, q.n, row, col, x.w, o);
+            if (!gp.dest) {
+                finish<D>(a, gp.b, gp.kvh, gp.n, row, col, x.w, o);
             } else {
-                float* to = part_of(me, gp.u0) + row * STRIDE;
+                float* to = gp.dest + row * STRIDE;
                 *reinterpret_cast<float4*>(to + col) = o;
                 if (col == 0) *reinterpret_cast<float4*>(to + D) = x;
             }
         }
-        if (pass == 1) break;
-        // the heads that the CTA's ends cut are the first and the last group
         sync_all();
-        if (tid < 2) {
-            int last = 0;
-            if (groups > tid) {
-                const Group& gp = s_group[tid == 0 ? 0 : groups - 1];
-                const int u1 = gp.u0 + SeqTiles(a, gp.b).tiles;
-                if (gp.u0 < lo || u1 > hi) {
-                    __threadfence();   // (after the barrier: covers what every thread has written)
-                    last = atomicAdd(a.counters + (long long)gp.b * a.Hkv + gp.kvh, 1) ==
-                           deal.taker(u1 - 1) / teams - deal.taker(gp.u0) / teams;
-                    __threadfence();
-                }
+        if (tid < 2) {   // the arrival of each end's head, and what is to be merged next
+            End& e = s_end[tid];
+            int take = 0;
+            if (e.level != 0) {
+                const bool all = e.level == 2;
+                e.step = all && e.parts > kFanOne ? kFan : 1;
+                e.first = all ? e.c0 : me - (me - e.c0) % kFan;
+                const int n = all ? (e.parts + e.step - 1) / e.step : min(kFan, e.parts - (e.first - e.c0));
+                int* counter = a.counters + (all ? e.unit : a.B * a.Hkv + part_index(e.first, e.u0));
+                __threadfence();   // (after the barrier: covers what every thread has written)
+                if (atomicAdd(counter, 1) == n - 1) take = n;
+                __threadfence();
+                e.level = take == 0 || all ? 0 : 2;
+                e.final = all;
             }
-            s_last[tid] = last;
+            e.take = take;
         }
         sync_all();
-        const bool first = s_last[0], second = s_last[1];
-        if (!first && !second) break;
-        const Group g0 = s_group[0], g1 = s_group[groups - 1];
-        const auto cta_of = [&](int x) { return deal.taker(x) / teams; };
-        const int c0 = cta_of(g0.u0), n0 = first ? cta_of(g0.u0 + SeqTiles(a, g0.b).tiles - 1) - c0 + 1 : 0;
-        const int c1 = cta_of(g1.u0), n1 = second ? cta_of(g1.u0 + SeqTiles(a, g1.b).tiles - 1) - c1 + 1 : 0;
-        sync_all();   // (everyone has read the groups)
-        for (int i = tid; i < n0 + n1; i += kConsumers)
-            source[i] = i < n0 ? part_of(c0 + i, g0.u0) : part_of(c1 + i - n0, g1.u0);
+        const int n0 = s_end[0].take, n1 = s_end[1].take;
+        if (n0 + n1 == 0) break;
+        if (tid < n0 + n1) {
+            const End& e = s_end[tid < n0 ? 0 : 1];
+            source[tid] = part_of(e.first + (tid < n0 ? tid : tid - n0) * e.step, e.u0);
+        }
         if (tid == 0) {
             int n = 0;
-            if (first) {
-                s_group[n] = g0;
-                s_group[n++].first = 0;
-            }
-            if (second) {
-                s_group[n] = g1;
-                s_group[n++].first = n0;
+            for (int k = 0; k < 2; ++k) {
+                const End& e = s_end[k];
+                if (e.take == 0) continue;
+                Group& gr = s_group[n++];
+                gr.first = k == 0 ? 0 : n0;
+                gr.b = e.b;
+                gr.kvh = e.kvh;
+                gr.n = e.n;
+                gr.dest = e.final ? nullptr : part_of(e.first, e.u0);
             }
             s_group[n].first = n0 + n1;
             s_groups = n;
@@ -1244,7 +1292,8 @@ int plan_cache8(const gsdpa_cache8* c, int Lq, int d_model, int Hq, int gate_mod
     if (rows > kMaxRows) return GSDPA_ERR_UNSUPPORTED;
     // (tiles are counted in 32 bits)
     if ((long long)c->B * c->H_kv * (c->capacity / kCacheBlock) > 0x7fffffffLL) return GSDPA_ERR_UNSUPPORTED;
-    if ((long long)c->B * Lq > 0x7fffffffLL / 8) return GSDPA_ERR_UNSUPPORTED;
+    if ((long long)c->B * Lq > 0x7fffffffLL / 8 || (long long)c->B * c->H_kv > 0x7fffffffLL - 2 * kMaxCtas)
+        return GSDPA_ERR_UNSUPPORTED;
     if (c->B == 0 || Lq == 0) return GSDPA_OK;   // an empty problem: nothing to plan
     Cache8Plan& o = *out;
     Problem& p = o.p;
@@ -1269,7 +1318,7 @@ int plan_cache8(const gsdpa_cache8* c, int Lq, int d_model, int Hq, int gate_mod
     const size_t part = sizeof(float) * (size_t)rows * (c->d_k + 4);
     o.piece = take(part * plan_sms() * 2 * (kSlots / shape_of((int)rows, c->d_k).R));
     o.part = take(part * plan_sms() * 2);
-    o.n_counters = c->B * c->H_kv;
+    o.n_counters = c->B * c->H_kv + 2 * kMaxCtas;   // heads; neighbouring CTAs' parts
     o.counters = take(sizeof(int) * (size_t)o.n_counters);
     o.total = off;
     return GSDPA_OK;
@@ -1361,11 +1410,13 @@ int gated_sdpa_cache8(const void* X, const void* Q, const gsdpa_cache8* cache, c
     a.Hq = H_q;
     a.Hkv = cache->H_kv;
     a.G = H_q / cache->H_kv;
+    a.g_inverse = (65536 + a.G - 1) / a.G;
     a.rows = a.G * L_q;
     a.blocks = cache->capacity / kCacheBlock;
     a.capacity = cache->capacity;
     const Shape sh = shape_of(a.rows, cache->d_k);
     a.R = sh.R;
+    a.lg_teams = sh.R == 1 ? 3 : (sh.R == 2 ? 2 : (sh.R == 4 ? 1 : 0));
     a.stages = sh.stages;
     a.gate_part = gated ? reinterpret_cast<const float*>(ws + pl.w.gate_part) : nullptr;
     a.gate_splits = pl.w.gate_splits;

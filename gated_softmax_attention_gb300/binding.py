@@ -8,6 +8,7 @@ built, every call raises: there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -546,18 +547,20 @@ class Rope:
             raise GsdpaError(int(st), where)
 
 
-def _head_rows(t, name, shape, dtype, device):
-    """The row length in elements of t, [B, L, H, d_k] with contiguous heads and
+# (The calls below run once per layer and token in a decoding loop, on kernels of
+# a few microseconds: their checks are the ones above, with each property of a
+# tensor read once.)
+def _head_rows(t, name, B, L, H, d, dtype, device):
+    """The row length in elements of t, [B, L, H, d] with contiguous heads and
     evenly spaced token rows (a contiguous tensor, or a column block of one)."""
     if t is None:
         raise ValueError(f"{name} is required")
-    if not t.is_cuda or t.device != device:
-        raise ValueError(f"{name} must be a CUDA tensor on {device}, not on {t.device}")
+    if t.shape != (B, L, H, d):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, the problem needs {(B, L, H, d)}")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, the problem needs {tuple(shape)}")
-    B, L, H, d = shape
+    if t.device != device or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor on {device}, not on {t.device}")
     s0, s1, s2, s3 = t.stride()
     ld = s1 if L > 1 else (s0 if B > 1 else H * d)
     if (s3 != 1 and d > 1) or (H > 1 and s2 != d) or (L > 1 and B > 1 and s0 != L * ld):
@@ -571,8 +574,31 @@ def _vector(t, name, n, dtype, device):
     """The address of an optional contiguous vector of n elements."""
     if t is None:
         return None
-    _expect(t, name, n, dtype, device)
+    if t.dtype != dtype or t.numel() != n or t.device != device or not t.is_cuda or not t.is_contiguous():
+        _expect(t, name, n, dtype, device)   # says which
     return t.data_ptr()
+
+
+def _current_stream(device):
+    """The handle of the current stream, which must be of the tensors' device."""
+    import torch
+    index = device.index
+    if index != torch.cuda.current_device():
+        _stream(None, device)                # raises
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
+def _on_stream(call):
+    """``stream=``: the call with that stream current, so that what it allocates
+    (outputs, workspace) is that stream's own and not reused under its kernels."""
+    @functools.wraps(call)
+    def on(*args, stream=None, **kw):
+        if stream is None:
+            return call(*args, **kw)
+        import torch
+        with torch.cuda.stream(stream):
+            return call(*args, **kw)
+    return on
 
 
 _DTYPES = {}
@@ -596,8 +622,9 @@ def _qk_dims(Q, K):
     return B, L, H_q, K.shape[2], d_k
 
 
+@_on_stream
 def qk_norm_rope(Q, K, *, gamma_q=None, gamma_k=None, norm=True, eps=1e-6, rope=None, positions=None, out_q=None,
-                 out_k=None, stream=None):
+                 out_k=None):
     """Per-head RMS norm of Q [B, L, H_q, d_k] and K [B, L, H_kv, d_k] and their
     rotary positions in one pass (gsdpa_qk_norm_rope); float32 or bfloat16.
 
@@ -609,35 +636,35 @@ def qk_norm_rope(Q, K, *, gamma_q=None, gamma_k=None, norm=True, eps=1e-6, rope=
     dt, dev = Q.dtype, Q.device
     code = _dtype_code(dt)
     B, L, H_q, H_kv, d_k = _qk_dims(Q, K)
-    ld_q, ld_k = _head_rows(Q, "Q", Q.shape, dt, dev), _head_rows(K, "K", K.shape, dt, dev)
+    ld_q, ld_k = _head_rows(Q, "Q", B, L, H_q, d_k, dt, dev), _head_rows(K, "K", B, L, H_kv, d_k, dt, dev)
     if out_q is None:
         out_q, ld_qo = torch.empty((B, L, H_q, d_k), dtype=dt, device=dev), H_q * d_k
     else:
-        ld_qo = _head_rows(out_q, "out_q", Q.shape, dt, dev)
+        ld_qo = _head_rows(out_q, "out_q", B, L, H_q, d_k, dt, dev)
     if out_k is None:
         out_k, ld_ko = torch.empty((B, L, H_kv, d_k), dtype=dt, device=dev), H_kv * d_k
     else:
-        ld_ko = _head_rows(out_k, "out_k", K.shape, dt, dev)
-    gq, gk = _vector(gamma_q, "gamma_q", d_k, dt, dev), _vector(gamma_k, "gamma_k", d_k, dt, dev)
-    pos = _vector(positions, "positions", B * L, torch.int32, dev)
-    s = _stream(stream, dev)
-    st = load().gsdpa_qk_norm_rope(Q.data_ptr(), K.data_ptr(), gq, gk, pos, out_q.data_ptr(), out_k.data_ptr(), ld_q,
-                                   ld_k, ld_qo, ld_ko, B, L, H_q, H_kv, d_k, 1 if norm else 0, eps,
-                                   None if rope is None else rope.ref, code, s.cuda_stream)
+        ld_ko = _head_rows(out_k, "out_k", B, L, H_kv, d_k, dt, dev)
+    st = (_lib or load()).gsdpa_qk_norm_rope(
+        Q.data_ptr(), K.data_ptr(), _vector(gamma_q, "gamma_q", d_k, dt, dev), _vector(gamma_k, "gamma_k", d_k, dt, dev),
+        _vector(positions, "positions", B * L, torch.int32, dev), out_q.data_ptr(), out_k.data_ptr(), ld_q, ld_k, ld_qo,
+        ld_ko, B, L, H_q, H_kv, d_k, 1 if norm else 0, eps, None if rope is None else rope.ref, code,
+        _current_stream(dev))
     if st != OK:
         raise GsdpaError(st, "gsdpa_qk_norm_rope")
     return out_q, out_k
 
 
 def qk_norm_rope_bwd_workspace_bytes(B, L, d_k, norm=True) -> int:
-    n = load().gsdpa_qk_norm_rope_bwd_workspace_bytes(B, L, d_k, 1 if norm else 0)
+    n = (_lib or load()).gsdpa_qk_norm_rope_bwd_workspace_bytes(B, L, d_k, 1 if norm else 0)
     if n == ctypes.c_size_t(-1).value:
         raise GsdpaError(ERR_INVALID_ARG, "gsdpa_qk_norm_rope_bwd_workspace_bytes")
     return n
 
 
+@_on_stream
 def qk_norm_rope_bwd(Q, K, dQo, dKo, *, gamma_q=None, gamma_k=None, norm=True, eps=1e-6, rope=None, positions=None,
-                     out_dq=None, out_dk=None, workspace=None, stream=None):
+                     out_dq=None, out_dk=None, workspace=None):
     """Backward of qk_norm_rope: from dQo, dKo (gradients of its outputs) and its
     inputs, a dict with dQ, dK and, with the norm, dgamma_q and dgamma_k (with
     respect to a gamma of 1 where none was given). out_dq, out_dk may be dQo, dKo
@@ -646,16 +673,16 @@ def qk_norm_rope_bwd(Q, K, dQo, dKo, *, gamma_q=None, gamma_k=None, norm=True, e
     dt, dev = Q.dtype, Q.device
     code = _dtype_code(dt)
     B, L, H_q, H_kv, d_k = _qk_dims(Q, K)
-    ld_q, ld_k = _head_rows(Q, "Q", Q.shape, dt, dev), _head_rows(K, "K", K.shape, dt, dev)
-    ld_dqo, ld_dko = _head_rows(dQo, "dQo", Q.shape, dt, dev), _head_rows(dKo, "dKo", K.shape, dt, dev)
+    ld_q, ld_k = _head_rows(Q, "Q", B, L, H_q, d_k, dt, dev), _head_rows(K, "K", B, L, H_kv, d_k, dt, dev)
+    ld_dqo, ld_dko = _head_rows(dQo, "dQo", B, L, H_q, d_k, dt, dev), _head_rows(dKo, "dKo", B, L, H_kv, d_k, dt, dev)
     if out_dq is None:
         out_dq, ld_dq = torch.empty((B, L, H_q, d_k), dtype=dt, device=dev), H_q * d_k
     else:
-        ld_dq = _head_rows(out_dq, "out_dq", Q.shape, dt, dev)
+        ld_dq = _head_rows(out_dq, "out_dq", B, L, H_q, d_k, dt, dev)
     if out_dk is None:
         out_dk, ld_dk = torch.empty((B, L, H_kv, d_k), dtype=dt, device=dev), H_kv * d_k
     else:
-        ld_dk = _head_rows(out_dk, "out_dk", K.shape, dt, dev)
+        ld_dk = _head_rows(out_dk, "out_dk", B, L, H_kv, d_k, dt, dev)
     gq, gk = _vector(gamma_q, "gamma_q", d_k, dt, dev), _vector(gamma_k, "gamma_k", d_k, dt, dev)
     pos = _vector(positions, "positions", B * L, torch.int32, dev)
     out = {"dQ": out_dq, "dK": out_dk}
@@ -667,11 +694,11 @@ def qk_norm_rope_bwd(Q, K, dQo, dKo, *, gamma_q=None, gamma_k=None, norm=True, e
         dgq, dgk = out["dgamma_q"].data_ptr(), out["dgamma_k"].data_ptr()
         need = qk_norm_rope_bwd_workspace_bytes(B, L, d_k)
     workspace, ws_bytes = _workspace(workspace, need, dev)
-    s = _stream(stream, dev)
-    st = load().gsdpa_qk_norm_rope_bwd(
+    st = (_lib or load()).gsdpa_qk_norm_rope_bwd(
         Q.data_ptr(), K.data_ptr(), gq, gk, pos, dQo.data_ptr(), dKo.data_ptr(), out_dq.data_ptr(), out_dk.data_ptr(),
         dgq, dgk, ld_q, ld_k, ld_dqo, ld_dko, ld_dq, ld_dk, B, L, H_q, H_kv, d_k, 1 if norm else 0, eps,
-        None if rope is None else rope.ref, code, _ptr(workspace), ws_bytes, s.cuda_stream)
+        None if rope is None else rope.ref, code, None if workspace is None else workspace.data_ptr(), ws_bytes,
+        _current_stream(dev))
     if st != OK:
         raise GsdpaError(st, "gsdpa_qk_norm_rope_bwd")
     return out
@@ -718,6 +745,21 @@ class Cache8:
         self.plan = _Cache8Plan(kinds[k8.dtype], B, H, d, n * CACHE_BLOCK, k8.data_ptr(), v8.data_ptr(),
                                 k_scale.data_ptr(), v_scale.data_ptr(), k_tail.data_ptr(), v_tail.data_ptr())
         self.ref = ctypes.addressof(self.plan)
+        self.need, self.work = {}, {}
+
+    def workspace(self, need, stream):
+        """A workspace for a call on this stream: one is kept for each stream, whose
+        calls follow one another. A captured call gets one of its own, which its
+        graph keeps (replays may run beside anything)."""
+        import torch
+        if need == 0:
+            return None
+        if torch.cuda.is_current_stream_capturing():
+            return torch.empty(need, dtype=torch.uint8, device=self.device)
+        held = self.work.get(stream)
+        if held is None or held.numel() < need:
+            held = self.work[stream] = torch.empty(need, dtype=torch.uint8, device=self.device)
+        return held
 
 
 def cache8_alloc(B, capacity, H_kv, d_k, kind="int8", device="cuda") -> Cache8:
@@ -734,24 +776,22 @@ def cache8_alloc(B, capacity, H_kv, d_k, kind="int8", device="cuda") -> Cache8:
                   make(B, H_kv, 2, d_k, CACHE_BLOCK, dtype=torch.bfloat16))
 
 
-def cache8_append(cache, K, V, lens, n_new=None, *, stream=None) -> None:
+@_on_stream
+def cache8_append(cache, K, V, lens, n_new=None) -> None:
     """Appends K, V [B, L, H_kv, d_k] bfloat16 to the cache (gsdpa_cache8_append):
     row i < n_new[b] becomes token lens[b] + i of sequence b. lens and n_new (None:
     L each) are int32 [B] on the device and are not changed."""
     import torch
-    dev = cache.device
+    dev, bf = cache.device, torch.bfloat16
     if K.dim() != 4:
         raise ValueError("K must be [B, L, H_kv, d_k]")
-    shape = (cache.B, K.shape[1], cache.H_kv, cache.d_k)
-    ld_k = _head_rows(K, "K", shape, torch.bfloat16, dev)
-    ld_v = _head_rows(V, "V", shape, torch.bfloat16, dev)
+    B, L, H, d = cache.B, K.shape[1], cache.H_kv, cache.d_k
+    ld_k, ld_v = _head_rows(K, "K", B, L, H, d, bf, dev), _head_rows(V, "V", B, L, H, d, bf, dev)
     if lens is None:
         raise ValueError("lens is required")
-    at = _vector(lens, "lens", cache.B, torch.int32, dev)
-    new = _vector(n_new, "n_new", cache.B, torch.int32, dev)
-    s = _stream(stream, dev)
-    st = load().gsdpa_cache8_append(cache.ref, K.data_ptr(), V.data_ptr(), ld_k, ld_v, at, new, shape[1],
-                                    s.cuda_stream)
+    st = (_lib or load()).gsdpa_cache8_append(
+        cache.ref, K.data_ptr(), V.data_ptr(), ld_k, ld_v, _vector(lens, "lens", B, torch.int32, dev),
+        _vector(n_new, "n_new", B, torch.int32, dev), L, _current_stream(dev))
     if st != OK:
         raise GsdpaError(st, "gsdpa_cache8_append")
 
@@ -763,8 +803,8 @@ def cache8_workspace_bytes(cache, L_q, H_q, d_model=0, gate="elementwise") -> in
     return n
 
 
-def gated_sdpa_cache8(X, Q, cache, lens, W_g=None, *, gate="elementwise", n_new=None, out=None, workspace=None,
-                      stream=None):
+@_on_stream
+def gated_sdpa_cache8(X, Q, cache, lens, W_g=None, *, gate="elementwise", n_new=None, out=None, workspace=None):
     """Gated attention of a step's tokens against the 8-bit cache (gated_sdpa_cache8),
     after cache8_append of their keys and values with the same lens and n_new: row i
     of Q [B, L_q, H_q, d_k] sees tokens 0 .. lens[b] + i. X [B, L_q, d_model] and W_g
@@ -777,29 +817,36 @@ def gated_sdpa_cache8(X, Q, cache, lens, W_g=None, *, gate="elementwise", n_new=
         raise ValueError(f"Q {tuple(Q.shape)} must be [B={cache.B}, L_q, H_q, d_k={cache.d_k}]")
     B, L_q, H_q, d_k = Q.shape
     n = B * L_q * H_q * d_k
-    _expect(Q, "Q", n, bf, dev)
+    q = _vector(Q, "Q", n, bf, dev)
     d_model, x, w = 0, None, None
     if gm != GATE_NONE:
         d_model = _x_dim(X, B, L_q)
-        _expect(X, "X", B * L_q * d_model, bf, dev)
-        _expect(W_g, "W_g", d_model * _gate_cols(gm, H_q, d_k), bf, dev)
-        x, w = X.data_ptr(), W_g.data_ptr()
-    if out is None:
-        out = torch.empty((B, L_q, H_q, d_k), dtype=bf, device=dev)
-    else:
-        _expect(out, "out", n, bf, dev)
+        if W_g is None:
+            raise ValueError("W_g is required")
+        x = _vector(X, "X", B * L_q * d_model, bf, dev)
+        w = _vector(W_g, "W_g", d_model * _gate_cols(gm, H_q, d_k), bf, dev)
     if lens is None:
         raise ValueError("lens is required")
     at = _vector(lens, "lens", B, torch.int32, dev)
     new = _vector(n_new, "n_new", B, torch.int32, dev)
-    lib = load()
-    need = lib.gsdpa_cache8_workspace_bytes(cache.ref, L_q, d_model, H_q, gm)
-    if need == ctypes.c_size_t(-1).value:
-        need = 0   # (the call itself says why)
-    workspace, ws_bytes = _workspace(workspace, need, dev)
-    s = _stream(stream, dev)
-    st = lib.gated_sdpa_cache8(x, Q.data_ptr(), cache.ref, at, new, w, out.data_ptr(), L_q, d_model, H_q, gm,
-                               None if workspace is None else workspace.data_ptr(), ws_bytes, s.cuda_stream)
+    if out is None:
+        out = torch.empty((B, L_q, H_q, d_k), dtype=bf, device=dev)
+    o = _vector(out, "out", n, bf, dev)
+    lib = _lib or load()
+    shape = (L_q, d_model, H_q, gm)
+    need = cache.need.get(shape)     # (the workspace's size, by the problem's shape)
+    if need is None:
+        need = lib.gsdpa_cache8_workspace_bytes(cache.ref, L_q, d_model, H_q, gm)
+        if need == ctypes.c_size_t(-1).value:
+            need = 0                 # (the call itself says why)
+        cache.need[shape] = need
+    stream = _current_stream(dev)
+    if workspace is not None:
+        workspace, need = _workspace(workspace, need, dev)
+    else:
+        workspace = cache.workspace(need, stream)
+    st = lib.gated_sdpa_cache8(x, q, cache.ref, at, new, w, o, L_q, d_model, H_q, gm,
+                               None if workspace is None else workspace.data_ptr(), need, stream)
     if st != OK:
         raise GsdpaError(st, "gated_sdpa_cache8")
     return out

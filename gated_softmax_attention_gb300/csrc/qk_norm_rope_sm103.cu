@@ -13,18 +13,22 @@
 //     dx = r h - x (r^3 s / d_k),      dgamma_c = sum over rows of dy_c x_c r
 //
 // Bound by HBM: every element is read once and written once (the backward
-// reads two), about 10 operations each. A warp takes one token: it turns the
-// position into the token's cosines and sines once, in shared memory, keeps
-// A, B in registers and walks over the token's heads, d_k / 8 lanes to a row,
-// 8 elements (one 16-byte load in bf16) to a lane, the pair's other column
-// from a shuffle.
+// reads two), about 10 operations each. A warp takes a part of a token's heads,
+// all of one tensor: it starts their loads, turns the position into its lanes'
+// cosines and sines meanwhile, and finishes the rows from registers; nothing is
+// shared between warps. d_k / 8 lanes have a row, each 4 columns and the 4 that they are
+// rotated with (half layout: two 8-byte pieces of a bf16 row, rotary_dim / 2
+// columns apart; else 16 bytes in one), so the rotation needs no exchange
+// between lanes, only the norm's sums do.
 //
 // Angles: a position times a frequency in float32 is off by 0.06 rad at
 // position 10^6, and FP64 arithmetic is slow here. The frequency is kept as a
 // 64-bit fraction of a whole turn per position instead; the low 64 bits of
 // position * fraction are the angle modulo one turn, exact but for the
 // fraction's own rounding (position * 2^-54 turns), and its upper 32 bits go
-// to sincospif. Everything after that is float32, rounded once at the store.
+// to sincospif for float32, to the hardware's sine and cosine (2^-20.9
+// absolute) for bf16, which rounds at 2^-9. Everything after that is float32, rounded
+// once at the store.
 #include "gsdpa.h"
 #include "gsdpa_internal.h"
 #include "sm103_ptx.cuh"
@@ -38,6 +42,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxPairs = 64;
+constexpr int kBwdCtasPerSm = 3;
 
 struct RopeArgs {
     const void *Q, *K;            // forward: inputs; backward: the forward's inputs (null without the norm)
@@ -47,23 +52,29 @@ struct RopeArgs {
     const int* positions;         // [B, L] or null: 0 .. L - 1
     float* part;                  // backward: [CTAs][2][d_k] shares of dgamma
     long long ld_q, ld_k, ld_dq, ld_dk, ld_qo, ld_ko;
-    long long tokens;             // B * L
     int L, Hq, Hkv;
-    int wpt;                      // warps per token (1, 2, 4 or 8)
+    int q_parts, k_parts;         // parts of a token's heads
+    unsigned tasks;               // tokens * (q_parts + k_parts)
     float eps;
     int rd;                       // rotated columns (0: none)
-    int interleaved;
     float attn_scale;
     unsigned long long turn[kMaxPairs];
 };
 
-// 8 elements of a row in one lane
-template <typename T>
+// 8 elements of a row in one lane: 4 at p and 4 at q.
+template <typename T, bool HALF>
 struct Raw;
-template <>
-struct Raw<__nv_bfloat16> {
+template <bool HALF>
+struct Raw<__nv_bfloat16, HALF> {
     uint4 v;
-    __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = *reinterpret_cast<const uint4*>(p); }
+    __device__ __forceinline__ void load(const __nv_bfloat16* p, const __nv_bfloat16* q) {
+        if constexpr (HALF) {
+            const uint2 a = *reinterpret_cast<const uint2*>(p), b = *reinterpret_cast<const uint2*>(q);
+            v = make_uint4(a.x, a.y, b.x, b.y);
+        } else {
+            v = *reinterpret_cast<const uint4*>(p);
+        }
+    }
     __device__ __forceinline__ void zero() { v = make_uint4(0, 0, 0, 0); }
     __device__ __forceinline__ void unpack(float2 (&f)[4]) const {
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -71,25 +82,23 @@ struct Raw<__nv_bfloat16> {
         for (int k = 0; k < 4; ++k)
             f[k] = make_float2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xffff0000u));
     }
-    __device__ __forceinline__ Raw from_lane(int src) const {
-        Raw o;
-        o.v.x = __shfl_sync(0xffffffffu, v.x, src);
-        o.v.y = __shfl_sync(0xffffffffu, v.y, src);
-        o.v.z = __shfl_sync(0xffffffffu, v.z, src);
-        o.v.w = __shfl_sync(0xffffffffu, v.w, src);
-        return o;
-    }
-    static __device__ __forceinline__ void store(__nv_bfloat16* p, const float2 (&f)[4]) {
-        *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(f[0].x, f[0].y), pack_bf16x2(f[1].x, f[1].y),
-                                                  pack_bf16x2(f[2].x, f[2].y), pack_bf16x2(f[3].x, f[3].y));
+    static __device__ __forceinline__ void store(__nv_bfloat16* p, __nv_bfloat16* q, const float2 (&f)[4]) {
+        const uint2 a = make_uint2(pack_bf16x2(f[0].x, f[0].y), pack_bf16x2(f[1].x, f[1].y));
+        const uint2 b = make_uint2(pack_bf16x2(f[2].x, f[2].y), pack_bf16x2(f[3].x, f[3].y));
+        if constexpr (HALF) {
+            *reinterpret_cast<uint2*>(p) = a;
+            *reinterpret_cast<uint2*>(q) = b;
+        } else {
+            *reinterpret_cast<uint4*>(p) = make_uint4(a.x, a.y, b.x, b.y);
+        }
     }
 };
-template <>
-struct Raw<float> {
+template <bool HALF>
+struct Raw<float, HALF> {
     float4 a, b;
-    __device__ __forceinline__ void load(const float* p) {
+    __device__ __forceinline__ void load(const float* p, const float* q) {
         a = *reinterpret_cast<const float4*>(p);
-        b = *reinterpret_cast<const float4*>(p + 4);
+        b = *reinterpret_cast<const float4*>(q);
     }
     __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
     __device__ __forceinline__ void unpack(float2 (&f)[4]) const {
@@ -98,29 +107,42 @@ struct Raw<float> {
         f[2] = make_float2(b.x, b.y);
         f[3] = make_float2(b.z, b.w);
     }
-    __device__ __forceinline__ Raw from_lane(int src) const {
-        Raw o;
-        o.a.x = __shfl_sync(0xffffffffu, a.x, src);
-        o.a.y = __shfl_sync(0xffffffffu, a.y, src);
-        o.a.z = __shfl_sync(0xffffffffu, a.z, src);
-        o.a.w = __shfl_sync(0xffffffffu, a.w, src);
-        o.b.x = __shfl_sync(0xffffffffu, b.x, src);
-        o.b.y = __shfl_sync(0xffffffffu, b.y, src);
-        o.b.z = __shfl_sync(0xffffffffu, b.z, src);
-        o.b.w = __shfl_sync(0xffffffffu, b.w, src);
-        return o;
-    }
-    static __device__ __forceinline__ void store(float* p, const float2 (&f)[4]) {
+    static __device__ __forceinline__ void store(float* p, float* q, const float2 (&f)[4]) {
         *reinterpret_cast<float4*>(p) = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
-        *reinterpret_cast<float4*>(p + 4) = make_float4(f[2].x, f[2].y, f[3].x, f[3].y);
+        *reinterpret_cast<float4*>(q) = make_float4(f[2].x, f[2].y, f[3].x, f[3].y);
     }
 };
 
-template <int LANES>
-__device__ __forceinline__ float row_sum(float s) {
+// The sums over a row's lanes of N values (1, 2 or 4) at once, every lane's v
+// becoming the totals through f: lanes exchange halves of the values while there
+// are some to give away, so that each ends with one total, applies f to it, and
+// hands it round (for 4 values and 16 lanes 9 shuffles instead of 16, and f once).
+template <int LANES, int N, typename F>
+__device__ __forceinline__ void row_sums(float (&v)[N], int lane, F f) {
+    float t[N];
 #pragma unroll
-    for (int sh = LANES / 2; sh > 0; sh >>= 1) s += __shfl_xor_sync(0xffffffffu, s, sh);
-    return s;
+    for (int k = 0; k < N; ++k) t[k] = v[k];
+    int sh = LANES / 2;
+#pragma unroll
+    for (int n = N; n > 1; n >>= 1, sh >>= 1) {
+        const bool upper = lane & sh;
+#pragma unroll
+        for (int k = 0; k < n / 2; ++k) {
+            const float keep = upper ? t[k + n / 2] : t[k], give = upper ? t[k] : t[k + n / 2];
+            t[k] = keep + __shfl_xor_sync(0xffffffffu, give, sh);
+        }
+    }
+#pragma unroll
+    for (; sh > 0; sh >>= 1) t[0] += __shfl_xor_sync(0xffffffffu, t[0], sh);
+    const float mine = f(t[0]);
+    if constexpr (N == 1) {
+        v[0] = mine;
+    } else {
+        // value k's total is in the lanes whose upper bits spell k
+        const int base = lane & ~(LANES - 1);
+#pragma unroll
+        for (int k = 0; k < N; ++k) v[k] = __shfl_sync(0xffffffffu, mine, base + k * (LANES / N));
+    }
 }
 
 __device__ __forceinline__ float dot2(const float2 (&a)[4], const float2 (&b)[4]) {
@@ -130,273 +152,204 @@ __device__ __forceinline__ float dot2(const float2 (&a)[4], const float2 (&b)[4]
     return s.x + s.y;
 }
 
-// What a lane needs of its row's geometry.
-struct LanePlan {
-    int lane, j, slot, partner;   // j: 8-column chunk; slot: which of the warp's rows; partner: lane of the pair
-    bool rotated;                 // the chunk lies in the rotated columns
-    float sign;                   // half layout: -1 for the first member's chunk, +1 for the second's
-    int i0;                       // first pair of the chunk (half: pair of column 8 j; interleaved: of 8 j, 8 j + 1)
+// Scaled cosines and sines of a lane's four pairs.
+struct Trig {
+    float c[4], s[4];
 };
-template <int LANES>
-__device__ __forceinline__ LanePlan lane_plan(const RopeArgs& a) {
-    LanePlan p;
-    p.lane = threadIdx.x & 31;
-    p.j = p.lane % LANES;
-    p.slot = p.lane / LANES;
-    p.partner = p.lane;
-    const int half = a.rd >> 1;
-    p.rotated = 8 * p.j < a.rd;
-    p.sign = 1.f;
-    p.i0 = 4 * p.j;
-    if (!a.interleaved) {
-        const bool first = 8 * p.j < half;
-        p.sign = first ? -1.f : 1.f;
-        p.i0 = first ? 8 * p.j : 8 * p.j - half;
-        if (p.rotated) p.partner = p.lane + (first ? half / 8 : -(half / 8));
-    }
-    return p;
-}
-
-// The token's scaled cosines and sines into the warp's table (all lanes call it).
-__device__ __forceinline__ void fill_table(float2* tab, const RopeArgs& a, long long tok, int lane) {
-    const int pairs = a.rd >> 1;
-    if (pairs == 0) return;
-    const long long pos = a.positions ? (long long)a.positions[tok] : tok % a.L;
-    for (int i = lane; i < pairs; i += 32) {
-        const unsigned long long at = (unsigned long long)pos * a.turn[i];
-        float s, c;
-        sincospif((float)(int)(at >> 32) * 4.656612873077393e-10f, &s, &c);   // 2^-31: half turns
-        tab[i] = make_float2(c * a.attn_scale, s * a.attn_scale);
-    }
-    __syncwarp();
-}
-
-// cos and sin of the lane's 8 columns (cos 1, sin 0 outside the rotated part);
-// sin with the sign of the forward's second term.
-__device__ __forceinline__ void lane_trig(const float2* tab, const RopeArgs& a, const LanePlan& p, float2 (&c)[4],
-                                          float2 (&s)[4]) {
-    if (!p.rotated) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            c[k] = make_float2(1.f, 1.f);
-            s[k] = make_float2(0.f, 0.f);
-        }
-    } else if (a.interleaved) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float2 t = tab[p.i0 + k];
-            c[k] = make_float2(t.x, t.x);
-            s[k] = make_float2(-t.y, t.y);
-        }
-    } else {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float2 t = tab[p.i0 + 2 * k], u = tab[p.i0 + 2 * k + 1];
-            c[k] = make_float2(t.x, u.x);
-            s[k] = make_float2(p.sign * t.y, p.sign * u.y);
-        }
-    }
-}
-
-// x_c' for each column c of the lane
 template <typename T>
-__device__ __forceinline__ void pair_of(const Raw<T>& raw, const float2 (&x)[4], const RopeArgs& a, const LanePlan& p,
-                                        float2 (&xp)[4]) {
-    if (a.interleaved) {
+__device__ __forceinline__ void angles(Trig& t, const RopeArgs& a, long long pos, int first_pair, bool rotated) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) xp[k] = make_float2(x[k].y, x[k].x);
+    for (int k = 0; k < 4; ++k) {
+        t.c[k] = 1.f;
+        t.s[k] = 0.f;
+    }
+    if (!rotated) return;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const unsigned long long at = (unsigned long long)pos * a.turn[first_pair + k];
+        const float x = (float)(int)(at >> 32);   // 2^-32 turns, within half a turn
+        float sn, cs;
+        if constexpr (std::is_same<T, float>::value) {
+            sincospif(x * 4.656612873077393e-10f, &sn, &cs);
+        } else {
+            const float w = x * 1.4629180792671596e-09f;   // 2 pi 2^-32
+            sn = __sinf(w);
+            cs = __cosf(w);
+        }
+        t.c[k] = cs * a.attn_scale;
+        t.s[k] = sn * a.attn_scale;
+    }
+}
+
+// The pairs (y_a, y_b) of a lane turned: forward by the angle, back by its
+// negative. Half layout: pair k is elements k and 4 + k; else 2 k and 2 k + 1.
+template <bool HALF, bool BACK>
+__device__ __forceinline__ void turn_pairs(float2 (&y)[4], const Trig& t) {
+    float s[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) s[k] = BACK ? -t.s[k] : t.s[k];
+    if constexpr (HALF) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const float2 u = y[k], v = y[2 + k];
+            y[k] = make_float2(fmaf(-v.x, s[2 * k], u.x * t.c[2 * k]), fmaf(-v.y, s[2 * k + 1], u.y * t.c[2 * k + 1]));
+            y[2 + k] = make_float2(fmaf(u.x, s[2 * k], v.x * t.c[2 * k]), fmaf(u.y, s[2 * k + 1], v.y * t.c[2 * k + 1]));
+        }
     } else {
-        raw.from_lane(p.partner).unpack(xp);
-    }
-}
-
-template <typename T>
-__device__ __forceinline__ void load_gamma(const void* gamma, int j, float2 (&g)[4]) {
-    if (gamma) {
-        Raw<T> r;
-        r.load(static_cast<const T*>(gamma) + 8 * j);
-        r.unpack(g);
-    } else {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) g[k] = make_float2(1.f, 1.f);
-    }
-}
-
-// ---------------------------------------------------------------- forward
-template <typename T, int D, bool NORM, int U>
-__device__ __forceinline__ void forward_rows(const T* src, T* dst, int H, int wi, int wpt, const void* gamma,
-                                             const float2 (&c)[4], const float2 (&s)[4], const RopeArgs& a,
-                                             const LanePlan& p) {
-    constexpr int LANES = D / 8, ROWS = 32 / LANES;
-    float2 A[4], B[4];
-    bool ready = false;
-    for (int hb = wi * ROWS; hb < H; hb += U * wpt * ROWS) {
-        Raw<T> raw[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int h = hb + u * wpt * ROWS + p.slot;
-            if (h < H) raw[u].load(src + (long long)h * D + 8 * p.j);
-            else raw[u].zero();
-        }
-        if (!ready) {
-            ready = true;
-            float2 g[4], gp[4];
-            if constexpr (NORM) {
-                load_gamma<T>(gamma, p.j, g);
-                if (a.interleaved) {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) gp[k] = make_float2(g[k].y, g[k].x);
-                } else {
-                    load_gamma<T>(gamma, p.partner % LANES, gp);
-                }
-            } else {
-#pragma unroll
-                for (int k = 0; k < 4; ++k) g[k] = gp[k] = make_float2(1.f, 1.f);
-            }
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                A[k] = __fmul2_rn(c[k], g[k]);
-                B[k] = __fmul2_rn(s[k], gp[k]);
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int h = hb + u * wpt * ROWS + p.slot;
-            float2 x[4], xp[4], z[4];
-            raw[u].unpack(x);
-            pair_of<T>(raw[u], x, a, p, xp);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) z[k] = __ffma2_rn(xp[k], B[k], __fmul2_rn(x[k], A[k]));
-            if constexpr (NORM) {
-                const float r = rsqrtf(row_sum<LANES>(dot2(x, x)) * (1.f / D) + a.eps);
-                const float2 r2 = make_float2(r, r);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) z[k] = __fmul2_rn(z[k], r2);
-            }
-            if (h < H) Raw<T>::store(dst + (long long)h * D + 8 * p.j, z);
+        for (int k = 0; k < 4; ++k) {
+            const float2 u = y[k];
+            y[k] = make_float2(fmaf(-u.y, s[k], u.x * t.c[k]), fmaf(u.x, s[k], u.y * t.c[k]));
         }
     }
 }
 
-template <typename T, int D, bool NORM>
+// Steps of ROWS rows to a part, all under way at once.
+template <typename T, bool BWD>
+__host__ __device__ constexpr int part_steps() {
+    return sizeof(T) == 2 ? 4 : 2;
+}
+
+// Forward and backward, a warp to a task: a token and a part of its Q or K heads.
+template <typename T, int D, bool NORM, bool HALF, bool BWD>
 __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const __grid_constant__ RopeArgs a) {
-    __shared__ float2 table[kWarps][kMaxPairs];
-    const LanePlan p = lane_plan<D / 8>(a);
-    const int warp = threadIdx.x / 32;
-    const int per_cta = kWarps / a.wpt;
-    const long long tok = (long long)blockIdx.x * per_cta + warp / a.wpt;
-    const int wi = warp % a.wpt;
+    constexpr int LANES = D / 8, ROWS = 32 / LANES;
+    constexpr int U = part_steps<T, BWD>();
+    __shared__ float2 share[BWD && NORM ? kWarps : 1][2][D / 2];
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int j = lane % LANES, slot = lane / LANES;
+    const bool rotated = 8 * j < a.rd;
+    const int col0 = HALF && rotated ? 4 * j : 8 * j, col1 = HALF && rotated ? (a.rd >> 1) + 4 * j : 8 * j + 4;
+    const unsigned parts = a.q_parts + a.k_parts;
+
     pdl_wait();   // the inputs may be the previous kernel's outputs
     pdl_trigger();
-    if (tok >= a.tokens) return;
-    fill_table(table[warp], a, tok, p.lane);
-    float2 c[4], s[4];
-    lane_trig(table[warp], a, p, c, s);
-    constexpr int U = 4;
-    forward_rows<T, D, NORM, U>(static_cast<const T*>(a.Q) + tok * a.ld_q, static_cast<T*>(a.Qo) + tok * a.ld_qo,
-                                a.Hq, wi, a.wpt, a.gamma_q, c, s, a, p);
-    forward_rows<T, D, NORM, U>(static_cast<const T*>(a.K) + tok * a.ld_k, static_cast<T*>(a.Ko) + tok * a.ld_ko,
-                                a.Hkv, wi, a.wpt, a.gamma_k, c, s, a, p);
-}
-
-// ---------------------------------------------------------------- backward
-template <typename T, int D, bool NORM, int U>
-__device__ __forceinline__ void backward_rows(const T* xsrc, const T* zsrc, T* dst, int H, int wi, int wpt,
-                                              const float2 (&g)[4], const float2 (&c)[4], const float2 (&s)[4],
-                                              const RopeArgs& a, const LanePlan& p, float2 (&dg)[4]) {
-    constexpr int LANES = D / 8, ROWS = 32 / LANES;
-    for (int hb = wi * ROWS; hb < H; hb += U * wpt * ROWS) {
-        Raw<T> rx[U], rz[U];
+    float2 dg[2][4];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int h = hb + u * wpt * ROWS + p.slot;
-            rz[u].zero();
-            if constexpr (NORM) rx[u].zero();
-            if (h < H) {
-                rz[u].load(zsrc + (long long)h * D + 8 * p.j);
-                if constexpr (NORM) rx[u].load(xsrc + (long long)h * D + 8 * p.j);
+    for (int k = 0; k < 4; ++k) dg[0][k] = dg[1][k] = make_float2(0.f, 0.f);
+    for (unsigned task = blockIdx.x * kWarps + warp; task < a.tasks; task += gridDim.x * kWarps) {
+        const unsigned tok = task / parts;
+        const int part = (int)(task - tok * parts);
+        const bool is_q = part < a.q_parts;
+        const int H = is_q ? a.Hq : a.Hkv;
+        const int h0 = (is_q ? part : part - a.q_parts) * U * ROWS + slot;
+        const long long at = (long long)h0 * D;
+        Raw<T, HALF> rx[U], rz[BWD ? U : 1];
+        if constexpr (!BWD || NORM) {
+            const T* x = static_cast<const T*>(is_q ? a.Q : a.K) + tok * (is_q ? a.ld_q : a.ld_k) + at;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                rx[u].zero();
+                if (h0 + u * ROWS < H) rx[u].load(x + u * ROWS * D + col0, x + u * ROWS * D + col1);
             }
         }
+        if constexpr (BWD) {
+            const T* z = static_cast<const T*>(is_q ? a.dQ : a.dK) + tok * (is_q ? a.ld_dq : a.ld_dk) + at;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int h = hb + u * wpt * ROWS + p.slot;
-            float2 z[4], zp[4], dy[4];
-            rz[u].unpack(z);
-            pair_of<T>(rz[u], z, a, p, zp);
-            // the inverse rotation: the forward's, with the sine's sign turned
+            for (int u = 0; u < U; ++u) {
+                rz[u].zero();
+                if (h0 + u * ROWS < H) rz[u].load(z + u * ROWS * D + col0, z + u * ROWS * D + col1);
+            }
+        }
+        float2 g[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                dy[k] = __ffma2_rn(zp[k], make_float2(-s[k].x, -s[k].y), __fmul2_rn(z[k], c[k]));
+        for (int k = 0; k < 4; ++k) g[k] = make_float2(1.f, 1.f);
+        if constexpr (NORM) {
+            const T* gamma = static_cast<const T*>(is_q ? a.gamma_q : a.gamma_k);
+            if (gamma) {
+                Raw<T, HALF> r;
+                r.load(gamma + col0, gamma + col1);
+                r.unpack(g);
+            }
+        }
+        Trig t;
+        angles<T>(t, a, a.positions ? (long long)a.positions[tok] : (long long)(tok % (unsigned)a.L), 4 * j, rotated);
+        T* o = static_cast<T*>(is_q ? a.Qo : a.Ko) + tok * (is_q ? a.ld_qo : a.ld_ko) + at;
+        if constexpr (!BWD) {
+            float r[U];
             if constexpr (NORM) {
-                float2 x[4], hh[4];
-                rx[u].unpack(x);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) hh[k] = __fmul2_rn(dy[k], g[k]);
-                float ss = dot2(x, x), hx = dot2(hh, x);
-                ss = row_sum<LANES>(ss);
-                hx = row_sum<LANES>(hx);
-                // (a row past the last head is all zeros: with eps = 0 its r would be infinite)
-                const float r = h < H ? rsqrtf(ss * (1.f / D) + a.eps) : 0.f;
-                const float2 r2 = make_float2(r, r);
-                // r^3 s / d_k, grouped so that no factor leaves the range before the others bring it back
-                const float m = -(r * hx) * (1.f / D) * r;
-                const float2 m2 = make_float2(m, m);
+                for (int u = 0; u < U; ++u) {
+                    float2 x[4];
+                    rx[u].unpack(x);
+                    r[u] = dot2(x, x);
+                }
+                row_sums<LANES, U>(r, lane, [&](float ss) { return rsqrtf(ss * (1.f / D) + a.eps); });
+            }
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float2 xh = __fmul2_rn(x[k], r2);
-                    dg[k] = __ffma2_rn(dy[k], xh, dg[k]);
-                    dy[k] = __ffma2_rn(xh, m2, __fmul2_rn(hh[k], r2));
+            for (int u = 0; u < U; ++u) {
+                float2 y[4];
+                rx[u].unpack(y);
+                if constexpr (NORM) {
+                    const float2 r2 = make_float2(r[u], r[u]);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) y[k] = __fmul2_rn(__fmul2_rn(y[k], r2), g[k]);
+                }
+                turn_pairs<HALF, false>(y, t);
+                if (h0 + u * ROWS < H) Raw<T, HALF>::store(o + u * ROWS * D + col0, o + u * ROWS * D + col1, y);
+            }
+        } else {
+#pragma unroll
+            for (int u0 = 0; u0 < U; u0 += 2) {   // two steps' sums at once
+                float2 dy[2][4];
+                float v[4];                       // sums of x^2 and of h x, of each step
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    rz[u0 + k].unpack(dy[k]);
+                    turn_pairs<HALF, true>(dy[k], t);
+                    if constexpr (NORM) {
+                        float2 x[4], hh[4];
+                        rx[u0 + k].unpack(x);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) hh[e] = __fmul2_rn(dy[k][e], g[e]);
+                        v[2 * k] = dot2(x, x);
+                        v[2 * k + 1] = dot2(hh, x);
+                    }
+                }
+                if constexpr (NORM) row_sums<LANES, 4>(v, lane, [](float x) { return x * (1.f / D); });
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const bool in = h0 + (u0 + k) * ROWS < H;
+                    if constexpr (NORM) {
+                        // r (h - xh mean(h xh)), xh = x r (rows past the last head are all zeros: r = 0 for eps = 0)
+                        const float r = in ? rsqrtf(v[2 * k] + a.eps) : 0.f;
+                        const float m = -(v[2 * k + 1] * r);
+                        const float2 r2 = make_float2(r, r), m2 = make_float2(m, m);
+                        float2 x[4];
+                        rx[u0 + k].unpack(x);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float2 xh = __fmul2_rn(x[e], r2), share_e = __fmul2_rn(dy[k][e], xh);
+                            if (is_q) dg[0][e] = __fadd2_rn(dg[0][e], share_e);
+                            else dg[1][e] = __fadd2_rn(dg[1][e], share_e);
+                            dy[k][e] = __fmul2_rn(__ffma2_rn(xh, m2, __fmul2_rn(dy[k][e], g[e])), r2);
+                        }
+                    }
+                    if (in) {
+                        T* to = o + (u0 + k) * ROWS * D;
+                        Raw<T, HALF>::store(to + col0, to + col1, dy[k]);
+                    }
                 }
             }
-            if (h < H) Raw<T>::store(dst + (long long)h * D + 8 * p.j, dy);
         }
     }
-}
-
-template <typename T, int D, bool NORM>
-__global__ void __launch_bounds__(kThreads) qk_norm_rope_bwd_kernel(const __grid_constant__ RopeArgs a) {
-    __shared__ float2 table[kWarps][kMaxPairs];
-    __shared__ float2 share[kWarps][2][D / 2];
-    constexpr int LANES = D / 8;
-    const LanePlan p = lane_plan<LANES>(a);
-    const int warp = threadIdx.x / 32;
-    const int per_cta = kWarps / a.wpt;
-    const int wi = warp % a.wpt;
-    pdl_wait();
-    pdl_trigger();
-    float2 gq[4], gk[4], dgq[4], dgk[4];
-    load_gamma<T>(NORM ? a.gamma_q : nullptr, p.j, gq);
-    load_gamma<T>(NORM ? a.gamma_k : nullptr, p.j, gk);
+    if constexpr (BWD && NORM) {
+        // the CTA's share of dgamma: a warp's rows, then the warps, in a fixed order
 #pragma unroll
-    for (int k = 0; k < 4; ++k) dgq[k] = dgk[k] = make_float2(0.f, 0.f);
-    constexpr int U = sizeof(T) == 2 ? 2 : 1;
-    for (long long tok = (long long)blockIdx.x * per_cta + warp / a.wpt; tok < a.tokens;
-         tok += (long long)gridDim.x * per_cta) {
-        __syncwarp();   // the table's readers of the previous token are done
-        fill_table(table[warp], a, tok, p.lane);
-        float2 c[4], s[4];
-        lane_trig(table[warp], a, p, c, s);
-        backward_rows<T, D, NORM, U>(static_cast<const T*>(a.Q) + tok * a.ld_q,
-                                     static_cast<const T*>(a.dQ) + tok * a.ld_dq,
-                                     static_cast<T*>(a.Qo) + tok * a.ld_qo, a.Hq, wi, a.wpt, gq, c, s, a, p, dgq);
-        backward_rows<T, D, NORM, U>(static_cast<const T*>(a.K) + tok * a.ld_k,
-                                     static_cast<const T*>(a.dK) + tok * a.ld_dk,
-                                     static_cast<T*>(a.Ko) + tok * a.ld_ko, a.Hkv, wi, a.wpt, gk, c, s, a, p, dgk);
-    }
-    if constexpr (NORM) {
-        // the CTA's share of dgamma: its rows, then its warps, in a fixed order
+        for (int q = 0; q < 2; ++q) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+            for (int k = 0; k < 4; ++k) {
 #pragma unroll
-            for (int sh = 16; sh >= LANES; sh >>= 1) {
-                dgq[k].x += __shfl_xor_sync(0xffffffffu, dgq[k].x, sh);
-                dgq[k].y += __shfl_xor_sync(0xffffffffu, dgq[k].y, sh);
-                dgk[k].x += __shfl_xor_sync(0xffffffffu, dgk[k].x, sh);
-                dgk[k].y += __shfl_xor_sync(0xffffffffu, dgk[k].y, sh);
+                for (int sh = 16; sh >= LANES; sh >>= 1) {
+                    dg[q][k].x += __shfl_xor_sync(0xffffffffu, dg[q][k].x, sh);
+                    dg[q][k].y += __shfl_xor_sync(0xffffffffu, dg[q][k].y, sh);
+                }
             }
-            if (p.slot == 0) {
-                share[warp][0][4 * p.j + k] = dgq[k];
-                share[warp][1][4 * p.j + k] = dgk[k];
+            if (slot == 0) {
+                share[warp][q][col0 / 2] = dg[q][0];
+                share[warp][q][col0 / 2 + 1] = dg[q][1];
+                share[warp][q][col1 / 2] = dg[q][2];
+                share[warp][q][col1 / 2 + 1] = dg[q][3];
             }
         }
         __syncthreads();
@@ -435,20 +388,10 @@ __global__ void __launch_bounds__(kThreads) dgamma_kernel(const float* __restric
     }
 }
 
-// Warps per token: one, as long as that gives every SM 16 warps; fewer tokens
-// are spread over up to 8 warps each, down to one row to a warp.
-int warps_per_token(long long tokens) {
-    const long long want = 16LL * plan_sms();
-    int w = 1;
-    while (w < kWarps && tokens * w < want) w *= 2;
-    return w;
-}
-
-// CTAs of the backward: each leaves one share of dgamma, so no more than two to an SM.
-long long bwd_ctas(long long tokens) {
-    const long long per_cta = kWarps / warps_per_token(tokens);
-    const long long need = (tokens + per_cta - 1) / per_cta;
-    const long long most = 2LL * plan_sms();
+// CTAs of the backward: each leaves one share of dgamma, so they stay for
+// several tasks, as many CTAs as fit on the SMs at once.
+long long bwd_ctas(long long tasks) {
+    const long long need = (tasks + kWarps - 1) / kWarps, most = kBwdCtasPerSm * plan_sms();
     return need < most ? need : most;
 }
 
@@ -481,34 +424,51 @@ int check_rows(const void* p, long long ld, int H, int dk, int dtype) {
     return GSDPA_OK;
 }
 
-void set_rope(RopeArgs& a, const gsdpa_rope* rope) {
-    a.rd = 0;
-    a.interleaved = 0;
+// What forward and backward share of the launch.
+int set_problem(RopeArgs& a, int steps, int B, int L, int Hq, int Hkv, int dk, float eps, const gsdpa_rope* rope,
+                const int* positions, const void* gamma_q, const void* gamma_k) {
+    a.positions = positions;
+    a.gamma_q = gamma_q;
+    a.gamma_k = gamma_k;
+    a.L = L;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    const int rows = 32 / (dk / 8) * steps;
+    a.q_parts = (Hq + rows - 1) / rows;
+    a.k_parts = (Hkv + rows - 1) / rows;
+    const long long tasks = (long long)B * L * (a.q_parts + a.k_parts);
+    if (tasks > 0x7fffffffLL) return GSDPA_ERR_UNSUPPORTED;
+    a.tasks = (unsigned)tasks;
+    a.eps = eps;
     a.attn_scale = 1.f;
-    for (int i = 0; i < kMaxPairs; ++i) a.turn[i] = 0;
-    if (!rope) return;
+    if (!rope) return GSDPA_OK;
     a.rd = rope->rotary_dim;
-    a.interleaved = rope->layout == GSDPA_ROPE_INTERLEAVED;
     a.attn_scale = rope->attn_scale;
     for (int i = 0; i < a.rd / 2; ++i) a.turn[i] = rope->turn[i];
+    return GSDPA_OK;
 }
 
-template <typename T, int D>
-cudaError_t launch_fwd(const RopeArgs& a, bool norm, cudaStream_t s) {
-    const long long per_cta = kWarps / a.wpt;
-    const dim3 grid((unsigned)((a.tokens + per_cta - 1) / per_cta));
-    return norm ? launch_dependent(qk_norm_rope_kernel<T, D, true>, grid, dim3(kThreads), 0, s, a)
-                : launch_dependent(qk_norm_rope_kernel<T, D, false>, grid, dim3(kThreads), 0, s, a);
+template <typename T, int D, bool BWD>
+cudaError_t launch_t(const RopeArgs& a, bool norm, bool half, unsigned grid, cudaStream_t s) {
+    const dim3 g(grid), t(kThreads);
+    if (norm)
+        return half ? launch_dependent(qk_norm_rope_kernel<T, D, true, true, BWD>, g, t, 0, s, a)
+                    : launch_dependent(qk_norm_rope_kernel<T, D, true, false, BWD>, g, t, 0, s, a);
+    return half ? launch_dependent(qk_norm_rope_kernel<T, D, false, true, BWD>, g, t, 0, s, a)
+                : launch_dependent(qk_norm_rope_kernel<T, D, false, false, BWD>, g, t, 0, s, a);
 }
-
-template <typename T, int D>
-cudaError_t launch_bwd(const RopeArgs& a, bool norm, void* dgq, void* dgk, cudaStream_t s) {
-    const dim3 grid((unsigned)bwd_ctas(a.tokens));
-    if (!norm) return launch_dependent(qk_norm_rope_bwd_kernel<T, D, false>, grid, dim3(kThreads), 0, s, a);
-    cudaError_t e = launch_dependent(qk_norm_rope_bwd_kernel<T, D, true>, grid, dim3(kThreads), 0, s, a);
-    if (e != cudaSuccess || (!dgq && !dgk)) return e;
-    return launch_dependent(dgamma_kernel<T>, dim3(2 * D / 8), dim3(kThreads), 0, s, (const float*)a.part,
-                            (int)grid.x, D, static_cast<T*>(dgq), static_cast<T*>(dgk));
+template <bool BWD>
+cudaError_t launch(const RopeArgs& a, bool norm, const gsdpa_rope* rope, int dk, int dtype, unsigned grid, cudaStream_t s) {
+    const bool half = rope && rope->layout == GSDPA_ROPE_HALF;   // (no rotation: the columns in order)
+    if (dtype == GSDPA_BF16)
+        return dk == 128 ? launch_t<__nv_bfloat16, 128, BWD>(a, norm, half, grid, s)
+                         : launch_t<__nv_bfloat16, 64, BWD>(a, norm, half, grid, s);
+    return dk == 128 ? launch_t<float, 128, BWD>(a, norm, half, grid, s) : launch_t<float, 64, BWD>(a, norm, half, grid, s);
+}
+template <typename T>
+cudaError_t launch_dgamma(const float* part, int parts, int dk, void* dgq, void* dgk, cudaStream_t s) {
+    return launch_dependent(dgamma_kernel<T>, dim3(2 * dk / 8), dim3(kThreads), 0, s, part, parts, dk, static_cast<T*>(dgq),
+                            static_cast<T*>(dgk));
 }
 
 }  // namespace
@@ -596,26 +556,15 @@ int gsdpa_qk_norm_rope(const void* Q, const void* K, const void* gamma_q, const 
     a.K = K;
     a.Qo = Qo;
     a.Ko = Ko;
-    a.gamma_q = gamma_q;
-    a.gamma_k = gamma_k;
-    a.positions = positions;
     a.ld_q = ld_q;
     a.ld_k = ld_k;
     a.ld_qo = ld_qo;
     a.ld_ko = ld_ko;
-    a.tokens = (long long)B * L;
-    a.L = L;
-    a.Hq = H_q;
-    a.Hkv = H_kv;
-    a.wpt = warps_per_token(a.tokens);
-    a.eps = eps;
-    set_rope(a, rope);
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
-    cudaError_t e;
-    if (dtype == GSDPA_BF16)
-        e = d_k == 128 ? launch_fwd<__nv_bfloat16, 128>(a, norm != 0, s) : launch_fwd<__nv_bfloat16, 64>(a, norm != 0, s);
-    else
-        e = d_k == 128 ? launch_fwd<float, 128>(a, norm != 0, s) : launch_fwd<float, 64>(a, norm != 0, s);
+    st = set_problem(a, dtype == GSDPA_BF16 ? part_steps<__nv_bfloat16, false>() : part_steps<float, false>(), B, L, H_q, H_kv,
+                     d_k, eps, rope, positions, gamma_q, gamma_k);
+    if (st != GSDPA_OK) return st;
+    const cudaError_t e = launch<false>(a, norm != 0, rope, d_k, dtype, (a.tasks + kWarps - 1) / kWarps,
+                                        static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? GSDPA_OK : GSDPA_ERR_LAUNCH;
 }
 
@@ -623,7 +572,7 @@ size_t gsdpa_qk_norm_rope_bwd_workspace_bytes(int B, int L, int d_k, int norm) {
     if (B < 0 || L < 0 || (d_k != 64 && d_k != 128) || (norm != 0 && norm != 1) || (long long)B * L > 0x7fffffffLL)
         return (size_t)-1;
     if (!norm || B == 0 || L == 0) return 0;
-    return (size_t)bwd_ctas((long long)B * L) * 2 * d_k * sizeof(float);
+    return (size_t)kBwdCtasPerSm * plan_sms() * 2 * d_k * sizeof(float);   // (the most CTAs there are)
 }
 
 int gsdpa_qk_norm_rope_bwd(const void* Q, const void* K, const void* gamma_q, const void* gamma_k,
@@ -662,9 +611,6 @@ int gsdpa_qk_norm_rope_bwd(const void* Q, const void* K, const void* gamma_q, co
     a.dK = dKo;
     a.Qo = dQ;
     a.Ko = dK;
-    a.gamma_q = gamma_q;
-    a.gamma_k = gamma_k;
-    a.positions = positions;
     a.part = static_cast<float*>(workspace);
     a.ld_q = ld_q;
     a.ld_k = ld_k;
@@ -672,21 +618,15 @@ int gsdpa_qk_norm_rope_bwd(const void* Q, const void* K, const void* gamma_q, co
     a.ld_dk = ld_dko;
     a.ld_qo = ld_dq;
     a.ld_ko = ld_dk;
-    a.tokens = (long long)B * L;
-    a.L = L;
-    a.Hq = H_q;
-    a.Hkv = H_kv;
-    a.wpt = warps_per_token(a.tokens);
-    a.eps = eps;
-    set_rope(a, rope);
+    st = set_problem(a, dtype == GSDPA_BF16 ? part_steps<__nv_bfloat16, true>() : part_steps<float, true>(), B, L, H_q, H_kv,
+                     d_k, eps, rope, positions, gamma_q, gamma_k);
+    if (st != GSDPA_OK) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    cudaError_t e;
-    if (dtype == GSDPA_BF16)
-        e = d_k == 128 ? launch_bwd<__nv_bfloat16, 128>(a, norm != 0, dgamma_q, dgamma_k, s)
-                       : launch_bwd<__nv_bfloat16, 64>(a, norm != 0, dgamma_q, dgamma_k, s);
-    else
-        e = d_k == 128 ? launch_bwd<float, 128>(a, norm != 0, dgamma_q, dgamma_k, s)
-                       : launch_bwd<float, 64>(a, norm != 0, dgamma_q, dgamma_k, s);
+    const int ctas = (int)(norm ? bwd_ctas(a.tasks) : (a.tasks + kWarps - 1) / kWarps);
+    cudaError_t e = launch<true>(a, norm != 0, rope, d_k, dtype, (unsigned)ctas, s);
+    if (e == cudaSuccess && (dgamma_q || dgamma_k))
+        e = dtype == GSDPA_BF16 ? launch_dgamma<__nv_bfloat16>(a.part, ctas, d_k, dgamma_q, dgamma_k, s)
+                                : launch_dgamma<float>(a.part, ctas, d_k, dgamma_q, dgamma_k, s);
     return e == cudaSuccess ? GSDPA_OK : GSDPA_ERR_LAUNCH;
 }
 

@@ -39,10 +39,12 @@
 namespace gsdpa {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;     // (256: 32/4 heads L4096 14.6 instead of 13.5 us)
 constexpr int kWarps = kThreads / 32;
+constexpr int kSumThreads = 256;
 constexpr int kMaxPairs = 64;
-constexpr int kBwdCtasPerSm = 3;
+constexpr int kRing = 3;          // backward: tasks whose rows a warp has in shared memory or on the way
+constexpr int kBwdCtasPerSm = 4;  // ... 4 CTAs of 48 KB
 
 struct RopeArgs {
     const void *Q, *K;            // forward: inputs; backward: the forward's inputs (null without the norm)
@@ -54,11 +56,13 @@ struct RopeArgs {
     long long ld_q, ld_k, ld_dq, ld_dk, ld_qo, ld_ko;
     int L, Hq, Hkv;
     int q_parts, k_parts;         // parts of a token's heads
-    unsigned tasks;               // tokens * (q_parts + k_parts)
+    unsigned tokens, tasks;       // B * L; tokens * (q_parts + k_parts)
+    int lg_split;                 // backward: warps that share a token's parts, 2^lg_split
     float eps;
     int rd;                       // rotated columns (0: none)
     float attn_scale;
-    unsigned long long turn[kMaxPairs];
+    WaitCtl ctl;
+    alignas(16) unsigned long long turn[kMaxPairs];
 };
 
 // 8 elements of a row in one lane: 4 at p and 4 at q.
@@ -164,9 +168,15 @@ __device__ __forceinline__ void angles(Trig& t, const RopeArgs& a, long long pos
         t.s[k] = 0.f;
     }
     if (!rotated) return;
+    // (a load from the parameters' generic address: indexed by the lane, constant memory would answer
+    // one lane after another)
+    unsigned long long turn[4];
+#pragma unroll
+    for (int k = 0; k < 4; k += 2)
+        asm("ld.v2.u64 {%0, %1}, [%2];" : "=l"(turn[k]), "=l"(turn[k + 1]) : "l"(a.turn + first_pair + k));
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-        const unsigned long long at = (unsigned long long)pos * a.turn[first_pair + k];
+        const unsigned long long at = (unsigned long long)pos * turn[k];
         const float x = (float)(int)(at >> 32);   // 2^-32 turns, within half a turn
         float sn, cs;
         if constexpr (std::is_same<T, float>::value) {
@@ -192,8 +202,10 @@ __device__ __forceinline__ void turn_pairs(float2 (&y)[4], const Trig& t) {
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             const float2 u = y[k], v = y[2 + k];
-            y[k] = make_float2(fmaf(-v.x, s[2 * k], u.x * t.c[2 * k]), fmaf(-v.y, s[2 * k + 1], u.y * t.c[2 * k + 1]));
-            y[2 + k] = make_float2(fmaf(u.x, s[2 * k], v.x * t.c[2 * k]), fmaf(u.y, s[2 * k + 1], v.y * t.c[2 * k + 1]));
+            const float2 c2 = make_float2(t.c[2 * k], t.c[2 * k + 1]), s2 = make_float2(s[2 * k], s[2 * k + 1]);
+            const float2 n2 = make_float2(-s2.x, -s2.y);
+            y[k] = __ffma2_rn(v, n2, __fmul2_rn(u, c2));
+            y[2 + k] = __ffma2_rn(u, s2, __fmul2_rn(v, c2));
         }
     } else {
 #pragma unroll
@@ -204,161 +216,284 @@ __device__ __forceinline__ void turn_pairs(float2 (&y)[4], const Trig& t) {
     }
 }
 
-// Steps of ROWS rows to a part, all under way at once.
-template <typename T, bool BWD>
+// Steps of ROWS rows to a part, all under way at once: 2 KB of rows.
+template <typename T>
 __host__ __device__ constexpr int part_steps() {
     return sizeof(T) == 2 ? 4 : 2;
 }
+constexpr int kPartBytes = 2048;
 
-// Forward and backward, a warp to a task: a token and a part of its Q or K heads.
-template <typename T, int D, bool NORM, bool HALF, bool BWD>
-__global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const __grid_constant__ RopeArgs a) {
-    constexpr int LANES = D / 8, ROWS = 32 / LANES;
-    constexpr int U = part_steps<T, BWD>();
-    __shared__ float2 share[BWD && NORM ? kWarps : 1][2][D / 2];
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int j = lane % LANES, slot = lane / LANES;
-    const bool rotated = 8 * j < a.rd;
-    const int col0 = HALF && rotated ? 4 * j : 8 * j, col1 = HALF && rotated ? (a.rd >> 1) + 4 * j : 8 * j + 4;
-    const unsigned parts = a.q_parts + a.k_parts;
-
-    pdl_wait();   // the inputs may be the previous kernel's outputs
-    pdl_trigger();
-    float2 dg[2][4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) dg[0][k] = dg[1][k] = make_float2(0.f, 0.f);
-    for (unsigned task = blockIdx.x * kWarps + warp; task < a.tasks; task += gridDim.x * kWarps) {
-        const unsigned tok = task / parts;
+// A warp's task: a token and a part of its Q or K heads.
+struct Task {
+    unsigned tok;
+    bool is_q;
+    int h0, rows;       // first head, heads (at most part_steps * ROWS)
+    long long at;       // of the first head in the token's row
+    template <int ROWS, int D>
+    __device__ __forceinline__ void set(const RopeArgs& a, unsigned task, int steps) {
+        const unsigned parts = a.q_parts + a.k_parts;
+        tok = task / parts;
         const int part = (int)(task - tok * parts);
-        const bool is_q = part < a.q_parts;
-        const int H = is_q ? a.Hq : a.Hkv;
-        const int h0 = (is_q ? part : part - a.q_parts) * U * ROWS + slot;
-        const long long at = (long long)h0 * D;
-        Raw<T, HALF> rx[U], rz[BWD ? U : 1];
-        if constexpr (!BWD || NORM) {
-            const T* x = static_cast<const T*>(is_q ? a.Q : a.K) + tok * (is_q ? a.ld_q : a.ld_k) + at;
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                rx[u].zero();
-                if (h0 + u * ROWS < H) rx[u].load(x + u * ROWS * D + col0, x + u * ROWS * D + col1);
-            }
-        }
-        if constexpr (BWD) {
-            const T* z = static_cast<const T*>(is_q ? a.dQ : a.dK) + tok * (is_q ? a.ld_dq : a.ld_dk) + at;
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                rz[u].zero();
-                if (h0 + u * ROWS < H) rz[u].load(z + u * ROWS * D + col0, z + u * ROWS * D + col1);
-            }
-        }
-        float2 g[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) g[k] = make_float2(1.f, 1.f);
-        if constexpr (NORM) {
-            const T* gamma = static_cast<const T*>(is_q ? a.gamma_q : a.gamma_k);
-            if (gamma) {
-                Raw<T, HALF> r;
-                r.load(gamma + col0, gamma + col1);
-                r.unpack(g);
-            }
-        }
-        Trig t;
-        angles<T>(t, a, a.positions ? (long long)a.positions[tok] : (long long)(tok % (unsigned)a.L), 4 * j, rotated);
-        T* o = static_cast<T*>(is_q ? a.Qo : a.Ko) + tok * (is_q ? a.ld_qo : a.ld_ko) + at;
-        if constexpr (!BWD) {
-            float r[U];
-            if constexpr (NORM) {
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    float2 x[4];
-                    rx[u].unpack(x);
-                    r[u] = dot2(x, x);
-                }
-                row_sums<LANES, U>(r, lane, [&](float ss) { return rsqrtf(ss * (1.f / D) + a.eps); });
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                float2 y[4];
-                rx[u].unpack(y);
-                if constexpr (NORM) {
-                    const float2 r2 = make_float2(r[u], r[u]);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) y[k] = __fmul2_rn(__fmul2_rn(y[k], r2), g[k]);
-                }
-                turn_pairs<HALF, false>(y, t);
-                if (h0 + u * ROWS < H) Raw<T, HALF>::store(o + u * ROWS * D + col0, o + u * ROWS * D + col1, y);
-            }
+        is_q = part < a.q_parts;
+        h0 = (is_q ? part : part - a.q_parts) * steps * ROWS;
+        rows = min(steps * ROWS, (is_q ? a.Hq : a.Hkv) - h0);
+        at = (long long)h0 * D;
+    }
+};
+
+__device__ __forceinline__ long long position(const RopeArgs& a, unsigned tok) {
+    return a.positions ? (long long)a.positions[tok] : (long long)(tok % (unsigned)a.L);
+}
+
+// The lane's columns of a row, and what it multiplies them by.
+template <typename T, int D, bool HALF>
+struct Lane {
+    int lane, j, slot, col0, col1;
+    bool rotated;
+    __device__ __forceinline__ explicit Lane(const RopeArgs& a) {
+        lane = threadIdx.x % 32;
+        j = lane % (D / 8);
+        slot = lane / (D / 8);
+        rotated = 8 * j < a.rd;
+        col0 = HALF && rotated ? 4 * j : 8 * j;
+        col1 = HALF && rotated ? (a.rd >> 1) + 4 * j : 8 * j + 4;
+    }
+    __device__ __forceinline__ void gamma(const void* p, float2 (&g)[4]) const {
+        if (p) {
+            Raw<T, HALF> r;
+            r.load(static_cast<const T*>(p) + col0, static_cast<const T*>(p) + col1);
+            r.unpack(g);
         } else {
 #pragma unroll
-            for (int u0 = 0; u0 < U; u0 += 2) {   // two steps' sums at once
-                float2 dy[2][4];
-                float v[4];                       // sums of x^2 and of h x, of each step
+            for (int k = 0; k < 4; ++k) g[k] = make_float2(1.f, 1.f);
+        }
+    }
+};
+
+// The forward: short warps, a task each, that hide one another's loads.
+template <typename T, int D, bool NORM, bool HALF>
+__global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const __grid_constant__ RopeArgs a) {
+    constexpr int LANES = D / 8, ROWS = 32 / LANES, U = part_steps<T>();
+    const unsigned task = blockIdx.x * kWarps + threadIdx.x / 32;
+    const Lane<T, D, HALF> ln(a);
+    pdl_wait();   // the inputs may be the previous kernel's outputs
+    pdl_trigger();
+    if (task >= a.tasks) return;
+    Task w = {};
+    w.set<ROWS, D>(a, task, U);
+    const T* x = static_cast<const T*>(w.is_q ? a.Q : a.K) + w.tok * (w.is_q ? a.ld_q : a.ld_k) + w.at + ln.slot * D;
+    T* o = static_cast<T*>(w.is_q ? a.Qo : a.Ko) + w.tok * (w.is_q ? a.ld_qo : a.ld_ko) + w.at + ln.slot * D;
+    Raw<T, HALF> rx[U];
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    rz[u0 + k].unpack(dy[k]);
-                    turn_pairs<HALF, true>(dy[k], t);
-                    if constexpr (NORM) {
-                        float2 x[4], hh[4];
-                        rx[u0 + k].unpack(x);
+    for (int u = 0; u < U; ++u) {
+        rx[u].zero();
+        if (u * ROWS + ln.slot < w.rows) rx[u].load(x + u * ROWS * D + ln.col0, x + u * ROWS * D + ln.col1);
+    }
+    float2 g[4];
+    if constexpr (NORM) ln.gamma(w.is_q ? a.gamma_q : a.gamma_k, g);
+    Trig t;
+    angles<T>(t, a, position(a, w.tok), 4 * ln.j, ln.rotated);
+    float r[U];
+    if constexpr (NORM) {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) hh[e] = __fmul2_rn(dy[k][e], g[e]);
-                        v[2 * k] = dot2(x, x);
-                        v[2 * k + 1] = dot2(hh, x);
+        for (int u = 0; u < U; ++u) {
+            float2 v[4];
+            rx[u].unpack(v);
+            r[u] = dot2(v, v);
+        }
+        row_sums<LANES, U>(r, ln.lane, [&](float ss) { return rsqrtf(ss * (1.f / D) + a.eps); });
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        if (u * ROWS >= w.rows) break;   // (the whole warp)
+        float2 y[4];
+        rx[u].unpack(y);
+        if constexpr (NORM) {
+            const float2 r2 = make_float2(r[u], r[u]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) y[k] = __fmul2_rn(__fmul2_rn(y[k], r2), g[k]);
+        }
+        turn_pairs<HALF, false>(y, t);
+        if (u * ROWS + ln.slot < w.rows)
+            Raw<T, HALF>::store(o + u * ROWS * D + ln.col0, o + u * ROWS * D + ln.col1, y);
+    }
+}
+
+// The backward: warps that stay (each CTA leaves a share of dgamma) and walk over
+// tokens, part by part, every warp with a ring of its own that asynchronous copies
+// keep filled with the rows of its next parts. It is bound by the instructions it issues,
+// so what does not change with the row is done once for the token.
+template <typename T, int D, bool NORM, bool HALF>
+__global__ void __launch_bounds__(kThreads, 4) qk_norm_rope_bwd_kernel(const __grid_constant__ RopeArgs a) {
+    constexpr int LANES = D / 8, ROWS = 32 / LANES, U = part_steps<T>();
+    constexpr int SLOT = (NORM ? 2 : 1) * kPartBytes;   // dz, and x with the norm
+    static_assert(U * ROWS * D * sizeof(T) == kPartBytes, "a part fills its half of a slot");
+    extern __shared__ __align__(128) uint8_t smem[];   // [warps][kRing][SLOT]
+    __shared__ uint64_t full[kWarps][kRing];
+    __shared__ int abort_flags[kWarps];
+    __shared__ float2 share[NORM ? kWarps : 1][2][D / 2];
+    const int warp = threadIdx.x / 32;
+    const Lane<T, D, HALF> ln(a);
+    uint8_t* ring = smem + warp * kRing * SLOT;
+    if (ln.lane == 0) {
+        for (int k = 0; k < kRing; ++k) mbar_init(&full[warp][k], 1);
+        abort_flags[warp] = 0;
+        mbar_fence_init();
+    }
+    __syncwarp();
+    pdl_wait();   // the inputs may be the previous kernel's outputs
+    pdl_trigger();
+
+    // the warp's tokens and, of each, its parts: every a.split-th
+    const unsigned gw = blockIdx.x * kWarps + warp, stride = (gridDim.x * kWarps) >> a.lg_split;
+    const unsigned tok0 = gw >> a.lg_split;
+    const int part0 = gw & ((1 << a.lg_split) - 1), step = 1 << a.lg_split, parts = a.q_parts + a.k_parts;
+    // the next part's copies (lane 0), and the place after it
+    unsigned next_tok = tok0;
+    int next_part = part0;
+    const auto fetch = [&](int slot) {
+        const bool is_q = next_part < a.q_parts;
+        const int h0 = (is_q ? next_part : next_part - a.q_parts) * U * ROWS;
+        const uint32_t bytes = min(U * ROWS, (is_q ? a.Hq : a.Hkv) - h0) * D * sizeof(T);
+        const long long at = (long long)h0 * D;
+        uint8_t* to = ring + slot * SLOT;
+        mbar_arrive_expect_tx(&full[warp][slot], NORM ? 2 * bytes : bytes);
+        bulk_load(to, static_cast<const T*>(is_q ? a.dQ : a.dK) + next_tok * (is_q ? a.ld_dq : a.ld_dk) + at, bytes,
+                  &full[warp][slot]);
+        if constexpr (NORM)
+            bulk_load(to + kPartBytes, static_cast<const T*>(is_q ? a.Q : a.K) + next_tok * (is_q ? a.ld_q : a.ld_k) + at,
+                      bytes, &full[warp][slot]);
+        next_part += step;
+        if (next_part >= parts) {
+            next_part = part0;
+            next_tok += stride;   // (no overflow: tokens and warps are below 2^30)
+        }
+    };
+    if (ln.lane == 0)
+        for (int k = 0; k < kRing; ++k)
+            if (next_tok < a.tokens) fetch(k);
+    float2 gq[4], gk[4], dgq[4], dgk[4];
+    if constexpr (NORM) {
+        ln.gamma(a.gamma_q, gq);
+        ln.gamma(a.gamma_k, gk);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) dgq[k] = dgk[k] = make_float2(0.f, 0.f);
+    int slot = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    Trig t;
+    // a part's rows from the slot, and their gradients to o
+    const auto part_rows = [&](const float2 (&g)[4], float2 (&dg)[4], T* o, int rows) {
+        const T* z = reinterpret_cast<const T*>(ring + slot * SLOT) + ln.slot * D;
+        const T* x = z + kPartBytes / sizeof(T);
+#pragma unroll
+        for (int u0 = 0; u0 < U; u0 += 2) {   // two steps' sums at once
+            if (u0 * ROWS >= rows) break;     // (the whole warp)
+            float2 dy[2][4], xs[2][4];
+            float v[4];                       // sums of x^2 and of h x, of each step
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const bool in = (u0 + k) * ROWS + ln.slot < rows;
+                const int off = (u0 + k) * ROWS * D;
+                Raw<T, HALF> r;
+                r.zero();   // (a slot's bytes past the part's rows are an earlier part's)
+                if (in) r.load(z + off + ln.col0, z + off + ln.col1);
+                r.unpack(dy[k]);
+                turn_pairs<HALF, true>(dy[k], t);
+                if constexpr (NORM) {
+                    r.zero();
+                    if (in) r.load(x + off + ln.col0, x + off + ln.col1);
+                    r.unpack(xs[k]);
+                    float2 hh[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) hh[e] = __fmul2_rn(dy[k][e], g[e]);
+                    v[2 * k] = dot2(xs[k], xs[k]);
+                    v[2 * k + 1] = dot2(hh, xs[k]);
+                }
+            }
+            if constexpr (NORM) row_sums<LANES, 4>(v, ln.lane, [](float s) { return s * (1.f / D); });
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const bool in = (u0 + k) * ROWS + ln.slot < rows;
+                if constexpr (NORM) {
+                    // r (h - xh mean(h xh)), xh = x r (rows past the last head are all zeros: r = 0 for eps = 0)
+                    const float r = in ? rsqrtf(v[2 * k] + a.eps) : 0.f;
+                    const float m = -(v[2 * k + 1] * r);
+                    const float2 r2 = make_float2(r, r), m2 = make_float2(m, m);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 xh = __fmul2_rn(xs[k][e], r2);
+                        dg[e] = __ffma2_rn(dy[k][e], xh, dg[e]);
+                        dy[k][e] = __fmul2_rn(__ffma2_rn(xh, m2, __fmul2_rn(dy[k][e], g[e])), r2);
                     }
                 }
-                if constexpr (NORM) row_sums<LANES, 4>(v, lane, [](float x) { return x * (1.f / D); });
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const bool in = h0 + (u0 + k) * ROWS < H;
-                    if constexpr (NORM) {
-                        // r (h - xh mean(h xh)), xh = x r (rows past the last head are all zeros: r = 0 for eps = 0)
-                        const float r = in ? rsqrtf(v[2 * k] + a.eps) : 0.f;
-                        const float m = -(v[2 * k + 1] * r);
-                        const float2 r2 = make_float2(r, r), m2 = make_float2(m, m);
-                        float2 x[4];
-                        rx[u0 + k].unpack(x);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float2 xh = __fmul2_rn(x[e], r2), share_e = __fmul2_rn(dy[k][e], xh);
-                            if (is_q) dg[0][e] = __fadd2_rn(dg[0][e], share_e);
-                            else dg[1][e] = __fadd2_rn(dg[1][e], share_e);
-                            dy[k][e] = __fmul2_rn(__ffma2_rn(xh, m2, __fmul2_rn(dy[k][e], g[e])), r2);
-                        }
-                    }
-                    if (in) {
-                        T* to = o + (u0 + k) * ROWS * D;
-                        Raw<T, HALF>::store(to + col0, to + col1, dy[k]);
-                    }
+                if (in) {
+                    T* to = o + (u0 + k) * ROWS * D;
+                    Raw<T, HALF>::store(to + ln.col0, to + ln.col1, dy[k]);
                 }
+            }
+        }
+    };
+    long long pos = tok0 < a.tokens ? position(a, tok0) : 0;
+    for (unsigned tok = tok0; ok && tok < a.tokens && part0 < parts; tok += stride) {
+        angles<T>(t, a, pos, 4 * ln.j, ln.rotated);
+        if (tok + stride < a.tokens) pos = position(a, tok + stride);
+        for (int part = part0; part < parts; part += step) {
+            ok = __all_sync(0xffffffffu, mbar_wait(&full[warp][slot], phase, &abort_flags[warp], a.ctl));
+            if (!ok) break;
+            if (part < a.q_parts) {
+                const int h0 = part * U * ROWS;
+                part_rows(gq, dgq, static_cast<T*>(a.Qo) + tok * a.ld_qo + (h0 + ln.slot) * D, a.Hq - h0);
+            } else {
+                const int h0 = (part - a.q_parts) * U * ROWS;
+                part_rows(gk, dgk, static_cast<T*>(a.Ko) + tok * a.ld_ko + (h0 + ln.slot) * D, a.Hkv - h0);
+            }
+            __syncwarp();   // every lane has read the slot
+            if (ln.lane == 0 && next_tok < a.tokens) fetch(slot);
+            if (++slot == kRing) {
+                slot = 0;
+                phase ^= 1u;
             }
         }
     }
-    if constexpr (BWD && NORM) {
+    if (!ok) {
+        // let copies in flight land before the CTA exits: of each slot, the phase being waited for
+        volatile int never = 0;
+        WaitCtl c2 = a.ctl;
+        if (c2.limit_ns < 1000000000ull) c2.limit_ns = 1000000000ull;
+        for (int k = 0; k < kRing; ++k) {
+            const int n = slot + k < kRing ? slot + k : slot + k - kRing;
+            mbar_wait(&full[warp][n], n >= slot ? phase : phase ^ 1u, &never, c2);
+        }
+    }
+    if constexpr (NORM) {
         // the CTA's share of dgamma: a warp's rows, then the warps, in a fixed order
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
+            float2(&dg)[4] = q == 0 ? dgq : dgk;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
 #pragma unroll
                 for (int sh = 16; sh >= LANES; sh >>= 1) {
-                    dg[q][k].x += __shfl_xor_sync(0xffffffffu, dg[q][k].x, sh);
-                    dg[q][k].y += __shfl_xor_sync(0xffffffffu, dg[q][k].y, sh);
+                    dg[k].x += __shfl_xor_sync(0xffffffffu, dg[k].x, sh);
+                    dg[k].y += __shfl_xor_sync(0xffffffffu, dg[k].y, sh);
                 }
             }
-            if (slot == 0) {
-                share[warp][q][col0 / 2] = dg[q][0];
-                share[warp][q][col0 / 2 + 1] = dg[q][1];
-                share[warp][q][col1 / 2] = dg[q][2];
-                share[warp][q][col1 / 2 + 1] = dg[q][3];
+            if (ln.slot == 0) {
+                share[warp][q][ln.col0 / 2] = dg[0];
+                share[warp][q][ln.col0 / 2 + 1] = dg[1];
+                share[warp][q][ln.col1 / 2] = dg[2];
+                share[warp][q][ln.col1 / 2 + 1] = dg[3];
             }
         }
         __syncthreads();
         const float* flat = reinterpret_cast<const float*>(share);
         for (int i = threadIdx.x; i < 2 * D; i += kThreads) {
-            float t = 0.f;
+            float s = 0.f;
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) t += flat[w * 2 * D + i];
-            a.part[(long long)blockIdx.x * 2 * D + i] = t;
+            for (int k = 0; k < kWarps; ++k) s += flat[k * 2 * D + i];
+            a.part[(long long)blockIdx.x * 2 * D + i] = s;
         }
     }
 }
@@ -366,7 +501,7 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const __grid_con
 // dgamma[c] = the CTAs' shares added up, always in the same order: 8 columns
 // to a CTA, 32 threads to a column.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) dgamma_kernel(const float* __restrict__ part, int parts, int d, T* dgq,
+__global__ void __launch_bounds__(kSumThreads) dgamma_kernel(const float* __restrict__ part, int parts, int d, T* dgq,
                                                           T* dgk) {
     __shared__ float red[32][8];
     pdl_wait();
@@ -390,8 +525,8 @@ __global__ void __launch_bounds__(kThreads) dgamma_kernel(const float* __restric
 
 // CTAs of the backward: each leaves one share of dgamma, so they stay for
 // several tasks, as many CTAs as fit on the SMs at once.
-long long bwd_ctas(long long tasks) {
-    const long long need = (tasks + kWarps - 1) / kWarps, most = kBwdCtasPerSm * plan_sms();
+long long bwd_ctas(long long tasks, int sms) {
+    const long long need = (tasks + kWarps - 1) / kWarps, most = kBwdCtasPerSm * (sms < plan_sms() ? sms : plan_sms());
     return need < most ? need : most;
 }
 
@@ -437,8 +572,13 @@ int set_problem(RopeArgs& a, int steps, int B, int L, int Hq, int Hkv, int dk, f
     a.q_parts = (Hq + rows - 1) / rows;
     a.k_parts = (Hkv + rows - 1) / rows;
     const long long tasks = (long long)B * L * (a.q_parts + a.k_parts);
-    if (tasks > 0x7fffffffLL) return GSDPA_ERR_UNSUPPORTED;
+    if (tasks > 0x7fffffffLL || (long long)B * L >= 1 << 30) return GSDPA_ERR_UNSUPPORTED;
+    a.tokens = (unsigned)(B * L);
     a.tasks = (unsigned)tasks;
+    // (backward) a warp to a token, or up to four while there are fewer tokens than warps
+    while (a.lg_split < 2 && (2 << a.lg_split) <= a.q_parts + a.k_parts &&
+           ((long long)a.tokens << a.lg_split) < kWarps * kBwdCtasPerSm * plan_sms())
+        ++a.lg_split;
     a.eps = eps;
     a.attn_scale = 1.f;
     if (!rope) return GSDPA_OK;
@@ -448,26 +588,34 @@ int set_problem(RopeArgs& a, int steps, int B, int L, int Hq, int Hkv, int dk, f
     return GSDPA_OK;
 }
 
-template <typename T, int D, bool BWD>
-cudaError_t launch_t(const RopeArgs& a, bool norm, bool half, unsigned grid, cudaStream_t s) {
-    const dim3 g(grid), t(kThreads);
-    if (norm)
-        return half ? launch_dependent(qk_norm_rope_kernel<T, D, true, true, BWD>, g, t, 0, s, a)
-                    : launch_dependent(qk_norm_rope_kernel<T, D, true, false, BWD>, g, t, 0, s, a);
-    return half ? launch_dependent(qk_norm_rope_kernel<T, D, false, true, BWD>, g, t, 0, s, a)
-                : launch_dependent(qk_norm_rope_kernel<T, D, false, false, BWD>, g, t, 0, s, a);
+template <typename T, int D, bool NORM, bool HALF>
+cudaError_t launch_n(const RopeArgs& a, bool bwd, unsigned grid, cudaStream_t s) {
+    if (!bwd) return launch_dependent(qk_norm_rope_kernel<T, D, NORM, HALF>, dim3(grid), dim3(kThreads), 0, s, a);
+    constexpr int bytes = kWarps * kRing * (NORM ? 2 : 1) * kPartBytes;
+    static PerDeviceSetup setup;
+    const cudaError_t e = setup_once_per_device(setup, [](int&) {
+        return cudaFuncSetAttribute(qk_norm_rope_bwd_kernel<T, D, NORM, HALF>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    bytes);
+    });
+    if (e != cudaSuccess) return e;
+    return launch_dependent(qk_norm_rope_bwd_kernel<T, D, NORM, HALF>, dim3(grid), dim3(kThreads), bytes, s, a);
 }
-template <bool BWD>
-cudaError_t launch(const RopeArgs& a, bool norm, const gsdpa_rope* rope, int dk, int dtype, unsigned grid, cudaStream_t s) {
+template <typename T, int D>
+cudaError_t launch_t(const RopeArgs& a, bool bwd, bool norm, bool half, unsigned grid, cudaStream_t s) {
+    if (norm) return half ? launch_n<T, D, true, true>(a, bwd, grid, s) : launch_n<T, D, true, false>(a, bwd, grid, s);
+    return half ? launch_n<T, D, false, true>(a, bwd, grid, s) : launch_n<T, D, false, false>(a, bwd, grid, s);
+}
+cudaError_t launch(const RopeArgs& a, bool bwd, bool norm, const gsdpa_rope* rope, int dk, int dtype, unsigned grid,
+                   cudaStream_t s) {
     const bool half = rope && rope->layout == GSDPA_ROPE_HALF;   // (no rotation: the columns in order)
     if (dtype == GSDPA_BF16)
-        return dk == 128 ? launch_t<__nv_bfloat16, 128, BWD>(a, norm, half, grid, s)
-                         : launch_t<__nv_bfloat16, 64, BWD>(a, norm, half, grid, s);
-    return dk == 128 ? launch_t<float, 128, BWD>(a, norm, half, grid, s) : launch_t<float, 64, BWD>(a, norm, half, grid, s);
+        return dk == 128 ? launch_t<__nv_bfloat16, 128>(a, bwd, norm, half, grid, s)
+                         : launch_t<__nv_bfloat16, 64>(a, bwd, norm, half, grid, s);
+    return dk == 128 ? launch_t<float, 128>(a, bwd, norm, half, grid, s) : launch_t<float, 64>(a, bwd, norm, half, grid, s);
 }
 template <typename T>
 cudaError_t launch_dgamma(const float* part, int parts, int dk, void* dgq, void* dgk, cudaStream_t s) {
-    return launch_dependent(dgamma_kernel<T>, dim3(2 * dk / 8), dim3(kThreads), 0, s, part, parts, dk, static_cast<T*>(dgq),
+    return launch_dependent(dgamma_kernel<T>, dim3(2 * dk / 8), dim3(kSumThreads), 0, s, part, parts, dk, static_cast<T*>(dgq),
                             static_cast<T*>(dgk));
 }
 
@@ -560,10 +708,10 @@ int gsdpa_qk_norm_rope(const void* Q, const void* K, const void* gamma_q, const 
     a.ld_k = ld_k;
     a.ld_qo = ld_qo;
     a.ld_ko = ld_ko;
-    st = set_problem(a, dtype == GSDPA_BF16 ? part_steps<__nv_bfloat16, false>() : part_steps<float, false>(), B, L, H_q, H_kv,
+    st = set_problem(a, dtype == GSDPA_BF16 ? part_steps<__nv_bfloat16>() : part_steps<float>(), B, L, H_q, H_kv,
                      d_k, eps, rope, positions, gamma_q, gamma_k);
     if (st != GSDPA_OK) return st;
-    const cudaError_t e = launch<false>(a, norm != 0, rope, d_k, dtype, (a.tasks + kWarps - 1) / kWarps,
+    const cudaError_t e = launch(a, false, norm != 0, rope, d_k, dtype, (a.tasks + kWarps - 1) / kWarps,
                                         static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? GSDPA_OK : GSDPA_ERR_LAUNCH;
 }
@@ -618,12 +766,14 @@ int gsdpa_qk_norm_rope_bwd(const void* Q, const void* K, const void* gamma_q, co
     a.ld_dk = ld_dko;
     a.ld_qo = ld_dq;
     a.ld_ko = ld_dk;
-    st = set_problem(a, dtype == GSDPA_BF16 ? part_steps<__nv_bfloat16, true>() : part_steps<float, true>(), B, L, H_q, H_kv,
+    st = set_problem(a, dtype == GSDPA_BF16 ? part_steps<__nv_bfloat16>() : part_steps<float>(), B, L, H_q, H_kv,
                      d_k, eps, rope, positions, gamma_q, gamma_k);
     if (st != GSDPA_OK) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const int ctas = (int)(norm ? bwd_ctas(a.tasks) : (a.tasks + kWarps - 1) / kWarps);
-    cudaError_t e = launch<true>(a, norm != 0, rope, d_k, dtype, (unsigned)ctas, s);
+    a.ctl.err = rt.err;
+    a.ctl.limit_ns = rt.limit_ns;
+    const int ctas = (int)bwd_ctas(a.tasks, rt.num_sms);
+    cudaError_t e = launch(a, true, norm != 0, rope, d_k, dtype, (unsigned)ctas, s);
     if (e == cudaSuccess && (dgamma_q || dgamma_k))
         e = dtype == GSDPA_BF16 ? launch_dgamma<__nv_bfloat16>(a.part, ctas, d_k, dgamma_q, dgamma_k, s)
                                 : launch_dgamma<float>(a.part, ctas, d_k, dgamma_q, dgamma_k, s);

@@ -119,6 +119,14 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* m, int
         : "memory");
 }
 
+// Untiled copy of `bytes` contiguous bytes (addresses and size multiples of 16).
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                     smem_u32(dst)),
+                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
+}
+
 // Five-dimensional tile load. With a tensor map whose innermost dimension is
 // 64 columns and whose outermost dimension steps through the 64-column blocks
 // of a row (stride 128 bytes), one request fills several consecutive

@@ -9,10 +9,10 @@
 //   e4m3: s = 2^e with the least e >= -126 that keeps amax <= 448 s (a power
 //         of two costs a floating-point code nothing but range and makes x / s
 //         exact), code = x / s rounded to nearest even.
-// The int8 quotient is decided exactly: q0 = rint(x * (1/s)) is off by one at
+// The int8 quotient is decided exactly: q0 = x * (1/s) rounded is off by one at
 // most, and the remainder x - q0 s, exact in one fused multiply-add (x has 8
 // significant bits, and where q0 is not zero its last bit is not below s's),
-// says which way.
+// says whether it is (hardly ever: four elements share the question).
 //
 // Bound by HBM for prompts (2 bytes in, 1 out for each element) and by latency
 // for single tokens. One CTA per (sequence, head, touched block) handles keys
@@ -49,8 +49,8 @@ __device__ __forceinline__ void unpack_bf16x8(const uint4& w, float (&f)[8]) {
     }
 }
 
-// |x| as bits: ordered like the values, NaN above infinity.
-__device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+// The largest |x| of two bf16 pairs each, as bits (ordered like the values, NaN above infinity).
+__device__ __forceinline__ uint32_t abs_max2(uint32_t m, uint32_t pair) { return __vmaxu2(m, pair & 0x7fff7fffu); }
 
 // A block's scale and how its elements are rounded.
 template <bool E4M3>
@@ -83,33 +83,48 @@ struct Quantiser {
             inv = __fdiv_rn(1.f, s);
         }
     }
-    __device__ __forceinline__ int code_int8(float x) const {
-        if (lift == 0.f) return 0;
+    // one code, exactly
+    __device__ __forceinline__ uint32_t exact(float x) const {
         const float y = x * lift;
         float q = rintf(y * inv);
         const float r = fmaf(-q, s, y), h = 0.5f * s;
-        const float up = r > 0.f ? 1.f : -1.f;
-        if (fabsf(r) > h || (fabsf(r) == h && ((int)q & 1))) q += up;
+        if (fabsf(r) > h || (fabsf(r) == h && ((int)q & 1))) q += r > 0.f ? 1.f : -1.f;
         q = fminf(fmaxf(q, -127.f), 127.f);
-        return (int)q;
+        return (uint32_t)(int)q & 255u;
     }
     // 4 codes as one word, the first in the lowest byte
     __device__ __forceinline__ uint32_t word(float a, float b, float c, float d) const {
+        if (lift == 0.f) return 0;
         if constexpr (E4M3) {
-            if (lift == 0.f) return 0;
             uint16_t lo, hi;
             asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b * inv), "f"(a * inv));
             asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d * inv), "f"(c * inv));
             return (uint32_t)lo | ((uint32_t)hi << 16);
         } else {
-            return ((uint32_t)code_int8(a) & 255u) | (((uint32_t)code_int8(b) & 255u) << 8) |
-                   (((uint32_t)code_int8(c) & 255u) << 16) | ((uint32_t)code_int8(d) << 24);
+            // x inv + 1.5 2^23 has the quotient, rounded to nearest even, in its low bits
+            constexpr float kRound = 12582912.f;
+            const float2 x[2] = {make_float2(a, b), make_float2(c, d)};
+            float2 t[2];
+            float off = 0.f;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                t[k] = __ffma2_rn(x[k], make_float2(inv, inv), make_float2(kRound, kRound));
+                const float2 q = __fadd2_rn(t[k], make_float2(-kRound, -kRound));
+                const float2 r = __ffma2_rn(q, make_float2(-s, -s), x[k]);
+                off = fmaxf(off, fmaxf(fabsf(r.x), fabsf(r.y)));
+            }
+            if (lift == 1.f && off < 0.5f * s) {   // every remainder is below half a step
+                const uint32_t lo = __byte_perm(__float_as_uint(t[0].x), __float_as_uint(t[0].y), 0x0040);
+                const uint32_t hi = __byte_perm(__float_as_uint(t[1].x), __float_as_uint(t[1].y), 0x0040);
+                return __byte_perm(lo, hi, 0x5410);
+            }
+            return exact(a) | (exact(b) << 8) | (exact(c) << 16) | (exact(d) << 24);
         }
     }
 };
 
 template <int D, bool E4M3>
-__global__ void __launch_bounds__(kThreads) cache8_append_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) cache8_append_kernel(const AppendArgs a) {
     constexpr int CH = D / 8;                              // 16-byte pieces of a row
     constexpr int KP = kCacheBlock * CH / kThreads;        // ... of the key tile per thread
     __shared__ uint32_t red[2][kThreads / 32];
@@ -135,8 +150,59 @@ __global__ void __launch_bounds__(kThreads) cache8_append_kernel(const AppendArg
     const bool has_v = vc < CH;
     const int p0 = j * kCacheBlock;
 
+    // The new tokens of the last two touched blocks also go to the open-block
+    // buffers: the last one may still be open, and the one before keeps the
+    // step reversible (a length taken back by up to 64 tokens finds its open
+    // block's tokens there).
+    const auto keep_open = [&]() {
+        for (int t = max(first, last - 1); t <= last; ++t) {
+            const int lo = max(q.len, t * kCacheBlock), hi = min(end, (t + 1) * kCacheBlock);
+            __nv_bfloat16* toK = tailK + (long long)(t & 1) * kCacheBlock * D;
+            __nv_bfloat16* toV = tailV + (long long)(t & 1) * kCacheBlock * D;
+            for (int i = tid; i < (hi - lo) * CH; i += kThreads) {
+                const int p = lo + i / CH, c = i % CH;
+                *reinterpret_cast<uint4*>(toK + (p - t * kCacheBlock) * D + 8 * c) =
+                    *reinterpret_cast<const uint4*>(newK + (long long)(p - q.len) * a.ld_k + 8 * c);
+            }
+            if (!has_v) continue;
+            const int pv = t * kCacheBlock + 4 * vq;
+            if (pv + 3 < lo || pv >= hi) continue;
+            uint32_t w[4][4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                uint4 r = make_uint4(0, 0, 0, 0);
+                if (pv + k >= lo && pv + k < hi)
+                    r = *reinterpret_cast<const uint4*>(newV + (long long)(pv + k - q.len) * a.ld_v + 8 * vc);
+                w[k][0] = r.x;
+                w[k][1] = r.y;
+                w[k][2] = r.z;
+                w[k][3] = r.w;
+            }
+            const bool whole = pv >= lo && pv + 3 < hi;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const uint32_t sel = (e & 1) ? 0x7632u : 0x5410u;
+                const uint32_t ab = __byte_perm(w[0][e / 2], w[1][e / 2], sel);
+                const uint32_t cd = __byte_perm(w[2][e / 2], w[3][e / 2], sel);
+                uint16_t* to = reinterpret_cast<uint16_t*>(toV) + (8 * vc + e) * kCacheBlock + 4 * vq;
+                if (whole) {
+                    *reinterpret_cast<uint2*>(to) = make_uint2(ab, cd);
+                } else {
+                    if (pv >= lo && pv < hi) to[0] = (uint16_t)ab;
+                    if (pv + 1 >= lo && pv + 1 < hi) to[1] = (uint16_t)(ab >> 16);
+                    if (pv + 2 >= lo && pv + 2 < hi) to[2] = (uint16_t)cd;
+                    if (pv + 3 >= lo && pv + 3 < hi) to[3] = (uint16_t)(cd >> 16);
+                }
+            }
+        }
+    };
+    // With one or two touched blocks no new token takes the place of an old one
+    // that the first block still needs, so there is nothing to wait for.
+    const bool early = last - first < 2;
+    if (x == 0 && early) keep_open();
+
     if (p0 + kCacheBlock <= end) {
-        uint4 kw[KP];
+        uint4 kw[KP], vw[4];
 #pragma unroll
         for (int i = 0; i < KP; ++i) {
             const int row = (i * kThreads + tid) / CH, c = (i * kThreads + tid) % CH;
@@ -145,8 +211,6 @@ __global__ void __launch_bounds__(kThreads) cache8_append_kernel(const AppendArg
                                                  : newK + (long long)(p - q.len) * a.ld_k;
             kw[i] = *reinterpret_cast<const uint4*>(src + 8 * c);
         }
-        uint4 vw[4];
-        uint2 old[8];
         const int pv = p0 + 4 * vq;
         const int n_old = q.len - pv;   // of the thread's 4 tokens, how many are in the open block
 #pragma unroll
@@ -155,39 +219,30 @@ __global__ void __launch_bounds__(kThreads) cache8_append_kernel(const AppendArg
             if (has_v && k >= n_old)
                 vw[k] = *reinterpret_cast<const uint4*>(newV + (long long)(pv + k - q.len) * a.ld_v + 8 * vc);
         }
+        if (has_v && n_old > 0) {   // (the first block only: 4 tokens of a column are 8 bytes there)
+            uint2 old[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            old[e] = make_uint2(0, 0);
-            if (has_v && n_old > 0)
-                old[e] = *reinterpret_cast<const uint2*>(tailV + ((long long)(j & 1) * D + 8 * vc + e) * kCacheBlock +
-                                                         4 * vq);
-        }
-        float v[4][8];
+            for (int e = 0; e < 8; ++e)
+                old[e] = *reinterpret_cast<const uint2*>(tailV + ((long long)(j & 1) * D + 8 * vc + e) * kCacheBlock + 4 * vq);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) unpack_bf16x8(vw[k], v[k]);
-        if (n_old > 0) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                if (0 < n_old) v[0][e] = __uint_as_float(old[e].x << 16);
-                if (1 < n_old) v[1][e] = __uint_as_float(old[e].x & 0xffff0000u);
-                if (2 < n_old) v[2][e] = __uint_as_float(old[e].y << 16);
-                if (3 < n_old) v[3][e] = __uint_as_float(old[e].y & 0xffff0000u);
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t sel = (k & 1) ? 0x7632u : 0x5410u;
+                if (k < n_old)
+                    vw[k] = k < 2 ? make_uint4(__byte_perm(old[0].x, old[1].x, sel), __byte_perm(old[2].x, old[3].x, sel),
+                                               __byte_perm(old[4].x, old[5].x, sel), __byte_perm(old[6].x, old[7].x, sel))
+                                  : make_uint4(__byte_perm(old[0].y, old[1].y, sel), __byte_perm(old[2].y, old[3].y, sel),
+                                               __byte_perm(old[4].y, old[5].y, sel), __byte_perm(old[6].y, old[7].y, sel));
             }
         }
         uint32_t mk = 0, mv = 0;
 #pragma unroll
-        for (int i = 0; i < KP; ++i) {
-            float f[8];
-            unpack_bf16x8(kw[i], f);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) mk = max(mk, abs_bits(f[e]));
-        }
+        for (int i = 0; i < KP; ++i)
+            mk = abs_max2(abs_max2(abs_max2(abs_max2(mk, kw[i].x), kw[i].y), kw[i].z), kw[i].w);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) mv = max(mv, abs_bits(v[k][e]));
-        mk = __reduce_max_sync(0xffffffffu, mk);
-        mv = __reduce_max_sync(0xffffffffu, mv);
+            mv = abs_max2(abs_max2(abs_max2(abs_max2(mv, vw[k].x), vw[k].y), vw[k].z), vw[k].w);
+        mk = __reduce_max_sync(0xffffffffu, max(mk & 0xffffu, mk >> 16));
+        mv = __reduce_max_sync(0xffffffffu, max(mv & 0xffffu, mv >> 16));
         if ((tid & 31) == 0) {
             red[0][tid / 32] = mk;
             red[1][tid / 32] = mv;
@@ -199,7 +254,7 @@ __global__ void __launch_bounds__(kThreads) cache8_append_kernel(const AppendArg
             mv = max(mv, red[1][w]);
         }
         const long long tile = (long long)unit * a.blocks + j;
-        const Quantiser<E4M3> qk(mk), qv(mv);
+        const Quantiser<E4M3> qk(mk << 16), qv(mv << 16);
         if (tid == 0) {
             a.k_scale[tile] = qk.scale;
             a.v_scale[tile] = qv.scale;
@@ -216,57 +271,18 @@ __global__ void __launch_bounds__(kThreads) cache8_append_kernel(const AppendArg
         }
         if (has_v) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                *reinterpret_cast<uint32_t*>(v8 + (8 * vc + e) * kCacheBlock + 4 * vq) =
-                    qv.word(v[0][e], v[1][e], v[2][e], v[3][e]);
-        }
-    }
-
-    // The new tokens of the last two touched blocks also go to the open-block
-    // buffers: the last one may still be open, and the one before keeps the
-    // step reversible (a length taken back by up to 64 tokens finds its open
-    // block's tokens there).
-    if (x != 0) return;
-    for (int t = max(first, last - 1); t <= last; ++t) {
-        const int lo = max(q.len, t * kCacheBlock), hi = min(end, (t + 1) * kCacheBlock);
-        __nv_bfloat16* toK = tailK + (long long)(t & 1) * kCacheBlock * D;
-        __nv_bfloat16* toV = tailV + (long long)(t & 1) * kCacheBlock * D;
-        for (int i = tid; i < (hi - lo) * CH; i += kThreads) {
-            const int p = lo + i / CH, c = i % CH;
-            *reinterpret_cast<uint4*>(toK + (p - t * kCacheBlock) * D + 8 * c) =
-                *reinterpret_cast<const uint4*>(newK + (long long)(p - q.len) * a.ld_k + 8 * c);
-        }
-        if (!has_v) continue;
-        uint32_t w[4][4];
+            for (int e = 0; e < 8; ++e) {
+                float f[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int p = t * kCacheBlock + 4 * vq + k;
-            uint4 r = make_uint4(0, 0, 0, 0);
-            if (p >= lo && p < hi)
-                r = *reinterpret_cast<const uint4*>(newV + (long long)(p - q.len) * a.ld_v + 8 * vc);
-            w[k][0] = r.x;
-            w[k][1] = r.y;
-            w[k][2] = r.z;
-            w[k][3] = r.w;
-        }
-        const int pv = t * kCacheBlock + 4 * vq;
-        const bool whole = pv >= lo && pv + 3 < hi;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const uint32_t sel = (e & 1) ? 0x7632u : 0x5410u;
-            const uint32_t ab = __byte_perm(w[0][e / 2], w[1][e / 2], sel);
-            const uint32_t cd = __byte_perm(w[2][e / 2], w[3][e / 2], sel);
-            uint16_t* to = reinterpret_cast<uint16_t*>(toV) + (8 * vc + e) * kCacheBlock + 4 * vq;
-            if (whole) {
-                *reinterpret_cast<uint2*>(to) = make_uint2(ab, cd);
-            } else {
-                if (pv >= lo && pv < hi) to[0] = (uint16_t)ab;
-                if (pv + 1 >= lo && pv + 1 < hi) to[1] = (uint16_t)(ab >> 16);
-                if (pv + 2 >= lo && pv + 2 < hi) to[2] = (uint16_t)cd;
-                if (pv + 3 >= lo && pv + 3 < hi) to[3] = (uint16_t)(cd >> 16);
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t r = e < 2 ? vw[k].x : (e < 4 ? vw[k].y : (e < 6 ? vw[k].z : vw[k].w));
+                    f[k] = __uint_as_float((e & 1) ? r & 0xffff0000u : r << 16);
+                }
+                *reinterpret_cast<uint32_t*>(v8 + (8 * vc + e) * kCacheBlock + 4 * vq) = qv.word(f[0], f[1], f[2], f[3]);
             }
         }
     }
+    if (x == 0 && !early) keep_open();
 }
 
 bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }

@@ -588,6 +588,25 @@ def _current_stream(device):
     return torch._C._cuda_getCurrentRawStream(index)
 
 
+_kept = {}
+
+
+def _kept_workspace(need, device, stream):
+    """A workspace for a call on this stream. One is kept for each stream, whose
+    calls follow one another; a captured call gets one of its own, which its graph
+    keeps (replays may run beside anything)."""
+    import torch
+    if need == 0:
+        return None
+    if torch.cuda.is_current_stream_capturing():
+        return torch.empty(need, dtype=torch.uint8, device=device)
+    key = (device.index, stream)
+    held = _kept.get(key)
+    if held is None or held.numel() < need:
+        held = _kept[key] = torch.empty(need, dtype=torch.uint8, device=device)
+    return held
+
+
 def _on_stream(call):
     """``stream=``: the call with that stream current, so that what it allocates
     (outputs, workspace) is that stream's own and not reused under its kernels."""
@@ -693,12 +712,15 @@ def qk_norm_rope_bwd(Q, K, dQo, dKo, *, gamma_q=None, gamma_k=None, norm=True, e
         out["dgamma_q"], out["dgamma_k"] = make(d_k, dtype=dt, device=dev), make(d_k, dtype=dt, device=dev)
         dgq, dgk = out["dgamma_q"].data_ptr(), out["dgamma_k"].data_ptr()
         need = qk_norm_rope_bwd_workspace_bytes(B, L, d_k)
-    workspace, ws_bytes = _workspace(workspace, need, dev)
+    stream = _current_stream(dev)
+    if workspace is not None:
+        workspace, need = _workspace(workspace, need, dev)
+    else:
+        workspace = _kept_workspace(need, dev, stream)
     st = (_lib or load()).gsdpa_qk_norm_rope_bwd(
         Q.data_ptr(), K.data_ptr(), gq, gk, pos, dQo.data_ptr(), dKo.data_ptr(), out_dq.data_ptr(), out_dk.data_ptr(),
         dgq, dgk, ld_q, ld_k, ld_dqo, ld_dko, ld_dq, ld_dk, B, L, H_q, H_kv, d_k, 1 if norm else 0, eps,
-        None if rope is None else rope.ref, code, None if workspace is None else workspace.data_ptr(), ws_bytes,
-        _current_stream(dev))
+        None if rope is None else rope.ref, code, None if workspace is None else workspace.data_ptr(), need, stream)
     if st != OK:
         raise GsdpaError(st, "gsdpa_qk_norm_rope_bwd")
     return out
@@ -745,21 +767,7 @@ class Cache8:
         self.plan = _Cache8Plan(kinds[k8.dtype], B, H, d, n * CACHE_BLOCK, k8.data_ptr(), v8.data_ptr(),
                                 k_scale.data_ptr(), v_scale.data_ptr(), k_tail.data_ptr(), v_tail.data_ptr())
         self.ref = ctypes.addressof(self.plan)
-        self.need, self.work = {}, {}
-
-    def workspace(self, need, stream):
-        """A workspace for a call on this stream: one is kept for each stream, whose
-        calls follow one another. A captured call gets one of its own, which its
-        graph keeps (replays may run beside anything)."""
-        import torch
-        if need == 0:
-            return None
-        if torch.cuda.is_current_stream_capturing():
-            return torch.empty(need, dtype=torch.uint8, device=self.device)
-        held = self.work.get(stream)
-        if held is None or held.numel() < need:
-            held = self.work[stream] = torch.empty(need, dtype=torch.uint8, device=self.device)
-        return held
+        self.need = {}   # workspace bytes, by the problem's shape
 
 
 def cache8_alloc(B, capacity, H_kv, d_k, kind="int8", device="cuda") -> Cache8:
@@ -844,7 +852,7 @@ def gated_sdpa_cache8(X, Q, cache, lens, W_g=None, *, gate="elementwise", n_new=
     if workspace is not None:
         workspace, need = _workspace(workspace, need, dev)
     else:
-        workspace = cache.workspace(need, stream)
+        workspace = _kept_workspace(need, dev, stream)
     st = lib.gated_sdpa_cache8(x, q, cache.ref, at, new, w, o, L_q, d_model, H_q, gm,
                                None if workspace is None else workspace.data_ptr(), need, stream)
     if st != OK:

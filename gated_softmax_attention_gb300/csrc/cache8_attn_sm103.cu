@@ -67,8 +67,9 @@ constexpr int kMaxCtas = 160;        // most CTAs (plan_sms)
 constexpr int kFanOne = 16;          // most CTAs whose parts of a head are merged at once
 constexpr int kFan = 8;              // ... else this many neighbours' at first
 constexpr int kMaxSources = 64;      // 2 heads' parts: of a CTA's warps, of kFanOne CTAs, or of kMaxCtas / kFan groups
-constexpr int kMaxGroups = 18;       // heads that a CTA has parts of, and one more; an even number
-static_assert((kMaxCtas + kFan - 1) / kFan <= 32 && kFanOne <= 32, "a lane to a source");
+constexpr int kMaxGroups = 18;       // heads that a CTA has parts of, and one more
+constexpr int kBatch = 8;            // sources that a thread of the merge has under way
+static_assert(2 * ((kMaxCtas + kFan - 1) / kFan) <= kMaxSources && 2 * kFanOne <= kMaxSources, "two heads' parts");
 constexpr int kTeamParts = 12;       // most teams to a head (about) for them to merge it without their CTAs
 constexpr int kWholeTiles = 16;      // most tiles of a head for one CTA to take it alone (see below)
 constexpr int kBars = 48;            // ring stages of all teams
@@ -454,7 +455,7 @@ struct Group {
     float* dest;
     int first, b, kvh, n;
 };
-static_assert(sizeof(Group) * kMaxGroups % 16 == 0 && kMaxGroups > 2 * kSlots, "what follows is 16-byte aligned");
+static_assert(kMaxGroups > 2 * kSlots, "each part a head of its own");
 
 // An end of a CTA's share that cuts a head: the head, the CTAs that have parts
 // of it, how far its merge is (0 nothing to do, 1 among neighbours, 2 of all), and
@@ -495,6 +496,7 @@ cache8_attn_kernel(const __grid_constant__ Cache8Args a) {
     if (tid < 2 * kSlots) s_piece[tid].rows = s_piece[tid].rows2 = nullptr;
     if (tid == 0) s_abort = 0;
     if (a.wait_first) pdl_wait();
+    pdl_trigger();   // the next kernel may be set up; it waits for this grid before it touches memory
 
     // ---- the CTA's share of all tiles, [lo, hi) of N, and the teams' shares of that
     const int per = (a.B + kThreads - 1) / kThreads;
@@ -550,10 +552,12 @@ cache8_attn_kernel(const __grid_constant__ Cache8Args a) {
             if (from < before || from >= before + mine || from == team_lo(k + 1)) continue;
             int at = from - before;
             int b = tid * per;
-            int in_seq = SeqTiles(a, b).tiles * a.Hkv;
-            while (at >= in_seq && b + 1 < a.B) {
-                at -= in_seq;
-                in_seq = SeqTiles(a, ++b).tiles * a.Hkv;
+            if (per > 1) {
+                int in_seq = SeqTiles(a, b).tiles * a.Hkv;
+                while (at >= in_seq && b + 1 < a.B) {
+                    at -= in_seq;
+                    in_seq = SeqTiles(a, ++b).tiles * a.Hkv;
+                }
             }
             s_b[k] = b;
             s_rem[k] = at;
@@ -1072,7 +1076,6 @@ cache8_attn_kernel(const __grid_constant__ Cache8Args a) {
     };
     const float** source = reinterpret_cast<const float**>(smem + (C::KS == 2 ? a.rows * STRIDE * 4 : 0));
     Group* s_group = reinterpret_cast<Group*>(source + kMaxSources);  // [groups + 1]
-    float* weight = reinterpret_cast<float*>(s_group + kMaxGroups);   // [sources][rows]
     if (warp == 0) {
         // a lane stands for a source (lane % 16: the part, upper half: its second warp's rows)
         const int piece = lane % (2 * kSlots);
@@ -1118,32 +1121,9 @@ cache8_attn_kernel(const __grid_constant__ Cache8Args a) {
     }
     for (;;) {
         sync_all();
-        const int groups = s_groups, total = s_group[groups].first;
-        float4* state = reinterpret_cast<float4*>(weight + ((total * a.rows + 3) & ~3));   // [groups][rows]: m, l, M, scale
-        // the sources' weights and each row's sums, a warp to a row, a lane to a source
-        for (int k = warp, gr = 0, row = warp; k < groups * a.rows; k += C::WARPS, row += C::WARPS) {
-            while (row >= a.rows) {
-                row -= a.rows;
-                ++gr;
-            }
-            const int i = s_group[gr].first + lane;
-            const bool in = i < s_group[gr + 1].first;
-            float4 x = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
-            if (in) x = *reinterpret_cast<const float4*>(source[i] + row * STRIDE + D);
-            float m = x.x, M = x.z;
-#pragma unroll
-            for (int sh = 1; sh < 32; sh <<= 1) {
-                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, sh));
-                M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, sh));
-            }
-            float l = x.y * part_weight(x.x, m);
-            if (in) weight[i * a.rows + row] = part_weight(x.z, M);
-#pragma unroll
-            for (int sh = 1; sh < 32; sh <<= 1) l += __shfl_xor_sync(0xffffffffu, l, sh);
-            if (lane == 0) state[k] = make_float4(m, l, M, out_scale(m, l, M));
-        }
-        sync_all();
-        // the weighted sums; a column's sources are split over lanes that would be idle
+        const int groups = s_groups;
+        // A thread has four columns of a row; its sources are split over lanes that
+        // would be idle, which merge theirs at the end.
         int lg = 0;
         while (lg < 3 && ((groups * items) << (lg + 1)) <= kConsumers) ++lg;
         for (int idx = tid; idx < (groups * items) << lg; idx += kConsumers) {
@@ -1154,43 +1134,65 @@ cache8_attn_kernel(const __grid_constant__ Cache8Args a) {
                 ++gr;
             }
             const int row = item / (D / 4), col = 4 * (item % (D / 4)), i1 = s_group[gr + 1].first;
+            float m = -INFINITY, l = 0.f, M = -INFINITY;
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int i0 = s_group[gr].first + sub; i0 < i1; i0 += 8 << lg) {   // eight loads under way
-                float4 v[8];
-                float w[8];
+            for (int i0 = s_group[gr].first + sub; i0 < i1; i0 += kBatch << lg) {   // a batch of loads under way
+                float4 x[kBatch], v[kBatch];
+                float mn = m, Mn = M;
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
+                for (int k = 0; k < kBatch; ++k) {
                     const int i = i0 + (k << lg);
+                    x[k] = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
                     v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    w[k] = 0.f;
                     if (i < i1) {
-                        v[k] = *reinterpret_cast<const float4*>(source[i] + row * STRIDE + col);
-                        w[k] = weight[i * a.rows + row];
+                        const float* from = source[i] + row * STRIDE;
+                        x[k] = *reinterpret_cast<const float4*>(from + D);
+                        v[k] = *reinterpret_cast<const float4*>(from + col);
                     }
                 }
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    o.x += v[k].x * w[k];
-                    o.y += v[k].y * w[k];
-                    o.z += v[k].z * w[k];
-                    o.w += v[k].w * w[k];
+                for (int k = 0; k < kBatch; ++k) {
+                    mn = fmaxf(mn, x[k].x);
+                    Mn = fmaxf(Mn, x[k].z);
+                }
+                const float w0 = part_weight(M, Mn);
+                l *= part_weight(m, mn);
+                o.x *= w0;
+                o.y *= w0;
+                o.z *= w0;
+                o.w *= w0;
+                m = mn;
+                M = Mn;
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) {
+                    const float w = part_weight(x[k].z, M);
+                    l += x[k].y * part_weight(x[k].x, m);
+                    o.x += v[k].x * w;
+                    o.y += v[k].y * w;
+                    o.z += v[k].z * w;
+                    o.w += v[k].w * w;
                 }
             }
             for (int sh = 1; sh < 1 << lg; sh <<= 1) {   // (whole warps: items come in sixteens)
-                o.x += __shfl_xor_sync(0xffffffffu, o.x, sh);
-                o.y += __shfl_xor_sync(0xffffffffu, o.y, sh);
-                o.z += __shfl_xor_sync(0xffffffffu, o.z, sh);
-                o.w += __shfl_xor_sync(0xffffffffu, o.w, sh);
+                const float m2 = __shfl_xor_sync(0xffffffffu, m, sh), M2 = __shfl_xor_sync(0xffffffffu, M, sh);
+                const float mn = fmaxf(m, m2), Mn = fmaxf(M, M2);
+                const float wa = part_weight(M, Mn), wb = part_weight(M2, Mn);
+                l = l * part_weight(m, mn) + __shfl_xor_sync(0xffffffffu, l, sh) * part_weight(m2, mn);
+                o.x = o.x * wa + __shfl_xor_sync(0xffffffffu, o.x, sh) * wb;
+                o.y = o.y * wa + __shfl_xor_sync(0xffffffffu, o.y, sh) * wb;
+                o.z = o.z * wa + __shfl_xor_sync(0xffffffffu, o.z, sh) * wb;
+                o.w = o.w * wa + __shfl_xor_sync(0xffffffffu, o.w, sh) * wb;
+                m = mn;
+                M = Mn;
             }
             if (sub != 0) continue;
             const Group& gp = s_group[gr];
-            const float4 x = state[gr * a.rows + row];
             if (!gp.dest) {
-                finish<D>(a, gp.b, gp.kvh, gp.n, row, col, x.w, o);
+                finish<D>(a, gp.b, gp.kvh, gp.n, row, col, out_scale(m, l, M), o);
             } else {
                 float* to = gp.dest + row * STRIDE;
                 *reinterpret_cast<float4*>(to + col) = o;
-                if (col == 0) *reinterpret_cast<float4*>(to + D) = x;
+                if (col == 0) *reinterpret_cast<float4*>(to + D) = make_float4(m, l, M, 0.f);
             }
         }
         sync_all();
@@ -1204,8 +1206,10 @@ cache8_attn_kernel(const __grid_constant__ Cache8Args a) {
                 const int n = all ? (e.parts + e.step - 1) / e.step : min(kFan, e.parts - (e.first - e.c0));
                 int* counter = a.counters + (all ? e.unit : a.B * a.Hkv + part_index(e.first, e.u0));
                 __threadfence();   // (after the barrier: covers what every thread has written)
-                if (atomicAdd(counter, 1) == n - 1) take = n;
-                __threadfence();
+                if (atomicAdd(counter, 1) == n - 1) {
+                    take = n;
+                    __threadfence();
+                }
                 e.level = take == 0 || all ? 0 : 2;
                 e.final = all;
             }
@@ -1218,20 +1222,18 @@ cache8_attn_kernel(const __grid_constant__ Cache8Args a) {
             const End& e = s_end[tid < n0 ? 0 : 1];
             source[tid] = part_of(e.first + (tid < n0 ? tid : tid - n0) * e.step, e.u0);
         }
+        if (tid < 2 && s_end[tid].take > 0) {
+            const End& e = s_end[tid];
+            Group& gr = s_group[tid == 1 && n0 > 0 ? 1 : 0];
+            gr.first = tid == 0 ? 0 : n0;
+            gr.b = e.b;
+            gr.kvh = e.kvh;
+            gr.n = e.n;
+            gr.dest = e.final ? nullptr : part_of(e.first, e.u0);
+        }
         if (tid == 0) {
-            int n = 0;
-            for (int k = 0; k < 2; ++k) {
-                const End& e = s_end[k];
-                if (e.take == 0) continue;
-                Group& gr = s_group[n++];
-                gr.first = k == 0 ? 0 : n0;
-                gr.b = e.b;
-                gr.kvh = e.kvh;
-                gr.n = e.n;
-                gr.dest = e.final ? nullptr : part_of(e.first, e.u0);
-            }
-            s_group[n].first = n0 + n1;
-            s_groups = n;
+            s_groups = (n0 > 0) + (n1 > 0);
+            s_group[s_groups].first = n0 + n1;
         }
     }
 

@@ -547,7 +547,8 @@ int validate(int B, int L, int Hq, int Hkv, int dk, int norm, float eps, const g
         if (!std::isfinite(rope->attn_scale)) return GSDPA_ERR_INVALID_ARG;
     }
     if (!aligned(gamma_q, 16) || !aligned(gamma_k, 16) || !aligned(positions, 4)) return GSDPA_ERR_ALIGNMENT;
-    if ((long long)B * L > 0x7fffffffLL) return GSDPA_ERR_UNSUPPORTED;
+    if ((long long)B * L > 0x7fffffffLL || (long long)Hq * dk > 0x7fffffffLL || (long long)Hkv * dk > 0x7fffffffLL)
+        return GSDPA_ERR_UNSUPPORTED;
     return GSDPA_OK;
 }
 

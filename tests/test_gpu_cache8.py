@@ -295,6 +295,35 @@ def test_attention_many_sequences_of_every_length():
     check_attention(O, None, Q, cache, None, "none", lens, new)
 
 
+@pytest.mark.parametrize("kind,Lq,G,gate", [("int8", 1, 4, "headwise"), ("e4m3", 1, 8, "none"), ("int8", 3, 4, "none")])
+def test_attention_heads_cut_into_few_parts(kind, Lq, G, gate):
+    # so many tiles that a team's share is of the order of a head: heads within a share, cut once,
+    # and cut several times, which the teams merge themselves
+    g = torch.Generator().manual_seed(35)
+    B, H, d = 24, 8, 64
+    lens = torch.randint(600, 2600, (B,), generator=g).tolist()
+    lens[3], lens[4], lens[11] = 0, 63, 2559
+    n = [Lq] * B
+    n[7] = 0
+    cache = fill_cache([a + b for a, b in zip(lens, n)], H, d, kind, 36)
+    Q = rows(B, Lq, H * G, d, 37, 1.5)
+    X, W = gate_inputs(gate, B, Lq, H * G, d, 256, 38)
+    O = gb.gated_sdpa_cache8(X, Q, cache, ints(*lens), W, gate=gate, n_new=ints(*n))
+    check_attention(O, X, Q, cache, W, gate, lens, n)
+    assert torch.equal(O, gb.gated_sdpa_cache8(X, Q, cache, ints(*lens), W, gate=gate, n_new=ints(*n)))
+
+
+@pytest.mark.parametrize("lens", [[1023, 0, 700], [1024], [1087, 3], [64 * 128]])
+def test_attention_in_a_cache_much_longer_than_its_sequences(lens):
+    # the grid is planned for the capacity; 16 tiles and 17 are on either side of a CTA to a head,
+    # 128 of a merge in one and in two levels
+    B, H, d = len(lens), 2, 128
+    cache = fill_cache([n + 1 for n in lens], H, d, "int8", 45, capacity=64 * 1024)
+    Q = rows(B, 1, 8, d, 46, 1.5)
+    O = gb.gated_sdpa_cache8(None, Q, cache, ints(*lens), gate="none")
+    check_attention(O, None, Q, cache, None, "none", lens, [1] * B)
+
+
 def test_attention_nothing_to_do_and_repeats():
     cache = fill_cache([5, 70], 2, 64, "int8", 33)
     Q = rows(2, 1, 4, 64, 34)
@@ -439,6 +468,45 @@ def test_two_streams_with_workspaces_of_their_own():
                                  stream=streams[i])
     torch.cuda.synchronize()
     assert all(torch.equal(outs[i][n], want[i]) for i in range(2) for n in range(10))
+
+
+def test_kept_workspaces_beside_a_graph_and_on_another_stream():
+    # eager calls keep a workspace for each stream, a captured call has its own: replays in between
+    # calls, and calls on a second stream at the same time, do not disturb them
+    cache = fill_cache([5000, 200], 2, 128, "e4m3", 85)
+    Q = rows(2, 1, 8, 128, 86)
+    lens = ints(4999, 199)
+    want = gb.gated_sdpa_cache8(None, Q, cache, lens, gate="none")
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=side):
+        captured = gb.gated_sdpa_cache8(None, Q, cache, lens, gate="none")
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(8):
+        with torch.cuda.stream(side):
+            graph.replay()
+        outs.append(gb.gated_sdpa_cache8(None, Q, cache, lens, gate="none"))
+        outs.append(gb.gated_sdpa_cache8(None, Q, cache, lens, gate="none", stream=side))
+    torch.cuda.synchronize()
+    assert torch.equal(captured, want) and all(torch.equal(o, want) for o in outs)
+
+
+def test_append_fewer_tokens_than_rows_of_a_padded_batch():
+    # L rows of K and V, more than the cache has room for; n_new of them are tokens
+    H, d = 2, 128
+    K, V = rows(3, 300, H, d, 12), rows(3, 300, H, d, 13)
+    cache = filled(3, 128, H, d, "int8")
+    gb.cache8_append(cache, K, V, ints(0, 0, 0), ints(128, 65, 0))
+    gb.cache8_append(cache, K[:, 200:].contiguous(), V[:, 200:].contiguous(), ints(128, 65, 0), ints(0, 63, 1))
+    want = filled(3, 128, H, d, "int8")
+    for b, parts in enumerate([[(0, 128)], [(0, 65), (200, 263)], [(200, 201)]]):
+        k, v = (torch.cat([t[b:b + 1, i:j] for i, j in parts], 1) for t in (K, V))
+        T = k.shape[1]
+        gb.cache8_append(want, k.expand(3, -1, -1, -1).contiguous(), v.expand(3, -1, -1, -1).contiguous(), ints(0, 0, 0),
+                         ints(*[T if x == b else 0 for x in range(3)]))
+        for h in range(H):
+            assert all(torch.equal(x, y) for x, y in zip(cache_rows(cache, b, h, T), cache_rows(want, b, h, T)))
 
 
 def test_refusals():

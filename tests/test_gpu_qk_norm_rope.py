@@ -61,7 +61,7 @@ def check_forward(out, x, gamma, pos, w, layout, scale, norm, eps=1e-6):
     assert not bool(bad.any()), f"{int(bad.sum())} of {bad.numel()}, worst {float(((out.double() - ref).abs() / (tol + 1e-300)).max()):.2f} x the tolerance"
 
 
-SHAPES = [(1, 1, 1, 1, 128), (2, 1, 8, 2, 64), (3, 7, 3, 1, 64), (2, 33, 16, 16, 128), (1, 300, 5, 2, 128)]
+SHAPES = [(1, 2, 131, 70, 64), (1, 1, 1, 1, 128), (2, 1, 8, 2, 64), (3, 7, 3, 1, 64), (2, 33, 16, 16, 128), (1, 300, 5, 2, 128)]
 ROPES = [(0, "half", {}), (128, "half", {}), (64, "interleaved", {}), (16, "interleaved", dict(scaling="linear", factor=4.0)),
          (48, "half", dict(scaling="base", factor=3.0, theta=500000.0)),
          (64, "half", dict(scaling="parts", factor=8.0, orig_len=4096))]
@@ -255,6 +255,22 @@ def test_captured_and_replayed_beside_an_eager_call():
     torch.cuda.synchronize()
     assert torch.equal(outs[0], q0) and torch.equal(outs[1], k0)
     assert all(torch.equal(g0[n], g1[n]) for n in g0)
+
+
+def test_on_another_stream_after_the_current_one():
+    # the outputs belong to the stream that the call ran on
+    _, Q, K, gq, gk, pos = make(2, 2000, 8, 2, 128, torch.bfloat16, 12)
+    kw = dict(gamma_q=gq, gamma_k=gk, rope=gb.Rope(64), positions=pos)
+    want = gb.qk_norm_rope(Q, K, **kw)
+    grads = gb.qk_norm_rope_bwd(Q, K, *want, **kw)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for _ in range(5):
+        q, k = gb.qk_norm_rope(Q, K, stream=side, **kw)
+        got = gb.qk_norm_rope_bwd(Q, K, q, k, stream=side, **kw)
+        side.synchronize()
+        assert torch.equal(q, want[0]) and torch.equal(k, want[1])
+        assert all(torch.equal(got[n], grads[n]) for n in grads)
 
 
 def test_refusals():

@@ -69,6 +69,7 @@ def test_qk_norm_rope_validation_before_any_device_work():
     assert rope_call(ld_q=1024) == gb.ERR_INVALID_ARG         # in place with another row length
     assert rope_call(d_k=96) == gb.ERR_UNSUPPORTED
     assert rope_call(B=1 << 20, L=1 << 20) == gb.ERR_UNSUPPORTED
+    assert rope_call(H_q=1 << 25) == gb.ERR_UNSUPPORTED
     assert rope_call(ld_k=260, Ko=32) == gb.ERR_ALIGNMENT     # a row that does not start on 16 bytes
     assert rope_call(Q=24) == gb.ERR_ALIGNMENT
     assert rope_call(gamma_q=24) == gb.ERR_ALIGNMENT

@@ -70,8 +70,8 @@ constexpr int kMaxSources = 64;      // 2 heads' parts: of a CTA's warps, of kFa
 constexpr int kMaxGroups = 18;       // heads that a CTA has parts of, and one more
 constexpr int kBatch = 8;            // sources that a thread of the merge has under way
 static_assert(2 * ((kMaxCtas + kFan - 1) / kFan) <= kMaxSources && 2 * kFanOne <= kMaxSources, "two heads' parts");
-constexpr int kTeamParts = 12;       // most teams to a head (about) for them to merge it without their CTAs
-constexpr int kWholeTiles = 16;      // most tiles of a head for one CTA to take it alone (see below)
+constexpr int kTeamRounds = 4;
+constexpr int kWholeTiles = 24;      // most tiles of a head for one CTA to take it alone (see below)
 constexpr int kBars = 48;            // ring stages of all teams
 constexpr uint32_t kSmemMax = 232448 - 1984;   // dynamic: what a CTA may have, less barriers, parts and a few words
 constexpr float kLog2e = 1.4426950408889634f;
@@ -442,6 +442,52 @@ __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
     return ok != 0;
 }
 
+// Four columns of a row, merged from several parts.
+struct Sums {
+    float m = -INFINITY, l = 0.f, M = -INFINITY;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    // parts i, i + step, .. below end; where(i) points to part i's row: its columns, then its m, l, M at `state`
+    template <typename F>
+    __device__ __forceinline__ void add(int i, int end, int step, int state, int col, F where) {
+        for (; i < end; i += kBatch * step) {   // a batch of loads under way
+            float4 x[kBatch], v[kBatch];
+            float mn = m, Mn = M;
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                x[k] = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
+                v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (i + k * step < end) {
+                    const float* from = where(i + k * step);
+                    x[k] = *reinterpret_cast<const float4*>(from + state);
+                    v[k] = *reinterpret_cast<const float4*>(from + col);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                mn = fmaxf(mn, x[k].x);
+                Mn = fmaxf(Mn, x[k].z);
+            }
+            const float w0 = part_weight(M, Mn);
+            l *= part_weight(m, mn);
+            o.x *= w0;
+            o.y *= w0;
+            o.z *= w0;
+            o.w *= w0;
+            m = mn;
+            M = Mn;
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                const float w = part_weight(x[k].z, M);
+                l += x[k].y * part_weight(x[k].x, m);
+                o.x += v[k].x * w;
+                o.y += v[k].y * w;
+                o.z += v[k].z * w;
+                o.w += v[k].w * w;
+            }
+        }
+    }
+};
+
 // A part of a cut head: where it is and whose.
 struct Piece {
     const float *rows, *rows2;   // [rows][STRIDE], in shared or global memory; what a second warp adds, or null
@@ -536,8 +582,11 @@ cache8_attn_kernel(const __grid_constant__ Cache8Args a) {
         hi = me < a.B * a.Hkv ? SeqTiles(a, me / a.Hkv).tiles : 0;
     }
     // Where a head is cut into few parts the teams merge it themselves, the last to
-    // arrive; else first each CTA what its teams have.
-    const bool by_team = !by_head && longest <= kTeamParts * deal.each;
+    // arrive (a team's threads need up to kTeamRounds rounds of loads for it); else
+    // each CTA first merges what its teams have.
+    const int most_parts = deal.each > 0 ? longest / deal.each + 2 : 1 << 20;
+    const bool by_team = !by_head && (most_parts + kBatch - 1) / kBatch *
+                                             ((a.rows * (D / 4) + 32 * team_warps - 1) / (32 * team_warps)) <= kTeamRounds;
     const auto team_lo = [&](int k) {
         return by_head ? Deal(hi, teams).from(k) : (me < ctas ? deal.from(me * teams + k) : N);
     };
@@ -1016,24 +1065,9 @@ cache8_attn_kernel(const __grid_constant__ Cache8Args a) {
                     if (a.gate_mode != GSDPA_GATE_NONE) pdl_wait();
                     for (int idx = team_tid; idx < a.rows * (D / 4); idx += team_threads) {
                         const int row = idx / (D / 4), col = 4 * (idx % (D / 4));
-                        float m = -INFINITY, l = 0.f, M = -INFINITY;
-                        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-                        for (int k = n0; k <= n1; ++k) {
-                            const float* from = team_part(k, u0) + row * STRIDE;
-                            const float4 x = __ldcg(reinterpret_cast<const float4*>(from + D));
-                            const float4 v = __ldcg(reinterpret_cast<const float4*>(from + col));
-                            const float mn = fmaxf(m, x.x), Mn = fmaxf(M, x.z);
-                            const float oa = part_weight(M, Mn), ob = part_weight(x.z, Mn);
-                            l = l * part_weight(m, mn) + x.y * part_weight(x.x, mn);
-                            m = mn;
-                            M = Mn;
-                            o.x = o.x * oa + v.x * ob;
-                            o.y = o.y * oa + v.y * ob;
-                            o.z = o.z * oa + v.z * ob;
-                            o.w = o.w * oa + v.w * ob;
-                        }
-                        finish<D>(a, at.b, at.kvh, q.n, row, col, out_scale(m, l, M), o);
+                        Sums r;
+                        r.add(n0, n1 + 1, 1, D, col, [&](int k) { return team_part(k, u0) + row * STRIDE; });
+                        finish<D>(a, at.b, at.kvh, q.n, row, col, out_scale(r.m, r.l, r.M), r.o);
                     }
                 }
             } else if (!final) {
@@ -1134,45 +1168,10 @@ cache8_attn_kernel(const __grid_constant__ Cache8Args a) {
                 ++gr;
             }
             const int row = item / (D / 4), col = 4 * (item % (D / 4)), i1 = s_group[gr + 1].first;
-            float m = -INFINITY, l = 0.f, M = -INFINITY;
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int i0 = s_group[gr].first + sub; i0 < i1; i0 += kBatch << lg) {   // a batch of loads under way
-                float4 x[kBatch], v[kBatch];
-                float mn = m, Mn = M;
-#pragma unroll
-                for (int k = 0; k < kBatch; ++k) {
-                    const int i = i0 + (k << lg);
-                    x[k] = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
-                    v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (i < i1) {
-                        const float* from = source[i] + row * STRIDE;
-                        x[k] = *reinterpret_cast<const float4*>(from + D);
-                        v[k] = *reinterpret_cast<const float4*>(from + col);
-                    }
-                }
-#pragma unroll
-                for (int k = 0; k < kBatch; ++k) {
-                    mn = fmaxf(mn, x[k].x);
-                    Mn = fmaxf(Mn, x[k].z);
-                }
-                const float w0 = part_weight(M, Mn);
-                l *= part_weight(m, mn);
-                o.x *= w0;
-                o.y *= w0;
-                o.z *= w0;
-                o.w *= w0;
-                m = mn;
-                M = Mn;
-#pragma unroll
-                for (int k = 0; k < kBatch; ++k) {
-                    const float w = part_weight(x[k].z, M);
-                    l += x[k].y * part_weight(x[k].x, m);
-                    o.x += v[k].x * w;
-                    o.y += v[k].y * w;
-                    o.z += v[k].z * w;
-                    o.w += v[k].w * w;
-                }
-            }
+            Sums r;
+            r.add(s_group[gr].first + sub, i1, 1 << lg, D, col, [&](int i) { return source[i] + row * STRIDE; });
+            float &m = r.m, &l = r.l, &M = r.M;
+            float4& o = r.o;
             for (int sh = 1; sh < 1 << lg; sh <<= 1) {   // (whole warps: items come in sixteens)
                 const float m2 = __shfl_xor_sync(0xffffffffu, m, sh), M2 = __shfl_xor_sync(0xffffffffu, M, sh);
                 const float mn = fmaxf(m, m2), Mn = fmaxf(M, M2);
@@ -1382,9 +1381,13 @@ int gated_sdpa_cache8(const void* X, const void* Q, const gsdpa_cache8* cache, c
     ZeroJob zero;
     zero.p = reinterpret_cast<int*>(ws + pl.counters);
     zero.n = pl.n_counters;
+    // (Where every head is one CTA's, however long the sequences are, there are none to zero.)
+    const int sms = rt.num_sms < kMaxCtas ? rt.num_sms : kMaxCtas;
+    const bool whole = cache->capacity / kCacheBlock <= kWholeTiles && (long long)cache->B * cache->H_kv <= sms;
+    if (whole) zero.n = 0;
     bool launched = false;
     cudaError_t e = launch_gate_logits_bf16(pl.p, pl.w, ws, rt, s, &launched, zero);
-    if (e == cudaSuccess && !launched)
+    if (e == cudaSuccess && !launched && !whole)
         e = launch_dependent(zero_counters_kernel, dim3((zero.n + 255) / 256), dim3(256), 0, s, zero.p, zero.n);
     if (e == cudaErrorInvalidValue) return GSDPA_ERR_INVALID_ARG;
     if (e != cudaSuccess) return GSDPA_ERR_LAUNCH;
@@ -1425,9 +1428,8 @@ int gated_sdpa_cache8(const void* X, const void* Q, const gsdpa_cache8* cache, c
     a.ctl.limit_ns = rt.limit_ns;
     // one CTA per SM, fewer where a full cache would not give each its tiles
     const long long most = (long long)a.B * a.Hkv * ((a.blocks + kSlots / a.R - 1) / (kSlots / a.R));
-    long long grid = rt.num_sms < plan_sms() ? rt.num_sms : plan_sms();
+    long long grid = sms;   // (no fewer than the heads, where those fit)
     if (grid > most) grid = most;
-    if (grid > kMaxCtas) grid = kMaxCtas;
     const bool e4m3 = cache->kind == GSDPA_CACHE_E4M3;
     if (cache->d_k == 128)
         e = e4m3 ? launch<128, true>(a, sh, (unsigned)grid, s) : launch<128, false>(a, sh, (unsigned)grid, s);

@@ -351,7 +351,10 @@ __global__ void __launch_bounds__(kThreads, 4) qk_norm_rope_bwd_kernel(const __g
     // the next part's copies (lane 0), and the place after it
     unsigned next_tok = tok0;
     int next_part = part0;
+    uint32_t fetched[kRing] = {};   // how often each slot was filled
     const auto fetch = [&](int slot) {
+#pragma unroll
+        for (int k = 0; k < kRing; ++k) fetched[k] += k == slot ? 1 : 0;
         const bool is_q = next_part < a.q_parts;
         const int h0 = (is_q ? next_part : next_part - a.q_parts) * U * ROWS;
         const uint32_t bytes = min(U * ROWS, (is_q ? a.Hq : a.Hkv) - h0) * D * sizeof(T);
@@ -457,16 +460,16 @@ __global__ void __launch_bounds__(kThreads, 4) qk_norm_rope_bwd_kernel(const __g
             }
         }
     }
-    if (!ok) {
-        // let copies in flight land before the CTA exits: of each slot, the phase being waited for
+    if (!ok && ln.lane == 0) {
+        // let copies in flight land before the CTA exits
         volatile int never = 0;
         WaitCtl c2 = a.ctl;
         if (c2.limit_ns < 1000000000ull) c2.limit_ns = 1000000000ull;
-        for (int k = 0; k < kRing; ++k) {
-            const int n = slot + k < kRing ? slot + k : slot + k - kRing;
-            mbar_wait(&full[warp][n], n >= slot ? phase : phase ^ 1u, &never, c2);
-        }
+#pragma unroll
+        for (int k = 0; k < kRing; ++k)
+            if (fetched[k] > 0) mbar_wait(&full[warp][k], (fetched[k] - 1) & 1u, &never, c2);
     }
+    __syncwarp();
     if constexpr (NORM) {
         // the CTA's share of dgamma: a warp's rows, then the warps, in a fixed order
 #pragma unroll

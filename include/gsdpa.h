@@ -486,7 +486,7 @@ GSDPA_API int gsdpa_cache8_append(const gsdpa_cache8* cache, const void* K, cons
 /*
  * The gated attention of a step's tokens against the cache, after their keys and
  * values have been appended: query row i of sequence b sees tokens 0 .. lens[b] + i.
- *   Q, O   : device bf16 [B, L_q, H_q, d_k].   X : bf16 [B, L_q, d_model].
+ *   Q, O   : device bf16 [B, L_q, H_q, d_k]; O overlaps no input.   X : bf16 [B, L_q, d_model].
  *   W_g    : as for gated_sdpa_fwd; gate_mode NONE, HEADWISE or ELEMENTWISE.
  *   lens   : device int32 [B], the tokens BEFORE this step (as passed to the append).
  *   n_new  : device int32 [B], rows of this step, or NULL for L_q each. Rows i >=
@@ -497,7 +497,7 @@ GSDPA_API int gsdpa_cache8_append(const gsdpa_cache8* cache, const void* K, cons
  * rows and GSDPA_ERR_CACHE_RANGE from the next gsdpa_check_device_error. Tokens past
  * a sequence's end are not seen whatever their bytes; a NaN or infinity among the
  * step's own keys is seen by the rows that may see it, one among its values in the
- * open block by every row of the step.
+ * open block, or a NaN code in v8, by every row of the step.
  * workspace: gsdpa_cache8_workspace_bytes(...) bytes, 256-byte aligned; calls that
  * share one must not overlap on the device. Asynchronous on `stream`; other errors
  * as for gated_sdpa_fwd.

@@ -545,6 +545,34 @@ def test_refusals():
         gb.Cache8(cache.k8, cache.v8, cache.k_scale, cache.v_scale[:, :, :1], cache.k_tail, cache.v_tail)
 
 
+def test_waits_that_run_out_are_reported_and_leave_nothing_behind():
+    # with a limit of 1 ns any wait that is not over within its first tries gives up: the calls report
+    # OK or a timeout, never a fault, and the next ones with the default limit are right
+    cache = fill_cache([30000, 700, 64 * 16], 2, 128, "int8", 87)
+    Q = rows(3, 1, 8, 128, 88)
+    lens, n = [29999, 699, 64 * 16 - 1], [1, 1, 1]
+    G = 2000
+    x, dx = rows(1, G, 6, 128, 89), rows(1, G, 6, 128, 90)
+    rope = gb.Rope(128)
+    want = gb.qk_norm_rope_bwd(x, x[:, :, :2].contiguous(), dx, dx[:, :, :2].contiguous(), rope=rope)
+    statuses = []
+    for _ in range(3):
+        gb.set_wait_limit_ns(1)
+        try:
+            gb.gated_sdpa_cache8(None, Q, cache, ints(*lens), gate="none")
+            statuses.append(gb.check_device_error())
+            gb.qk_norm_rope_bwd(x, x[:, :, :2].contiguous(), dx, dx[:, :, :2].contiguous(), rope=rope)
+            statuses.append(gb.check_device_error())
+        finally:
+            gb.set_wait_limit_ns(0)
+        O = gb.gated_sdpa_cache8(None, Q, cache, ints(*lens), gate="none")
+        got = gb.qk_norm_rope_bwd(x, x[:, :, :2].contiguous(), dx, dx[:, :, :2].contiguous(), rope=rope)
+        assert gb.check_device_error() == gb.OK
+        check_attention(O, None, Q, cache, None, "none", lens, n)
+        assert all(torch.equal(got[k], want[k]) for k in want)
+    assert set(statuses) <= {gb.OK, gb.ERR_DEVICE_TIMEOUT}
+
+
 # ---------------------------------------------------------------- together, as they are used
 @pytest.mark.parametrize("kind", KINDS)
 def test_a_prompt_and_decoding_steps_together(kind):

@@ -60,17 +60,12 @@
 namespace gsdpa {
 namespace {
 
-constexpr int kSlots = 8;            // warps' parts in the merge buffer
+constexpr int kSlots = 8;            // most teams of a CTA, and warps that share no tokens
 constexpr int kMaxRows = 128;        // query rows (heads of a group x new tokens) per K/V head
 constexpr int kMaxStages = 16;       // ring stages per team
 constexpr int kMaxCtas = 160;        // most CTAs (plan_sms)
-constexpr int kFanOne = 16;          // most CTAs whose parts of a head are merged at once
-constexpr int kFan = 8;              // ... else this many neighbours' at first
-constexpr int kMaxSources = 64;      // 2 heads' parts: of a CTA's warps, of kFanOne CTAs, or of kMaxCtas / kFan groups
-constexpr int kMaxGroups = 18;       // heads that a CTA has parts of, and one more
-constexpr int kBatch = 8;            // sources that a thread of the merge has under way
-static_assert(2 * ((kMaxCtas + kFan - 1) / kFan) <= kMaxSources && 2 * kFanOne <= kMaxSources, "two heads' parts");
-constexpr int kTeamRounds = 4;
+constexpr int kMergeThreads = 512;
+constexpr int kBatch = 8;            // parts that a thread of a merge has under way
 constexpr int kWholeTiles = 24;      // most tiles of a head for one CTA to take it alone (see below)
 constexpr int kBars = 48;            // ring stages of all teams
 constexpr uint32_t kSmemMax = 232448 - 1984;   // dynamic: what a CTA may have, less barriers, parts and a few words
@@ -92,20 +87,11 @@ struct Cache8Args {
     int R, stages;                   // groups of query rows (of 8 NT) to a team; ring stages per team
     const float* gate_part;          // [gate_splits, B * Lq, gate_cols] or null
     int gate_splits, gate_cols, gate_mode;
-    float* piece;                    // [CTAs][teams][2][rows][D + 4]: a team's first and last head
-    float* part;                     // [CTAs][2][rows][D + 4]: a CTA's first and last head
-    int* counters;                   // [B * Hkv], then [2 * CTAs]
+    float* part;                     // [CTAs][teams][2][rows][D + 4]: a team's first and last head, where cut
+    int ctas;                        // of the attention kernel
     int wait_first;                  // no gate kernel: everything before this kernel is waited for at once
     WaitCtl ctl;
 };
-
-// Zeroes the arrival counters where no gate kernel does. The attention kernel is
-// let start at once and waits for this one to end.
-__global__ void zero_counters_kernel(int* __restrict__ p, int n) {
-    pdl_trigger();
-    pdl_wait();
-    for (int k = blockIdx.x * blockDim.x + threadIdx.x; k < n; k += gridDim.x * blockDim.x) p[k] = 0;
-}
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -486,30 +472,74 @@ struct Sums {
             }
         }
     }
+    __device__ __forceinline__ void join(float m2, float l2, float M2, const float4& o2) {
+        const float mn = fmaxf(m, m2), Mn = fmaxf(M, M2);
+        const float wa = part_weight(M, Mn), wb = part_weight(M2, Mn);
+        l = l * part_weight(m, mn) + l2 * part_weight(m2, mn);
+        o.x = o.x * wa + o2.x * wb;
+        o.y = o.y * wa + o2.y * wb;
+        o.z = o.z * wa + o2.z * wb;
+        o.w = o.w * wa + o2.w * wb;
+        m = mn;
+        M = Mn;
+    }
+    __device__ __forceinline__ void join_lane(int sh) {
+        const float m2 = __shfl_xor_sync(0xffffffffu, m, sh), l2 = __shfl_xor_sync(0xffffffffu, l, sh);
+        const float M2 = __shfl_xor_sync(0xffffffffu, M, sh);
+        join(m2, l2, M2, make_float4(__shfl_xor_sync(0xffffffffu, o.x, sh), __shfl_xor_sync(0xffffffffu, o.y, sh),
+                                     __shfl_xor_sync(0xffffffffu, o.z, sh), __shfl_xor_sync(0xffffffffu, o.w, sh)));
+    }
 };
 
-// A part of a cut head: where it is and whose.
-struct Piece {
-    const float *rows, *rows2;   // [rows][STRIDE], in shared or global memory; what a second warp adds, or null
-    int u0;                      // the head's first tile in the sequence of all tiles
-    int b, kvh;
-};
+// Where team n leaves its rows of the cut head whose first tile is u0: the first
+// head of its share, or the last.
+template <int D>
+__device__ __forceinline__ float* part_of(const Cache8Args& a, const Deal& deal, int n, int u0) {
+    return a.part + (long long)(2 * n + (u0 <= deal.from(n) ? 0 : 1)) * a.rows * (D + 4);
+}
 
-// Sources of one head, up to the next group's first; where the merged rows go
-// (null: they are the output), n tokens of the step.
-struct Group {
-    float* dest;
-    int first, b, kvh, n;
-};
-static_assert(kMaxGroups > 2 * kSlots, "each part a head of its own");
-
-// An end of a CTA's share that cuts a head: the head, the CTAs that have parts
-// of it, how far its merge is (0 nothing to do, 1 among neighbours, 2 of all), and
-// what to merge next.
-struct End {
-    int u0, unit, b, kvh, n, c0, parts, level;
-    int first, step, take;
-    bool final;
+// The sequence of all tiles, and how the CTAs and their teams share it; by all
+// threads of a block (the first `threads`).
+template <int THREADS>
+struct Layout {
+    int per, mine, before;   // the thread's sequences, from per * tid on: their tiles (of all heads), and those before
+    int N, longest;          // all tiles; most of a head
+    int ctas;                // that have any
+    bool by_head;
+    int* s_scan;             // [2][THREADS / 32]
+    __device__ __forceinline__ Layout(const Cache8Args& a, int* s, int tid) : s_scan(s) {
+        const int warp = tid / 32, lane = tid % 32;
+        per = (a.B + THREADS - 1) / THREADS;
+        mine = longest = 0;
+        for (int b = tid * per; b < min(a.B, (tid + 1) * per); ++b) {
+            const int n = SeqTiles(a, b).tiles;
+            mine += n;
+            longest = max(longest, n);
+        }
+        mine *= a.Hkv;
+        int scan = mine;
+#pragma unroll
+        for (int sh = 1; sh < 32; sh <<= 1) {
+            const int up = __shfl_up_sync(0xffffffffu, scan, sh);
+            if (lane >= sh) scan += up;
+        }
+        longest = __reduce_max_sync(0xffffffffu, longest);
+        if (lane == 31) s_scan[warp] = scan;
+        if (lane == 0) s_scan[THREADS / 32 + warp] = longest;
+        __syncthreads();
+        N = 0;   // (fits: the host checks the cache's number of tiles)
+        before = scan - mine;
+#pragma unroll
+        for (int w = 0; w < THREADS / 32; ++w) {
+            if (w < warp) before += s_scan[w];
+            N += s_scan[w];
+            longest = max(longest, s_scan[THREADS / 32 + w]);
+        }
+        ctas = max(1, min(a.ctas, N >> a.lg_teams));   // every team has a tile (or there is one CTA)
+        // Short sequences, a CTA for each head: no head is cut between CTAs, whose
+        // merge would take longer than the tiles.
+        by_head = longest <= kWholeTiles && a.B * (long long)a.Hkv <= a.ctas;
+    }
 };
 
 template <int D, bool E4M3, int NT>
@@ -520,12 +550,8 @@ cache8_attn_kernel(const __grid_constant__ Cache8Args a) {
     constexpr int kThreads = C::THREADS, kConsumers = C::CONSUMERS, MT = C::MT, STRIDE = C::STRIDE;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ uint64_t s_full[kBars], s_empty[kBars];
-    __shared__ int s_scan[kThreads / 32], s_longest[kThreads / 32];
-    __shared__ Piece s_piece[2 * kSlots];   // in the order of the tiles; rows null: none
-    __shared__ End s_end[2];
-    __shared__ int s_groups;
+    __shared__ int s_scan[2 * kThreads / 32];
     __shared__ int s_b[kSlots], s_rem[kSlots];
-    __shared__ int s_last[kSlots];
     __shared__ int s_abort;
     volatile int* abort_flag = &s_abort;
 
@@ -539,69 +565,31 @@ cache8_attn_kernel(const __grid_constant__ Cache8Args a) {
         mbar_init(&s_empty[tid], team_warps);
     }
     mbar_fence_init();
-    if (tid < 2 * kSlots) s_piece[tid].rows = s_piece[tid].rows2 = nullptr;
     if (tid == 0) s_abort = 0;
     if (a.wait_first) pdl_wait();
     pdl_trigger();   // the next kernel may be set up; it waits for this grid before it touches memory
 
     // ---- the CTA's share of all tiles, [lo, hi) of N, and the teams' shares of that
-    const int per = (a.B + kThreads - 1) / kThreads;
-    int mine = 0, longest = 0;
-    for (int b = tid * per; b < min(a.B, (tid + 1) * per); ++b) {
-        const int n = SeqTiles(a, b).tiles;
-        mine += n;
-        longest = max(longest, n);
-    }
-    mine *= a.Hkv;
-    int scan = mine;
-#pragma unroll
-    for (int sh = 1; sh < 32; sh <<= 1) {
-        const int up = __shfl_up_sync(0xffffffffu, scan, sh);
-        if (lane >= sh) scan += up;
-    }
-    longest = __reduce_max_sync(0xffffffffu, longest);
-    if (lane == 31) s_scan[warp] = scan;
-    if (lane == 0) s_longest[warp] = longest;
-    __syncthreads();
-    int N = 0, before = scan - mine;   // (fits: the host checks the cache's number of tiles)
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
-        if (w < warp) before += s_scan[w];
-        N += s_scan[w];
-        longest = max(longest, s_longest[w]);
-    }
-    const int me = blockIdx.x;
-    const int ctas = max(1, min((int)gridDim.x, N >> a.lg_teams));   // every team has a tile (or there is one CTA)
+    const Layout<kThreads> all(a, s_scan, tid);
+    const int me = blockIdx.x, N = all.N, ctas = all.ctas;
+    const bool by_head = all.by_head;
     const Deal deal(N, ctas * teams);
-    int lo = me < ctas ? deal.from(me * teams) : N, hi = me < ctas ? deal.from((me + 1) * teams) : N;
-    // Short sequences, a CTA for each head: no head is cut between CTAs, whose
-    // merge would take longer than the tiles (the CTA's own head is then all there is).
-    const bool by_head = longest <= kWholeTiles && a.B * (long long)a.Hkv <= gridDim.x;
-    if (by_head) {
-        lo = 0;
-        hi = me < a.B * a.Hkv ? SeqTiles(a, me / a.Hkv).tiles : 0;
-    }
-    // Where a head is cut into few parts the teams merge it themselves, the last to
-    // arrive (a team's threads need up to kTeamRounds rounds of loads for it); else
-    // each CTA first merges what its teams have.
-    const int most_parts = deal.each > 0 ? longest / deal.each + 2 : 1 << 20;
-    const bool by_team = !by_head && (most_parts + kBatch - 1) / kBatch *
-                                             ((a.rows * (D / 4) + 32 * team_warps - 1) / (32 * team_warps)) <= kTeamRounds;
+    const int whole_head = by_head && me < a.B * a.Hkv ? SeqTiles(a, me / a.Hkv).tiles : 0;   // the CTA's own head
     const auto team_lo = [&](int k) {
-        return by_head ? Deal(hi, teams).from(k) : (me < ctas ? deal.from(me * teams + k) : N);
+        return by_head ? Deal(whole_head, teams).from(k) : (me < ctas ? deal.from(me * teams + k) : N);
     };
     if (by_head) {
         if (tid < teams) {
             s_b[tid] = me / a.Hkv;
-            s_rem[tid] = me % a.Hkv * hi + team_lo(tid);
+            s_rem[tid] = me % a.Hkv * whole_head + team_lo(tid);
         }
-    } else if (mine > 0) {
+    } else if (all.mine > 0) {
         for (int k = 0; k < teams; ++k) {
             const int from = team_lo(k);
-            if (from < before || from >= before + mine || from == team_lo(k + 1)) continue;
-            int at = from - before;
-            int b = tid * per;
-            if (per > 1) {
+            if (from < all.before || from >= all.before + all.mine || from == team_lo(k + 1)) continue;
+            int at = from - all.before;
+            int b = tid * all.per;
+            if (all.per > 1) {
                 int in_seq = SeqTiles(a, b).tiles * a.Hkv;
                 while (at >= in_seq && b + 1 < a.B) {
                     at -= in_seq;
@@ -736,9 +724,6 @@ cache8_attn_kernel(const __grid_constant__ Cache8Args a) {
                 stage = 0;
                 phase ^= 1u;
             }
-        };
-        const auto team_part = [&](int n, int u0) {   // team n's part of the head at u0: its first head's or its last's
-            return a.piece + (long long)(2 * n + (u0 <= deal.from(n) ? 0 : 1)) * a.rows * STRIDE;
         };
         RowState<D, NT> st;
         // (the lane's tokens of a tile's first 16: see soften)
@@ -977,7 +962,7 @@ cache8_attn_kernel(const __grid_constant__ Cache8Args a) {
                 break;
             }
 
-            // ---- the segment's rows into the team's slot, merged where two warps shared the tokens
+            // ---- the segment's rows, merged where two warps shared the tokens
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -1002,16 +987,19 @@ cache8_attn_kernel(const __grid_constant__ Cache8Args a) {
                             *reinterpret_cast<float4*>(to + D) = make_float4(st.m[n][e], st.l[n][e], st.M[n][e], 0.f);
                     }
             };
+            // A head of the team's alone is finished; else its part is left in global
+            // memory for the merge kernel, or, of the CTA's own head, in shared memory:
+            // the first warp's rows in the slot, the second's in the ring, which is empty.
             const bool whole = at.j == 0 && j1 == at.tiles, final = j1 - at.j == at.left;
-            // (the share's last part: the ring is empty and holds the second warp's rows)
-            float* spare = reinterpret_cast<float*>(smem + (size_t)team * a.stages * STAGE);
-            const bool apart = C::KS == 2 && final && !whole && !by_team;
+            const bool apart = C::KS == 2 && by_head && !whole;
+            float* to = whole || by_head
+                            ? slot : part_of<D>(a, deal, me * teams + team, here - at.j);
             if (C::KS == 2 && !apart && kh == 1) put(slot);
-            if (C::KS == 1 || (apart && kh == 0)) put(slot);
+            if (C::KS == 1 || (apart && kh == 0)) put(to);
             ok = named_bar_and(1 + team, team_threads, ok && !*abort_flag);
             if (!ok) break;
             if (apart) {
-                if (kh == 1) put(spare);
+                if (kh == 1) put(reinterpret_cast<float*>(smem + (size_t)team * a.stages * STAGE));
             } else if constexpr (C::KS == 2) {
                 if (kh == 0) {
 #pragma unroll
@@ -1034,11 +1022,10 @@ cache8_attn_kernel(const __grid_constant__ Cache8Args a) {
                             }
                         }
                     __syncwarp();
-                    put(slot);
+                    put(to);
                 }
-                named_bar_sync(1 + team, team_threads);
+                if (whole || !final) named_bar_sync(1 + team, team_threads);   // (the slot may be written again)
             }
-            const float* kept = slot;   // the last head's rows stay here
             if (whole) {
                 if (a.gate_mode != GSDPA_GATE_NONE) pdl_wait();   // the gate logits
                 for (int idx = team_tid; idx < a.rows * (D / 4); idx += team_threads) {
@@ -1048,191 +1035,31 @@ cache8_attn_kernel(const __grid_constant__ Cache8Args a) {
                     finish<D>(a, at.b, at.kvh, q.n, row, col, out_scale(x.x, x.y, x.z),
                               *reinterpret_cast<const float4*>(from + col));
                 }
-            } else if (by_team) {
-                const int u0 = here - at.j, n = me * teams + team;
-                float4* to = reinterpret_cast<float4*>(team_part(n, u0));
-                for (int idx = team_tid; idx < a.rows * (STRIDE / 4); idx += team_threads)
-                    to[idx] = reinterpret_cast<const float4*>(slot)[idx];
-                named_bar_sync(1 + team, team_threads);
-                const int n0 = deal.taker(u0), n1 = deal.taker(u0 + at.tiles - 1);
-                if (team_tid == 0) {
-                    __threadfence();   // (after the barrier: covers what every thread of the team has written)
-                    s_last[team] = atomicAdd(a.counters + unit, 1) == n1 - n0;
-                    __threadfence();
-                }
-                named_bar_sync(1 + team, team_threads);
-                if (s_last[team]) {
-                    if (a.gate_mode != GSDPA_GATE_NONE) pdl_wait();
-                    for (int idx = team_tid; idx < a.rows * (D / 4); idx += team_threads) {
-                        const int row = idx / (D / 4), col = 4 * (idx % (D / 4));
-                        Sums r;
-                        r.add(n0, n1 + 1, 1, D, col, [&](int k) { return team_part(k, u0) + row * STRIDE; });
-                        finish<D>(a, at.b, at.kvh, q.n, row, col, out_scale(r.m, r.l, r.M), r.o);
-                    }
-                }
-            } else if (!final) {
-                float4* to = reinterpret_cast<float4*>(team_part(me * teams + team, here));
-                for (int idx = team_tid; idx < a.rows * (STRIDE / 4); idx += team_threads)
-                    to[idx] = reinterpret_cast<const float4*>(slot)[idx];
-                kept = reinterpret_cast<const float*>(to);
+                if (!final) named_bar_sync(1 + team, team_threads);
             }
-            if (!whole && !by_team && team_tid == 0) {
-                Piece& p = s_piece[2 * team + (final ? 1 : 0)];
-                p.rows = kept;
-                p.rows2 = apart ? spare : nullptr;
-                p.u0 = here - at.j;
-                p.b = at.b;
-                p.kvh = at.kvh;
-            }
-            if (!final) named_bar_sync(1 + team, team_threads);   // the slot may be written again
             here += j1 - at.j;
             at.skip(a, j1 - at.j);
         }
     }
 
-    // ---- the heads that the teams' shares cut
-    const auto sync_all = [&]() { named_bar_sync(kSlots + 1, kConsumers); };
-    if (!named_bar_and(kSlots + 1, kConsumers, ok && !*abort_flag)) {
-        pdl_wait();
-        return;
-    }
-    // One code merges at every level: the CTA's parts first; then, where this CTA
-    // is the last to arrive, the parts of a head that its ends cut, of up to
-    // kFanOne CTAs at once, else of kFan neighbouring CTAs and then of those groups
-    // (one CTA reading all parts of a head cut over half the GPU took 15 us).
-    // Sources (pointers to rows) of one head are a group of the merge; all of it in
-    // the ring, behind the second warp's rows of the first team.
-    pdl_wait();   // the gate logits; and the next kernel on the stream may rely on the gate kernel having ended
-    const int items = a.rows * (D / 4);
-    const auto part_index = [&](int c, int u0) { return 2 * c + (u0 <= deal.from(c << a.lg_teams) ? 0 : 1); };
-    const auto part_of = [&](int c, int u0) {   // CTA c's part of the head at u0
-        return a.part + (long long)part_index(c, u0) * a.rows * STRIDE;
-    };
-    const float** source = reinterpret_cast<const float**>(smem + (C::KS == 2 ? a.rows * STRIDE * 4 : 0));
-    Group* s_group = reinterpret_cast<Group*>(source + kMaxSources);  // [groups + 1]
-    if (warp == 0) {
-        // a lane stands for a source (lane % 16: the part, upper half: its second warp's rows)
-        const int piece = lane % (2 * kSlots);
-        const bool upper = lane >= 2 * kSlots;
-        const float* at = upper ? s_piece[piece].rows2 : s_piece[piece].rows;
-        const uint32_t there = __ballot_sync(0xffffffffu, at != nullptr);
-        const uint32_t lower = there & 0xffffu, under = (1u << piece) - 1;
-        const int u0 = s_piece[piece].u0, before_me = (lower & under) ? 31 - __clz(lower & under) : piece;
-        const int u0_before = __shfl_sync(0xffffffffu, u0, before_me);
-        const bool head = !upper && at && (!(lower & under) || u0_before != u0);
-        const uint32_t heads = __ballot_sync(0xffffffffu, head);
-        const int place = __popc(lower & under) + __popc((there >> 16) & under) + (upper ? (int)((lower >> piece) & 1u) : 0);
-        if (at) source[place] = at;
-        if (head) {
-            Group& gr = s_group[__popc(heads & under)];
-            const SeqTiles q(a, s_piece[piece].b);
-            gr.first = place;
-            gr.b = s_piece[piece].b;
-            gr.kvh = s_piece[piece].kvh;
-            gr.n = q.n;
-            gr.dest = u0 >= lo && u0 + q.tiles <= hi ? nullptr : part_of(me, u0);
-            // an end of the CTA's share that cuts a head: its first group or its last
-            const bool first = !(heads & under), last = !(heads >> (piece + 1));
-            if (gr.dest) {
-                End& e = s_end[first ? 0 : 1];
-                e.c0 = deal.taker(u0) >> a.lg_teams;
-                e.parts = (deal.taker(u0 + q.tiles - 1) >> a.lg_teams) - e.c0 + 1;
-                e.u0 = u0;
-                e.unit = gr.b * a.Hkv + gr.kvh;
-                e.b = gr.b;
-                e.kvh = gr.kvh;
-                e.n = gr.n;
-                e.level = e.parts > kFanOne ? 1 : 2;
-            }
-            if (first && !gr.dest) s_end[0].level = 0;
-            if (last && (first || !gr.dest)) s_end[1].level = 0;
-        }
-        if (lane == 0) {
-            s_groups = __popc(heads);
-            s_group[__popc(heads)].first = __popc(there);
-            if (!heads) s_end[0].level = s_end[1].level = 0;
-        }
-    }
-    for (;;) {
-        sync_all();
-        const int groups = s_groups;
-        // A thread has four columns of a row; its sources are split over lanes that
-        // would be idle, which merge theirs at the end.
+    pdl_wait();   // the gate logits; and what follows on the stream may rely on the gate kernel having ended
+    const int parts = min(whole_head, teams);   // (of the CTA's own head: more than one, or it is done)
+    if (by_head && named_bar_and(kSlots + 1, kConsumers, ok && !*abort_flag) && parts > 1) {
+        const int items = a.rows * (D / 4), b = me / a.Hkv, n = SeqTiles(a, b).n;
+        // A thread has four columns of a row; its parts are split over lanes that
+        // would be idle (whole warps: items come in sixteens).
         int lg = 0;
-        while (lg < 3 && ((groups * items) << (lg + 1)) <= kConsumers) ++lg;
-        for (int idx = tid; idx < (groups * items) << lg; idx += kConsumers) {
-            const int sub = idx & ((1 << lg) - 1);
-            int item = idx >> lg, gr = 0;
-            while (item >= items) {
-                item -= items;
-                ++gr;
-            }
-            const int row = item / (D / 4), col = 4 * (item % (D / 4)), i1 = s_group[gr + 1].first;
+        while (lg < 3 && (items << (lg + 1)) <= kConsumers) ++lg;
+        for (int idx = tid; idx < items << lg; idx += kConsumers) {
+            const int item = idx >> lg, row = item / (D / 4), col = 4 * (item % (D / 4));
             Sums r;
-            r.add(s_group[gr].first + sub, i1, 1 << lg, D, col, [&](int i) { return source[i] + row * STRIDE; });
-            float &m = r.m, &l = r.l, &M = r.M;
-            float4& o = r.o;
-            for (int sh = 1; sh < 1 << lg; sh <<= 1) {   // (whole warps: items come in sixteens)
-                const float m2 = __shfl_xor_sync(0xffffffffu, m, sh), M2 = __shfl_xor_sync(0xffffffffu, M, sh);
-                const float mn = fmaxf(m, m2), Mn = fmaxf(M, M2);
-                const float wa = part_weight(M, Mn), wb = part_weight(M2, Mn);
-                l = l * part_weight(m, mn) + __shfl_xor_sync(0xffffffffu, l, sh) * part_weight(m2, mn);
-                o.x = o.x * wa + __shfl_xor_sync(0xffffffffu, o.x, sh) * wb;
-                o.y = o.y * wa + __shfl_xor_sync(0xffffffffu, o.y, sh) * wb;
-                o.z = o.z * wa + __shfl_xor_sync(0xffffffffu, o.z, sh) * wb;
-                o.w = o.w * wa + __shfl_xor_sync(0xffffffffu, o.w, sh) * wb;
-                m = mn;
-                M = Mn;
-            }
-            if (sub != 0) continue;
-            const Group& gp = s_group[gr];
-            if (!gp.dest) {
-                finish<D>(a, gp.b, gp.kvh, gp.n, row, col, out_scale(m, l, M), o);
-            } else {
-                float* to = gp.dest + row * STRIDE;
-                *reinterpret_cast<float4*>(to + col) = o;
-                if (col == 0) *reinterpret_cast<float4*>(to + D) = make_float4(m, l, M, 0.f);
-            }
-        }
-        sync_all();
-        if (tid < 2) {   // the arrival of each end's head, and what is to be merged next
-            End& e = s_end[tid];
-            int take = 0;
-            if (e.level != 0) {
-                const bool all = e.level == 2;
-                e.step = all && e.parts > kFanOne ? kFan : 1;
-                e.first = all ? e.c0 : me - (me - e.c0) % kFan;
-                const int n = all ? (e.parts + e.step - 1) / e.step : min(kFan, e.parts - (e.first - e.c0));
-                int* counter = a.counters + (all ? e.unit : a.B * a.Hkv + part_index(e.first, e.u0));
-                __threadfence();   // (after the barrier: covers what every thread has written)
-                if (atomicAdd(counter, 1) == n - 1) {
-                    take = n;
-                    __threadfence();
-                }
-                e.level = take == 0 || all ? 0 : 2;
-                e.final = all;
-            }
-            e.take = take;
-        }
-        sync_all();
-        const int n0 = s_end[0].take, n1 = s_end[1].take;
-        if (n0 + n1 == 0) break;
-        if (tid < n0 + n1) {
-            const End& e = s_end[tid < n0 ? 0 : 1];
-            source[tid] = part_of(e.first + (tid < n0 ? tid : tid - n0) * e.step, e.u0);
-        }
-        if (tid < 2 && s_end[tid].take > 0) {
-            const End& e = s_end[tid];
-            Group& gr = s_group[tid == 1 && n0 > 0 ? 1 : 0];
-            gr.first = tid == 0 ? 0 : n0;
-            gr.b = e.b;
-            gr.kvh = e.kvh;
-            gr.n = e.n;
-            gr.dest = e.final ? nullptr : part_of(e.first, e.u0);
-        }
-        if (tid == 0) {
-            s_groups = (n0 > 0) + (n1 > 0);
-            s_group[s_groups].first = n0 + n1;
+            r.add(idx & ((1 << lg) - 1), parts * C::KS, 1 << lg, D, col, [&](int i) {
+                return (i < parts ? slots + (size_t)i * a.rows * STRIDE
+                                  : reinterpret_cast<const float*>(smem + (size_t)(i - parts) * a.stages * STAGE)) +
+                       row * STRIDE;
+            });
+            for (int sh = 1; sh < 1 << lg; sh <<= 1) r.join_lane(sh);
+            if ((idx & ((1 << lg) - 1)) == 0) finish<D>(a, b, me % a.Hkv, n, row, col, out_scale(r.m, r.l, r.M), r.o);
         }
     }
 
@@ -1244,6 +1071,79 @@ cache8_attn_kernel(const __grid_constant__ Cache8Args a) {
         for (long long i = from + tid; i < to; i += kConsumers)
             reinterpret_cast<uint4*>(a.O)[i] = make_uint4(0, 0, 0, 0);
     }
+}
+
+// The heads that were cut between teams, from the teams' parts. Four lanes have
+// 16 columns of a row; a head's parts are split over as many such groups as give
+// every thread of the grid work, down to four parts each (one sequence of 131072
+// tokens leaves 608 parts of each head), and joined by shuffles and through
+// shared memory. Its own kernel, because the end of the attention kernel is the
+// one point at which all parts are known to be there without atomics: a launch
+// that was set up early costs less than a chain of counters.
+template <int D>
+__global__ void __launch_bounds__(kMergeThreads) cache8_merge_kernel(const __grid_constant__ Cache8Args a) {
+    constexpr int kWarps = kMergeThreads / 32;
+    __shared__ int s_scan[2 * kWarps];
+    __shared__ int s_before[kMergeThreads];
+    __shared__ float4 s_o[kWarps][4], s_x[kWarps][4];
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    pdl_trigger();
+    // (the attention kernel started after everything before this call had ended: the lengths may be read)
+    const Layout<kMergeThreads> all(a, s_scan, tid);
+    s_before[tid] = all.before;
+    __syncthreads();
+    const Deal deal(all.N, all.ctas << a.lg_teams);
+    const int items = a.rows * (D / 4);
+    const long long heads = all.by_head ? 0 : (long long)a.B * a.Hkv, threads = (long long)gridDim.x * kMergeThreads;
+    const int most = deal.each > 0 ? all.longest / deal.each + 2 : 1;   // parts of a head
+    int lg = 0;
+    while ((8 << lg) <= kMergeThreads && ((heads * items) << (lg + 1)) <= threads && (4 << lg) < most) ++lg;
+    const long long total = (heads * items) << lg;
+    bool waited = false;
+    for (long long base = (long long)blockIdx.x * kMergeThreads; base < total; base += threads) {
+        const long long idx = base + tid;
+        const int per_head = items << lg;
+        const bool in = idx < total;
+        const long long unit = in ? idx / per_head : 0;
+        const int x = (int)(idx - unit * per_head), item = (x >> (lg + 2) << 2) + (x & 3), sub = (x >> 2) & ((1 << lg) - 1);
+        const int row = item / (D / 4), col = 4 * (item % (D / 4));
+        const int b = (int)(unit / a.Hkv), kvh = (int)(unit % a.Hkv);
+        int at = s_before[b / all.per];
+        for (int k = b / all.per * all.per; k < b; ++k) at += SeqTiles(a, k).tiles * a.Hkv;
+        const SeqTiles q(a, b);
+        const int u0 = at + kvh * q.tiles;
+        int n0 = 0, n1 = 0;
+        if (in && q.tiles > 0) {
+            n0 = deal.taker(u0);
+            n1 = deal.taker(u0 + q.tiles - 1);
+        }
+        if (!waited) pdl_wait();
+        waited = true;
+        const bool cut = n1 > n0;
+        Sums r;
+        if (cut)
+            r.add(n0 + sub, n1 + 1, 1 << lg, D, col, [&](int k) { return part_of<D>(a, deal, k, u0) + row * (D + 4); });
+        for (int k = 0; k < min(lg, 3); ++k) r.join_lane(4 << k);
+        if (lg > 3) {   // warps that share items
+            const int share = 1 << (lg - 3);
+            if (lane < 4) {
+                s_o[warp][lane] = r.o;
+                s_x[warp][lane] = make_float4(r.m, r.l, r.M, 0.f);
+            }
+            __syncthreads();
+            if (warp % share == 0) {
+                r = Sums();
+                for (int k = lane >> 2; k < share; k += 8) {
+                    const float4 y = s_x[warp + k][lane & 3];
+                    r.join(y.x, y.y, y.z, s_o[warp + k][lane & 3]);
+                }
+                for (int k = 0; k < 3; ++k) r.join_lane(4 << k);
+            }
+            __syncthreads();
+        }
+        if (cut && sub == 0) finish<D>(a, b, kvh, q.n, row, col, out_scale(r.m, r.l, r.M), r.o);
+    }
+    if (!waited) pdl_wait();   // the next kernel on the stream relies on the attention kernel having ended
 }
 
 // Shared memory and ring of one problem.
@@ -1270,8 +1170,7 @@ Shape shape_of(int rows, int D) {
 struct Cache8Plan {
     Problem p{};
     WorkspacePlan w;   // the gate kernel's part
-    size_t piece = 0, part = 0, counters = 0, total = 0;
-    int n_counters = 0;
+    size_t part = 0, total = 0;
 };
 
 int plan_cache8(const gsdpa_cache8* c, int Lq, int d_model, int Hq, int gate_mode, Cache8Plan* out) {
@@ -1310,10 +1209,7 @@ int plan_cache8(const gsdpa_cache8* c, int Lq, int d_model, int Hq, int gate_mod
     if (gate_mode != GSDPA_GATE_NONE) plan_gate_rows(p, plan_sms(), &o.w);
     o.w.gate_part = take(sizeof(float) * (size_t)o.w.gate_splits * o.w.gate_rows * o.w.gate_cols);
     const size_t part = sizeof(float) * (size_t)rows * (c->d_k + 4);
-    o.piece = take(part * plan_sms() * 2 * (kSlots / shape_of((int)rows, c->d_k).R));
-    o.part = take(part * plan_sms() * 2);
-    o.n_counters = c->B * c->H_kv + 2 * kMaxCtas;   // heads; neighbouring CTAs' parts
-    o.counters = take(sizeof(int) * (size_t)o.n_counters);
+    o.part = take(part * plan_sms() * 2 * (kSlots / shape_of((int)rows, c->d_k).R));
     o.total = off;
     return GSDPA_OK;
 }
@@ -1373,22 +1269,12 @@ int gated_sdpa_cache8(const void* X, const void* Q, const gsdpa_cache8* cache, c
     pl.p.X = X;
     pl.p.Wg = W_g;
 
-    // The arrival counters are zeroed by the kernel that runs first. The gate
-    // logits' kernel does it after waiting for the kernels before it, and then lets
-    // the attention, its programmatic dependent, start: that finds the cache and
-    // the queries written and waits for the logits where it reads them. Without a
-    // gate zero_counters_kernel does it, and the attention waits for its end.
-    ZeroJob zero;
-    zero.p = reinterpret_cast<int*>(ws + pl.counters);
-    zero.n = pl.n_counters;
-    // (Where every head is one CTA's, however long the sequences are, there are none to zero.)
+    // The gate logits' kernel first: it waits for the kernels before it and then lets
+    // the attention, its programmatic dependent, start: that finds the cache and the
+    // queries written and waits for the logits where it reads them.
     const int sms = rt.num_sms < kMaxCtas ? rt.num_sms : kMaxCtas;
-    const bool whole = cache->capacity / kCacheBlock <= kWholeTiles && (long long)cache->B * cache->H_kv <= sms;
-    if (whole) zero.n = 0;
     bool launched = false;
-    cudaError_t e = launch_gate_logits_bf16(pl.p, pl.w, ws, rt, s, &launched, zero);
-    if (e == cudaSuccess && !launched && !whole)
-        e = launch_dependent(zero_counters_kernel, dim3((zero.n + 255) / 256), dim3(256), 0, s, zero.p, zero.n);
+    cudaError_t e = launch_gate_logits_bf16(pl.p, pl.w, ws, rt, s, &launched, ZeroJob());
     if (e == cudaErrorInvalidValue) return GSDPA_ERR_INVALID_ARG;
     if (e != cudaSuccess) return GSDPA_ERR_LAUNCH;
 
@@ -1420,9 +1306,7 @@ int gated_sdpa_cache8(const void* X, const void* Q, const gsdpa_cache8* cache, c
     a.gate_splits = pl.w.gate_splits;
     a.gate_cols = pl.w.gate_cols;
     a.gate_mode = gate_mode;
-    a.piece = reinterpret_cast<float*>(ws + pl.piece);
     a.part = reinterpret_cast<float*>(ws + pl.part);
-    a.counters = zero.p;
     a.wait_first = launched ? 0 : 1;
     a.ctl.err = rt.err;
     a.ctl.limit_ns = rt.limit_ns;
@@ -1430,11 +1314,16 @@ int gated_sdpa_cache8(const void* X, const void* Q, const gsdpa_cache8* cache, c
     const long long most = (long long)a.B * a.Hkv * ((a.blocks + kSlots / a.R - 1) / (kSlots / a.R));
     long long grid = sms;   // (no fewer than the heads, where those fit)
     if (grid > most) grid = most;
+    a.ctas = (int)grid;
     const bool e4m3 = cache->kind == GSDPA_CACHE_E4M3;
     if (cache->d_k == 128)
         e = e4m3 ? launch<128, true>(a, sh, (unsigned)grid, s) : launch<128, false>(a, sh, (unsigned)grid, s);
     else
         e = e4m3 ? launch<64, true>(a, sh, (unsigned)grid, s) : launch<64, false>(a, sh, (unsigned)grid, s);
+    // (where every head is one CTA's, however long the sequences are, there is nothing to merge)
+    if (e == cudaSuccess && !(a.blocks <= kWholeTiles && (long long)a.B * a.Hkv <= grid))
+        e = launch_dependent(cache->d_k == 128 ? cache8_merge_kernel<128> : cache8_merge_kernel<64>, dim3((unsigned)sms),
+                             dim3(kMergeThreads), 0, s, a);
     return e == cudaSuccess ? GSDPA_OK : GSDPA_ERR_LAUNCH;
 }
 

@@ -42,12 +42,14 @@
 // 32 of a tile's tokens each; beyond, teams of one, two, four or eight warps
 // with 16 query rows each. A team streams its tiles through a ring of its own
 // (one warp issues all copies) and needs no other team until its share is done: a
-// K/V head that lies within the share is finished by the team, the two heads
-// that its ends cut are left as parts (outputs, m, l, M) and merged at the end of
-// the CTA, and heads that the CTA's ends cut by the CTA that arrives last (an
-// atomic counter; parts are added in a fixed order). No CTA waits for another.
+// K/V head that lies within the share is finished by the team, of the two heads
+// that its ends cut it leaves parts (outputs, m, l, M) in global memory, and a
+// second kernel merges these in a fixed order. No CTA waits for another.
 // (With the tiles dealt to the teams in turn, and all warps merging at the end of
-// every head, the same 64 sequences took 90 us.)
+// every head, the same 64 sequences took 90 us. Dealing out the last fifth of
+// the tiles in small chunks to the teams that were done first made all SMs end
+// at the same time, with even shares they do between 140 and 170 us for 64
+// sequences of 8192 tokens, but none earlier: the memory is busy to the end.)
 //
 // The order of the tokens inside a tile's products is chosen so that 16
 // consecutive bytes of a value column are one lane's share of the second
@@ -69,6 +71,8 @@ constexpr int kBatch = 8;            // parts that a thread of a merge has under
 constexpr int kWholeTiles = 24;      // most tiles of a head for one CTA to take it alone (see below)
 constexpr int kBars = 48;            // ring stages of all teams
 constexpr uint32_t kSmemMax = 232448 - 1984;   // dynamic: what a CTA may have, less barriers, parts and a few words
+constexpr int kSwitch = 4;           // most places after a head without a tile
+constexpr int kScan = 128;           // places in the sequence of all tiles that are looked up
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kMove = 8.0f;
 
@@ -160,6 +164,16 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 // 1 / (1 + e^-x), accurate to a few units of float32's last place.
 __device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
 
+// Places of a head in the sequence of all tiles: after its tiles come some without
+// one. A team that goes on to another head stores what it has, reads other
+// queries and has, at a sequence's end, an open block of twice the bytes, which
+// even shares of the tiles alone do not show: of 1216 teams with 11 tiles each of
+// 24 sequences of up to 32767 tokens, the 48 that went on ended 5 us after the
+// others. (Measured with 2, 4, 6 and 8 places: that 52.2, 50.4, 50.9, 51.5 us, up
+// to 5000 tokens 19.3, 17.7, 17.5, 17.9; 64 x 200 tokens, heads of 4 tiles, 18.4,
+// 21.0, 20.3, 20.1.)
+__device__ __forceinline__ int span_of(int tiles) { return tiles + min(kSwitch, tiles / 2); }
+
 struct SeqTiles {
     int len, n, T, tiles;
     __device__ __forceinline__ SeqTiles(const Cache8Args& a, int b) {
@@ -170,32 +184,29 @@ struct SeqTiles {
         tiles = (T + kCacheBlock - 1) / kCacheBlock;
     }
     __device__ __forceinline__ bool open(int j) const { return (j + 1) * kCacheBlock > T; }
+    __device__ __forceinline__ int span() const { return span_of(tiles); }
 };
 
-// A place in the sequence of all tiles. (Where tiles are left a sequence with
+// A place in the sequence of all tiles. (Where places are left a sequence with
 // tiles follows; lengths that change during the call, which they must not, end
 // the walk instead of leading it out of the batch.)
 struct Cursor {
     int b, kvh, j, tiles;
-    int left;   // tiles of the share from here on
-    __device__ __forceinline__ void skip(const Cache8Args& a, int n) {
-        left -= n;
+    int left;   // places of the share from here on
+    __device__ __forceinline__ void next_head(const Cache8Args& a) {
+        left -= span_of(tiles) - j;
+        j = 0;
         if (left <= 0) return;
-        int at = j + n;
-        while (at >= tiles) {
-            at -= tiles;
-            if (++kvh == a.Hkv) {
-                kvh = 0;
-                do {
-                    if (++b >= a.B) {
-                        left = 0;
-                        return;
-                    }
-                    tiles = SeqTiles(a, b).tiles;
-                } while (tiles == 0);
-            }
+        if (++kvh == a.Hkv) {
+            kvh = 0;
+            do {
+                if (++b >= a.B) {
+                    left = 0;
+                    return;
+                }
+                tiles = SeqTiles(a, b).tiles;
+            } while (tiles == 0);
         }
-        j = at;
     }
 };
 
@@ -498,47 +509,76 @@ __device__ __forceinline__ float* part_of(const Cache8Args& a, const Deal& deal,
     return a.part + (long long)(2 * n + (u0 <= deal.from(n) ? 0 : 1)) * a.rows * (D + 4);
 }
 
-// The sequence of all tiles, and how the CTAs and their teams share it; by all
-// threads of a block (the first `threads`).
-template <int THREADS>
+// The sequence of all tiles: sequence after sequence, in each one K/V head after
+// the other. (Its scan in four warps: in all twenty of a block it took 0.6 us more.)
 struct Layout {
-    int per, mine, before;   // the thread's sequences, from per * tid on: their tiles (of all heads), and those before
-    int N, longest;          // all tiles; most of a head
-    int ctas;                // that have any
+    int per;            // sequences to a place
+    int N, longest;     // all places; most tiles of a head
+    int ctas;           // that have any
     bool by_head;
-    int* s_scan;             // [2][THREADS / 32]
-    __device__ __forceinline__ Layout(const Cache8Args& a, int* s, int tid) : s_scan(s) {
+    const int* place;   // [kScan + 1], in shared memory: the places before sequence per * k
+    // by all threads of a block of kScan or more
+    __device__ __forceinline__ Layout(const Cache8Args& a, int* s_place, int* s_scan, int tid) : place(s_place) {
         const int warp = tid / 32, lane = tid % 32;
-        per = (a.B + THREADS - 1) / THREADS;
-        mine = longest = 0;
-        for (int b = tid * per; b < min(a.B, (tid + 1) * per); ++b) {
-            const int n = SeqTiles(a, b).tiles;
-            mine += n;
-            longest = max(longest, n);
-        }
-        mine *= a.Hkv;
-        int scan = mine;
+        constexpr int W = kScan / 32;
+        per = (a.B + kScan - 1) / kScan;
+        int mine = 0, scan = 0;
+        if (warp < W) {
+            longest = 0;
+            for (int b = tid * per; b < min(a.B, (tid + 1) * per); ++b) {
+                const SeqTiles q(a, b);
+                mine += q.span();
+                longest = max(longest, q.tiles);
+            }
+            mine *= a.Hkv;
+            scan = mine;
 #pragma unroll
-        for (int sh = 1; sh < 32; sh <<= 1) {
-            const int up = __shfl_up_sync(0xffffffffu, scan, sh);
-            if (lane >= sh) scan += up;
+            for (int sh = 1; sh < 32; sh <<= 1) {
+                const int up = __shfl_up_sync(0xffffffffu, scan, sh);
+                if (lane >= sh) scan += up;
+            }
+            longest = __reduce_max_sync(0xffffffffu, longest);
+            if (lane == 31) s_scan[warp] = scan;
+            if (lane == 0) s_scan[W + warp] = longest;
         }
-        longest = __reduce_max_sync(0xffffffffu, longest);
-        if (lane == 31) s_scan[warp] = scan;
-        if (lane == 0) s_scan[THREADS / 32 + warp] = longest;
         __syncthreads();
-        N = 0;   // (fits: the host checks the cache's number of tiles)
-        before = scan - mine;
+        N = longest = 0;   // (fits: the host checks the number of places)
+        int before = scan - mine;
 #pragma unroll
-        for (int w = 0; w < THREADS / 32; ++w) {
+        for (int w = 0; w < W; ++w) {
             if (w < warp) before += s_scan[w];
             N += s_scan[w];
-            longest = max(longest, s_scan[THREADS / 32 + w]);
+            longest = max(longest, s_scan[W + w]);
         }
+        if (warp < W) s_place[tid] = before;
+        if (tid == 0) s_place[kScan] = N;
+        __syncthreads();
         ctas = max(1, min(a.ctas, N >> a.lg_teams));   // every team has a tile (or there is one CTA)
         // Short sequences, a CTA for each head: no head is cut between CTAs, whose
         // merge would take longer than the tiles.
         by_head = longest <= kWholeTiles && a.B * (long long)a.Hkv <= a.ctas;
+    }
+    // place x < N is place `rem` of sequence b
+    __device__ __forceinline__ void find(const Cache8Args& a, int x, int& b, int& rem) const {
+        int k = 0;
+#pragma unroll
+        for (int step = kScan / 2; step > 0; step >>= 1)
+            if (place[k + step] <= x) k += step;
+        b = k * per;
+        rem = x - place[k];
+        if (per > 1) {
+            int in_seq = SeqTiles(a, b).span() * a.Hkv;
+            while (rem >= in_seq && b + 1 < a.B) {
+                rem -= in_seq;
+                in_seq = SeqTiles(a, ++b).span() * a.Hkv;
+            }
+        }
+    }
+    // places before sequence b
+    __device__ __forceinline__ int before(const Cache8Args& a, int b) const {
+        int at = place[b / per];
+        for (int k = b / per * per; k < b; ++k) at += SeqTiles(a, k).span() * a.Hkv;
+        return at;
     }
 };
 
@@ -547,11 +587,10 @@ __global__ void __launch_bounds__(Config<D, E4M3, NT>::THREADS, 1)
 cache8_attn_kernel(const __grid_constant__ Cache8Args a) {
     using C = Config<D, E4M3, NT>;
     constexpr uint32_t STAGE = C::STAGE;
-    constexpr int kThreads = C::THREADS, kConsumers = C::CONSUMERS, MT = C::MT, STRIDE = C::STRIDE;
+    constexpr int kConsumers = C::CONSUMERS, MT = C::MT, STRIDE = C::STRIDE;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ uint64_t s_full[kBars], s_empty[kBars];
-    __shared__ int s_scan[2 * kThreads / 32];
-    __shared__ int s_b[kSlots], s_rem[kSlots];
+    __shared__ int s_place[kScan + 1], s_scan[2 * kScan / 32];
     __shared__ int s_abort;
     volatile int* abort_flag = &s_abort;
 
@@ -570,7 +609,7 @@ cache8_attn_kernel(const __grid_constant__ Cache8Args a) {
     pdl_trigger();   // the next kernel may be set up; it waits for this grid before it touches memory
 
     // ---- the CTA's share of all tiles, [lo, hi) of N, and the teams' shares of that
-    const Layout<kThreads> all(a, s_scan, tid);
+    const Layout all(a, s_place, s_scan, tid);
     const int me = blockIdx.x, N = all.N, ctas = all.ctas;
     const bool by_head = all.by_head;
     const Deal deal(N, ctas * teams);
@@ -578,41 +617,29 @@ cache8_attn_kernel(const __grid_constant__ Cache8Args a) {
     const auto team_lo = [&](int k) {
         return by_head ? Deal(whole_head, teams).from(k) : (me < ctas ? deal.from(me * teams + k) : N);
     };
-    if (by_head) {
-        if (tid < teams) {
-            s_b[tid] = me / a.Hkv;
-            s_rem[tid] = me % a.Hkv * whole_head + team_lo(tid);
-        }
-    } else if (all.mine > 0) {
-        for (int k = 0; k < teams; ++k) {
-            const int from = team_lo(k);
-            if (from < all.before || from >= all.before + all.mine || from == team_lo(k + 1)) continue;
-            int at = from - all.before;
-            int b = tid * all.per;
-            if (all.per > 1) {
-                int in_seq = SeqTiles(a, b).tiles * a.Hkv;
-                while (at >= in_seq && b + 1 < a.B) {
-                    at -= in_seq;
-                    in_seq = SeqTiles(a, ++b).tiles * a.Hkv;
-                }
-            }
-            s_b[k] = b;
-            s_rem[k] = at;
-        }
-    }
-    __syncthreads();
     const auto start_of = [&](int k) {
         Cursor c;
-        c.left = team_lo(k + 1) - team_lo(k);
+        const int from = team_lo(k);
+        c.left = team_lo(k + 1) - from;
         c.b = c.kvh = c.j = c.tiles = 0;
         if (c.left > 0) {
-            c.b = s_b[k];
+            if (by_head) {
+                c.b = me / a.Hkv;
+                c.tiles = whole_head;
+                c.kvh = me % a.Hkv;
+                c.j = from;
+                return c;
+            }
+            int rem;
+            all.find(a, from, c.b, rem);
             c.tiles = SeqTiles(a, c.b).tiles;
             if (c.tiles == 0) {
                 c.left = 0;
             } else {
-                c.kvh = s_rem[k] / c.tiles;
-                c.j = s_rem[k] % c.tiles;
+                const int span = span_of(c.tiles);
+                c.kvh = rem / span;
+                c.j = rem % span;
+                if (c.j >= c.tiles) c.next_head(a);
             }
         }
         return c;
@@ -659,7 +686,7 @@ cache8_attn_kernel(const __grid_constant__ Cache8Args a) {
                         ++next.j;
                         --next.left;
                     } else {
-                        next.skip(a, 1);
+                        next.next_head(a);
                         if (next.left > 0) enter();
                     }
                 }
@@ -730,7 +757,7 @@ cache8_attn_kernel(const __grid_constant__ Cache8Args a) {
         const int key0 = 16 * (g >> 1) + 4 * MT * kh + (g & 1) * pair_step<E4M3>();
         const float unscaled = kLog2e * rsqrtf((float)D);
         Cursor at = start_of(team);
-        int here = team_lo(team);   // the cursor's place in the sequence of all tiles
+        const int share_end = team_lo(team + 1);
         while (at.left > 0) {
             const SeqTiles q(a, at.b);
             const long long unit = (long long)at.b * a.Hkv + at.kvh;
@@ -990,10 +1017,10 @@ cache8_attn_kernel(const __grid_constant__ Cache8Args a) {
             // A head of the team's alone is finished; else its part is left in global
             // memory for the merge kernel, or, of the CTA's own head, in shared memory:
             // the first warp's rows in the slot, the second's in the ring, which is empty.
-            const bool whole = at.j == 0 && j1 == at.tiles, final = j1 - at.j == at.left;
+            const bool whole = at.j == 0 && j1 == at.tiles, final = at.left <= span_of(at.tiles) - at.j;
             const bool apart = C::KS == 2 && by_head && !whole;
             float* to = whole || by_head
-                            ? slot : part_of<D>(a, deal, me * teams + team, here - at.j);
+                            ? slot : part_of<D>(a, deal, me * teams + team, share_end - at.left - at.j);
             if (C::KS == 2 && !apart && kh == 1) put(slot);
             if (C::KS == 1 || (apart && kh == 0)) put(to);
             ok = named_bar_and(1 + team, team_threads, ok && !*abort_flag);
@@ -1037,8 +1064,7 @@ cache8_attn_kernel(const __grid_constant__ Cache8Args a) {
                 }
                 if (!final) named_bar_sync(1 + team, team_threads);
             }
-            here += j1 - at.j;
-            at.skip(a, j1 - at.j);
+            at.next_head(a);
         }
     }
 
@@ -1079,19 +1105,19 @@ cache8_attn_kernel(const __grid_constant__ Cache8Args a) {
 // tokens leaves 608 parts of each head), and joined by shuffles and through
 // shared memory. Its own kernel, because the end of the attention kernel is the
 // one point at which all parts are known to be there without atomics: a launch
-// that was set up early costs less than a chain of counters.
+// that was set up early costs less than a chain of counters (one sequence of
+// 131072 tokens: merged in the attention kernel, by the CTAs that arrive last at
+// two levels of counters, 26.7 us in all, so 23.1; two blocks to an SM with half
+// the registers and batches of four: 25.7).
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads) cache8_merge_kernel(const __grid_constant__ Cache8Args a) {
     constexpr int kWarps = kMergeThreads / 32;
-    __shared__ int s_scan[2 * kWarps];
-    __shared__ int s_before[kMergeThreads];
+    __shared__ int s_place[kScan + 1], s_scan[2 * kScan / 32];
     __shared__ float4 s_o[kWarps][4], s_x[kWarps][4];
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     pdl_trigger();
     // (the attention kernel started after everything before this call had ended: the lengths may be read)
-    const Layout<kMergeThreads> all(a, s_scan, tid);
-    s_before[tid] = all.before;
-    __syncthreads();
+    const Layout all(a, s_place, s_scan, tid);
     const Deal deal(all.N, all.ctas << a.lg_teams);
     const int items = a.rows * (D / 4);
     const long long heads = all.by_head ? 0 : (long long)a.B * a.Hkv, threads = (long long)gridDim.x * kMergeThreads;
@@ -1108,10 +1134,8 @@ __global__ void __launch_bounds__(kMergeThreads) cache8_merge_kernel(const __gri
         const int x = (int)(idx - unit * per_head), item = (x >> (lg + 2) << 2) + (x & 3), sub = (x >> 2) & ((1 << lg) - 1);
         const int row = item / (D / 4), col = 4 * (item % (D / 4));
         const int b = (int)(unit / a.Hkv), kvh = (int)(unit % a.Hkv);
-        int at = s_before[b / all.per];
-        for (int k = b / all.per * all.per; k < b; ++k) at += SeqTiles(a, k).tiles * a.Hkv;
         const SeqTiles q(a, b);
-        const int u0 = at + kvh * q.tiles;
+        const int u0 = all.before(a, b) + kvh * q.span();
         int n0 = 0, n1 = 0;
         if (in && q.tiles > 0) {
             n0 = deal.taker(u0);
@@ -1183,8 +1207,8 @@ int plan_cache8(const gsdpa_cache8* c, int Lq, int d_model, int Hq, int gate_mod
     if (gate_mode == GSDPA_GATE_HEADWISE && Hq % 8 != 0) return GSDPA_ERR_UNSUPPORTED;
     const long long rows = (long long)(Hq / c->H_kv) * Lq;
     if (rows > kMaxRows) return GSDPA_ERR_UNSUPPORTED;
-    // (tiles are counted in 32 bits)
-    if ((long long)c->B * c->H_kv * (c->capacity / kCacheBlock) > 0x7fffffffLL) return GSDPA_ERR_UNSUPPORTED;
+    // (places are counted in 32 bits)
+    if ((long long)c->B * c->H_kv * (c->capacity / kCacheBlock + kSwitch) > 0x7fffffffLL) return GSDPA_ERR_UNSUPPORTED;
     if ((long long)c->B * Lq > 0x7fffffffLL / 8 || (long long)c->B * c->H_kv > 0x7fffffffLL - 2 * kMaxCtas)
         return GSDPA_ERR_UNSUPPORTED;
     if (c->B == 0 || Lq == 0) return GSDPA_OK;   // an empty problem: nothing to plan
@@ -1320,9 +1344,11 @@ int gated_sdpa_cache8(const void* X, const void* Q, const gsdpa_cache8* cache, c
         e = e4m3 ? launch<128, true>(a, sh, (unsigned)grid, s) : launch<128, false>(a, sh, (unsigned)grid, s);
     else
         e = e4m3 ? launch<64, true>(a, sh, (unsigned)grid, s) : launch<64, false>(a, sh, (unsigned)grid, s);
+    // (Not a CTA for every SM: the SMs that are done first take them all, and they are
+    // set up when the last are done.)
     // (where every head is one CTA's, however long the sequences are, there is nothing to merge)
     if (e == cudaSuccess && !(a.blocks <= kWholeTiles && (long long)a.B * a.Hkv <= grid))
-        e = launch_dependent(cache->d_k == 128 ? cache8_merge_kernel<128> : cache8_merge_kernel<64>, dim3((unsigned)sms),
+        e = launch_dependent(cache->d_k == 128 ? cache8_merge_kernel<128> : cache8_merge_kernel<64>, dim3((unsigned)(sms - sms / 8)),
                              dim3(kMergeThreads), 0, s, a);
     return e == cudaSuccess ? GSDPA_OK : GSDPA_ERR_LAUNCH;
 }

@@ -550,16 +550,19 @@ class Rope:
 # (The calls below run once per layer and token in a decoding loop, on kernels of
 # a few microseconds: their checks are the ones above, with each property of a
 # tensor read once.)
-def _head_rows(t, name, B, L, H, d, dtype, device):
-    """The row length in elements of t, [B, L, H, d] with contiguous heads and
+def _head_rows(t, name, shape, dtype, device):
+    """The row length in elements of t, shape [B, L, H, d] with contiguous heads and
     evenly spaced token rows (a contiguous tensor, or a column block of one)."""
+    if t is not None and t.shape == shape and t.dtype == dtype and t.device == device and t.is_contiguous():
+        return shape[2] * shape[3]
+    B, L, H, d = shape
     if t is None:
         raise ValueError(f"{name} is required")
-    if t.shape != (B, L, H, d):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, the problem needs {(B, L, H, d)}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, the problem needs {shape}")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
-    if t.device != device or not t.is_cuda:
+    if t.device != device:
         raise ValueError(f"{name} must be a CUDA tensor on {device}, not on {t.device}")
     s0, s1, s2, s3 = t.stride()
     ld = s1 if L > 1 else (s0 if B > 1 else H * d)
@@ -574,7 +577,7 @@ def _vector(t, name, n, dtype, device):
     """The address of an optional contiguous vector of n elements."""
     if t is None:
         return None
-    if t.dtype != dtype or t.numel() != n or t.device != device or not t.is_cuda or not t.is_contiguous():
+    if t.dtype != dtype or t.numel() != n or t.device != device or not t.is_contiguous():
         _expect(t, name, n, dtype, device)   # says which
     return t.data_ptr()
 
@@ -583,7 +586,7 @@ def _current_stream(device):
     """The handle of the current stream, which must be of the tensors' device."""
     import torch
     index = device.index
-    if index != torch.cuda.current_device():
+    if index != torch._C._cuda_getDevice():
         _stream(None, device)                # raises
     return torch._C._cuda_getCurrentRawStream(index)
 
@@ -632,13 +635,24 @@ def _dtype_code(dt):
     return _DTYPES[dt]
 
 
-def _qk_dims(Q, K):
-    if Q.dim() != 4 or K.dim() != 4:
+def _qk_shapes(Q, K):
+    """The shapes of Q [B, L, H_q, d_k] and K [B, L, H_kv, d_k]."""
+    q, k = tuple(Q.shape), tuple(K.shape)
+    if len(q) != 4 or len(k) != 4:
         raise ValueError("Q and K must be 4-D: [B, L, H, d_k]")
-    B, L, H_q, d_k = Q.shape
-    if K.shape[0] != B or K.shape[1] != L or K.shape[3] != d_k:
-        raise ValueError(f"K {tuple(K.shape)} must be [B={B}, L={L}, H_kv, d_k={d_k}]")
-    return B, L, H_q, K.shape[2], d_k
+    if k[0] != q[0] or k[1] != q[1] or k[3] != q[3]:
+        raise ValueError(f"K {k} must be [B={q[0]}, L={q[1]}, H_kv, d_k={q[3]}]")
+    if not Q.is_cuda:
+        raise ValueError(f"Q must be a CUDA tensor, not on {Q.device}")
+    return q, k
+
+
+def _rows_or_new(t, name, shape, dtype, device):
+    """An output, given or new, and its row length."""
+    if t is None:
+        import torch
+        return torch.empty(shape, dtype=dtype, device=device), shape[2] * shape[3]
+    return t, _head_rows(t, name, shape, dtype, device)
 
 
 @_on_stream
@@ -654,26 +668,22 @@ def qk_norm_rope(Q, K, *, gamma_q=None, gamma_k=None, norm=True, eps=1e-6, rope=
     import torch
     dt, dev = Q.dtype, Q.device
     code = _dtype_code(dt)
-    B, L, H_q, H_kv, d_k = _qk_dims(Q, K)
-    ld_q, ld_k = _head_rows(Q, "Q", B, L, H_q, d_k, dt, dev), _head_rows(K, "K", B, L, H_kv, d_k, dt, dev)
-    if out_q is None:
-        out_q, ld_qo = torch.empty((B, L, H_q, d_k), dtype=dt, device=dev), H_q * d_k
-    else:
-        ld_qo = _head_rows(out_q, "out_q", B, L, H_q, d_k, dt, dev)
-    if out_k is None:
-        out_k, ld_ko = torch.empty((B, L, H_kv, d_k), dtype=dt, device=dev), H_kv * d_k
-    else:
-        ld_ko = _head_rows(out_k, "out_k", B, L, H_kv, d_k, dt, dev)
+    q, k = _qk_shapes(Q, K)
+    B, L, H_q, d_k = q
+    ld_q, ld_k = _head_rows(Q, "Q", q, dt, dev), _head_rows(K, "K", k, dt, dev)
+    out_q, ld_qo = _rows_or_new(out_q, "out_q", q, dt, dev)
+    out_k, ld_ko = _rows_or_new(out_k, "out_k", k, dt, dev)
     st = (_lib or load()).gsdpa_qk_norm_rope(
         Q.data_ptr(), K.data_ptr(), _vector(gamma_q, "gamma_q", d_k, dt, dev), _vector(gamma_k, "gamma_k", d_k, dt, dev),
         _vector(positions, "positions", B * L, torch.int32, dev), out_q.data_ptr(), out_k.data_ptr(), ld_q, ld_k, ld_qo,
-        ld_ko, B, L, H_q, H_kv, d_k, 1 if norm else 0, eps, None if rope is None else rope.ref, code,
+        ld_ko, B, L, H_q, k[2], d_k, 1 if norm else 0, eps, None if rope is None else rope.ref, code,
         _current_stream(dev))
     if st != OK:
         raise GsdpaError(st, "gsdpa_qk_norm_rope")
     return out_q, out_k
 
 
+@functools.lru_cache(maxsize=256)
 def qk_norm_rope_bwd_workspace_bytes(B, L, d_k, norm=True) -> int:
     n = (_lib or load()).gsdpa_qk_norm_rope_bwd_workspace_bytes(B, L, d_k, 1 if norm else 0)
     if n == ctypes.c_size_t(-1).value:
@@ -691,17 +701,12 @@ def qk_norm_rope_bwd(Q, K, dQo, dKo, *, gamma_q=None, gamma_k=None, norm=True, e
     import torch
     dt, dev = Q.dtype, Q.device
     code = _dtype_code(dt)
-    B, L, H_q, H_kv, d_k = _qk_dims(Q, K)
-    ld_q, ld_k = _head_rows(Q, "Q", B, L, H_q, d_k, dt, dev), _head_rows(K, "K", B, L, H_kv, d_k, dt, dev)
-    ld_dqo, ld_dko = _head_rows(dQo, "dQo", B, L, H_q, d_k, dt, dev), _head_rows(dKo, "dKo", B, L, H_kv, d_k, dt, dev)
-    if out_dq is None:
-        out_dq, ld_dq = torch.empty((B, L, H_q, d_k), dtype=dt, device=dev), H_q * d_k
-    else:
-        ld_dq = _head_rows(out_dq, "out_dq", B, L, H_q, d_k, dt, dev)
-    if out_dk is None:
-        out_dk, ld_dk = torch.empty((B, L, H_kv, d_k), dtype=dt, device=dev), H_kv * d_k
-    else:
-        ld_dk = _head_rows(out_dk, "out_dk", B, L, H_kv, d_k, dt, dev)
+    q, k = _qk_shapes(Q, K)
+    B, L, H_q, d_k = q
+    ld_q, ld_k = _head_rows(Q, "Q", q, dt, dev), _head_rows(K, "K", k, dt, dev)
+    ld_dqo, ld_dko = _head_rows(dQo, "dQo", q, dt, dev), _head_rows(dKo, "dKo", k, dt, dev)
+    out_dq, ld_dq = _rows_or_new(out_dq, "out_dq", q, dt, dev)
+    out_dk, ld_dk = _rows_or_new(out_dk, "out_dk", k, dt, dev)
     gq, gk = _vector(gamma_q, "gamma_q", d_k, dt, dev), _vector(gamma_k, "gamma_k", d_k, dt, dev)
     pos = _vector(positions, "positions", B * L, torch.int32, dev)
     out = {"dQ": out_dq, "dK": out_dk}
@@ -719,7 +724,7 @@ def qk_norm_rope_bwd(Q, K, dQo, dKo, *, gamma_q=None, gamma_k=None, norm=True, e
         workspace = _kept_workspace(need, dev, stream)
     st = (_lib or load()).gsdpa_qk_norm_rope_bwd(
         Q.data_ptr(), K.data_ptr(), gq, gk, pos, dQo.data_ptr(), dKo.data_ptr(), out_dq.data_ptr(), out_dk.data_ptr(),
-        dgq, dgk, ld_q, ld_k, ld_dqo, ld_dko, ld_dq, ld_dk, B, L, H_q, H_kv, d_k, 1 if norm else 0, eps,
+        dgq, dgk, ld_q, ld_k, ld_dqo, ld_dko, ld_dq, ld_dk, B, L, H_q, k[2], d_k, 1 if norm else 0, eps,
         None if rope is None else rope.ref, code, None if workspace is None else workspace.data_ptr(), need, stream)
     if st != OK:
         raise GsdpaError(st, "gsdpa_qk_norm_rope_bwd")
@@ -793,8 +798,9 @@ def cache8_append(cache, K, V, lens, n_new=None) -> None:
     dev, bf = cache.device, torch.bfloat16
     if K.dim() != 4:
         raise ValueError("K must be [B, L, H_kv, d_k]")
-    B, L, H, d = cache.B, K.shape[1], cache.H_kv, cache.d_k
-    ld_k, ld_v = _head_rows(K, "K", B, L, H, d, bf, dev), _head_rows(V, "V", B, L, H, d, bf, dev)
+    B, L = cache.B, K.shape[1]
+    shape = (B, L, cache.H_kv, cache.d_k)
+    ld_k, ld_v = _head_rows(K, "K", shape, bf, dev), _head_rows(V, "V", shape, bf, dev)
     if lens is None:
         raise ValueError("lens is required")
     st = (_lib or load()).gsdpa_cache8_append(

@@ -123,15 +123,18 @@ struct Quantiser {
     }
 };
 
-template <int D, bool E4M3>
-__global__ void __launch_bounds__(kThreads, 4) cache8_append_kernel(const AppendArgs a) {
+// CTAS: of an SM. Prompts gain by the fifth (4 x 8190 tokens 35.1 -> 34.2 us), whose
+// fewer registers cost a step or a short prompt (one token of 64 sequences 5.1 ->
+// 5.9 us, 4 x 1000 tokens 9.5 -> 10.3).
+template <int D, bool E4M3, int CTAS>
+__global__ void __launch_bounds__(kThreads, CTAS) cache8_append_kernel(const AppendArgs a) {
     constexpr int CH = D / 8;                              // 16-byte pieces of a row
     constexpr int KP = kCacheBlock * CH / kThreads;        // ... of the key tile per thread
     __shared__ uint32_t red[2][kThreads / 32];
     const int tid = threadIdx.x;
-    const int x = blockIdx.x % a.touched;
-    const int unit = blockIdx.x / a.touched;               // b * H_kv + h
-    const int h = unit % a.Hkv, b = unit / a.Hkv;
+    // (heads first: CTAs that run together read whole token rows; one head's blocks after the other 36.7 instead of 35.1 us)
+    const int h = blockIdx.x % a.Hkv, x = blockIdx.x / a.Hkv % a.touched, b = blockIdx.x / a.Hkv / a.touched;
+    const int unit = b * a.Hkv + h;
     pdl_wait();   // the new rows and lengths may be the previous kernel's outputs
     pdl_trigger();
     const SeqRange q = seq_range(a.lens, a.n_new, b, a.L, a.capacity);
@@ -285,6 +288,12 @@ __global__ void __launch_bounds__(kThreads, 4) cache8_append_kernel(const Append
     if (x == 0 && !early) keep_open();
 }
 
+template <int D, bool E4M3>
+cudaError_t launch(const AppendArgs& a, bool many, unsigned grid, cudaStream_t s) {
+    return many ? launch_dependent(cache8_append_kernel<D, E4M3, 5>, dim3(grid), dim3(kThreads), 0, s, a)
+                : launch_dependent(cache8_append_kernel<D, E4M3, 4>, dim3(grid), dim3(kThreads), 0, s, a);
+}
+
 bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
 
 }  // namespace
@@ -355,13 +364,10 @@ extern "C" int gsdpa_cache8_append(const gsdpa_cache8* cache, const void* K, con
     a.err = rt.err;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e;
-    const dim3 g((unsigned)grid), t(kThreads);
-    const bool e4m3 = cache->kind == GSDPA_CACHE_E4M3;
+    const bool e4m3 = cache->kind == GSDPA_CACHE_E4M3, many = touched > 2 && grid > 4LL * rt.num_sms;
     if (cache->d_k == 128)
-        e = e4m3 ? launch_dependent(cache8_append_kernel<128, true>, g, t, 0, s, a)
-                 : launch_dependent(cache8_append_kernel<128, false>, g, t, 0, s, a);
+        e = e4m3 ? launch<128, true>(a, many, (unsigned)grid, s) : launch<128, false>(a, many, (unsigned)grid, s);
     else
-        e = e4m3 ? launch_dependent(cache8_append_kernel<64, true>, g, t, 0, s, a)
-                 : launch_dependent(cache8_append_kernel<64, false>, g, t, 0, s, a);
+        e = e4m3 ? launch<64, true>(a, many, (unsigned)grid, s) : launch<64, false>(a, many, (unsigned)grid, s);
     return e == cudaSuccess ? GSDPA_OK : GSDPA_ERR_LAUNCH;
 }

@@ -614,7 +614,7 @@ cache8_attn_kernel(const __grid_constant__ Cache8Args a) {
     if (a.wait_first) pdl_wait();
     pdl_trigger();   // the next kernel may be set up; it waits for this grid before it touches memory
 
-    // ---- the CTA's share of all tiles, [lo, hi) of N, and the teams' shares of that
+    // ---- the teams' shares of all tiles, or of the CTA's own head
     const Layout all(a, s_place, s_scan, tid);
     const int me = blockIdx.x, N = all.N, ctas = all.ctas;
     const bool by_head = all.by_head;

@@ -129,6 +129,28 @@ def test_append_does_not_depend_on_the_split(kind):
 
 
 @pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("d", [64, 128])
+def test_append_of_long_prompts_is_that_of_short_pieces(kind, d):
+    # more blocks than the GPU holds at once, from inside a block on; against pieces of at most 64 tokens
+    B, H, capacity, start = 5, 8, 1280, [0, 63, 64, 17, 100]
+    new = [1100, 1025, 1, 1047, 1100]
+    K, V = rows(B, 1200, H, d, 21), rows(B, 1200, H, d, 22, 3.0)
+    one, many = filled(B, capacity, H, d, kind), filled(B, capacity, H, d, kind)
+    for c in (one, many):
+        gb.cache8_append(c, K[:, :100].contiguous(), V[:, :100].contiguous(), ints(*[0] * B), ints(*start))
+    late_k, late_v = K[:, 100:].contiguous(), V[:, 100:].contiguous()
+    gb.cache8_append(one, late_k, late_v, ints(*start), ints(*new))
+    for at in range(0, 1100, 64):
+        n = [max(0, min(64, x - at)) for x in new]
+        gb.cache8_append(many, late_k[:, at:at + 64].contiguous(), late_v[:, at:at + 64].contiguous(),
+                         ints(*[s + min(at, x) for s, x in zip(start, new)]), ints(*n))
+    for b in range(B):
+        for h in range(H):
+            for x, y in zip(cache_rows(one, b, h, start[b] + new[b]), cache_rows(many, b, h, start[b] + new[b])):
+                assert torch.equal(x, y), (b, h)
+
+
+@pytest.mark.parametrize("kind", KINDS)
 def test_append_takes_back_up_to_64_tokens(kind):
     H, d = 2, 64
     K, V = rows(1, 300, H, d, 3), rows(1, 300, H, d, 4)
@@ -322,6 +344,21 @@ def test_attention_in_a_cache_much_longer_than_its_sequences(lens):
     Q = rows(B, 1, 8, d, 46, 1.5)
     O = gb.gated_sdpa_cache8(None, Q, cache, ints(*lens), gate="none")
     check_attention(O, None, Q, cache, None, "none", lens, [1] * B)
+
+
+@pytest.mark.parametrize("kind,d,H,G,Lq,gate", [("e4m3", 128, 2, 8, 1, "headwise"), ("int8", 64, 3, 2, 2, "elementwise"),
+                                               ("int8", 128, 1, 16, 3, "none"), ("e4m3", 64, 2, 32, 4, "none")])
+def test_attention_heads_in_many_parts_beside_short_ones(kind, d, H, G, Lq, gate):
+    # long heads cut into more parts than a thread merges at once, between heads of a few tiles, whose
+    # ends (with and without an open block) and the places after them fall anywhere in the teams' shares
+    lens_after = [40001, 5, 64, 129, 3 * 64, 0, 40000, 1, 700, 64 * 40]
+    n = [min(Lq, x) for x in lens_after]
+    cache = fill_cache(lens_after, H, d, kind, 91)
+    X, W_g = gate_inputs(gate, len(n), Lq, H * G, d, 256, 92)
+    Q = rows(len(n), Lq, H * G, d, 93)
+    lens = [x - y for x, y in zip(lens_after, n)]
+    O = gb.gated_sdpa_cache8(X, Q, cache, ints(*lens), W_g, gate=gate, n_new=ints(*n))
+    check_attention(O, X, Q, cache, W_g, gate, lens, n)
 
 
 def test_attention_nothing_to_do_and_repeats():

@@ -559,7 +559,7 @@ def _head_rows(t, name, shape, dtype, device):
     if t is None:
         raise ValueError(f"{name} is required")
     if t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, the problem needs {shape}")
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, the problem needs {tuple(shape)}")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
     if t.device != device:
@@ -637,22 +637,14 @@ def _dtype_code(dt):
 
 def _qk_shapes(Q, K):
     """The shapes of Q [B, L, H_q, d_k] and K [B, L, H_kv, d_k]."""
-    q, k = tuple(Q.shape), tuple(K.shape)
+    q, k = Q.shape, K.shape
     if len(q) != 4 or len(k) != 4:
         raise ValueError("Q and K must be 4-D: [B, L, H, d_k]")
     if k[0] != q[0] or k[1] != q[1] or k[3] != q[3]:
-        raise ValueError(f"K {k} must be [B={q[0]}, L={q[1]}, H_kv, d_k={q[3]}]")
+        raise ValueError(f"K {tuple(k)} must be [B={q[0]}, L={q[1]}, H_kv, d_k={q[3]}]")
     if not Q.is_cuda:
         raise ValueError(f"Q must be a CUDA tensor, not on {Q.device}")
     return q, k
-
-
-def _rows_or_new(t, name, shape, dtype, device):
-    """An output, given or new, and its row length."""
-    if t is None:
-        import torch
-        return torch.empty(shape, dtype=dtype, device=device), shape[2] * shape[3]
-    return t, _head_rows(t, name, shape, dtype, device)
 
 
 @_on_stream
@@ -664,15 +656,21 @@ def qk_norm_rope(Q, K, *, gamma_q=None, gamma_k=None, norm=True, eps=1e-6, rope=
     Q and K (and out_q, out_k) may be column blocks of a packed projection's
     output, and out_q, out_k may be Q, K themselves. gamma_q, gamma_k [d_k] or
     None for 1; ``rope`` a Rope or None for no rotation; positions int32 [B, L] or
-    None for 0 .. L - 1. Returns (Q', K')."""
+    None for 0 .. L - 1. ``stream``: else the current one. Returns (Q', K')."""
     import torch
     dt, dev = Q.dtype, Q.device
     code = _dtype_code(dt)
     q, k = _qk_shapes(Q, K)
     B, L, H_q, d_k = q
     ld_q, ld_k = _head_rows(Q, "Q", q, dt, dev), _head_rows(K, "K", k, dt, dev)
-    out_q, ld_qo = _rows_or_new(out_q, "out_q", q, dt, dev)
-    out_k, ld_ko = _rows_or_new(out_k, "out_k", k, dt, dev)
+    if out_q is None:
+        out_q, ld_qo = torch.empty(q, dtype=dt, device=dev), H_q * d_k
+    else:
+        ld_qo = _head_rows(out_q, "out_q", q, dt, dev)
+    if out_k is None:
+        out_k, ld_ko = torch.empty(k, dtype=dt, device=dev), k[2] * d_k
+    else:
+        ld_ko = _head_rows(out_k, "out_k", k, dt, dev)
     st = (_lib or load()).gsdpa_qk_norm_rope(
         Q.data_ptr(), K.data_ptr(), _vector(gamma_q, "gamma_q", d_k, dt, dev), _vector(gamma_k, "gamma_k", d_k, dt, dev),
         _vector(positions, "positions", B * L, torch.int32, dev), out_q.data_ptr(), out_k.data_ptr(), ld_q, ld_k, ld_qo,
@@ -697,7 +695,8 @@ def qk_norm_rope_bwd(Q, K, dQo, dKo, *, gamma_q=None, gamma_k=None, norm=True, e
     """Backward of qk_norm_rope: from dQo, dKo (gradients of its outputs) and its
     inputs, a dict with dQ, dK and, with the norm, dgamma_q and dgamma_k (with
     respect to a gamma of 1 where none was given). out_dq, out_dk may be dQo, dKo
-    or column blocks of the packed projection's gradient."""
+    or column blocks of the packed projection's gradient. ``stream``: else the
+    current one."""
     import torch
     dt, dev = Q.dtype, Q.device
     code = _dtype_code(dt)
@@ -705,8 +704,14 @@ def qk_norm_rope_bwd(Q, K, dQo, dKo, *, gamma_q=None, gamma_k=None, norm=True, e
     B, L, H_q, d_k = q
     ld_q, ld_k = _head_rows(Q, "Q", q, dt, dev), _head_rows(K, "K", k, dt, dev)
     ld_dqo, ld_dko = _head_rows(dQo, "dQo", q, dt, dev), _head_rows(dKo, "dKo", k, dt, dev)
-    out_dq, ld_dq = _rows_or_new(out_dq, "out_dq", q, dt, dev)
-    out_dk, ld_dk = _rows_or_new(out_dk, "out_dk", k, dt, dev)
+    if out_dq is None:
+        out_dq, ld_dq = torch.empty(q, dtype=dt, device=dev), H_q * d_k
+    else:
+        ld_dq = _head_rows(out_dq, "out_dq", q, dt, dev)
+    if out_dk is None:
+        out_dk, ld_dk = torch.empty(k, dtype=dt, device=dev), k[2] * d_k
+    else:
+        ld_dk = _head_rows(out_dk, "out_dk", k, dt, dev)
     gq, gk = _vector(gamma_q, "gamma_q", d_k, dt, dev), _vector(gamma_k, "gamma_k", d_k, dt, dev)
     pos = _vector(positions, "positions", B * L, torch.int32, dev)
     out = {"dQ": out_dq, "dK": out_dk}
@@ -793,7 +798,8 @@ def cache8_alloc(B, capacity, H_kv, d_k, kind="int8", device="cuda") -> Cache8:
 def cache8_append(cache, K, V, lens, n_new=None) -> None:
     """Appends K, V [B, L, H_kv, d_k] bfloat16 to the cache (gsdpa_cache8_append):
     row i < n_new[b] becomes token lens[b] + i of sequence b. lens and n_new (None:
-    L each) are int32 [B] on the device and are not changed."""
+    L each) are int32 [B] on the device and are not changed. ``stream``: else the
+    current one."""
     import torch
     dev, bf = cache.device, torch.bfloat16
     if K.dim() != 4:
@@ -823,7 +829,7 @@ def gated_sdpa_cache8(X, Q, cache, lens, W_g=None, *, gate="elementwise", n_new=
     after cache8_append of their keys and values with the same lens and n_new: row i
     of Q [B, L_q, H_q, d_k] sees tokens 0 .. lens[b] + i. X [B, L_q, d_model] and W_g
     as for gated_sdpa_fwd (None for gate="none"). Rows i >= n_new[b] of the result
-    are zero. Returns O, like Q."""
+    are zero. ``stream``: else the current one. Returns O, like Q."""
     import torch
     dev, bf = cache.device, torch.bfloat16
     gm = GATE_CODES[gate]

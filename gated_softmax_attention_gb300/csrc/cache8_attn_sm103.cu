@@ -55,6 +55,10 @@
 // consecutive bytes of a value column are one lane's share of the second
 // product's wide operand; the weights reach their place in its narrow operand
 // by one 8 x 8 transposition (movmatrix) for each 8 tokens.
+//
+// Measured, heads of 128, without a gate: 64 sequences of 8192 tokens, 32/8 heads
+// 171 us (6.3 TB/s, 93 % of a plain copy); one of 131072 tokens, 16/2 heads 23 us;
+// 24 of up to 32767 tokens, 16/2 heads 48.5 us; one of 1000 tokens 11.5 us.
 #include "cache8_internal.h"
 
 #include <cuda_fp16.h>

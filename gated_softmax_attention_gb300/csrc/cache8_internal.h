@@ -1,9 +1,7 @@
 // cache8_internal.h -- what the append and the attention of the 8-bit K/V
 // cache share. Not part of the public ABI.
 #pragma once
-#include "gsdpa.h"
-#include "gsdpa_internal.h"
-#include "sm103_ptx.cuh"
+#include "ops_internal.h"
 
 namespace gsdpa {
 

@@ -3,6 +3,7 @@
 // device error word that bounded waits report into.
 #include "gsdpa.h"
 #include "gsdpa_internal.h"
+#include "ops_internal.h"
 #include "proj_internal.h"
 #include "sm103_ptx.cuh"
 
@@ -15,7 +16,7 @@
 namespace gsdpa {
 
 // Set by a kernel's bounded wait when it runs out, or by a length outside its
-// cache (the bits of sm103_ptx.cuh); read and cleared by
+// cache (ERR_CACHE_RANGE); read and cleared by
 // gsdpa_check_device_error().
 __device__ uint32_t g_error_word;
 

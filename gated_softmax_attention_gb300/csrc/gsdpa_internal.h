@@ -151,9 +151,6 @@ cudaError_t launch_gate_average_bf16(const Problem& p, const WorkspacePlan& w, c
 // Launchers: return cudaSuccess or the launch error. `ws` is the workspace base.
 cudaError_t launch_f32_simt(const Problem& p, const WorkspacePlan& w, char* ws, const Runtime& rt,
                             cudaStream_t s);
-// The gate-logit pre-pass over few rows (decode): rows, columns and K splits,
-// enough of them to spread the read of W_g over the SMs (gsdpa_api.cu).
-void plan_gate_rows(const Problem& p, int num_sms, WorkspacePlan* w);
 // A kernel that runs first in a call and zeroes `n` ints at `p` (its CTA 0,
 // before it lets the dependent kernel start); n = 0: nothing to zero.
 struct ZeroJob {

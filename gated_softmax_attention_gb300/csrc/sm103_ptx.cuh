@@ -13,11 +13,9 @@ namespace gsdpa {
 
 // ---------------------------------------------------------------- device error word
 // Bits a kernel ORs into the error word (a __device__ global owned by the
-// host API): one of its bounded waits ran out; a sequence's length or token
-// count, read on the device, lies outside its cache.
+// host API) when one of its bounded waits runs out.
 enum : uint32_t {
     ERR_WAIT_TIMEOUT = 1u,
-    ERR_CACHE_RANGE = 2u,
 };
 
 struct WaitCtl {
@@ -117,14 +115,6 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* m, int
         " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
         "l"(reinterpret_cast<uint64_t>(m)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar))
         : "memory");
-}
-
-// Untiled copy of `bytes` contiguous bytes (addresses and size multiples of 16).
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                     smem_u32(dst)),
-                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
-                 : "memory");
 }
 
 // Five-dimensional tile load. With a tensor map whose innermost dimension is

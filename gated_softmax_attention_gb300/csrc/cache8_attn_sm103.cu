@@ -71,7 +71,7 @@ constexpr int kMaxRows = 128;        // query rows (heads of a group x new token
 constexpr int kMaxStages = 16;       // ring stages per team
 constexpr int kMaxCtas = 160;        // most CTAs (plan_sms)
 constexpr int kMergeThreads = 512;
-constexpr int kBatch = 8;            // parts that a thread of a merge has under way
+constexpr int kBatch = 6;            // parts that a thread of a merge has under way
 // A head is one CTA's where all have at most this many tiles and there are CTAs for
 // all: its teams then merge in shared memory. If the capacity says so already, the
 // merge kernel is not launched (1000 tokens: 11.5 us and 2.5 us less of the host's
@@ -1129,27 +1129,43 @@ __global__ void __launch_bounds__(kMergeThreads) cache8_merge_kernel(const __gri
     // (the attention kernel started after everything before this call had ended: the lengths may be read)
     const Layout all(a, s_place, s_scan, tid);
     const Deal deal(all.N, all.ctas << a.lg_teams);
-    const int items = a.rows * (D / 4);
-    const long long heads = all.by_head ? 0 : (long long)a.B * a.Hkv, threads = (long long)gridDim.x * kMergeThreads;
+    const int items = a.rows * (D / 4), takers = all.ctas << a.lg_teams, threads = gridDim.x * kMergeThreads;
+    // A unit of the work is a head, or where there are more heads than places at which
+    // shares begin, such a place, for the head that it is the first to cut.
+    const long long heads = (long long)a.B * a.Hkv;
+    const bool by_place = heads >= takers;
+    const int units = all.by_head ? 0 : (by_place ? takers - 1 : (int)heads);
     const int most = deal.each > 0 ? all.longest / deal.each + 2 : 1;   // parts of a head
     int lg = 0;
-    while ((8 << lg) <= kMergeThreads && ((heads * items) << (lg + 1)) <= threads && (4 << lg) < most) ++lg;
-    const long long total = (heads * items) << lg;
+    while ((8 << lg) <= kMergeThreads && ((units * items) << (lg + 1)) <= threads && (4 << lg) < most) ++lg;
+    const int total = (units * items) << lg;   // (below 1280 x 4096, or the grid's threads)
     bool waited = false;
-    for (long long base = (long long)blockIdx.x * kMergeThreads; base < total; base += threads) {
-        const long long idx = base + tid;
-        const int per_head = items << lg;
-        const bool in = idx < total;
-        const long long unit = in ? idx / per_head : 0;
-        const int x = (int)(idx - unit * per_head), item = (x >> (lg + 2) << 2) + (x & 3), sub = (x >> 2) & ((1 << lg) - 1);
+    for (int base = blockIdx.x * kMergeThreads; base < total; base += threads) {
+        const int idx = base + tid, unit = idx / (items << lg);
+        const int x = idx - unit * (items << lg), item = (x >> (lg + 2) << 2) + (x & 3), sub = (x >> 2) & ((1 << lg) - 1);
         const int row = item / (D / 4), col = 4 * (item % (D / 4));
-        const int b = (int)(unit / a.Hkv), kvh = (int)(unit % a.Hkv);
-        const SeqTiles q(a, b);
-        const int u0 = all.before(a, b) + kvh * q.span();
-        int n0 = 0, n1 = 0;
-        if (in && q.tiles > 0) {
-            n0 = deal.taker(u0);
-            n1 = deal.taker(u0 + q.tiles - 1);
+        int b = 0, kvh = 0, u0 = 0, n0 = 0, n1 = 0;
+        if (by_place) {
+            const int from = idx < total ? deal.from(unit + 1) : all.N;
+            if (from < all.N) {
+                all.find(a, from, b, u0);
+                const int tiles = SeqTiles(a, b).tiles, span = span_of(tiles), at = u0 % max(span, 1);
+                kvh = u0 / max(span, 1);
+                u0 = from - at;
+                if (at > 0 && at < tiles && deal.taker(u0) == unit) {
+                    n0 = unit;
+                    n1 = deal.taker(u0 + tiles - 1);
+                }
+            }
+        } else if (idx < total) {
+            b = unit / a.Hkv;
+            kvh = unit % a.Hkv;
+            const int tiles = SeqTiles(a, b).tiles;
+            u0 = all.before(a, b) + kvh * span_of(tiles);
+            if (tiles > 0) {
+                n0 = deal.taker(u0);
+                n1 = deal.taker(u0 + tiles - 1);
+            }
         }
         if (!waited) pdl_wait();
         waited = true;
@@ -1175,7 +1191,7 @@ __global__ void __launch_bounds__(kMergeThreads) cache8_merge_kernel(const __gri
             }
             __syncthreads();
         }
-        if (cut && sub == 0) finish<D>(a, b, kvh, q.n, row, col, out_scale(r.m, r.l, r.M), r.o);
+        if (cut && sub == 0) finish<D>(a, b, kvh, SeqTiles(a, b).n, row, col, out_scale(r.m, r.l, r.M), r.o);
     }
     if (!waited) pdl_wait();   // the next kernel on the stream relies on the attention kernel having ended
 }

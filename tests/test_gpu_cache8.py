@@ -361,6 +361,42 @@ def test_attention_heads_in_many_parts_beside_short_ones(kind, d, H, G, Lq, gate
     check_attention(O, X, Q, cache, W_g, gate, lens, n)
 
 
+@pytest.mark.parametrize("H,d,Lq,G,gate", [(8, 64, 1, 4, "none"), (2, 128, 2, 8, "headwise")])
+def test_attention_more_heads_than_teams(H, d, Lq, G, gate):
+    # thousands of short heads, most of them a team's alone, empty sequences between them; and one long enough
+    # to be cut into several parts
+    g = torch.Generator().manual_seed(94)
+    lens_after = [int(x) for x in torch.randint(0, 400, (700,), generator=g)]
+    for b in range(0, 700, 9):
+        lens_after[b] = 0
+    lens_after[333], lens_after[699] = 64 * 50 + 3, 64
+    n = [min(Lq, x) for x in lens_after]
+    B, capacity = 700, 64 * 51
+    cache = filled(B, capacity, H, d, "int8")
+    step = 448
+    K, V = rows(B, step, H, d, 95), rows(B, step, H, d, 96)
+    for at in range(0, capacity, step):
+        gb.cache8_append(cache, K, V, ints(*[min(at, x) for x in lens_after]),
+                         ints(*[max(0, min(step, x - at)) for x in lens_after]))
+    X, W_g = gate_inputs(gate, B, Lq, H * G, d, 64, 97)
+    Q = rows(B, Lq, H * G, d, 98)
+    lens = [x - y for x, y in zip(lens_after, n)]
+    O = gb.gated_sdpa_cache8(X, Q, cache, ints(*lens), W_g, gate=gate, n_new=ints(*n))
+    for b in [0, 1, 9, 332, 333, 334, 500, 698, 699]:
+        one = gb.Cache8(*(t[b:b + 1] for t in (cache.k8, cache.v8, cache.k_scale, cache.v_scale, cache.k_tail, cache.v_tail)))
+        x = None if X is None else X[b:b + 1]
+        check_attention(O[b:b + 1], x, Q[b:b + 1], one, W_g, gate, [lens[b]], [n[b]])
+    check = list(range(0, B, 7)) + [333]
+    got = O[check].double()
+    part = gb.Cache8(*(t[check].contiguous() for t in (cache.k8, cache.v8, cache.k_scale, cache.v_scale, cache.k_tail,
+                                                        cache.v_tail)))
+    again = gb.gated_sdpa_cache8(None if X is None else X[check].contiguous(), Q[check].contiguous(), part,
+                                 ints(*[lens[b] for b in check]), W_g, gate=gate, n_new=ints(*[n[b] for b in check])).double()
+    # the same sums cut elsewhere: each side within 2^-7 of the largest value of the definition (bf16's half step
+    # 2^-9, the weights' 2^-9 for the open block, both of values no larger than that)
+    assert float((got - again).abs().max()) <= 2.0 ** -6 * float(again.abs().max())
+
+
 def test_attention_nothing_to_do_and_repeats():
     cache = fill_cache([5, 70], 2, 64, "int8", 33)
     Q = rows(2, 1, 4, 64, 34)

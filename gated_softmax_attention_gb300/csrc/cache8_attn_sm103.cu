@@ -393,31 +393,49 @@ __device__ __forceinline__ float out_scale(float m, float l, float M) {
     return l > 0.f || l != l ? (M == -INFINITY ? 0.f : ex2_approx(M - m)) / l : 0.f;
 }
 
-// Output columns [col, col + 4) of query row `row`: the sums o, scaled by k,
-// gated and stored.
+// The gate's values for columns [col, col + 4) of query row `row`: of all K splits of
+// the logits a batch of loads is under way at a time.
 template <int D>
-__device__ __forceinline__ void finish(const Cache8Args& a, int b, int kvh, int n, int row, int col, float k,
-                                       const float4& o) {
+__device__ __forceinline__ float4 gate_of(const Cache8Args& a, int b, int kvh, int n, int row, int col) {
     const int i = row * a.g_inverse >> 16;
-    if (i >= n) return;
+    if (a.gate_mode == GSDPA_GATE_NONE || i >= n) return make_float4(1.f, 1.f, 1.f, 1.f);
     const int h = (kvh - i) * a.G + row;   // kvh G + row % G
-    float y[4] = {o.x * k, o.y * k, o.z * k, o.w * k};
-    const long long token = (long long)b * a.Lq + i;
-    if (a.gate_mode != GSDPA_GATE_NONE) {
-        const bool per_col = a.gate_mode == GSDPA_GATE_ELEMENTWISE;
-        const float* gp = a.gate_part + token * a.gate_cols + (per_col ? (long long)h * D + col : h);
-        const long long step = (long long)a.B * a.Lq * a.gate_cols;
-        float gl[4] = {0.f, 0.f, 0.f, 0.f};
-        for (int sp = 0; sp < a.gate_splits; ++sp) {
+    const long long token = (long long)b * a.Lq + i, step = (long long)a.B * a.Lq * a.gate_cols;
+    const bool per_col = a.gate_mode == GSDPA_GATE_ELEMENTWISE;
+    const float* gp = a.gate_part + token * a.gate_cols + (per_col ? (long long)h * D + col : h);
+    float4 gl = make_float4(0.f, 0.f, 0.f, 0.f);
+    constexpr int BATCH = 8;
+    for (int sp = 0; sp < a.gate_splits; sp += BATCH) {
+        float4 v[BATCH];
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (per_col || e == 0) gl[e] += gp[sp * step + e];
+        for (int k = 0; k < BATCH; ++k) {
+            v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (sp + k >= a.gate_splits) continue;
+            if (per_col) v[k] = *reinterpret_cast<const float4*>(gp + (sp + k) * step);
+            else v[k].x = gp[(sp + k) * step];
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) y[e] *= sigmoid(per_col ? gl[e] : gl[0]);
+        for (int k = 0; k < BATCH; ++k) {
+            gl.x += v[k].x;
+            gl.y += v[k].y;
+            gl.z += v[k].z;
+            gl.w += v[k].w;
+        }
     }
-    *reinterpret_cast<uint2*>(a.O + (token * a.Hq + h) * D + col) =
-        make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
+    if (!per_col) gl.y = gl.z = gl.w = gl.x;
+    return make_float4(sigmoid(gl.x), sigmoid(gl.y), sigmoid(gl.z), sigmoid(gl.w));
+}
+
+// Output columns [col, col + 4) of query row `row`: the sums o, scaled by k, times
+// the gate, stored.
+template <int D>
+__device__ __forceinline__ void finish(const Cache8Args& a, int b, int kvh, int n, int row, int col, float k,
+                                       const float4& o, const float4& gate) {
+    const int i = row * a.g_inverse >> 16;
+    if (i >= n) return;
+    const int h = (kvh - i) * a.G + row;
+    *reinterpret_cast<uint2*>(a.O + (((long long)b * a.Lq + i) * a.Hq + h) * D + col) =
+        make_uint2(pack_bf16x2(o.x * k * gate.x, o.y * k * gate.y), pack_bf16x2(o.z * k * gate.z, o.w * k * gate.w));
 }
 
 // 2^(x - top), 0 for a part that saw nothing.
@@ -1070,7 +1088,7 @@ cache8_attn_kernel(const __grid_constant__ Cache8Args a) {
                     const float* from = slot + row * STRIDE;
                     const float4 x = *reinterpret_cast<const float4*>(from + D);
                     finish<D>(a, at.b, at.kvh, q.n, row, col, out_scale(x.x, x.y, x.z),
-                              *reinterpret_cast<const float4*>(from + col));
+                              *reinterpret_cast<const float4*>(from + col), gate_of<D>(a, at.b, at.kvh, q.n, row, col));
                 }
                 if (!final) named_bar_sync(1 + team, team_threads);
             }
@@ -1088,6 +1106,7 @@ cache8_attn_kernel(const __grid_constant__ Cache8Args a) {
         while (lg < 3 && (items << (lg + 1)) <= kConsumers) ++lg;
         for (int idx = tid; idx < items << lg; idx += kConsumers) {
             const int item = idx >> lg, row = item / (D / 4), col = 4 * (item % (D / 4));
+            const float4 gate = gate_of<D>(a, b, me % a.Hkv, n, row, col);
             Sums r;
             r.add(idx & ((1 << lg) - 1), parts * C::KS, 1 << lg, D, col, [&](int i) {
                 return (i < parts ? slots + (size_t)i * a.rows * STRIDE
@@ -1095,7 +1114,8 @@ cache8_attn_kernel(const __grid_constant__ Cache8Args a) {
                        row * STRIDE;
             });
             for (int sh = 1; sh < 1 << lg; sh <<= 1) r.join_lane(sh);
-            if ((idx & ((1 << lg) - 1)) == 0) finish<D>(a, b, me % a.Hkv, n, row, col, out_scale(r.m, r.l, r.M), r.o);
+            if ((idx & ((1 << lg) - 1)) == 0)
+                finish<D>(a, b, me % a.Hkv, n, row, col, out_scale(r.m, r.l, r.M), r.o, gate);
         }
     }
 
@@ -1170,6 +1190,9 @@ __global__ void __launch_bounds__(kMergeThreads) cache8_merge_kernel(const __gri
         if (!waited) pdl_wait();
         waited = true;
         const bool cut = n1 > n0;
+        const int n = cut ? SeqTiles(a, b).n : 0;
+        float4 gate = make_float4(1.f, 1.f, 1.f, 1.f);
+        if (cut && sub == 0) gate = gate_of<D>(a, b, kvh, n, row, col);
         Sums r;
         if (cut)
             r.add(n0 + sub, n1 + 1, 1 << lg, D, col, [&](int k) { return part_of<D>(a, deal, k, u0) + row * (D + 4); });
@@ -1191,7 +1214,7 @@ __global__ void __launch_bounds__(kMergeThreads) cache8_merge_kernel(const __gri
             }
             __syncthreads();
         }
-        if (cut && sub == 0) finish<D>(a, b, kvh, SeqTiles(a, b).n, row, col, out_scale(r.m, r.l, r.M), r.o);
+        if (cut && sub == 0) finish<D>(a, b, kvh, n, row, col, out_scale(r.m, r.l, r.M), r.o, gate);
     }
     if (!waited) pdl_wait();   // the next kernel on the stream relies on the attention kernel having ended
 }

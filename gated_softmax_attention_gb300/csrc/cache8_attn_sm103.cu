@@ -72,12 +72,13 @@ constexpr int kMaxStages = 16;       // ring stages per team
 constexpr int kMaxCtas = 160;        // most CTAs (plan_sms)
 constexpr int kMergeThreads = 512;
 constexpr int kBatch = 6;            // parts that a thread of a merge has under way
-// A head is one CTA's where all have at most this many tiles and there are CTAs for
-// all: its teams then merge in shared memory. If the capacity says so already, the
-// merge kernel is not launched (1000 tokens: 11.5 us and 2.5 us less of the host's
-// time, cut up 10.3 us); if only the lengths do, it is, for nothing (60 tokens: 6.9
-// us, cut up 10.1; 500 tokens 10.1 and 10.1; 1000 tokens 12.1 and 10.3).
-constexpr int kWholeTiles = 24, kFewTiles = 8;
+// A head is one CTA's where all have at most this many tiles for each team of it and
+// there are CTAs for all: the teams then merge in shared memory. If the capacity says
+// so already, the merge kernel is not launched (1000 tokens, 8 teams: 11.5 us and 2.5
+// us less of the host's time, cut up 10.3 us); if only the lengths do, it is, for
+// nothing (60 tokens: 6.9 us, cut up 10.1; 500 tokens 10.1 and 10.1; 1000 tokens 12.1
+// and 10.3). (128 query rows are one team's: 1000 tokens by a CTA 47.7 us, cut up 14.3.)
+constexpr int kWholeTiles = 3, kFewTiles = 1;
 constexpr int kBars = 48;            // ring stages of all teams
 constexpr uint32_t kSmemMax = 232448 - 1984;   // dynamic: what a CTA may have, less barriers, parts and a few words
 constexpr int kSwitch = 4;           // most places after a head without a tile
@@ -1388,8 +1389,8 @@ int gated_sdpa_cache8(const void* X, const void* Q, const gsdpa_cache8* cache, c
     long long grid = sms;   // (no fewer than the heads, where those fit)
     if (grid > most) grid = most;
     a.ctas = (int)grid;
-    const bool whole = a.blocks <= kWholeTiles && (long long)a.B * a.Hkv <= grid;
-    a.whole_tiles = whole ? kWholeTiles : kFewTiles;
+    const bool whole = a.blocks <= kWholeTiles << a.lg_teams && (long long)a.B * a.Hkv <= grid;
+    a.whole_tiles = (whole ? kWholeTiles : kFewTiles) << a.lg_teams;
     const bool e4m3 = cache->kind == GSDPA_CACHE_E4M3;
     if (cache->d_k == 128)
         e = e4m3 ? launch<128, true>(a, sh, (unsigned)grid, s) : launch<128, false>(a, sh, (unsigned)grid, s);

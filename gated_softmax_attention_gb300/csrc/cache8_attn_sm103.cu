@@ -741,14 +741,15 @@ cache8_attn_kernel(const __grid_constant__ Cache8Args a) {
             }
             __nanosleep(40);
         }
-        if (!__all_sync(0xffffffffu, next.left <= 0)) {
-            // let copies in flight land before the CTA exits
-            volatile int never = 0;
-            WaitCtl c2 = a.ctl;
-            if (c2.limit_ns < 1000000000ull) c2.limit_ns = 1000000000ull;
-            for (int k = 0; k < a.stages; ++k)
-                if (armed & (1u << k)) mbar_wait(&full[k], (armed_phase >> k) & 1u, &never, c2);
-        }
+        // The CTA keeps its shared memory until this warp is done: it stays until what it
+        // has issued is there, whoever gave up. (A share that is no longer than its ring is
+        // issued at once, and its consumers may still give up; where they wait for the same
+        // copies this costs nothing.)
+        volatile int never = 0;
+        WaitCtl c2 = a.ctl;
+        if (c2.limit_ns < 1000000000ull) c2.limit_ns = 1000000000ull;
+        for (int k = 0; k < a.stages; ++k)
+            if (armed & (1u << k)) mbar_wait(&full[k], (armed_phase >> k) & 1u, &never, c2);
         return;
     }
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS));

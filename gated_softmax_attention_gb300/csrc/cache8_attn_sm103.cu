@@ -746,8 +746,7 @@ cache8_attn_kernel(const __grid_constant__ Cache8Args a) {
         // issued at once, and its consumers may still give up; where they wait for the same
         // copies this costs nothing.)
         volatile int never = 0;
-        WaitCtl c2 = a.ctl;
-        if (c2.limit_ns < 1000000000ull) c2.limit_ns = 1000000000ull;
+        const WaitCtl c2 = landing_limit(a.ctl);
         for (int k = 0; k < a.stages; ++k)
             if (armed & (1u << k)) mbar_wait(&full[k], (armed_phase >> k) & 1u, &never, c2);
         return;

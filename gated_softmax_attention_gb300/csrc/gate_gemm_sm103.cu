@@ -117,9 +117,8 @@ gate_logits_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
             uint32_t armed_phase[NS];
             bool armed[NS];
             for (int s = 0; s < NS; ++s) armed[s] = false;
-            bool ok = true;
             for (int kc = kc0; kc < kc1; ++kc) {
-                if (!(ok = mbar_wait(&empty[stage], phase ^ 1u, abort_flag, args.ctl))) break;
+                if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, args.ctl)) break;
                 mbar_arrive_expect_tx(&full[stage], C::STAGE);
                 armed[stage] = true;
                 armed_phase[stage] = phase;
@@ -132,11 +131,12 @@ gate_logits_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
                     phase ^= 1u;
                 }
             }
-            if (!ok) {
-                volatile int never = 0;
-                for (int s = 0; s < NS; ++s)
-                    if (armed[s]) mbar_wait(&full[s], armed_phase[s], &never, args.ctl);
-            }
+            // the CTA ends after this thread: what it has issued is there by then, also where
+            // it had issued everything before another warp's wait ran out
+            volatile int never = 0;
+            const WaitCtl c2 = landing_limit(args.ctl);
+            for (int s = 0; s < NS; ++s)
+                if (armed[s]) mbar_wait(&full[s], armed_phase[s], &never, c2);
         }
     } else if (warp == 1) {
         if (lane == 0) {
@@ -160,13 +160,12 @@ gate_logits_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
                     phase ^= 1u;
                 }
             }
-            if (ok) {
-                mma_commit(acc_full);
-            } else {
-                volatile int never = 0;
-                mma_commit(drain);
-                mbar_wait(drain, 0, &never, args.ctl);
-            }
+            // tensor memory is freed after this thread: every MMA is complete by then, also
+            // where the epilogue's wait for them ran out
+            volatile int never = 0;
+            uint64_t* done = ok ? acc_full : drain;
+            mma_commit(done);
+            mbar_wait(done, 0, &never, landing_limit(args.ctl));
         }
     } else {
         const int qd = warp & 3;

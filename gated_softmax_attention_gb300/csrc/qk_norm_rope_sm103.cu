@@ -465,8 +465,7 @@ __global__ void __launch_bounds__(kThreads, 4) qk_norm_rope_bwd_kernel(const __g
     if (!ok && ln.lane == 0) {
         // let copies in flight land before the CTA exits
         volatile int never = 0;
-        WaitCtl c2 = a.ctl;
-        if (c2.limit_ns < 1000000000ull) c2.limit_ns = 1000000000ull;
+        const WaitCtl c2 = landing_limit(a.ctl);
 #pragma unroll
         for (int k = 0; k < kRing; ++k)
             if (fetched[k] > 0) mbar_wait(&full[warp][k], (fetched[k] - 1) & 1u, &never, c2);

@@ -86,6 +86,13 @@ static __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity,
     }
 }
 
+// The limit of a wait for what is already under way (copies, MMAs) before a CTA that
+// gave up ends: a second at least, however short the caller's limit is.
+static __device__ __forceinline__ WaitCtl landing_limit(WaitCtl ctl) {
+    if (ctl.limit_ns < 1000000000ull) ctl.limit_ns = 1000000000ull;
+    return ctl;
+}
+
 // ---------------------------------------------------------------- TMA (tensor maps)
 __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap* m) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");

@@ -57,3 +57,20 @@ def test_shares_shorter_than_their_ring_give_up_cleanly(lens, H, Hq, d, Lq):
     for _ in range(10):
         assert with_a_tiny_limit(call) in (gb.OK, gb.ERR_DEVICE_TIMEOUT)
         assert torch.equal(call(), want) and gb.check_device_error() == gb.OK
+
+
+@pytest.mark.parametrize("gate,dm", [("headwise", 64), ("headwise", 8192), ("elementwise", 256), ("elementwise", 8192)])
+def test_gate_logits_give_up_cleanly(gate, dm):
+    # few chunks of d_model, all copied at once, and many, whose products the epilogue waits for longest
+    lens, H, Hq, d = [300, 64], 2, 8, 128
+    cache = filled_cache(lens, H, d, "e4m3", 3)
+    g = torch.Generator(device="cuda").manual_seed(4)
+    Q = torch.randn(2, 1, Hq, d, generator=g, device="cuda").bfloat16()
+    X = torch.randn(2, 1, dm, generator=g, device="cuda").bfloat16()
+    W = (torch.randn(dm, Hq if gate == "headwise" else Hq * d, generator=g, device="cuda") / dm ** 0.5).bfloat16()
+    at = torch.tensor([n - 1 for n in lens], dtype=torch.int32, device="cuda")
+    call = lambda: gb.gated_sdpa_cache8(X, Q, cache, at, W, gate=gate)  # noqa: E731
+    want = call()
+    for _ in range(10):
+        assert with_a_tiny_limit(call) in (gb.OK, gb.ERR_DEVICE_TIMEOUT)
+        assert torch.equal(call(), want) and gb.check_device_error() == gb.OK

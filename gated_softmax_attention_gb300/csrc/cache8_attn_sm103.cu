@@ -32,7 +32,10 @@
 // M for the outputs, which carry the value scales: a block adds
 // (p c) V8 with c = vs 2^(m - M), so that a block of large values that the
 // query hardly looks at cannot push the others' products out of fp16's range.
-// They move when a tile exceeds them by 2^8 (rarely after the first tile).
+// They move when a tile exceeds them by 2^8 (rarely after the first tile). M also
+// follows m from kApart below: where the row's weight went to a block whose
+// values are zero or next to it, c would exceed float32 for the blocks whose weights
+// vanish beside it (less than 2^-126 of the row's largest weight is nothing).
 //
 // Tile = one block: K8 [64][d_k] and V8 [d_k][64], each 64 d_k contiguous bytes,
 // brought by cp.async.bulk. The tiles of all sequences and K/V heads form one
@@ -85,6 +88,7 @@ constexpr int kSwitch = 4;           // most places after a head without a tile
 constexpr int kScan = 128;           // places in the sequence of all tiles that are looked up
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kMove = 8.0f;
+constexpr float kApart = 100.0f;
 
 struct Cache8Args {
     const __nv_bfloat16* Q;          // [B, Lq, Hq, D]
@@ -297,7 +301,8 @@ __device__ __forceinline__ void soften(float (&s)[NT][MT][4], const float (&f)[N
             k[n][e] = f[n][e] * ks;
             // (a score that is no number is not above anything: the weights show it)
             top[n][e] = top[n][e] == -INFINITY ? -INFINITY : top[n][e] * k[n][e];
-            need = need || top[n][e] > st.m[n][e] + kMove || top[n][e] + ev + 1.f > st.M[n][e] + kMove;
+            need = need || top[n][e] > st.m[n][e] + kMove ||
+                   fmaxf(top[n][e], st.m[n][e] - kApart) + ev + 1.f > st.M[n][e] + kMove;
         }
     }
     if (__any_sync(0xffffffffu, need)) {
@@ -309,7 +314,7 @@ __device__ __forceinline__ void soften(float (&s)[NT][MT][4], const float (&f)[N
                 float x = top[n][e];
 #pragma unroll
                 for (int sh = 4; sh < 32; sh <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, sh));
-                const float m = fmaxf(st.m[n][e], x), M = fmaxf(st.M[n][e], x + ev + 1.f);
+                const float m = fmaxf(st.m[n][e], x), M = fmaxf(st.M[n][e], fmaxf(x, m - kApart) + ev + 1.f);
                 st.l[n][e] *= st.m[n][e] == -INFINITY ? 0.f : ex2_approx(st.m[n][e] - m);
                 fo[e] = st.M[n][e] == -INFINITY ? 0.f : ex2_approx(st.M[n][e] - M);
                 st.m[n][e] = m;

@@ -24,15 +24,19 @@
 //
 // int8 and e4m3 codes are exact in fp16; q, a bf16 row scaled by a power of two
 // to below 1, too (elements under 2^-14 of the row's largest lose bits that
-// weigh less than 2^-24 of it). The weights are rounded to fp16 (11 bits) for
-// the second product; the open block's, whose values may exceed fp16's range,
-// to two bf16 parts (16 bits).
+// weigh less than 2^-24 of it). The weights, times their block's value scale, are
+// rounded to fp16 for the second product. fp16's own range is short, so they use
+// all of it: the largest stand for 2^12 to 2^15, those down to 2^-26 of them keep 11
+// bits, smaller ones lose bits and from 2^-37 on vanish (with the largest at 2^-1,
+// 8192 tokens beside one of zero values that had 99.9 % of the weight came out 10 %
+// off). The open block's, whose values may exceed fp16's range, become two bf16
+// parts (16 bits).
 //
 // Two running references, both only for range: m for the sum of weights, and
 // M for the outputs, which carry the value scales: a block adds
 // (p c) V8 with c = vs 2^(m - M), so that a block of large values that the
 // query hardly looks at cannot push the others' products out of fp16's range.
-// They move when a tile exceeds them by 2^8 (rarely after the first tile). M also
+// They move when a tile exceeds them by 2^8 and 2^2 (rarely after the first tile). M also
 // follows m from kApart below: where the row's weight went to a block whose
 // values are zero or next to it, c would exceed float32 for the blocks whose weights
 // vanish beside it (less than 2^-126 of the row's largest weight is nothing).
@@ -87,7 +91,8 @@ constexpr uint32_t kSmemMax = 232448 - 1984;   // dynamic: what a CTA may have, 
 constexpr int kSwitch = 4;           // most places after a head without a tile
 constexpr int kScan = 128;           // places in the sequence of all tiles that are looked up
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kMove = 8.0f;
+constexpr float kMove = 8.0f, kMoveOut = 2.0f;   // how far a tile may exceed m, and M, in log2 units
+constexpr float kUp = 13.0f;         // M stands 2^kUp below the largest product: 2^(kUp + kMoveOut) is in fp16's range
 constexpr float kApart = 100.0f;
 
 struct Cache8Args {
@@ -302,7 +307,7 @@ __device__ __forceinline__ void soften(float (&s)[NT][MT][4], const float (&f)[N
             // (a score that is no number is not above anything: the weights show it)
             top[n][e] = top[n][e] == -INFINITY ? -INFINITY : top[n][e] * k[n][e];
             need = need || top[n][e] > st.m[n][e] + kMove ||
-                   fmaxf(top[n][e], st.m[n][e] - kApart) + ev + 1.f > st.M[n][e] + kMove;
+                   fmaxf(top[n][e], st.m[n][e] - kApart) + ev + 1.f - kUp > st.M[n][e] + kMoveOut;
         }
     }
     if (__any_sync(0xffffffffu, need)) {
@@ -314,7 +319,7 @@ __device__ __forceinline__ void soften(float (&s)[NT][MT][4], const float (&f)[N
                 float x = top[n][e];
 #pragma unroll
                 for (int sh = 4; sh < 32; sh <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, sh));
-                const float m = fmaxf(st.m[n][e], x), M = fmaxf(st.M[n][e], fmaxf(x, m - kApart) + ev + 1.f);
+                const float m = fmaxf(st.m[n][e], x), M = fmaxf(st.M[n][e], fmaxf(x, m - kApart) + ev + 1.f - kUp);
                 st.l[n][e] *= st.m[n][e] == -INFINITY ? 0.f : ex2_approx(st.m[n][e] - m);
                 fo[e] = st.M[n][e] == -INFINITY ? 0.f : ex2_approx(st.M[n][e] - M);
                 st.m[n][e] = m;
@@ -394,9 +399,11 @@ __device__ __forceinline__ float row_to_f16(uint32_t (&w)[D / 16][2]) {
 }
 
 // What turns a row's summed outputs into the attention's (a row whose weights
-// leave nothing is zero).
-__device__ __forceinline__ float out_scale(float m, float l, float M) {
-    return l > 0.f || l != l ? (M == -INFINITY ? 0.f : ex2_approx(M - m)) / l : 0.f;
+// leave nothing is zero): two factors, because 2^(M - m) alone may leave float32's
+// range where the output does not.
+__device__ __forceinline__ float2 out_scale(float m, float l, float M) {
+    const float half = M == -INFINITY ? 0.f : ex2_approx(0.5f * (M - m));
+    return make_float2(half, l > 0.f || l != l ? half / l : 0.f);
 }
 
 // The gate's values for columns [col, col + 4) of query row `row`: of all K splits of
@@ -432,16 +439,17 @@ __device__ __forceinline__ float4 gate_of(const Cache8Args& a, int b, int kvh, i
     return make_float4(sigmoid(gl.x), sigmoid(gl.y), sigmoid(gl.z), sigmoid(gl.w));
 }
 
-// Output columns [col, col + 4) of query row `row`: the sums o, scaled by k, times
-// the gate, stored.
+// Output columns [col, col + 4) of query row `row`: the sums o, scaled by both of k,
+// times the gate, stored.
 template <int D>
-__device__ __forceinline__ void finish(const Cache8Args& a, int b, int kvh, int n, int row, int col, float k,
+__device__ __forceinline__ void finish(const Cache8Args& a, int b, int kvh, int n, int row, int col, const float2& k,
                                        const float4& o, const float4& gate) {
     const int i = row * a.g_inverse >> 16;
     if (i >= n) return;
     const int h = (kvh - i) * a.G + row;
     *reinterpret_cast<uint2*>(a.O + (((long long)b * a.Lq + i) * a.Hq + h) * D + col) =
-        make_uint2(pack_bf16x2(o.x * k * gate.x, o.y * k * gate.y), pack_bf16x2(o.z * k * gate.z, o.w * k * gate.w));
+        make_uint2(pack_bf16x2(o.x * k.x * k.y * gate.x, o.y * k.x * k.y * gate.y),
+                   pack_bf16x2(o.z * k.x * k.y * gate.z, o.w * k.x * k.y * gate.w));
 }
 
 // 2^(x - top), 0 for a part that saw nothing.

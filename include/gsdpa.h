@@ -498,6 +498,10 @@ GSDPA_API int gsdpa_cache8_append(const gsdpa_cache8* cache, const void* K, cons
  * a sequence's end are not seen whatever their bytes; a NaN or infinity among the
  * step's own keys is seen by the rows that may see it, one among its values in the
  * open block, or a NaN code in v8, by every row of the step.
+ * Scores, softmax statistics and sums are float32; before they multiply V the weights
+ * are rounded to fp16 (11 bits down to 2^-26 of the row's largest product of a weight
+ * and a block's value scale, fewer below, nothing from 2^-37 on), the open block's to
+ * 16 bits. The sums hold values up to 2^100 in magnitude.
  * workspace: gsdpa_cache8_workspace_bytes(...) bytes, 256-byte aligned; calls that
  * share one must not overlap on the device. Asynchronous on `stream`; other errors
  * as for gated_sdpa_fwd.

@@ -526,6 +526,10 @@ class Rope:
     rotary_dim / 2 of the caller's own. attn_scale multiplies cosine and sine
     (None: 1, or 0.1 ln(factor) + 1 with "parts")."""
 
+    # (``ref``, the plan's address as the calls take it, belongs to one object: a copy's is its own)
+    def __reduce__(self):
+        return _rope_of, (bytes(self.plan),)
+
     def __init__(self, rotary_dim, *, layout="half", theta=10000.0, scaling="none", factor=1.0, orig_len=0,
                  beta_fast=32.0, beta_slow=1.0, attn_scale=None, inv_freq=None):
         self.plan = _RopePlan()
@@ -545,6 +549,16 @@ class Rope:
             where = "gsdpa_rope_init"
         if st != OK:
             raise GsdpaError(int(st), where)
+
+
+def _rope_of(plan):
+    """A Rope of the bytes of another's plan (copies, and pickles of this version of the library)."""
+    if len(plan) != ctypes.sizeof(_RopePlan):
+        raise ValueError(f"a Rope's plan has {ctypes.sizeof(_RopePlan)} bytes, not {len(plan)}")
+    r = Rope.__new__(Rope)
+    r.plan = _RopePlan.from_buffer_copy(plan)
+    r.ref = ctypes.addressof(r.plan)
+    return r
 
 
 # (The calls below run once per layer and token in a decoding loop, on kernels of
@@ -778,6 +792,10 @@ class Cache8:
                                 k_scale.data_ptr(), v_scale.data_ptr(), k_tail.data_ptr(), v_tail.data_ptr())
         self.ref = ctypes.addressof(self.plan)
         self.need = {}   # workspace bytes, by the problem's shape
+
+    # A copy is a cache over its own tensors: the plan's addresses are made anew.
+    def __reduce__(self):
+        return Cache8, (self.k8, self.v8, self.k_scale, self.v_scale, self.k_tail, self.v_tail)
 
 
 def cache8_alloc(B, capacity, H_kv, d_k, kind="int8", device="cuda") -> Cache8:

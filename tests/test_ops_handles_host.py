@@ -1,0 +1,59 @@
+"""The handles of the operators around the attention on the host: copies and pickles of
+the rotary plan, of a cache's description."""
+import copy
+import ctypes
+import pickle
+
+import pytest
+import torch
+
+from gated_softmax_attention_gb300 import binding as gb
+from gated_softmax_attention_gb300 import build as gbuild
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    gbuild.build()
+    return gb.load()
+
+
+@pytest.mark.parametrize("how", [copy.copy, copy.deepcopy, lambda r: pickle.loads(pickle.dumps(r))], ids=["copy", "deepcopy", "pickle"])
+def test_a_copied_rope_points_to_its_own_plan(how):
+    rope = gb.Rope(64, layout="interleaved", scaling="parts", factor=8.0, orig_len=4096)
+    bits = bytes(rope.plan)
+    other = how(rope)
+    assert other.ref == ctypes.addressof(other.plan)
+    assert other.plan is not rope.plan and other.ref != rope.ref
+    del rope
+    assert bytes(other.plan) == bits
+    # as part of a model, twice: still one plan
+    a, b = how([other, other])
+    assert bytes(a.plan) == bits and a.ref == ctypes.addressof(a.plan) and a is b
+
+
+def test_a_plan_of_another_size_is_refused():
+    with pytest.raises(ValueError, match="bytes"):
+        gb._rope_of(b"\0" * 8)
+
+
+class _Tensors(gb.Cache8):
+    """A Cache8 over host tensors, for the copies alone (no call takes it)."""
+
+    def __init__(self, *tensors):
+        self.k8, self.v8, self.k_scale, self.v_scale, self.k_tail, self.v_tail = tensors
+        self.plan = gb._Cache8Plan(0, 1, 1, 64, 64, *(t.data_ptr() for t in tensors))
+        self.ref = ctypes.addressof(self.plan)
+
+
+def test_a_copied_cache_is_made_of_its_own_tensors(monkeypatch):
+    monkeypatch.setattr(gb, "Cache8", _Tensors)
+    c = _Tensors(*(torch.full((4,), float(k)) for k in range(6)))
+    for other in (copy.deepcopy(c), pickle.loads(pickle.dumps([t for t in c.__reduce__()[1]]))):
+        ts = other if isinstance(other, list) else [getattr(other, n) for n in ("k8", "v8", "k_scale", "v_scale", "k_tail", "v_tail")]
+        for k, t in enumerate(ts):
+            assert torch.equal(t, torch.full((4,), float(k)))
+            assert t.data_ptr() != (c.k8, c.v8, c.k_scale, c.v_scale, c.k_tail, c.v_tail)[k].data_ptr()
+        if other is not ts:
+            assert other.ref == ctypes.addressof(other.plan) and other.plan.k8 == other.k8.data_ptr()
+    same = copy.copy(c)      # a second handle over the same tensors
+    assert same.k8 is c.k8 and same.ref == ctypes.addressof(same.plan) != c.ref and same.plan.k8 == c.k8.data_ptr()

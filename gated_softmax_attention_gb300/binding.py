@@ -605,22 +605,28 @@ def _current_stream(device):
     return torch._C._cuda_getCurrentRawStream(index)
 
 
-_kept = {}
+class _Kept(threading.local):
+    def __init__(self):
+        self.by_stream = {}     # workspaces, by (device index, stream handle)
+
+
+_kept = _Kept()
 
 
 def _kept_workspace(need, device, stream):
-    """A workspace for a call on this stream. One is kept for each stream, whose
-    calls follow one another; a captured call gets one of its own, which its graph
-    keeps (replays may run beside anything)."""
+    """A workspace for a call on this stream. Each thread keeps one for each stream
+    that it calls on: its calls there follow one another, while the kernels of two
+    threads' calls may take turns. A captured call gets one of its own, which its
+    graph keeps (replays may run beside anything)."""
     import torch
     if need == 0:
         return None
     if torch.cuda.is_current_stream_capturing():
         return torch.empty(need, dtype=torch.uint8, device=device)
     key = (device.index, stream)
-    held = _kept.get(key)
+    held = _kept.by_stream.get(key)
     if held is None or held.numel() < need:
-        held = _kept[key] = torch.empty(need, dtype=torch.uint8, device=device)
+        held = _kept.by_stream[key] = torch.empty(need, dtype=torch.uint8, device=device)
     return held
 
 

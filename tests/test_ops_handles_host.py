@@ -57,3 +57,32 @@ def test_a_copied_cache_is_made_of_its_own_tensors(monkeypatch):
             assert other.ref == ctypes.addressof(other.plan) and other.plan.k8 == other.k8.data_ptr()
     same = copy.copy(c)      # a second handle over the same tensors
     assert same.k8 is c.k8 and same.ref == ctypes.addressof(same.plan) != c.ref and same.plan.k8 == c.k8.data_ptr()
+
+
+# ---------------------------------------------------------------- kept workspaces
+@pytest.fixture
+def on_the_host(monkeypatch):
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    return torch.device("cpu")
+
+
+def in_a_thread(f):
+    import threading
+    out = []
+    t = threading.Thread(target=lambda: out.append(f()))
+    t.start()
+    t.join()
+    return out[0]
+
+
+def test_two_threads_on_one_stream_do_not_share_a_workspace(on_the_host):
+    # a call is several kernels, and the library is called without the interpreter's lock: on one stream
+    # another thread's kernels may come between them
+    mine = gb._kept_workspace(256, on_the_host, 11)
+    assert gb._kept_workspace(200, on_the_host, 11) is mine          # the next call of this thread
+    assert gb._kept_workspace(256, on_the_host, 12) is not mine      # another stream
+    other = in_a_thread(lambda: gb._kept_workspace(256, on_the_host, 11))
+    assert other.data_ptr() != mine.data_ptr()
+    assert gb._kept_workspace(256, on_the_host, 11) is mine
+    assert gb._kept_workspace(512, on_the_host, 11).numel() == 512   # a larger one takes its place
+    assert gb._kept_workspace(0, on_the_host, 11) is None

@@ -617,7 +617,8 @@ def _kept_workspace(need, device, stream):
     """A workspace for a call on this stream. Each thread keeps one for each stream
     that it calls on: its calls there follow one another, while the kernels of two
     threads' calls may take turns. A captured call gets one of its own, which its
-    graph keeps (replays may run beside anything)."""
+    graph keeps (replays may run beside anything). release_workspaces() lets the
+    thread's go, as the thread's end does."""
     import torch
     if need == 0:
         return None
@@ -628,6 +629,14 @@ def _kept_workspace(need, device, stream):
     if held is None or held.numel() < need:
         held = _kept.by_stream[key] = torch.empty(need, dtype=torch.uint8, device=device)
     return held
+
+
+def release_workspaces() -> None:
+    """Lets go of the workspaces that qk_norm_rope_bwd and gated_sdpa_cache8 keep for
+    this thread, one for each stream it has called them on, of the largest size
+    they needed there. The memory goes back to torch's allocator; calls that are
+    still running are not disturbed, and the next ones allocate anew."""
+    _kept.by_stream.clear()
 
 
 def _on_stream(call):

@@ -86,3 +86,16 @@ def test_two_threads_on_one_stream_do_not_share_a_workspace(on_the_host):
     assert gb._kept_workspace(256, on_the_host, 11) is mine
     assert gb._kept_workspace(512, on_the_host, 11).numel() == 512   # a larger one takes its place
     assert gb._kept_workspace(0, on_the_host, 11) is None
+
+
+def test_kept_workspaces_are_released(on_the_host):
+    import weakref
+    ref = weakref.ref(gb._kept_workspace(256, on_the_host, 21))
+    assert ref() is not None
+    in_a_thread(gb.release_workspaces)                                # another thread's: not this one's
+    assert gb._kept_workspace(256, on_the_host, 21) is ref()
+    gb.release_workspaces()
+    assert ref() is None
+    gone = in_a_thread(lambda: weakref.ref(gb._kept_workspace(256, on_the_host, 21)))
+    assert gone() is None                                             # a thread's end is as good
+    assert gb._kept_workspace(64, on_the_host, 21).numel() == 64

@@ -15,10 +15,12 @@
 
 namespace gsdpa {
 
-// Set by a kernel's bounded wait when it runs out, or by a length outside its
-// cache (ERR_CACHE_RANGE); read and cleared by
-// gsdpa_check_device_error().
+// Bits set by a kernel's bounded wait when it runs out, or by a length outside its
+// cache (ERR_CACHE_RANGE); gsdpa_check_device_error() reports and clears one at a time.
 __device__ uint32_t g_error_word;
+
+// (atomic: kernels on other streams may be setting bits)
+__global__ void clear_error_kernel(uint32_t bits) { atomicAnd(&g_error_word, ~bits); }
 
 namespace {
 
@@ -708,12 +710,12 @@ int gsdpa_check_device_error(void* stream) {
     if (cudaStreamSynchronize(s) != cudaSuccess) return GSDPA_ERR_LAUNCH;
     uint32_t v = 0;
     if (cudaMemcpyFromSymbol(&v, g_error_word, sizeof(v)) != cudaSuccess) return GSDPA_ERR_LAUNCH;
-    if (v != 0) {
-        const uint32_t zero = 0;
-        cudaMemcpyToSymbol(g_error_word, &zero, sizeof(zero));
-        return (v & ERR_WAIT_TIMEOUT) ? GSDPA_ERR_DEVICE_TIMEOUT : GSDPA_ERR_CACHE_RANGE;
-    }
-    return GSDPA_OK;
+    if (v == 0) return GSDPA_OK;
+    const bool timeout = (v & ERR_WAIT_TIMEOUT) != 0;   // (a length error beside it is the next call's answer)
+    // (on the stream of the copy above, which is the current device's)
+    clear_error_kernel<<<1, 1>>>(timeout ? ERR_WAIT_TIMEOUT : ~ERR_WAIT_TIMEOUT);
+    if (cudaGetLastError() != cudaSuccess || cudaStreamSynchronize(nullptr) != cudaSuccess) return GSDPA_ERR_LAUNCH;
+    return timeout ? GSDPA_ERR_DEVICE_TIMEOUT : GSDPA_ERR_CACHE_RANGE;
 }
 
 const char* gsdpa_status_string(int status) {

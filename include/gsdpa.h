@@ -516,7 +516,8 @@ GSDPA_API int gated_sdpa_cache8(const void* X, const void* Q, const gsdpa_cache8
  * Synchronises `stream`, then reads and clears the device error word that
  * bounded waits inside the kernels set when they run out, and the 8-bit
  * cache's kernels when a sequence's length or token count does not fit its
- * cache. Returns GSDPA_OK, GSDPA_ERR_DEVICE_TIMEOUT, GSDPA_ERR_CACHE_RANGE, or
+ * cache. Returns GSDPA_OK, GSDPA_ERR_DEVICE_TIMEOUT, GSDPA_ERR_CACHE_RANGE (where
+ * both have occurred the timeout, and the range error from the next call), or
  * GSDPA_ERR_LAUNCH if the stream itself reports a CUDA error.
  */
 GSDPA_API int gsdpa_check_device_error(void* stream);

@@ -71,3 +71,21 @@ def test_two_threads_on_one_stream():
     for t in threads:
         t.join()
     assert wrong == [0, 0]
+
+
+def test_a_timeout_and_a_length_out_of_range_are_both_reported():
+    cache = filled_cache([64], 1, 64, "int8", 1)
+    K = randn(2, 1, 1, 1, 64)
+    for first in (0, 1):
+        for step in (first, 1 - first):
+            if step:
+                gb.cache8_append(cache, K, K, ints(64))
+            else:
+                gb.set_wait_limit_ns(200_000)
+                try:
+                    assert gb.wait_self_test() == gb.OK      # a wait that nothing completes
+                finally:
+                    gb.set_wait_limit_ns(0)
+        assert [gb.check_device_error() for _ in range(3)] == [gb.ERR_DEVICE_TIMEOUT, gb.ERR_CACHE_RANGE, gb.OK]
+    gb.cache8_append(cache, K, K, ints(-1))
+    assert [gb.check_device_error() for _ in range(2)] == [gb.ERR_CACHE_RANGE, gb.OK]

@@ -89,3 +89,106 @@ def test_a_timeout_and_a_length_out_of_range_are_both_reported():
         assert [gb.check_device_error() for _ in range(3)] == [gb.ERR_DEVICE_TIMEOUT, gb.ERR_CACHE_RANGE, gb.OK]
     gb.cache8_append(cache, K, K, ints(-1))
     assert [gb.check_device_error() for _ in range(2)] == [gb.ERR_CACHE_RANGE, gb.OK]
+
+
+# ---------------------------------------------------------------- the attention to the kernel's own bound
+def check(O, X, Q, cache, W, gate, lens, new, sequences=None):
+    """Every row against the formula in 64 bits. With A the sum of weights times |v| over full blocks and A' over the
+    open one, the output is off by at most 2^-11 A (weights rounded to fp16) + 2^-17 A' (two bf16 parts) + 2^-37 of
+    the largest product of a weight and a value scale for each unit of a code (fp16's range) + twice the scores'
+    error (d additions of 2^-23) and 2^-13 (additions of the weights, exponentials, the gate's sigmoid) of A + A';
+    then it is rounded to bf16."""
+    B, Lq, Hq, d = Q.shape
+    H, G = cache.H_kv, Hq // cache.H_kv
+    for b in range(B) if sequences is None else sequences:
+        T, n = lens[b] + new[b], new[b]
+        assert not bool(O[b, n:].any()), f"rows past n_new of sequence {b} are not zero"
+        if n == 0:
+            continue
+        full, rest = T // 64, T % 64
+        sig = torch.ones(n, Hq, d, dtype=torch.float64, device="cuda")
+        if gate != "none":
+            s = torch.sigmoid(X[b, :n].double() @ W.double())
+            sig = s[..., None].expand(-1, -1, d) if gate == "headwise" else s.view(n, Hq, d)
+        codes = cache.v8[b, :, :full].double().transpose(-1, -2).reshape(H, -1, d)
+        scale = cache.v_scale[b, :, :full].double()
+        k = (cache.k8[b, :, :full].double() * cache.k_scale[b, :, :full, None, None].double()).reshape(H, -1, d)
+        k = torch.cat((k, cache.k_tail[b, :, full % 2, :rest].double()), 1)
+        v = torch.cat((codes * scale.repeat_interleave(64, 1)[..., None],
+                       cache.v_tail[b, :, full % 2, :, :rest].double().transpose(-1, -2)), 1)
+        q = Q[b, :n].double().view(n, H, G, d).permute(1, 0, 2, 3).reshape(H, n * G, d)
+        seen = torch.arange(T, device="cuda") <= lens[b] + torch.arange(n, device="cuda").repeat_interleave(G)[:, None]
+        score = (q @ k.transpose(1, 2) / math.sqrt(d)).masked_fill(~seen, -math.inf)
+        top = (q.abs() @ k.abs().transpose(1, 2)).masked_fill(~seen, 0).amax(-1, keepdim=True) / math.sqrt(d)
+        w = torch.softmax(score, -1)
+        ref = w @ v
+        closed, opened = w[..., :64 * full] @ v[:, :64 * full].abs(), w[..., 64 * full:] @ v[:, 64 * full:].abs()
+        tol = (2.0 ** -11 * closed + 2.0 ** -17 * opened + (2 * d * 2.0 ** -23 * top + 2.0 ** -13) * (closed + opened))
+        if full:
+            tol = tol + 2.0 ** -37 * w.amax(-1, keepdim=True) * scale.amax(1)[:, None, None] * codes.abs().sum(1)[:, None]
+
+        def rows(t):
+            return t.view(H, n, G, d).permute(1, 0, 2, 3).reshape(n, Hq, d) * sig
+        ref, tol = rows(ref), rows(tol) + 2.0 ** -8 * rows(ref).abs() + 1e-30
+        err = (O[b, :n].double() - ref).abs()
+        assert bool((err <= tol).all()), (b, T, float((err / tol).max()))
+
+
+def run(cache, lens, new, G, Lq, gate, seed, sequences=None):
+    B, H, d = len(lens), cache.H_kv, cache.d_k
+    Q = randn(seed, B, Lq, H * G, d)
+    X = W = None
+    if gate != "none":
+        X, W = randn(seed + 1, B, Lq, 256), randn(seed + 2, 256, H * G * (1 if gate == "headwise" else d)) / 16
+    n = None if new == [Lq] * B else ints(*new)
+    O = gb.gated_sdpa_cache8(X, Q, cache, ints(*lens), W, gate=gate, n_new=n)
+    check(O, X, Q, cache, W, gate, lens, new, sequences)
+    return O
+
+
+@pytest.mark.parametrize("kind,gate", [("int8", "none"), ("e4m3", "headwise"), ("int8", "elementwise")])
+@pytest.mark.parametrize("d,H,G,Lq", [(128, 2, 4, 1), (64, 1, 8, 1), (128, 8, 3, 5), (64, 2, 8, 4), (128, 1, 16, 8), (64, 1, 1, 70)])
+@pytest.mark.parametrize("T", [64, 960, 3000])
+def test_attention_to_its_bound(T, d, H, G, Lq, kind, gate):
+    # full blocks alone, and an open block beside them, for each number of query rows
+    if gate == "headwise" and H * G % 8:
+        gate = "elementwise"
+    T = max(T, 128 if Lq > 64 else T)
+    lens_after, new = [T, T + 37, T - 5], [Lq, Lq, Lq // 2]
+    cache = filled_cache(lens_after, H, d, kind, 3)
+    run(cache, [a - n for a, n in zip(lens_after, new)], new, G, Lq, gate, 5)
+
+
+@pytest.mark.parametrize("gate", ["none", "headwise"])
+@pytest.mark.parametrize("G,Lq", [(4, 1), (16, 1), (8, 4), (8, 8), (32, 4)])
+@pytest.mark.parametrize("T", [1, 63, 127, 128, 129, 255, 256, 257, 511, 512, 513, 1024])
+def test_short_sequences_in_a_long_cache(T, G, Lq, gate):
+    # a head is one block of threads' where all have at most a tile for each of its teams (8, 4, 2 or 1 by the
+    # number of query rows): lengths on both sides, in a cache for far more, an empty sequence beside them
+    if T < Lq:
+        Lq = 1
+    lens_after, new = [T, 0, max(T - 7, 0)], [Lq, 0, min(Lq, max(T - 7, 0))]
+    cache = filled_cache(lens_after, 2, 128, "int8", 6, capacity=64 * 1024)
+    run(cache, [a - n for a, n in zip(lens_after, new)], new, G, Lq, gate, 7)
+
+
+@pytest.mark.parametrize("kind", ["int8", "e4m3"])
+@pytest.mark.parametrize("G,Lq,blocks", [(4, 1, 24), (4, 1, 25), (12, 1, 24), (12, 1, 25), (8, 4, 12), (8, 4, 13), (8, 8, 6), (8, 8, 7),
+                                         (32, 4, 3), (32, 4, 4)])
+def test_capacities_that_choose_one_launch_or_two(kind, G, Lq, blocks):
+    # three tiles for each team of a head's one block of threads, by the capacity: full, almost, and nearly empty
+    T = 64 * blocks
+    for lens_after in ([T, T - 1], [T - 64, 65], [9, 200]):
+        lens_after = [min(x, T) for x in lens_after]
+        cache = filled_cache(lens_after, 2, 64, kind, 8, capacity=T)
+        new = [min(Lq, x) for x in lens_after]
+        run(cache, [a - n for a, n in zip(lens_after, new)], new, G, Lq, "none", 9)
+
+
+def test_many_short_sequences_by_the_length_and_by_the_place():
+    # as many heads as there are blocks of threads and one more (152 multiprocessors): from there on heads are not
+    # one block's each, whatever their length
+    for B in (75, 76, 77, 80):
+        lens_after = [1 + 37 * b % 500 for b in range(B)]
+        cache = filled_cache(lens_after, 2, 64, "e4m3", 10, capacity=8192)
+        run(cache, [n - 1 for n in lens_after], [1] * B, 4, 1, "none", 11)

@@ -74,3 +74,16 @@ def test_gate_logits_give_up_cleanly(gate, dm):
     for _ in range(10):
         assert with_a_tiny_limit(call) in (gb.OK, gb.ERR_DEVICE_TIMEOUT)
         assert torch.equal(call(), want) and gb.check_device_error() == gb.OK
+
+
+def test_a_share_longer_than_its_ring_reports_the_timeout():
+    # the copying warp finds its rings full until the first tiles have been used: with 1 ns it does not wait that long
+    lens, H, Hq, d = [32768] * 8, 8, 32, 128
+    cache = filled_cache(lens, H, d, "int8", 7)
+    Q = torch.randn(8, 1, Hq, d, generator=torch.Generator(device="cuda").manual_seed(8), device="cuda").bfloat16()
+    at = torch.tensor([n - 1 for n in lens], dtype=torch.int32, device="cuda")
+    call = lambda: gb.gated_sdpa_cache8(None, Q, cache, at, gate="none")  # noqa: E731
+    want = call()
+    for _ in range(5):
+        assert with_a_tiny_limit(call) == gb.ERR_DEVICE_TIMEOUT
+        assert torch.equal(call(), want) and gb.check_device_error() == gb.OK

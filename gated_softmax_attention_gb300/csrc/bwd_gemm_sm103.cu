@@ -236,6 +236,7 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     }
 
     __syncthreads();
+    let_land_after_abort(ab.local);
     pair::cluster_sync();
     if (warp == 1) {
         tc_fence_after();

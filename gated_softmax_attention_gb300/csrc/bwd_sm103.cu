@@ -418,6 +418,7 @@ gemm_bf16_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         tc_fence_before();
     }
     __syncthreads();
+    let_land_after_abort(abort_flag);
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem, 128);
@@ -752,6 +753,7 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
         tc_fence_before();
     }
     __syncthreads();
+    let_land_after_abort(abort_flag);
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
@@ -1057,6 +1059,7 @@ bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         tc_fence_before();
     }
     __syncthreads();
+    let_land_after_abort(abort_flag);
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);

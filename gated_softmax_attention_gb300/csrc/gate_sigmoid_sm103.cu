@@ -362,6 +362,7 @@ gate_sigmoid_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_consta
     }
 
     __syncthreads();
+    let_land_after_abort(ab.local);
     pair::cluster_sync();
     if (warp == 1) {
         tc_fence_after();

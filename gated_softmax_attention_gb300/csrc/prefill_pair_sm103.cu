@@ -271,13 +271,6 @@ prefill_pair_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
             ok = load(-1, 0, U.nkv > 1 ? 1 : -1);
             for (int j = 0; j < U.nkv && ok; ++j) ok = load(j, -1, j + 2 < U.nkv ? j + 2 : -1);
             }   // units
-            if (!ok) {
-                // Gave up: the other CTA stops too (both abort flags are raised);
-                // give copies already issued time to land before the CTA exits.
-                const unsigned long long t0 = globaltimer_ns();
-                while (globaltimer_ns() - t0 < 200000ull) {
-                }
-            }
         }
     } else if (warp == 1) {
         // ================================================================ MMA issuer (even CTA)
@@ -647,6 +640,7 @@ prefill_pair_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
     }
 
     __syncthreads();
+    let_land_after_abort(ab.local);
     pair::cluster_sync();   // no CTA leaves while the other may still reach its memory
     if (warp == 1) {
         tc_fence_after();

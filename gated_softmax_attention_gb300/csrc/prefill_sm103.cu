@@ -662,6 +662,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
     }
 
     __syncthreads();
+    let_land_after_abort(abort_flag);
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);

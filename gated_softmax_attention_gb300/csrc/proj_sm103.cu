@@ -300,6 +300,7 @@ pair_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
     }
 
     __syncthreads();
+    let_land_after_abort(ab.local);
     pair::cluster_sync();
     if (warp == 1) {
         tc_fence_after();

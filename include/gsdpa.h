@@ -474,8 +474,11 @@ typedef struct {
  *         to nearest, ties to even.
  * amax = 0: scale and codes 0. A block that holds a NaN or an infinity: scale NaN,
  * codes 0 (every row that sees one of its tokens becomes NaN). Each token is rounded
- * once: the contents do not depend on how tokens were split over calls. Up to 64
- * tokens may be taken back (drafts that were not accepted) by lowering lens.
+ * once: the contents do not depend on how tokens were split over calls. Tokens may be
+ * taken back (drafts that were not accepted) by lowering lens, repeatedly, to no less
+ * than 64 below the longest length that the sequence has had since the tokens that stay
+ * were appended: further back the open block's tokens have been written over, which no
+ * call can see.
  * A sequence with lens[b] < 0, n_new[b] outside 0 .. L or more tokens than capacity
  * is left as it was, and the next gsdpa_check_device_error returns
  * GSDPA_ERR_CACHE_RANGE. Asynchronous on `stream`; sm_103 device.

@@ -9,6 +9,7 @@ import torch
 
 from gated_softmax_attention_gb300 import binding as gb
 from gated_softmax_attention_gb300 import build as gbuild
+from ops_ref import cache_rows
 
 pytestmark = pytest.mark.gpu
 
@@ -192,3 +193,30 @@ def test_many_short_sequences_by_the_length_and_by_the_place():
         lens_after = [1 + 37 * b % 500 for b in range(B)]
         cache = filled_cache(lens_after, 2, 64, "e4m3", 10, capacity=8192)
         run(cache, [n - 1 for n in lens_after], [1] * B, 4, 1, "none", 11)
+
+
+@pytest.mark.parametrize("kind", ["int8", "e4m3"])
+def test_drafts_taken_back_again_and_again(kind):
+    # steps of up to 90 tokens, and lengths taken back by anything that stays within 64 of the longest so far: the
+    # cache is that of the tokens that were kept, appended at once
+    H, d, cap = 2, 64, 1024
+    g = torch.Generator().manual_seed(13)
+
+    def pick(lo, hi):
+        return int(torch.randint(lo, hi + 1, (1,), generator=g))
+    for seed in range(6):
+        cache, longest = gb.cache8_alloc(1, cap, H, d, kind), 0
+        k = v = torch.zeros(1, 0, H, d, device="cuda", dtype=torch.bfloat16)
+        for step in range(40):
+            n = min(pick(1, 90) if step % 3 == 0 else pick(1, 6), cap - k.shape[1])
+            new = [randn(100 * step + 10 * seed + i, 1, n, H, d) for i in range(2)]
+            gb.cache8_append(cache, *new, ints(k.shape[1]))
+            k, v = torch.cat((k, new[0]), 1), torch.cat((v, new[1]), 1)
+            longest = max(longest, k.shape[1])
+            T = pick(max(longest - 64, 0), k.shape[1]) if longest < cap - 90 else k.shape[1]
+            k, v = k[:, :T], v[:, :T]
+            want = gb.cache8_alloc(1, cap, H, d, kind)
+            gb.cache8_append(want, k.contiguous(), v.contiguous(), ints(0))
+            for h in range(H):
+                for x, y in zip(cache_rows(cache, 0, h, T), cache_rows(want, 0, h, T)):
+                    assert torch.equal(x, y), (seed, step, T, longest)

@@ -25,7 +25,7 @@
 // position 10^6, and FP64 arithmetic is slow here. The frequency is kept as a
 // 64-bit fraction of a whole turn per position instead; the low 64 bits of
 // position * fraction are the angle modulo one turn, exact but for the
-// fraction's own rounding (position * 2^-54 turns), and its upper 32 bits go
+// fraction's own rounding (position * 2^-63 turns), and its upper 32 bits go
 // to sincospif for float32, to the hardware's sine and cosine (2^-20.9
 // absolute) for bf16, which rounds at 2^-9. Everything after that is float32, rounded
 // once at the store.
@@ -632,6 +632,14 @@ cudaError_t launch_dgamma(const float* part, int parts, int dk, void* dgq, void*
                             static_cast<T*>(dgk));
 }
 
+constexpr double kTwoPi = 6.283185307179586, kTwoPiRest = 2.4492935982947064e-16;
+
+// Turns modulo one, times 2^64: positions are whole numbers, so whole turns drop out.
+unsigned long long part_of_turn(double turns) {
+    const double scaled = std::ldexp(turns - std::rint(turns), 64);   // (the difference is exact)
+    return scaled >= 9223372036854775808.0 ? 1ull << 63 : (unsigned long long)(long long)std::rint(scaled);
+}
+
 }  // namespace
 }  // namespace gsdpa
 
@@ -652,11 +660,9 @@ int gsdpa_rope_init_freqs(gsdpa_rope* rope, int rotary_dim, int layout, const do
     rope->reserved = 0;
     for (int i = 0; i < kMaxPairs; ++i) rope->turn[i] = 0;
     for (int i = 0; i < rotary_dim / 2; ++i) {
-        // turns per position; positions are whole numbers, so whole turns drop out
-        double t = inv_freq[i] / 6.283185307179586;
-        t -= std::floor(t);
-        const double scaled = std::floor(std::ldexp(t, 64) + 0.5);
-        rope->turn[i] = scaled >= 18446744073709551616.0 ? 0ull : (unsigned long long)scaled;
+        // turns per position, as a double and the rest of the quotient (2 pi in two doubles)
+        const double q = inv_freq[i] / kTwoPi, rest = (std::fma(-q, kTwoPi, inv_freq[i]) - q * kTwoPiRest) / kTwoPi;
+        rope->turn[i] = part_of_turn(q) + part_of_turn(rest);
     }
     return GSDPA_OK;
 }
@@ -672,9 +678,9 @@ int gsdpa_rope_init(gsdpa_rope* rope, int rotary_dim, int layout, double theta, 
     if (scaling == GSDPA_ROPE_PARTS) {
         if (!(orig_len >= 1.0 && std::isfinite(orig_len))) return GSDPA_ERR_INVALID_ARG;
         if (!(beta_slow > 0.0 && beta_fast >= beta_slow && std::isfinite(beta_fast))) return GSDPA_ERR_INVALID_ARG;
-        const double turn = 6.283185307179586, k = 2.0 * std::log(theta);
-        lo = std::floor(rd * std::log(orig_len / (beta_fast * turn)) / k);
-        hi = std::ceil(rd * std::log(orig_len / (beta_slow * turn)) / k);
+        const double k = 2.0 * std::log(theta);
+        lo = std::floor(rd * std::log(orig_len / (beta_fast * kTwoPi)) / k);
+        hi = std::ceil(rd * std::log(orig_len / (beta_slow * kTwoPi)) / k);
         lo = lo < 0.0 ? 0.0 : lo;
         hi = hi > rd - 1.0 ? rd - 1.0 : hi;
     }

@@ -351,7 +351,8 @@ GSDPA_API int gated_sdpa_bwd_saved_gate(const void* X, const void* Q, const void
  * with (a, b) = (i, i + rotary_dim / 2) (half layout) or (2i, 2i + 1)
  * (interleaved), w_i the pair's frequency and t = attn_scale; the columns from
  * rotary_dim on are not rotated. Everything in float32, rounded once; the angle
- * p w_i is exact to about |p| 2^-52 rad for every 32-bit position.
+ * p w_i is that of the float64 frequency to |p| 2^-59 rad, modulo a turn, for every
+ * 32-bit position (before it is rounded to float32).
  *
  * gsdpa_rope is the plan, made once on the host by one of the two init
  * functions and passed to every call (its contents are copied at the call).

@@ -99,3 +99,28 @@ def test_kept_workspaces_are_released(on_the_host):
     gone = in_a_thread(lambda: weakref.ref(gb._kept_workspace(256, on_the_host, 21)))
     assert gone() is None                                             # a thread's end is as good
     assert gb._kept_workspace(64, on_the_host, 21).numel() == 64
+
+
+# ---------------------------------------------------------------- the rotary plan's angles
+def two_pi(bits):
+    """2 pi as an integer, times 2^bits (Machin's formula: pi = 16 atan(1/5) - 4 atan(1/239))."""
+    def atan_inverse(n):
+        term = (1 << bits + 32) // n
+        total, k, sign = term, 1, 1
+        while term:
+            term //= n * n
+            k, sign = k + 2, -sign
+            total += sign * (term // k)
+        return total
+    return 2 * (16 * atan_inverse(5) - 4 * atan_inverse(239)) >> 32
+
+
+@pytest.mark.parametrize("w", [1.0, 0.75, 2.0 ** -40, -2.0 ** -40, 1e-9, -0.25, 7.0, -1000.5, 12345.678, 3e8, -2.5e15, 1e300, 0.0])
+def test_frequencies_of_any_size_keep_their_angle(w):
+    # turns per position modulo one, to the 64 bits that are kept: an angle at any 32-bit position is then off by
+    # |p| 2^-62 turns at most
+    from fractions import Fraction
+    rope = gb.Rope(16, inv_freq=[w] * 8)
+    want = Fraction(w) / Fraction(two_pi(1400), 1 << 1400)
+    off = (Fraction(rope.plan.turn[3], 1 << 64) - want) % 1
+    assert min(off, 1 - off) <= Fraction(1, 1 << 62) + abs(want) / (1 << 100)

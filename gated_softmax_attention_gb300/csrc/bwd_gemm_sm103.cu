@@ -28,6 +28,7 @@
 // soon as its four warps have staged it. Rows and columns past the end of C
 // and the K tail load as zeros (TMA out-of-bounds fill) and are not stored.
 #include "gsdpa_internal.h"
+#include "landing.cuh"
 #include "proj_internal.h"
 #include "sm103_pair.cuh"
 #include "sm103_ptx.cuh"

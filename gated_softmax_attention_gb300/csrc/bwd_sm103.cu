@@ -49,6 +49,7 @@
 // CTAs leave free, and the last CTA of each waits for its predecessor before
 // it exits, so that the call completes after all of them.
 #include "gsdpa_internal.h"
+#include "landing.cuh"
 #include "proj_internal.h"
 #include "sm103_ptx.cuh"
 

@@ -26,6 +26,7 @@
 // tensor-map operand (its rows are 2 bytes apart): gate_rowdot_kernel, one
 // warp per row, 16-byte loads of X and W_g.
 #include "gsdpa_internal.h"
+#include "landing.cuh"
 #include "sm103_ptx.cuh"
 
 namespace gsdpa {

@@ -43,6 +43,7 @@
 // Rows past the end of X, columns past the end of W_g and the K tail load as
 // zeros (TMA out-of-bounds fill) and are not stored.
 #include "gsdpa_internal.h"
+#include "landing.cuh"
 #include "sm103_pair.cuh"
 #include "sm103_ptx.cuh"
 #include "gate_fn.cuh"

@@ -4,6 +4,7 @@
 #pragma once
 #include "gsdpa.h"
 #include "gsdpa_internal.h"
+#include "landing.cuh"
 #include "sm103_ptx.cuh"
 
 namespace gsdpa {

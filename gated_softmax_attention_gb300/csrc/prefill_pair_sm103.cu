@@ -64,6 +64,7 @@
 // numbered heaviest first: a longest-first greedy schedule) and hands it to
 // every role of both CTAs through a small ring in shared memory.
 #include "gsdpa_internal.h"
+#include "landing.cuh"
 #include "sm103_pair.cuh"
 #include "sm103_ptx.cuh"
 #include "gate_fn.cuh"

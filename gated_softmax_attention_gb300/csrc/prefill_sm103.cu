@@ -40,6 +40,7 @@
 // roles through a small ring in shared memory; barrier phases carry over
 // from one unit to the next.
 #include "gsdpa_internal.h"
+#include "landing.cuh"
 #include "sm103_ptx.cuh"
 #include "gate_fn.cuh"
 #include "proj_internal.h"

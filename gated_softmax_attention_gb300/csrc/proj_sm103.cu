@@ -36,6 +36,7 @@
 // past N and the K tail load as zeros (TMA out-of-bounds fill) and are not
 // stored.
 #include "gsdpa_internal.h"
+#include "landing.cuh"
 #include "proj_internal.h"
 #include "sm103_pair.cuh"
 #include "sm103_ptx.cuh"

@@ -67,6 +67,7 @@
 // 171 us (6.3 TB/s, 93 % of a plain copy); one of 131072 tokens, 16/2 heads 23 us;
 // 24 of up to 32767 tokens, 16/2 heads 48.5 us; one of 1000 tokens 11.5 us.
 #include "cache8_internal.h"
+#include "landing.cuh"
 
 #include <cuda_fp16.h>
 

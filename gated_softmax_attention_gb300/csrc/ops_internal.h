@@ -4,7 +4,6 @@
 #pragma once
 #include "gsdpa.h"
 #include "gsdpa_internal.h"
-#include "landing.cuh"
 #include "sm103_ptx.cuh"
 
 namespace gsdpa {

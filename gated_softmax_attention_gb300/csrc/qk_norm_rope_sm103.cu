@@ -33,6 +33,7 @@
 // Measured: 32/4 heads of 128, 4096 tokens 12.6 us (6.0 TB/s, 88 % of a plain copy),
 // one token of 64 sequences 1.9 us; backward, 16/2 heads, 32768 tokens 74 us (6.1
 // TB/s), 16/16 heads, 2 x 2048 tokens 22 us.
+#include "landing.cuh"
 #include "ops_internal.h"
 
 #include <cmath>

@@ -220,3 +220,49 @@ def test_drafts_taken_back_again_and_again(kind):
             for h in range(H):
                 for x, y in zip(cache_rows(cache, 0, h, T), cache_rows(want, 0, h, T)):
                     assert torch.equal(x, y), (seed, step, T, longest)
+
+
+@pytest.mark.parametrize("kind", ["int8", "e4m3"])
+def test_a_cache_of_more_than_32_bits_of_bytes(kind):
+    # 4.6 GB each of keys and values: the last sequences' blocks, scales, open blocks and rows lie past 2^32 bytes
+    B, H, d, cap = 1100, 8, 128, 4096
+    lens_after = [0] * B
+    for b, n in ((0, 130), (549, 64), (1097, 200), (1098, 1), (1099, 199)):
+        lens_after[b] = n
+    cache = gb.cache8_alloc(B, cap, H, d, kind)
+    assert cache.k8.numel() > 2 ** 32
+    K, V = randn(14, B, 200, H, d), randn(15, B, 200, H, d)
+    gb.cache8_append(cache, K, V, ints(*[0] * B), ints(*lens_after))
+    for b in (0, 1097, 1099):
+        want = gb.cache8_alloc(1, cap, H, d, kind)
+        gb.cache8_append(want, K[b:b + 1].contiguous(), V[b:b + 1].contiguous(), ints(0), ints(lens_after[b]))
+        for h in (0, H - 1):
+            for x, y in zip(cache_rows(cache, b, h, lens_after[b]), cache_rows(want, 0, h, lens_after[b])):
+                assert torch.equal(x, y)
+    new = [min(1, n) for n in lens_after]
+    run(cache, [n - m for n, m in zip(lens_after, new)], new, 4, 1, "headwise", 16, [0, 5, 549, 1096, 1097, 1098, 1099])
+    del cache, K, V
+    torch.cuda.empty_cache()
+
+
+def test_one_sequence_of_more_than_32_bits_of_bytes():
+    # one head, 2^26 tokens of 64 columns: 4.3 GB each; every key but a few is zero, so the weights are known
+    d, T = 64, 2 ** 26 + 64
+    cache = gb.cache8_alloc(1, T, 1, d, "int8")
+    for t in (cache.k8, cache.v8, cache.k_scale, cache.v_scale):
+        t.zero_()
+    cache.k_scale.fill_(1.0)
+    cache.v_scale.fill_(1.0)
+    last = T // 64 - 1
+    cache.k8[0, 0, last, 63, 0] = 100          # the last token: 100 q / sqrt(d) = 25 above the others, e^25 = 7.2e10
+    cache.v8[0, 0, last, :, 63] = 3
+    cache.v8[0, 0, 5, :, 7] = 1                # and one far from it, of weight e^-25
+    Q = torch.zeros(1, 1, 4, d, device="cuda", dtype=torch.bfloat16)
+    Q[..., 0] = 2.0
+    O = gb.gated_sdpa_cache8(None, Q, cache, ints(T - 1), gate="none")
+    w = 1 / (1 + (T - 1) * math.exp(-25.0))
+    assert float((O.double() - 3 * w).abs().max()) <= 2.0 ** -8 * 3
+    O = gb.gated_sdpa_cache8(None, Q, cache, ints(T - 65), gate="none")      # without the last block: even weights
+    assert float((O.double() * (T - 64) - 1).abs().max()) <= 2.0 ** -7
+    del cache
+    torch.cuda.empty_cache()

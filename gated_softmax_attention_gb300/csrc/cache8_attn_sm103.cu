@@ -67,19 +67,13 @@
 // 171 us (6.3 TB/s, 93 % of a plain copy); one of 131072 tokens, 16/2 heads 23 us;
 // 24 of up to 32767 tokens, 16/2 heads 48.5 us; one of 1000 tokens 11.5 us.
 #include "cache8_internal.h"
+#include "cache_attn.cuh"
 #include "landing.cuh"
-
-#include <cuda_fp16.h>
 
 namespace gsdpa {
 namespace {
 
-constexpr int kSlots = 8;            // most teams of a CTA, and warps that share no tokens
-constexpr int kMaxRows = 128;        // query rows (heads of a group x new tokens) per K/V head
 constexpr int kMaxStages = 16;       // ring stages per team
-constexpr int kMaxCtas = 160;        // most CTAs (plan_sms)
-constexpr int kMergeThreads = 512;
-constexpr int kBatch = 6;            // parts that a thread of a merge has under way
 // A head is one CTA's where all have at most this many tiles for each team of it and
 // there are CTAs for all: the teams then merge in shared memory. If the capacity says
 // so already, the merge kernel is not launched (1000 tokens, 8 teams: 11.5 us and 2.5
@@ -89,14 +83,15 @@ constexpr int kBatch = 6;            // parts that a thread of a merge has under
 constexpr int kWholeTiles = 3, kFewTiles = 1;
 constexpr int kBars = 48;            // ring stages of all teams
 constexpr uint32_t kSmemMax = 232448 - 1984;   // dynamic: what a CTA may have, less barriers, parts and a few words
-constexpr int kSwitch = 4;           // most places after a head without a tile
-constexpr int kScan = 128;           // places in the sequence of all tiles that are looked up
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kMove = 8.0f, kMoveOut = 2.0f;   // how far a tile may exceed m, and M, in log2 units
 constexpr float kUp = 13.0f;         // M stands 2^kUp below the largest product: 2^(kUp + kMoveOut) is in fp16's range
 constexpr float kApart = 100.0f;
 
+struct SeqTiles;
 struct Cache8Args {
+    using Seq = SeqTiles;
+    __device__ __forceinline__ long long token(int b, int i) const { return (long long)b * Lq + i; }
+    __device__ __forceinline__ long long tokens() const { return (long long)B * Lq; }
     const __nv_bfloat16* Q;          // [B, Lq, Hq, D]
     __nv_bfloat16* O;
     const int *lens, *n_new;
@@ -118,11 +113,6 @@ struct Cache8Args {
     WaitCtl ctl;
 };
 
-__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
 __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -170,31 +160,6 @@ __device__ __forceinline__ void pair_up(uint32_t& a, uint32_t& b) {
     }
 }
 
-// An 8 x 8 matrix of 16-bit elements, row g columns 2 t, 2 t + 1 in lane (g, t), transposed.
-__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
-    uint32_t r;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
-    return r;
-}
-
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-// 1 / (1 + e^-x), accurate to a few units of float32's last place.
-__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
-
-// Places of a head in the sequence of all tiles: after its tiles come some without
-// one. A team that goes on to another head stores what it has, reads other
-// queries and has, at a sequence's end, an open block of twice the bytes, which
-// even shares of the tiles alone do not show: of 1216 teams with 11 tiles each of
-// 24 sequences of up to 32767 tokens, the 48 that went on ended 5 us after the
-// others. (Measured with 2, 4, 6 and 8 places: that 52.2, 50.4, 50.9, 51.5 us, up
-// to 5000 tokens 19.3, 17.7, 17.5, 17.9; 64 x 200 tokens, heads of 4 tiles, 18.4,
-// 21.0, 20.3, 20.1.)
-__device__ __forceinline__ int span_of(int tiles) { return tiles + min(kSwitch, tiles / 2); }
-
 struct SeqTiles {
     int len, n, T, tiles;
     __device__ __forceinline__ SeqTiles(const Cache8Args& a, int b) {
@@ -206,62 +171,6 @@ struct SeqTiles {
     }
     __device__ __forceinline__ bool open(int j) const { return (j + 1) * kCacheBlock > T; }
     __device__ __forceinline__ int span() const { return span_of(tiles); }
-};
-
-// A place in the sequence of all tiles. (Where places are left a sequence with
-// tiles follows; lengths that change during the call, which they must not, end
-// the walk instead of leading it out of the batch.)
-struct Cursor {
-    int b, kvh, j, tiles;
-    int left;   // places of the share from here on
-    __device__ __forceinline__ void next_head(const Cache8Args& a) {
-        left -= span_of(tiles) - j;
-        j = 0;
-        if (left <= 0) return;
-        if (++kvh == a.Hkv) {
-            kvh = 0;
-            do {
-                if (++b >= a.B) {
-                    left = 0;
-                    return;
-                }
-                tiles = SeqTiles(a, b).tiles;
-            } while (tiles == 0);
-        }
-    }
-};
-
-// n things dealt to k takers in order, each as many as the next or one more:
-// where a taker's share begins, and whose share holds thing x.
-struct Deal {
-    int each, more;
-    __device__ __forceinline__ Deal(int n, int k) : each(n / k), more(n % k) {}
-    __device__ __forceinline__ int from(int c) const { return c * each + min(c, more); }
-    __device__ __forceinline__ int taker(int x) const {
-        const int fat = more * (each + 1);
-        return x < fat ? x / (each + 1) : more + (x - fat) / each;
-    }
-};
-
-// What a warp keeps of its 8 NT query rows; lane (g, t) has rows 8 n + 2 t + e.
-template <int D, int NT>
-struct RowState {
-    float o[NT][D / 16][4];   // element 2 x + e: column 16 i + 8 x + g of row 8 n + 2 t + e
-    float m[NT][2], l[NT][2], M[NT][2];
-    __device__ __forceinline__ void clear() {
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) o[n][i][e] = 0.f;
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                m[n][e] = M[n][e] = -INFINITY;
-                l[n][e] = 0.f;
-            }
-        }
-    }
 };
 
 // A value scale as frac 2^ev, frac in [1, 2) (0, NaN and infinity stay what they are).
@@ -399,63 +308,6 @@ __device__ __forceinline__ float row_to_f16(uint32_t (&w)[D / 16][2]) {
     return __uint_as_float((e + 1u) << 23);
 }
 
-// What turns a row's summed outputs into the attention's (a row whose weights
-// leave nothing is zero): two factors, because 2^(M - m) alone may leave float32's
-// range where the output does not.
-__device__ __forceinline__ float2 out_scale(float m, float l, float M) {
-    const float half = M == -INFINITY ? 0.f : ex2_approx(0.5f * (M - m));
-    return make_float2(half, l > 0.f || l != l ? half / l : 0.f);
-}
-
-// The gate's values for columns [col, col + 4) of query row `row`: of all K splits of
-// the logits a batch of loads is under way at a time.
-template <int D>
-__device__ __forceinline__ float4 gate_of(const Cache8Args& a, int b, int kvh, int n, int row, int col) {
-    const int i = row * a.g_inverse >> 16;
-    if (a.gate_mode == GSDPA_GATE_NONE || i >= n) return make_float4(1.f, 1.f, 1.f, 1.f);
-    const int h = (kvh - i) * a.G + row;   // kvh G + row % G
-    const long long token = (long long)b * a.Lq + i, step = (long long)a.B * a.Lq * a.gate_cols;
-    const bool per_col = a.gate_mode == GSDPA_GATE_ELEMENTWISE;
-    const float* gp = a.gate_part + token * a.gate_cols + (per_col ? (long long)h * D + col : h);
-    float4 gl = make_float4(0.f, 0.f, 0.f, 0.f);
-    constexpr int BATCH = 8;
-    for (int sp = 0; sp < a.gate_splits; sp += BATCH) {
-        float4 v[BATCH];
-#pragma unroll
-        for (int k = 0; k < BATCH; ++k) {
-            v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (sp + k >= a.gate_splits) continue;
-            if (per_col) v[k] = *reinterpret_cast<const float4*>(gp + (sp + k) * step);
-            else v[k].x = gp[(sp + k) * step];
-        }
-#pragma unroll
-        for (int k = 0; k < BATCH; ++k) {
-            gl.x += v[k].x;
-            gl.y += v[k].y;
-            gl.z += v[k].z;
-            gl.w += v[k].w;
-        }
-    }
-    if (!per_col) gl.y = gl.z = gl.w = gl.x;
-    return make_float4(sigmoid(gl.x), sigmoid(gl.y), sigmoid(gl.z), sigmoid(gl.w));
-}
-
-// Output columns [col, col + 4) of query row `row`: the sums o, scaled by both of k,
-// times the gate, stored.
-template <int D>
-__device__ __forceinline__ void finish(const Cache8Args& a, int b, int kvh, int n, int row, int col, const float2& k,
-                                       const float4& o, const float4& gate) {
-    const int i = row * a.g_inverse >> 16;
-    if (i >= n) return;
-    const int h = (kvh - i) * a.G + row;
-    *reinterpret_cast<uint2*>(a.O + (((long long)b * a.Lq + i) * a.Hq + h) * D + col) =
-        make_uint2(pack_bf16x2(o.x * k.x * k.y * gate.x, o.y * k.x * k.y * gate.y),
-                   pack_bf16x2(o.z * k.x * k.y * gate.z, o.w * k.x * k.y * gate.w));
-}
-
-// 2^(x - top), 0 for a part that saw nothing.
-__device__ __forceinline__ float part_weight(float x, float top) { return x == -INFINITY ? 0.f : ex2_approx(x - top); }
-
 template <int D, bool E4M3, int NT>
 struct Config {
     static constexpr int KS = NT == 1 ? 2 : 1;          // warps that share a tile's tokens
@@ -468,161 +320,6 @@ struct Config {
     static constexpr int MT = 4 / KS;                   // groups of 16 tokens to a warp
     static constexpr int STRIDE = D + 4;                // floats of a row's part: D columns, then m, l, M
     static constexpr uint32_t STAGE = kCacheBlock * D;  // bytes: an 8-bit tile's K or V, or half the open block's
-};
-
-__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-
-// Four columns of a row, merged from several parts.
-struct Sums {
-    float m = -INFINITY, l = 0.f, M = -INFINITY;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    // parts i, i + step, .. below end; where(i) points to part i's row: its columns, then its m, l, M at `state`
-    template <typename F>
-    __device__ __forceinline__ void add(int i, int end, int step, int state, int col, F where) {
-        for (; i < end; i += kBatch * step) {   // a batch of loads under way
-            float4 x[kBatch], v[kBatch];
-            float mn = m, Mn = M;
-#pragma unroll
-            for (int k = 0; k < kBatch; ++k) {
-                x[k] = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
-                v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (i + k * step < end) {
-                    const float* from = where(i + k * step);
-                    x[k] = *reinterpret_cast<const float4*>(from + state);
-                    v[k] = *reinterpret_cast<const float4*>(from + col);
-                }
-            }
-#pragma unroll
-            for (int k = 0; k < kBatch; ++k) {
-                mn = fmaxf(mn, x[k].x);
-                Mn = fmaxf(Mn, x[k].z);
-            }
-            const float w0 = part_weight(M, Mn);
-            l *= part_weight(m, mn);
-            o.x *= w0;
-            o.y *= w0;
-            o.z *= w0;
-            o.w *= w0;
-            m = mn;
-            M = Mn;
-#pragma unroll
-            for (int k = 0; k < kBatch; ++k) {
-                const float w = part_weight(x[k].z, M);
-                l += x[k].y * part_weight(x[k].x, m);
-                o.x += v[k].x * w;
-                o.y += v[k].y * w;
-                o.z += v[k].z * w;
-                o.w += v[k].w * w;
-            }
-        }
-    }
-    __device__ __forceinline__ void join(float m2, float l2, float M2, const float4& o2) {
-        const float mn = fmaxf(m, m2), Mn = fmaxf(M, M2);
-        const float wa = part_weight(M, Mn), wb = part_weight(M2, Mn);
-        l = l * part_weight(m, mn) + l2 * part_weight(m2, mn);
-        o.x = o.x * wa + o2.x * wb;
-        o.y = o.y * wa + o2.y * wb;
-        o.z = o.z * wa + o2.z * wb;
-        o.w = o.w * wa + o2.w * wb;
-        m = mn;
-        M = Mn;
-    }
-    __device__ __forceinline__ void join_lane(int sh) {
-        const float m2 = __shfl_xor_sync(0xffffffffu, m, sh), l2 = __shfl_xor_sync(0xffffffffu, l, sh);
-        const float M2 = __shfl_xor_sync(0xffffffffu, M, sh);
-        join(m2, l2, M2, make_float4(__shfl_xor_sync(0xffffffffu, o.x, sh), __shfl_xor_sync(0xffffffffu, o.y, sh),
-                                     __shfl_xor_sync(0xffffffffu, o.z, sh), __shfl_xor_sync(0xffffffffu, o.w, sh)));
-    }
-};
-
-// Where team n leaves its rows of the cut head whose first tile is u0: the first
-// head of its share, or the last.
-template <int D>
-__device__ __forceinline__ float* part_of(const Cache8Args& a, const Deal& deal, int n, int u0) {
-    return a.part + (long long)(2 * n + (u0 <= deal.from(n) ? 0 : 1)) * a.rows * (D + 4);
-}
-
-// The sequence of all tiles: sequence after sequence, in each one K/V head after
-// the other. (Its scan in four warps: in all twenty of a block it took 0.6 us more.)
-struct Layout {
-    int per;            // sequences to a place
-    int N, longest;     // all places; most tiles of a head
-    int ctas;           // that have any
-    bool by_head;
-    const int* place;   // [kScan + 1], in shared memory: the places before sequence per * k
-    // by all threads of a block of kScan or more
-    __device__ __forceinline__ Layout(const Cache8Args& a, int* s_place, int* s_scan, int tid) : place(s_place) {
-        const int warp = tid / 32, lane = tid % 32;
-        constexpr int W = kScan / 32;
-        per = (a.B + kScan - 1) / kScan;
-        int mine = 0, scan = 0;
-        if (warp < W) {
-            longest = 0;
-            for (int b = tid * per; b < min(a.B, (tid + 1) * per); ++b) {
-                const SeqTiles q(a, b);
-                mine += q.span();
-                longest = max(longest, q.tiles);
-            }
-            mine *= a.Hkv;
-            scan = mine;
-#pragma unroll
-            for (int sh = 1; sh < 32; sh <<= 1) {
-                const int up = __shfl_up_sync(0xffffffffu, scan, sh);
-                if (lane >= sh) scan += up;
-            }
-            longest = __reduce_max_sync(0xffffffffu, longest);
-            if (lane == 31) s_scan[warp] = scan;
-            if (lane == 0) s_scan[W + warp] = longest;
-        }
-        __syncthreads();
-        N = longest = 0;   // (fits: the host checks the number of places)
-        int before = scan - mine;
-#pragma unroll
-        for (int w = 0; w < W; ++w) {
-            if (w < warp) before += s_scan[w];
-            N += s_scan[w];
-            longest = max(longest, s_scan[W + w]);
-        }
-        if (warp < W) s_place[tid] = before;
-        if (tid == 0) s_place[kScan] = N;
-        __syncthreads();
-        ctas = max(1, min(a.ctas, N >> a.lg_teams));   // every team has a tile (or there is one CTA)
-        // Short sequences, a CTA for each head: no head is cut between CTAs, whose
-        // merge would take longer than the tiles.
-        by_head = longest <= a.whole_tiles && a.B * (long long)a.Hkv <= a.ctas;
-    }
-    // place x < N is place `rem` of sequence b
-    __device__ __forceinline__ void find(const Cache8Args& a, int x, int& b, int& rem) const {
-        int k = 0;
-#pragma unroll
-        for (int step = kScan / 2; step > 0; step >>= 1)
-            if (place[k + step] <= x) k += step;
-        b = k * per;
-        rem = x - place[k];
-        if (per > 1) {
-            int in_seq = SeqTiles(a, b).span() * a.Hkv;
-            while (rem >= in_seq && b + 1 < a.B) {
-                rem -= in_seq;
-                in_seq = SeqTiles(a, ++b).span() * a.Hkv;
-            }
-        }
-    }
-    // places before sequence b
-    __device__ __forceinline__ int before(const Cache8Args& a, int b) const {
-        int at = place[b / per];
-        for (int k = b / per * per; k < b; ++k) at += SeqTiles(a, k).span() * a.Hkv;
-        return at;
-    }
 };
 
 template <int D, bool E4M3, int NT>
@@ -1144,96 +841,6 @@ cache8_attn_kernel(const __grid_constant__ Cache8Args a) {
     }
 }
 
-// The heads that were cut between teams, from the teams' parts. Four lanes have
-// 16 columns of a row; a head's parts are split over as many such groups as give
-// every thread of the grid work, down to four parts each (one sequence of 131072
-// tokens leaves 608 parts of each head), and joined by shuffles and through
-// shared memory. Its own kernel, because the end of the attention kernel is the
-// one point at which all parts are known to be there without atomics: a launch
-// that was set up early costs less than a chain of counters (one sequence of
-// 131072 tokens: merged in the attention kernel, by the CTAs that arrive last at
-// two levels of counters, 26.7 us in all, so 23.1; two blocks to an SM with half
-// the registers and batches of four: 25.7).
-template <int D>
-__global__ void __launch_bounds__(kMergeThreads) cache8_merge_kernel(const __grid_constant__ Cache8Args a) {
-    constexpr int kWarps = kMergeThreads / 32;
-    __shared__ int s_place[kScan + 1], s_scan[2 * kScan / 32];
-    __shared__ float4 s_o[kWarps][4], s_x[kWarps][4];
-    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-    pdl_trigger();
-    // (the attention kernel started after everything before this call had ended: the lengths may be read)
-    const Layout all(a, s_place, s_scan, tid);
-    const Deal deal(all.N, all.ctas << a.lg_teams);
-    const int items = a.rows * (D / 4), takers = all.ctas << a.lg_teams, threads = gridDim.x * kMergeThreads;
-    // A unit of the work is a head, or where there are more heads than places at which
-    // shares begin, such a place, for the head that it is the first to cut.
-    const long long heads = (long long)a.B * a.Hkv;
-    const bool by_place = heads >= takers;
-    const int units = all.by_head ? 0 : (by_place ? takers - 1 : (int)heads);
-    const int most = deal.each > 0 ? all.longest / deal.each + 2 : 1;   // parts of a head
-    int lg = 0;
-    while ((8 << lg) <= kMergeThreads && ((units * items) << (lg + 1)) <= threads && (4 << lg) < most) ++lg;
-    const int total = (units * items) << lg;   // (below 1280 x 4096, or the grid's threads)
-    bool waited = false;
-    for (int base = blockIdx.x * kMergeThreads; base < total; base += threads) {
-        const int idx = base + tid, unit = idx / (items << lg);
-        const int x = idx - unit * (items << lg), item = (x >> (lg + 2) << 2) + (x & 3), sub = (x >> 2) & ((1 << lg) - 1);
-        const int row = item / (D / 4), col = 4 * (item % (D / 4));
-        int b = 0, kvh = 0, u0 = 0, n0 = 0, n1 = 0;
-        if (by_place) {
-            const int from = idx < total ? deal.from(unit + 1) : all.N;
-            if (from < all.N) {
-                all.find(a, from, b, u0);
-                const int tiles = SeqTiles(a, b).tiles, span = span_of(tiles), at = u0 % max(span, 1);
-                kvh = u0 / max(span, 1);
-                u0 = from - at;
-                if (at > 0 && at < tiles && deal.taker(u0) == unit) {
-                    n0 = unit;
-                    n1 = deal.taker(u0 + tiles - 1);
-                }
-            }
-        } else if (idx < total) {
-            b = unit / a.Hkv;
-            kvh = unit % a.Hkv;
-            const int tiles = SeqTiles(a, b).tiles;
-            u0 = all.before(a, b) + kvh * span_of(tiles);
-            if (tiles > 0) {
-                n0 = deal.taker(u0);
-                n1 = deal.taker(u0 + tiles - 1);
-            }
-        }
-        if (!waited) pdl_wait();
-        waited = true;
-        const bool cut = n1 > n0;
-        const int n = cut ? SeqTiles(a, b).n : 0;
-        float4 gate = make_float4(1.f, 1.f, 1.f, 1.f);
-        if (cut && sub == 0) gate = gate_of<D>(a, b, kvh, n, row, col);
-        Sums r;
-        if (cut)
-            r.add(n0 + sub, n1 + 1, 1 << lg, D, col, [&](int k) { return part_of<D>(a, deal, k, u0) + row * (D + 4); });
-        for (int k = 0; k < min(lg, 3); ++k) r.join_lane(4 << k);
-        if (lg > 3) {   // warps that share items
-            const int share = 1 << (lg - 3);
-            if (lane < 4) {
-                s_o[warp][lane] = r.o;
-                s_x[warp][lane] = make_float4(r.m, r.l, r.M, 0.f);
-            }
-            __syncthreads();
-            if (warp % share == 0) {
-                r = Sums();
-                for (int k = lane >> 2; k < share; k += 8) {
-                    const float4 y = s_x[warp + k][lane & 3];
-                    r.join(y.x, y.y, y.z, s_o[warp + k][lane & 3]);
-                }
-                for (int k = 0; k < 3; ++k) r.join_lane(4 << k);
-            }
-            __syncthreads();
-        }
-        if (cut && sub == 0) finish<D>(a, b, kvh, n, row, col, out_scale(r.m, r.l, r.M), r.o, gate);
-    }
-    if (!waited) pdl_wait();   // the next kernel on the stream relies on the attention kernel having ended
-}
-
 // Shared memory and ring of one problem.
 struct Shape {
     int NT, R, stages;
@@ -1413,7 +1020,7 @@ int gated_sdpa_cache8(const void* X, const void* Q, const gsdpa_cache8* cache, c
     // (Not a CTA for every SM: the SMs that are done first take them all, and they are
     // set up when the last are done.)
     if (e == cudaSuccess && !whole)
-        e = launch_dependent(cache->d_k == 128 ? cache8_merge_kernel<128> : cache8_merge_kernel<64>, dim3((unsigned)(sms - sms / 8)),
+        e = launch_dependent(cache->d_k == 128 ? cache_merge_kernel<128, Cache8Args> : cache_merge_kernel<64, Cache8Args>, dim3((unsigned)(sms - sms / 8)),
                              dim3(kMergeThreads), 0, s, a);
     return e == cudaSuccess ? GSDPA_OK : GSDPA_ERR_LAUNCH;
 }

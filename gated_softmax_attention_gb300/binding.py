@@ -53,6 +53,11 @@ SIGNATURES = {
     "gsdpa_cache8_append": (_I, [_VP] * 3 + [_LL] * 2 + [_VP] * 2 + [_I, _VP]),
     "gsdpa_cache8_workspace_bytes": (_SZ, [_VP] + [_I] * 4),
     "gated_sdpa_cache8": (_I, [_VP] * 7 + [_I] * 4 + [_VP, _SZ, _VP]),
+    "gsdpa_pages_step": (_I, [_VP] * 11 + [_I] * 4 + [_VP]),
+    "gsdpa_cache4_append": (_I, [_VP] * 3 + [_LL] * 2 + [_VP, _I, _VP]),
+    "gsdpa_cache4_read": (_I, [_VP] * 4 + [_LL] * 2 + [_I, _VP]),
+    "gsdpa_cache4_workspace_bytes": (_SZ, [_VP] + [_I] * 7),
+    "gated_sdpa_cache4": (_I, [_VP] * 9 + [_I] * 7 + [_VP, _SZ, _VP]),
 }
 
 _lock = threading.Lock()
@@ -632,8 +637,8 @@ def _kept_workspace(need, device, stream):
 
 
 def release_workspaces() -> None:
-    """Lets go of the workspaces that qk_norm_rope_bwd and gated_sdpa_cache8 keep for
-    this thread, one for each stream it has called them on, of the largest size
+    """Lets go of the workspaces that qk_norm_rope_bwd, gated_sdpa_cache8 and
+    gated_sdpa_cache4 keep for this thread, one for each stream it has called them on, of the largest size
     they needed there. The memory goes back to torch's allocator; calls that are
     still running are not disturbed, and the next ones allocate anew."""
     _kept.by_stream.clear()
@@ -902,4 +907,212 @@ def gated_sdpa_cache8(X, Q, cache, lens, W_g=None, *, gate="elementwise", n_new=
                                None if workspace is None else workspace.data_ptr(), need, stream)
     if st != OK:
         raise GsdpaError(st, "gated_sdpa_cache8")
+    return out
+
+
+PAGE = 64          # tokens of a page of the 4-bit cache
+CACHE4_KINDS = {"int4": 0, "e2m1": 1}
+
+
+class _Cache4Plan(ctypes.Structure):
+    _fields_ = [("kind", _I), ("n_pages", _I), ("H_kv", _I), ("d_k", _I), ("k_exp", _I), ("v_exp", _I), ("pool", _VP)]
+
+
+class Cache4:
+    """A paged K/V cache held in 4 bits (gsdpa_cache4) over the caller's pool, uint8
+    [n_pages, H_kv, 72 d_k], pages of 64 tokens. kind "int4" or "e2m1"; a code stands for
+    code * scale * 2^k_exp (2^v_exp), scales up to 448: the exponents put the largest
+    keys and values, over 7 or 6, below that. Block tables and lengths are the caller's."""
+
+    def __init__(self, pool, kind="e2m1", *, k_exp=0, v_exp=0):
+        import torch
+        if pool.dtype != torch.uint8:
+            raise TypeError(f"pool must be uint8, not {pool.dtype}")
+        if pool.dim() != 3 or pool.shape[2] % 72 != 0:
+            raise ValueError(f"pool {tuple(pool.shape)} must be [n_pages, H_kv, 72 d_k]")
+        if kind not in CACHE4_KINDS:
+            raise ValueError(f"kind must be one of {sorted(CACHE4_KINDS)}, not {kind!r}")
+        for name, v in (("k_exp", k_exp), ("v_exp", v_exp)):
+            if not isinstance(v, int) or not -64 <= v <= 64:
+                raise ValueError(f"{name} must be a whole number in -64 .. 64, not {v!r}")
+        _expect(pool, "pool", pool.numel(), torch.uint8, pool.device)
+        n, H, page = pool.shape
+        self.pool, self.kind, self.k_exp, self.v_exp = pool, kind, k_exp, v_exp
+        self.n_pages, self.H_kv, self.d_k, self.device = n, H, page // 72, pool.device
+        self.plan = _Cache4Plan(CACHE4_KINDS[kind], n, H, page // 72, k_exp, v_exp, pool.data_ptr())
+        self.ref = ctypes.addressof(self.plan)
+        self.need = {}   # workspace bytes, by the problem's shape
+
+    # A copy is a cache over its own pool: the plan's address is made anew.
+    def __reduce__(self):
+        return _cache4_again, (self.pool, self.kind, self.k_exp, self.v_exp)
+
+
+def _cache4_again(pool, kind, k_exp, v_exp):
+    return Cache4(pool, kind, k_exp=k_exp, v_exp=v_exp)
+
+
+def cache4_alloc(n_pages, H_kv, d_k, kind="e2m1", *, k_exp=0, v_exp=0, device="cuda") -> Cache4:
+    """A Cache4 of n_pages pages of 64 tokens."""
+    import torch
+    return Cache4(torch.empty((n_pages, H_kv, 72 * d_k), dtype=torch.uint8, device=device), kind, k_exp=k_exp, v_exp=v_exp)
+
+
+class PagesStep:
+    """What pages_step returns: cu [B + 1] and granted [B] int32, slots [n_rows] int64,
+    positions [n_rows] int32, n_free [1] int32."""
+    __slots__ = ("cu", "granted", "slots", "positions", "n_free")
+
+    def __init__(self, cu, granted, slots, positions, n_free):
+        self.cu, self.granted, self.slots, self.positions, self.n_free = cu, granted, slots, positions, n_free
+
+
+@_on_stream
+def pages_step(lens, n_new, table, free_pages, n_free, n_rows, *, keep=None, out=None) -> PagesStep:
+    """The plan of a step (gsdpa_pages_step): request b goes back from lens[b] tokens to
+    keep[b] (None: keeps them), gives the pages past them back, and takes n_new[b] more;
+    their pages come off the free stack in the requests' order. lens, n_new, keep int32
+    [B]; table int32 [B, max_pages] and free_pages int32 [n_pages] (the numbers of the
+    free pages come first, n_free[0] of them) are brought up to date in place, n_free is not
+    unless it is ``out.n_free``: the result has the new one. n_rows: the rows of the
+    step's packed tensors, at least the sum of n_new; rows past it get slot -1.
+    ``out``: a PagesStep to write to. ``stream``: else the current one."""
+    import torch
+    dev, i32 = table.device, torch.int32
+    if table.dim() != 2:
+        raise ValueError(f"table {tuple(table.shape)} must be [B, max_pages]")
+    B, width = table.shape
+    if lens is None or n_new is None or free_pages is None or n_free is None:
+        raise ValueError("lens, n_new, free_pages and n_free are required")
+    if out is None:
+        if not table.is_cuda:
+            raise ValueError(f"table must be a CUDA tensor, not on {table.device}")
+        flat = torch.empty(2 * B + 2 + n_rows, dtype=i32, device=dev)
+        cu, granted, left, positions = flat.split((B + 1, B, 1, n_rows))
+        out = PagesStep(cu, granted, torch.empty(n_rows, dtype=torch.int64, device=dev), positions, left)
+    st = (_lib or load()).gsdpa_pages_step(
+        _vector(lens, "lens", B, i32, dev), _vector(keep, "keep", B, i32, dev), _vector(n_new, "n_new", B, i32, dev),
+        _vector(table, "table", B * width, i32, dev), _vector(free_pages, "free_pages", free_pages.numel(), i32, dev),
+        _vector(n_free, "n_free", 1, i32, dev), _vector(out.n_free, "out.n_free", 1, i32, dev),
+        _vector(out.cu, "out.cu", B + 1, i32, dev), _vector(out.granted, "out.granted", B, i32, dev),
+        _vector(out.slots, "out.slots", n_rows, torch.int64, dev),
+        _vector(out.positions, "out.positions", n_rows, i32, dev), B, width, free_pages.numel(), n_rows,
+        _current_stream(dev))
+    if st != OK:
+        raise GsdpaError(st, "gsdpa_pages_step")
+    return out
+
+
+def _token_rows(t, name, N, cache):
+    """The row length of t [N, H_kv, d_k] (heads contiguous, rows evenly spaced)."""
+    import torch
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if t.dim() != 3:
+        raise ValueError(f"{name} {tuple(t.shape)} must be [n_rows, H_kv, d_k]")
+    return _head_rows(t.unsqueeze(0), name, (1, N, cache.H_kv, cache.d_k), torch.bfloat16, cache.device)
+
+
+@_on_stream
+def cache4_append(cache, K, V, slots) -> None:
+    """Writes K, V [n_rows, H_kv, d_k] bfloat16 (column blocks of a packed projection's
+    output, too) to their slots, int64 [n_rows] of different numbers, negative ones passed over
+    (gsdpa_cache4_append). ``stream``: else the current one."""
+    import torch
+    dev = cache.device
+    if slots is None:
+        raise ValueError("slots is required")
+    N = slots.numel()
+    ld_k, ld_v = _token_rows(K, "K", N, cache), _token_rows(V, "V", N, cache)
+    st = (_lib or load()).gsdpa_cache4_append(cache.ref, K.data_ptr(), V.data_ptr(), ld_k, ld_v,
+                                              _vector(slots, "slots", N, torch.int64, dev), N, _current_stream(dev))
+    if st != OK:
+        raise GsdpaError(st, "gsdpa_cache4_append")
+
+
+@_on_stream
+def cache4_read(cache, slots, *, out_k=None, out_v=None):
+    """Keys and values at slots (int64 [n_rows]) as the bfloat16 numbers that their codes
+    stand for (gsdpa_cache4_read): what gated_sdpa_fwd takes for a later piece of a
+    prompt. Token p of a request is at slot table[b, p // 64] * 64 + p % 64; rows of
+    negative slots are zero. ``stream``: else the current one. Returns (K, V) [n_rows, H_kv, d_k]."""
+    import torch
+    dev = cache.device
+    if slots is None:
+        raise ValueError("slots is required")
+    N = slots.numel()
+    shape = (N, cache.H_kv, cache.d_k)
+    if out_k is None:
+        out_k = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    if out_v is None:
+        out_v = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    ld_k, ld_v = _token_rows(out_k, "out_k", N, cache), _token_rows(out_v, "out_v", N, cache)
+    st = (_lib or load()).gsdpa_cache4_read(cache.ref, _vector(slots, "slots", N, torch.int64, dev), out_k.data_ptr(),
+                                            out_v.data_ptr(), ld_k, ld_v, N, _current_stream(dev))
+    if st != OK:
+        raise GsdpaError(st, "gsdpa_cache4_read")
+    return out_k, out_v
+
+
+def cache4_workspace_bytes(cache, B, max_pages, n_rows, max_new, H_q, d_model=0, gate="elementwise") -> int:
+    n = load().gsdpa_cache4_workspace_bytes(cache.ref, B, max_pages, n_rows, max_new, d_model, H_q, GATE_CODES[gate])
+    if n == ctypes.c_size_t(-1).value:
+        raise GsdpaError(ERR_UNSUPPORTED, "gsdpa_cache4_workspace_bytes")
+    return n
+
+
+@_on_stream
+def gated_sdpa_cache4(X, Q, cache, table, lens, cu, W_g=None, *, gate="elementwise", max_new=1, n_new=None, out=None,
+                      workspace=None):
+    """Gated attention of a step's tokens against the 4-bit cache through the block
+    table (gated_sdpa_cache4), after cache4_append of their keys and values: request b has
+    rows cu[b] .. cu[b + 1] of Q [n_rows, H_q, d_k] and X [n_rows, d_model], at most max_new of them,
+    and row i sees its tokens 0 .. lens[b] + i. table int32 [B, max_pages], lens int32
+    [B] (the tokens before this step), cu int32 [B + 1]; n_new (the plan's granted) int32
+    [B], the rows that count, or None for all. W_g as for gated_sdpa_fwd (None for gate="none").
+    Rows that do not count are zero. ``stream``: else the current one. Returns O, like Q."""
+    import torch
+    dev, bf, i32 = cache.device, torch.bfloat16, torch.int32
+    gm = GATE_CODES[gate]
+    if Q.dim() != 3 or Q.shape[2] != cache.d_k:
+        raise ValueError(f"Q {tuple(Q.shape)} must be [n_rows, H_q, d_k={cache.d_k}]")
+    if table.dim() != 2:
+        raise ValueError(f"table {tuple(table.shape)} must be [B, max_pages]")
+    N, H_q, d_k = Q.shape
+    B, width = table.shape
+    q = _vector(Q, "Q", N * H_q * d_k, bf, dev)
+    d_model, x, w = 0, None, None
+    if gm != GATE_NONE:
+        d_model = _x_dim(X, 1, N)
+        if W_g is None:
+            raise ValueError("W_g is required")
+        x = _vector(X, "X", N * d_model, bf, dev)
+        w = _vector(W_g, "W_g", d_model * _gate_cols(gm, H_q, d_k), bf, dev)
+    if lens is None or cu is None:
+        raise ValueError("lens and cu are required")
+    pages, at, rows = _vector(table, "table", B * width, i32, dev), _vector(lens, "lens", B, i32, dev), \
+        _vector(cu, "cu", B + 1, i32, dev)
+    new = _vector(n_new, "n_new", B, i32, dev)
+    if out is None:
+        out = torch.empty((N, H_q, d_k), dtype=bf, device=dev)
+    o = _vector(out, "out", N * H_q * d_k, bf, dev)
+    lib = _lib or load()
+    shape = (B, width, N, max_new, d_model, H_q, gm)
+    need = cache.need.get(shape)     # (the workspace's size, by the problem's shape)
+    if need is None:
+        need = lib.gsdpa_cache4_workspace_bytes(cache.ref, B, width, N, max_new, d_model, H_q, gm)
+        if need == ctypes.c_size_t(-1).value:
+            need = 0                 # (the call itself says why)
+        if len(cache.need) >= 256:
+            cache.need.clear()       # (steps of ever other sizes)
+        cache.need[shape] = need
+    stream = _current_stream(dev)
+    if workspace is not None:
+        workspace, need = _workspace(workspace, need, dev)
+    else:
+        workspace = _kept_workspace(need, dev, stream)
+    st = lib.gated_sdpa_cache4(x, q, cache.ref, pages, at, rows, new, w, o, B, width, N, max_new, d_model, H_q, gm,
+                               None if workspace is None else workspace.data_ptr(), need, stream)
+    if st != OK:
+        raise GsdpaError(st, "gated_sdpa_cache4")
     return out

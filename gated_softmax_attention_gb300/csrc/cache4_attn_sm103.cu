@@ -1,0 +1,938 @@
+// cache4_attn_sm103.cu -- gated attention of a step's new tokens against the paged
+// K/V cache held in 4 bits (a scale per token and 16 columns), through a block table.
+//
+// For request b with T = len + n tokens, query row i < n of head h:
+//     s_j = q . k_j / sqrt(d_k), j <= len + i;   O = softmax(s) V (.) sigma(gl)
+// with k_j[c] = 2^ke ks(j, c / 16) K4[j, c], v_j[c] = 2^ve vs(j, c / 16) V4[j, c].
+//
+// Bound by HBM: the cache is read once for all the query heads that share it, 1.125
+// d_k bytes a token and K/V head. In the time that a 4-bit code takes to arrive an SM
+// has 8 half-rate (integer and conversion) instructions for 64 codes, so both products
+// run on the tensor cores with mma.sync (16 tokens, then 16 value columns, on the
+// wide side, 8 query rows on the narrow one; tcgen05 wants 64 or 128 rows and its
+// operands in shared memory in a type of its own), and a page's bytes lie so
+// that what a lane loads becomes its operand with as few of these as possible:
+//   e2m1  a byte is two codes, one conversion to fp16 each. For keys these are
+//         neighbouring columns, the contraction's axis, and done; for values the axis is the
+//         tokens, and so that a token has whole bytes (the append writes them alone)
+//         the two tokens' halves of two bytes change places first, four operations a word.
+//   int4  code + 8 as the low bits of a subnormal fp16 number, u 2^-24 or, the next
+//         4 bits, u 2^-20: one AND each and a shift for every two, exact. The 8
+//         comes off in the sums: the keys' start at -8 sum q instead of zero, the values'
+//         take one more product, with the constant -8. (mma takes subnormal operands
+//         as they are: measured, products exact.) The factor 16 between the two is in q
+//         for the keys, in the result's columns for the values.
+// A key's scale multiplies the sum over its 16 columns in float32, one product's
+// depth. A value's multiplies the weights, in fp16, whose pairs are the same for all 16
+// columns: 2 instructions for 256 codes instead of 8.
+//
+// q, a bf16 row scaled by a power of two to below 2^15, is exact in fp16 (elements
+// under 2^-27 of the row's largest lose bits that weigh less than 2^-35 of it). The
+// weights p 2^-m are rounded to fp16, and again where they take the value scale. fp16's
+// range is short, so they use all of it: m follows the row's largest score plus ev, ev
+// the exponent of the page's largest value scale where that is above 1 (0 .. 9), and stands
+// 2^13 below, so that neither p nor p vs exceeds 2^15. It moves when a tile exceeds it by 2^2.
+//
+// Tile = one page: keys with their scales, then values with theirs, 36 d_k contiguous
+// bytes each, brought by cp.async.bulk from where the table says. The tiles of all
+// requests and K/V heads are dealt evenly to teams of warps and the heads that they cut
+// merged by a second kernel, as for the 8-bit cache (cache_attn.cuh).
+#include "cache4_internal.h"
+#include "cache_attn.cuh"
+#include "landing.cuh"
+
+namespace gsdpa {
+namespace {
+
+constexpr int kMaxStages = 16;       // ring stages per team
+constexpr int kBars = 48;            // ring stages of all teams
+constexpr uint32_t kSmemMax = 232448 - 1984;   // dynamic: what a CTA may have, less barriers, parts and a few words
+// A head is one CTA's where all have at most this many tiles for each team of it (by
+// the table's width, then by the lengths) and there are CTAs for all.
+constexpr int kWholeTiles = 3, kFewTiles = 1;
+constexpr float kUp = 13.0f, kMove = 2.0f;     // where m stands, and how far a tile may exceed it: see above
+
+struct PagedSeq;
+struct Cache4Args {
+    using Seq = PagedSeq;
+    __device__ __forceinline__ long long token(int b, int i) const { return (long long)cu[b] + i; }
+    __device__ __forceinline__ long long tokens() const { return N; }
+    const __nv_bfloat16* Q;          // [N, Hq, D]
+    __nv_bfloat16* O;
+    const int *table, *lens, *cu, *n_new;
+    const uint8_t* pool;             // [n_pages, Hkv, 72 D]
+    int B, N, max_new, Hq, Hkv, G;   // G = Hq / Hkv
+    int g_inverse;                   // 65536 / G, rounded up: row / G is row * g_inverse >> 16 for the rows there are
+    int rows;                        // G * max_new
+    int width, n_pages;              // pages of a request's row of the table; of the pool
+    int lg_teams;                    // teams of a CTA, 2^lg_teams = 8 / R
+    int R, stages;                   // groups of query rows (of 8 NT) to a team; ring stages per team
+    float k_up;                      // 2^k_exp
+    float v_exp;
+    const float* gate_part;          // [gate_splits, N, gate_cols] or null
+    int gate_splits, gate_cols, gate_mode;
+    float* part;                     // [CTAs][teams][2][rows][D + 4]: a team's first and last head, where cut
+    int ctas;                        // of the attention kernel
+    int whole_tiles;                 // most tiles of a head for one CTA to take it alone
+    int wait_first;                  // no gate kernel: everything before this kernel is waited for at once
+    WaitCtl ctl;
+};
+
+// A request's tokens before (len) and of this step (n), as the kernels take them:
+// numbers out of range make it empty (ok = false), so that no read or write can leave
+// the table, the queries or the outputs.
+struct PagedSeq {
+    int len, n, T, tiles;
+    bool ok;
+    __device__ __forceinline__ PagedSeq(const Cache4Args& a, int b) {
+        const int c0 = a.cu[b], c1 = a.cu[b + 1];
+        len = a.lens[b];
+        const int brought = c0 >= 0 && c1 >= c0 && c1 <= a.N ? c1 - c0 : -1;
+        n = a.n_new ? a.n_new[b] : brought;
+        ok = brought >= 0 && brought <= a.max_new && n >= 0 && n <= brought && len >= 0 && len <= a.width * kPage - n;
+        if (!ok) len = n = 0;
+        T = n > 0 ? len + n : 0;   // (a request without new tokens has no rows to compute)
+        tiles = (T + kPage - 1) / kPage;
+    }
+    __device__ __forceinline__ int span() const { return span_of(tiles); }
+};
+
+// A word of eight codes -> four fp16 pairs: pair p from bits 4 p .. and 16 + 4 p .. (int4:
+// (code + 8) 2^-24 for p even, 2^-20 for p odd), or from byte p (e2m1).
+template <bool E2M1>
+__device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t (&x)[4]) {
+    if constexpr (E2M1) {
+        asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+            "mov.b32 {a, b, c, d}, %4;\n\t"
+            "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+            "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+            "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+            "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+            : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+            : "r"(w));
+    } else {
+        const uint32_t v = w >> 8;
+        x[0] = w & 0x000f000fu;
+        x[1] = w & 0x00f000f0u;
+        x[2] = v & 0x000f000fu;
+        x[3] = v & 0x00f000f0u;
+    }
+}
+
+// A word of values has bytes [two columns] of two tokens, twice: e2m1 wants bytes of
+// [two tokens] of a column.
+__device__ __forceinline__ uint32_t swap_halves(uint32_t w) {
+    const uint32_t d = (w ^ (w >> 4)) & 0x00f000f0u;
+    return w ^ d ^ (d << 4);
+}
+
+// Four scales -> two fp16 pairs.
+__device__ __forceinline__ void scales_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    asm("{\n\t.reg .b16 a, b;\n\t"
+        "mov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+    const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ float2 floats(uint32_t h) { return __half22float2(*reinterpret_cast<const __half2*>(&h)); }
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// Words of a token's or lane's share, in as wide loads as they allow.
+template <int N>
+__device__ __forceinline__ void load_words(const uint8_t* from, uint32_t (&w)[N]) {
+    if constexpr (N % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < N / 4; ++i) {
+            const uint4 v = reinterpret_cast<const uint4*>(from)[i];
+            w[4 * i] = v.x;
+            w[4 * i + 1] = v.y;
+            w[4 * i + 2] = v.z;
+            w[4 * i + 3] = v.w;
+        }
+    } else if constexpr (N == 2) {
+        const uint2 v = *reinterpret_cast<const uint2*>(from);
+        w[0] = v.x;
+        w[1] = v.y;
+    } else {
+        w[0] = *reinterpret_cast<const uint32_t*>(from);
+    }
+}
+
+// Which of a word's four tokens (2 t, 2 t + 1, 2 t + 8, 2 t + 9 of 16) are among the
+// first `left` of the 16, as bytes.
+__device__ __forceinline__ uint32_t keep_tokens(int left, int t) {
+    const int over = left - 2 * t;
+    return (over > 0 ? 0xffu : 0u) | (over > 1 ? 0xff00u : 0u) | (over > 8 ? 0xff0000u : 0u) | (over > 9 ? 0xff000000u : 0u);
+}
+
+// The exponent ev >= 0 of the largest of a warp's value scales: all are below 2^ev or
+// at most 1. Each lane looks at its share of the 16 MT tokens', past `left` tokens at none.
+template <int D, int MT>
+__device__ __forceinline__ float scale_exponent(const uint8_t* scales, int lane, int left) {
+    constexpr int W = MT * D / 128;   // words of a lane
+    uint32_t w[W], top = 0;
+    load_words(scales + 4 * W * lane, w);
+#pragma unroll
+    for (int k = 0; k < W; ++k) {
+        uint32_t x = w[k] & 0x7f7f7f7fu;
+        if (left < 16 * MT) {
+            const int word = W * lane + k;
+            x &= keep_tokens(left - 16 * (word / (D / 4)), word % (D / 4) / (D / 16));
+        }
+        top = max_u16x2(top, max_u16x2(x, x << 8));
+    }
+    const uint32_t byte = __reduce_max_sync(0xffffffffu, max(top >> 24, top >> 8 & 0xffu));
+    return (float)max((int)(byte >> 3) - 6, 0);
+}
+
+// The products of a warp's 16 MT tokens become weights: element 2 x + e of s[n][i] is token
+// at + 16 i + 8 x and row 8 n + 2 t + e, seen up to token lim; times f it is the score
+// (log2 units). On return s holds p 2^-m, and l and m are up to date. m is compared with
+// the lane's own largest score only; the row's is found when one of them has to move.
+// (Sums with m are rounded towards larger m: whatever the scores' size, no weight times
+// 2^ev exceeds 2^(kUp + kMove).)
+template <int D, int NT, int MT, bool MASK>
+__device__ __forceinline__ void soften(float (&s)[NT][MT][4], const float (&f)[NT][2], int at, const int (&lim)[NT][2],
+                                       float ev, RowState<D, NT>& st) {
+    float top[NT][2];
+    bool need = false;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        top[n][0] = top[n][1] = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                s[n][i][e] = __fmul_rn(s[n][i][e], f[n][e & 1]);   // (rounded, as m is)
+                if (MASK && at + 16 * i + 8 * (e >> 1) > lim[n][e & 1]) s[n][i][e] = -INFINITY;
+                top[n][e & 1] = fmaxf(top[n][e & 1], s[n][i][e]);   // (a score that is no number: the weights show it)
+            }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) need = need || __fadd_ru(top[n][e], ev - (kUp + kMove)) > st.m[n][e];
+    }
+    if (__any_sync(0xffffffffu, need)) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            float fo[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float x = top[n][e];
+#pragma unroll
+                for (int sh = 4; sh < 32; sh <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, sh));
+                const float m = fmaxf(st.m[n][e], __fadd_ru(x, ev - kUp));
+                fo[e] = st.m[n][e] == -INFINITY ? 0.f : ex2_approx(st.m[n][e] - m);
+                st.l[n][e] *= fo[e];
+                st.m[n][e] = m;
+            }
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) st.o[n][i][e] *= fo[e & 1];
+        }
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        float m[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) m[e] = st.m[n][e] == -INFINITY ? 0.f : st.m[n][e];   // (no token seen yet)
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float p = ex2_approx(__fsub_rn(s[n][i][e], m[e & 1]));   // (masked: 2^-inf)
+                st.l[n][e & 1] += p;
+                s[n][i][e] = p;
+            }
+    }
+}
+
+// A query row as the first product's narrow operand: product j of lane t covers
+// columns 16 j + 4 t .. + 3.
+template <int D>
+__device__ __forceinline__ void load_row(const __nv_bfloat16* src, int t, uint32_t (&w)[D / 16][2]) {
+#pragma unroll
+    for (int j = 0; j < D / 16; ++j) {
+        uint2 v = make_uint2(0, 0);
+        if (src) v = *reinterpret_cast<const uint2*>(src + 16 * j + 4 * t);
+        w[j][0] = v.x;
+        w[j][1] = v.y;
+    }
+}
+
+// A bf16 row -> fp16 scaled by a power of two to below 2^15 (int4: the second pair of
+// each product by 1/16 more), and, int4, -8 2^-24 times its sum over each 16
+// columns; returns the factor that undoes the scale.
+template <int D, bool E2M1>
+__device__ __forceinline__ float row_to_f16(uint32_t (&w)[D / 16][2], float (&off)[D / 16]) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) top = max(top, max(w[j][h] & 0x7fffu, (w[j][h] >> 16) & 0x7fffu));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    const uint32_t e = min(max(top >> 7, 15u), 252u);   // the largest element's exponent field, so that both factors are
+    const float scale = __uint_as_float((268u - e) << 23);
+#pragma unroll
+    for (int j = 0; j < D / 16; ++j) {
+        float sum = 0.f;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t v = w[j][h];
+            const float k = E2M1 || h == 0 ? scale : scale * 0.0625f;
+            w[j][h] = pack_f16x2(__uint_as_float(v << 16) * k, __uint_as_float(v & 0xffff0000u) * k);
+            if (!E2M1) {
+                const float2 q = floats(w[j][h]);   // (as the products have them)
+                sum += (q.x + q.y) * (h == 0 ? 1.f : 16.f);
+            }
+        }
+        if (!E2M1) {
+            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+            off[j] = sum * -4.76837158203125e-07f;   // -8 2^-24
+        }
+    }
+    return __uint_as_float((e - 14u) << 23) * (E2M1 ? 1.f : 16777216.f);
+}
+
+template <int D, bool E2M1, int NT>
+struct Config {
+    static constexpr int KS = NT == 1 ? 2 : 1;          // warps that share a tile's tokens
+    static constexpr int WARPS = kSlots * KS;           // ... that compute
+    static constexpr int CONSUMERS = WARPS * 32;
+    static constexpr int THREADS = CONSUMERS + 128;     // one more warp issues the copies, in a group of four of its own:
+    // its registers go to the others (at launch 640 threads have 96 each, 384 have 168: 61440 and 64512 in
+    // all, which is 512 x 112 + 128 x 32 and 256 x 232 + 128 x 40)
+    static constexpr int REGS = NT == 1 ? 112 : 232, COPY_REGS = NT == 1 ? 32 : 40;
+    static constexpr int MT = 4 / KS;                   // groups of 16 tokens to a warp
+    static constexpr int STRIDE = D + 4;                // floats of a row's part: D columns, then m, l, M
+    static constexpr uint32_t STAGE = half_bytes(D);    // bytes: a page's keys or values, with their scales
+};
+
+template <int D, bool E2M1, int NT>
+__global__ void __launch_bounds__(Config<D, E2M1, NT>::THREADS, 1)
+cache4_attn_kernel(const __grid_constant__ Cache4Args a) {
+    using C = Config<D, E2M1, NT>;
+    constexpr uint32_t STAGE = C::STAGE;
+    constexpr int kConsumers = C::CONSUMERS, MT = C::MT, STRIDE = C::STRIDE;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ uint64_t s_full[kBars], s_empty[kBars];
+    __shared__ int s_place[kScan + 1], s_scan[2 * kScan / 32];
+    __shared__ int s_abort;
+    volatile int* abort_flag = &s_abort;
+
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    const int g = lane >> 2, t = lane & 3;
+    const int team_warps = C::KS * a.R, teams = 1 << a.lg_teams;
+    const int team = warp / team_warps, in_team = warp % team_warps;   // (the copying warp: neither)
+    float* slots = reinterpret_cast<float*>(smem + (size_t)teams * a.stages * STAGE);   // [teams][rows][STRIDE]
+    if (tid < teams * a.stages) {
+        mbar_init(&s_full[tid], 1);
+        mbar_init(&s_empty[tid], team_warps);
+    }
+    mbar_fence_init();
+    if (tid == 0) s_abort = 0;
+    if (a.wait_first) pdl_wait();
+    pdl_trigger();   // the next kernel may be set up; it waits for this grid before it touches memory
+
+    // ---- the teams' shares of all tiles, or of the CTA's own head
+    const Layout all(a, s_place, s_scan, tid);
+    const int me = blockIdx.x, N = all.N, ctas = all.ctas;
+    const bool by_head = all.by_head;
+    const Deal deal(N, ctas * teams);
+    const int whole_head = by_head && me < a.B * a.Hkv ? PagedSeq(a, me / a.Hkv).tiles : 0;   // the CTA's own head
+    const auto team_lo = [&](int k) {
+        return by_head ? Deal(whole_head, teams).from(k) : (me < ctas ? deal.from(me * teams + k) : N);
+    };
+    const auto start_of = [&](int k) {
+        Cursor c;
+        const int from = team_lo(k);
+        c.left = team_lo(k + 1) - from;
+        c.b = c.kvh = c.j = c.tiles = 0;
+        if (c.left > 0) {
+            if (by_head) {
+                c.b = me / a.Hkv;
+                c.tiles = whole_head;
+                c.kvh = me % a.Hkv;
+                c.j = from;
+                return c;
+            }
+            int rem;
+            all.find(a, from, c.b, rem);
+            c.tiles = PagedSeq(a, c.b).tiles;
+            if (c.tiles == 0) {
+                c.left = 0;
+            } else {
+                const int span = span_of(c.tiles);
+                c.kvh = rem / span;
+                c.j = rem % span;
+                if (c.j >= c.tiles) c.next_head(a);
+            }
+        }
+        return c;
+    };
+    if (warp >= C::WARPS) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::COPY_REGS));
+        if (warp > C::WARPS) return;
+        // ---- copies: lane k serves team k, in the order the team consumes them
+        Cursor next;
+        next.left = 0;
+        if (lane < teams) next = start_of(lane);
+        uint8_t* ring = smem + (size_t)lane * a.stages * STAGE;
+        uint64_t *full = s_full + lane * a.stages, *empty = s_empty + lane * a.stages;
+        uint32_t stage = 0, phase = 0, armed = 0, armed_phase = 0;
+        bool values = false;   // the half of the page at `next` that is copied next
+        // the pages of the tile at `next` and the one after it
+        const int* row = a.table;
+        int page = 0, page_after = 0;
+        const auto enter = [&]() {
+            row = a.table + (long long)next.b * a.width;
+            page = row[next.j];
+            page_after = next.j + 1 < next.tiles ? row[next.j + 1] : 0;
+        };
+        if (next.left > 0) enter();
+        unsigned long long idle_since = 0;
+        while (__any_sync(0xffffffffu, next.left > 0)) {
+            bool did = false;
+            if (next.left > 0 && mbar_test(&empty[stage], phase ^ 1u)) {
+                did = true;
+                uint8_t* to = ring + stage * STAGE;
+                if (page >= 0 && page < a.n_pages) {
+                    mbar_arrive_expect_tx(&full[stage], STAGE);
+                    armed |= 1u << stage;
+                    armed_phase = (armed_phase & ~(1u << stage)) | (phase << stage);
+                    bulk_load(to, a.pool + (((long long)page * a.Hkv + next.kvh) * 2 + (values ? 1 : 0)) * STAGE, STAGE,
+                              &full[stage]);
+                } else {
+                    // no page of the pool: keys whose scales are NaN (who sees them is NaN), values of scale 0
+                    uint4* scales = reinterpret_cast<uint4*>(to + key_scales_at(D));
+                    const uint32_t x = values ? 0u : 0x7f7f7f7fu;
+                    for (int k = 0; k < 4 * D / 16; ++k) scales[k] = make_uint4(x, x, x, x);
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // (before the stage's next copy)
+                    mbar_arrive(&full[stage]);
+                    atomicOr(a.ctl.err, ERR_CACHE_RANGE);
+                }
+                if (values) {
+                    if (next.j + 1 < next.tiles) {
+                        ++next.j;
+                        --next.left;
+                        page = page_after;
+                        if (next.j + 1 < next.tiles) page_after = row[next.j + 1];
+                    } else {
+                        next.next_head(a);
+                        if (next.left > 0) enter();
+                    }
+                }
+                values = !values;
+                if (++stage == (uint32_t)a.stages) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+            if (__any_sync(0xffffffffu, did)) {
+                idle_since = 0;
+                continue;
+            }
+            // every team's ring is full: look again shortly, but not for ever
+            if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
+            const unsigned long long now = globaltimer_ns();
+            if (idle_since == 0) idle_since = now;
+            if (__any_sync(0xffffffffu, now - idle_since > a.ctl.limit_ns)) {
+                if (lane == 0) {
+                    atomicOr(a.ctl.err, ERR_WAIT_TIMEOUT);
+                    *abort_flag = 1;
+                }
+                break;
+            }
+            __nanosleep(40);
+        }
+        // The CTA keeps its shared memory until this warp is done: it stays until what it
+        // has issued is there, whoever gave up. (A share that is no longer than its ring is
+        // issued at once, and its consumers may still give up; where they wait for the same
+        // copies this costs nothing.)
+        volatile int never = 0;
+        const WaitCtl c2 = landing_limit(a.ctl);
+        for (int k = 0; k < a.stages; ++k)
+            if (armed & (1u << k)) mbar_wait(&full[k], (armed_phase >> k) & 1u, &never, c2);
+        return;
+    }
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS));
+    bool ok = true;
+    {
+        // ---- the team's tiles
+        const uint8_t* ring = smem + (size_t)team * a.stages * STAGE;
+        uint64_t *full = s_full + team * a.stages, *empty = s_empty + team * a.stages;
+        const int rt = in_team / C::KS, kh = in_team % C::KS;   // the warp's query rows and part of a tile's tokens
+        const int team_threads = 32 * team_warps, team_tid = 32 * in_team + lane;
+        float* slot = slots + (size_t)team * a.rows * STRIDE;
+        uint32_t stage = 0, phase = 0;   // the oldest stage that is not released
+        const auto wait_full = [&]() -> const uint8_t* {
+            if (!__all_sync(0xffffffffu, mbar_wait(&full[stage], phase, abort_flag, a.ctl))) {
+                ok = false;
+                return nullptr;
+            }
+            return ring + stage * STAGE;
+        };
+        const auto release = [&]() {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&empty[stage]);
+            if (++stage == (uint32_t)a.stages) {
+                stage = 0;
+                phase ^= 1u;
+            }
+        };
+        RowState<D, NT> st;
+        const int first = 16 * MT * kh;   // the warp's tokens of a tile: first .. first + 16 MT
+        const float unscaled = kLog2e * rsqrtf((float)D) * a.k_up;
+        Cursor at = start_of(team);
+        const int share_end = team_lo(team + 1);
+        while (at.left > 0) {
+            const PagedSeq q(a, at.b);
+            const int j1 = min(at.tiles, at.j + at.left);   // segment: tiles [at.j, j1) of the head
+            uint32_t qf[NT][D / 16][2];
+            float f[NT][2], off[NT][D / 16][2];   // (off: of the lane's two rows, int4)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const int row = 8 * (NT * rt + n) + g, i = row * a.g_inverse >> 16;
+                load_row<D>(row < a.rows && i < q.n
+                                ? a.Q + (a.token(at.b, i) * a.Hq + (at.kvh - i) * a.G + row) * D : nullptr, t, qf[n]);
+                float sums[D / 16];
+                const float back = row_to_f16<D, E2M1>(qf[n], sums) * unscaled;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    f[n][e] = __shfl_sync(0xffffffffu, back, 4 * (2 * t + e));
+                    if (!E2M1) {
+#pragma unroll
+                        for (int j = 0; j < D / 16; ++j) off[n][j][e] = __shfl_sync(0xffffffffu, sums[j], 4 * (2 * t + e));
+                    }
+                }
+            }
+            st.clear();
+            for (int j = at.j; ok && j < j1; ++j) {
+                float s[NT][MT][4];
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int i = 0; i < MT; ++i)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) s[n][i][e] = 0.f;
+                const uint8_t* kt = wait_full();
+                if (!kt) break;
+#pragma unroll
+                for (int i = 0; i < MT; ++i) {
+                    const int n0 = first + 16 * i + g;   // and n0 + 8
+                    uint32_t x[D / 32], y[D / 32], xs[D / 64], ys[D / 64];
+                    load_words(kt + n0 * (D / 2) + t * (D / 8), x);
+                    load_words(kt + (n0 + 8) * (D / 2) + t * (D / 8), y);
+                    load_words(kt + key_scales_at(D) + n0 * (D / 16), xs);
+                    load_words(kt + key_scales_at(D) + (n0 + 8) * (D / 16), ys);
+#pragma unroll
+                    for (int w = 0; w < D / 32; ++w) {   // two groups of columns
+                        uint32_t xc[4], yc[4], hx[2], hy[2];
+                        codes_to_f16<E2M1>(x[w], xc);
+                        codes_to_f16<E2M1>(y[w], yc);
+                        scales_to_f16(xs[w / 2], hx[0], hx[1]);
+                        scales_to_f16(ys[w / 2], hy[0], hy[1]);
+                        const float2 fx = floats(hx[w % 2]), fy = floats(hy[w % 2]);
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const uint32_t op[4] = {xc[2 * k], yc[2 * k], xc[2 * k + 1], yc[2 * k + 1]};
+                            const float kx = k ? fx.y : fx.x, ky = k ? fy.y : fy.x;
+#pragma unroll
+                            for (int n = 0; n < NT; ++n) {
+                                const int c = 2 * w + k;
+                                float r[4];
+                                r[0] = r[2] = E2M1 ? 0.f : off[n][c][0];
+                                r[1] = r[3] = E2M1 ? 0.f : off[n][c][1];
+                                mma_f16(r, op, qf[n][c][0], qf[n][c][1]);
+                                s[n][i][0] = fmaf(r[0], kx, s[n][i][0]);
+                                s[n][i][1] = fmaf(r[1], kx, s[n][i][1]);
+                                s[n][i][2] = fmaf(r[2], ky, s[n][i][2]);
+                                s[n][i][3] = fmaf(r[3], ky, s[n][i][3]);
+                            }
+                        }
+                    }
+                }
+                release();
+                const uint8_t* vt = wait_full();
+                if (!vt) break;
+                // (the first query row sees tokens up to len: tiles before need no mask)
+                const int base = j * kPage + first, left = q.T - base;
+                const bool masked = j * kPage + kPage - 1 > q.len;
+                const uint8_t* scales = vt + 32 * D + kh * MT * D;
+                const float ev = scale_exponent<D, MT>(scales, lane, masked ? left : 16 * MT);
+                int lim[NT][2] = {};
+                if (masked) {
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {   // the last token that each of the lane's rows sees
+                            const int row = 8 * (NT * rt + n) + 2 * t + e, i = row * a.g_inverse >> 16;
+                            lim[n][e] = row < a.rows && i < q.n ? q.len + i : -1;
+                        }
+                    soften<D, NT, MT, true>(s, f, base + g, lim, ev, st);
+                } else {
+                    soften<D, NT, MT, false>(s, f, base + g, lim, ev, st);
+                }
+#pragma unroll
+                for (int i = 0; i < MT; ++i) {
+                    uint32_t pf[NT][2], sw[D / 16];
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) pf[n][x] = transpose8(pack_f16x2(s[n][i][2 * x], s[n][i][2 * x + 1]));
+                    load_words(scales + i * D + t * (D / 4), sw);
+                    if (masked) {
+                        // slots past the request's end hold whatever was there before: scale 0, not NaN
+                        const uint32_t keep = keep_tokens(left - 16 * i, t);
+#pragma unroll
+                        for (int c = 0; c < D / 16; ++c) sw[c] &= keep;
+                    }
+#pragma unroll
+                    for (int quad = 0; quad < D / 64; ++quad) {
+                        uint32_t w[4];
+                        load_words(vt + (((kh * MT + i) * (D / 64) + quad) * 32 + lane) * 16, w);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int c = 4 * quad + k;
+                            uint32_t op[4], sc[2];
+                            codes_to_f16<E2M1>(E2M1 ? swap_halves(w[k]) : w[k], op);
+                            scales_to_f16(sw[c], sc[0], sc[1]);
+#pragma unroll
+                            for (int n = 0; n < NT; ++n) {
+                                const uint32_t b0 = mul_f16x2(pf[n][0], sc[0]), b1 = mul_f16x2(pf[n][1], sc[1]);
+                                mma_f16(st.o[n][c], op, b0, b1);
+                                if (!E2M1) {
+                                    const uint32_t eight[4] = {0x80088008u, 0x80808080u, 0x80088008u, 0x80808080u};
+                                    mma_f16(st.o[n][c], eight, b0, b1);
+                                }
+                            }
+                        }
+                    }
+                }
+                release();
+            }
+
+            // ---- the segment's rows: sums over the lanes, and the codes' units out of the outputs
+            const float unit = exp2f(a.v_exp + (E2M1 ? 0.f : 24.f)), unit8 = E2M1 ? unit : unit * 0.0625f;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    st.M[n][e] = st.m[n][e];
+#pragma unroll
+                    for (int sh = 4; sh < 32; sh <<= 1)
+                        st.l[n][e] += __shfl_xor_sync(0xffffffffu, st.l[n][e], sh);
+                }
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) st.o[n][i][e] *= e < 2 ? unit : unit8;
+            }
+            const auto put = [&](float* base) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int row = 8 * (NT * rt + n) + 2 * t + e;
+                        if (row >= a.rows) continue;
+                        float* to = base + row * STRIDE;
+#pragma unroll
+                        for (int i = 0; i < D / 16; ++i) {
+                            to[16 * i + g] = st.o[n][i][e];
+                            to[16 * i + 8 + g] = st.o[n][i][2 + e];
+                        }
+                        if (g == 0)
+                            *reinterpret_cast<float4*>(to + D) = make_float4(st.m[n][e], st.l[n][e], st.M[n][e], 0.f);
+                    }
+            };
+            // A head of the team's alone is finished; else its part is left in global
+            // memory for the merge kernel, or, of the CTA's own head, in shared memory:
+            // the first warp's rows in the slot, the second's in the ring, which is empty.
+            const bool whole = at.j == 0 && j1 == at.tiles, final = at.left <= span_of(at.tiles) - at.j;
+            const bool apart = C::KS == 2 && by_head && !whole;
+            float* to = whole || by_head
+                            ? slot : part_of<D>(a, deal, me * teams + team, share_end - at.left - at.j);
+            if (C::KS == 2 && !apart && kh == 1) put(slot);
+            if (C::KS == 1 || (apart && kh == 0)) put(to);
+            ok = named_bar_and(1 + team, team_threads, ok && !*abort_flag);
+            if (!ok) break;
+            if (apart) {
+                if (kh == 1) put(reinterpret_cast<float*>(smem + (size_t)team * a.stages * STAGE));
+            } else if constexpr (C::KS == 2) {
+                if (kh == 0) {
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int row = 8 * (NT * rt + n) + 2 * t + e;
+                            if (row >= a.rows) continue;
+                            const float* from = slot + row * STRIDE;
+                            const float4 x = *reinterpret_cast<const float4*>(from + D);
+                            const float m = fmaxf(st.m[n][e], x.x), M = fmaxf(st.M[n][e], x.z);
+                            const float oa = part_weight(st.M[n][e], M), ob = part_weight(x.z, M);
+                            st.l[n][e] = st.l[n][e] * part_weight(st.m[n][e], m) + x.y * part_weight(x.x, m);
+                            st.m[n][e] = m;
+                            st.M[n][e] = M;
+#pragma unroll
+                            for (int i = 0; i < D / 16; ++i) {
+                                st.o[n][i][e] = st.o[n][i][e] * oa + from[16 * i + g] * ob;
+                                st.o[n][i][2 + e] = st.o[n][i][2 + e] * oa + from[16 * i + 8 + g] * ob;
+                            }
+                        }
+                    __syncwarp();
+                    put(to);
+                }
+                if (whole || !final) named_bar_sync(1 + team, team_threads);   // (the slot may be written again)
+            }
+            if (whole) {
+                if (a.gate_mode != GSDPA_GATE_NONE) pdl_wait();   // the gate logits
+                for (int idx = team_tid; idx < a.rows * (D / 4); idx += team_threads) {
+                    const int row = idx / (D / 4), col = 4 * (idx % (D / 4));
+                    const float* from = slot + row * STRIDE;
+                    const float4 x = *reinterpret_cast<const float4*>(from + D);
+                    finish<D>(a, at.b, at.kvh, q.n, row, col, out_scale(x.x, x.y, x.z),
+                              *reinterpret_cast<const float4*>(from + col), gate_of<D>(a, at.b, at.kvh, q.n, row, col));
+                }
+                if (!final) named_bar_sync(1 + team, team_threads);
+            }
+            at.next_head(a);
+        }
+    }
+
+    pdl_wait();   // the gate logits; and what follows on the stream may rely on the gate kernel having ended
+    const int parts = min(whole_head, teams);   // (of the CTA's own head: more than one, or it is done)
+    if (by_head && named_bar_and(kSlots + 1, kConsumers, ok && !*abort_flag) && parts > 1) {
+        const int items = a.rows * (D / 4), b = me / a.Hkv, n = PagedSeq(a, b).n;
+        // A thread has four columns of a row; its parts are split over lanes that
+        // would be idle (whole warps: items come in sixteens).
+        int lg = 0;
+        while (lg < 3 && (items << (lg + 1)) <= kConsumers) ++lg;
+        for (int idx = tid; idx < items << lg; idx += kConsumers) {
+            const int item = idx >> lg, row = item / (D / 4), col = 4 * (item % (D / 4));
+            const float4 gate = gate_of<D>(a, b, me % a.Hkv, n, row, col);
+            Sums r;
+            r.add(idx & ((1 << lg) - 1), parts * C::KS, 1 << lg, D, col, [&](int i) {
+                return (i < parts ? slots + (size_t)i * a.rows * STRIDE
+                                  : reinterpret_cast<const float*>(smem + (size_t)(i - parts) * a.stages * STAGE)) +
+                       row * STRIDE;
+            });
+            for (int sh = 1; sh < 1 << lg; sh <<= 1) r.join_lane(sh);
+            if ((idx & ((1 << lg) - 1)) == 0)
+                finish<D>(a, b, me % a.Hkv, n, row, col, out_scale(r.m, r.l, r.M), r.o, gate);
+        }
+    }
+
+    // rows that count for no request are zero
+    const auto clear_rows = [&](int from, int to) {
+        const long long words = (long long)a.Hq * D / 8;
+        for (long long i = from * words + tid; i < to * words; i += kConsumers)
+            reinterpret_cast<uint4*>(a.O)[i] = make_uint4(0, 0, 0, 0);
+    };
+    const auto row_at = [&](int b) { return min(max(a.cu[b], 0), a.N); };
+    for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+        const PagedSeq r(a, b);
+        if (!r.ok && tid == 0) atomicOr(a.ctl.err, ERR_CACHE_RANGE);
+        clear_rows(row_at(b) + r.n, row_at(b + 1));
+    }
+    if (blockIdx.x == 0) clear_rows(0, row_at(0));
+    if (blockIdx.x == gridDim.x - 1) clear_rows(row_at(a.B), a.N);
+}
+
+// Shared memory and ring of one problem.
+struct Shape {
+    int NT, R, stages;
+    uint32_t smem;
+};
+Shape shape_of(int rows, int D) {
+    Shape s;
+    s.NT = rows <= 8 ? 1 : 2;
+    s.R = rows <= 16 ? 1 : (rows <= 32 ? 2 : (rows <= 64 ? 4 : 8));
+    const uint32_t merge = (uint32_t)(kSlots / s.R * rows * (D + 4)) * 4;
+    const uint32_t per_stage = (uint32_t)(kSlots / s.R) * half_bytes(D);
+    // as many copies in flight as fit, up to 192 KB
+    s.stages = (int)((kSmemMax - merge) / per_stage);
+    const int most = (int)(196608 / per_stage);
+    if (s.stages > most) s.stages = most;
+    if (s.stages > kMaxStages) s.stages = kMaxStages;
+    if (s.stages > kBars * s.R / kSlots) s.stages = kBars * s.R / kSlots;
+    s.smem = (uint32_t)s.stages * per_stage + merge;
+    return s;
+}
+
+struct Cache4Plan {
+    Problem p{};
+    WorkspacePlan w;   // the gate kernel's part
+    size_t part = 0, total = 0;
+};
+
+int plan_cache4(const gsdpa_cache4* c, int B, int max_pages, int n_rows, int max_new, int d_model, int Hq, int gate_mode,
+                Cache4Plan* out) {
+    const int st = validate_cache4(c);
+    if (st != GSDPA_OK) return st;
+    if (B < 0 || max_pages < 1 || n_rows < 0 || max_new < 1 || Hq < 1 || Hq % c->H_kv != 0) return GSDPA_ERR_INVALID_ARG;
+    if (gate_mode < GSDPA_GATE_NONE || gate_mode > GSDPA_GATE_ELEMENTWISE) return GSDPA_ERR_INVALID_ARG;
+    if (gate_mode != GSDPA_GATE_NONE && d_model < 1) return GSDPA_ERR_INVALID_ARG;
+    if (gate_mode != GSDPA_GATE_NONE && d_model % 8 != 0) return GSDPA_ERR_UNSUPPORTED;
+    if (gate_mode == GSDPA_GATE_HEADWISE && Hq % 8 != 0) return GSDPA_ERR_UNSUPPORTED;
+    const long long rows = (long long)(Hq / c->H_kv) * max_new;
+    if (rows > kMaxRows) return GSDPA_ERR_UNSUPPORTED;
+    // (places are counted in 32 bits, and so are a request's tokens)
+    if (max_pages > 0x7fffffff / kPage - 1) return GSDPA_ERR_UNSUPPORTED;
+    const long long heads = (long long)B * c->H_kv;
+    if (heads > 0x7fffffffLL - 2 * kMaxCtas || heads * (max_pages + kSwitch) > 0x7fffffffLL) return GSDPA_ERR_UNSUPPORTED;
+    if (n_rows > 0x7fffffff / 8) return GSDPA_ERR_UNSUPPORTED;
+    if (B == 0 || n_rows == 0) return GSDPA_OK;   // an empty problem: nothing to plan
+    Cache4Plan& o = *out;
+    Problem& p = o.p;
+    p.B = 1;
+    p.Lq = n_rows;
+    p.d_model = d_model;
+    p.Hq = Hq;
+    p.Hkv = c->H_kv;
+    p.dk = c->d_k;
+    p.gate_mode = gate_mode;
+    p.causal = 1;
+    p.dtype = GSDPA_BF16;
+    size_t off = 0;
+    auto take = [&](size_t bytes) {
+        const size_t at = off;
+        off = (off + bytes + 255) & ~size_t(255);
+        return at;
+    };
+    if (gate_mode != GSDPA_GATE_NONE) plan_gate_rows(p, plan_sms(), &o.w);
+    o.w.gate_part = take(sizeof(float) * (size_t)o.w.gate_splits * o.w.gate_rows * o.w.gate_cols);
+    const size_t part = sizeof(float) * (size_t)rows * (c->d_k + 4);
+    o.part = take(part * plan_sms() * 2 * (kSlots / shape_of((int)rows, c->d_k).R));
+    o.total = off;
+    return GSDPA_OK;
+}
+
+template <int D, bool E2M1, int NT>
+cudaError_t launch(const Cache4Args& a, const Shape& sh, unsigned grid, cudaStream_t s) {
+    static PerDeviceSetup setup;
+    const cudaError_t e = setup_once_per_device(setup, [](int&) {
+        return cudaFuncSetAttribute(cache4_attn_kernel<D, E2M1, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    (int)kSmemMax);
+    });
+    if (e != cudaSuccess) return e;
+    return launch_dependent(cache4_attn_kernel<D, E2M1, NT>, dim3(grid), dim3(Config<D, E2M1, NT>::THREADS), sh.smem, s,
+                            a);
+}
+template <int D, bool E2M1>
+cudaError_t launch(const Cache4Args& a, const Shape& sh, unsigned grid, cudaStream_t s) {
+    return sh.NT == 1 ? launch<D, E2M1, 1>(a, sh, grid, s) : launch<D, E2M1, 2>(a, sh, grid, s);
+}
+
+}  // namespace
+}  // namespace gsdpa
+
+using namespace gsdpa;
+
+extern "C" {
+
+size_t gsdpa_cache4_workspace_bytes(const gsdpa_cache4* cache, int B, int max_pages, int n_rows, int max_new,
+                                    int d_model, int H_q, int gate_mode) {
+    Cache4Plan pl;
+    if (plan_cache4(cache, B, max_pages, n_rows, max_new, d_model, H_q, gate_mode, &pl) != GSDPA_OK) return (size_t)-1;
+    return pl.total;
+}
+
+int gated_sdpa_cache4(const void* X, const void* Q, const gsdpa_cache4* cache, const int* table, const int* lens,
+                      const int* cu, const int* n_new, const void* W_g, void* O, int B, int max_pages, int n_rows,
+                      int max_new, int d_model, int H_q, int gate_mode, void* workspace, size_t workspace_bytes,
+                      void* stream) {
+    Cache4Plan pl;
+    int st = plan_cache4(cache, B, max_pages, n_rows, max_new, d_model, H_q, gate_mode, &pl);
+    if (st != GSDPA_OK) return st;
+    if (n_rows == 0) return GSDPA_OK;
+    if ((st = validate_cache4_pointers(cache)) != GSDPA_OK) return st;
+    const bool gated = gate_mode != GSDPA_GATE_NONE;
+    if (!Q || !O || (B > 0 && (!table || !lens || !cu)) || (gated && (!X || !W_g))) return GSDPA_ERR_INVALID_ARG;
+    const auto off = [](const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) != 0; };
+    if (off(Q, 16) || off(O, 16) || (gated && (off(X, 16) || off(W_g, 16)))) return GSDPA_ERR_ALIGNMENT;
+    if (off(table, 4) || off(lens, 4) || off(cu, 4) || off(n_new, 4)) return GSDPA_ERR_ALIGNMENT;
+    Runtime rt;
+    int major = 0, minor = 0;
+    if (!current_runtime(&rt, &major, &minor)) return GSDPA_ERR_LAUNCH;
+    if (!(major == 10 && minor == 3) || !encode_tiled_fn()) return GSDPA_ERR_UNSUPPORTED;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (B == 0)   // rows of no request
+        return cudaMemsetAsync(O, 0, (size_t)n_rows * H_q * cache->d_k * 2, s) == cudaSuccess ? GSDPA_OK : GSDPA_ERR_LAUNCH;
+    if (!workspace || workspace_bytes < pl.total) return GSDPA_ERR_WORKSPACE;
+    if (off(workspace, 256)) return GSDPA_ERR_ALIGNMENT;
+    char* ws = static_cast<char*>(workspace);
+    pl.p.X = X;
+    pl.p.Wg = W_g;
+
+    // The gate logits' kernel first: it waits for the kernels before it and then lets
+    // the attention, its programmatic dependent, start: that finds the cache and the
+    // queries written and waits for the logits where it reads them.
+    const int sms = rt.num_sms < kMaxCtas ? rt.num_sms : kMaxCtas;
+    bool launched = false;
+    cudaError_t e = launch_gate_logits_bf16(pl.p, pl.w, ws, rt, s, &launched, ZeroJob());
+    if (e == cudaErrorInvalidValue) return GSDPA_ERR_INVALID_ARG;
+    if (e != cudaSuccess) return GSDPA_ERR_LAUNCH;
+
+    Cache4Args a;
+    a.Q = static_cast<const __nv_bfloat16*>(Q);
+    a.O = static_cast<__nv_bfloat16*>(O);
+    a.table = table;
+    a.lens = lens;
+    a.cu = cu;
+    a.n_new = n_new;
+    a.pool = static_cast<const uint8_t*>(cache->pool);
+    a.B = B;
+    a.N = n_rows;
+    a.max_new = max_new;
+    a.Hq = H_q;
+    a.Hkv = cache->H_kv;
+    a.G = H_q / cache->H_kv;
+    a.g_inverse = (65536 + a.G - 1) / a.G;
+    a.rows = a.G * max_new;
+    a.width = max_pages;
+    a.n_pages = cache->n_pages;
+    const Shape sh = shape_of(a.rows, cache->d_k);
+    a.R = sh.R;
+    a.lg_teams = sh.R == 1 ? 3 : (sh.R == 2 ? 2 : (sh.R == 4 ? 1 : 0));
+    a.stages = sh.stages;
+    a.k_up = ldexpf(1.f, cache->k_exp);
+    a.v_exp = (float)cache->v_exp;
+    a.gate_part = gated ? reinterpret_cast<const float*>(ws + pl.w.gate_part) : nullptr;
+    a.gate_splits = pl.w.gate_splits;
+    a.gate_cols = pl.w.gate_cols;
+    a.gate_mode = gate_mode;
+    a.part = reinterpret_cast<float*>(ws + pl.part);
+    a.wait_first = launched ? 0 : 1;
+    a.ctl.err = rt.err;
+    a.ctl.limit_ns = rt.limit_ns;
+    // one CTA per SM, fewer where full tables would not give each its tiles
+    const long long most = (long long)B * a.Hkv * ((max_pages + kSlots / a.R - 1) / (kSlots / a.R));
+    long long grid = sms;   // (no fewer than the heads, where those fit)
+    if (grid > most) grid = most;
+    a.ctas = (int)grid;
+    const bool whole = max_pages <= kWholeTiles << a.lg_teams && (long long)B * a.Hkv <= grid;
+    a.whole_tiles = (whole ? kWholeTiles : kFewTiles) << a.lg_teams;
+    const bool e2m1 = cache->kind == GSDPA_CACHE_E2M1;
+    if (cache->d_k == 128)
+        e = e2m1 ? launch<128, true>(a, sh, (unsigned)grid, s) : launch<128, false>(a, sh, (unsigned)grid, s);
+    else
+        e = e2m1 ? launch<64, true>(a, sh, (unsigned)grid, s) : launch<64, false>(a, sh, (unsigned)grid, s);
+    // (Not a CTA for every SM: the SMs that are done first take them all, and they are
+    // set up when the last are done.)
+    if (e == cudaSuccess && !whole)
+        e = launch_dependent(cache->d_k == 128 ? cache_merge_kernel<128, Cache4Args> : cache_merge_kernel<64, Cache4Args>,
+                             dim3((unsigned)(sms - sms / 8)), dim3(kMergeThreads), 0, s, a);
+    return e == cudaSuccess ? GSDPA_OK : GSDPA_ERR_LAUNCH;
+}
+
+}  // extern "C"

@@ -517,10 +517,138 @@ GSDPA_API int gated_sdpa_cache8(const void* X, const void* Q, const gsdpa_cache8
                    void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * A K/V cache held in 4 bits, in pages of 64 tokens that any sequence may take
+ * ("GatedAttention [2025]", sec. 1.3.1: the grouped-query cache is what decode
+ * reads). The caller owns the pool; the struct (on the host) describes it and its
+ * contents are copied at each call.
+ *   pool    : device uint8 [n_pages, H_kv, 72 d_k], 16-byte aligned. Nothing needs to be
+ *             initialised. Token p % 64 of page s / 64 is slot s = 64 page + p % 64.
+ *   kind    : GSDPA_CACHE_INT4 (integers -7 .. 7) or GSDPA_CACHE_E2M1 (4-bit floating
+ *             point: 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives).
+ *   k_exp, v_exp : -64 .. 64. Every 16 columns of a token's key (value) have a scale
+ *             with 4 exponent and 3 mantissa bits (e4m3, up to 448): a code stands for
+ *             code * scale * 2^k_exp (2^v_exp), which is exact in bfloat16. They put the
+ *             data's largest magnitudes, over 6 or 7, below 448: larger ones are cut off
+ *             there, groups whose largest magnitude is under 2^exp 2^-10 times 6 or 7 become
+ *             zero.   d_k : 64 or 128.
+ * Of one page and head, in bytes: key codes [64][d_k / 2], key scales [64][d_k / 16],
+ * value codes [4][d_k / 64][8][4][4] words, value scales [4][4][d_k / 16] words. A key's
+ * byte t d_k / 8 + 2 j + p (e2m1) holds columns 16 j + 4 t + 2 p and the one after it,
+ * the first in the low 4 bits; int4 has bit 16 s + 4 (2 (j % 2) + p) of the 32-bit
+ * word at t d_k / 8 + 4 (j / 2) for column 16 j + 4 t + 2 p + s, and code + 8. The value
+ * word [n / 16][j / 4][g][t][j % 4] has columns 16 j + g (low 4 bits) and 16 j + 8 + g of
+ * tokens n % 16 = 2 t, 2 t + 1, 2 t + 8, 2 t + 9 in bytes 0, 1, 2, 3 (e2m1) or 0, 2, 1, 3
+ * (int4), the scale word [n / 16][t][j] their scales in bytes 0, 1, 2, 3.
+ */
+typedef enum { GSDPA_CACHE_INT4 = 0, GSDPA_CACHE_E2M1 = 1 } gsdpa_cache4_kind;
+typedef struct {
+    int kind, n_pages, H_kv, d_k, k_exp, v_exp;
+    void* pool;
+} gsdpa_cache4;
+
+/*
+ * The plan of a step: pages for the tokens that the requests bring, the block table
+ * brought up to date, and for every token of the step, packed request after request,
+ * its slot and position. Request b holds lens[b] tokens; it goes back to keep[b] of
+ * them (drafts that were not accepted; 0 ends it) and then takes n_new[b] more.
+ *   lens, n_new : device int32 [B].    keep : device int32 [B], or NULL for lens.
+ *   table       : device int32 [B, max_pages], in and out: the pages of request b in
+ *                 the order of its tokens. Entries past a request's pages mean nothing.
+ *   free_pages  : device int32 [n_pages], n_free : device int32 [1]: the pages that no
+ *                 request has, free_pages[0 .. n_free), last in first out. n_free_out,
+ *                 device int32 [1], is what is left; it may be n_free.
+ *   cu          : out, int32 [B + 1]: request b's tokens are rows cu[b] .. cu[b + 1].
+ *   granted     : out, int32 [B]: n_new[b], or 0 where the pages did not suffice. Pages
+ *                 are taken in the requests' order: a request gets its own if it needs
+ *                 none or if the needs up to and with it fit what is free (pages given
+ *                 back in this call among it, request after request, in order).
+ *   slots       : out, int64 [n_rows], -1 for tokens that were not granted and rows from
+ *                 cu[B] on.    positions : out, int32 [n_rows] (there 0), or NULL.
+ * lens is not changed: set it to keep + granted once, after the last layer's attention
+ * (until then keep is what the attention takes as lens). A request whose numbers are out of range
+ * (negative, keep > lens, more than 64 max_pages tokens, rows past n_rows) is left as
+ * it was, with granted 0 (a negative n_new has no rows), and the next
+ * gsdpa_check_device_error returns GSDPA_ERR_CACHE_RANGE; so does a page number
+ * outside the pool, whose tokens get slot -1. B <= 8192 (GSDPA_ERR_UNSUPPORTED
+ * otherwise). Repeated on the same contents it gives the same result, bit for bit.
+ * Asynchronous on `stream`; sm_103 device; no workspace.
+ */
+GSDPA_API int gsdpa_pages_step(const int* lens, const int* keep, const int* n_new, int* table, int* free_pages,
+                   const int* n_free, int* n_free_out, int* cu, int* granted, long long* slots, int* positions,
+                   int B, int max_pages, int n_pages, int n_rows, void* stream);
+
+/*
+ * Writes keys and values of n_rows tokens to their slots.
+ *   K, V  : device bf16 [n_rows, H_kv, d_k], heads contiguous, rows ld_k, ld_v elements
+ *           apart (multiples of 8, >= H_kv d_k), 16-byte aligned.
+ *   slots : device int64 [n_rows], different ones (of two equal ones either may be
+ *           kept, or bytes of both); negative ones are passed over.
+ * Every 16 columns of a token, with amax their largest |x| and top = 7 (int4) or 6
+ * (e2m1): scale = e4m3 nearest to amax 2^-exp (1 / top), reciprocal and product rounded to
+ * float32, ties to even, at most 448; code = x / (scale 2^exp) to nearest (the exact
+ * quotient), ties to even, at most top. Scale 0: codes 0. A
+ * group with a NaN or an infinity: scale NaN, codes 0 (every row that sees its token
+ * becomes NaN). A token is rounded by itself: the contents do not depend on how tokens
+ * were split over calls, and other tokens' bytes are left as they were. A slot past the
+ * pool is passed over, and the next gsdpa_check_device_error returns
+ * GSDPA_ERR_CACHE_RANGE. Asynchronous on `stream`; sm_103 device.
+ */
+GSDPA_API int gsdpa_cache4_append(const gsdpa_cache4* cache, const void* K, const void* V, long long ld_k,
+                   long long ld_v, const long long* slots, int n_rows, void* stream);
+
+/*
+ * Reads keys and values back from slots, as the bfloat16 numbers that their codes
+ * stand for, exactly: what gated_sdpa_fwd takes for a later piece of a prompt, whose
+ * queries are too many for gated_sdpa_cache4. K, V : out, as for the append (rows
+ * ld_k, ld_v elements apart); rows of negative slots are zero; a slot past the pool
+ * gives a zero row and GSDPA_ERR_CACHE_RANGE from the next gsdpa_check_device_error.
+ */
+GSDPA_API int gsdpa_cache4_read(const gsdpa_cache4* cache, const long long* slots, void* K, void* V,
+                   long long ld_k, long long ld_v, int n_rows, void* stream);
+
+/*
+ * The gated attention of a step's tokens against the cache through the block table,
+ * after their keys and values have been appended. The step's tokens are packed:
+ * request b has rows cu[b] .. cu[b + 1] of Q, X and O, and its row i sees its tokens
+ * 0 .. lens[b] + i.
+ *   Q, O  : device bf16 [n_rows, H_q, d_k]; O overlaps no input.   X : bf16 [n_rows, d_model].
+ *   W_g   : as for gated_sdpa_fwd; gate_mode NONE, HEADWISE or ELEMENTWISE.
+ *   table : device int32 [B, max_pages].   lens : device int32 [B], the tokens BEFORE
+ *           this step.   cu : device int32 [B + 1].   n_new : device int32 [B] (the plan's
+ *           granted), rows of a request that count, or NULL for all. Rows that
+ *           do not count, and rows from cu[B] on, are zero.
+ *   max_new : most rows of a request; (H_q / H_kv) max_new <= 128
+ *           (GSDPA_ERR_UNSUPPORTED otherwise).
+ * H_q a multiple of H_kv; d_model and the headwise gate's H_q multiples of 8. A request
+ * whose numbers are out of range (cu decreasing or past n_rows, more than max_new rows,
+ * more than 64 max_pages tokens) gives zero rows and GSDPA_ERR_CACHE_RANGE from the
+ * next gsdpa_check_device_error; so does a page number outside the pool, and rows that
+ * see one of its tokens become NaN. A page may be in several requests' tables. Tokens
+ * past a request's end are not seen whatever their bytes; a NaN scale among the step's
+ * own keys is seen by the rows that may see it, one among its values by every row of
+ * the request.
+ * Scores, softmax statistics and sums are float32; queries are exact (bf16; elements
+ * under 2^-27 of the row's largest lose bits that weigh less than 2^-35 of it). The
+ * weights are rounded to fp16 twice, before and after they take the value's scale, 11 bits
+ * each. fp16's range ends at 2^-38 W, W the row's largest product of a weight and a page's
+ * largest value scale (rounded up to a power of two, at least 1): a weight is off by no
+ * less than that, nor is its product with a scale.
+ * workspace: gsdpa_cache4_workspace_bytes(...) bytes, 256-byte aligned; calls that
+ * share one must not overlap on the device. Asynchronous on `stream`; other errors as
+ * for gated_sdpa_fwd.
+ */
+GSDPA_API size_t gsdpa_cache4_workspace_bytes(const gsdpa_cache4* cache, int B, int max_pages, int n_rows, int max_new,
+                   int d_model, int H_q, int gate_mode);
+GSDPA_API int gated_sdpa_cache4(const void* X, const void* Q, const gsdpa_cache4* cache, const int* table,
+                   const int* lens, const int* cu, const int* n_new, const void* W_g, void* O, int B, int max_pages,
+                   int n_rows, int max_new, int d_model, int H_q, int gate_mode, void* workspace,
+                   size_t workspace_bytes, void* stream);
+
+/*
  * Synchronises `stream`, then reads and clears the device error word that
- * bounded waits inside the kernels set when they run out, and the 8-bit
- * cache's kernels when a sequence's length or token count does not fit its
- * cache. Returns GSDPA_OK, GSDPA_ERR_DEVICE_TIMEOUT, GSDPA_ERR_CACHE_RANGE (where
+ * bounded waits inside the kernels set when they run out, and the kernels of
+ * the 8-bit and 4-bit caches when a sequence's length or token count, a slot or a
+ * page number does not fit its cache. Returns GSDPA_OK, GSDPA_ERR_DEVICE_TIMEOUT, GSDPA_ERR_CACHE_RANGE (where
  * both have occurred the timeout, and the range error from the next call), or
  * GSDPA_ERR_LAUNCH if the stream itself reports a CUDA error.
  */

@@ -18,8 +18,9 @@
 //         the two tokens' halves of two bytes change places first, four operations a word.
 //   int4  code + 8 as the low bits of a subnormal fp16 number, u 2^-24 or, the next
 //         4 bits, u 2^-20: one AND each and a shift for every two, exact. The 8
-//         comes off in the sums: the keys' start at -8 sum q instead of zero, the values'
-//         take one more product, with the constant -8. (mma takes subnormal operands
+//         comes off in the sums, by one more product of 16 tokens: the keys' start with
+//         their scales times -8 sum q, the values' have one with the constant -8 for
+//         each 16 columns. (mma takes subnormal operands
 //         as they are: measured, products exact.) The factor 16 between the two is in q
 //         for the keys, in the result's columns for the values.
 // A key's scale multiplies the sum over its 16 columns in float32, one product's
@@ -119,11 +120,35 @@ __device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t (&x)[4]) {
     }
 }
 
-// A word of values has bytes [two columns] of two tokens, twice: e2m1 wants bytes of
-// [two tokens] of a column.
-__device__ __forceinline__ uint32_t swap_halves(uint32_t w) {
-    const uint32_t d = (w ^ (w >> 4)) & 0x00f000f0u;
-    return w ^ d ^ (d << 4);
+// A word of values -> the wide operand of its 16 tokens and 16 columns. e2m1: a byte has a
+// column 16 j + g and one 8 further of one token, a pair wants two tokens of one column.
+template <bool E2M1>
+__device__ __forceinline__ void values_to_f16(uint32_t w, uint32_t (&x)[4]) {
+    if constexpr (E2M1) {
+        const uint32_t low = (w & 0x0f0f0f0fu) | (w >> 4 & 0xf0f0f0f0u);    // bytes 0, 2: the columns' low halves
+        const uint32_t high = (w & 0xf0f0f0f0u) | (w << 4 & 0x0f0f0f0fu);   // bytes 1, 3: the high ones
+        asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+            "mov.b32 {a, b, c, d}, %2;\n\t"
+            "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+            "cvt.rn.f16x2.e2m1x2 %1, c;\n\t}"
+            : "=r"(x[0]), "=r"(x[2])
+            : "r"(low));
+        asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+            "mov.b32 {a, b, c, d}, %2;\n\t"
+            "cvt.rn.f16x2.e2m1x2 %0, b;\n\t"
+            "cvt.rn.f16x2.e2m1x2 %1, d;\n\t}"
+            : "=r"(x[1]), "=r"(x[3])
+            : "r"(high));
+    } else {
+        codes_to_f16<false>(w, x);
+    }
+}
+
+// r = operands' product + c.
+__device__ __forceinline__ void mma_f16_from(float (&r)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, float c) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+                 : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c));
 }
 
 // Four scales -> two fp16 pairs.
@@ -134,6 +159,12 @@ __device__ __forceinline__ void scales_to_f16(uint32_t w, uint32_t& lo, uint32_t
         "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
         : "=r"(lo), "=r"(hi)
         : "r"(w));
+}
+// Two scales, a word's half.
+__device__ __forceinline__ uint32_t scale_pair(const uint8_t* from) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(*reinterpret_cast<const uint16_t*>(from)));
+    return r;
 }
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
     const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
@@ -269,10 +300,12 @@ __device__ __forceinline__ void load_row(const __nv_bfloat16* src, int t, uint32
 }
 
 // A bf16 row -> fp16 scaled by a power of two to below 2^15 (int4: the second pair of
-// each product by 1/16 more), and, int4, -8 2^-24 times its sum over each 16
-// columns; returns the factor that undoes the scale.
+// each product by 1/16 more); returns the factor that undoes the scale. int4: off, the
+// narrow operand that gives the codes' 8, -2^-4 times the row's sums over each 16 columns,
+// as two fp16 parts (22 bits): lane t has those of groups 2 t, 2 t + 1 (d_k 64: the
+// first parts in t < 2, the second in t >= 2).
 template <int D, bool E2M1>
-__device__ __forceinline__ float row_to_f16(uint32_t (&w)[D / 16][2], float (&off)[D / 16]) {
+__device__ __forceinline__ float row_to_f16(uint32_t (&w)[D / 16][2], int t, uint32_t (&off)[2]) {
     uint32_t top = 0;
 #pragma unroll
     for (int j = 0; j < D / 16; ++j)
@@ -282,6 +315,7 @@ __device__ __forceinline__ float row_to_f16(uint32_t (&w)[D / 16][2], float (&of
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
     const uint32_t e = min(max(top >> 7, 15u), 252u);   // the largest element's exponent field, so that both factors are
     const float scale = __uint_as_float((268u - e) << 23);
+    float mine[2] = {0.f, 0.f};
 #pragma unroll
     for (int j = 0; j < D / 16; ++j) {
         float sum = 0.f;
@@ -298,8 +332,15 @@ __device__ __forceinline__ float row_to_f16(uint32_t (&w)[D / 16][2], float (&of
         if (!E2M1) {
             sum += __shfl_xor_sync(0xffffffffu, sum, 1);
             sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-            off[j] = sum * -4.76837158203125e-07f;   // -8 2^-24
+            if (j / 2 == (D == 128 ? t : t % 2)) mine[j % 2] = sum * -0.0625f;
         }
+    }
+    if (!E2M1) {
+        const uint32_t hi = pack_f16x2(mine[0], mine[1]);
+        const float2 h = floats(hi);
+        const uint32_t lo = pack_f16x2(mine[0] - h.x, mine[1] - h.y);
+        off[0] = D == 128 || t < 2 ? hi : lo;
+        off[1] = D == 128 ? lo : 0u;
     }
     return __uint_as_float((e - 14u) << 23) * (E2M1 ? 1.f : 16777216.f);
 }
@@ -499,32 +540,20 @@ cache4_attn_kernel(const __grid_constant__ Cache4Args a) {
             const PagedSeq q(a, at.b);
             const int j1 = min(at.tiles, at.j + at.left);   // segment: tiles [at.j, j1) of the head
             uint32_t qf[NT][D / 16][2];
-            float f[NT][2], off[NT][D / 16][2];   // (off: of the lane's two rows, int4)
+            float f[NT][2];
+            uint32_t off[NT][2];
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 const int row = 8 * (NT * rt + n) + g, i = row * a.g_inverse >> 16;
                 load_row<D>(row < a.rows && i < q.n
                                 ? a.Q + (a.token(at.b, i) * a.Hq + (at.kvh - i) * a.G + row) * D : nullptr, t, qf[n]);
-                float sums[D / 16];
-                const float back = row_to_f16<D, E2M1>(qf[n], sums) * unscaled;
+                const float back = row_to_f16<D, E2M1>(qf[n], t, off[n]) * unscaled;
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    f[n][e] = __shfl_sync(0xffffffffu, back, 4 * (2 * t + e));
-                    if (!E2M1) {
-#pragma unroll
-                        for (int j = 0; j < D / 16; ++j) off[n][j][e] = __shfl_sync(0xffffffffu, sums[j], 4 * (2 * t + e));
-                    }
-                }
+                for (int e = 0; e < 2; ++e) f[n][e] = __shfl_sync(0xffffffffu, back, 4 * (2 * t + e));
             }
             st.clear();
             for (int j = at.j; ok && j < j1; ++j) {
                 float s[NT][MT][4];
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int i = 0; i < MT; ++i)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) s[n][i][e] = 0.f;
                 const uint8_t* kt = wait_full();
                 if (!kt) break;
 #pragma unroll
@@ -535,14 +564,28 @@ cache4_attn_kernel(const __grid_constant__ Cache4Args a) {
                     load_words(kt + (n0 + 8) * (D / 2) + t * (D / 8), y);
                     load_words(kt + key_scales_at(D) + n0 * (D / 16), xs);
                     load_words(kt + key_scales_at(D) + (n0 + 8) * (D / 16), ys);
+                    if constexpr (!E2M1) {   // the sums start at -8 times q's
+                        const uint8_t* own = kt + key_scales_at(D) + n0 * (D / 16) + 2 * (D == 128 ? t : t % 2);
+                        const uint32_t ax = scale_pair(own), ay = scale_pair(own + 8 * (D / 16)), op[4] = {ax, ay, ax, ay};
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            mma_f16_from(s[n][i], op, off[n][0], off[n][1], 0.f);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) s[n][i][e] *= 7.62939453125e-06f;   // 2^-17
+                        }
+                    }
+                    uint32_t hx[D / 32], hy[D / 32];
+#pragma unroll
+                    for (int w = 0; w < D / 64; ++w) {
+                        scales_to_f16(xs[w], hx[2 * w], hx[2 * w + 1]);
+                        scales_to_f16(ys[w], hy[2 * w], hy[2 * w + 1]);
+                    }
 #pragma unroll
                     for (int w = 0; w < D / 32; ++w) {   // two groups of columns
-                        uint32_t xc[4], yc[4], hx[2], hy[2];
+                        uint32_t xc[4], yc[4];
                         codes_to_f16<E2M1>(x[w], xc);
                         codes_to_f16<E2M1>(y[w], yc);
-                        scales_to_f16(xs[w / 2], hx[0], hx[1]);
-                        scales_to_f16(ys[w / 2], hy[0], hy[1]);
-                        const float2 fx = floats(hx[w % 2]), fy = floats(hy[w % 2]);
+                        const float2 fx = floats(hx[w]), fy = floats(hy[w]);
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
                             const uint32_t op[4] = {xc[2 * k], yc[2 * k], xc[2 * k + 1], yc[2 * k + 1]};
@@ -551,13 +594,10 @@ cache4_attn_kernel(const __grid_constant__ Cache4Args a) {
                             for (int n = 0; n < NT; ++n) {
                                 const int c = 2 * w + k;
                                 float r[4];
-                                r[0] = r[2] = E2M1 ? 0.f : off[n][c][0];
-                                r[1] = r[3] = E2M1 ? 0.f : off[n][c][1];
-                                mma_f16(r, op, qf[n][c][0], qf[n][c][1]);
-                                s[n][i][0] = fmaf(r[0], kx, s[n][i][0]);
-                                s[n][i][1] = fmaf(r[1], kx, s[n][i][1]);
-                                s[n][i][2] = fmaf(r[2], ky, s[n][i][2]);
-                                s[n][i][3] = fmaf(r[3], ky, s[n][i][3]);
+                                mma_f16_from(r, op, qf[n][c][0], qf[n][c][1], 0.f);
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    s[n][i][e] = E2M1 && c == 0 ? r[e] * (e < 2 ? kx : ky) : fmaf(r[e], e < 2 ? kx : ky, s[n][i][e]);
                             }
                         }
                     }
@@ -605,7 +645,7 @@ cache4_attn_kernel(const __grid_constant__ Cache4Args a) {
                         for (int k = 0; k < 4; ++k) {
                             const int c = 4 * quad + k;
                             uint32_t op[4], sc[2];
-                            codes_to_f16<E2M1>(E2M1 ? swap_halves(w[k]) : w[k], op);
+                            values_to_f16<E2M1>(w[k], op);
                             scales_to_f16(sw[c], sc[0], sc[1]);
 #pragma unroll
                             for (int n = 0; n < NT; ++n) {

@@ -9,12 +9,13 @@
 // up to half a place, and so are ties).
 //
 // Bound by HBM for prompts (4 d bytes in, 1.125 d out per token and head), by latency
-// for a decoding step. A block has 32 rows of one head: it reads them whole,
-// leaves codes and scales in shared memory token by token, and writes what
-// the pages want: a key is 8 d bits of contiguous page, but a value's codes go one
-// byte to each of d / 2 words, whose other bytes are other tokens'. Where the block
-// has all four tokens of a word it writes the word, else bytes, so that tokens next
-// to each other can be written by different blocks and calls.
+// for a decoding step. A block has some rows of one head: it reads them whole, leaves codes
+// and scales in shared memory token by token, and writes what the pages want: a
+// key is d / 2 bytes in a row, but a value's go one to each of d / 2 words, whose other
+// bytes are other tokens'. A thread has four words next to each other, 16 bytes, for
+// which it turns four tokens' words around; where the block has all four tokens it
+// writes them at once, else their bytes one by one, so that tokens next to each other can be
+// written by different blocks and calls. The reading goes the same way back.
 #include "cache4_internal.h"
 
 #include <cuda_fp16.h>
@@ -23,7 +24,6 @@
 namespace gsdpa {
 namespace {
 
-constexpr int kRows = 32;        // rows of a block: one warp of them
 constexpr int kThreads = 256;
 
 struct RowsArgs {
@@ -33,7 +33,7 @@ struct RowsArgs {
     const long long* slots;
     uint8_t* pool;
     int n_rows, Hkv, n_pages;
-    float k_down, v_down;        // 2^-exp (append), 2^exp (reading)
+    float k_unit, v_unit;        // 2^exp
     uint32_t* err;
 };
 
@@ -44,252 +44,377 @@ __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
     return r;
 }
 
-// Two numbers -> their e2m1 codes, the first in the low 4 bits.
-__device__ __forceinline__ uint32_t to_e2m1x2(float lo, float hi) {
+// Eight quotients -> their e2m1 codes, the first in the low 4 bits.
+__device__ __forceinline__ uint32_t to_e2m1x8(const float (&y)[8]) {
     uint32_t r;
-    asm("{\n\t.reg .b8 t;\n\tcvt.rn.satfinite.e2m1x2.f32 t, %2, %1;\n\tcvt.u32.u8 %0, t;\n\t}" : "=r"(r) : "f"(lo), "f"(hi));
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+        "mov.b32 %0, {a, b, c, d};\n\t}"
+        : "=r"(r)
+        : "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]), "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7]));
     return r;
 }
-__device__ __forceinline__ uint32_t to_int4(float y) {
-    return (uint32_t)(min(max(__float2int_rn(y), -7), 7) + 8);
+// ... -> rounded to whole numbers -7 .. 7, plus 8: added to 1.5 2^23 + 8 a number is rounded
+// to even and stands in the low bits.
+__device__ __forceinline__ uint32_t to_int4x8(const float (&y)[8]) {
+    uint32_t r = 0;
+#pragma unroll
+    for (int k = 7; k >= 0; --k) r = r * 16 + __float_as_uint(fminf(fmaxf(y[k], -7.f), 7.f) + 12582920.f);
+    return r - 0x4b400000u * 0x11111111u;
 }
 
-// Eight columns, half of a group (the other half is the neighbouring lane's) -> eight
-// codes, 4 bits each, and the group's scale.
+using Pair = unsigned long long;   // two float32 numbers
+__device__ __forceinline__ Pair pair_of(float lo, float hi) {
+    Pair r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
+    Pair r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+    Pair r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+// The 16 columns of a group -> their codes, 4 bits each, and the scale.
 template <bool E2M1>
-__device__ __forceinline__ uint32_t quantise(const uint4& x, float down, uint32_t& scale) {
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+__device__ __forceinline__ void quantise(const uint4 (&x)[2], float unit, uint32_t (&codes)[2], uint32_t& scale) {
+    const uint32_t w[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
     uint32_t top = 0;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) top = max_bf16x2(top, w[k] & 0x7fff7fffu);
-    top = max_bf16x2(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    const float amax = fmaxf(__uint_as_float(top << 16), __uint_as_float(top & 0xffff0000u));
+    for (int k = 0; k < 8; ++k) top = max_bf16x2(top, w[k] & 0x7fff7fffu);
     const bool number = (top & 0x7fff) < 0x7f80 && (top >> 16) < 0x7f80;   // (no NaN, no infinity)
+    const float amax = fmaxf(__uint_as_float(top << 16), __uint_as_float(top & 0xffff0000u));
+    const float down = __uint_as_float(0x7f000000u - __float_as_uint(unit));   // 1 / unit
     const __nv_fp8_storage_t byte = __nv_cvt_float_to_fp8(amax * down * (1.f / (E2M1 ? 6.f : 7.f)), __NV_SATFINITE, __NV_E4M3);
     scale = number ? byte : 0x7fu;
+    codes[0] = codes[1] = E2M1 ? 0u : 0x88888888u;
+    if (!number || byte == 0) return;
     const float s = __half2float(__half(__nv_cvt_fp8_to_halfraw(byte, __NV_E4M3)));
-    if (!number || byte == 0) return E2M1 ? 0u : 0x88888888u;
-    const float inv = __frcp_rn(s);
-    // (an infinite quotient, of a scale cut off at 448, has no correction)
-    const auto over = [&](uint32_t bits) {
-        const float v = __uint_as_float(bits) * down, y = v * inv;
-        return fabsf(y) <= 16.f ? fmaf(fmaf(-y, s, v), inv, y) : y;
-    };
-    uint32_t codes = 0;
+    const float step = s * unit, inv = __fdividef(1.f, s) * down;   // (the powers of two: exact)
+    const Pair inv2 = pair_of(inv, inv), step2 = pair_of(-step, -step);
+    Pair y[8];
+    const bool far = amax * inv > 1024.f;   // (a scale cut off at 448 under numbers far above: the step may overflow)
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const float lo = over(w[k] << 16), hi = over(w[k] & 0xffff0000u);
-        codes |= (E2M1 ? to_e2m1x2(lo, hi) : to_int4(lo) | to_int4(hi) << 4) << (8 * k);
+    for (int k = 0; k < 8; ++k) {
+        const Pair v = pair_of(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xffff0000u));
+        y[k] = mul2(v, inv2);
+        if (!far) y[k] = fma2(fma2(y[k], step2, v), inv2, y[k]);
     }
-    return codes;
-}
-
-// Where code c (0 .. 7) of columns 8 half .. of group j goes: byte of a token's key
-// row, and which 4 bits.
-template <int D, bool E2M1>
-__device__ __forceinline__ void key_place(int j, int half, int c, int& byte, int& high) {
-    const int r = 8 * half + c, t = r / 4, pair = r / 2 % 2, side = r % 2;
-    if (E2M1) {
-        byte = t * (D / 8) + 2 * j + pair;
-        high = side;
-    } else {
-        byte = t * (D / 8) + 4 * (j / 2) + 2 * side + j % 2;
-        high = pair;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        float q[8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) asm("mov.b64 {%0, %1}, %2;" : "=f"(q[2 * k]), "=f"(q[2 * k + 1]) : "l"(y[4 * h + k]));
+        codes[h] = E2M1 ? to_e2m1x8(q) : to_int4x8(q);
     }
 }
 
-// 4-bit places 0 .. 7 of a word in another order.
-__device__ __forceinline__ uint32_t nibble(uint32_t codes, int k) { return codes >> (4 * k) & 15u; }
+// Byte b of words 0 .. 3 -> byte 0 .. 3 of word b.
+__device__ __forceinline__ void turn_bytes(uint32_t (&w)[4]) {
+    const uint32_t a = __byte_perm(w[0], w[1], 0x5140), b = __byte_perm(w[2], w[3], 0x5140);
+    const uint32_t c = __byte_perm(w[0], w[1], 0x7362), d = __byte_perm(w[2], w[3], 0x7362);
+    w[0] = __byte_perm(a, b, 0x5410);
+    w[1] = __byte_perm(a, b, 0x7632);
+    w[2] = __byte_perm(c, d, 0x5410);
+    w[3] = __byte_perm(c, d, 0x7632);
+}
 
-// Rows of one block: the slot of each, and the runs of rows that lie in one tile of
+// The rows of one block: the slot of each, and the runs of rows that lie in one tile of
 // 16 tokens (a run begins where the tile changes).
+template <int R>
 struct Runs {
-    long long slot[kRows];       // -1: none
-    int lead[kRows];             // row at which this row's run begins
-    signed char at[kRows][16];   // by leading row: the run's row at each place of the tile, or -1
+    long long slot[R];        // -1: none
+    long long tile[R];        // by run: slot / 16
+    int run[R];               // by row
+    signed char at[R][16];    // by run: its row at each place of the tile, or -1
+    int n;                    // runs
+    __device__ __forceinline__ void find(const RowsArgs& a, long long first) {
+        const int tid = threadIdx.x;
+        for (int k = tid; k < R * 4; k += kThreads) reinterpret_cast<uint32_t*>(at)[k] = 0xffffffffu;
+        __syncthreads();
+        if (tid < 32) {
+            const long long row = first + tid;
+            long long s = tid < R && row < a.n_rows ? a.slots[row] : -1;
+            if (s >= (long long)a.n_pages * kPage) {
+                s = -1;
+                atomicOr(a.err, ERR_CACHE_RANGE);
+            }
+            if (s < 0) s = -1;
+            const long long before = __shfl_up_sync(0xffffffffu, s, 1);
+            const bool lead = s >= 0 && (tid == 0 || (s >> 4) != (before >> 4));
+            const uint32_t leads = __ballot_sync(0xffffffffu, lead);
+            const int run_of = __popc(leads & (0xffffffffu >> (31 - tid))) - 1;
+            if (tid < R) {
+                slot[tid] = s;
+                run[tid] = run_of;
+            }
+            if (lead) tile[run_of] = s >> 4;
+            if (s >= 0) at[run_of][s & 15] = (signed char)tid;
+            if (tid == 0) n = __popc(leads);
+        }
+        __syncthreads();
+    }
 };
 
-__device__ __forceinline__ void find_runs(const RowsArgs& a, long long first, Runs& s) {
-    const int tid = threadIdx.x;
-    for (int k = tid; k < kRows * 4; k += kThreads) reinterpret_cast<uint32_t*>(s.at)[k] = 0xffffffffu;
-    __syncthreads();
-    if (tid < 32) {
-        const long long row = first + tid;
-        long long slot = row < a.n_rows ? a.slots[row] : -1;
-        if (slot >= (long long)a.n_pages * kPage) {
-            slot = -1;
-            atomicOr(a.err, ERR_CACHE_RANGE);
-        }
-        if (slot < 0) slot = -1;
-        const long long before = __shfl_up_sync(0xffffffffu, slot, 1);
-        const uint32_t leads = __ballot_sync(0xffffffffu, tid == 0 || (slot >> 4) != (before >> 4));
-        const int lead = 31 - __clz(leads & (0xffffffffu >> (31 - tid)));
-        s.slot[tid] = slot;
-        s.lead[tid] = lead;
-        if (slot >= 0) s.at[lead][slot & 15] = (signed char)tid;
-    }
-    __syncthreads();
-}
+// A block's tokens as bytes: keys as the pages have them, values [quad][g][j % 4], whose rows lie
+// so that four tokens' words 2 t are in different banks.
+template <int D, int R>
+struct Tokens {
+    static constexpr int LDV = D == 128 ? 80 : 48;
+    __align__(16) uint8_t key[R][D / 2];
+    __align__(16) uint8_t value[R][LDV];
+    __align__(16) uint8_t kscale[R][D / 16], vscale[R][D / 16];
+};
 
-template <int D, bool E2M1>
+// The 16-byte pieces of a tile's value codes (quad, g, t) and, behind them, of its scales (t, 4 groups).
+template <int D>
+struct Pieces {
+    static constexpr int CODES = D / 2, ALL = D / 2 + D / 16;
+    int t, from, to;   // lane; first byte of a token's; byte of the page's tile
+    bool scales;
+    __device__ __forceinline__ explicit Pieces(int w) {
+        scales = w >= CODES;
+        if (scales) {
+            t = (w - CODES) / (D / 64);
+            from = 4 * ((w - CODES) % (D / 64));
+        } else {
+            t = w % 4;
+            from = 4 * (w / 4);
+        }
+        to = 16 * (scales ? w - CODES : w);
+    }
+    __device__ __forceinline__ uint8_t* at(uint8_t* page, int tile) const {
+        return page + (scales ? value_scales_at(D) + D * tile : value_codes_at(D) + 8 * D * tile) + to;
+    }
+    // place of the piece's token b, and byte of a word that it has
+    __device__ __forceinline__ int place(int b) const { return 2 * t + (b & 1) + 8 * (b >> 1); }
+    template <bool E2M1>
+    __device__ __forceinline__ int byte(int b) const { return scales || E2M1 ? b : (b >> 1) + 2 * (b & 1); }
+};
+
+template <int D, bool E2M1, int R>
 __global__ void __launch_bounds__(kThreads) cache4_append_kernel(const __grid_constant__ RowsArgs a) {
-    __shared__ Runs runs;
-    __shared__ __align__(16) uint8_t s_key[kRows][D / 2], s_value[kRows][D / 2];   // value: [quad][g][j % 4]
-    __shared__ __align__(16) uint8_t s_kscale[kRows][D / 16], s_vscale[kRows][D / 16];
+    __shared__ Runs<R> runs;
+    __shared__ Tokens<D, R> tok;
     pdl_trigger();
     pdl_wait();
     const int tid = threadIdx.x, h = blockIdx.y;
-    const long long first = (long long)blockIdx.x * kRows;
-    find_runs(a, first, runs);
+    const long long first = (long long)blockIdx.x * R;
+    runs.find(a, first);
 
-    // ---- codes and scales, a lane to eight columns
-    for (int k = tid; k < 2 * kRows * (D / 8); k += kThreads) {
-        const bool value = k >= kRows * (D / 8);
-        const int i = k % (kRows * (D / 8)), r = i / (D / 8), j = i % (D / 8) / 2, half = i % 2;
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (runs.slot[r] >= 0)
-            x = *reinterpret_cast<const uint4*>((value ? a.V + (first + r) * a.ld_v : a.K + (first + r) * a.ld_k) +
-                                                (long long)h * D + 16 * j + 8 * half);
-        uint32_t scale;
-        const uint32_t codes = quantise<E2M1>(x, value ? a.v_down : a.k_down, scale);
-        if (half == 0) (value ? s_vscale : s_kscale)[r][j] = (uint8_t)scale;
-        if (!value) {
-            // e2m1: pairs of columns are pairs of bytes; int4: the sides of a pair are 2 bytes apart
+    // ---- codes and scales, a lane to a group's 16 columns; lanes next to each other have the groups of one token
 #pragma unroll
-            for (int c = 0; c < 8; c += 4) {
-                const int t = 2 * half + c / 4;
-                if (E2M1) {
-                    *reinterpret_cast<uint16_t*>(&s_key[r][t * (D / 8) + 2 * j]) = (uint16_t)(codes >> (4 * c));
-                } else {
-                    uint8_t* to = &s_key[r][t * (D / 8) + 4 * (j / 2) + j % 2];
-                    to[0] = (uint8_t)(nibble(codes, c) | nibble(codes, c + 2) << 4);
-                    to[2] = (uint8_t)(nibble(codes, c + 1) | nibble(codes, c + 3) << 4);
+    for (int k0 = 0; k0 < 2 * R * (D / 16); k0 += kThreads) {
+        const int k = k0 + tid;
+        if (2 * R * (D / 16) < kThreads && k >= 2 * R * (D / 16)) break;   // (whole warps)
+        const bool value = k >= R * (D / 16);
+        const int i = k % (R * (D / 16)), r = i / (D / 16), j = i % (D / 16);
+        uint4 x[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+        if (runs.slot[r] >= 0) {
+            const uint4* from = reinterpret_cast<const uint4*>((value ? a.V + (first + r) * a.ld_v : a.K + (first + r) * a.ld_k) +
+                                                               (long long)h * D + 16 * j);
+            x[0] = from[0];
+            x[1] = from[1];
+        }
+        uint32_t codes[2], scale;
+        quantise<E2M1>(x, value ? a.v_unit : a.k_unit, codes, scale);
+        (value ? tok.vscale : tok.kscale)[r][j] = (uint8_t)scale;
+        if (!value) {
+            if (E2M1) {   // two bytes of each t
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+                    *reinterpret_cast<uint16_t*>(&tok.key[r][t * (D / 8) + 2 * j]) = (uint16_t)(codes[t / 2] >> (16 * (t % 2)));
+            } else {
+                // a word of each t: of this group and its neighbour columns 0 | 2, 0 | 2, 1 | 3, 1 | 3. Lanes
+                // of even groups take those of t = 0, 1.
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const uint32_t d = (codes[c] ^ (codes[c] >> 4)) & 0x00f000f0u;
+                    codes[c] ^= d ^ (d << 4);
                 }
+                const uint32_t other = __shfl_xor_sync(0xffffffffu, j % 2 ? codes[0] : codes[1], 1);
+                const uint32_t even = j % 2 ? other : codes[0], odd = j % 2 ? codes[1] : other;
+                uint8_t* to = &tok.key[r][2 * (j % 2) * (D / 8) + 4 * (j / 2)];
+                *reinterpret_cast<uint32_t*>(to) = __byte_perm(even, odd, 0x5140);
+                *reinterpret_cast<uint32_t*>(to + D / 8) = __byte_perm(even, odd, 0x7362);
             }
         } else {
-            // a byte holds columns g and 8 + g: the two halves' codes
-            const uint32_t other = __shfl_xor_sync(0xffffffffu, codes, 1);
-            const uint32_t lo = half ? other : codes, hi = half ? codes : other;
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const int g = 4 * half + c;
-                s_value[r][j / 4 * 32 + g * 4 + j % 4] = (uint8_t)(nibble(lo, g) | nibble(hi, g) << 4);
+            // bytes of columns g and 8 + g, the even and the odd g; four groups' of one g are a word: lane j % 4 ends
+            // with those of two of the eight
+            uint32_t mine = (codes[0] & 0x0f0f0f0fu) | (codes[1] << 4 & 0xf0f0f0f0u);
+            uint32_t give = (codes[0] >> 4 & 0x0f0f0f0fu) | (codes[1] & 0xf0f0f0f0u);
+            if (j & 1) {
+                const uint32_t x = mine;
+                mine = give;
+                give = x;
             }
+            uint32_t got = __shfl_xor_sync(0xffffffffu, give, 1);
+            const uint32_t lo = j & 1 ? got : mine, hi = j & 1 ? mine : got;
+            mine = __byte_perm(lo, hi, 0x5140);   // two of this lane's g (the first two of its four)
+            give = __byte_perm(lo, hi, 0x7362);
+            if (j & 2) {
+                const uint32_t x = mine;
+                mine = give;
+                give = x;
+            }
+            got = __shfl_xor_sync(0xffffffffu, give, 2);
+            const uint32_t first_two = j & 2 ? got : mine, last_two = j & 2 ? mine : got;
+            uint32_t* to = reinterpret_cast<uint32_t*>(&tok.value[r][j / 4 * 32]) + (j & 1) + 2 * (j & 2);
+            to[0] = __byte_perm(first_two, last_two, 0x5410);
+            to[2] = __byte_perm(first_two, last_two, 0x7632);
         }
     }
     __syncthreads();
 
     // ---- keys: rows of D / 2 bytes, and their scales
     const auto page_of = [&](long long slot) { return a.pool + ((slot / kPage) * a.Hkv + h) * page_bytes(D); };
-    for (int k = tid; k < kRows * (D / 32); k += kThreads) {
+    for (int k = tid; k < R * (D / 32); k += kThreads) {
         const int r = k / (D / 32), c = k % (D / 32);
         const long long slot = runs.slot[r];
         if (slot >= 0)
             *reinterpret_cast<uint4*>(page_of(slot) + (slot % kPage) * (D / 2) + 16 * c) =
-                *reinterpret_cast<const uint4*>(&s_key[r][16 * c]);
+                *reinterpret_cast<const uint4*>(&tok.key[r][16 * c]);
     }
-    for (int k = tid; k < kRows * (D / 64); k += kThreads) {
+    for (int k = tid; k < R * (D / 64); k += kThreads) {
         const int r = k / (D / 64), c = k % (D / 64);
         const long long slot = runs.slot[r];
         if (slot >= 0)
             *reinterpret_cast<uint32_t*>(page_of(slot) + key_scales_at(D) + (slot % kPage) * (D / 16) + 4 * c) =
-                *reinterpret_cast<const uint32_t*>(&s_kscale[r][4 * c]);
+                *reinterpret_cast<const uint32_t*>(&tok.kscale[r][4 * c]);
     }
 
-    // ---- values: words of four tokens, run by run
-    constexpr int WORDS = 2 * D, SCALES = D / 4;   // of a tile
-    for (int k = tid; k < kRows * (WORDS + SCALES); k += kThreads) {
-        const int r = k / (WORDS + SCALES), w = k % (WORDS + SCALES);
-        if (runs.lead[r] != r || runs.slot[r] < 0) continue;
-        const bool scales = w >= WORDS;
-        int t, from;   // lane of the tile's operand, byte of a token
-        if (scales) {
-            t = (w - WORDS) / (D / 16);
-            from = (w - WORDS) % (D / 16);
-        } else {
-            t = w / 4 % 4;
-            from = w / 128 * 32 + w % 128 / 16 * 4 + w % 4;
-        }
-        const int places[4] = {2 * t, 2 * t + 1, 2 * t + 8, 2 * t + 9};
-        uint32_t word = 0;
+    // ---- values: four words of four tokens, run by run
+    using P = Pieces<D>;
+    for (int k = tid; k < runs.n * P::ALL; k += kThreads) {
+        const int run = k / P::ALL;
+        const P p(k % P::ALL);
+        uint32_t w[4];
         int have = 0;
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
-            const int row = runs.at[r][places[b]];
-            const int byte = scales || E2M1 ? b : (b == 1 ? 2 : (b == 2 ? 1 : b));
+            const int row = runs.at[run][p.place(b)], to = p.template byte<E2M1>(b);
+            uint32_t x = 0;
             if (row >= 0) {
-                have |= 1 << byte;
-                word |= (uint32_t)(scales ? s_vscale[row][from] : s_value[row][from]) << (8 * byte);
+                have |= 1 << to;
+                x = *reinterpret_cast<const uint32_t*>(p.scales ? &tok.vscale[row][p.from] : &tok.value[row][p.from]);
             }
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                if (c == to) w[c] = x;
         }
-        const long long slot = runs.slot[r];
-        const int tile = (int)(slot % kPage) / 16;
-        uint8_t* to = page_of(slot) + (scales ? value_scales_at(D) + 4 * (tile * SCALES + w - WORDS)
-                                              : value_codes_at(D) + 4 * (tile * WORDS + w));
+        turn_bytes(w);
+        if (have == 0) continue;
+        uint8_t* to = p.at(page_of(runs.tile[run] * 16), (int)(runs.tile[run] % 4));
         if (have == 15) {
-            *reinterpret_cast<uint32_t*>(to) = word;
+            *reinterpret_cast<uint4*>(to) = make_uint4(w[0], w[1], w[2], w[3]);
         } else {
 #pragma unroll
             for (int b = 0; b < 4; ++b)
-                if (have & (1 << b)) to[b] = (uint8_t)(word >> (8 * b));
+                if (have & (1 << b))
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) to[4 * c + b] = (uint8_t)(w[c] >> (8 * b));
         }
     }
-}
-
-// A code of 4 bits as the number it stands for.
-template <bool E2M1>
-__device__ __forceinline__ float code_value(uint32_t c) {
-    if (!E2M1) return (float)((int)c - 8);
-    const uint32_t m = c & 7u;
-    // exponent 1 + m / 2 of a number whose exponents start at 2^-1, or the subnormal 0 and 0.5
-    const float v = m < 2 ? 0.5f * m : __uint_as_float((126u + m / 2) << 23 | (m & 1u) << 22);
-    return c & 8u ? -v : v;
 }
 
 __device__ __forceinline__ float scale_value(uint32_t byte) {
     return __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)byte, __NV_E4M3)));
 }
+// The two codes of a byte as the numbers they stand for.
+template <bool E2M1>
+__device__ __forceinline__ float2 code_values(uint32_t byte) {
+    if constexpr (E2M1) {
+        uint32_t h;
+        asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, a;\n\t}" : "=r"(h) : "r"(byte));
+        return __half22float2(*reinterpret_cast<const __half2*>(&h));
+    } else {
+        return make_float2((float)((int)(byte & 15u) - 8), (float)((int)(byte >> 4 & 15u) - 8));
+    }
+}
 
-template <int D, bool E2M1>
+template <int D, bool E2M1, int R>
 __global__ void __launch_bounds__(kThreads) cache4_read_kernel(const __grid_constant__ RowsArgs a) {
+    __shared__ Runs<R> runs;
+    __shared__ Tokens<D, R> tok;
     pdl_trigger();
     pdl_wait();
-    const int h = blockIdx.y;
-    const long long first = (long long)blockIdx.x * kRows;
-    for (int k = threadIdx.x; k < 2 * kRows * (D / 8); k += kThreads) {
-        const bool value = k >= kRows * (D / 8);
-        const int i = k % (kRows * (D / 8)), r = i / (D / 8), j = i % (D / 8) / 2, half = i % 2;
-        if (first + r >= a.n_rows) continue;
-        const long long slot = a.slots[first + r];
-        uint32_t out[4] = {0, 0, 0, 0};
-        if (slot >= (long long)a.n_pages * kPage) {
-            atomicOr(a.err, ERR_CACHE_RANGE);
-        } else if (slot >= 0) {
-            const uint8_t* page = a.pool + ((slot / kPage) * a.Hkv + h) * page_bytes(D);
-            const int n = (int)(slot % kPage), t = n % 8 / 2, y = n % 16 / 8, z = n % 2;
-            float s, x[8];
-            if (!value) {
-                s = scale_value(page[key_scales_at(D) + n * (D / 16) + j]) * a.k_down;
+    const int tid = threadIdx.x, h = blockIdx.y;
+    const long long first = (long long)blockIdx.x * R;
+    runs.find(a, first);
+    const auto page_of = [&](long long slot) { return a.pool + ((slot / kPage) * a.Hkv + h) * page_bytes(D); };
+    for (int k = tid; k < R * (D / 32); k += kThreads) {
+        const int r = k / (D / 32), c = k % (D / 32);
+        const long long slot = runs.slot[r];
+        if (slot >= 0)
+            *reinterpret_cast<uint4*>(&tok.key[r][16 * c]) =
+                *reinterpret_cast<const uint4*>(page_of(slot) + (slot % kPage) * (D / 2) + 16 * c);
+    }
+    for (int k = tid; k < R * (D / 64); k += kThreads) {
+        const int r = k / (D / 64), c = k % (D / 64);
+        const long long slot = runs.slot[r];
+        if (slot >= 0)
+            *reinterpret_cast<uint32_t*>(&tok.kscale[r][4 * c]) =
+                *reinterpret_cast<const uint32_t*>(page_of(slot) + key_scales_at(D) + (slot % kPage) * (D / 16) + 4 * c);
+    }
+    using P = Pieces<D>;
+    for (int k = tid; k < runs.n * P::ALL; k += kThreads) {
+        const int run = k / P::ALL;
+        const P p(k % P::ALL);
+        const uint4 x = *reinterpret_cast<const uint4*>(p.at(page_of(runs.tile[run] * 16), (int)(runs.tile[run] % 4)));
+        uint32_t w[4] = {x.x, x.y, x.z, x.w};
+        turn_bytes(w);
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    int byte, high;
-                    key_place<D, E2M1>(j, half, c, byte, high);
-                    x[c] = code_value<E2M1>(page[n * (D / 2) + byte] >> (4 * high) & 15u) * s;
+        for (int b = 0; b < 4; ++b) {
+            const int row = runs.at[run][p.place(b)], of = p.template byte<E2M1>(b);
+            if (row >= 0)
+                *reinterpret_cast<uint32_t*>(p.scales ? &tok.vscale[row][p.from] : &tok.value[row][p.from]) =
+                    of == 0 ? w[0] : (of == 1 ? w[1] : (of == 2 ? w[2] : w[3]));
+        }
+    }
+    __syncthreads();
+
+    // ---- a thread to a group's 16 columns
+    for (int k = tid; k < 2 * R * (D / 16); k += kThreads) {
+        const bool value = k >= R * (D / 16);
+        const int i = k % (R * (D / 16)), r = i / (D / 16), j = i % (D / 16);
+        if (first + r >= a.n_rows) continue;
+        uint32_t out[8] = {};
+        if (runs.slot[r] >= 0) {
+            // (of rows with the same slot the values' bytes are one row's)
+            const int from_row = value ? runs.at[runs.run[r]][runs.slot[r] & 15] : r;
+            const float s = scale_value((value ? tok.vscale : tok.kscale)[from_row][j]) * (value ? a.v_unit : a.k_unit);
+            if (value) {
+                float2 x[8];   // columns g and 8 + g
+#pragma unroll
+                for (int g = 0; g < 8; ++g) x[g] = code_values<E2M1>(tok.value[from_row][j / 4 * 32 + g * 4 + j % 4]);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    out[c] = pack_bf16x2(x[2 * c].x * s, x[2 * c + 1].x * s);
+                    out[4 + c] = pack_bf16x2(x[2 * c].y * s, x[2 * c + 1].y * s);
                 }
             } else {
-                s = scale_value(page[value_scales_at(D) + 4 * ((n / 16 * 4 + t) * (D / 16) + j) + 2 * y + z]) * a.v_down;
-                const int byte = E2M1 ? 2 * y + z : 2 * z + y;
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    const int word = ((n / 16 * (D / 64) + j / 4) * 32 + 4 * c + t) * 4 + j % 4;
-                    x[c] = code_value<E2M1>(page[value_codes_at(D) + 4 * word + byte] >> (4 * half) & 15u) * s;
+                for (int t = 0; t < 4; ++t) {
+                    const uint8_t* from = &tok.key[r][t * (D / 8) + (E2M1 ? 2 * j : 4 * (j / 2) + j % 2)];
+                    const float2 x = code_values<E2M1>(from[0]), y = code_values<E2M1>(from[E2M1 ? 1 : 2]);
+                    // e2m1: columns 0, 1 and 2, 3 of the lane's four; int4: 0, 2 and 1, 3
+                    out[2 * t] = E2M1 ? pack_bf16x2(x.x * s, x.y * s) : pack_bf16x2(x.x * s, y.x * s);
+                    out[2 * t + 1] = E2M1 ? pack_bf16x2(y.x * s, y.y * s) : pack_bf16x2(x.y * s, y.y * s);
                 }
             }
-#pragma unroll
-            for (int c = 0; c < 4; ++c) out[c] = pack_bf16x2(x[2 * c], x[2 * c + 1]);
         }
-        __nv_bfloat16* to = value ? a.Vo + (first + r) * a.ld_v : a.Ko + (first + r) * a.ld_k;
-        *reinterpret_cast<uint4*>(to + (long long)h * D + 16 * j + 8 * half) = make_uint4(out[0], out[1], out[2], out[3]);
+        uint4* to = reinterpret_cast<uint4*>((value ? a.Vo + (first + r) * a.ld_v : a.Ko + (first + r) * a.ld_k) +
+                                             (long long)h * D + 16 * j);
+        to[0] = make_uint4(out[0], out[1], out[2], out[3]);
+        to[1] = make_uint4(out[4], out[5], out[6], out[7]);
     }
 }
 
@@ -314,8 +439,22 @@ int check_rows(const gsdpa_cache4* c, const void* K, const void* V, long long ld
     return GSDPA_OK;
 }
 
-template <typename F>
-int launch_rows(const gsdpa_cache4* c, RowsArgs& a, F launch) {
+template <bool READ, int D, bool E2M1>
+cudaError_t launch(const RowsArgs& a, int sms, cudaStream_t s) {
+    const auto go = [&](auto kernel, int rows) {
+        const dim3 grid((unsigned)((a.n_rows + (long long)rows - 1) / rows), (unsigned)a.Hkv);
+        return launch_dependent(kernel, grid, dim3(kThreads), 0, s, a);
+    };
+    // Blocks of few rows until there are four for every SM.
+    const bool few = (a.n_rows + 31LL) / 32 * a.Hkv < 4LL * sms;
+    if constexpr (READ)
+        return few ? go(cache4_read_kernel<D, E2M1, 8>, 8) : go(cache4_read_kernel<D, E2M1, 32>, 32);
+    else
+        return few ? go(cache4_append_kernel<D, E2M1, 8>, 8) : go(cache4_append_kernel<D, E2M1, 32>, 32);
+}
+
+template <bool READ>
+int launch_rows(const gsdpa_cache4* c, RowsArgs& a, void* stream) {
     Runtime rt;
     int major = 0, minor = 0;
     if (!current_runtime(&rt, &major, &minor)) return GSDPA_ERR_LAUNCH;
@@ -323,9 +462,14 @@ int launch_rows(const gsdpa_cache4* c, RowsArgs& a, F launch) {
     a.pool = static_cast<uint8_t*>(c->pool);
     a.Hkv = c->H_kv;
     a.n_pages = c->n_pages;
+    a.k_unit = ldexpf(1.f, c->k_exp);
+    a.v_unit = ldexpf(1.f, c->v_exp);
     a.err = rt.err;
-    return launch(dim3((unsigned)((a.n_rows + (long long)kRows - 1) / kRows), (unsigned)c->H_kv)) == cudaSuccess
-               ? GSDPA_OK : GSDPA_ERR_LAUNCH;
+    const bool e2m1 = c->kind == GSDPA_CACHE_E2M1;
+    const auto s = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = c->d_k == 128 ? (e2m1 ? launch<READ, 128, true>(a, rt.num_sms, s) : launch<READ, 128, false>(a, rt.num_sms, s))
+                                        : (e2m1 ? launch<READ, 64, true>(a, rt.num_sms, s) : launch<READ, 64, false>(a, rt.num_sms, s));
+    return e == cudaSuccess ? GSDPA_OK : GSDPA_ERR_LAUNCH;
 }
 
 }  // namespace
@@ -355,14 +499,14 @@ int gsdpa_cache4_append(const gsdpa_cache4* cache, const void* K, const void* V,
     bool any;
     const int st = check_rows(cache, K, V, ld_k, ld_v, slots, n_rows, &any);
     if (st != GSDPA_OK || !any) return st;
-    RowsArgs a{static_cast<const __nv_bfloat16*>(K), static_cast<const __nv_bfloat16*>(V), nullptr, nullptr, ld_k, ld_v,
-               slots, nullptr, n_rows, 0, 0, ldexpf(1.f, -cache->k_exp), ldexpf(1.f, -cache->v_exp), nullptr};
-    return launch_rows(cache, a, [&](dim3 grid) {
-        const bool e2m1 = cache->kind == GSDPA_CACHE_E2M1;
-        const auto k = cache->d_k == 128 ? (e2m1 ? cache4_append_kernel<128, true> : cache4_append_kernel<128, false>)
-                                         : (e2m1 ? cache4_append_kernel<64, true> : cache4_append_kernel<64, false>);
-        return launch_dependent(k, grid, dim3(kThreads), 0, static_cast<cudaStream_t>(stream), a);
-    });
+    RowsArgs a{};
+    a.K = static_cast<const __nv_bfloat16*>(K);
+    a.V = static_cast<const __nv_bfloat16*>(V);
+    a.ld_k = ld_k;
+    a.ld_v = ld_v;
+    a.slots = slots;
+    a.n_rows = n_rows;
+    return launch_rows<false>(cache, a, stream);
 }
 
 int gsdpa_cache4_read(const gsdpa_cache4* cache, const long long* slots, void* K, void* V, long long ld_k,
@@ -370,14 +514,14 @@ int gsdpa_cache4_read(const gsdpa_cache4* cache, const long long* slots, void* K
     bool any;
     const int st = check_rows(cache, K, V, ld_k, ld_v, slots, n_rows, &any);
     if (st != GSDPA_OK || !any) return st;
-    RowsArgs a{nullptr, nullptr, static_cast<__nv_bfloat16*>(K), static_cast<__nv_bfloat16*>(V), ld_k, ld_v,
-               slots, nullptr, n_rows, 0, 0, ldexpf(1.f, cache->k_exp), ldexpf(1.f, cache->v_exp), nullptr};
-    return launch_rows(cache, a, [&](dim3 grid) {
-        const bool e2m1 = cache->kind == GSDPA_CACHE_E2M1;
-        const auto k = cache->d_k == 128 ? (e2m1 ? cache4_read_kernel<128, true> : cache4_read_kernel<128, false>)
-                                         : (e2m1 ? cache4_read_kernel<64, true> : cache4_read_kernel<64, false>);
-        return launch_dependent(k, grid, dim3(kThreads), 0, static_cast<cudaStream_t>(stream), a);
-    });
+    RowsArgs a{};
+    a.Ko = static_cast<__nv_bfloat16*>(K);
+    a.Vo = static_cast<__nv_bfloat16*>(V);
+    a.ld_k = ld_k;
+    a.ld_v = ld_v;
+    a.slots = slots;
+    a.n_rows = n_rows;
+    return launch_rows<true>(cache, a, stream);
 }
 
 }  // extern "C"

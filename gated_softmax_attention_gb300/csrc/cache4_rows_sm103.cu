@@ -37,10 +37,10 @@ struct RowsArgs {
     uint32_t* err;
 };
 
-// |x| of two bf16 numbers, larger of each half; NaN wins.
+// Of two pairs of bf16 numbers the larger magnitudes, with some sign; NaN wins.
 __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
     uint32_t r;
-    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
 
@@ -57,12 +57,17 @@ __device__ __forceinline__ uint32_t to_e2m1x8(const float (&y)[8]) {
         : "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]), "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7]));
     return r;
 }
-// ... -> rounded to whole numbers -7 .. 7, plus 8: added to 1.5 2^23 + 8 a number is rounded
-// to even and stands in the low bits.
-__device__ __forceinline__ uint32_t to_int4x8(const float (&y)[8]) {
+// ... -> rounded to whole numbers, plus 8: added to 1.5 2^23 + 8 a number is rounded to
+// even and stands in the low bits. (The largest quotient is at most 7 / (1 - 1 / 17) < 7.5, unless the scale
+// is cut off at 448 or one of the least: `over`.)
+__device__ __forceinline__ uint32_t to_int4x8(float (&y)[8], bool over) {
+    if (over) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) y[k] = fminf(fmaxf(y[k], -7.f), 7.f);
+    }
     uint32_t r = 0;
 #pragma unroll
-    for (int k = 7; k >= 0; --k) r = r * 16 + __float_as_uint(fminf(fmaxf(y[k], -7.f), 7.f) + 12582920.f);
+    for (int k = 7; k >= 0; --k) r = r * 16 + __float_as_uint(y[k] + 12582920.f);
     return r - 0x4b400000u * 0x11111111u;
 }
 
@@ -89,7 +94,8 @@ __device__ __forceinline__ void quantise(const uint4 (&x)[2], float unit, uint32
     const uint32_t w[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
     uint32_t top = 0;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) top = max_bf16x2(top, w[k] & 0x7fff7fffu);
+    for (int k = 0; k < 8; ++k) top = max_bf16x2(top, w[k]);
+    top &= 0x7fff7fffu;
     const bool number = (top & 0x7fff) < 0x7f80 && (top >> 16) < 0x7f80;   // (no NaN, no infinity)
     const float amax = fmaxf(__uint_as_float(top << 16), __uint_as_float(top & 0xffff0000u));
     const float down = __uint_as_float(0x7f000000u - __float_as_uint(unit));   // 1 / unit
@@ -113,7 +119,7 @@ __device__ __forceinline__ void quantise(const uint4 (&x)[2], float unit, uint32
         float q[8];
 #pragma unroll
         for (int k = 0; k < 4; ++k) asm("mov.b64 {%0, %1}, %2;" : "=f"(q[2 * k]), "=f"(q[2 * k + 1]) : "l"(y[4 * h + k]));
-        codes[h] = E2M1 ? to_e2m1x8(q) : to_int4x8(q);
+        codes[h] = E2M1 ? to_e2m1x8(q) : to_int4x8(q, amax * inv > 7.45f);
     }
 }
 
@@ -208,24 +214,35 @@ __global__ void __launch_bounds__(kThreads) cache4_append_kernel(const __grid_co
     pdl_wait();
     const int tid = threadIdx.x, h = blockIdx.y;
     const long long first = (long long)blockIdx.x * R;
-    runs.find(a, first);
-
-    // ---- codes and scales, a lane to a group's 16 columns; lanes next to each other have the groups of one token
+    // ---- a lane has a group's 16 columns; lanes next to each other the groups of one token. All is loaded at once,
+    // before the slots are known.
+    constexpr int GROUPS = 2 * R * (D / 16), EACH = (GROUPS + kThreads - 1) / kThreads;
+    static_assert(GROUPS % kThreads == 0 || GROUPS < kThreads, "whole warps");
+    uint4 x[EACH][2];
 #pragma unroll
-    for (int k0 = 0; k0 < 2 * R * (D / 16); k0 += kThreads) {
-        const int k = k0 + tid;
-        if (2 * R * (D / 16) < kThreads && k >= 2 * R * (D / 16)) break;   // (whole warps)
+    for (int n = 0; n < EACH; ++n) {
+        const int k = n * kThreads + tid;
         const bool value = k >= R * (D / 16);
         const int i = k % (R * (D / 16)), r = i / (D / 16), j = i % (D / 16);
-        uint4 x[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-        if (runs.slot[r] >= 0) {
+        x[n][0] = x[n][1] = make_uint4(0, 0, 0, 0);
+        if (k < GROUPS && first + r < a.n_rows) {
             const uint4* from = reinterpret_cast<const uint4*>((value ? a.V + (first + r) * a.ld_v : a.K + (first + r) * a.ld_k) +
                                                                (long long)h * D + 16 * j);
-            x[0] = from[0];
-            x[1] = from[1];
+            x[n][0] = from[0];
+            x[n][1] = from[1];
         }
+    }
+    runs.find(a, first);
+
+    // ---- codes and scales
+#pragma unroll
+    for (int n = 0; n < EACH; ++n) {
+        const int k = n * kThreads + tid;
+        if (k >= GROUPS) break;
+        const bool value = k >= R * (D / 16);
+        const int i = k % (R * (D / 16)), r = i / (D / 16), j = i % (D / 16);
         uint32_t codes[2], scale;
-        quantise<E2M1>(x, value ? a.v_unit : a.k_unit, codes, scale);
+        quantise<E2M1>(x[n], value ? a.v_unit : a.k_unit, codes, scale);
         (value ? tok.vscale : tok.kscale)[r][j] = (uint8_t)scale;
         if (!value) {
             if (E2M1) {   // two bytes of each t

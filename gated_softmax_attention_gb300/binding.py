@@ -987,9 +987,10 @@ def pages_step(lens, n_new, table, free_pages, n_free, n_rows, *, keep=None, out
     if out is None:
         if not table.is_cuda:
             raise ValueError(f"table must be a CUDA tensor, not on {table.device}")
-        flat = torch.empty(2 * B + 2 + n_rows, dtype=i32, device=dev)
-        cu, granted, left, positions = flat.split((B + 1, B, 1, n_rows))
-        out = PagesStep(cu, granted, torch.empty(n_rows, dtype=torch.int64, device=dev), positions, left)
+        # (one allocation and slices of it: the host's time of a step is longer than the kernel's)
+        flat = table.new_empty(2 * B + 2 + n_rows)
+        out = PagesStep(flat[:B + 1], flat[B + 1:2 * B + 1], torch.empty(n_rows, dtype=torch.int64, device=dev),
+                        flat[2 * B + 2:], flat[2 * B + 1:2 * B + 2])
     st = (_lib or load()).gsdpa_pages_step(
         _vector(lens, "lens", B, i32, dev), _vector(keep, "keep", B, i32, dev), _vector(n_new, "n_new", B, i32, dev),
         _vector(table, "table", B * width, i32, dev), _vector(free_pages, "free_pages", free_pages.numel(), i32, dev),
@@ -1004,13 +1005,20 @@ def pages_step(lens, n_new, table, free_pages, n_free, n_rows, *, keep=None, out
 
 
 def _token_rows(t, name, N, cache):
-    """The row length of t [N, H_kv, d_k] (heads contiguous, rows evenly spaced)."""
+    """The row length of t [N, H_kv, d_k] bfloat16 (heads contiguous, rows evenly spaced)."""
     import torch
+    H, d = cache.H_kv, cache.d_k
+    if t is not None and t.dtype is torch.bfloat16 and t.shape == (N, H, d) and t.device == cache.device:
+        if t.is_contiguous():
+            return H * d
+        ld, head, col = t.stride()
+        if col == 1 and head == d and ld >= H * d and N > 1:
+            return ld
     if t is None:
         raise ValueError(f"{name} is required")
     if t.dim() != 3:
         raise ValueError(f"{name} {tuple(t.shape)} must be [n_rows, H_kv, d_k]")
-    return _head_rows(t.unsqueeze(0), name, (1, N, cache.H_kv, cache.d_k), torch.bfloat16, cache.device)
+    return _head_rows(t.unsqueeze(0), name, (1, N, H, d), torch.bfloat16, cache.device)   # says which
 
 
 @_on_stream

@@ -46,8 +46,8 @@ namespace gsdpa {
 namespace {
 
 constexpr int kMaxStages = 16;       // ring stages per team
-constexpr int kBars = 48;            // ring stages of all teams
-constexpr uint32_t kSmemMax = 232448 - 1984;   // dynamic: what a CTA may have, less barriers, parts and a few words
+constexpr int kBars = 96;            // ring stages of all teams
+constexpr uint32_t kSmemMax = 232448 - 4608;   // dynamic: what a CTA may have, less barriers, parts and a few words
 // A head is one CTA's where all have at most this many tiles for each team of it (by
 // the table's width, then by the lengths) and there are CTAs for all.
 constexpr int kWholeTiles = 3, kFewTiles = 1;
@@ -56,6 +56,7 @@ constexpr float kUp = 13.0f, kMove = 2.0f;     // where m stands, and how far a 
 struct PagedSeq;
 struct Cache4Args {
     using Seq = PagedSeq;
+    static constexpr bool kJoins = true;   // a CTA whose share is one head's leaves one part
     __device__ __forceinline__ long long token(int b, int i) const { return (long long)cu[b] + i; }
     __device__ __forceinline__ long long tokens() const { return N; }
     const __nv_bfloat16* Q;          // [N, Hq, D]
@@ -66,7 +67,7 @@ struct Cache4Args {
     int g_inverse;                   // 65536 / G, rounded up: row / G is row * g_inverse >> 16 for the rows there are
     int rows;                        // G * max_new
     int width, n_pages;              // pages of a request's row of the table; of the pool
-    int lg_teams;                    // teams of a CTA, 2^lg_teams = 8 / R
+    int lg_teams;                    // teams of a CTA, 2^lg_teams: 16, or 8 / R
     int R, stages;                   // groups of query rows (of 8 NT) to a team; ring stages per team
     float k_up;                      // 2^k_exp
     float v_exp;
@@ -75,6 +76,7 @@ struct Cache4Args {
     float* part;                     // [CTAs][teams][2][rows][D + 4]: a team's first and last head, where cut
     int ctas;                        // of the attention kernel
     int whole_tiles;                 // most tiles of a head for one CTA to take it alone
+    int whole;                       // that many at most by the table's width: a head is one CTA's
     int wait_first;                  // no gate kernel: everything before this kernel is waited for at once
     WaitCtl ctl;
 };
@@ -345,40 +347,138 @@ __device__ __forceinline__ float row_to_f16(uint32_t (&w)[D / 16][2], int t, uin
     return __uint_as_float((e - 14u) << 23) * (E2M1 ? 1.f : 16777216.f);
 }
 
-template <int D, bool E2M1, int NT>
+// The finished rows of a head that a warp has alone: element 2 x + e of o[i] is column
+// 16 i + 8 x + g of row 2 t + e. Turned around by shuffles, so that a lane has columns 2 t, 2 t + 1
+// of row g, times the gate, stored.
+template <int D>
+__device__ __forceinline__ void finish_warp(const Cache4Args& a, int b, int kvh, int n, int lane,
+                                            const float (&o)[D / 16][4]) {
+    const int row = lane >> 2, t = lane & 3, i = row * a.g_inverse >> 16;
+    const bool live = row < a.rows && i < n;
+    const int h = live ? (kvh - i) * a.G + row : 0;   // kvh G + row % G
+    const long long token = live ? a.token(b, i) : 0;
+    const bool gated = a.gate_mode != GSDPA_GATE_NONE, per_col = a.gate_mode == GSDPA_GATE_ELEMENTWISE;
+    const long long step = a.tokens() * a.gate_cols;
+    const float* gp = gated ? a.gate_part + token * a.gate_cols + (per_col ? (long long)h * D + 2 * t : h) : nullptr;
+    float2 gate = make_float2(1.f, 1.f);
+    if (gated) pdl_wait();   // the gate logits
+    if (gated && !per_col && live) {
+        float gl = 0.f;
+        for (int sp = 0; sp < a.gate_splits; ++sp) gl += gp[sp * step];
+        gate.x = gate.y = sigmoid(gl);
+    }
+    __nv_bfloat16* to = a.O + (token * a.Hq + h) * D + 2 * t;
+    const int from = 8 * t + (row >> 1);   // the lane that has column 2 t of the eight; column 2 t + 1: 4 further
+#pragma unroll
+    for (int c = 0; c < D / 8; ++c) {   // eight columns
+        const float x = o[c / 2][2 * (c % 2)], y = o[c / 2][2 * (c % 2) + 1];
+        const float x0 = __shfl_sync(0xffffffffu, x, from), y0 = __shfl_sync(0xffffffffu, y, from);
+        const float x1 = __shfl_sync(0xffffffffu, x, from + 4), y1 = __shfl_sync(0xffffffffu, y, from + 4);
+        if (!live) continue;
+        if (per_col) {
+            float2 gl = make_float2(0.f, 0.f);
+#pragma unroll 4
+            for (int sp = 0; sp < a.gate_splits; ++sp) {
+                const float2 v = *reinterpret_cast<const float2*>(gp + sp * step + 8 * c);
+                gl.x += v.x;
+                gl.y += v.y;
+            }
+            gate = make_float2(sigmoid(gl.x), sigmoid(gl.y));
+        }
+        *reinterpret_cast<uint32_t*>(to + 8 * c) = pack_bf16x2((row & 1 ? y0 : x0) * gate.x, (row & 1 ? y1 : x1) * gate.y);
+    }
+}
+
+// Up to 8 query rows, a team is one warp and copies for itself; beyond, a team's warps
+// share its tiles and one more warp issues all copies, in a group of four of its own: its registers
+// go to the others (at launch 384 threads have 168 each: 64512 in all, which is 256 x 232 + 128 x 40).
+template <int D, int NT>
 struct Config {
-    static constexpr int KS = NT == 1 ? 2 : 1;          // warps that share a tile's tokens
-    static constexpr int WARPS = kSlots * KS;           // ... that compute
+    static constexpr bool ALONE = NT == 1;
+    static constexpr int WARPS = ALONE ? 16 : 8;        // that compute
     static constexpr int CONSUMERS = WARPS * 32;
-    static constexpr int THREADS = CONSUMERS + 128;     // one more warp issues the copies, in a group of four of its own:
-    // its registers go to the others (at launch 640 threads have 96 each, 384 have 168: 61440 and 64512 in
-    // all, which is 512 x 112 + 128 x 32 and 256 x 232 + 128 x 40)
-    static constexpr int REGS = NT == 1 ? 112 : 232, COPY_REGS = NT == 1 ? 32 : 40;
-    static constexpr int MT = 4 / KS;                   // groups of 16 tokens to a warp
+    static constexpr int THREADS = CONSUMERS + (ALONE ? 0 : 128);
+    static constexpr int REGS = 232, COPY_REGS = 40;
     static constexpr int STRIDE = D + 4;                // floats of a row's part: D columns, then m, l, M
     static constexpr uint32_t STAGE = half_bytes(D);    // bytes: a page's keys or values, with their scales
 };
 
+// What is copied next for a team: the tiles of its share, keys, then values.
+template <int D>
+struct Feed {
+    Cursor next;
+    const int* row;     // of the table
+    int page, after;    // of the tile at `next` and of the one after it
+    bool values;
+    __device__ __forceinline__ void enter(const Cache4Args& a) {
+        row = a.table + (long long)next.b * a.width;
+        page = row[next.j];
+        after = next.j + 1 < next.tiles ? row[next.j + 1] : 0;
+    }
+    __device__ __forceinline__ void start(const Cache4Args& a, const Cursor& at) {
+        next = at;
+        values = false;
+        row = a.table;
+        page = after = 0;
+        if (next.left > 0) enter(a);
+    }
+    __device__ __forceinline__ bool more() const { return next.left > 0; }
+    // The next half page, to `to`; `go` in the thread that issues it.
+    __device__ __forceinline__ void issue(const Cache4Args& a, uint8_t* to, uint64_t* full, bool go) {
+        constexpr uint32_t STAGE = half_bytes(D);
+        if (go) {
+            if (page >= 0 && page < a.n_pages) {
+                mbar_arrive_expect_tx(full, STAGE);
+                bulk_load(to, a.pool + (((long long)page * a.Hkv + next.kvh) * 2 + (values ? 1 : 0)) * STAGE, STAGE, full);
+            } else {
+                // no page of the pool: keys whose scales are NaN (who sees them is NaN), values of scale 0
+                uint4* scales = reinterpret_cast<uint4*>(to + key_scales_at(D));
+                const uint32_t x = values ? 0u : 0x7f7f7f7fu;
+                for (int k = 0; k < 4 * D / 16; ++k) scales[k] = make_uint4(x, x, x, x);
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // (before the stage's next copy)
+                mbar_arrive(full);
+                atomicOr(a.ctl.err, ERR_CACHE_RANGE);
+            }
+        }
+        if (values) {
+            if (next.j + 1 < next.tiles) {
+                ++next.j;
+                --next.left;
+                page = after;
+                if (next.j + 1 < next.tiles) after = row[next.j + 1];
+            } else {
+                next.next_head(a);
+                if (next.left > 0) enter(a);
+            }
+        }
+        values = !values;
+    }
+};
+
 template <int D, bool E2M1, int NT>
-__global__ void __launch_bounds__(Config<D, E2M1, NT>::THREADS, 1)
-cache4_attn_kernel(const __grid_constant__ Cache4Args a) {
-    using C = Config<D, E2M1, NT>;
+__global__ void __launch_bounds__(Config<D, NT>::THREADS, 1) cache4_attn_kernel(const __grid_constant__ Cache4Args a) {
+    using C = Config<D, NT>;
     constexpr uint32_t STAGE = C::STAGE;
-    constexpr int kConsumers = C::CONSUMERS, MT = C::MT, STRIDE = C::STRIDE;
+    constexpr int kConsumers = C::CONSUMERS, MT = 4, STRIDE = C::STRIDE;   // (MT: groups of 16 tokens of a tile)
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ uint64_t s_full[kBars], s_empty[kBars];
+    __shared__ uint64_t s_full[kBars], s_empty[C::ALONE ? 1 : kBars];
     __shared__ int s_place[kScan + 1], s_scan[2 * kScan / 32];
+    __shared__ float s_weight[kSlots * 16], s_l[C::ALONE ? 8 : kMaxRows], s_m[C::ALONE ? 8 : kMaxRows];   // [part][row]; by row
     __shared__ int s_abort;
     volatile int* abort_flag = &s_abort;
 
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const int g = lane >> 2, t = lane & 3;
-    const int team_warps = C::KS * a.R, teams = 1 << a.lg_teams;
-    const int team = warp / team_warps, in_team = warp % team_warps;   // (the copying warp: neither)
-    float* slots = reinterpret_cast<float*>(smem + (size_t)teams * a.stages * STAGE);   // [teams][rows][STRIDE]
+    const int team_warps = C::ALONE ? 1 : a.R, teams = 1 << a.lg_teams;
+    const int team = warp / team_warps, rt = warp % team_warps;   // (rt: the warp's query rows; the copying warp: neither)
+    // Where a team leaves its rows: a lone warp in its ring, when that is empty.
+    const auto slot_of = [&](int k) {
+        return reinterpret_cast<float*>(smem + (C::ALONE ? (size_t)k * a.stages * STAGE
+                                                          : (size_t)teams * a.stages * STAGE + (size_t)k * a.rows * STRIDE * 4));
+    };
     if (tid < teams * a.stages) {
         mbar_init(&s_full[tid], 1);
-        mbar_init(&s_empty[tid], team_warps);
+        if (!C::ALONE) mbar_init(&s_empty[tid], team_warps);
     }
     mbar_fence_init();
     if (tid == 0) s_abort = 0;
@@ -386,7 +486,8 @@ cache4_attn_kernel(const __grid_constant__ Cache4Args a) {
     pdl_trigger();   // the next kernel may be set up; it waits for this grid before it touches memory
 
     // ---- the teams' shares of all tiles, or of the CTA's own head
-    const Layout all(a, s_place, s_scan, tid);
+    if (a.whole) __syncthreads();   // (the barriers; else the layout's)
+    const Layout all = a.whole ? Layout(s_place) : Layout(a, s_place, s_scan, tid);
     const int me = blockIdx.x, N = all.N, ctas = all.ctas;
     const bool by_head = all.by_head;
     const Deal deal(N, ctas * teams);
@@ -421,101 +522,78 @@ cache4_attn_kernel(const __grid_constant__ Cache4Args a) {
         }
         return c;
     };
-    if (warp >= C::WARPS) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::COPY_REGS));
-        if (warp > C::WARPS) return;
-        // ---- copies: lane k serves team k, in the order the team consumes them
-        Cursor next;
-        next.left = 0;
-        if (lane < teams) next = start_of(lane);
-        uint8_t* ring = smem + (size_t)lane * a.stages * STAGE;
-        uint64_t *full = s_full + lane * a.stages, *empty = s_empty + lane * a.stages;
-        uint32_t stage = 0, phase = 0, armed = 0, armed_phase = 0;
-        bool values = false;   // the half of the page at `next` that is copied next
-        // the pages of the tile at `next` and the one after it
-        const int* row = a.table;
-        int page = 0, page_after = 0;
-        const auto enter = [&]() {
-            row = a.table + (long long)next.b * a.width;
-            page = row[next.j];
-            page_after = next.j + 1 < next.tiles ? row[next.j + 1] : 0;
-        };
-        if (next.left > 0) enter();
-        unsigned long long idle_since = 0;
-        while (__any_sync(0xffffffffu, next.left > 0)) {
-            bool did = false;
-            if (next.left > 0 && mbar_test(&empty[stage], phase ^ 1u)) {
-                did = true;
-                uint8_t* to = ring + stage * STAGE;
-                if (page >= 0 && page < a.n_pages) {
-                    mbar_arrive_expect_tx(&full[stage], STAGE);
+    if constexpr (!C::ALONE) {
+        if (warp >= C::WARPS) {
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::COPY_REGS));
+            if (warp > C::WARPS) return;
+            // ---- copies: lane k serves team k, in the order the team consumes them
+            Cursor none;
+            none.left = none.b = none.kvh = none.j = none.tiles = 0;
+            Feed<D> feed;
+            feed.start(a, lane < teams ? start_of(lane) : none);
+            uint8_t* ring = smem + (size_t)lane * a.stages * STAGE;
+            uint64_t *full = s_full + lane * a.stages, *empty = s_empty + lane * a.stages;
+            uint32_t stage = 0, phase = 0, armed = 0, armed_phase = 0;
+            unsigned long long idle_since = 0;
+            while (__any_sync(0xffffffffu, feed.more())) {
+                bool did = false;
+                if (feed.more() && mbar_test(&empty[stage], phase ^ 1u)) {
+                    did = true;
                     armed |= 1u << stage;
                     armed_phase = (armed_phase & ~(1u << stage)) | (phase << stage);
-                    bulk_load(to, a.pool + (((long long)page * a.Hkv + next.kvh) * 2 + (values ? 1 : 0)) * STAGE, STAGE,
-                              &full[stage]);
-                } else {
-                    // no page of the pool: keys whose scales are NaN (who sees them is NaN), values of scale 0
-                    uint4* scales = reinterpret_cast<uint4*>(to + key_scales_at(D));
-                    const uint32_t x = values ? 0u : 0x7f7f7f7fu;
-                    for (int k = 0; k < 4 * D / 16; ++k) scales[k] = make_uint4(x, x, x, x);
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // (before the stage's next copy)
-                    mbar_arrive(&full[stage]);
-                    atomicOr(a.ctl.err, ERR_CACHE_RANGE);
-                }
-                if (values) {
-                    if (next.j + 1 < next.tiles) {
-                        ++next.j;
-                        --next.left;
-                        page = page_after;
-                        if (next.j + 1 < next.tiles) page_after = row[next.j + 1];
-                    } else {
-                        next.next_head(a);
-                        if (next.left > 0) enter();
+                    feed.issue(a, ring + stage * STAGE, &full[stage], true);
+                    if (++stage == (uint32_t)a.stages) {
+                        stage = 0;
+                        phase ^= 1u;
                     }
                 }
-                values = !values;
-                if (++stage == (uint32_t)a.stages) {
-                    stage = 0;
-                    phase ^= 1u;
+                if (__any_sync(0xffffffffu, did)) {
+                    idle_since = 0;
+                    continue;
                 }
-            }
-            if (__any_sync(0xffffffffu, did)) {
-                idle_since = 0;
-                continue;
-            }
-            // every team's ring is full: look again shortly, but not for ever
-            if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
-            const unsigned long long now = globaltimer_ns();
-            if (idle_since == 0) idle_since = now;
-            if (__any_sync(0xffffffffu, now - idle_since > a.ctl.limit_ns)) {
-                if (lane == 0) {
-                    atomicOr(a.ctl.err, ERR_WAIT_TIMEOUT);
-                    *abort_flag = 1;
+                // every team's ring is full: look again shortly, but not for ever
+                if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
+                const unsigned long long now = globaltimer_ns();
+                if (idle_since == 0) idle_since = now;
+                if (__any_sync(0xffffffffu, now - idle_since > a.ctl.limit_ns)) {
+                    if (lane == 0) {
+                        atomicOr(a.ctl.err, ERR_WAIT_TIMEOUT);
+                        *abort_flag = 1;
+                    }
+                    break;
                 }
-                break;
+                __nanosleep(40);
             }
-            __nanosleep(40);
+            // The CTA keeps its shared memory until this warp is done: it stays until what it
+            // has issued is there, whoever gave up. (A share that is no longer than its ring is
+            // issued at once, and its consumers may still give up; where they wait for the same
+            // copies this costs nothing.)
+            volatile int never = 0;
+            const WaitCtl c2 = landing_limit(a.ctl);
+            for (int k = 0; k < a.stages; ++k)
+                if (armed & (1u << k)) mbar_wait(&full[k], (armed_phase >> k) & 1u, &never, c2);
+            return;
         }
-        // The CTA keeps its shared memory until this warp is done: it stays until what it
-        // has issued is there, whoever gave up. (A share that is no longer than its ring is
-        // issued at once, and its consumers may still give up; where they wait for the same
-        // copies this costs nothing.)
-        volatile int never = 0;
-        const WaitCtl c2 = landing_limit(a.ctl);
-        for (int k = 0; k < a.stages; ++k)
-            if (armed & (1u << k)) mbar_wait(&full[k], (armed_phase >> k) & 1u, &never, c2);
-        return;
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS));
     }
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS));
-    bool ok = true;
+    bool ok = true, joined = false;
+    int head_place = 0, head_tiles = 0;   // where the CTA's share is all of one head: of its first tile; its tiles
     {
         // ---- the team's tiles
         const uint8_t* ring = smem + (size_t)team * a.stages * STAGE;
-        uint64_t *full = s_full + team * a.stages, *empty = s_empty + team * a.stages;
-        const int rt = in_team / C::KS, kh = in_team % C::KS;   // the warp's query rows and part of a tile's tokens
-        const int team_threads = 32 * team_warps, team_tid = 32 * in_team + lane;
-        float* slot = slots + (size_t)team * a.rows * STRIDE;
+        uint64_t *full = s_full + team * a.stages, *empty = C::ALONE ? s_empty : s_empty + team * a.stages;
+        const int team_threads = 32 * team_warps, team_tid = 32 * rt + lane;
+        float* slot = slot_of(team);
         uint32_t stage = 0, phase = 0;   // the oldest stage that is not released
+        int ahead = 0;                   // ALONE: half pages that are issued and not released
+        Cursor at = start_of(team);
+        const int share_end = team_lo(team + 1);
+        Feed<D> feed;
+        if constexpr (C::ALONE) {
+            feed.start(a, at);
+            for (; ahead < a.stages && feed.more(); ++ahead)
+                feed.issue(a, smem + ((size_t)team * a.stages + ahead) * STAGE, &full[ahead], lane == 0);
+        }
         const auto wait_full = [&]() -> const uint8_t* {
             if (!__all_sync(0xffffffffu, mbar_wait(&full[stage], phase, abort_flag, a.ctl))) {
                 ok = false;
@@ -525,17 +603,41 @@ cache4_attn_kernel(const __grid_constant__ Cache4Args a) {
         };
         const auto release = [&]() {
             __syncwarp();
-            if (lane == 0) mbar_arrive(&empty[stage]);
+            if constexpr (C::ALONE) {
+                --ahead;
+                if (feed.more()) {
+                    feed.issue(a, const_cast<uint8_t*>(ring) + stage * STAGE, &full[stage], lane == 0);
+                    ++ahead;
+                }
+            } else {
+                if (lane == 0) mbar_arrive(&empty[stage]);
+            }
             if (++stage == (uint32_t)a.stages) {
                 stage = 0;
                 phase ^= 1u;
             }
         };
+        const auto team_and = [&](bool x) {
+            if constexpr (C::ALONE) {
+                x = __all_sync(0xffffffffu, x);
+                __syncwarp();
+                return x;
+            } else {
+                return named_bar_and(1 + team, team_threads, x);
+            }
+        };
+        // All tiles of the CTA's share are one head's: its teams' parts are joined here, and one is left.
+        if (!by_head && me < ctas) {   // (looked up after the first copies are on their way)
+            const int from = deal.from(me * teams), to = deal.from((me + 1) * teams);
+            int b, rem;
+            all.find(a, from, b, rem);
+            const PagedSeq q(a, b);
+            head_tiles = q.tiles;
+            head_place = from - rem % max(q.span(), 1);
+            joined = from < head_place + head_tiles && joins(a.lg_teams, from, to, head_place, q.span());
+        }
         RowState<D, NT> st;
-        const int first = 16 * MT * kh;   // the warp's tokens of a tile: first .. first + 16 MT
         const float unscaled = kLog2e * rsqrtf((float)D) * a.k_up;
-        Cursor at = start_of(team);
-        const int share_end = team_lo(team + 1);
         while (at.left > 0) {
             const PagedSeq q(a, at.b);
             const int j1 = min(at.tiles, at.j + at.left);   // segment: tiles [at.j, j1) of the head
@@ -558,7 +660,7 @@ cache4_attn_kernel(const __grid_constant__ Cache4Args a) {
                 if (!kt) break;
 #pragma unroll
                 for (int i = 0; i < MT; ++i) {
-                    const int n0 = first + 16 * i + g;   // and n0 + 8
+                    const int n0 = 16 * i + g;   // and n0 + 8
                     uint32_t x[D / 32], y[D / 32], xs[D / 64], ys[D / 64];
                     load_words(kt + n0 * (D / 2) + t * (D / 8), x);
                     load_words(kt + (n0 + 8) * (D / 2) + t * (D / 8), y);
@@ -606,9 +708,9 @@ cache4_attn_kernel(const __grid_constant__ Cache4Args a) {
                 const uint8_t* vt = wait_full();
                 if (!vt) break;
                 // (the first query row sees tokens up to len: tiles before need no mask)
-                const int base = j * kPage + first, left = q.T - base;
-                const bool masked = j * kPage + kPage - 1 > q.len;
-                const uint8_t* scales = vt + 32 * D + kh * MT * D;
+                const int base = j * kPage, left = q.T - base;
+                const bool masked = base + kPage - 1 > q.len;
+                const uint8_t* scales = vt + key_scales_at(D);   // (as far into the values' half)
                 const float ev = scale_exponent<D, MT>(scales, lane, masked ? left : 16 * MT);
                 int lim[NT][2] = {};
                 if (masked) {
@@ -640,7 +742,7 @@ cache4_attn_kernel(const __grid_constant__ Cache4Args a) {
 #pragma unroll
                     for (int quad = 0; quad < D / 64; ++quad) {
                         uint32_t w[4];
-                        load_words(vt + (((kh * MT + i) * (D / 64) + quad) * 32 + lane) * 16, w);
+                        load_words(vt + ((i * (D / 64) + quad) * 32 + lane) * 16, w);
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             const int c = 4 * quad + k;
@@ -663,20 +765,25 @@ cache4_attn_kernel(const __grid_constant__ Cache4Args a) {
             }
 
             // ---- the segment's rows: sums over the lanes, and the codes' units out of the outputs
-            const float unit = exp2f(a.v_exp + (E2M1 ? 0.f : 24.f)), unit8 = E2M1 ? unit : unit * 0.0625f;
+            const bool whole = at.j == 0 && j1 == at.tiles && !joined, final = at.left <= span_of(at.tiles) - at.j;
+            const float unit = exp2f(a.v_exp + (E2M1 ? 0.f : 24.f));
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
+                float k[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     st.M[n][e] = st.m[n][e];
 #pragma unroll
                     for (int sh = 4; sh < 32; sh <<= 1)
                         st.l[n][e] += __shfl_xor_sync(0xffffffffu, st.l[n][e], sh);
+                    k[e] = unit;
+                    // (a row that saw nothing is zero)
+                    if (C::ALONE && whole) k[e] = st.l[n][e] > 0.f || st.l[n][e] != st.l[n][e] ? unit / st.l[n][e] : 0.f;
                 }
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) st.o[n][i][e] *= e < 2 ? unit : unit8;
+                    for (int e = 0; e < 4; ++e) st.o[n][i][e] *= E2M1 || e < 2 ? k[e & 1] : k[e & 1] * 0.0625f;
             }
             const auto put = [&](float* base) {
 #pragma unroll
@@ -695,80 +802,86 @@ cache4_attn_kernel(const __grid_constant__ Cache4Args a) {
                             *reinterpret_cast<float4*>(to + D) = make_float4(st.m[n][e], st.l[n][e], st.M[n][e], 0.f);
                     }
             };
-            // A head of the team's alone is finished; else its part is left in global
-            // memory for the merge kernel, or, of the CTA's own head, in shared memory:
-            // the first warp's rows in the slot, the second's in the ring, which is empty.
-            const bool whole = at.j == 0 && j1 == at.tiles, final = at.left <= span_of(at.tiles) - at.j;
-            const bool apart = C::KS == 2 && by_head && !whole;
-            float* to = whole || by_head
-                            ? slot : part_of<D>(a, deal, me * teams + team, share_end - at.left - at.j);
-            if (C::KS == 2 && !apart && kh == 1) put(slot);
-            if (C::KS == 1 || (apart && kh == 0)) put(to);
-            ok = named_bar_and(1 + team, team_threads, ok && !*abort_flag);
-            if (!ok) break;
-            if (apart) {
-                if (kh == 1) put(reinterpret_cast<float*>(smem + (size_t)team * a.stages * STAGE));
-            } else if constexpr (C::KS == 2) {
-                if (kh == 0) {
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int row = 8 * (NT * rt + n) + 2 * t + e;
-                            if (row >= a.rows) continue;
-                            const float* from = slot + row * STRIDE;
-                            const float4 x = *reinterpret_cast<const float4*>(from + D);
-                            const float m = fmaxf(st.m[n][e], x.x), M = fmaxf(st.M[n][e], x.z);
-                            const float oa = part_weight(st.M[n][e], M), ob = part_weight(x.z, M);
-                            st.l[n][e] = st.l[n][e] * part_weight(st.m[n][e], m) + x.y * part_weight(x.x, m);
-                            st.m[n][e] = m;
-                            st.M[n][e] = M;
-#pragma unroll
-                            for (int i = 0; i < D / 16; ++i) {
-                                st.o[n][i][e] = st.o[n][i][e] * oa + from[16 * i + g] * ob;
-                                st.o[n][i][2 + e] = st.o[n][i][2 + e] * oa + from[16 * i + 8 + g] * ob;
-                            }
-                        }
-                    __syncwarp();
-                    put(to);
+            // A head of the team's alone is finished; else its part is left in global memory
+            // for the merge kernel, or in shared memory where the CTA's teams have one head.
+            if (C::ALONE && whole) {
+                if constexpr (C::ALONE) finish_warp<D>(a, at.b, at.kvh, q.n, lane, st.o[0]);
+                ok = team_and(ok && !*abort_flag);
+                if (!ok) break;
+            } else {
+                put(whole || by_head || joined ? slot
+                                               : part_of<D>(a, deal, me * teams + team, share_end - at.left - at.j));
+                ok = team_and(ok && !*abort_flag);
+                if (!ok) break;
+                if (whole) {
+                    if (a.gate_mode != GSDPA_GATE_NONE) pdl_wait();   // the gate logits
+                    for (int idx = team_tid; idx < a.rows * (D / 4); idx += team_threads) {
+                        const int row = idx / (D / 4), col = 4 * (idx % (D / 4));
+                        const float* from = slot + row * STRIDE;
+                        const float4 x = *reinterpret_cast<const float4*>(from + D);
+                        finish<D>(a, at.b, at.kvh, q.n, row, col, out_scale(x.x, x.y, x.z),
+                                  *reinterpret_cast<const float4*>(from + col), gate_of<D>(a, at.b, at.kvh, q.n, row, col));
+                    }
+                    if (!final) team_and(true);   // (the slot may be written again)
                 }
-                if (whole || !final) named_bar_sync(1 + team, team_threads);   // (the slot may be written again)
-            }
-            if (whole) {
-                if (a.gate_mode != GSDPA_GATE_NONE) pdl_wait();   // the gate logits
-                for (int idx = team_tid; idx < a.rows * (D / 4); idx += team_threads) {
-                    const int row = idx / (D / 4), col = 4 * (idx % (D / 4));
-                    const float* from = slot + row * STRIDE;
-                    const float4 x = *reinterpret_cast<const float4*>(from + D);
-                    finish<D>(a, at.b, at.kvh, q.n, row, col, out_scale(x.x, x.y, x.z),
-                              *reinterpret_cast<const float4*>(from + col), gate_of<D>(a, at.b, at.kvh, q.n, row, col));
-                }
-                if (!final) named_bar_sync(1 + team, team_threads);
             }
             at.next_head(a);
+        }
+        if constexpr (C::ALONE) {
+            // (a warp that gave up stays until its copies have landed: the CTA keeps its shared memory that long)
+            volatile int never = 0;
+            const WaitCtl c2 = landing_limit(a.ctl);
+            for (; ahead > 0; --ahead) {
+                mbar_wait(&full[stage], phase, &never, c2);
+                if (++stage == (uint32_t)a.stages) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
         }
     }
 
     pdl_wait();   // the gate logits; and what follows on the stream may rely on the gate kernel having ended
-    const int parts = min(whole_head, teams);   // (of the CTA's own head: more than one, or it is done)
-    if (by_head && named_bar_and(kSlots + 1, kConsumers, ok && !*abort_flag) && parts > 1) {
-        const int items = a.rows * (D / 4), b = me / a.Hkv, n = PagedSeq(a, b).n;
-        // A thread has four columns of a row; its parts are split over lanes that
-        // would be idle (whole warps: items come in sixteens).
-        int lg = 0;
-        while (lg < 3 && (items << (lg + 1)) <= kConsumers) ++lg;
-        for (int idx = tid; idx < items << lg; idx += kConsumers) {
-            const int item = idx >> lg, row = item / (D / 4), col = 4 * (item % (D / 4));
-            const float4 gate = gate_of<D>(a, b, me % a.Hkv, n, row, col);
-            Sums r;
-            r.add(idx & ((1 << lg) - 1), parts * C::KS, 1 << lg, D, col, [&](int i) {
-                return (i < parts ? slots + (size_t)i * a.rows * STRIDE
-                                  : reinterpret_cast<const float*>(smem + (size_t)(i - parts) * a.stages * STAGE)) +
-                       row * STRIDE;
-            });
-            for (int sh = 1; sh < 1 << lg; sh <<= 1) r.join_lane(sh);
-            if ((idx & ((1 << lg) - 1)) == 0)
-                finish<D>(a, b, me % a.Hkv, n, row, col, out_scale(r.m, r.l, r.M), r.o, gate);
+    // Parts in shared memory: of the CTA's own head (more than one, or it is done), or of a piece of a head.
+    int parts = 0;
+    if (by_head) parts = min(whole_head, teams);
+    else if (joined) parts = min(teams, deal.taker(head_place + head_tiles - 1) - me * teams + 1);
+    if ((by_head || joined) && named_bar_and(kSlots + 1, kConsumers, ok && !*abort_flag) && (joined || parts > 1)) {
+        const int b = by_head ? me / a.Hkv : 0, n = by_head ? PagedSeq(a, b).n : 0;
+        // each part's weight in each row, and the rows' sums
+        for (int idx = tid; idx < a.rows * parts; idx += kConsumers) {
+            const int row = idx % a.rows, part = idx / a.rows;
+            const auto state = [&](int i) { return *reinterpret_cast<const float2*>(slot_of(i) + row * STRIDE + D); };
+            float m = -INFINITY, l = 0.f;
+            for (int i = 0; i < parts; ++i) m = fmaxf(m, state(i).x);
+            s_weight[idx] = part_weight(state(part).x, m);
+            if (part == 0) {
+                for (int i = 0; i < parts; ++i) l += state(i).y * part_weight(state(i).x, m);
+                s_l[row] = l;
+                s_m[row] = m;
+            }
+        }
+        named_bar_sync(kSlots + 1, kConsumers);
+        for (int idx = tid; idx < a.rows * (D / 4); idx += kConsumers) {
+            const int row = idx / (D / 4), col = 4 * (idx % (D / 4));
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+            for (int i = 0; i < parts; ++i) {
+                const float w = s_weight[i * a.rows + row];
+                const float4 x = *reinterpret_cast<const float4*>(slot_of(i) + row * STRIDE + col);
+                o.x = fmaf(w, x.x, o.x);
+                o.y = fmaf(w, x.y, o.y);
+                o.z = fmaf(w, x.z, o.z);
+                o.w = fmaf(w, x.w, o.w);
+            }
+            if (by_head) {
+                finish<D>(a, b, me % a.Hkv, n, row, col, out_scale(s_m[row], s_l[row], s_m[row]), o,
+                          gate_of<D>(a, b, me % a.Hkv, n, row, col));
+            } else {
+                float* to = part_of<D>(a, deal, me * teams, head_place) + row * STRIDE;
+                *reinterpret_cast<float4*>(to + col) = o;
+                if (col == 0) *reinterpret_cast<float4*>(to + D) = make_float4(s_m[row], s_l[row], s_m[row], 0.f);
+            }
         }
     }
 
@@ -790,21 +903,20 @@ cache4_attn_kernel(const __grid_constant__ Cache4Args a) {
 
 // Shared memory and ring of one problem.
 struct Shape {
-    int NT, R, stages;
+    int NT, R, teams, stages;
     uint32_t smem;
 };
 Shape shape_of(int rows, int D) {
     Shape s;
     s.NT = rows <= 8 ? 1 : 2;
     s.R = rows <= 16 ? 1 : (rows <= 32 ? 2 : (rows <= 64 ? 4 : 8));
-    const uint32_t merge = (uint32_t)(kSlots / s.R * rows * (D + 4)) * 4;
-    const uint32_t per_stage = (uint32_t)(kSlots / s.R) * half_bytes(D);
-    // as many copies in flight as fit, up to 192 KB
+    s.teams = (s.NT == 1 ? 2 * kSlots : kSlots) / s.R;
+    const uint32_t merge = s.NT == 1 ? 0 : (uint32_t)(s.teams * rows * (D + 4)) * 4;
+    const uint32_t per_stage = (uint32_t)s.teams * half_bytes(D);
+    // as many copies in flight as fit
     s.stages = (int)((kSmemMax - merge) / per_stage);
-    const int most = (int)(196608 / per_stage);
-    if (s.stages > most) s.stages = most;
     if (s.stages > kMaxStages) s.stages = kMaxStages;
-    if (s.stages > kBars * s.R / kSlots) s.stages = kBars * s.R / kSlots;
+    if (s.stages > kBars / s.teams) s.stages = kBars / s.teams;
     s.smem = (uint32_t)s.stages * per_stage + merge;
     return s;
 }
@@ -852,7 +964,7 @@ int plan_cache4(const gsdpa_cache4* c, int B, int max_pages, int n_rows, int max
     if (gate_mode != GSDPA_GATE_NONE) plan_gate_rows(p, plan_sms(), &o.w);
     o.w.gate_part = take(sizeof(float) * (size_t)o.w.gate_splits * o.w.gate_rows * o.w.gate_cols);
     const size_t part = sizeof(float) * (size_t)rows * (c->d_k + 4);
-    o.part = take(part * plan_sms() * 2 * (kSlots / shape_of((int)rows, c->d_k).R));
+    o.part = take(part * plan_sms() * 2 * shape_of((int)rows, c->d_k).teams);
     o.total = off;
     return GSDPA_OK;
 }
@@ -865,7 +977,7 @@ cudaError_t launch(const Cache4Args& a, const Shape& sh, unsigned grid, cudaStre
                                     (int)kSmemMax);
     });
     if (e != cudaSuccess) return e;
-    return launch_dependent(cache4_attn_kernel<D, E2M1, NT>, dim3(grid), dim3(Config<D, E2M1, NT>::THREADS), sh.smem, s,
+    return launch_dependent(cache4_attn_kernel<D, E2M1, NT>, dim3(grid), dim3(Config<D, NT>::THREADS), sh.smem, s,
                             a);
 }
 template <int D, bool E2M1>
@@ -943,7 +1055,8 @@ int gated_sdpa_cache4(const void* X, const void* Q, const gsdpa_cache4* cache, c
     a.n_pages = cache->n_pages;
     const Shape sh = shape_of(a.rows, cache->d_k);
     a.R = sh.R;
-    a.lg_teams = sh.R == 1 ? 3 : (sh.R == 2 ? 2 : (sh.R == 4 ? 1 : 0));
+    a.lg_teams = 0;
+    while (1 << a.lg_teams < sh.teams) ++a.lg_teams;
     a.stages = sh.stages;
     a.k_up = ldexpf(1.f, cache->k_exp);
     a.v_exp = (float)cache->v_exp;
@@ -956,11 +1069,12 @@ int gated_sdpa_cache4(const void* X, const void* Q, const gsdpa_cache4* cache, c
     a.ctl.err = rt.err;
     a.ctl.limit_ns = rt.limit_ns;
     // one CTA per SM, fewer where full tables would not give each its tiles
-    const long long most = (long long)B * a.Hkv * ((max_pages + kSlots / a.R - 1) / (kSlots / a.R));
+    const long long most = (long long)B * a.Hkv * ((max_pages + sh.teams - 1) / sh.teams);
     long long grid = sms;   // (no fewer than the heads, where those fit)
     if (grid > most) grid = most;
     a.ctas = (int)grid;
     const bool whole = max_pages <= kWholeTiles << a.lg_teams && (long long)B * a.Hkv <= grid;
+    a.whole = whole;
     a.whole_tiles = (whole ? kWholeTiles : kFewTiles) << a.lg_teams;
     const bool e2m1 = cache->kind == GSDPA_CACHE_E2M1;
     if (cache->d_k == 128)

@@ -90,6 +90,7 @@ constexpr float kApart = 100.0f;
 struct SeqTiles;
 struct Cache8Args {
     using Seq = SeqTiles;
+    static constexpr bool kJoins = false;   // (a head's parts are its teams')
     __device__ __forceinline__ long long token(int b, int i) const { return (long long)b * Lq + i; }
     __device__ __forceinline__ long long tokens() const { return (long long)B * Lq; }
     const __nv_bfloat16* Q;          // [B, Lq, Hq, D]

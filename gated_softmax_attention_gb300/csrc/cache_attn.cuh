@@ -7,6 +7,7 @@
 //   A::Seq(a, b)   sequence b: n (new tokens), T (tokens in all, 0 without new ones), tiles, span()
 //   token(b, i)    the row of Q, X and O that holds new token i of sequence b
 //   tokens()       all rows
+//   kJoins         a CTA whose share is all of one head leaves one part
 #pragma once
 #include "ops_internal.h"
 
@@ -250,6 +251,39 @@ __device__ __forceinline__ float* part_of(const A& a, const Deal& deal, int n, i
     return a.part + (long long)(2 * n + (u0 <= deal.from(n) ? 0 : 1)) * a.rows * (D + 4);
 }
 
+// Whether the places [from, to) of a CTA, the first of them a tile, are all of the head
+// at [u0, u0 + span): its teams' parts are then joined and left as one, its first team's. (Not of a
+// single team: it may have the whole head.)
+__device__ __forceinline__ bool joins(int lg_teams, int from, int to, int u0, int span) {
+    return lg_teams > 0 && from >= u0 && to <= u0 + span;
+}
+
+// The parts of a cut head that teams first .. last have tiles of: one each, or one of a
+// CTA whose teams' are joined (any CTA but those of the first and the last team, and maybe these).
+template <class A>
+struct Parts {
+    int n;             // how many
+    int n0, lead, mid, lg;   // first team; parts of its CTA; CTAs between that and the last team's
+    __device__ __forceinline__ Parts(const A& a, const Deal& deal, int first, int last, int u0, int span) : n0(first) {
+        n = last - first + 1;
+        if constexpr (A::kJoins) {
+            lg = a.lg_teams;
+            const int c0 = first >> lg, c1 = last >> lg;
+            const auto joined = [&](int c) { return joins(lg, deal.from(c << lg), deal.from((c + 1) << lg), u0, span); };
+            lead = joined(c0) ? 1 : min(last, ((c0 + 1) << lg) - 1) - first + 1;
+            mid = max(c1 - c0 - 1, 0);
+            n = lead + mid + (c1 == c0 ? 0 : (joined(c1) ? 1 : last - (c1 << lg) + 1));
+        }
+    }
+    __device__ __forceinline__ int team(int k) const {
+        if constexpr (A::kJoins) {
+            const int c0 = n0 >> lg;
+            if (k >= lead) return k < lead + mid ? (c0 + 1 + k - lead) << lg : ((c0 + 1 + mid) << lg) + (k - lead - mid);
+        }
+        return n0 + k;
+    }
+};
+
 // The sequence of all tiles: sequence after sequence, in each one K/V head after
 // the other. (Its scan in four warps: in all twenty of a block it took 0.6 us more.)
 struct Layout {
@@ -258,6 +292,9 @@ struct Layout {
     int ctas;           // that have any
     bool by_head;
     const int* place;   // [kScan + 1], in shared memory: the places before sequence per * k
+    // a CTA to each head, whatever the lengths (nothing is looked up)
+    __device__ __forceinline__ explicit Layout(const int* s_place)
+        : per(1), N(0), longest(0), ctas(1), by_head(true), place(s_place) {}
     // by all threads of a block of kScan or more
     template <class A>
     __device__ __forceinline__ Layout(const A& a, int* s_place, int* s_scan, int tid) : place(s_place) {
@@ -352,7 +389,8 @@ __global__ void __launch_bounds__(kMergeThreads) cache_merge_kernel(const __grid
     const long long heads = (long long)a.B * a.Hkv;
     const bool by_place = heads >= takers;
     const int units = all.by_head ? 0 : (by_place ? takers - 1 : (int)heads);
-    const int most = deal.each > 0 ? all.longest / deal.each + 2 : 1;   // parts of a head
+    int most = deal.each > 0 ? all.longest / deal.each + 2 : 1;   // parts of a head
+    if (A::kJoins) most = min(most, (most >> a.lg_teams) + (1 << a.lg_teams));
     int lg = 0;
     while ((8 << lg) <= kMergeThreads && ((units * items) << (lg + 1)) <= threads && (4 << lg) < most) ++lg;
     const int total = (units * items) << lg;   // (below 1280 x 4096, or the grid's threads)
@@ -361,12 +399,14 @@ __global__ void __launch_bounds__(kMergeThreads) cache_merge_kernel(const __grid
         const int idx = base + tid, unit = idx / (items << lg);
         const int x = idx - unit * (items << lg), item = (x >> (lg + 2) << 2) + (x & 3), sub = (x >> 2) & ((1 << lg) - 1);
         const int row = item / (D / 4), col = 4 * (item % (D / 4));
-        int b = 0, kvh = 0, u0 = 0, n0 = 0, n1 = 0;
+        int b = 0, kvh = 0, u0 = 0, n0 = 0, n1 = 0, span = 0;
         if (by_place) {
             const int from = idx < total ? deal.from(unit + 1) : all.N;
             if (from < all.N) {
                 all.find(a, from, b, u0);
-                const int tiles = typename A::Seq(a, b).tiles, span = span_of(tiles), at = u0 % max(span, 1);
+                const int tiles = typename A::Seq(a, b).tiles;
+                span = span_of(tiles);
+                const int at = u0 % max(span, 1);
                 kvh = u0 / max(span, 1);
                 u0 = from - at;
                 if (at > 0 && at < tiles && deal.taker(u0) == unit) {
@@ -378,7 +418,8 @@ __global__ void __launch_bounds__(kMergeThreads) cache_merge_kernel(const __grid
             b = unit / a.Hkv;
             kvh = unit % a.Hkv;
             const int tiles = typename A::Seq(a, b).tiles;
-            u0 = all.before(a, b) + kvh * span_of(tiles);
+            span = span_of(tiles);
+            u0 = all.before(a, b) + kvh * span;
             if (tiles > 0) {
                 n0 = deal.taker(u0);
                 n1 = deal.taker(u0 + tiles - 1);
@@ -387,12 +428,14 @@ __global__ void __launch_bounds__(kMergeThreads) cache_merge_kernel(const __grid
         if (!waited) pdl_wait();
         waited = true;
         const bool cut = n1 > n0;
+        const Parts<A> parts(a, deal, n0, n1, u0, span);
         const int n = cut ? typename A::Seq(a, b).n : 0;
         float4 gate = make_float4(1.f, 1.f, 1.f, 1.f);
         if (cut && sub == 0) gate = gate_of<D>(a, b, kvh, n, row, col);
         Sums r;
         if (cut)
-            r.add(n0 + sub, n1 + 1, 1 << lg, D, col, [&](int k) { return part_of<D>(a, deal, k, u0) + row * (D + 4); });
+            r.add(sub, parts.n, 1 << lg, D, col,
+                  [&](int k) { return part_of<D>(a, deal, parts.team(k), u0) + row * (D + 4); });
         for (int k = 0; k < min(lg, 3); ++k) r.join_lane(4 << k);
         if (lg > 3) {   // warps that share items
             const int share = 1 << (lg - 3);

@@ -305,9 +305,11 @@ def test_shares_shorter_than_their_ring_give_up_cleanly(T, H, Hq, d, n, bad):
         assert same(call()) and gb.check_device_error() == fine
 
 
-def test_a_share_longer_than_its_ring_reports_the_timeout():
-    # the copying warp finds its rings full until the first tiles have been used: with 1 ns it does not wait that long
-    B, T, H, Hq, d = 8, 32768, 8, 32, 128
+# up to 8 query rows a warp waits for its own copies only, which may be there before it looks at the time; with
+# more a copying warp finds its rings full until the first tiles have been used, and with 1 ns does not wait that long
+@pytest.mark.parametrize("Hq,certain", [(32, False), (128, True)])
+def test_shares_longer_than_their_ring_give_up_cleanly(Hq, certain):
+    B, T, H, d = 8, 32768, 8, 128
     s = Server(B, T // PAGE, B * T // PAGE, H, d, "e2m1")
     s.table.copy_(s.free.view(B, -1))
     s.cache.pool.copy_(torch.randint(0, 100, s.cache.pool.shape, device="cuda", dtype=torch.uint8))    # no scale is NaN
@@ -315,7 +317,8 @@ def test_a_share_longer_than_its_ring_reports_the_timeout():
     call = lambda: gb.gated_sdpa_cache4(*args, gate="none")  # noqa: E731
     want = call()
     for _ in range(5):
-        assert with_a_tiny_limit(call) == gb.ERR_DEVICE_TIMEOUT
+        status = with_a_tiny_limit(call)
+        assert status == gb.ERR_DEVICE_TIMEOUT or (status == gb.OK and not certain)
         assert torch.equal(call(), want) and gb.check_device_error() == gb.OK
 
 

@@ -464,6 +464,8 @@ __global__ void __launch_bounds__(Config<D, NT>::THREADS, 1) cache4_attn_kernel(
     __shared__ uint64_t s_full[kBars], s_empty[C::ALONE ? 1 : kBars];
     __shared__ int s_place[kScan + 1], s_scan[2 * kScan / 32];
     __shared__ float s_weight[kSlots * 16], s_l[C::ALONE ? 8 : kMaxRows], s_m[C::ALONE ? 8 : kMaxRows];   // [part][row]; by row
+    __shared__ Cursor s_start[2 * kSlots];
+    __shared__ int2 s_head;
     __shared__ int s_abort;
     volatile int* abort_flag = &s_abort;
 
@@ -522,6 +524,23 @@ __global__ void __launch_bounds__(Config<D, NT>::THREADS, 1) cache4_attn_kernel(
         }
         return c;
     };
+    if (warp == 0 && lane < teams) s_start[lane] = start_of(lane);
+    // All tiles of the CTA's share are one head's: its teams' parts are joined here, and one is left.
+    if (tid == 32) {
+        int2 head = make_int2(-1, 0);
+        if (!by_head && me < ctas) {
+            const int from = deal.from(me * teams), to = deal.from((me + 1) * teams);
+            int b, rem;
+            all.find(a, from, b, rem);
+            const PagedSeq q(a, b);
+            const int first = from - rem % max(q.span(), 1);
+            if (from < first + q.tiles && joins(a.lg_teams, from, to, first, q.span())) head = make_int2(first, q.tiles);
+        }
+        s_head = head;
+    }
+    __syncthreads();
+    const bool joined = s_head.x >= 0;
+    const int head_place = s_head.x, head_tiles = s_head.y;   // of its first tile; its tiles
     if constexpr (!C::ALONE) {
         if (warp >= C::WARPS) {
             asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::COPY_REGS));
@@ -530,7 +549,7 @@ __global__ void __launch_bounds__(Config<D, NT>::THREADS, 1) cache4_attn_kernel(
             Cursor none;
             none.left = none.b = none.kvh = none.j = none.tiles = 0;
             Feed<D> feed;
-            feed.start(a, lane < teams ? start_of(lane) : none);
+            feed.start(a, lane < teams ? s_start[lane] : none);
             uint8_t* ring = smem + (size_t)lane * a.stages * STAGE;
             uint64_t *full = s_full + lane * a.stages, *empty = s_empty + lane * a.stages;
             uint32_t stage = 0, phase = 0, armed = 0, armed_phase = 0;
@@ -576,8 +595,7 @@ __global__ void __launch_bounds__(Config<D, NT>::THREADS, 1) cache4_attn_kernel(
         }
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS));
     }
-    bool ok = true, joined = false;
-    int head_place = 0, head_tiles = 0;   // where the CTA's share is all of one head: of its first tile; its tiles
+    bool ok = true;
     {
         // ---- the team's tiles
         const uint8_t* ring = smem + (size_t)team * a.stages * STAGE;
@@ -586,8 +604,19 @@ __global__ void __launch_bounds__(Config<D, NT>::THREADS, 1) cache4_attn_kernel(
         float* slot = slot_of(team);
         uint32_t stage = 0, phase = 0;   // the oldest stage that is not released
         int ahead = 0;                   // ALONE: half pages that are issued and not released
-        Cursor at = start_of(team);
+        Cursor at = s_start[team];
         const int share_end = team_lo(team + 1);
+        // The first head's queries are asked for before the copies: behind 30 MB of these they took 4 us more.
+        uint32_t qf[NT][D / 16][2];
+        const auto load_queries = [&](const PagedSeq& q) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const int row = 8 * (NT * rt + n) + g, i = row * a.g_inverse >> 16;
+                load_row<D>(row < a.rows && i < q.n
+                                ? a.Q + (a.token(at.b, i) * a.Hq + (at.kvh - i) * a.G + row) * D : nullptr, t, qf[n]);
+            }
+        };
+        if (at.left > 0) load_queries(PagedSeq(a, at.b));
         Feed<D> feed;
         if constexpr (C::ALONE) {
             feed.start(a, at);
@@ -626,29 +655,29 @@ __global__ void __launch_bounds__(Config<D, NT>::THREADS, 1) cache4_attn_kernel(
                 return named_bar_and(1 + team, team_threads, x);
             }
         };
-        // All tiles of the CTA's share are one head's: its teams' parts are joined here, and one is left.
-        if (!by_head && me < ctas) {   // (looked up after the first copies are on their way)
-            const int from = deal.from(me * teams), to = deal.from((me + 1) * teams);
-            int b, rem;
-            all.find(a, from, b, rem);
-            const PagedSeq q(a, b);
-            head_tiles = q.tiles;
-            head_place = from - rem % max(q.span(), 1);
-            joined = from < head_place + head_tiles && joins(a.lg_teams, from, to, head_place, q.span());
+        // rows that count for no request are zero
+        const auto clear_rows = [&](int from, int to) {
+            const long long words = (long long)a.Hq * D / 8;
+            for (long long i = from * words + tid; i < to * words; i += kConsumers)
+                reinterpret_cast<uint4*>(a.O)[i] = make_uint4(0, 0, 0, 0);
+        };
+        const auto row_at = [&](int b) { return min(max(a.cu[b], 0), a.N); };
+        for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+            const PagedSeq r(a, b);
+            if (!r.ok && tid == 0) atomicOr(a.ctl.err, ERR_CACHE_RANGE);
+            clear_rows(row_at(b) + r.n, row_at(b + 1));
         }
+        if (blockIdx.x == 0) clear_rows(0, row_at(0));
+        if (blockIdx.x == gridDim.x - 1) clear_rows(row_at(a.B), a.N);
         RowState<D, NT> st;
         const float unscaled = kLog2e * rsqrtf((float)D) * a.k_up;
         while (at.left > 0) {
             const PagedSeq q(a, at.b);
             const int j1 = min(at.tiles, at.j + at.left);   // segment: tiles [at.j, j1) of the head
-            uint32_t qf[NT][D / 16][2];
             float f[NT][2];
             uint32_t off[NT][2];
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                const int row = 8 * (NT * rt + n) + g, i = row * a.g_inverse >> 16;
-                load_row<D>(row < a.rows && i < q.n
-                                ? a.Q + (a.token(at.b, i) * a.Hq + (at.kvh - i) * a.G + row) * D : nullptr, t, qf[n]);
                 const float back = row_to_f16<D, E2M1>(qf[n], t, off[n]) * unscaled;
 #pragma unroll
                 for (int e = 0; e < 2; ++e) f[n][e] = __shfl_sync(0xffffffffu, back, 4 * (2 * t + e));
@@ -826,6 +855,7 @@ __global__ void __launch_bounds__(Config<D, NT>::THREADS, 1) cache4_attn_kernel(
                 }
             }
             at.next_head(a);
+            if (at.left > 0) load_queries(PagedSeq(a, at.b));
         }
         if constexpr (C::ALONE) {
             // (a warp that gave up stays until its copies have landed: the CTA keeps its shared memory that long)
@@ -848,17 +878,24 @@ __global__ void __launch_bounds__(Config<D, NT>::THREADS, 1) cache4_attn_kernel(
     else if (joined) parts = min(teams, deal.taker(head_place + head_tiles - 1) - me * teams + 1);
     if ((by_head || joined) && named_bar_and(kSlots + 1, kConsumers, ok && !*abort_flag) && (joined || parts > 1)) {
         const int b = by_head ? me / a.Hkv : 0, n = by_head ? PagedSeq(a, b).n : 0;
-        // each part's weight in each row, and the rows' sums
-        for (int idx = tid; idx < a.rows * parts; idx += kConsumers) {
-            const int row = idx % a.rows, part = idx / a.rows;
-            const auto state = [&](int i) { return *reinterpret_cast<const float2*>(slot_of(i) + row * STRIDE + D); };
+        // each part's weight in each row, and the rows' sums: a row's parts in lanes next to each other
+        if (tid < ((a.rows * teams + 31) & ~31)) {
+            const int row = tid >> a.lg_teams, part = tid & (teams - 1);
             float m = -INFINITY, l = 0.f;
-            for (int i = 0; i < parts; ++i) m = fmaxf(m, state(i).x);
-            s_weight[idx] = part_weight(state(part).x, m);
-            if (part == 0) {
-                for (int i = 0; i < parts; ++i) l += state(i).y * part_weight(state(i).x, m);
+            if (row < a.rows && part < parts) {
+                const float2 x = *reinterpret_cast<const float2*>(slot_of(part) + row * STRIDE + D);
+                m = x.x;
+                l = x.y;
+            }
+            float top = m;
+            for (int sh = 1; sh < teams; sh <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, sh));
+            const float w = part_weight(m, top);
+            l *= w;
+            for (int sh = 1; sh < teams; sh <<= 1) l += __shfl_xor_sync(0xffffffffu, l, sh);
+            if (row < a.rows) {
+                s_weight[part * a.rows + row] = w;
                 s_l[row] = l;
-                s_m[row] = m;
+                s_m[row] = top;
             }
         }
         named_bar_sync(kSlots + 1, kConsumers);
@@ -884,21 +921,6 @@ __global__ void __launch_bounds__(Config<D, NT>::THREADS, 1) cache4_attn_kernel(
             }
         }
     }
-
-    // rows that count for no request are zero
-    const auto clear_rows = [&](int from, int to) {
-        const long long words = (long long)a.Hq * D / 8;
-        for (long long i = from * words + tid; i < to * words; i += kConsumers)
-            reinterpret_cast<uint4*>(a.O)[i] = make_uint4(0, 0, 0, 0);
-    };
-    const auto row_at = [&](int b) { return min(max(a.cu[b], 0), a.N); };
-    for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
-        const PagedSeq r(a, b);
-        if (!r.ok && tid == 0) atomicOr(a.ctl.err, ERR_CACHE_RANGE);
-        clear_rows(row_at(b) + r.n, row_at(b + 1));
-    }
-    if (blockIdx.x == 0) clear_rows(0, row_at(0));
-    if (blockIdx.x == gridDim.x - 1) clear_rows(row_at(a.B), a.N);
 }
 
 // Shared memory and ring of one problem.

@@ -207,52 +207,90 @@ __device__ __forceinline__ uint32_t keep_tokens(int left, int t) {
     return (over > 0 ? 0xffu : 0u) | (over > 1 ? 0xff00u : 0u) | (over > 8 ? 0xff0000u : 0u) | (over > 9 ? 0xff000000u : 0u);
 }
 
-// The exponent ev >= 0 of the largest of a warp's value scales: all are below 2^ev or
-// at most 1. Each lane looks at its share of the 16 MT tokens', past `left` tokens at none.
+// The exponent ev >= 0 of the largest of the value scales of 16 MT tokens: all are below 2^ev or
+// at most 1.
 template <int D, int MT>
-__device__ __forceinline__ float scale_exponent(const uint8_t* scales, int lane, int left) {
+__device__ __forceinline__ float scale_exponent(const uint8_t* scales, int lane) {
     constexpr int W = MT * D / 128;   // words of a lane
     uint32_t w[W], top = 0;
     load_words(scales + 4 * W * lane, w);
 #pragma unroll
     for (int k = 0; k < W; ++k) {
-        uint32_t x = w[k] & 0x7f7f7f7fu;
-        if (left < 16 * MT) {
-            const int word = W * lane + k;
-            x &= keep_tokens(left - 16 * (word / (D / 4)), word % (D / 4) / (D / 16));
-        }
+        const uint32_t x = w[k] & 0x7f7f7f7fu;
         top = max_u16x2(top, max_u16x2(x, x << 8));
     }
     const uint32_t byte = __reduce_max_sync(0xffffffffu, max(top >> 24, top >> 8 & 0xffu));
     return (float)max((int)(byte >> 3) - 6, 0);
 }
 
-// The products of a warp's 16 MT tokens become weights: element 2 x + e of s[n][i] is token
+// Value scales of the tokens past the page's first `left`: zero, not what was there before (NaN,
+// maybe). In shared memory, by a warp.
+template <int D>
+__device__ __forceinline__ void clear_scales(uint8_t* scales, int lane, int left) {
+#pragma unroll
+    for (int k = 0; k < D / 32; ++k) {
+        const int word = 32 * k + lane;
+        reinterpret_cast<uint32_t*>(scales)[word] &= keep_tokens(left - 16 * (word / (D / 4)), word % (D / 4) / (D / 16));
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // (before the stage's next copy)
+    __syncwarp();
+}
+
+using Pair = unsigned long long;   // two float32 numbers
+__device__ __forceinline__ Pair pair_of(float lo, float hi) {
+    Pair r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void unpair(Pair x, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x));
+}
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+    Pair r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ Pair add2(Pair a, Pair b) {
+    Pair r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// The products of 16 MT tokens become weights: element 2 x + e of s[n][i] is token
 // at + 16 i + 8 x and row 8 n + 2 t + e, seen up to token lim; times f it is the score
 // (log2 units). On return s holds p 2^-m, and l and m are up to date. m is compared with
 // the lane's own largest score only; the row's is found when one of them has to move.
-// (Sums with m are rounded towards larger m: whatever the scores' size, no weight times
-// 2^ev exceeds 2^(kUp + kMove).)
+// No weight times 2^ev exceeds 2^(kUp + kMove + 1 / 16): sums with m are rounded towards larger m,
+// and where m is so large that its own last place counts (far), so is every score.
 template <int D, int NT, int MT, bool MASK>
 __device__ __forceinline__ void soften(float (&s)[NT][MT][4], const float (&f)[NT][2], int at, const int (&lim)[NT][2],
-                                       float ev, RowState<D, NT>& st) {
+                                       float ev, RowState<D, NT>& st, bool& far) {
     float top[NT][2];
     bool need = false;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-        top[n][0] = top[n][1] = -INFINITY;
 #pragma unroll
         for (int i = 0; i < MT; ++i)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                s[n][i][e] = __fmul_rn(s[n][i][e], f[n][e & 1]);   // (rounded, as m is)
+            for (int e = 0; e < 4; ++e)
                 if (MASK && at + 16 * i + 8 * (e >> 1) > lim[n][e & 1]) s[n][i][e] = -INFINITY;
-                top[n][e & 1] = fmaxf(top[n][e & 1], s[n][i][e]);   // (a score that is no number: the weights show it)
-            }
 #pragma unroll
-        for (int e = 0; e < 2; ++e) need = need || __fadd_ru(top[n][e], ev - (kUp + kMove)) > st.m[n][e];
+        for (int e = 0; e < 2; ++e) {
+            // (a score that is no number is not above anything: the weights show it)
+            float x = fmaxf(s[n][0][e], s[n][0][2 + e]);
+#pragma unroll
+            for (int i = 1; i < MT; ++i) x = max3(x, s[n][i][e], s[n][i][2 + e]);
+            top[n][e] = MASK && x == -INFINITY ? x : x * f[n][e];
+            need = need || __fadd_ru(top[n][e], ev - (kUp + kMove)) > st.m[n][e];
+        }
     }
     if (__any_sync(0xffffffffu, need)) {
+        bool large = false;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             float fo[2];
@@ -265,26 +303,43 @@ __device__ __forceinline__ void soften(float (&s)[NT][MT][4], const float (&f)[N
                 fo[e] = st.m[n][e] == -INFINITY ? 0.f : ex2_approx(st.m[n][e] - m);
                 st.l[n][e] *= fo[e];
                 st.m[n][e] = m;
+                large = large || (fabsf(m) > 1048576.f && m != -INFINITY);
             }
 #pragma unroll
             for (int i = 0; i < D / 16; ++i)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) st.o[n][i][e] *= fo[e & 1];
         }
+        far = __any_sync(0xffffffffu, large);
     }
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
         float m[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) m[e] = st.m[n][e] == -INFINITY ? 0.f : st.m[n][e];   // (no token seen yet)
+        const Pair minus = pair_of(-m[0], -m[1]), scale = pair_of(f[n][0], f[n][1]);
+        Pair l = pair_of(st.l[n][0], st.l[n][1]);
 #pragma unroll
         for (int i = 0; i < MT; ++i)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float p = ex2_approx(__fsub_rn(s[n][i][e], m[e & 1]));   // (masked: 2^-inf)
-                st.l[n][e & 1] += p;
-                s[n][i][e] = p;
+            for (int x = 0; x < 2; ++x) {
+                float p[2];
+                if (far) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) p[e] = __fsub_rn(__fmul_rn(s[n][i][2 * x + e], f[n][e]), m[e]);
+                } else {
+                    unpair(fma2(pair_of(s[n][i][2 * x], s[n][i][2 * x + 1]), scale, minus), p[0], p[1]);
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    p[e] = ex2_approx(p[e]);
+                    // masked: nothing, whatever the factors are (0 * -inf among them)
+                    if (MASK && at + 16 * i + 8 * x > lim[n][e]) p[e] = 0.f;
+                    s[n][i][2 * x + e] = p[e];
+                }
+                l = add2(l, pair_of(p[0], p[1]));
             }
+        unpair(l, st.l[n][0], st.l[n][1]);
     }
 }
 
@@ -423,22 +478,27 @@ struct Feed {
         if (next.left > 0) enter(a);
     }
     __device__ __forceinline__ bool more() const { return next.left > 0; }
-    // The next half page, to `to`; `go` in the thread that issues it.
+    // The next half page, to `to`; `go` in the thread that issues it. (No branch for one thread of a warp: two such a
+    // page were a tenth of its time.)
     __device__ __forceinline__ void issue(const Cache4Args& a, uint8_t* to, uint64_t* full, bool go) {
         constexpr uint32_t STAGE = half_bytes(D);
-        if (go) {
-            if (page >= 0 && page < a.n_pages) {
-                mbar_arrive_expect_tx(full, STAGE);
-                bulk_load(to, a.pool + (((long long)page * a.Hkv + next.kvh) * 2 + (values ? 1 : 0)) * STAGE, STAGE, full);
-            } else {
-                // no page of the pool: keys whose scales are NaN (who sees them is NaN), values of scale 0
-                uint4* scales = reinterpret_cast<uint4*>(to + key_scales_at(D));
-                const uint32_t x = values ? 0u : 0x7f7f7f7fu;
-                for (int k = 0; k < 4 * D / 16; ++k) scales[k] = make_uint4(x, x, x, x);
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // (before the stage's next copy)
-                mbar_arrive(full);
-                atomicOr(a.ctl.err, ERR_CACHE_RANGE);
-            }
+        if (page >= 0 && page < a.n_pages) {
+            const uint8_t* from = a.pool + (((long long)page * a.Hkv + next.kvh) * 2 + (values ? 1 : 0)) * STAGE;
+            asm volatile(
+                "{\n\t.reg .pred p;\n\t"
+                "setp.ne.u32 p, %4, 0;\n\t"
+                "@p mbarrier.arrive.expect_tx.shared::cta.b64 _, [%2], %3;\n\t"
+                "@p cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %3, [%2];\n\t}" ::"r"(smem_u32(to)),
+                "l"(from), "r"(smem_u32(full)), "r"(STAGE), "r"((uint32_t)go)
+                : "memory");
+        } else if (go) {
+            // no page of the pool: keys whose scales are NaN (who sees them is NaN), values of scale 0
+            uint4* scales = reinterpret_cast<uint4*>(to + key_scales_at(D));
+            const uint32_t x = values ? 0u : 0x7f7f7f7fu;
+            for (int k = 0; k < 4 * D / 16; ++k) scales[k] = make_uint4(x, x, x, x);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // (before the stage's next copy)
+            mbar_arrive(full);
+            atomicOr(a.ctl.err, ERR_CACHE_RANGE);
         }
         if (values) {
             if (next.j + 1 < next.tiles) {
@@ -623,12 +683,17 @@ __global__ void __launch_bounds__(Config<D, NT>::THREADS, 1) cache4_attn_kernel(
             for (; ahead < a.stages && feed.more(); ++ahead)
                 feed.issue(a, smem + ((size_t)team * a.stages + ahead) * STAGE, &full[ahead], lane == 0);
         }
-        const auto wait_full = [&]() -> const uint8_t* {
-            if (!__all_sync(0xffffffffu, mbar_wait(&full[stage], phase, abort_flag, a.ctl))) {
+        const auto wait_full = [&](uint32_t next) -> const uint8_t* {   // that stage, or the next
+            uint32_t k = stage + next, ph = phase;
+            if (k >= (uint32_t)a.stages) {
+                k -= a.stages;
+                ph ^= 1u;
+            }
+            if (!__all_sync(0xffffffffu, mbar_wait(&full[k], ph, abort_flag, a.ctl))) {
                 ok = false;
                 return nullptr;
             }
-            return ring + stage * STAGE;
+            return ring + k * STAGE;
         };
         const auto release = [&]() {
             __syncwarp();
@@ -683,10 +748,19 @@ __global__ void __launch_bounds__(Config<D, NT>::THREADS, 1) cache4_attn_kernel(
                 for (int e = 0; e < 2; ++e) f[n][e] = __shfl_sync(0xffffffffu, back, 4 * (2 * t + e));
             }
             st.clear();
+            bool far = false;   // (scores so large that their own last place counts: see soften)
             for (int j = at.j; ok && j < j1; ++j) {
                 float s[NT][MT][4];
-                const uint8_t* kt = wait_full();
+                const uint8_t* kt = wait_full(0);
                 if (!kt) break;
+                const uint8_t* vt = wait_full(1);
+                if (!vt) break;
+                // (the first query row sees tokens up to len: tiles before need no mask)
+                const int base = j * kPage;
+                const bool masked = base + kPage - 1 > q.len;
+                const uint8_t* scales = vt + key_scales_at(D);   // (as far into the values' half)
+                if (masked && q.T < base + kPage) clear_scales<D>(const_cast<uint8_t*>(scales), lane, q.T - base);
+                const float ev = scale_exponent<D, MT>(scales, lane);
 #pragma unroll
                 for (int i = 0; i < MT; ++i) {
                     const int n0 = 16 * i + g;   // and n0 + 8
@@ -734,13 +808,6 @@ __global__ void __launch_bounds__(Config<D, NT>::THREADS, 1) cache4_attn_kernel(
                     }
                 }
                 release();
-                const uint8_t* vt = wait_full();
-                if (!vt) break;
-                // (the first query row sees tokens up to len: tiles before need no mask)
-                const int base = j * kPage, left = q.T - base;
-                const bool masked = base + kPage - 1 > q.len;
-                const uint8_t* scales = vt + key_scales_at(D);   // (as far into the values' half)
-                const float ev = scale_exponent<D, MT>(scales, lane, masked ? left : 16 * MT);
                 int lim[NT][2] = {};
                 if (masked) {
 #pragma unroll
@@ -750,9 +817,9 @@ __global__ void __launch_bounds__(Config<D, NT>::THREADS, 1) cache4_attn_kernel(
                             const int row = 8 * (NT * rt + n) + 2 * t + e, i = row * a.g_inverse >> 16;
                             lim[n][e] = row < a.rows && i < q.n ? q.len + i : -1;
                         }
-                    soften<D, NT, MT, true>(s, f, base + g, lim, ev, st);
+                    soften<D, NT, MT, true>(s, f, base + g, lim, ev, st, far);
                 } else {
-                    soften<D, NT, MT, false>(s, f, base + g, lim, ev, st);
+                    soften<D, NT, MT, false>(s, f, base + g, lim, ev, st, far);
                 }
 #pragma unroll
                 for (int i = 0; i < MT; ++i) {
@@ -762,12 +829,6 @@ __global__ void __launch_bounds__(Config<D, NT>::THREADS, 1) cache4_attn_kernel(
 #pragma unroll
                         for (int x = 0; x < 2; ++x) pf[n][x] = transpose8(pack_f16x2(s[n][i][2 * x], s[n][i][2 * x + 1]));
                     load_words(scales + i * D + t * (D / 4), sw);
-                    if (masked) {
-                        // slots past the request's end hold whatever was there before: scale 0, not NaN
-                        const uint32_t keep = keep_tokens(left - 16 * i, t);
-#pragma unroll
-                        for (int c = 0; c < D / 16; ++c) sw[c] &= keep;
-                    }
 #pragma unroll
                     for (int quad = 0; quad < D / 64; ++quad) {
                         uint32_t w[4];

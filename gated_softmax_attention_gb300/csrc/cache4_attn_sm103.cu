@@ -262,13 +262,13 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 }
 
 // The products of 16 MT tokens become weights: element 2 x + e of s[n][i] is token
-// at + 16 i + 8 x and row 8 n + 2 t + e, seen up to token lim; times f it is the score
+// at + 16 i + 8 x and row 8 n + 2 t + e (EL = 2: row 2 (t % 2) + e), seen up to token lim; times f it is the score
 // (log2 units). On return s holds p 2^-m, and l and m are up to date. m is compared with
 // the lane's own largest score only; the row's is found when one of them has to move.
 // No weight times 2^ev exceeds 2^(kUp + kMove + 1 / 16): sums with m are rounded towards larger m,
 // and where m is so large that its own last place counts (far), so is every score.
-template <int D, int NT, int MT, bool MASK>
-__device__ __forceinline__ void soften(float (&s)[NT][MT][4], const float (&f)[NT][2], int at, const int (&lim)[NT][2],
+template <int D, int NT, int MT, int EL, bool MASK>
+__device__ __forceinline__ void soften(float (&s)[NT][MT][EL], const float (&f)[NT][2], int at, const int (&lim)[NT][2],
                                        float ev, RowState<D, NT>& st, bool& far) {
     float top[NT][2];
     bool need = false;
@@ -277,14 +277,19 @@ __device__ __forceinline__ void soften(float (&s)[NT][MT][4], const float (&f)[N
 #pragma unroll
         for (int i = 0; i < MT; ++i)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
+            for (int e = 0; e < EL; ++e)
                 if (MASK && at + 16 * i + 8 * (e >> 1) > lim[n][e & 1]) s[n][i][e] = -INFINITY;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             // (a score that is no number is not above anything: the weights show it)
-            float x = fmaxf(s[n][0][e], s[n][0][2 + e]);
-#pragma unroll
-            for (int i = 1; i < MT; ++i) x = max3(x, s[n][i][e], s[n][i][2 + e]);
+            static_assert(MT == 4, "four groups of 16 tokens");
+            float x = max3(s[n][0][e], s[n][1][e], s[n][2][e]);
+            if constexpr (EL == 4) {
+                x = max3(x, s[n][3][e], s[n][0][2 + e]);
+                x = fmaxf(max3(x, s[n][1][2 + e], s[n][2][2 + e]), s[n][3][2 + e]);
+            } else {
+                x = fmaxf(x, s[n][3][e]);
+            }
             top[n][e] = MASK && x == -INFINITY ? x : x * f[n][e];
             need = need || __fadd_ru(top[n][e], ev - (kUp + kMove)) > st.m[n][e];
         }
@@ -298,7 +303,7 @@ __device__ __forceinline__ void soften(float (&s)[NT][MT][4], const float (&f)[N
             for (int e = 0; e < 2; ++e) {
                 float x = top[n][e];
 #pragma unroll
-                for (int sh = 4; sh < 32; sh <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, sh));
+                for (int sh = EL == 4 ? 4 : 2; sh < 32; sh <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, sh));
                 const float m = fmaxf(st.m[n][e], __fadd_ru(x, ev - kUp));
                 fo[e] = st.m[n][e] == -INFINITY ? 0.f : ex2_approx(st.m[n][e] - m);
                 st.l[n][e] *= fo[e];
@@ -322,7 +327,7 @@ __device__ __forceinline__ void soften(float (&s)[NT][MT][4], const float (&f)[N
 #pragma unroll
         for (int i = 0; i < MT; ++i)
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
+            for (int x = 0; x < EL / 2; ++x) {
                 float p[2];
                 if (far) {
 #pragma unroll
@@ -344,13 +349,13 @@ __device__ __forceinline__ void soften(float (&s)[NT][MT][4], const float (&f)[N
 }
 
 // A query row as the first product's narrow operand: product j of lane t covers
-// columns 16 j + 4 t .. + 3.
-template <int D>
-__device__ __forceinline__ void load_row(const __nv_bfloat16* src, int t, uint32_t (&w)[D / 16][2]) {
+// columns 16 j + 4 t .. + 3. HALF: of the even or the odd products only, the others zero.
+template <int D, bool HALF>
+__device__ __forceinline__ void load_row(const __nv_bfloat16* src, int t, int odd, uint32_t (&w)[D / 16][2]) {
 #pragma unroll
     for (int j = 0; j < D / 16; ++j) {
         uint2 v = make_uint2(0, 0);
-        if (src) v = *reinterpret_cast<const uint2*>(src + 16 * j + 4 * t);
+        if (src && (!HALF || j % 2 == odd)) v = *reinterpret_cast<const uint2*>(src + 16 * j + 4 * t);
         w[j][0] = v.x;
         w[j][1] = v.y;
     }
@@ -361,7 +366,7 @@ __device__ __forceinline__ void load_row(const __nv_bfloat16* src, int t, uint32
 // narrow operand that gives the codes' 8, -2^-4 times the row's sums over each 16 columns,
 // as two fp16 parts (22 bits): lane t has those of groups 2 t, 2 t + 1 (d_k 64: the
 // first parts in t < 2, the second in t >= 2).
-template <int D, bool E2M1>
+template <int D, bool E2M1, bool HALF>
 __device__ __forceinline__ float row_to_f16(uint32_t (&w)[D / 16][2], int t, uint32_t (&off)[2]) {
     uint32_t top = 0;
 #pragma unroll
@@ -370,6 +375,7 @@ __device__ __forceinline__ float row_to_f16(uint32_t (&w)[D / 16][2], int t, uin
         for (int h = 0; h < 2; ++h) top = max(top, max(w[j][h] & 0x7fffu, (w[j][h] >> 16) & 0x7fffu));
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    if (HALF) top = max(top, __shfl_xor_sync(0xffffffffu, top, 16));   // (the row's other products)
     const uint32_t e = min(max(top >> 7, 15u), 252u);   // the largest element's exponent field, so that both factors are
     const float scale = __uint_as_float((268u - e) << 23);
     float mine[2] = {0.f, 0.f};
@@ -515,7 +521,7 @@ struct Feed {
     }
 };
 
-template <int D, bool E2M1, int NT>
+template <int D, bool E2M1, int NT, bool HALF>
 __global__ void __launch_bounds__(Config<D, NT>::THREADS, 1) cache4_attn_kernel(const __grid_constant__ Cache4Args a) {
     using C = Config<D, NT>;
     constexpr uint32_t STAGE = C::STAGE;
@@ -671,9 +677,10 @@ __global__ void __launch_bounds__(Config<D, NT>::THREADS, 1) cache4_attn_kernel(
         const auto load_queries = [&](const PagedSeq& q) {
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                const int row = 8 * (NT * rt + n) + g, i = row * a.g_inverse >> 16;
-                load_row<D>(row < a.rows && i < q.n
-                                ? a.Q + (a.token(at.b, i) * a.Hq + (at.kvh - i) * a.G + row) * D : nullptr, t, qf[n]);
+                const int row = HALF ? g & 3 : 8 * (NT * rt + n) + g, i = row * a.g_inverse >> 16;
+                load_row<D, HALF>(row < a.rows && i < q.n
+                                      ? a.Q + (a.token(at.b, i) * a.Hq + (at.kvh - i) * a.G + row) * D : nullptr,
+                                  t, g >> 2, qf[n]);
             }
         };
         if (at.left > 0) load_queries(PagedSeq(a, at.b));
@@ -743,14 +750,15 @@ __global__ void __launch_bounds__(Config<D, NT>::THREADS, 1) cache4_attn_kernel(
             uint32_t off[NT][2];
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                const float back = row_to_f16<D, E2M1>(qf[n], t, off[n]) * unscaled;
+                const float back = row_to_f16<D, E2M1, HALF>(qf[n], t, off[n]) * unscaled;
 #pragma unroll
-                for (int e = 0; e < 2; ++e) f[n][e] = __shfl_sync(0xffffffffu, back, 4 * (2 * t + e));
+                for (int e = 0; e < 2; ++e) f[n][e] = __shfl_sync(0xffffffffu, back, 4 * (2 * (HALF ? t & 1 : t) + e));
             }
             st.clear();
             bool far = false;   // (scores so large that their own last place counts: see soften)
             for (int j = at.j; ok && j < j1; ++j) {
-                float s[NT][MT][4];
+                constexpr int EL = HALF ? 2 : 4;
+                float s[NT][MT][EL];
                 const uint8_t* kt = wait_full(0);
                 if (!kt) break;
                 const uint8_t* vt = wait_full(1);
@@ -769,57 +777,100 @@ __global__ void __launch_bounds__(Config<D, NT>::THREADS, 1) cache4_attn_kernel(
                     load_words(kt + (n0 + 8) * (D / 2) + t * (D / 8), y);
                     load_words(kt + key_scales_at(D) + n0 * (D / 16), xs);
                     load_words(kt + key_scales_at(D) + (n0 + 8) * (D / 16), ys);
+                    float sum[NT][4];
                     if constexpr (!E2M1) {   // the sums start at -8 times q's
                         const uint8_t* own = kt + key_scales_at(D) + n0 * (D / 16) + 2 * (D == 128 ? t : t % 2);
                         const uint32_t ax = scale_pair(own), ay = scale_pair(own + 8 * (D / 16)), op[4] = {ax, ay, ax, ay};
 #pragma unroll
                         for (int n = 0; n < NT; ++n) {
-                            mma_f16_from(s[n][i], op, off[n][0], off[n][1], 0.f);
+                            mma_f16_from(sum[n], op, off[n][0], off[n][1], 0.f);
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) s[n][i][e] *= 7.62939453125e-06f;   // 2^-17
+                            for (int e = 0; e < 4; ++e) sum[n][e] *= 7.62939453125e-06f;   // 2^-17
                         }
                     }
-                    uint32_t hx[D / 32], hy[D / 32];
+                    const auto add = [&](int n, const float (&r)[4], float kx, float ky, bool first) {
 #pragma unroll
-                    for (int w = 0; w < D / 64; ++w) {
-                        scales_to_f16(xs[w], hx[2 * w], hx[2 * w + 1]);
-                        scales_to_f16(ys[w], hy[2 * w], hy[2 * w + 1]);
-                    }
+                        for (int e = 0; e < 4; ++e)
+                            sum[n][e] = E2M1 && first ? r[e] * (e < 2 ? kx : ky) : fmaf(r[e], e < 2 ? kx : ky, sum[n][e]);
+                    };
+                    if constexpr (HALF) {
+                        // lanes t < 2 have the even groups' sums of rows 0 .. 3, the others the odd groups'
+                        float2 fx[D / 64], fy[D / 64];
 #pragma unroll
-                    for (int w = 0; w < D / 32; ++w) {   // two groups of columns
-                        uint32_t xc[4], yc[4];
-                        codes_to_f16<E2M1>(x[w], xc);
-                        codes_to_f16<E2M1>(y[w], yc);
-                        const float2 fx = floats(hx[w]), fy = floats(hy[w]);
+                        for (int w = 0; w < D / 64; ++w) {
+                            const uint32_t pick = t & 2 ? 0x4431u : 0x4420u;
+                            uint32_t hx, hy, none;
+                            scales_to_f16(__byte_perm(xs[w], 0, pick), hx, none);
+                            scales_to_f16(__byte_perm(ys[w], 0, pick), hy, none);
+                            fx[w] = floats(hx);
+                            fy[w] = floats(hy);
+                        }
 #pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const uint32_t op[4] = {xc[2 * k], yc[2 * k], xc[2 * k + 1], yc[2 * k + 1]};
-                            const float kx = k ? fx.y : fx.x, ky = k ? fy.y : fy.x;
+                        for (int w = 0; w < D / 32; ++w) {   // two groups of columns
+                            uint32_t xc[4], yc[4];
+                            codes_to_f16<E2M1>(x[w], xc);
+                            codes_to_f16<E2M1>(y[w], yc);
+                            const uint32_t even[4] = {xc[0], yc[0], xc[1], yc[1]}, odd[4] = {xc[2], yc[2], xc[3], yc[3]};
 #pragma unroll
                             for (int n = 0; n < NT; ++n) {
-                                const int c = 2 * w + k;
                                 float r[4];
-                                mma_f16_from(r, op, qf[n][c][0], qf[n][c][1], 0.f);
-#pragma unroll
-                                for (int e = 0; e < 4; ++e)
-                                    s[n][i][e] = E2M1 && c == 0 ? r[e] * (e < 2 ? kx : ky) : fmaf(r[e], e < 2 ? kx : ky, s[n][i][e]);
+                                mma_f16_from(r, even, qf[n][2 * w][0], qf[n][2 * w][1], 0.f);
+                                mma_f16(r, odd, qf[n][2 * w + 1][0], qf[n][2 * w + 1][1]);
+                                add(n, r, w % 2 ? fx[w / 2].y : fx[w / 2].x, w % 2 ? fy[w / 2].y : fy[w / 2].x, w == 0);
                             }
                         }
+                        // both added up: token n0 in lanes t < 2, n0 + 8 in the others
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e)
+                                s[n][i][e] = (t & 2 ? sum[n][2 + e] : sum[n][e]) +
+                                             __shfl_xor_sync(0xffffffffu, t & 2 ? sum[n][e] : sum[n][2 + e], 2);
+                    } else {
+                        uint32_t hx[D / 32], hy[D / 32];
+#pragma unroll
+                        for (int w = 0; w < D / 64; ++w) {
+                            scales_to_f16(xs[w], hx[2 * w], hx[2 * w + 1]);
+                            scales_to_f16(ys[w], hy[2 * w], hy[2 * w + 1]);
+                        }
+#pragma unroll
+                        for (int w = 0; w < D / 32; ++w) {   // two groups of columns
+                            uint32_t xc[4], yc[4];
+                            codes_to_f16<E2M1>(x[w], xc);
+                            codes_to_f16<E2M1>(y[w], yc);
+                            const float2 fx = floats(hx[w]), fy = floats(hy[w]);
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                const uint32_t op[4] = {xc[2 * k], yc[2 * k], xc[2 * k + 1], yc[2 * k + 1]};
+#pragma unroll
+                                for (int n = 0; n < NT; ++n) {
+                                    const int c = 2 * w + k;
+                                    float r[4];
+                                    mma_f16_from(r, op, qf[n][c][0], qf[n][c][1], 0.f);
+                                    add(n, r, k ? fx.y : fx.x, k ? fy.y : fy.x, c == 0);
+                                }
+                            }
+                        }
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int e = 0; e < EL; ++e) s[n][i][e] = sum[n][e];
                     }
                 }
                 release();
                 int lim[NT][2] = {};
+                const int at0 = base + g + (HALF ? 4 * (t & 2) : 0);   // the lane's first token
                 if (masked) {
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {   // the last token that each of the lane's rows sees
-                            const int row = 8 * (NT * rt + n) + 2 * t + e, i = row * a.g_inverse >> 16;
+                            const int row = 8 * (NT * rt + n) + 2 * (HALF ? t & 1 : t) + e, i = row * a.g_inverse >> 16;
                             lim[n][e] = row < a.rows && i < q.n ? q.len + i : -1;
                         }
-                    soften<D, NT, MT, true>(s, f, base + g, lim, ev, st, far);
+                    soften<D, NT, MT, EL, true>(s, f, at0, lim, ev, st, far);
                 } else {
-                    soften<D, NT, MT, false>(s, f, base + g, lim, ev, st, far);
+                    soften<D, NT, MT, EL, false>(s, f, at0, lim, ev, st, far);
                 }
 #pragma unroll
                 for (int i = 0; i < MT; ++i) {
@@ -827,7 +878,12 @@ __global__ void __launch_bounds__(Config<D, NT>::THREADS, 1) cache4_attn_kernel(
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
 #pragma unroll
-                        for (int x = 0; x < 2; ++x) pf[n][x] = transpose8(pack_f16x2(s[n][i][2 * x], s[n][i][2 * x + 1]));
+                        for (int x = 0; x < EL / 2; ++x)
+                            pf[n][x] = transpose8(pack_f16x2(s[n][i][2 * x], s[n][i][2 * x + 1]));
+                    if constexpr (HALF) {   // (tokens 8 .. 15 came out in lanes g >= 4)
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) pf[n][1] = __shfl_xor_sync(0xffffffffu, pf[n][0], 16);
+                    }
                     load_words(scales + i * D + t * (D / 4), sw);
 #pragma unroll
                     for (int quad = 0; quad < D / 64; ++quad) {
@@ -864,7 +920,7 @@ __global__ void __launch_bounds__(Config<D, NT>::THREADS, 1) cache4_attn_kernel(
                 for (int e = 0; e < 2; ++e) {
                     st.M[n][e] = st.m[n][e];
 #pragma unroll
-                    for (int sh = 4; sh < 32; sh <<= 1)
+                    for (int sh = HALF ? 2 : 4; sh < 32; sh <<= 1)
                         st.l[n][e] += __shfl_xor_sync(0xffffffffu, st.l[n][e], sh);
                     k[e] = unit;
                     // (a row that saw nothing is zero)
@@ -1052,20 +1108,21 @@ int plan_cache4(const gsdpa_cache4* c, int B, int max_pages, int n_rows, int max
     return GSDPA_OK;
 }
 
-template <int D, bool E2M1, int NT>
+template <int D, bool E2M1, int NT, bool HALF>
 cudaError_t launch(const Cache4Args& a, const Shape& sh, unsigned grid, cudaStream_t s) {
     static PerDeviceSetup setup;
     const cudaError_t e = setup_once_per_device(setup, [](int&) {
-        return cudaFuncSetAttribute(cache4_attn_kernel<D, E2M1, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        return cudaFuncSetAttribute(cache4_attn_kernel<D, E2M1, NT, HALF>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     (int)kSmemMax);
     });
     if (e != cudaSuccess) return e;
-    return launch_dependent(cache4_attn_kernel<D, E2M1, NT>, dim3(grid), dim3(Config<D, NT>::THREADS), sh.smem, s,
+    return launch_dependent(cache4_attn_kernel<D, E2M1, NT, HALF>, dim3(grid), dim3(Config<D, NT>::THREADS), sh.smem, s,
                             a);
 }
 template <int D, bool E2M1>
 cudaError_t launch(const Cache4Args& a, const Shape& sh, unsigned grid, cudaStream_t s) {
-    return sh.NT == 1 ? launch<D, E2M1, 1>(a, sh, grid, s) : launch<D, E2M1, 2>(a, sh, grid, s);
+    if (sh.NT == 2) return launch<D, E2M1, 2, false>(a, sh, grid, s);
+    return a.rows <= 4 ? launch<D, E2M1, 1, true>(a, sh, grid, s) : launch<D, E2M1, 1, false>(a, sh, grid, s);
 }
 
 }  // namespace

@@ -987,10 +987,10 @@ def pages_step(lens, n_new, table, free_pages, n_free, n_rows, *, keep=None, out
     if out is None:
         if not table.is_cuda:
             raise ValueError(f"table must be a CUDA tensor, not on {table.device}")
-        # (one allocation and slices of it: the host's time of a step is longer than the kernel's)
-        flat = table.new_empty(2 * B + 2 + n_rows)
-        out = PagesStep(flat[:B + 1], flat[B + 1:2 * B + 1], torch.empty(n_rows, dtype=torch.int64, device=dev),
-                        flat[2 * B + 2:], flat[2 * B + 1:2 * B + 2])
+        # (allocations of their own: slices of one take the host longer)
+        make = table.new_empty
+        out = PagesStep(make(B + 1), make(B), torch.empty(n_rows, dtype=torch.int64, device=dev), make(n_rows),
+                        torch.empty_like(n_free))
     st = (_lib or load()).gsdpa_pages_step(
         _vector(lens, "lens", B, i32, dev), _vector(keep, "keep", B, i32, dev), _vector(n_new, "n_new", B, i32, dev),
         _vector(table, "table", B * width, i32, dev), _vector(free_pages, "free_pages", free_pages.numel(), i32, dev),
@@ -1102,7 +1102,7 @@ def gated_sdpa_cache4(X, Q, cache, table, lens, cu, W_g=None, *, gate="elementwi
         _vector(cu, "cu", B + 1, i32, dev)
     new = _vector(n_new, "n_new", B, i32, dev)
     if out is None:
-        out = torch.empty((N, H_q, d_k), dtype=bf, device=dev)
+        out = torch.empty_like(Q)
     o = _vector(out, "out", N * H_q * d_k, bf, dev)
     lib = _lib or load()
     shape = (B, width, N, max_new, d_model, H_q, gm)

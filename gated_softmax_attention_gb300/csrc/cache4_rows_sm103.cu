@@ -24,7 +24,9 @@
 namespace gsdpa {
 namespace {
 
-constexpr int kThreads = 256;
+// Threads of a block of 32 rows. (Prompts of 4 x 8190 tokens, e2m1: with 128 threads 37.0 us, with 256 38.0 and with 512
+// 45.0; reading 98k tokens 23.3, 25.5 and 37.6 us.)
+constexpr int kMany = 128;
 
 struct RowsArgs {
     const __nv_bfloat16 *K, *V;  // the append's
@@ -135,7 +137,7 @@ __device__ __forceinline__ void turn_bytes(uint32_t (&w)[4]) {
 
 // The rows of one block: the slot of each, and the runs of rows that lie in one tile of
 // 16 tokens (a run begins where the tile changes).
-template <int R>
+template <int R, int THREADS>
 struct Runs {
     long long slot[R];        // -1: none
     long long tile[R];        // by run: slot / 16
@@ -144,7 +146,7 @@ struct Runs {
     int n;                    // runs
     __device__ __forceinline__ void find(const RowsArgs& a, long long first) {
         const int tid = threadIdx.x;
-        for (int k = tid; k < R * 4; k += kThreads) reinterpret_cast<uint32_t*>(at)[k] = 0xffffffffu;
+        for (int k = tid; k < R * 4; k += THREADS) reinterpret_cast<uint32_t*>(at)[k] = 0xffffffffu;
         __syncthreads();
         if (tid < 32) {
             const long long row = first + tid;
@@ -206,9 +208,9 @@ struct Pieces {
     __device__ __forceinline__ int byte(int b) const { return scales || E2M1 ? b : (b >> 1) + 2 * (b & 1); }
 };
 
-template <int D, bool E2M1, int R>
-__global__ void __launch_bounds__(kThreads) cache4_append_kernel(const __grid_constant__ RowsArgs a) {
-    __shared__ Runs<R> runs;
+template <int D, bool E2M1, int R, int THREADS>
+__global__ void __launch_bounds__(THREADS) cache4_append_kernel(const __grid_constant__ RowsArgs a) {
+    __shared__ Runs<R, THREADS> runs;
     __shared__ Tokens<D, R> tok;
     pdl_trigger();
     pdl_wait();
@@ -216,12 +218,12 @@ __global__ void __launch_bounds__(kThreads) cache4_append_kernel(const __grid_co
     const long long first = (long long)blockIdx.x * R;
     // ---- a lane has a group's 16 columns; lanes next to each other the groups of one token. All is loaded at once,
     // before the slots are known.
-    constexpr int GROUPS = 2 * R * (D / 16), EACH = (GROUPS + kThreads - 1) / kThreads;
-    static_assert(GROUPS % kThreads == 0 || GROUPS < kThreads, "whole warps");
+    constexpr int GROUPS = 2 * R * (D / 16), EACH = (GROUPS + THREADS - 1) / THREADS;
+    static_assert(GROUPS % THREADS == 0 || GROUPS < THREADS, "whole warps");
     uint4 x[EACH][2];
 #pragma unroll
     for (int n = 0; n < EACH; ++n) {
-        const int k = n * kThreads + tid;
+        const int k = n * THREADS + tid;
         const bool value = k >= R * (D / 16);
         const int i = k % (R * (D / 16)), r = i / (D / 16), j = i % (D / 16);
         x[n][0] = x[n][1] = make_uint4(0, 0, 0, 0);
@@ -237,7 +239,7 @@ __global__ void __launch_bounds__(kThreads) cache4_append_kernel(const __grid_co
     // ---- codes and scales
 #pragma unroll
     for (int n = 0; n < EACH; ++n) {
-        const int k = n * kThreads + tid;
+        const int k = n * THREADS + tid;
         if (k >= GROUPS) break;
         const bool value = k >= R * (D / 16);
         const int i = k % (R * (D / 16)), r = i / (D / 16), j = i % (D / 16);
@@ -293,14 +295,14 @@ __global__ void __launch_bounds__(kThreads) cache4_append_kernel(const __grid_co
 
     // ---- keys: rows of D / 2 bytes, and their scales
     const auto page_of = [&](long long slot) { return a.pool + ((slot / kPage) * a.Hkv + h) * page_bytes(D); };
-    for (int k = tid; k < R * (D / 32); k += kThreads) {
+    for (int k = tid; k < R * (D / 32); k += THREADS) {
         const int r = k / (D / 32), c = k % (D / 32);
         const long long slot = runs.slot[r];
         if (slot >= 0)
             *reinterpret_cast<uint4*>(page_of(slot) + (slot % kPage) * (D / 2) + 16 * c) =
                 *reinterpret_cast<const uint4*>(&tok.key[r][16 * c]);
     }
-    for (int k = tid; k < R * (D / 64); k += kThreads) {
+    for (int k = tid; k < R * (D / 64); k += THREADS) {
         const int r = k / (D / 64), c = k % (D / 64);
         const long long slot = runs.slot[r];
         if (slot >= 0)
@@ -310,7 +312,7 @@ __global__ void __launch_bounds__(kThreads) cache4_append_kernel(const __grid_co
 
     // ---- values: four words of four tokens, run by run
     using P = Pieces<D>;
-    for (int k = tid; k < runs.n * P::ALL; k += kThreads) {
+    for (int k = tid; k < runs.n * P::ALL; k += THREADS) {
         const int run = k / P::ALL;
         const P p(k % P::ALL);
         uint32_t w[4];
@@ -357,9 +359,9 @@ __device__ __forceinline__ float2 code_values(uint32_t byte) {
     }
 }
 
-template <int D, bool E2M1, int R>
-__global__ void __launch_bounds__(kThreads) cache4_read_kernel(const __grid_constant__ RowsArgs a) {
-    __shared__ Runs<R> runs;
+template <int D, bool E2M1, int R, int THREADS>
+__global__ void __launch_bounds__(THREADS) cache4_read_kernel(const __grid_constant__ RowsArgs a) {
+    __shared__ Runs<R, THREADS> runs;
     __shared__ Tokens<D, R> tok;
     pdl_trigger();
     pdl_wait();
@@ -367,14 +369,14 @@ __global__ void __launch_bounds__(kThreads) cache4_read_kernel(const __grid_cons
     const long long first = (long long)blockIdx.x * R;
     runs.find(a, first);
     const auto page_of = [&](long long slot) { return a.pool + ((slot / kPage) * a.Hkv + h) * page_bytes(D); };
-    for (int k = tid; k < R * (D / 32); k += kThreads) {
+    for (int k = tid; k < R * (D / 32); k += THREADS) {
         const int r = k / (D / 32), c = k % (D / 32);
         const long long slot = runs.slot[r];
         if (slot >= 0)
             *reinterpret_cast<uint4*>(&tok.key[r][16 * c]) =
                 *reinterpret_cast<const uint4*>(page_of(slot) + (slot % kPage) * (D / 2) + 16 * c);
     }
-    for (int k = tid; k < R * (D / 64); k += kThreads) {
+    for (int k = tid; k < R * (D / 64); k += THREADS) {
         const int r = k / (D / 64), c = k % (D / 64);
         const long long slot = runs.slot[r];
         if (slot >= 0)
@@ -382,7 +384,7 @@ __global__ void __launch_bounds__(kThreads) cache4_read_kernel(const __grid_cons
                 *reinterpret_cast<const uint32_t*>(page_of(slot) + key_scales_at(D) + (slot % kPage) * (D / 16) + 4 * c);
     }
     using P = Pieces<D>;
-    for (int k = tid; k < runs.n * P::ALL; k += kThreads) {
+    for (int k = tid; k < runs.n * P::ALL; k += THREADS) {
         const int run = k / P::ALL;
         const P p(k % P::ALL);
         const uint4 x = *reinterpret_cast<const uint4*>(p.at(page_of(runs.tile[run] * 16), (int)(runs.tile[run] % 4)));
@@ -399,7 +401,7 @@ __global__ void __launch_bounds__(kThreads) cache4_read_kernel(const __grid_cons
     __syncthreads();
 
     // ---- a thread to a group's 16 columns
-    for (int k = tid; k < 2 * R * (D / 16); k += kThreads) {
+    for (int k = tid; k < 2 * R * (D / 16); k += THREADS) {
         const bool value = k >= R * (D / 16);
         const int i = k % (R * (D / 16)), r = i / (D / 16), j = i % (D / 16);
         if (first + r >= a.n_rows) continue;
@@ -458,16 +460,19 @@ int check_rows(const gsdpa_cache4* c, const void* K, const void* V, long long ld
 
 template <bool READ, int D, bool E2M1>
 cudaError_t launch(const RowsArgs& a, int sms, cudaStream_t s) {
-    const auto go = [&](auto kernel, int rows) {
+    const auto go = [&](auto kernel, int rows, int threads) {
         const dim3 grid((unsigned)((a.n_rows + (long long)rows - 1) / rows), (unsigned)a.Hkv);
-        return launch_dependent(kernel, grid, dim3(kThreads), 0, s, a);
+        return launch_dependent(kernel, grid, dim3(threads), 0, s, a);
     };
-    // Blocks of few rows until there are four for every SM.
-    const bool few = (a.n_rows + 31LL) / 32 * a.Hkv < 4LL * sms;
-    if constexpr (READ)
-        return few ? go(cache4_read_kernel<D, E2M1, 8>, 8) : go(cache4_read_kernel<D, E2M1, 32>, 32);
-    else
-        return few ? go(cache4_append_kernel<D, E2M1, 8>, 8) : go(cache4_append_kernel<D, E2M1, 32>, 32);
+    // Blocks of few rows, with more threads to a row, until there are two of the others for every SM (2849 tokens, 5 heads of
+    // 64: 450 of the others, 3.6 us, of these 4.4; one token of 64 sequences, 8 heads of 128: 3.1 and 3.0).
+    constexpr int FEW = 2 * D;
+    if ((a.n_rows + 31LL) / 32 * a.Hkv < 2LL * sms) {
+        if constexpr (READ) return go(cache4_read_kernel<D, E2M1, 8, FEW>, 8, FEW);
+        else return go(cache4_append_kernel<D, E2M1, 8, FEW>, 8, FEW);
+    }
+    if constexpr (READ) return go(cache4_read_kernel<D, E2M1, 32, kMany>, 32, kMany);
+    else return go(cache4_append_kernel<D, E2M1, 32, kMany>, 32, kMany);
 }
 
 template <bool READ>

@@ -107,7 +107,7 @@ def test_short_requests_in_a_wide_table(T, G, most, kind):
 
 
 @pytest.mark.parametrize("kind", KINDS)
-@pytest.mark.parametrize("G,most,width", [(4, 1, 24), (4, 1, 25), (12, 1, 24), (12, 1, 25), (8, 4, 12), (8, 4, 13), (8, 8, 6),
+@pytest.mark.parametrize("G,most,width", [(4, 1, 48), (4, 1, 49), (8, 1, 48), (8, 1, 49), (4, 1, 24), (4, 1, 25), (12, 1, 24), (12, 1, 25), (8, 4, 12), (8, 4, 13), (8, 8, 6),
                                           (8, 8, 7), (32, 4, 3), (32, 4, 4)])
 def test_widths_that_choose_one_launch_or_two(G, most, width, kind):
     T = PAGE * width
@@ -125,6 +125,34 @@ def test_many_requests(d, kind):
         T = [1 + 37 * b % 500 for b in range(B)]
         cache, table = filled(T, 2, d, kind, 10, width=128)
         run(cache, table, T, [1] * B, 4, "none", 11)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("G,most", [(1, 3), (2, 2), (3, 1), (5, 1), (1, 4), (1, 5), (4, 2), (9, 1)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_numbers_of_query_rows_on_both_sides_of_a_change(d, G, most, kind):
+    # up to 4, 8 and 16 rows a K/V head's products are laid out in another way
+    T = [most, 70, 333, 1500, 5000]
+    cache, table = filled(T, 2, d, kind, 50)
+    run(cache, table, T, [most] * 4 + [1], G, "elementwise", 51, most=most)
+
+
+@pytest.mark.parametrize("G,most", [(4, 1), (8, 1), (8, 2), (16, 4), (16, 8)])
+def test_more_heads_than_teams(G, most):
+    # the merge goes by the places where shares begin; heads of no, one and several pages
+    B, H = 330, 8
+    T = [(53 * b) % 300 + most if b % 7 else 0 for b in range(B)]
+    cache, table = filled(T, H, 64, "e2m1", 52)
+    run(cache, table, T, [most if t else 0 for t in T], G, "none", 53, most=most, requests=range(0, B, 5))
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("T", [[30000], [64 * 152 * 16 + 1], [40000, 17, 25000], [0, 90000, 0, 3000]])
+def test_blocks_of_threads_within_one_head_and_across_two(T, kind):
+    # a block whose share is all of one head leaves one part, others one for each team
+    cache, table = filled(T, 1, 64, kind, 54)
+    new = [min(2, t) for t in T]
+    run(cache, table, T, new, 4, "none", 55, most=2)
 
 
 @pytest.mark.parametrize("kind", KINDS)

@@ -390,7 +390,8 @@ __global__ void __launch_bounds__(kMergeThreads) cache_merge_kernel(const __grid
     const bool by_place = heads >= takers;
     const int units = all.by_head ? 0 : (by_place ? takers - 1 : (int)heads);
     int most = deal.each > 0 ? all.longest / deal.each + 2 : 1;   // parts of a head
-    if (A::kJoins) most = min(most, (most >> a.lg_teams) + (1 << a.lg_teams));
+    if (A::kJoins && all.N > 0)   // CTAs that a head lies across, and the teams of the two at its ends
+        most = min(most, (int)((long long)all.longest * all.ctas / all.N) + (1 << a.lg_teams));
     int lg = 0;
     while ((8 << lg) <= kMergeThreads && ((units * items) << (lg + 1)) <= threads && (4 << lg) < most) ++lg;
     const int total = (units * items) << lg;   // (below 1280 x 4096, or the grid's threads)

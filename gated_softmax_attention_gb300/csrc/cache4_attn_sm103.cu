@@ -57,6 +57,7 @@ struct PagedSeq;
 struct Cache4Args {
     using Seq = PagedSeq;
     static constexpr bool kJoins = true;   // a CTA whose share is one head's leaves one part
+    static constexpr int kSwitch = 1;
     __device__ __forceinline__ long long token(int b, int i) const { return (long long)cu[b] + i; }
     __device__ __forceinline__ long long tokens() const { return N; }
     const __nv_bfloat16* Q;          // [N, Hq, D]
@@ -97,7 +98,7 @@ struct PagedSeq {
         T = n > 0 ? len + n : 0;   // (a request without new tokens has no rows to compute)
         tiles = (T + kPage - 1) / kPage;
     }
-    __device__ __forceinline__ int span() const { return span_of(tiles); }
+    __device__ __forceinline__ int span() const { return span_of<Cache4Args>(tiles); }
 };
 
 // A word of eight codes -> four fp16 pairs: pair p from bits 4 p .. and 16 + 4 p .. (int4:
@@ -582,7 +583,7 @@ __global__ void __launch_bounds__(Config<D, NT>::THREADS, 1) cache4_attn_kernel(
             if (c.tiles == 0) {
                 c.left = 0;
             } else {
-                const int span = span_of(c.tiles);
+                const int span = span_of<Cache4Args>(c.tiles);
                 c.kvh = rem / span;
                 c.j = rem % span;
                 if (c.j >= c.tiles) c.next_head(a);
@@ -911,7 +912,7 @@ __global__ void __launch_bounds__(Config<D, NT>::THREADS, 1) cache4_attn_kernel(
             }
 
             // ---- the segment's rows: sums over the lanes, and the codes' units out of the outputs
-            const bool whole = at.j == 0 && j1 == at.tiles && !joined, final = at.left <= span_of(at.tiles) - at.j;
+            const bool whole = at.j == 0 && j1 == at.tiles && !joined, final = at.left <= span_of<Cache4Args>(at.tiles) - at.j;
             const float unit = exp2f(a.v_exp + (E2M1 ? 0.f : 24.f));
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
@@ -1080,7 +1081,7 @@ int plan_cache4(const gsdpa_cache4* c, int B, int max_pages, int n_rows, int max
     // (places are counted in 32 bits, and so are a request's tokens)
     if (max_pages > 0x7fffffff / kPage - 1) return GSDPA_ERR_UNSUPPORTED;
     const long long heads = (long long)B * c->H_kv;
-    if (heads > 0x7fffffffLL - 2 * kMaxCtas || heads * (max_pages + kSwitch) > 0x7fffffffLL) return GSDPA_ERR_UNSUPPORTED;
+    if (heads > 0x7fffffffLL - 2 * kMaxCtas || heads * (max_pages + Cache4Args::kSwitch) > 0x7fffffffLL) return GSDPA_ERR_UNSUPPORTED;
     if (n_rows > 0x7fffffff / 8) return GSDPA_ERR_UNSUPPORTED;
     if (B == 0 || n_rows == 0) return GSDPA_OK;   // an empty problem: nothing to plan
     Cache4Plan& o = *out;

@@ -91,6 +91,7 @@ struct SeqTiles;
 struct Cache8Args {
     using Seq = SeqTiles;
     static constexpr bool kJoins = false;   // (a head's parts are its teams')
+    static constexpr int kSwitch = 4;
     __device__ __forceinline__ long long token(int b, int i) const { return (long long)b * Lq + i; }
     __device__ __forceinline__ long long tokens() const { return (long long)B * Lq; }
     const __nv_bfloat16* Q;          // [B, Lq, Hq, D]
@@ -171,7 +172,7 @@ struct SeqTiles {
         tiles = (T + kCacheBlock - 1) / kCacheBlock;
     }
     __device__ __forceinline__ bool open(int j) const { return (j + 1) * kCacheBlock > T; }
-    __device__ __forceinline__ int span() const { return span_of(tiles); }
+    __device__ __forceinline__ int span() const { return span_of<Cache8Args>(tiles); }
 };
 
 // A value scale as frac 2^ev, frac in [1, 2) (0, NaN and infinity stay what they are).
@@ -377,7 +378,7 @@ cache8_attn_kernel(const __grid_constant__ Cache8Args a) {
             if (c.tiles == 0) {
                 c.left = 0;
             } else {
-                const int span = span_of(c.tiles);
+                const int span = span_of<Cache8Args>(c.tiles);
                 c.kvh = rem / span;
                 c.j = rem % span;
                 if (c.j >= c.tiles) c.next_head(a);
@@ -758,7 +759,7 @@ cache8_attn_kernel(const __grid_constant__ Cache8Args a) {
             // A head of the team's alone is finished; else its part is left in global
             // memory for the merge kernel, or, of the CTA's own head, in shared memory:
             // the first warp's rows in the slot, the second's in the ring, which is empty.
-            const bool whole = at.j == 0 && j1 == at.tiles, final = at.left <= span_of(at.tiles) - at.j;
+            const bool whole = at.j == 0 && j1 == at.tiles, final = at.left <= span_of<Cache8Args>(at.tiles) - at.j;
             const bool apart = C::KS == 2 && by_head && !whole;
             float* to = whole || by_head
                             ? slot : part_of<D>(a, deal, me * teams + team, share_end - at.left - at.j);
@@ -880,7 +881,7 @@ int plan_cache8(const gsdpa_cache8* c, int Lq, int d_model, int Hq, int gate_mod
     const long long rows = (long long)(Hq / c->H_kv) * Lq;
     if (rows > kMaxRows) return GSDPA_ERR_UNSUPPORTED;
     // (places are counted in 32 bits)
-    if ((long long)c->B * c->H_kv * (c->capacity / kCacheBlock + kSwitch) > 0x7fffffffLL) return GSDPA_ERR_UNSUPPORTED;
+    if ((long long)c->B * c->H_kv * (c->capacity / kCacheBlock + Cache8Args::kSwitch) > 0x7fffffffLL) return GSDPA_ERR_UNSUPPORTED;
     if ((long long)c->B * Lq > 0x7fffffffLL / 8 || (long long)c->B * c->H_kv > 0x7fffffffLL - 2 * kMaxCtas)
         return GSDPA_ERR_UNSUPPORTED;
     if (c->B == 0 || Lq == 0) return GSDPA_OK;   // an empty problem: nothing to plan

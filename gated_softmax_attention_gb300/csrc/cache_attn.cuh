@@ -8,6 +8,7 @@
 //   token(b, i)    the row of Q, X and O that holds new token i of sequence b
 //   tokens()       all rows
 //   kJoins         a CTA whose share is all of one head leaves one part
+//   kSwitch        most places after a head without a tile
 #pragma once
 #include "ops_internal.h"
 
@@ -20,7 +21,6 @@ constexpr int kMaxRows = 128;        // query rows (heads of a group x new token
 constexpr int kMaxCtas = 160;        // most CTAs (plan_sms)
 constexpr int kMergeThreads = 512;
 constexpr int kBatch = 6;            // parts that a thread of a merge has under way
-constexpr int kSwitch = 4;           // most places after a head without a tile
 constexpr int kScan = 128;           // places in the sequence of all tiles that are looked up
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -50,10 +50,14 @@ __device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f +
 // queries and has, at a sequence's end, an open block of twice the bytes, which
 // even shares of the tiles alone do not show: of 1216 teams with 11 tiles each of
 // 24 sequences of up to 32767 tokens, the 48 that went on ended 5 us after the
-// others. (Measured with 2, 4, 6 and 8 places: that 52.2, 50.4, 50.9, 51.5 us, up
+// others. (Measured, 8 bits, with 2, 4, 6 and 8 places: that 52.2, 50.4, 50.9, 51.5 us, up
 // to 5000 tokens 19.3, 17.7, 17.5, 17.9; 64 x 200 tokens, heads of 4 tiles, 18.4,
-// 21.0, 20.3, 20.1.)
-__device__ __forceinline__ int span_of(int tiles) { return tiles + min(kSwitch, tiles / 2); }
+// 21.0, 20.3, 20.1. 4 bits, where a team is one warp that ends a head without a barrier and
+// takes longer for a tile, with 0, 1, 2, 4 and 6: 200 sequences of up to 1500 tokens 69.6, 66.5, 69.6,
+// 72.1, 71.3 us; 24 of up to 32767 47.8, 46.5, 46.8, 46.5, 47.2; 64 x 8192 with the gate 132.1, 134, 134.5,
+// 134, 138; 7 of up to 4099, 5 rows, 16.7, 16.5, 16.4, 16.1, 16.1.)
+template <class A>
+__device__ __forceinline__ int span_of(int tiles) { return tiles + min(A::kSwitch, tiles / 2); }
 
 // A place in the sequence of all tiles. (Where places are left a sequence with
 // tiles follows; lengths that change during the call, which they must not, end
@@ -63,7 +67,7 @@ struct Cursor {
     int left;   // places of the share from here on
     template <class A>
     __device__ __forceinline__ void next_head(const A& a) {
-        left -= span_of(tiles) - j;
+        left -= span_of<A>(tiles) - j;
         j = 0;
         if (left <= 0) return;
         if (++kvh == a.Hkv) {
@@ -394,7 +398,7 @@ __global__ void __launch_bounds__(kMergeThreads) cache_merge_kernel(const __grid
         most = min(most, (int)((long long)all.longest * all.ctas / all.N) + (1 << a.lg_teams));
     int lg = 0;
     while ((8 << lg) <= kMergeThreads && ((units * items) << (lg + 1)) <= threads && (4 << lg) < most) ++lg;
-    const int total = (units * items) << lg;   // (below 1280 x 4096, or the grid's threads)
+    const int total = (units * items) << lg;   // (below 2560 x 4096, or the grid's threads)
     bool waited = false;
     for (int base = blockIdx.x * kMergeThreads; base < total; base += threads) {
         const int idx = base + tid, unit = idx / (items << lg);
@@ -406,7 +410,7 @@ __global__ void __launch_bounds__(kMergeThreads) cache_merge_kernel(const __grid
             if (from < all.N) {
                 all.find(a, from, b, u0);
                 const int tiles = typename A::Seq(a, b).tiles;
-                span = span_of(tiles);
+                span = span_of<A>(tiles);
                 const int at = u0 % max(span, 1);
                 kvh = u0 / max(span, 1);
                 u0 = from - at;
@@ -419,7 +423,7 @@ __global__ void __launch_bounds__(kMergeThreads) cache_merge_kernel(const __grid
             b = unit / a.Hkv;
             kvh = unit % a.Hkv;
             const int tiles = typename A::Seq(a, b).tiles;
-            span = span_of(tiles);
+            span = span_of<A>(tiles);
             u0 = all.before(a, b) + kvh * span;
             if (tiles > 0) {
                 n0 = deal.taker(u0);

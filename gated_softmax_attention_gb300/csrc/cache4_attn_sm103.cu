@@ -48,9 +48,9 @@ namespace {
 constexpr int kMaxStages = 16;       // ring stages per team
 constexpr int kBars = 96;            // ring stages of all teams
 constexpr uint32_t kSmemMax = 232448 - 4608;   // dynamic: what a CTA may have, less barriers, parts and a few words
-// A head is one CTA's where all have at most this many tiles for each team of it (by
-// the table's width, then by the lengths) and there are CTAs for all.
-constexpr int kWholeTiles = 3, kFewTiles = 1;
+// Most tiles of a head for each team of a CTA that takes it alone.
+constexpr int kWholeTiles = 4;
+constexpr int kRegs = 232, kCopyRegs = 40;       // of a thread where a warp copies for the others: see Config
 constexpr float kUp = 13.0f, kMove = 2.0f;     // where m stands, and how far a tile may exceed it: see above
 
 struct PagedSeq;
@@ -60,6 +60,14 @@ struct Cache4Args {
     static constexpr int kSwitch = 1;
     __device__ __forceinline__ long long token(int b, int i) const { return (long long)cu[b] + i; }
     __device__ __forceinline__ long long tokens() const { return N; }
+    // A CTA to each head, no merge, but the others idle: where the longest head gives its teams at most
+    // 2 tiles more than an even share. (8 heads of 1000, 2000, 3000 tokens 13.2, 16.7, 20.2 us so,
+    // cut 15.7, 16.5, 14.6; 32 heads 13.8, 17.9, 22.0 and 18.6, 19.4, 17.4; 128 heads of 2000, 4000, 6000
+    // 18.3, 26.3, 36.4 and 20.5, 29.8, 36.6.)
+    __device__ __forceinline__ bool by_head(int longest, int N) const {
+        const int each = (longest + (1 << lg_teams) - 1) >> lg_teams;
+        return each <= kWholeTiles && each * ctas - (N >> lg_teams) <= 2 * ctas;
+    }
     const __nv_bfloat16* Q;          // [N, Hq, D]
     __nv_bfloat16* O;
     const int *table, *lens, *cu, *n_new;
@@ -76,8 +84,7 @@ struct Cache4Args {
     int gate_splits, gate_cols, gate_mode;
     float* part;                     // [CTAs][teams][2][rows][D + 4]: a team's first and last head, where cut
     int ctas;                        // of the attention kernel
-    int whole_tiles;                 // most tiles of a head for one CTA to take it alone
-    int whole;                       // that many at most by the table's width: a head is one CTA's
+    int whole;                       // a CTA to each head, known from the table's width
     int wait_first;                  // no gate kernel: everything before this kernel is waited for at once
     WaitCtl ctl;
 };
@@ -460,7 +467,6 @@ struct Config {
     static constexpr int WARPS = ALONE ? 16 : 8;        // that compute
     static constexpr int CONSUMERS = WARPS * 32;
     static constexpr int THREADS = CONSUMERS + (ALONE ? 0 : 128);
-    static constexpr int REGS = 232, COPY_REGS = 40;
     static constexpr int STRIDE = D + 4;                // floats of a row's part: D columns, then m, l, M
     static constexpr uint32_t STAGE = half_bytes(D);    // bytes: a page's keys or values, with their scales
 };
@@ -610,7 +616,7 @@ __global__ void __launch_bounds__(Config<D, NT>::THREADS, 1) cache4_attn_kernel(
     const int head_place = s_head.x, head_tiles = s_head.y;   // of its first tile; its tiles
     if constexpr (!C::ALONE) {
         if (warp >= C::WARPS) {
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::COPY_REGS));
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCopyRegs));
             if (warp > C::WARPS) return;
             // ---- copies: lane k serves team k, in the order the team consumes them
             Cursor none;
@@ -660,7 +666,7 @@ __global__ void __launch_bounds__(Config<D, NT>::THREADS, 1) cache4_attn_kernel(
                 if (armed & (1u << k)) mbar_wait(&full[k], (armed_phase >> k) & 1u, &never, c2);
             return;
         }
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
     }
     bool ok = true;
     {
@@ -1214,9 +1220,11 @@ int gated_sdpa_cache4(const void* X, const void* Q, const gsdpa_cache4* cache, c
     long long grid = sms;   // (no fewer than the heads, where those fit)
     if (grid > most) grid = most;
     a.ctas = (int)grid;
-    const bool whole = max_pages <= kWholeTiles << a.lg_teams && (long long)B * a.Hkv <= grid;
+    // By the table's width, which saves the lengths' lookup and the merge kernel: the same with 2 tiles (8 heads of 1000, 2000,
+    // 3000 tokens 10.5, 14.5, 18.2 us, 32 heads 11.8, 15.9, 19.8, 128 heads of 2000, 4000 15.7, 23.7).
+    const long long heads = (long long)B * a.Hkv, each = (max_pages + sh.teams - 1) / sh.teams;
+    const bool whole = heads <= grid && each <= kWholeTiles && each * (sms - heads) <= 2 * sms;
     a.whole = whole;
-    a.whole_tiles = (whole ? kWholeTiles : kFewTiles) << a.lg_teams;
     const bool e2m1 = cache->kind == GSDPA_CACHE_E2M1;
     if (cache->d_k == 128)
         e = e2m1 ? launch<128, true>(a, sh, (unsigned)grid, s) : launch<128, false>(a, sh, (unsigned)grid, s);

@@ -94,6 +94,7 @@ struct Cache8Args {
     static constexpr int kSwitch = 4;
     __device__ __forceinline__ long long token(int b, int i) const { return (long long)b * Lq + i; }
     __device__ __forceinline__ long long tokens() const { return (long long)B * Lq; }
+    __device__ __forceinline__ bool by_head(int longest, int) const { return longest <= whole_tiles; }
     const __nv_bfloat16* Q;          // [B, Lq, Hq, D]
     __nv_bfloat16* O;
     const int *lens, *n_new;

@@ -5,6 +5,7 @@
 //
 // A kernel's arguments A have the members used here and
 //   A::Seq(a, b)   sequence b: n (new tokens), T (tokens in all, 0 without new ones), tiles, span()
+//   by_head(longest, N)   whether heads of at most so many tiles, N places in all, are better one CTA's each
 //   token(b, i)    the row of Q, X and O that holds new token i of sequence b
 //   tokens()       all rows
 //   kJoins         a CTA whose share is all of one head leaves one part
@@ -339,7 +340,7 @@ struct Layout {
         ctas = max(1, min(a.ctas, N >> a.lg_teams));   // every team has a tile (or there is one CTA)
         // Short sequences, a CTA for each head: no head is cut between CTAs, whose
         // merge would take longer than the tiles.
-        by_head = longest <= a.whole_tiles && a.B * (long long)a.Hkv <= a.ctas;
+        by_head = a.B * (long long)a.Hkv <= a.ctas && a.by_head(longest, N);
     }
     // place x < N is place `rem` of sequence b
     template <class A>

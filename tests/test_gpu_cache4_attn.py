@@ -118,6 +118,18 @@ def test_widths_that_choose_one_launch_or_two(G, most, width, kind):
 
 
 @pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("width", [47, 64, 65, 700])
+@pytest.mark.parametrize("B", [37, 50, 51, 75, 76, 152, 153])
+def test_numbers_of_heads_that_choose_one_block_for_each(B, width, kind):
+    # heads of up to four pages to a team are one block of threads' where there are enough of them, by the table's width or
+    # by the lengths: all alike, and as different as can be
+    most = PAGE * min(width, 64)
+    for T in ([most] * B, [most if b % 3 else 1 + 41 * b % most for b in range(B)], [most if b == B // 2 else 70 for b in range(B)]):
+        cache, table = filled(T, 1, 64, kind, 60, width=width)
+        run(cache, table, T, [1] * B, 4, "elementwise" if B % 2 else "none", 61, requests=sorted({0, 1, B // 2, B - 1, *range(3, B, 11)}))
+
+
+@pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("d", [64, 128])
 def test_many_requests(d, kind):
     # more than the schedule looks up one by one, and as many heads as there are blocks of threads and one more

@@ -20,8 +20,9 @@ namespace {
 constexpr int kMaxRequests = 8192;
 constexpr int kPlanThreads = 1024, kFillThreads = 256;
 constexpr int kEach = kMaxRequests / kPlanThreads;
-// Rows that the planning block fills in itself.
-constexpr int kFewRows = 2048;
+// Rows to a thread that the planning block fills in itself (64 requests, 256 threads, 64, 1024, 2048 rows: 4.2, 6.5,
+// 8.8 us so, 5.9, 5.6, 5.6 with the second kernel, which also costs the host 2.5 us).
+constexpr int kFewRows = 2;
 
 struct PagesArgs {
     const int *lens, *keep, *n_new;
@@ -244,7 +245,7 @@ extern "C" int gsdpa_pages_step(const int* lens, const int* keep, const int* n_n
     const PagesArgs a{lens, keep, n_new, table, free_pages, n_free, n_free_out, cu, granted, slots, positions,
                       B, max_pages, n_pages, n_rows, rt.err};
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const int fill = n_rows <= kFewRows;
+    const int fill = n_rows <= kFewRows * (B <= 256 ? 256 : kPlanThreads);
     const size_t smem = 3 * sizeof(int) * ((size_t)B + 1);
     cudaError_t e;
     if (B <= 256) {

@@ -86,6 +86,14 @@ def test_prompts_of_many_rows():
         check(lens, new, 200, 400, 5, more=3)
 
 
+@pytest.mark.parametrize("rows", [511, 512, 513, 2047, 2048, 2049])
+@pytest.mark.parametrize("B", [1, 256, 257])
+def test_rows_on_both_sides_of_the_second_kernel(B, rows):
+    # two rows to a thread of the planning block, which has 256 or 1024
+    new = [rows - (B - 1)] + [1] * (B - 1)
+    check([17 * k % 200 for k in range(B)], new, 40, 400 + B, 6, more=0)
+
+
 def test_in_place_and_written_again():
     # n_free in place, as a captured step has it; the same step on the same contents gives the same
     lens, new, width = [60, 0, 130], [10, 70, 1], 4

@@ -2,11 +2,12 @@
 // keys and values to codes and scales at their slots) and the reading back.
 //
 // Per 16 columns x of a token: scale s = e4m3(max |x| 2^-exp / top), codes
-// round(x 2^-exp / s). x has 8 significant bits and s 4: their quotient is either on a
-// border between two codes, and then a float32 number, or 2^-13 of itself away from it.
-// So one step of correction of the product with the rounded reciprocal gives the code of
-// the exact quotient, ties among it (without the step one code in 500 was not: 1/13 is off by
-// up to half a place, and so are ties).
+// round(x 2^-exp / s). x has 8 significant bits, s 4 and a border b between two codes 4, so
+// that x and b s are whole numbers below 2^8 times powers of two: the quotient is on the border or
+// 2^-8 of it away. The product with the rounded reciprocal is off by 2^-21 of itself at most; rounded
+// to a multiple of 2^-15, as one fused multiply-add with 384 does, it is on a border where the
+// quotient is and on its side elsewhere, so ties go as they should (plain products gave one code in 500
+// another).
 //
 // Bound by HBM for prompts (4 d bytes in, 1.125 d out per token and head), by latency
 // for a decoding step. A block has some rows of one head: it reads them whole, leaves codes
@@ -59,35 +60,25 @@ __device__ __forceinline__ uint32_t to_e2m1x8(const float (&y)[8]) {
         : "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]), "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7]));
     return r;
 }
-// ... -> rounded to whole numbers, plus 8: added to 1.5 2^23 + 8 a number is rounded to
-// even and stands in the low bits. (The largest quotient is at most 7 / (1 - 1 / 17) < 7.5, unless the scale
-// is cut off at 448 or one of the least: `over`.)
-__device__ __forceinline__ uint32_t to_int4x8(float (&y)[8], bool over) {
-    if (over) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) y[k] = fminf(fmaxf(y[k], -7.f), 7.f);
-    }
-    uint32_t r = 0;
-#pragma unroll
-    for (int k = 7; k >= 0; --k) r = r * 16 + __float_as_uint(y[k] + 12582920.f);
-    return r - 0x4b400000u * 0x11111111u;
-}
-
 using Pair = unsigned long long;   // two float32 numbers
 __device__ __forceinline__ Pair pair_of(float lo, float hi) {
     Pair r;
     asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
     return r;
 }
-__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
-    Pair r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
 __device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
     Pair r;
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
     return r;
+}
+
+__device__ __forceinline__ Pair add2(Pair a, Pair b) {
+    Pair r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ void unpair(Pair x, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x));
 }
 
 // The 16 columns of a group -> their codes, 4 bits each, and the scale.
@@ -98,30 +89,44 @@ __device__ __forceinline__ void quantise(const uint4 (&x)[2], float unit, uint32
 #pragma unroll
     for (int k = 0; k < 8; ++k) top = max_bf16x2(top, w[k]);
     top &= 0x7fff7fffu;
-    const bool number = (top & 0x7fff) < 0x7f80 && (top >> 16) < 0x7f80;   // (no NaN, no infinity)
-    const float amax = fmaxf(__uint_as_float(top << 16), __uint_as_float(top & 0xffff0000u));
+    const uint32_t most = max(top & 0xffffu, top >> 16);   // (a NaN is above all)
+    const bool number = most < 0x7f80u;                    // (no NaN, no infinity)
+    const float amax = __uint_as_float(most << 16);
     const float down = __uint_as_float(0x7f000000u - __float_as_uint(unit));   // 1 / unit
     const __nv_fp8_storage_t byte = __nv_cvt_float_to_fp8(amax * down * (1.f / (E2M1 ? 6.f : 7.f)), __NV_SATFINITE, __NV_E4M3);
     scale = number ? byte : 0x7fu;
     codes[0] = codes[1] = E2M1 ? 0u : 0x88888888u;
     if (!number || byte == 0) return;
     const float s = __half2float(__half(__nv_cvt_fp8_to_halfraw(byte, __NV_E4M3)));
-    const float step = s * unit, inv = __fdividef(1.f, s) * down;   // (the powers of two: exact)
-    const Pair inv2 = pair_of(inv, inv), step2 = pair_of(-step, -step);
-    Pair y[8];
-    const bool far = amax * inv > 1024.f;   // (a scale cut off at 448 under numbers far above: the step may overflow)
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        const Pair v = pair_of(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xffff0000u));
-        y[k] = mul2(v, inv2);
-        if (!far) y[k] = fma2(fma2(y[k], step2, v), inv2, y[k]);
-    }
+    const float inv = __fdividef(1.f, s) * down;   // (the power of two: exact)
+    const Pair inv2 = pair_of(inv, inv), up = pair_of(384.f, 384.f);
+    // The largest quotient is at most 7 / (1 - 1 / 17) < 7.5, unless the scale is cut off at 448 or one of the least.
+    const bool over = !E2M1 && amax * inv > 7.45f;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         float q[8];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) asm("mov.b64 {%0, %1}, %2;" : "=f"(q[2 * k]), "=f"(q[2 * k + 1]) : "l"(y[4 * h + k]));
-        codes[h] = E2M1 ? to_e2m1x8(q) : to_int4x8(q, amax * inv > 7.45f);
+        for (int k = 0; k < 4; ++k) {
+            const uint32_t v = w[4 * h + k];
+            Pair y = fma2(pair_of(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u)), inv2, up);
+            if (over) {
+                float a, b;
+                unpair(y, a, b);
+                y = pair_of(fminf(fmaxf(a, 377.f), 391.f), fminf(fmaxf(b, 377.f), 391.f));
+            }
+            // e2m1: the 384 off again. int4: added to 1.5 2^23 + 8 (less the 384) a number is rounded to even and
+            // stands in the low bits.
+            y = add2(y, E2M1 ? pair_of(-384.f, -384.f) : pair_of(12582536.f, 12582536.f));
+            unpair(y, q[2 * k], q[2 * k + 1]);
+        }
+        if constexpr (E2M1) {
+            codes[h] = to_e2m1x8(q);
+        } else {
+            uint32_t r = 0;
+#pragma unroll
+            for (int k = 7; k >= 0; --k) r = r * 16 + __float_as_uint(q[k]);
+            codes[h] = r - 0x4b400000u * 0x11111111u;
+        }
     }
 }
 

@@ -45,8 +45,10 @@
 // brought it there: up to 8 rows every warp is a team of its own and copies for itself, three half
 // pages ahead (221 KB of an SM's shared memory under way; a copying warp and eight teams of two warps 133, 140 int4,
 // 95 in heads of 64; two stages are as fast); up to 4 rows both halves of the narrow side are in use (HALF: 127 without).
-// Beyond 8 rows the codes are converted again for every 16 rows: 16 x 8000 tokens, 16, 32, 64 and 128
-// rows 45, 48, 58 and 58 us of 22 for the bytes.
+// Beyond 8 rows the codes are converted again for every 16: 16 x 8000 tokens, 22 us of bytes, 4, 8, 16, 32, 64 and
+// 128 rows 45, 48, 58, 96, 173 and 324 us. (A page converted once for its team, in shared memory, with rows on the side
+// of 16 and scales in the operands: 71 us for 16 rows, 120, 198 and 346; eight warps that meet at two barriers a page
+// leave the SM idle more than the second conversion costs.)
 #include "cache4_internal.h"
 #include "cache_attn.cuh"
 #include "landing.cuh"

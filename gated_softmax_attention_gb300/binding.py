@@ -987,9 +987,10 @@ def pages_step(lens, n_new, table, free_pages, n_free, n_rows, *, keep=None, out
     if out is None:
         if not table.is_cuda:
             raise ValueError(f"table must be a CUDA tensor, not on {table.device}")
-        # (allocations of their own: slices of one take the host longer)
-        make = table.new_empty
-        out = PagesStep(make(B + 1), make(B), torch.empty(n_rows, dtype=torch.int64, device=dev), make(n_rows),
+        # (allocations of their own, made so: slices of one take the host longer, and so does new_empty)
+        make = torch.empty
+        out = PagesStep(make(B + 1, dtype=i32, device=dev), make(B, dtype=i32, device=dev),
+                        make(n_rows, dtype=torch.int64, device=dev), make(n_rows, dtype=i32, device=dev),
                         torch.empty_like(n_free))
     st = (_lib or load()).gsdpa_pages_step(
         _vector(lens, "lens", B, i32, dev), _vector(keep, "keep", B, i32, dev), _vector(n_new, "n_new", B, i32, dev),

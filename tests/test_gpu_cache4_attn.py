@@ -139,6 +139,16 @@ def test_many_requests(d, kind):
         run(cache, table, T, [1] * B, 4, "none", 11)
 
 
+@pytest.mark.parametrize("G", [2, 20])
+@pytest.mark.parametrize("B", [1000, 8200])
+def test_thousands_of_requests(B, G):
+    # several to a place of the schedule's lookup, most of them of a page or none
+    r = random.Random(B)
+    T = [r.choice([0, 1, 30, 64, 65, r.randint(1, 200), 900 if b % 97 == 5 else 2]) for b in range(B)]
+    cache, table = filled(T, 1, 64, "e2m1", 70, width=15)
+    run(cache, table, T, [min(t, 1) for t in T], G, "none", 71, requests=sorted({0, B // 2, B - 1, *r.sample(range(B), 40), *range(5, B, 970)}))
+
+
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("G,most", [(1, 3), (2, 2), (3, 1), (5, 1), (1, 4), (1, 5), (4, 2), (9, 1)])
 @pytest.mark.parametrize("d", [64, 128])

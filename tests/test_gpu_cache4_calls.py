@@ -171,6 +171,34 @@ def test_a_captured_step(kind):
     assert t.lens.tolist() == s.lens.tolist() and t.n_free.tolist() == s.n_free.tolist() and torch.equal(t.table, s.table)
 
 
+@pytest.mark.parametrize("Hq", [8, 24, 80])
+def test_a_captured_call_for_other_lengths(Hq):
+    # captured once for a wide table and replayed for lengths at which heads are one block's each, are cut, or are not there
+    B, H, d, width = 6, 2, 64, 300
+    s = Server(B, width, B * width, H, d, "int4")
+    s.table.copy_(s.free.view(B, -1))
+    pos = torch.arange(B * width * PAGE, device="cuda")
+    gb.cache4_append(s.cache, randn(1, len(pos), H, d), randn(2, len(pos), H, d), pos)
+    Q, lens, cu = randn(3, B, Hq, d), ints([0] * B), ints(list(range(B + 1)))
+    call = lambda: gb.gated_sdpa_cache4(None, Q, s.cache, s.table, lens, cu, gate="none")  # noqa: E731
+    call()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        O = call()
+    for T in ([1] * B, [64 * 15] * B, [1500, 40, 1, 700, 1500, 2], [width * PAGE] * B, [1, 1, 19000, 1, 1, 1], [5] * B,
+              [4000, 9000, 0, 63, 64, 65], [64 * 31] * B):
+        lens.copy_(ints([t - 1 for t in T]))
+        O.fill_(7.0)
+        graph.replay()
+        assert torch.equal(O, call())
+        if 0 not in T:
+            check_attention(O, None, Q, s.cache, s.table, [t - 1 for t in T], [1] * B, list(range(B + 1)), None, "none")
+            continue
+        empty = T.index(0)        # (a length that is none, -1: a zero row, and the error)
+        assert not bool(O[empty].any())
+        assert gb.check_device_error() == gb.ERR_CACHE_RANGE
+
+
 def test_two_captured_graphs_at_once():
     graphs = []
     for k in range(2):

@@ -17,7 +17,7 @@
 // which it turns four tokens' words around; where the block has all four tokens it
 // writes them at once, else their bytes one by one, so that tokens next to each other can be
 // written by different blocks and calls. The reading goes the same way back.
-// Measured: prompts of 4 x 8190 tokens, 8 heads of 128 (172 MB), e2m1 32 us, 5.4 TB/s, int4 37.6 us, 4.6 TB/s, the
+// Measured: prompts of 4 x 8190 tokens, 8 heads of 128 (172 MB), e2m1 33.5 us, 5.1 TB/s, int4 37.6 us, 4.6 TB/s, the
 // integer pipe 70 % busy with unpacking, codes and exchanges; heads of 64 20.5 us int4; 64 single tokens 3.0 us;
 // reading 98k tokens, 2 heads of 128 (110 MB) 23 us, 4.8 TB/s.
 #include "cache4_internal.h"
@@ -28,7 +28,8 @@
 namespace gsdpa {
 namespace {
 
-// Threads of a block of 32 rows. (Prompts of 4 x 8190 tokens, e2m1, with 64, 128, 256 threads 36.0, 31.9, 33.5 us, int4
+// Threads of a block of 32 rows. (Prompts of 4 x 8190 tokens, e2m1, with 64, 128, 256 threads 36.0, 31.9, 33.5 us before a
+// zero had its sign, int4
 // 42.7, 37.6, 38.8; reading 98k tokens 23.7, 22.9, 25.1.)
 constexpr int kMany = 128;
 
@@ -123,7 +124,9 @@ __device__ __forceinline__ void quantise(const uint4 (&x)[2], float unit, uint32
             unpair(y, q[2 * k], q[2 * k + 1]);
         }
         if constexpr (E2M1) {
-            codes[h] = to_e2m1x8(q);
+            // (a number that is rounded to 384 has lost its sign, which the code of zero has too: bit 7 of every other byte)
+            const uint32_t a = __byte_perm(w[4 * h], w[4 * h + 1], 0x7351), b = __byte_perm(w[4 * h + 2], w[4 * h + 3], 0x7351);
+            codes[h] = to_e2m1x8(q) | (__byte_perm(a, b, 0x5410) >> 4 & 0x08080808u) | (__byte_perm(a, b, 0x7632) & 0x80808080u);
         } else {
             uint32_t r = 0;
 #pragma unroll

@@ -586,7 +586,7 @@ GSDPA_API int gsdpa_pages_step(const int* lens, const int* keep, const int* n_ne
  * Every 16 columns of a token, with amax their largest |x| and top = 7 (int4) or 6
  * (e2m1): scale = e4m3 nearest to amax 2^-exp (1 / top), reciprocal and product rounded to
  * float32, ties to even, at most 448; code = x / (scale 2^exp) to nearest (the exact
- * quotient), ties to even, at most top. Scale 0: codes 0. A
+ * quotient), ties to even, at most top (e2m1: zero with the sign of x). Scale 0: codes 0. A
  * group with a NaN or an infinity: scale NaN, codes 0 (every row that sees its token
  * becomes NaN). A token is rounded by itself: the contents do not depend on how tokens
  * were split over calls, and other tokens' bytes are left as they were. A slot past the

@@ -7,7 +7,7 @@ import torch
 
 from gated_softmax_attention_gb300 import binding as gb
 from gated_softmax_attention_gb300 import build as gbuild
-from cache4_ref import CODES, GROUP, PAGE, TOP, codes_and_scales, held, quantise
+from cache4_ref import CODES, GROUP, PAGE, TOP, codes_and_scales, held, places, quantise
 
 pytestmark = pytest.mark.gpu
 KINDS = ["int4", "e2m1"]
@@ -112,6 +112,27 @@ def test_values_where_rounding_is_decided(kind):
         before = cache.pool.clone()
         gb.cache4_append(cache, K, V, slots)
         check(cache, before, K, V, slots)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_the_sign_of_what_becomes_zero(d):
+    # e2m1 has a zero of either sign: that of the number, however small it is beside the group's largest
+    small = [0.0, 2.0 ** -130, 2.0 ** -40, 2.0 ** -18, 2.0 ** -17, 2.0 ** -16, 2.0 ** -15, 2.0 ** -8, 0.125, 0.2421875, 0.25, 0.2578125]
+    g = torch.Generator().manual_seed(4)
+    x = torch.tensor(small)[torch.randint(len(small), (40, d), generator=g)] * torch.where(torch.rand(40, d, generator=g) < 0.5, -1.0, 1.0)
+    x[:, 7::16] = torch.where(torch.rand(40, d // 16, generator=g) < 0.5, -6.0, 6.0)
+    K = x[:, None].bfloat16().cuda()
+    V = -K.flip(0).contiguous()
+    slots = torch.arange(40, device="cuda")
+    cache = filled(1, 1, d, "e2m1")
+    before = cache.pool.clone()
+    gb.cache4_append(cache, K, V, slots)
+    check(cache, before, K, V, slots)
+    k, v, _, _ = (t.cuda() for t in places(d, "e2m1"))
+    flat = cache.pool.reshape(-1).int()
+    for x, where in ((K, k), (V, v)):
+        codes = flat[where[:40, :, 0]] >> where[:40, :, 1].int() & 15
+        assert torch.equal(codes >= 8, torch.signbit(x[:, 0]))
 
 
 @pytest.mark.parametrize("kind", KINDS)

@@ -28,9 +28,8 @@
 namespace gsdpa {
 namespace {
 
-// Threads of a block of 32 rows. (Prompts of 4 x 8190 tokens, e2m1, with 64, 128, 256 threads 36.0, 31.9, 33.5 us before a
-// zero had its sign, int4
-// 42.7, 37.6, 38.8; reading 98k tokens 23.7, 22.9, 25.1.)
+// Threads of a block of 32 rows. (Prompts of 4 x 8190 tokens, int4, with 64, 128, 256 threads 42.7, 37.6, 38.8 us;
+// reading 98k tokens 23.7, 22.9, 25.1.)
 constexpr int kMany = 128;
 
 struct RowsArgs {
@@ -106,23 +105,26 @@ __device__ __forceinline__ void quantise(const uint4 (&x)[2], float unit, uint32
     const Pair inv2 = pair_of(inv, inv), up = pair_of(384.f, 384.f);
     // The largest quotient is at most 7 / (1 - 1 / 17) < 7.5, unless the scale is cut off at 448 or one of the least.
     const bool over = !E2M1 && amax * inv > 7.45f;
+    Pair y[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        y[k] = fma2(pair_of(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xffff0000u)), inv2, up);
+    if (over) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            float a, b;
+            unpair(y[k], a, b);
+            y[k] = pair_of(fminf(fmaxf(a, 377.f), 391.f), fminf(fmaxf(b, 377.f), 391.f));
+        }
+    }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         float q[8];
+        // e2m1: the 384 off again. int4: added to 1.5 2^23 + 8 (less the 384) a number is rounded to even and
+        // stands in the low bits.
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const uint32_t v = w[4 * h + k];
-            Pair y = fma2(pair_of(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u)), inv2, up);
-            if (over) {
-                float a, b;
-                unpair(y, a, b);
-                y = pair_of(fminf(fmaxf(a, 377.f), 391.f), fminf(fmaxf(b, 377.f), 391.f));
-            }
-            // e2m1: the 384 off again. int4: added to 1.5 2^23 + 8 (less the 384) a number is rounded to even and
-            // stands in the low bits.
-            y = add2(y, E2M1 ? pair_of(-384.f, -384.f) : pair_of(12582536.f, 12582536.f));
-            unpair(y, q[2 * k], q[2 * k + 1]);
-        }
+        for (int k = 0; k < 4; ++k)
+            unpair(add2(y[4 * h + k], E2M1 ? pair_of(-384.f, -384.f) : pair_of(12582536.f, 12582536.f)), q[2 * k], q[2 * k + 1]);
         if constexpr (E2M1) {
             // (a number that is rounded to 384 has lost its sign, which the code of zero has too: bit 7 of every other byte)
             const uint32_t a = __byte_perm(w[4 * h], w[4 * h + 1], 0x7351), b = __byte_perm(w[4 * h + 2], w[4 * h + 3], 0x7351);

@@ -17,8 +17,8 @@
 // which it turns four tokens' words around; where the block has all four tokens it
 // writes them at once, else their bytes one by one, so that tokens next to each other can be
 // written by different blocks and calls. The reading goes the same way back.
-// Measured: prompts of 4 x 8190 tokens, 8 heads of 128 (172 MB), e2m1 33.5 us, 5.1 TB/s, int4 37.6 us, 4.6 TB/s, the
-// integer pipe 70 % busy with unpacking, codes and exchanges; heads of 64 20.5 us int4; 64 single tokens 3.0 us;
+// Measured: prompts of 4 x 8190 tokens, 8 heads of 128 (172 MB), e2m1 33.5 us, 5.1 TB/s, int4 34.9 us, 4.9 TB/s, the
+// issue slots three quarters busy with unpacking, codes and exchanges; heads of 64 18.8 us int4; 64 single tokens 3.0 us;
 // reading 98k tokens, 2 heads of 128 (110 MB) 23 us, 4.8 TB/s.
 #include "cache4_internal.h"
 
@@ -28,8 +28,8 @@
 namespace gsdpa {
 namespace {
 
-// Threads of a block of 32 rows. (Prompts of 4 x 8190 tokens, int4, with 64, 128, 256 threads 42.7, 37.6, 38.8 us;
-// reading 98k tokens 23.7, 22.9, 25.1.)
+// Threads of a block of 32 rows. (64 and 256 took 13 and 4 % longer for prompts of 4 x 8190 tokens, 3 and 9 % for
+// reading 98k.)
 constexpr int kMany = 128;
 
 struct RowsArgs {
@@ -215,10 +215,12 @@ struct Pieces {
     __device__ __forceinline__ uint8_t* at(uint8_t* page, int tile) const {
         return page + (scales ? value_scales_at(D) + D * tile : value_codes_at(D) + 8 * D * tile) + to;
     }
-    // place of the piece's token b, and byte of a word that it has
-    __device__ __forceinline__ int place(int b) const { return 2 * t + (b & 1) + 8 * (b >> 1); }
+    // place of the token that has byte b of a word
     template <bool E2M1>
-    __device__ __forceinline__ int byte(int b) const { return scales || E2M1 ? b : (b >> 1) + 2 * (b & 1); }
+    __device__ __forceinline__ int place(int b) const {
+        if (E2M1 || b == 0 || b == 3) return 2 * t + (b & 1) + 8 * (b >> 1);
+        return 2 * t + (scales == (b == 1) ? 1 : 8);
+    }
 };
 
 template <int D, bool E2M1, int R, int THREADS>
@@ -332,15 +334,12 @@ __global__ void __launch_bounds__(THREADS) cache4_append_kernel(const __grid_con
         int have = 0;
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
-            const int row = runs.at[run][p.place(b)], to = p.template byte<E2M1>(b);
-            uint32_t x = 0;
+            const int row = runs.at[run][p.template place<E2M1>(b)];
+            w[b] = 0;
             if (row >= 0) {
-                have |= 1 << to;
-                x = *reinterpret_cast<const uint32_t*>(p.scales ? &tok.vscale[row][p.from] : &tok.value[row][p.from]);
+                have |= 1 << b;
+                w[b] = *reinterpret_cast<const uint32_t*>(p.scales ? &tok.vscale[row][p.from] : &tok.value[row][p.from]);
             }
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-                if (c == to) w[c] = x;
         }
         turn_bytes(w);
         if (have == 0) continue;
@@ -405,10 +404,9 @@ __global__ void __launch_bounds__(THREADS) cache4_read_kernel(const __grid_const
         turn_bytes(w);
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
-            const int row = runs.at[run][p.place(b)], of = p.template byte<E2M1>(b);
+            const int row = runs.at[run][p.template place<E2M1>(b)];
             if (row >= 0)
-                *reinterpret_cast<uint32_t*>(p.scales ? &tok.vscale[row][p.from] : &tok.value[row][p.from]) =
-                    of == 0 ? w[0] : (of == 1 ? w[1] : (of == 2 ? w[2] : w[3]));
+                *reinterpret_cast<uint32_t*>(p.scales ? &tok.vscale[row][p.from] : &tok.value[row][p.from]) = w[b];
         }
     }
     __syncthreads();

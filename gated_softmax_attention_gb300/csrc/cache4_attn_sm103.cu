@@ -40,10 +40,10 @@
 // merged by a second kernel, as for the 8-bit cache (cache_attn.cuh).
 //
 // Measured (32 query heads, 8 K/V heads of 128, 64 x 8192 tokens, 604 MB, no gate): e2m1 121 us, 5.0 TB/s, int4
-// 124 us, heads of 64 81 us. Of the 121 the copies alone take 102 and the products
+// 124 us, heads of 64 71 and 74 us. Of the 121 the copies alone take 102 and the products
 // alone 102 (integer pipe 68 % busy, two thirds of the issue slots): neither hides behind the other wholly. What
 // brought it there: up to 8 rows every warp is a team of its own and copies for itself, three half
-// pages ahead (221 KB of an SM's shared memory under way; a copying warp and eight teams of two warps 133, 140 int4,
+// pages ahead, in heads of 64 three pages (221 KB of an SM's shared memory under way; by halves 81 us; a copying warp and eight teams of two warps 133, 140 int4,
 // 95 in heads of 64; two stages are as fast); up to 4 rows both halves of the narrow side are in use (HALF: 127 without).
 // Beyond 8 rows the codes are converted again for every 16: 16 x 8000 tokens, 22 us of bytes, 4, 8, 16, 32, 64 and
 // 128 rows 45, 48, 58, 96, 173 and 324 us. (A page converted once for its team, in shared memory, with rows on the side
@@ -479,11 +479,12 @@ struct Config {
     static constexpr int CONSUMERS = WARPS * 32;
     static constexpr int THREADS = CONSUMERS + (ALONE ? 0 : 128);
     static constexpr int STRIDE = D + 4;                // floats of a row's part: D columns, then m, l, M
-    static constexpr uint32_t STAGE = half_bytes(D);    // bytes: a page's keys or values, with their scales
+    static constexpr bool BOTH = ALONE && D == 64;      // a stage is a page, else half of one: keys or values, with their scales
+    static constexpr uint32_t STAGE = BOTH ? page_bytes(D) : half_bytes(D);
 };
 
-// What is copied next for a team: the tiles of its share, keys, then values.
-template <int D>
+// What is copied next for a team: the tiles of its share, keys, then values, or both at once.
+template <int D, bool BOTH>
 struct Feed {
     Cursor next;
     const int* row;     // of the table
@@ -502,12 +503,12 @@ struct Feed {
         if (next.left > 0) enter(a);
     }
     __device__ __forceinline__ bool more() const { return next.left > 0; }
-    // The next half page, to `to`; `go` in the thread that issues it. (No branch for one thread of a warp: two such a
+    // The next stage, to `to`; `go` in the thread that issues it. (No branch for one thread of a warp: two such a
     // page were a tenth of its time.)
     __device__ __forceinline__ void issue(const Cache4Args& a, uint8_t* to, uint64_t* full, bool go) {
-        constexpr uint32_t STAGE = half_bytes(D);
+        constexpr uint32_t STAGE = BOTH ? page_bytes(D) : half_bytes(D);
         if (page >= 0 && page < a.n_pages) {
-            const uint8_t* from = a.pool + (((long long)page * a.Hkv + next.kvh) * 2 + (values ? 1 : 0)) * STAGE;
+            const uint8_t* from = a.pool + ((long long)page * a.Hkv + next.kvh) * page_bytes(D) + (!BOTH && values ? STAGE : 0);
             asm volatile(
                 "{\n\t.reg .pred p;\n\t"
                 "setp.ne.u32 p, %4, 0;\n\t"
@@ -518,13 +519,16 @@ struct Feed {
         } else if (go) {
             // no page of the pool: keys whose scales are NaN (who sees them is NaN), values of scale 0
             uint4* scales = reinterpret_cast<uint4*>(to + key_scales_at(D));
-            const uint32_t x = values ? 0u : 0x7f7f7f7fu;
-            for (int k = 0; k < 4 * D / 16; ++k) scales[k] = make_uint4(x, x, x, x);
+            const uint32_t x = !BOTH && values ? 0u : 0x7f7f7f7fu;
+            for (int k = 0; k < 4 * D / 16; ++k) {
+                scales[k] = make_uint4(x, x, x, x);
+                if (BOTH) scales[k + half_bytes(D) / 16] = make_uint4(0, 0, 0, 0);
+            }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // (before the stage's next copy)
             mbar_arrive(full);
             atomicOr(a.ctl.err, ERR_CACHE_RANGE);
         }
-        if (values) {
+        if (BOTH || values) {
             if (next.j + 1 < next.tiles) {
                 ++next.j;
                 --next.left;
@@ -632,7 +636,7 @@ __global__ void __launch_bounds__(Config<D, NT>::THREADS, 1) cache4_attn_kernel(
             // ---- copies: lane k serves team k, in the order the team consumes them
             Cursor none;
             none.left = none.b = none.kvh = none.j = none.tiles = 0;
-            Feed<D> feed;
+            Feed<D, C::BOTH> feed;
             feed.start(a, lane < teams ? s_start[lane] : none);
             uint8_t* ring = smem + (size_t)lane * a.stages * STAGE;
             uint64_t *full = s_full + lane * a.stages, *empty = s_empty + lane * a.stages;
@@ -687,7 +691,7 @@ __global__ void __launch_bounds__(Config<D, NT>::THREADS, 1) cache4_attn_kernel(
         const int team_threads = 32 * team_warps, team_tid = 32 * rt + lane;
         float* slot = slot_of(team);
         uint32_t stage = 0, phase = 0;   // the oldest stage that is not released
-        int ahead = 0;                   // ALONE: half pages that are issued and not released
+        int ahead = 0;                   // ALONE: stages that are issued and not released
         Cursor at = s_start[team];
         const int share_end = team_lo(team + 1);
         // The first head's queries are asked for before the copies: behind 30 MB of these they took 4 us more.
@@ -702,7 +706,7 @@ __global__ void __launch_bounds__(Config<D, NT>::THREADS, 1) cache4_attn_kernel(
             }
         };
         if (at.left > 0) load_queries(PagedSeq(a, at.b));
-        Feed<D> feed;
+        Feed<D, C::BOTH> feed;
         if constexpr (C::ALONE) {
             feed.start(a, at);
             for (; ahead < a.stages && feed.more(); ++ahead)
@@ -779,7 +783,7 @@ __global__ void __launch_bounds__(Config<D, NT>::THREADS, 1) cache4_attn_kernel(
                 float s[NT][MT][EL];
                 const uint8_t* kt = wait_full(0);
                 if (!kt) break;
-                const uint8_t* vt = wait_full(1);
+                const uint8_t* vt = C::BOTH ? kt + half_bytes(D) : wait_full(1);
                 if (!vt) break;
                 // (the first query row sees tokens up to len: tiles before need no mask)
                 const int base = j * kPage;
@@ -875,7 +879,7 @@ __global__ void __launch_bounds__(Config<D, NT>::THREADS, 1) cache4_attn_kernel(
                             for (int e = 0; e < EL; ++e) s[n][i][e] = sum[n][e];
                     }
                 }
-                release();
+                if (!C::BOTH) release();
                 int lim[NT][2] = {};
                 const int at0 = base + g + (HALF ? 4 * (t & 2) : 0);   // the lane's first token
                 if (masked) {
@@ -1069,7 +1073,7 @@ Shape shape_of(int rows, int D) {
     s.R = rows <= 16 ? 1 : (rows <= 32 ? 2 : (rows <= 64 ? 4 : 8));
     s.teams = (s.NT == 1 ? 2 * kSlots : kSlots) / s.R;
     const uint32_t merge = s.NT == 1 ? 0 : (uint32_t)(s.teams * rows * (D + 4)) * 4;
-    const uint32_t per_stage = (uint32_t)s.teams * half_bytes(D);
+    const uint32_t per_stage = (uint32_t)s.teams * (s.NT == 1 && D == 64 ? page_bytes(D) : half_bytes(D));   // (Config::BOTH)
     // as many copies in flight as fit
     s.stages = (int)((kSmemMax - merge) / per_stage);
     if (s.stages > kMaxStages) s.stages = kMaxStages;

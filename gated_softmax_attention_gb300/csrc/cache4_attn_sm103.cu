@@ -39,12 +39,13 @@
 // requests and K/V heads are dealt evenly to teams of warps and the heads that they cut
 // merged by a second kernel, as for the 8-bit cache (cache_attn.cuh).
 //
-// Measured (32 query heads, 8 K/V heads of 128, 64 x 8192 tokens, 604 MB, no gate): e2m1 121 us, 5.0 TB/s, int4
-// 124 us, heads of 64 71 and 74 us. Of the 121 the copies alone take 102 and the products
+// Measured (32 query heads, 8 K/V heads of 128, 64 x 8192 tokens, 604 MB, no gate): e2m1 119 us, 5.1 TB/s, int4
+// 123 us, heads of 64 71 and 74 us. Of the 119 the copies alone take 102 and the products
 // alone 102 (integer pipe 68 % busy, two thirds of the issue slots): neither hides behind the other wholly. What
-// brought it there: up to 8 rows every warp is a team of its own and copies for itself, three half
-// pages ahead, in heads of 64 three pages (221 KB of an SM's shared memory under way; by halves 81 us; a copying warp and eight teams of two warps 133, 140 int4,
-// 95 in heads of 64; two stages are as fast); up to 4 rows both halves of the narrow side are in use (HALF: 127 without).
+// brought it there: up to 8 rows every warp is a team of its own and copies for itself, keys
+// into one buffer and values into another, the next page's where this page's have just been used (a ring of three halves 121 us),
+// in heads of 64 a page in one copy, three ahead (by halves 81 us; a copying warp and eight teams of two warps 133, 140 int4,
+// 95 in heads of 64); up to 4 rows both halves of the narrow side are in use (HALF: 127 without).
 // Beyond 8 rows the codes are converted again for every 16: 16 x 8000 tokens, 22 us of bytes, 4, 8, 16, 32, 64 and
 // 128 rows 45, 48, 58, 96, 173 and 324 us. (A page converted once for its team, in shared memory, with rows on the side
 // of 16 and scales in the operands: 71 us for 16 rows, 120, 198 and 346; eight warps that meet at two barriers a page
@@ -480,6 +481,7 @@ struct Config {
     static constexpr int THREADS = CONSUMERS + (ALONE ? 0 : 128);
     static constexpr int STRIDE = D + 4;                // floats of a row's part: D columns, then m, l, M
     static constexpr bool BOTH = ALONE && D == 64;      // a stage is a page, else half of one: keys or values, with their scales
+    static constexpr bool PAIR = ALONE && !BOTH;        // two stages: one for keys, one for values
     static constexpr uint32_t STAGE = BOTH ? page_bytes(D) : half_bytes(D);
 };
 
@@ -489,7 +491,7 @@ struct Feed {
     Cursor next;
     const int* row;     // of the table
     int page, after;    // of the tile at `next` and of the one after it
-    bool values;
+    bool values;        // of two halves the second is next
     __device__ __forceinline__ void enter(const Cache4Args& a) {
         row = a.table + (long long)next.b * a.width;
         page = row[next.j];
@@ -505,7 +507,7 @@ struct Feed {
     __device__ __forceinline__ bool more() const { return next.left > 0; }
     // The next stage, to `to`; `go` in the thread that issues it. (No branch for one thread of a warp: two such a
     // page were a tenth of its time.)
-    __device__ __forceinline__ void issue(const Cache4Args& a, uint8_t* to, uint64_t* full, bool go) {
+    __device__ __forceinline__ void issue(const Cache4Args& a, uint8_t* to, uint64_t* full, bool go, bool values) {
         constexpr uint32_t STAGE = BOTH ? page_bytes(D) : half_bytes(D);
         if (page >= 0 && page < a.n_pages) {
             const uint8_t* from = a.pool + ((long long)page * a.Hkv + next.kvh) * page_bytes(D) + (!BOTH && values ? STAGE : 0);
@@ -539,7 +541,6 @@ struct Feed {
                 if (next.left > 0) enter(a);
             }
         }
-        values = !values;
     }
 };
 
@@ -648,7 +649,8 @@ __global__ void __launch_bounds__(Config<D, NT>::THREADS, 1) cache4_attn_kernel(
                     did = true;
                     armed |= 1u << stage;
                     armed_phase = (armed_phase & ~(1u << stage)) | (phase << stage);
-                    feed.issue(a, ring + stage * STAGE, &full[stage], true);
+                    feed.issue(a, ring + stage * STAGE, &full[stage], true, feed.values);
+                    feed.values = !feed.values;
                     if (++stage == (uint32_t)a.stages) {
                         stage = 0;
                         phase ^= 1u;
@@ -710,11 +712,11 @@ __global__ void __launch_bounds__(Config<D, NT>::THREADS, 1) cache4_attn_kernel(
         if constexpr (C::ALONE) {
             feed.start(a, at);
             for (; ahead < a.stages && feed.more(); ++ahead)
-                feed.issue(a, smem + ((size_t)team * a.stages + ahead) * STAGE, &full[ahead], lane == 0);
+                feed.issue(a, smem + ((size_t)team * a.stages + ahead) * STAGE, &full[ahead], lane == 0, C::PAIR && ahead == 1);
         }
         const auto wait_full = [&](uint32_t next) -> const uint8_t* {   // that stage, or the next
             uint32_t k = stage + next, ph = phase;
-            if (k >= (uint32_t)a.stages) {
+            if (!C::PAIR && k >= (uint32_t)a.stages) {
                 k -= a.stages;
                 ph ^= 1u;
             }
@@ -724,12 +726,21 @@ __global__ void __launch_bounds__(Config<D, NT>::THREADS, 1) cache4_attn_kernel(
             }
             return ring + k * STAGE;
         };
-        const auto release = [&]() {
+        const auto release = [&](bool values) {
             __syncwarp();
+            if constexpr (C::PAIR) {
+                --ahead;
+                if (feed.more()) {
+                    feed.issue(a, const_cast<uint8_t*>(ring) + (values ? STAGE : 0), &full[values ? 1 : 0], lane == 0, values);
+                    ++ahead;
+                }
+                if (values) phase ^= 1u;
+                return;
+            }
             if constexpr (C::ALONE) {
                 --ahead;
                 if (feed.more()) {
-                    feed.issue(a, const_cast<uint8_t*>(ring) + stage * STAGE, &full[stage], lane == 0);
+                    feed.issue(a, const_cast<uint8_t*>(ring) + stage * STAGE, &full[stage], lane == 0, false);
                     ++ahead;
                 }
             } else {
@@ -879,7 +890,7 @@ __global__ void __launch_bounds__(Config<D, NT>::THREADS, 1) cache4_attn_kernel(
                             for (int e = 0; e < EL; ++e) s[n][i][e] = sum[n][e];
                     }
                 }
-                if (!C::BOTH) release();
+                if (!C::BOTH) release(false);
                 int lim[NT][2] = {};
                 const int at0 = base + g + (HALF ? 4 * (t & 2) : 0);   // the lane's first token
                 if (masked) {
@@ -929,7 +940,7 @@ __global__ void __launch_bounds__(Config<D, NT>::THREADS, 1) cache4_attn_kernel(
                         }
                     }
                 }
-                release();
+                release(true);
             }
 
             // ---- the segment's rows: sums over the lanes, and the codes' units out of the outputs
@@ -1077,6 +1088,7 @@ Shape shape_of(int rows, int D) {
     // as many copies in flight as fit
     s.stages = (int)((kSmemMax - merge) / per_stage);
     if (s.stages > kMaxStages) s.stages = kMaxStages;
+    if (s.NT == 1 && D == 128) s.stages = 2;   // (Config::PAIR)
     if (s.stages > kBars / s.teams) s.stages = kBars / s.teams;
     s.smem = (uint32_t)s.stages * per_stage + merge;
     return s;

@@ -40,11 +40,12 @@
 // merged by a second kernel, as for the 8-bit cache (cache_attn.cuh).
 //
 // Measured (32 query heads, 8 K/V heads of 128, 64 x 8192 tokens, 604 MB, no gate): e2m1 119 us, 5.1 TB/s, int4
-// 123 us, heads of 64 71 and 74 us. Of the 119 the copies alone take 102 and the products
+// 121 us, heads of 64 71 and 74 us. Of the 119 the copies alone take 102 and the products
 // alone 102 (integer pipe 68 % busy, two thirds of the issue slots): neither hides behind the other wholly. What
-// brought it there: up to 8 rows every warp is a team of its own and copies for itself, keys
-// into one buffer and values into another, the next page's where this page's have just been used (a ring of three halves 121 us),
-// in heads of 64 a page in one copy, three ahead (by halves 81 us; a copying warp and eight teams of two warps 133, 140 int4,
+// brought it there: up to 8 rows every warp is a team of its own and copies for itself, a
+// page at a time, into one buffer, where the one before has just been used (the other 15 warps are work enough
+// meanwhile; keys' and values' halves in a ring of three 121 us, int4 125, in two buffers of their own 119, 123), in heads of 64 three
+// pages ahead (by halves 81 us; a copying warp and eight teams of two warps 133, 140 int4,
 // 95 in heads of 64); up to 4 rows both halves of the narrow side are in use (HALF: 127 without).
 // Beyond 8 rows the codes are converted again for every 16: 16 x 8000 tokens, 22 us of bytes, 4, 8, 16, 32, 64 and
 // 128 rows 45, 48, 58, 96, 173 and 324 us. (A page converted once for its team, in shared memory, with rows on the side
@@ -480,9 +481,9 @@ struct Config {
     static constexpr int CONSUMERS = WARPS * 32;
     static constexpr int THREADS = CONSUMERS + (ALONE ? 0 : 128);
     static constexpr int STRIDE = D + 4;                // floats of a row's part: D columns, then m, l, M
-    static constexpr bool BOTH = ALONE && D == 64;      // a stage is a page, else half of one: keys or values, with their scales
-    static constexpr bool PAIR = ALONE && !BOTH;        // two stages: one for keys, one for values
-    static constexpr uint32_t STAGE = BOTH ? page_bytes(D) : half_bytes(D);
+    // bytes of a stage: a page, else half of one: keys or values, with their scales
+    static constexpr uint32_t STAGE = ALONE ? page_bytes(D) : half_bytes(D);
+    static constexpr int STAGES = kSmemMax / (WARPS * STAGE);   // of a lone warp: 1 (d_k 128), 3
 };
 
 // What is copied next for a team: the tiles of its share, keys, then values, or both at once.
@@ -491,7 +492,7 @@ struct Feed {
     Cursor next;
     const int* row;     // of the table
     int page, after;    // of the tile at `next` and of the one after it
-    bool values;        // of two halves the second is next
+    bool values;
     __device__ __forceinline__ void enter(const Cache4Args& a) {
         row = a.table + (long long)next.b * a.width;
         page = row[next.j];
@@ -507,7 +508,7 @@ struct Feed {
     __device__ __forceinline__ bool more() const { return next.left > 0; }
     // The next stage, to `to`; `go` in the thread that issues it. (No branch for one thread of a warp: two such a
     // page were a tenth of its time.)
-    __device__ __forceinline__ void issue(const Cache4Args& a, uint8_t* to, uint64_t* full, bool go, bool values) {
+    __device__ __forceinline__ void issue(const Cache4Args& a, uint8_t* to, uint64_t* full, bool go) {
         constexpr uint32_t STAGE = BOTH ? page_bytes(D) : half_bytes(D);
         if (page >= 0 && page < a.n_pages) {
             const uint8_t* from = a.pool + ((long long)page * a.Hkv + next.kvh) * page_bytes(D) + (!BOTH && values ? STAGE : 0);
@@ -541,6 +542,7 @@ struct Feed {
                 if (next.left > 0) enter(a);
             }
         }
+        values = !values;
     }
 };
 
@@ -637,7 +639,7 @@ __global__ void __launch_bounds__(Config<D, NT>::THREADS, 1) cache4_attn_kernel(
             // ---- copies: lane k serves team k, in the order the team consumes them
             Cursor none;
             none.left = none.b = none.kvh = none.j = none.tiles = 0;
-            Feed<D, C::BOTH> feed;
+            Feed<D, C::ALONE> feed;
             feed.start(a, lane < teams ? s_start[lane] : none);
             uint8_t* ring = smem + (size_t)lane * a.stages * STAGE;
             uint64_t *full = s_full + lane * a.stages, *empty = s_empty + lane * a.stages;
@@ -649,8 +651,7 @@ __global__ void __launch_bounds__(Config<D, NT>::THREADS, 1) cache4_attn_kernel(
                     did = true;
                     armed |= 1u << stage;
                     armed_phase = (armed_phase & ~(1u << stage)) | (phase << stage);
-                    feed.issue(a, ring + stage * STAGE, &full[stage], true, feed.values);
-                    feed.values = !feed.values;
+                    feed.issue(a, ring + stage * STAGE, &full[stage], true);
                     if (++stage == (uint32_t)a.stages) {
                         stage = 0;
                         phase ^= 1u;
@@ -692,6 +693,7 @@ __global__ void __launch_bounds__(Config<D, NT>::THREADS, 1) cache4_attn_kernel(
         uint64_t *full = s_full + team * a.stages, *empty = C::ALONE ? s_empty : s_empty + team * a.stages;
         const int team_threads = 32 * team_warps, team_tid = 32 * rt + lane;
         float* slot = slot_of(team);
+        const int stages = C::ALONE ? C::STAGES : a.stages;
         uint32_t stage = 0, phase = 0;   // the oldest stage that is not released
         int ahead = 0;                   // ALONE: stages that are issued and not released
         Cursor at = s_start[team];
@@ -708,16 +710,16 @@ __global__ void __launch_bounds__(Config<D, NT>::THREADS, 1) cache4_attn_kernel(
             }
         };
         if (at.left > 0) load_queries(PagedSeq(a, at.b));
-        Feed<D, C::BOTH> feed;
+        Feed<D, C::ALONE> feed;
         if constexpr (C::ALONE) {
             feed.start(a, at);
-            for (; ahead < a.stages && feed.more(); ++ahead)
-                feed.issue(a, smem + ((size_t)team * a.stages + ahead) * STAGE, &full[ahead], lane == 0, C::PAIR && ahead == 1);
+            for (; ahead < stages && feed.more(); ++ahead)
+                feed.issue(a, smem + ((size_t)team * stages + ahead) * STAGE, &full[ahead], lane == 0);
         }
         const auto wait_full = [&](uint32_t next) -> const uint8_t* {   // that stage, or the next
             uint32_t k = stage + next, ph = phase;
-            if (!C::PAIR && k >= (uint32_t)a.stages) {
-                k -= a.stages;
+            if (k >= (uint32_t)stages) {
+                k -= stages;
                 ph ^= 1u;
             }
             if (!__all_sync(0xffffffffu, mbar_wait(&full[k], ph, abort_flag, a.ctl))) {
@@ -726,27 +728,18 @@ __global__ void __launch_bounds__(Config<D, NT>::THREADS, 1) cache4_attn_kernel(
             }
             return ring + k * STAGE;
         };
-        const auto release = [&](bool values) {
+        const auto release = [&]() {
             __syncwarp();
-            if constexpr (C::PAIR) {
-                --ahead;
-                if (feed.more()) {
-                    feed.issue(a, const_cast<uint8_t*>(ring) + (values ? STAGE : 0), &full[values ? 1 : 0], lane == 0, values);
-                    ++ahead;
-                }
-                if (values) phase ^= 1u;
-                return;
-            }
             if constexpr (C::ALONE) {
                 --ahead;
                 if (feed.more()) {
-                    feed.issue(a, const_cast<uint8_t*>(ring) + stage * STAGE, &full[stage], lane == 0, false);
+                    feed.issue(a, const_cast<uint8_t*>(ring) + stage * STAGE, &full[stage], lane == 0);
                     ++ahead;
                 }
             } else {
                 if (lane == 0) mbar_arrive(&empty[stage]);
             }
-            if (++stage == (uint32_t)a.stages) {
+            if (++stage == (uint32_t)stages) {
                 stage = 0;
                 phase ^= 1u;
             }
@@ -794,7 +787,7 @@ __global__ void __launch_bounds__(Config<D, NT>::THREADS, 1) cache4_attn_kernel(
                 float s[NT][MT][EL];
                 const uint8_t* kt = wait_full(0);
                 if (!kt) break;
-                const uint8_t* vt = C::BOTH ? kt + half_bytes(D) : wait_full(1);
+                const uint8_t* vt = C::ALONE ? kt + half_bytes(D) : wait_full(1);
                 if (!vt) break;
                 // (the first query row sees tokens up to len: tiles before need no mask)
                 const int base = j * kPage;
@@ -890,7 +883,7 @@ __global__ void __launch_bounds__(Config<D, NT>::THREADS, 1) cache4_attn_kernel(
                             for (int e = 0; e < EL; ++e) s[n][i][e] = sum[n][e];
                     }
                 }
-                if (!C::BOTH) release(false);
+                if (!C::ALONE) release();
                 int lim[NT][2] = {};
                 const int at0 = base + g + (HALF ? 4 * (t & 2) : 0);   // the lane's first token
                 if (masked) {
@@ -940,7 +933,7 @@ __global__ void __launch_bounds__(Config<D, NT>::THREADS, 1) cache4_attn_kernel(
                         }
                     }
                 }
-                release(true);
+                release();
             }
 
             // ---- the segment's rows: sums over the lanes, and the codes' units out of the outputs
@@ -1013,7 +1006,7 @@ __global__ void __launch_bounds__(Config<D, NT>::THREADS, 1) cache4_attn_kernel(
             const WaitCtl c2 = landing_limit(a.ctl);
             for (; ahead > 0; --ahead) {
                 mbar_wait(&full[stage], phase, &never, c2);
-                if (++stage == (uint32_t)a.stages) {
+                if (++stage == (uint32_t)stages) {
                     stage = 0;
                     phase ^= 1u;
                 }
@@ -1084,11 +1077,10 @@ Shape shape_of(int rows, int D) {
     s.R = rows <= 16 ? 1 : (rows <= 32 ? 2 : (rows <= 64 ? 4 : 8));
     s.teams = (s.NT == 1 ? 2 * kSlots : kSlots) / s.R;
     const uint32_t merge = s.NT == 1 ? 0 : (uint32_t)(s.teams * rows * (D + 4)) * 4;
-    const uint32_t per_stage = (uint32_t)s.teams * (s.NT == 1 && D == 64 ? page_bytes(D) : half_bytes(D));   // (Config::BOTH)
+    const uint32_t per_stage = (uint32_t)s.teams * (s.NT == 1 ? page_bytes(D) : half_bytes(D));
     // as many copies in flight as fit
     s.stages = (int)((kSmemMax - merge) / per_stage);
     if (s.stages > kMaxStages) s.stages = kMaxStages;
-    if (s.NT == 1 && D == 128) s.stages = 2;   // (Config::PAIR)
     if (s.stages > kBars / s.teams) s.stages = kBars / s.teams;
     s.smem = (uint32_t)s.stages * per_stage + merge;
     return s;

@@ -34,23 +34,23 @@
 // the exponent of the page's largest value scale where that is above 1 (0 .. 9), and stands
 // 2^13 below, so that neither p nor p vs exceeds 2^15. It moves when a tile exceeds it by 2^2.
 //
-// Tile = one page: keys with their scales, then values with theirs, 36 d_k contiguous
-// bytes each, brought by cp.async.bulk from where the table says. The tiles of all
+// Tile = one page: keys with their scales, then values with theirs, 72 d_k contiguous
+// bytes, brought by one cp.async.bulk from where the table says. The tiles of all
 // requests and K/V heads are dealt evenly to teams of warps and the heads that they cut
 // merged by a second kernel, as for the 8-bit cache (cache_attn.cuh).
 //
-// Measured (32 query heads, 8 K/V heads of 128, 64 x 8192 tokens, 604 MB, no gate): e2m1 119 us, 5.1 TB/s, int4
-// 121 us, heads of 64 71 and 74 us. Of the 119 the copies alone take 102 and the products
+// Measured (32 query heads, 8 K/V heads of 128, 64 x 8192 tokens, 604 MB, no gate): e2m1 118 us, 5.1 TB/s, int4
+// 121 us, heads of 64 71 and 76 us. Of the 118 the copies alone take 102 and the products
 // alone 102 (integer pipe 68 % busy, two thirds of the issue slots): neither hides behind the other wholly. What
 // brought it there: up to 8 rows every warp is a team of its own and copies for itself, a
 // page at a time, into one buffer, where the one before has just been used (the other 15 warps are work enough
 // meanwhile; keys' and values' halves in a ring of three 121 us, int4 125, in two buffers of their own 119, 123), in heads of 64 three
 // pages ahead (by halves 81 us; a copying warp and eight teams of two warps 133, 140 int4,
 // 95 in heads of 64); up to 4 rows both halves of the narrow side are in use (HALF: 127 without).
-// Beyond 8 rows the codes are converted again for every 16: 16 x 8000 tokens, 22 us of bytes, 4, 8, 16, 32, 64 and
-// 128 rows 45, 48, 58, 96, 173 and 324 us. (A page converted once for its team, in shared memory, with rows on the side
-// of 16 and scales in the operands: 71 us for 16 rows, 120, 198 and 346; eight warps that meet at two barriers a page
-// leave the SM idle more than the second conversion costs.)
+// Beyond 8 rows the codes are converted again for every 16: 16 x 8000 tokens, 22 us of bytes, 16, 32 and 64 rows
+// 55, 90 and 161 us (58, 96, 173 by halves of a page; a page converted once for its team, in shared memory, with rows on the
+// side of 16 and scales in the operands 71, 120, 198: eight warps that meet at two barriers a page leave the SM idle
+// more than the second conversion costs).
 #include "cache4_internal.h"
 #include "cache_attn.cuh"
 #include "landing.cuh"
@@ -481,18 +481,16 @@ struct Config {
     static constexpr int CONSUMERS = WARPS * 32;
     static constexpr int THREADS = CONSUMERS + (ALONE ? 0 : 128);
     static constexpr int STRIDE = D + 4;                // floats of a row's part: D columns, then m, l, M
-    // bytes of a stage: a page, else half of one: keys or values, with their scales
-    static constexpr uint32_t STAGE = ALONE ? page_bytes(D) : half_bytes(D);
+    static constexpr uint32_t STAGE = page_bytes(D);    // bytes: a page
     static constexpr int STAGES = kSmemMax / (WARPS * STAGE);   // of a lone warp: 1 (d_k 128), 3
 };
 
-// What is copied next for a team: the tiles of its share, keys, then values, or both at once.
-template <int D, bool BOTH>
+// What is copied next for a team: the tiles of its share.
+template <int D>
 struct Feed {
     Cursor next;
     const int* row;     // of the table
     int page, after;    // of the tile at `next` and of the one after it
-    bool values;
     __device__ __forceinline__ void enter(const Cache4Args& a) {
         row = a.table + (long long)next.b * a.width;
         page = row[next.j];
@@ -500,7 +498,6 @@ struct Feed {
     }
     __device__ __forceinline__ void start(const Cache4Args& a, const Cursor& at) {
         next = at;
-        values = false;
         row = a.table;
         page = after = 0;
         if (next.left > 0) enter(a);
@@ -509,9 +506,9 @@ struct Feed {
     // The next stage, to `to`; `go` in the thread that issues it. (No branch for one thread of a warp: two such a
     // page were a tenth of its time.)
     __device__ __forceinline__ void issue(const Cache4Args& a, uint8_t* to, uint64_t* full, bool go) {
-        constexpr uint32_t STAGE = BOTH ? page_bytes(D) : half_bytes(D);
+        constexpr uint32_t STAGE = page_bytes(D);
         if (page >= 0 && page < a.n_pages) {
-            const uint8_t* from = a.pool + ((long long)page * a.Hkv + next.kvh) * page_bytes(D) + (!BOTH && values ? STAGE : 0);
+            const uint8_t* from = a.pool + ((long long)page * a.Hkv + next.kvh) * STAGE;
             asm volatile(
                 "{\n\t.reg .pred p;\n\t"
                 "setp.ne.u32 p, %4, 0;\n\t"
@@ -521,28 +518,24 @@ struct Feed {
                 : "memory");
         } else if (go) {
             // no page of the pool: keys whose scales are NaN (who sees them is NaN), values of scale 0
-            uint4* scales = reinterpret_cast<uint4*>(to + key_scales_at(D));
-            const uint32_t x = !BOTH && values ? 0u : 0x7f7f7f7fu;
+            const uint32_t x = 0x7f7f7f7fu;
             for (int k = 0; k < 4 * D / 16; ++k) {
-                scales[k] = make_uint4(x, x, x, x);
-                if (BOTH) scales[k + half_bytes(D) / 16] = make_uint4(0, 0, 0, 0);
+                reinterpret_cast<uint4*>(to + key_scales_at(D))[k] = make_uint4(x, x, x, x);
+                reinterpret_cast<uint4*>(to + value_scales_at(D))[k] = make_uint4(0, 0, 0, 0);
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // (before the stage's next copy)
             mbar_arrive(full);
             atomicOr(a.ctl.err, ERR_CACHE_RANGE);
         }
-        if (BOTH || values) {
-            if (next.j + 1 < next.tiles) {
-                ++next.j;
-                --next.left;
-                page = after;
-                if (next.j + 1 < next.tiles) after = row[next.j + 1];
-            } else {
-                next.next_head(a);
-                if (next.left > 0) enter(a);
-            }
+        if (next.j + 1 < next.tiles) {
+            ++next.j;
+            --next.left;
+            page = after;
+            if (next.j + 1 < next.tiles) after = row[next.j + 1];
+        } else {
+            next.next_head(a);
+            if (next.left > 0) enter(a);
         }
-        values = !values;
     }
 };
 
@@ -639,7 +632,7 @@ __global__ void __launch_bounds__(Config<D, NT>::THREADS, 1) cache4_attn_kernel(
             // ---- copies: lane k serves team k, in the order the team consumes them
             Cursor none;
             none.left = none.b = none.kvh = none.j = none.tiles = 0;
-            Feed<D, C::ALONE> feed;
+            Feed<D> feed;
             feed.start(a, lane < teams ? s_start[lane] : none);
             uint8_t* ring = smem + (size_t)lane * a.stages * STAGE;
             uint64_t *full = s_full + lane * a.stages, *empty = s_empty + lane * a.stages;
@@ -710,23 +703,18 @@ __global__ void __launch_bounds__(Config<D, NT>::THREADS, 1) cache4_attn_kernel(
             }
         };
         if (at.left > 0) load_queries(PagedSeq(a, at.b));
-        Feed<D, C::ALONE> feed;
+        Feed<D> feed;
         if constexpr (C::ALONE) {
             feed.start(a, at);
             for (; ahead < stages && feed.more(); ++ahead)
                 feed.issue(a, smem + ((size_t)team * stages + ahead) * STAGE, &full[ahead], lane == 0);
         }
-        const auto wait_full = [&](uint32_t next) -> const uint8_t* {   // that stage, or the next
-            uint32_t k = stage + next, ph = phase;
-            if (k >= (uint32_t)stages) {
-                k -= stages;
-                ph ^= 1u;
-            }
-            if (!__all_sync(0xffffffffu, mbar_wait(&full[k], ph, abort_flag, a.ctl))) {
+        const auto wait_full = [&]() -> const uint8_t* {
+            if (!__all_sync(0xffffffffu, mbar_wait(&full[stage], phase, abort_flag, a.ctl))) {
                 ok = false;
                 return nullptr;
             }
-            return ring + k * STAGE;
+            return ring + stage * STAGE;
         };
         const auto release = [&]() {
             __syncwarp();
@@ -785,14 +773,13 @@ __global__ void __launch_bounds__(Config<D, NT>::THREADS, 1) cache4_attn_kernel(
             for (int j = at.j; ok && j < j1; ++j) {
                 constexpr int EL = HALF ? 2 : 4;
                 float s[NT][MT][EL];
-                const uint8_t* kt = wait_full(0);
+                const uint8_t* kt = wait_full();
                 if (!kt) break;
-                const uint8_t* vt = C::ALONE ? kt + half_bytes(D) : wait_full(1);
-                if (!vt) break;
+                const uint8_t* vt = kt + value_codes_at(D);
                 // (the first query row sees tokens up to len: tiles before need no mask)
                 const int base = j * kPage;
                 const bool masked = base + kPage - 1 > q.len;
-                const uint8_t* scales = vt + key_scales_at(D);   // (as far into the values' half)
+                const uint8_t* scales = kt + value_scales_at(D);
                 if (masked && q.T < base + kPage) clear_scales<D>(const_cast<uint8_t*>(scales), lane, q.T - base);
                 const float ev = scale_exponent<D, MT>(scales, lane);
 #pragma unroll
@@ -883,7 +870,6 @@ __global__ void __launch_bounds__(Config<D, NT>::THREADS, 1) cache4_attn_kernel(
                             for (int e = 0; e < EL; ++e) s[n][i][e] = sum[n][e];
                     }
                 }
-                if (!C::ALONE) release();
                 int lim[NT][2] = {};
                 const int at0 = base + g + (HALF ? 4 * (t & 2) : 0);   // the lane's first token
                 if (masked) {
@@ -1077,7 +1063,7 @@ Shape shape_of(int rows, int D) {
     s.R = rows <= 16 ? 1 : (rows <= 32 ? 2 : (rows <= 64 ? 4 : 8));
     s.teams = (s.NT == 1 ? 2 * kSlots : kSlots) / s.R;
     const uint32_t merge = s.NT == 1 ? 0 : (uint32_t)(s.teams * rows * (D + 4)) * 4;
-    const uint32_t per_stage = (uint32_t)s.teams * (s.NT == 1 ? page_bytes(D) : half_bytes(D));
+    const uint32_t per_stage = (uint32_t)s.teams * page_bytes(D);
     // as many copies in flight as fit
     s.stages = (int)((kSmemMax - merge) / per_stage);
     if (s.stages > kMaxStages) s.stages = kMaxStages;

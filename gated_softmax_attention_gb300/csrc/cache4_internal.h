@@ -12,7 +12,6 @@ constexpr int kMaxExp = 64;      // of k_exp and v_exp
 // Offsets in the 72 d bytes that a page has of one head: key codes, key scales,
 // value codes, value scales.
 constexpr int page_bytes(int d) { return 72 * d; }
-constexpr int half_bytes(int d) { return 36 * d; }
 constexpr int key_scales_at(int d) { return 32 * d; }
 constexpr int value_codes_at(int d) { return 36 * d; }
 constexpr int value_scales_at(int d) { return 68 * d; }

@@ -549,7 +549,7 @@ __global__ void __launch_bounds__(Config<D, NT>::THREADS, 1) cache4_attn_kernel(
     __shared__ int s_place[kScan + 1], s_scan[2 * kScan / 32];
     __shared__ float s_weight[kSlots * 16], s_l[C::ALONE ? 8 : kMaxRows], s_m[C::ALONE ? 8 : kMaxRows];   // [part][row]; by row
     __shared__ Cursor s_start[2 * kSlots];
-    __shared__ int2 s_head;
+    __shared__ JoinedHead s_head;
     __shared__ int s_abort;
     volatile int* abort_flag = &s_abort;
 
@@ -611,20 +611,13 @@ __global__ void __launch_bounds__(Config<D, NT>::THREADS, 1) cache4_attn_kernel(
     if (warp == 0 && lane < teams) s_start[lane] = start_of(lane);
     // All tiles of the CTA's share are one head's: its teams' parts are joined here, and one is left.
     if (tid == 32) {
-        int2 head = make_int2(-1, 0);
-        if (!by_head && me < ctas) {
-            const int from = deal.from(me * teams), to = deal.from((me + 1) * teams);
-            int b, rem;
-            all.find(a, from, b, rem);
-            const PagedSeq q(a, b);
-            const int first = from - rem % max(q.span(), 1);
-            if (from < first + q.tiles && joins(a.lg_teams, from, to, first, q.span())) head = make_int2(first, q.tiles);
-        }
+        JoinedHead head{-1, 0};
+        if (!by_head && me < ctas) head = joined_head(a, deal, me, [&](int x, int& b, int& rem) { all.find(a, x, b, rem); });
         s_head = head;
     }
     __syncthreads();
-    const bool joined = s_head.x >= 0;
-    const int head_place = s_head.x, head_tiles = s_head.y;   // of its first tile; its tiles
+    const bool joined = s_head.first >= 0;
+    const int head_place = s_head.first, head_tiles = s_head.tiles;   // of its first tile; its tiles
     if constexpr (!C::ALONE) {
         if (warp >= C::WARPS) {
             asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCopyRegs));

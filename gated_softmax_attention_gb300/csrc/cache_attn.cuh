@@ -1,16 +1,15 @@
 // cache_attn.cuh -- what the attention kernels over a cache of few bits (8 bits,
-// one piece per sequence; 4 bits, in pages) have in common: how the tiles of all
-// sequences and K/V heads are dealt to teams of warps, how the parts of a head that
-// several teams share are merged, and the gate at the end. Not part of the public ABI.
+// one piece per sequence; 4 bits, in pages) have in common: the walk of a team through
+// its tiles, how the parts of a head that several teams share are merged, and the gate at
+// the end. (How tiles are dealt: cache_deal.h.) Not part of the public ABI.
 //
 // A kernel's arguments A have the members used here and
 //   A::Seq(a, b)   sequence b: n (new tokens), T (tokens in all, 0 without new ones), tiles, span()
 //   by_head(longest, N)   whether heads of at most so many tiles, N places in all, are better one CTA's each
 //   token(b, i)    the row of Q, X and O that holds new token i of sequence b
 //   tokens()       all rows
-//   kJoins         a CTA whose share is all of one head leaves one part
-//   kSwitch        most places after a head without a tile
 #pragma once
+#include "cache_deal.h"
 #include "ops_internal.h"
 
 #include <cuda_fp16.h>
@@ -46,20 +45,6 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 // 1 / (1 + e^-x), accurate to a few units of float32's last place.
 __device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
 
-// Places of a head in the sequence of all tiles: after its tiles come some without
-// one. A team that goes on to another head stores what it has, reads other
-// queries and has, at a sequence's end, an open block of twice the bytes, which
-// even shares of the tiles alone do not show: of 1216 teams with 11 tiles each of
-// 24 sequences of up to 32767 tokens, the 48 that went on ended 5 us after the
-// others. (Measured, 8 bits, with 2, 4, 6 and 8 places: that 52.2, 50.4, 50.9, 51.5 us, up
-// to 5000 tokens 19.3, 17.7, 17.5, 17.9; 64 x 200 tokens, heads of 4 tiles, 18.4,
-// 21.0, 20.3, 20.1. 4 bits, where a team is one warp that ends a head without a barrier and
-// takes longer for a tile, with 0, 1, 2, 4 and 6: 200 sequences of up to 1500 tokens 69.6, 66.5, 69.6,
-// 72.1, 71.3 us; 24 of up to 32767 47.8, 46.5, 46.8, 46.5, 47.2; 64 x 8192 with the gate 132.1, 134, 134.5,
-// 134, 138; 7 of up to 4099, 5 rows, 16.7, 16.5, 16.4, 16.1, 16.1.)
-template <class A>
-__device__ __forceinline__ int span_of(int tiles) { return tiles + min(A::kSwitch, tiles / 2); }
-
 // A place in the sequence of all tiles. (Where places are left a sequence with
 // tiles follows; lengths that change during the call, which they must not, end
 // the walk instead of leading it out of the batch.)
@@ -81,18 +66,6 @@ struct Cursor {
                 tiles = typename A::Seq(a, b).tiles;
             } while (tiles == 0);
         }
-    }
-};
-
-// n things dealt to k takers in order, each as many as the next or one more:
-// where a taker's share begins, and whose share holds thing x.
-struct Deal {
-    int each, more;
-    __device__ __forceinline__ Deal(int n, int k) : each(n / k), more(n % k) {}
-    __device__ __forceinline__ int from(int c) const { return c * each + min(c, more); }
-    __device__ __forceinline__ int taker(int x) const {
-        const int fat = more * (each + 1);
-        return x < fat ? x / (each + 1) : more + (x - fat) / each;
     }
 };
 
@@ -249,45 +222,11 @@ struct Sums {
     }
 };
 
-// Where team n leaves its rows of the cut head whose first tile is u0: the first
-// head of its share, or the last.
+// Where team n leaves its rows of the cut head whose first tile is u0.
 template <int D, class A>
 __device__ __forceinline__ float* part_of(const A& a, const Deal& deal, int n, int u0) {
-    return a.part + (long long)(2 * n + (u0 <= deal.from(n) ? 0 : 1)) * a.rows * (D + 4);
+    return a.part + (long long)part_index(deal, n, u0) * a.rows * (D + 4);
 }
-
-// Whether the places [from, to) of a CTA, the first of them a tile, are all of the head
-// at [u0, u0 + span): its teams' parts are then joined and left as one, its first team's. (Not of a
-// single team: it may have the whole head.)
-__device__ __forceinline__ bool joins(int lg_teams, int from, int to, int u0, int span) {
-    return lg_teams > 0 && from >= u0 && to <= u0 + span;
-}
-
-// The parts of a cut head that teams first .. last have tiles of: one each, or one of a
-// CTA whose teams' are joined (any CTA but those of the first and the last team, and maybe these).
-template <class A>
-struct Parts {
-    int n;             // how many
-    int n0, lead, mid, lg;   // first team; parts of its CTA; CTAs between that and the last team's
-    __device__ __forceinline__ Parts(const A& a, const Deal& deal, int first, int last, int u0, int span) : n0(first) {
-        n = last - first + 1;
-        if constexpr (A::kJoins) {
-            lg = a.lg_teams;
-            const int c0 = first >> lg, c1 = last >> lg;
-            const auto joined = [&](int c) { return joins(lg, deal.from(c << lg), deal.from((c + 1) << lg), u0, span); };
-            lead = joined(c0) ? 1 : min(last, ((c0 + 1) << lg) - 1) - first + 1;
-            mid = max(c1 - c0 - 1, 0);
-            n = lead + mid + (c1 == c0 ? 0 : (joined(c1) ? 1 : last - (c1 << lg) + 1));
-        }
-    }
-    __device__ __forceinline__ int team(int k) const {
-        if constexpr (A::kJoins) {
-            const int c0 = n0 >> lg;
-            if (k >= lead) return k < lead + mid ? (c0 + 1 + k - lead) << lg : ((c0 + 1 + mid) << lg) + (k - lead - mid);
-        }
-        return n0 + k;
-    }
-};
 
 // The sequence of all tiles: sequence after sequence, in each one K/V head after
 // the other. (Its scan in four warps: in all twenty of a block it took 0.6 us more.)

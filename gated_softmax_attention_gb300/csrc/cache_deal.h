@@ -53,9 +53,10 @@ struct Deal {
 // head of its share, or of the last.
 GSDPA_DEAL int part_index(const Deal& deal, int n, int u0) { return 2 * n + (u0 <= deal.from(n) ? 0 : 1); }
 
-// Whether the places [from, to) of a CTA, the first of them a tile, are all of the head
-// at [u0, u0 + span): its teams' parts are then joined and left as one, its first team's. (Not of a
-// single team: it may have the whole head.)
+// Whether the places [from, to) of a CTA, the first of them a tile, are all of the cut head
+// at [u0, u0 + span): its teams' parts are then joined and left as one, its first team's. (Asked of cut
+// heads only. One that a team has whole that team finishes, and the merge does not look at it, though
+// the CTA's other teams may have nothing but the head's last place, which is no tile, or nothing at all.)
 GSDPA_DEAL bool joins(int lg_teams, int from, int to, int u0, int span) {
     return lg_teams > 0 && from >= u0 && to <= u0 + span;
 }
@@ -72,7 +73,8 @@ GSDPA_DEAL JoinedHead joined_head(const A& a, const Deal& deal, int c, Find find
     find(from, b, rem);
     const typename A::Seq q(a, b);
     const int first = from - rem % greater(q.span(), 1);
-    if (from < first + q.tiles && joins(a.lg_teams, from, to, first, q.span())) return {first, q.tiles};
+    const bool cut = q.tiles > 0 && deal.taker(first) < deal.taker(first + q.tiles - 1);
+    if (cut && from < first + q.tiles && joins(a.lg_teams, from, to, first, q.span())) return {first, q.tiles};
     return {-1, 0};
 }
 

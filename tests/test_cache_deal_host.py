@@ -158,3 +158,32 @@ def test_long_requests_are_finished_once(go_through, lg):
         tiles = [r.choice([0, 40, 64, 200, r.randint(40, 600)]) for _ in range(B)]
         if any(tiles):
             assert go_through(tiles, H, lg, 152) == (0, -1), (tiles, H)
+
+
+@pytest.mark.parametrize("lg", TEAMS)
+@pytest.mark.parametrize("H", [1, 2, 3, 5, 8])
+def test_a_head_that_one_team_has_whole(go_through, H, lg):
+    # two tiles beside a long request: with two teams the first may have both, and the second only the place after them
+    for tiles in ([2, 17], [17, 2], [2, 17, 2], [1, 9], [3, 31]):
+        assert go_through(tiles, H, lg, 152) == (0, -1), tiles
+    # a single tile among more requests than there are blocks of threads
+    for B in (153, 200, 256, 1000):
+        for at in (0, 100, B - 1):
+            for n in (1, 2, 3):
+                tiles = [0] * B
+                tiles[at] = n
+                assert go_through(tiles, H, lg, 152) == (0, -1), (B, at, n)
+    # as many requests of two tiles as there are blocks of threads, and some more
+    for B in range(140, 200):
+        assert go_through([2] * B, H, lg, 148) == (0, -1), B
+
+
+@pytest.mark.parametrize("lg", TEAMS)
+def test_any_batch_is_finished_once(go_through, lg):
+    r = random.Random(100 + lg)
+    for _ in range(1000):
+        B = r.choice([r.randint(1, 8), r.randint(1, 8), r.randint(9, 200)])
+        H = r.randint(1, 8)
+        tiles = [r.choice([0, 1, 2, 2, 3, 4, 5, r.randint(1, 40)]) for _ in range(B)]
+        if any(tiles):
+            assert go_through(tiles, H, lg, r.choice([148, 152])) == (0, -1), (tiles, H)

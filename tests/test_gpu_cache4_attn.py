@@ -178,6 +178,28 @@ def test_blocks_of_threads_within_one_head_and_across_two(T, kind):
 
 
 @pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("first", [65, 100, 128])
+@pytest.mark.parametrize("H", [1, 3, 5])
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_head_of_two_pages_that_one_team_has_whole(d, H, first, kind):
+    # 64 rows, two teams to a block of threads: the first has both pages of a head, the second only the place after them
+    for T in ([first, 1088], [1088, first], [first, 1088, first, 0, first, first]):
+        cache, table = filled(T, H, d, kind, 56)
+        run(cache, table, T, [min(8, t) for t in T], 8, "none", 57)
+
+
+@pytest.mark.parametrize("G,most", [(4, 1), (8, 1), (12, 1), (8, 3), (8, 8), (16, 8)])
+@pytest.mark.parametrize("T", [5, 64, 65, 200])
+def test_one_live_request_among_more_than_there_are_blocks(T, G, most):
+    # a captured step with room for many requests, in which one has rows
+    for B, at in ((256, 100), (200, 0), (153, 152)):
+        lengths = [T if b == at else 0 for b in range(B)]
+        new = [min(most, T) if b == at else 0 for b in range(B)]
+        cache, table = filled(lengths, 1, 64, "int4", 58, width=4)
+        run(cache, table, lengths, new, G, "none", 59, most=most, more=2)
+
+
+@pytest.mark.parametrize("kind", KINDS)
 def test_long_requests_beside_short_ones(kind):
     T = [20000, 3, 64 * 100, 1, 777]
     cache, table = filled(T, 2, 128, kind, 12)

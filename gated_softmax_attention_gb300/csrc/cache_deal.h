@@ -69,6 +69,7 @@ struct JoinedHead {
 template <class A, class Find>
 GSDPA_DEAL JoinedHead joined_head(const A& a, const Deal& deal, int c, Find find) {
     const int from = deal.from(c << a.lg_teams), to = deal.from((c + 1) << a.lg_teams);
+    if (from >= to) return {-1, 0};   // (no tile at all: place 0 is no request's)
     int b, rem;
     find(from, b, rem);
     const typename A::Seq q(a, b);

@@ -187,3 +187,9 @@ def test_any_batch_is_finished_once(go_through, lg):
         tiles = [r.choice([0, 1, 2, 2, 3, 4, 5, r.randint(1, 40)]) for _ in range(B)]
         if any(tiles):
             assert go_through(tiles, H, lg, r.choice([148, 152])) == (0, -1), (tiles, H)
+
+
+@pytest.mark.parametrize("lg", TEAMS)
+def test_nothing_is_looked_up_where_no_request_has_rows(go_through, lg):
+    for B, H in ((1, 1), (64, 8), (200, 1), (8192, 8)):
+        assert go_through([0] * B, H, lg, 152, width=4) == (0, -1), (B, H)

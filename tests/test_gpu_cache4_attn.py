@@ -199,6 +199,29 @@ def test_one_live_request_among_more_than_there_are_blocks(T, G, most):
         run(cache, table, lengths, new, G, "none", 59, most=most, more=2)
 
 
+@pytest.mark.parametrize("G,most", [(4, 1), (8, 1), (12, 1), (8, 3), (8, 8)])
+@pytest.mark.parametrize("B,H", [(64, 8), (200, 1), (300, 2)])
+def test_a_step_in_which_no_request_has_rows(B, H, G, most):
+    # nothing granted, or nothing brought, with more heads than blocks of threads: rows are zero, nothing is left in
+    # the workspace, and what lies behind the arrays (numbers that a longer batch would have) is not taken for requests
+    width, n_rows, behind = 40, B * most, 9000
+    cache = gb.cache4_alloc(50, H, 64, "e2m1")
+    cache.pool.zero_()
+    Q = randn(62, n_rows, H * G, 64)
+    table = torch.zeros(behind, width, dtype=torch.int32, device="cuda")
+    lens, granted = ints([64 * b % 2000 + 5 for b in range(behind)]), ints([most] * behind)
+    granted[:B] = 0
+    full = torch.arange(behind, dtype=torch.int32, device="cuda") * most
+    none = full - full[B]
+    none[:B] = 0
+    need = gb.cache4_workspace_bytes(cache, B, width, n_rows, most, H * G, gate="none")
+    for cu, new in ((full, granted), (none, None)):
+        workspace, O = torch.full((need,), 0x5A, dtype=torch.uint8, device="cuda"), torch.full_like(Q, 7.0)
+        gb.gated_sdpa_cache4(None, Q, cache, table[:B], lens[:B], cu[:B + 1], gate="none", max_new=most,
+                             n_new=None if new is None else new[:B], out=O, workspace=workspace)
+        assert not bool(O.any()) and bool((workspace == 0x5A).all())
+
+
 @pytest.mark.parametrize("kind", KINDS)
 def test_long_requests_beside_short_ones(kind):
     T = [20000, 3, 64 * 100, 1, 777]

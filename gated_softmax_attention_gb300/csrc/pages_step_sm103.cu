@@ -173,7 +173,9 @@ __global__ void __launch_bounds__(THREADS) pages_plan_kernel(const __grid_consta
     for (int k = tid; k < back; k += THREADS) {
         const int b = owner(s_free, B - 1, k);   // (requests that give back none share their sum with the next)
         const Request r(a, b);
-        a.free_pages[held + k] = a.table[(long long)b * a.width + pages_of(r.kept) + (k - s_free[b])];
+        const int page = a.table[(long long)b * a.width + pages_of(r.kept) + (k - s_free[b])];
+        bad = bad || page < 0 || page >= a.n_pages;
+        a.free_pages[held + k] = page;
     }
     const int top = held + back;
     // ---- who gets what: the needs are served in order as long as they fit

@@ -569,7 +569,8 @@ typedef struct {
  * (negative, keep > lens, more than 64 max_pages tokens, rows past n_rows) is left as
  * it was, with granted 0 (a negative n_new has no rows), and the next
  * gsdpa_check_device_error returns GSDPA_ERR_CACHE_RANGE; so does a page number
- * outside the pool, whose tokens get slot -1. B <= 8192 (GSDPA_ERR_UNSUPPORTED
+ * outside the pool, whose tokens get slot -1 (one that is given back is reported then, and
+ * goes on the stack as it is). B <= 8192 (GSDPA_ERR_UNSUPPORTED
  * otherwise). Repeated on the same contents it gives the same result, bit for bit.
  * Asynchronous on `stream`; sm_103 device; no workspace.
  */

@@ -164,6 +164,22 @@ def test_pages_out_of_range_give_no_slot():
     assert step.n_free.tolist() == [3]
 
 
+@pytest.mark.parametrize("page", [-1, 10, 2 ** 31 - 1, -2 ** 31])
+@pytest.mark.parametrize("B", [2, 300, 1100])
+def test_a_page_out_of_range_that_is_given_back_is_reported(B, page):
+    # by the step that puts it on the stack, whether it is taken again in it or not; where it stays, nothing is said
+    for new, kept in ((0, 64), (1, 64), (0, 65)):
+        t, stack = ints([[5, page, 0], [6, 0, 0]] + [[0, 0, 0]] * (B - 2)), ints([1, 2, 3] + [0] * 7)
+        lens, keep, more = [100, 3] + [0] * (B - 2), [kept, 3] + [0] * (B - 2), [0, 61 + new] + [0] * (B - 2)
+        step = gb.pages_step(ints(lens), ints(more), t, stack, ints([3]), sum(more), keep=ints(keep))
+        given_back = kept == 64
+        assert gb.check_device_error() == (gb.ERR_CACHE_RANGE if given_back else gb.OK)
+        assert stack.tolist()[:4] == ([1, 2, 3, page] if given_back else [1, 2, 3, 0])
+        assert step.granted.tolist()[:2] == [0, 61 + new] and step.n_free.tolist() == [3 + given_back - new]
+        if new:
+            assert t.tolist()[1][1] == page and step.slots.tolist()[-1] == -1
+
+
 def test_many_steps_keep_every_page_once():
     # a serving run: requests come, grow, are cut back and end; no page is ever two requests' or lost
     r = random.Random(11)

@@ -426,7 +426,7 @@ __device__ __forceinline__ float row_to_f16(uint32_t (&w)[D / 16][2], int t, uin
         off[0] = D == 128 || t < 2 ? hi : lo;
         off[1] = D == 128 ? lo : 0u;
     }
-    return __uint_as_float((e - 14u) << 23) * (E2M1 ? 1.f : 16777216.f);
+    return __uint_as_float((e - 14u) << 23);
 }
 
 // The finished rows of a head that a warp has alone: element 2 x + e of o[i] is column
@@ -749,7 +749,8 @@ __global__ void __launch_bounds__(Config<D, NT>::THREADS, 1) cache4_attn_kernel(
         if (blockIdx.x == 0) clear_rows(0, row_at(0));
         if (blockIdx.x == gridDim.x - 1) clear_rows(row_at(a.B), a.N);
         RowState<D, NT> st;
-        const float unscaled = kLog2e * rsqrtf((float)D) * a.k_up;
+        // (int4's codes count 2^-24: with k_up, because that alone may leave float32's range after a large query's factor)
+        const float unscaled = kLog2e * rsqrtf((float)D) * (a.k_up * (E2M1 ? 1.f : 16777216.f));
         while (at.left > 0) {
             const PagedSeq q(a, at.b);
             const int j1 = min(at.tiles, at.j + at.left);   // segment: tiles [at.j, j1) of the head

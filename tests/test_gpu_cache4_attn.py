@@ -8,7 +8,7 @@ import torch
 
 from gated_softmax_attention_gb300 import binding as gb
 from gated_softmax_attention_gb300 import build as gbuild
-from cache4_ref import PAGE, check_attention, pages_of
+from cache4_ref import PAGE, check_attention, codes_and_scales, held, pages_of
 
 pytestmark = pytest.mark.gpu
 KINDS = ["int4", "e2m1"]
@@ -301,6 +301,42 @@ def test_large_scores_and_queries(kind):
     Q[1] = 2.0 ** -130
     O = gb.gated_sdpa_cache4(None, Q, cache, table, ints([299] * 3), ints([0, 1, 2, 3]), gate="none")
     assert bool(O.isfinite().all())
+
+
+def check_one_token_has_all(cache, table, T, Q, O):
+    """Scores so far apart that each row is its largest score's token: its values, which bf16 holds, to the last bit. Rows
+    whose two largest scores are nearer to each other than the kernel's sums (see check_attention) may be off are left out."""
+    d, G = cache.d_k, Q.shape[1] // cache.H_kv
+    pos = torch.arange(T, device="cuda")
+    k, v = held(cache, table[0].long()[pos // PAGE] * PAGE + pos % PAGE)
+    _, _, ks, _ = codes_and_scales(cache.pool, table[0].long()[pos // PAGE] * PAGE + pos % PAGE, cache.kind)
+    wide = k.abs() + (16 * ks.repeat_interleave(16, -1) * 2.0 ** cache.k_exp if cache.kind == "int4" else 0.0)
+    k, v, wide = (x.repeat_interleave(G, 1) for x in (k, v, wide))                 # [T, Hq, d]
+    scores, off = torch.einsum("hd,thd->ht", Q[0].double(), k), torch.einsum("hd,thd->ht", Q[0].double().abs(), wide).amax(-1)
+    top = scores.topk(2, -1)
+    sure = top.values[:, 0] - top.values[:, 1] > 2 * 2 * d * 2.0 ** -23 * off
+    assert int(sure.sum()) * 2 > len(sure)
+    want = v[top.indices[:, 0], torch.arange(len(sure), device="cuda")]
+    assert torch.equal(O[0].double()[sure], want[sure]), (O[0].double() - want)[sure].abs().max()
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("G", [4, 8, 12])
+@pytest.mark.parametrize("d", [64, 128])
+def test_queries_as_large_as_keys_are_small(d, G, kind):
+    # products of 2^120 and 2^-64: scores are ordinary numbers, those of zero keys zero
+    T, H = 300, 2
+    cache, table = filled([T], H, d, kind, 80, exp=0)
+    small = gb.Cache4(cache.pool, kind, k_exp=-64)
+    for exp in (117, 118, 120, 124):
+        Q = (randn(81, 1, H * G, d).double().clamp(-2, 2) * 2.0 ** exp).bfloat16()
+        O = gb.gated_sdpa_cache4(None, Q, small, table, ints([T - 1]), ints([0, 1]), gate="none")
+        check_one_token_has_all(small, table, T, Q, O)
+    pos = torch.arange(T, device="cuda")
+    slots = table[0].long()[pos // PAGE] * PAGE + pos % PAGE
+    gb.cache4_append(cache, torch.zeros(T, H, d, dtype=torch.bfloat16, device="cuda"), randn(82, T, H, d), slots)
+    O = gb.gated_sdpa_cache4(None, Q, small, table, ints([T - 1]), ints([0, 1]), gate="none")
+    check_attention(O, None, Q, small, table, [T - 1], [1], [0, 1], None, "none")
 
 
 @pytest.mark.parametrize("kind", KINDS)

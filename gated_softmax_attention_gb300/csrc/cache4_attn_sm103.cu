@@ -397,7 +397,9 @@ __device__ __forceinline__ float row_to_f16(uint32_t (&w)[D / 16][2], int t, uin
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
     if (HALF) top = max(top, __shfl_xor_sync(0xffffffffu, top, 16));   // (the row's other products)
-    const uint32_t e = min(max(top >> 7, 15u), 252u);   // the largest element's exponent field, so that both factors are
+    // The largest element's exponent field; not below 15, so that the factor which undoes the scale is a number. (Up to
+    // 254, bf16's largest, and 255, infinity and NaN, which stay what they are, both factors are.)
+    const uint32_t e = max(top >> 7, 15u);
     const float scale = __uint_as_float((268u - e) << 23);
     float mine[2] = {0.f, 0.f};
 #pragma unroll

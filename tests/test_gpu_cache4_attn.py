@@ -340,6 +340,21 @@ def test_queries_as_large_as_keys_are_small(d, G, kind):
 
 
 @pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("G", [4, 8, 12])
+@pytest.mark.parametrize("top", [2.0 ** 126, 2.0 ** 127, 1.984375 * 2.0 ** 127, 3.3895313892515355e38])
+def test_the_largest_queries(top, G, kind):
+    # up to bf16's largest number
+    T, H, d = 300, 2, 64
+    cache, table = filled([T], H, d, kind, 83, exp=0)
+    small = gb.Cache4(cache.pool, kind, k_exp=-64)
+    Q = randn(84, 1, H * G, d).double()
+    Q = (Q / Q.abs().amax(-1, keepdim=True) * top).bfloat16()
+    assert bool(Q.isfinite().all())
+    O = gb.gated_sdpa_cache4(None, Q, small, table, ints([T - 1]), ints([0, 1]), gate="none")
+    check_one_token_has_all(small, table, T, Q, O)
+
+
+@pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("k_exp,v_exp", [(-64, 64), (64, -64), (-30, 3), (10, -20)])
 def test_exponents(k_exp, v_exp, kind):
     T, H, d, G = [200, 70], 2, 64, 4

@@ -66,6 +66,12 @@ constexpr int kWholeTiles = 4;
 constexpr int kRegs = 232, kCopyRegs = 40;       // of a thread where a warp copies for the others: see Config
 constexpr float kUp = 13.0f, kMove = 2.0f;     // where m stands, and how far a tile may exceed it: see above
 
+// The largest factor from a row's sums to its scores. A row's scaled elements are below 2^15, so its sums are below
+// 2^33.4 (int4, in units of 2^-24: 2^9.6): times this factor they are numbers. Two sums that differ do so by
+// 2^-34 at least (2^-57), which is 2^59 and more in scores: under a larger factor, too, the largest has all the weight.
+template <bool E2M1>
+constexpr float kMostFactor = E2M1 ? 0x1p93f : 0x1p117f;
+
 struct PagedSeq;
 struct Cache4Args {
     using Seq = PagedSeq;
@@ -760,7 +766,7 @@ __global__ void __launch_bounds__(Config<D, NT>::THREADS, 1) cache4_attn_kernel(
             uint32_t off[NT][2];
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                const float back = row_to_f16<D, E2M1, HALF>(qf[n], t, off[n]) * unscaled;
+                const float back = fminf(row_to_f16<D, E2M1, HALF>(qf[n], t, off[n]) * unscaled, kMostFactor<E2M1>);
 #pragma unroll
                 for (int e = 0; e < 2; ++e) f[n][e] = __shfl_sync(0xffffffffu, back, 4 * (2 * (HALF ? t & 1 : t) + e));
             }

@@ -355,6 +355,29 @@ def test_the_largest_queries(top, G, kind):
 
 
 @pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("G", [4, 8, 12])
+@pytest.mark.parametrize("exp,k_exp", [(59, 64), (70, 64), (120, 64), (124, 0), (100, 30)])
+def test_scores_past_float32(exp, k_exp, G, kind):
+    # on both sides of zero, and all of them below it; zero keys beside them
+    T, H, d = 300, 2, 128
+    cache, table = filled([T], H, d, kind, 85, exp=0)
+    large = gb.Cache4(cache.pool, kind, k_exp=k_exp)
+    call = lambda Q: gb.gated_sdpa_cache4(None, Q, large, table, ints([T - 1]), ints([0, 1]), gate="none")  # noqa: E731
+    Q = (randn(86, 1, H * G, d).double().clamp(-3.5, 3.5) * 2.0 ** exp).bfloat16()
+    check_one_token_has_all(large, table, T, Q, call(Q))
+    pos = torch.arange(T, device="cuda")
+    slots = table[0].long()[pos // PAGE] * PAGE + pos % PAGE
+    K, V = -randn(87, T, H, d).abs() * 100, randn(88, T, H, d)
+    gb.cache4_append(cache, K, V, slots)
+    check_one_token_has_all(large, table, T, Q.abs(), call(Q.abs()))
+    K[7] = 0
+    gb.cache4_append(cache, K, V, slots)
+    check_one_token_has_all(large, table, T, Q.abs(), call(Q.abs()))
+    gb.cache4_append(cache, torch.zeros_like(K), V, slots)
+    check_attention(call(Q), None, Q, large, table, [T - 1], [1], [0, 1], None, "none")
+
+
+@pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("k_exp,v_exp", [(-64, 64), (64, -64), (-30, 3), (10, -20)])
 def test_exponents(k_exp, v_exp, kind):
     T, H, d, G = [200, 70], 2, 64, 4

@@ -74,7 +74,8 @@ GSDPA_DEAL JoinedHead joined_head(const A& a, const Deal& deal, int c, Find find
     find(from, b, rem);
     const typename A::Seq q(a, b);
     const int first = from - rem % greater(q.span(), 1);
-    const bool cut = q.tiles > 0 && deal.taker(first) < deal.taker(first + q.tiles - 1);
+    // (cut: tiles before the CTA's share, or more of them than its first team has)
+    const bool cut = first < from || q.tiles > deal.from((c << a.lg_teams) + 1) - from;
     if (cut && from < first + q.tiles && joins(a.lg_teams, from, to, first, q.span())) return {first, q.tiles};
     return {-1, 0};
 }

@@ -16,19 +16,17 @@
 //         neighbouring columns, the contraction's axis, and done; for values the axis is the
 //         tokens, and so that a token has whole bytes (the append writes them alone)
 //         the two tokens' halves of two bytes change places first, four operations a word.
-//   int4  code + 8 as the low bits of a subnormal fp16 number, u 2^-24 or, the next
-//         4 bits, u 2^-20: one AND each and a shift for every two, exact. The 8
-//         comes off in the sums, by one more product of 16 tokens: the keys' start with
-//         their scales times -8 sum q, the values' have one with the constant -8 for
-//         each 16 columns. (mma takes subnormal operands
-//         as they are: measured, products exact.) The factor 16 between the two is in q
-//         for the keys, in the result's columns for the values.
+//   int4  code + 8 as the low bits of the fp16 number 1024 or, the next 4 bits, 16 (code + 8): one LOP3 each and a
+//         shift for every two, then 1032 or 72 taken off by a multiply-add on a pipe that has room, exact. (As subnormal
+//         numbers, without the second step and with the 8 taken off in the sums by one more product, the sums were
+//         not float32's: products are lined up by the exponent that an operand has in name, and beside one of a subnormal 8,
+//         which a code of zero was too, all under 2^-18 of it was lost; measured, with ordinary operands 2^-23.)
 // A key's scale multiplies the sum over its 16 columns in float32, one product's
 // depth. A value's multiplies the weights, in fp16, whose pairs are the same for all 16
 // columns: 2 instructions for 256 codes instead of 8.
 //
 // q, a bf16 row scaled by a power of two to below 2^15, is exact in fp16 (elements
-// under 2^-27 of the row's largest lose bits that weigh less than 2^-35 of it). The
+// under 2^-31 of the row's largest lose bits that weigh less than 2^-39 of it). The
 // weights p 2^-m are rounded to fp16, and again where they take the value scale. fp16's
 // range is short, so they use all of it: m follows the row's largest score plus ev, ev
 // the exponent of the page's largest value scale where that is above 1 (0 .. 9), and stands
@@ -40,12 +38,12 @@
 // merged by a second kernel, as for the 8-bit cache (cache_attn.cuh).
 //
 // Measured (32 query heads, 8 K/V heads of 128, 64 x 8192 tokens, 604 MB, no gate): e2m1 118 us, 5.1 TB/s, int4
-// 121 us, heads of 64 71 and 76 us. Of the 118 the copies alone take 102 and the products
+// 117 us, heads of 64 71 and 70 us. Of the 118 the copies alone take 102 and the products
 // alone 102 (integer pipe 68 % busy, two thirds of the issue slots): neither hides behind the other wholly. What
 // brought it there: up to 8 rows every warp is a team of its own and copies for itself, a
 // page at a time, into one buffer, where the one before has just been used (the other 15 warps are work enough
-// meanwhile; keys' and values' halves in a ring of three 121 us, int4 125, in two buffers of their own 119, 123), in heads of 64 three
-// pages ahead (by halves 81 us; a copying warp and eight teams of two warps 133, 140 int4,
+// meanwhile; keys' and values' halves in a ring of three 121 us, in two buffers of their own 119), in heads of 64 three
+// pages ahead (by halves 81 us; a copying warp and eight teams of two warps 133,
 // 95 in heads of 64); up to 4 rows both halves of the narrow side are in use (HALF: 127 without).
 // Beyond 8 rows the codes are converted again for every 16: 16 x 8000 tokens, 22 us of bytes, 16, 32 and 64 rows
 // 55, 90 and 161 us (58, 96, 173 by halves of a page; a page converted once for its team, in shared memory, with rows on the
@@ -67,10 +65,9 @@ constexpr int kRegs = 232, kCopyRegs = 40;       // of a thread where a warp cop
 constexpr float kUp = 13.0f, kMove = 2.0f;     // where m stands, and how far a tile may exceed it: see above
 
 // The largest factor from a row's sums to its scores. A row's scaled elements are below 2^15, so its sums are below
-// 2^33.4 (int4, in units of 2^-24: 2^9.6): times this factor they are numbers. Two sums that differ do so by
-// 2^-34 at least (2^-57), which is 2^59 and more in scores: under a larger factor, too, the largest has all the weight.
-template <bool E2M1>
-constexpr float kMostFactor = E2M1 ? 0x1p93f : 0x1p117f;
+// 2^33.6: times this factor they are numbers. Two sums that differ do so by 2^-34 at least, which is 2^59
+// in scores: under a larger factor, too, the largest has all the weight.
+constexpr float kMostFactor = 0x1p93f;
 
 struct PagedSeq;
 struct Cache4Args {
@@ -127,8 +124,7 @@ struct PagedSeq {
     __device__ __forceinline__ int span() const { return span_of<Cache4Args>(tiles); }
 };
 
-// A word of eight codes -> four fp16 pairs: pair p from bits 4 p .. and 16 + 4 p .. (int4:
-// (code + 8) 2^-24 for p even, 2^-20 for p odd), or from byte p (e2m1).
+// A word of eight codes -> four fp16 pairs: pair p from bits 4 p .. and 16 + 4 p .. (int4), or from byte p (e2m1).
 template <bool E2M1>
 __device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t (&x)[4]) {
     if constexpr (E2M1) {
@@ -141,11 +137,16 @@ __device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t (&x)[4]) {
             : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
             : "r"(w));
     } else {
+        const __half2 off = __half2half2(__ushort_as_half(0x6408));                                        // 1032
+        const __half2 down = __half2half2(__ushort_as_half(0x2c00)), low = __half2half2(__ushort_as_half(0xd480));   // 1/16, -72
         const uint32_t v = w >> 8;
-        x[0] = w & 0x000f000fu;
-        x[1] = w & 0x00f000f0u;
-        x[2] = v & 0x000f000fu;
-        x[3] = v & 0x00f000f0u;
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+            uint32_t a;   // 1024 | the codes: 1024 + code + 8, or 1024 + 16 (code + 8)
+            asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(a) : "r"(p < 2 ? w : v), "r"(p % 2 ? 0x00f000f0u : 0x000f000fu), "r"(0x64006400u));
+            const __half2 h = *reinterpret_cast<const __half2*>(&a), c = p % 2 ? __hfma2(h, down, low) : __hsub2(h, off);
+            x[p] = *reinterpret_cast<const uint32_t*>(&c);
+        }
     }
 }
 
@@ -188,12 +189,6 @@ __device__ __forceinline__ void scales_to_f16(uint32_t w, uint32_t& lo, uint32_t
         "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
         : "=r"(lo), "=r"(hi)
         : "r"(w));
-}
-// Two scales, a word's half.
-__device__ __forceinline__ uint32_t scale_pair(const uint8_t* from) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(*reinterpret_cast<const uint16_t*>(from)));
-    return r;
 }
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
     const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
@@ -388,13 +383,9 @@ __device__ __forceinline__ void load_row(const __nv_bfloat16* src, int t, int od
     }
 }
 
-// A bf16 row -> fp16 scaled by a power of two to below 2^15 (int4: the second pair of
-// each product by 1/16 more); returns the factor that undoes the scale. int4: off, the
-// narrow operand that gives the codes' 8, -2^-4 times the row's sums over each 16 columns,
-// as two fp16 parts (22 bits): lane t has those of groups 2 t, 2 t + 1 (d_k 64: the
-// first parts in t < 2, the second in t >= 2).
-template <int D, bool E2M1, bool HALF>
-__device__ __forceinline__ float row_to_f16(uint32_t (&w)[D / 16][2], int t, uint32_t (&off)[2]) {
+// A bf16 row -> fp16 scaled by a power of two to below 2^15; returns the factor that undoes the scale.
+template <int D, bool HALF>
+__device__ __forceinline__ float row_to_f16(uint32_t (&w)[D / 16][2]) {
     uint32_t top = 0;
 #pragma unroll
     for (int j = 0; j < D / 16; ++j)
@@ -407,33 +398,11 @@ __device__ __forceinline__ float row_to_f16(uint32_t (&w)[D / 16][2], int t, uin
     // 254, bf16's largest, and 255, infinity and NaN, which stay what they are, both factors are.)
     const uint32_t e = max(top >> 7, 15u);
     const float scale = __uint_as_float((268u - e) << 23);
-    float mine[2] = {0.f, 0.f};
 #pragma unroll
-    for (int j = 0; j < D / 16; ++j) {
-        float sum = 0.f;
+    for (int j = 0; j < D / 16; ++j)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const uint32_t v = w[j][h];
-            const float k = E2M1 || h == 0 ? scale : scale * 0.0625f;
-            w[j][h] = pack_f16x2(__uint_as_float(v << 16) * k, __uint_as_float(v & 0xffff0000u) * k);
-            if (!E2M1) {
-                const float2 q = floats(w[j][h]);   // (as the products have them)
-                sum += (q.x + q.y) * (h == 0 ? 1.f : 16.f);
-            }
-        }
-        if (!E2M1) {
-            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-            if (j / 2 == (D == 128 ? t : t % 2)) mine[j % 2] = sum * -0.0625f;
-        }
-    }
-    if (!E2M1) {
-        const uint32_t hi = pack_f16x2(mine[0], mine[1]);
-        const float2 h = floats(hi);
-        const uint32_t lo = pack_f16x2(mine[0] - h.x, mine[1] - h.y);
-        off[0] = D == 128 || t < 2 ? hi : lo;
-        off[1] = D == 128 ? lo : 0u;
-    }
+        for (int h = 0; h < 2; ++h)
+            w[j][h] = pack_f16x2(__uint_as_float(w[j][h] << 16) * scale, __uint_as_float(w[j][h] & 0xffff0000u) * scale);
     return __uint_as_float((e - 14u) << 23);
 }
 
@@ -757,16 +726,14 @@ __global__ void __launch_bounds__(Config<D, NT>::THREADS, 1) cache4_attn_kernel(
         if (blockIdx.x == 0) clear_rows(0, row_at(0));
         if (blockIdx.x == gridDim.x - 1) clear_rows(row_at(a.B), a.N);
         RowState<D, NT> st;
-        // (int4's codes count 2^-24: with k_up, because that alone may leave float32's range after a large query's factor)
-        const float unscaled = kLog2e * rsqrtf((float)D) * (a.k_up * (E2M1 ? 1.f : 16777216.f));
+        const float unscaled = kLog2e * rsqrtf((float)D) * a.k_up;
         while (at.left > 0) {
             const PagedSeq q(a, at.b);
             const int j1 = min(at.tiles, at.j + at.left);   // segment: tiles [at.j, j1) of the head
             float f[NT][2];
-            uint32_t off[NT][2];
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                const float back = fminf(row_to_f16<D, E2M1, HALF>(qf[n], t, off[n]) * unscaled, kMostFactor<E2M1>);
+                const float back = fminf(row_to_f16<D, HALF>(qf[n]) * unscaled, kMostFactor);
 #pragma unroll
                 for (int e = 0; e < 2; ++e) f[n][e] = __shfl_sync(0xffffffffu, back, 4 * (2 * (HALF ? t & 1 : t) + e));
             }
@@ -793,20 +760,10 @@ __global__ void __launch_bounds__(Config<D, NT>::THREADS, 1) cache4_attn_kernel(
                     load_words(kt + key_scales_at(D) + n0 * (D / 16), xs);
                     load_words(kt + key_scales_at(D) + (n0 + 8) * (D / 16), ys);
                     float sum[NT][4];
-                    if constexpr (!E2M1) {   // the sums start at -8 times q's
-                        const uint8_t* own = kt + key_scales_at(D) + n0 * (D / 16) + 2 * (D == 128 ? t : t % 2);
-                        const uint32_t ax = scale_pair(own), ay = scale_pair(own + 8 * (D / 16)), op[4] = {ax, ay, ax, ay};
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) {
-                            mma_f16_from(sum[n], op, off[n][0], off[n][1], 0.f);
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) sum[n][e] *= 7.62939453125e-06f;   // 2^-17
-                        }
-                    }
                     const auto add = [&](int n, const float (&r)[4], float kx, float ky, bool first) {
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            sum[n][e] = E2M1 && first ? r[e] * (e < 2 ? kx : ky) : fmaf(r[e], e < 2 ? kx : ky, sum[n][e]);
+                            sum[n][e] = first ? r[e] * (e < 2 ? kx : ky) : fmaf(r[e], e < 2 ? kx : ky, sum[n][e]);
                     };
                     if constexpr (HALF) {
                         // lanes t < 2 have the even groups' sums of rows 0 .. 3, the others the odd groups'
@@ -913,10 +870,6 @@ __global__ void __launch_bounds__(Config<D, NT>::THREADS, 1) cache4_attn_kernel(
                             for (int n = 0; n < NT; ++n) {
                                 const uint32_t b0 = mul_f16x2(pf[n][0], sc[0]), b1 = mul_f16x2(pf[n][1], sc[1]);
                                 mma_f16(st.o[n][c], op, b0, b1);
-                                if (!E2M1) {
-                                    const uint32_t eight[4] = {0x80088008u, 0x80808080u, 0x80088008u, 0x80808080u};
-                                    mma_f16(st.o[n][c], eight, b0, b1);
-                                }
                             }
                         }
                     }
@@ -924,9 +877,9 @@ __global__ void __launch_bounds__(Config<D, NT>::THREADS, 1) cache4_attn_kernel(
                 release();
             }
 
-            // ---- the segment's rows: sums over the lanes, and the codes' units out of the outputs
+            // ---- the segment's rows: sums over the lanes, and the values' unit into the outputs
             const bool whole = at.j == 0 && j1 == at.tiles && !joined, final = at.left <= span_of<Cache4Args>(at.tiles) - at.j;
-            const float unit = exp2f(a.v_exp + (E2M1 ? 0.f : 24.f));
+            const float unit = exp2f(a.v_exp);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 float k[2];
@@ -943,7 +896,7 @@ __global__ void __launch_bounds__(Config<D, NT>::THREADS, 1) cache4_attn_kernel(
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) st.o[n][i][e] *= E2M1 || e < 2 ? k[e & 1] : k[e & 1] * 0.0625f;
+                    for (int e = 0; e < 4; ++e) st.o[n][i][e] *= k[e & 1];
             }
             const auto put = [&](float* base) {
 #pragma unroll

@@ -121,18 +121,18 @@ def quantise(x, kind, exp):
 
 
 # ---------------------------------------------------------------- the attention, to the kernel's bound
-def check_attention(O, X, Q, cache, table, lens, new, cu, W, gate, requests=None):
+def check_attention(O, X, Q, cache, table, lens, new, cu, W, gate, requests=None, more=16.0):
     """Every row against the formula in 64 bits, on the cache's own bytes. With A the sum of weights times |v|:
-    a score's 16-column sums are those of exact products, in float32 (int4: of codes + 8, with -8 taken off, 16 more in
-    magnitude than the code), and so is their sum over the groups: d additions of 2^-23 of the sum of |q_c| (|code| + 16)
-    scale. A weight is rounded to fp16 twice, 2^-11 each, and nothing is finer than 2^-38 W (see the header). The sums of
-    weights and values are float32 too, over T / 16 products of 16 tokens (int4: as many again), 2^-23 of the running
+    a score's 16-column sums are those of exact products, in float32, and so is their sum over the groups: d additions of
+    2^-23 of the sum of |q_c| (|code| + more) scale; more, of int4 alone, is room for a kernel that sums codes + 8 and
+    takes 8 off: 0 where the codes are summed. A weight is rounded to fp16 twice, 2^-11 each, and nothing is finer than 2^-38 W (see the header). The sums of
+    weights and values are float32 too, over T / 16 products of 16 tokens (with more as many again), 2^-23 of the running
     sum each; 2^-16 covers the exponentials (2 ulp of an argument below 2^7 in magnitude), sums of weights and the
     gate's sigmoid. Then the output is rounded to bf16."""
     d, H = cache.d_k, cache.H_kv
     Hq = Q.shape[1]
     G = Hq // H
-    more = 16.0 if cache.kind == "int4" else 0.0
+    more = more if cache.kind == "int4" else 0.0
     done = torch.zeros(len(Q), dtype=torch.bool, device=Q.device)
     for b in range(len(lens)) if requests is None else requests:
         n, T, at = new[b], lens[b] + new[b], cu[b]

@@ -290,6 +290,34 @@ def test_a_token_of_no_value_that_takes_most_of_the_weight(G, share, kind):
 
 
 @pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("G,most", [(4, 1), (8, 1), (4, 3), (8, 4), (16, 5)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_code_of_zero_takes_no_part(d, G, most, kind):
+    # keys whose codes are zero where the query is 2^14 times what it is elsewhere, and a token whose codes are zero in
+    # most columns under a scale of 256 beside values of 2^-6: neither may cost the others' sums their last bits
+    H, T = 2, [64, 65, 200]
+    cache, table = filled(T, H, d, kind, 90, exp=0)
+    N = sum(T)
+    K, V = randn(91, N, H, d), randn(92, N, H, d) * 2.0 ** -6
+    K[..., :16] *= 8
+    K[..., 0], K[..., 1] = 0, 8 * (7 if kind == "int4" else 6)
+    at = 0
+    for t in T:
+        V[at + 5], at = 0, at + t
+    for b in range(len(T)):
+        V[sum(T[:b]) + 5, :, ::16] = 256 * (7 if kind == "int4" else 6)
+    slots = torch.cat([table[b].long()[torch.arange(t, device="cuda") // PAGE] * PAGE + torch.arange(t, device="cuda") % PAGE
+                       for b, t in enumerate(T)])
+    gb.cache4_append(cache, K, V, slots)
+    new, cu, lens = [most] * 3, [most * b for b in range(4)], [t - most for t in T]
+    Q = randn(93, 3 * most, H * G, d)
+    Q[..., 2:16] *= 2.0 ** -4
+    Q[..., 0], Q[..., 1] = 2.0 ** 14, 0
+    O = gb.gated_sdpa_cache4(None, Q, cache, table, ints(lens), ints(cu), gate="none", max_new=most)
+    check_attention(O, None, Q, cache, table, lens, new, cu, None, "none", more=0.0)
+
+
+@pytest.mark.parametrize("kind", KINDS)
 def test_large_scores_and_queries(kind):
     # one token has all the weight; queries of 2^-100, 2^60 and zero
     T = [300, 300, 300]

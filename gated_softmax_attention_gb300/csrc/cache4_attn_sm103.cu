@@ -39,7 +39,7 @@
 //
 // Measured (32 query heads, 8 K/V heads of 128, 64 x 8192 tokens, 604 MB, no gate): e2m1 118 us, 5.1 TB/s, int4
 // 117 us, heads of 64 71 and 70 us. Of the 118 the copies alone take 102 and the products
-// alone 102 (integer pipe 68 % busy, two thirds of the issue slots): neither hides behind the other wholly. What
+// alone 102 (integer pipe 65 to 66 % busy, issue slots 59 %): neither hides behind the other wholly. What
 // brought it there: up to 8 rows every warp is a team of its own and copies for itself, a
 // page at a time, into one buffer, where the one before has just been used (the other 15 warps are work enough
 // meanwhile; keys' and values' halves in a ring of three 121 us, in two buffers of their own 119), in heads of 64 three
@@ -77,9 +77,13 @@ struct Cache4Args {
     __device__ __forceinline__ long long token(int b, int i) const { return (long long)cu[b] + i; }
     __device__ __forceinline__ long long tokens() const { return N; }
     // A CTA to each head, no merge, but the others idle: where the longest head gives its teams at most
-    // 2 tiles more than an even share. (8 heads of 1000, 2000, 3000 tokens 13.2, 16.7, 20.2 us so,
-    // cut 15.7, 16.5, 14.6; 32 heads 13.8, 17.9, 22.0 and 18.6, 19.4, 17.4; 128 heads of 2000, 4000, 6000
-    // 18.3, 26.3, 36.4 and 20.5, 29.8, 36.6.)
+    // 2 tiles more than an even share. (4 rows, heads of 128: 8 of them of 1000, 2000, 3000 tokens 12.0, 15.3,
+    // 18.6 us so, cut 14.5, 15.9, 14.0; 32 heads 12.4, 15.8, 19.2 and 14.2, 14.7, 15.5; 128 heads of 2000, 4000,
+    // 6000 17.1, 24.4, 34.1 and 19.4, 28.4, 35.3. Heads of 64: 10.2, 12.1, 13.8 and 12.0, 13.2, 11.7; 10.6, 12.4,
+    // 14.5 and 11.8, 12.2, 12.0; 13.4, 17.9, 21.9 and 15.1, 20.5, 22.4. 16 rows, of which a team has its own ring, heads
+    // of 128: 16.1, 21.2, 25.9 and 15.5, 15.9, 15.9; 128 heads 22.1, 32.5, 46.8 and 25.3, 33.9, 47.8; of 64: 11.0, 13.8,
+    // 16.7 and 11.6, 11.4, 11.6; 15.3, 21.0, 27.1 and 17.5, 22.4, 27.1. One rule for all: at worst 3 us off the better;
+    // where the table's width leaves few CTAs 4.5: 8 heads of 3000 tokens in 47 pages 18.5 so, cut 14.0 in a wider table.)
     __device__ __forceinline__ bool by_head(int longest, int N) const {
         const int each = (longest + (1 << lg_teams) - 1) >> lg_teams;
         return each <= kWholeTiles && each * ctas - (N >> lg_teams) <= 2 * ctas;
@@ -1180,8 +1184,9 @@ int gated_sdpa_cache4(const void* X, const void* Q, const gsdpa_cache4* cache, c
     long long grid = sms;   // (no fewer than the heads, where those fit)
     if (grid > most) grid = most;
     a.ctas = (int)grid;
-    // By the table's width, which saves the lengths' lookup and the merge kernel: the same with 2 tiles (8 heads of 1000, 2000,
-    // 3000 tokens 10.5, 14.5, 18.2 us, 32 heads 11.8, 15.9, 19.8, 128 heads of 2000, 4000 15.7, 23.7).
+    // By the table's width, which saves the lengths' lookup and the merge kernel: the same with 2 tiles (4 rows, heads of
+    // 128: 8 heads of 1000, 2000 tokens 9.9, 13.8 us, 32 heads 10.4, 14.0, 128 heads of 2000, 4000 14.9, 22.2; of 64: 8.1, 10.6,
+    // 8.5, 10.8 and 11.4, 16.1).
     const long long heads = (long long)B * a.Hkv, each = (max_pages + sh.teams - 1) / sh.teams;
     const bool whole = heads <= grid && each <= kWholeTiles && each * (sms - heads) <= 2 * sms;
     a.whole = whole;

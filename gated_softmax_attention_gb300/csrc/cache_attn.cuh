@@ -16,7 +16,7 @@
 
 namespace gsdpa {
 
-constexpr int kSlots = 8;            // most teams of a CTA, and warps that share no tokens
+constexpr int kSlots = 8;            // most teams that a copying warp serves (twice as many where each warp copies for itself)
 constexpr int kMaxRows = 128;        // query rows (heads of a group x new tokens) per K/V head
 constexpr int kMaxCtas = 160;        // most CTAs (plan_sms)
 constexpr int kMergeThreads = 512;
@@ -276,7 +276,7 @@ struct Layout {
         if (warp < W) s_place[tid] = before;
         if (tid == 0) s_place[kScan] = N;
         __syncthreads();
-        ctas = max(1, min(a.ctas, N >> a.lg_teams));   // every team has a tile (or there is one CTA)
+        ctas = max(1, min(a.ctas, N >> a.lg_teams));   // every team has a place (or there is one CTA)
         // Short sequences, a CTA for each head: no head is cut between CTAs, whose
         // merge would take longer than the tiles.
         by_head = a.B * (long long)a.Hkv <= a.ctas && a.by_head(longest, N);

@@ -563,7 +563,8 @@ typedef struct {
  *                 none or if the needs up to and with it fit what is free (pages given
  *                 back in this call among it, request after request, in order).
  *   slots       : out, int64 [n_rows], -1 for tokens that were not granted and rows from
- *                 cu[B] on.    positions : out, int32 [n_rows] (there 0), or NULL.
+ *                 cu[B] on.    positions : out, int32 [n_rows], keep and on, granted or not (0 from
+ *                 cu[B] on, and where lens, keep or n_new is out of range), or NULL.
  * lens is not changed: set it to keep + granted once, after the last layer's attention
  * (until then keep is what the attention takes as lens). A request whose numbers are out of range
  * (negative, keep > lens, more than 64 max_pages tokens, rows past n_rows) is left as
@@ -629,7 +630,9 @@ GSDPA_API int gsdpa_cache4_read(const gsdpa_cache4* cache, const long long* slot
  * own keys is seen by the rows that may see it, one among its values by every row of
  * the request.
  * Scores, softmax statistics and sums are float32; queries are exact (bf16; elements
- * under 2^-27 of the row's largest lose bits that weigh less than 2^-35 of it). The
+ * under 2^-31 of the row's largest lose bits that weigh less than 2^-39 of it). Finite queries
+ * have finite scores: where these would leave float32, the largest has all the weight. (A query
+ * with infinities gives NaN, or zero if it makes all scores -infinity.) The
  * weights are rounded to fp16 twice, before and after they take the value's scale, 11 bits
  * each. fp16's range ends at 2^-38 W, W the row's largest product of a weight and a page's
  * largest value scale (rounded up to a power of two, at least 1): a weight is off by no

@@ -115,6 +115,24 @@ def test_values_where_rounding_is_decided(kind):
 
 
 @pytest.mark.parametrize("d", [64, 128])
+def test_the_sign_of_a_zero_code(d):
+    # to the bit, which a comparison of numbers does not see: that of the number, of zeros themselves too; none under a scale of zero
+    g = torch.Generator().manual_seed(5)
+    x = torch.randn(70, 2, d, generator=g) * torch.exp2(torch.randint(-30, 1, (70, 2, d), generator=g).float())
+    x[::3] = torch.where(torch.rand(x[::3].shape, generator=g) < 0.5, -0.0, x[::3])
+    x[5] = -1e-9
+    K = x.bfloat16().cuda()
+    cache = filled(2, 2, d, "e2m1")
+    slots = torch.arange(70, device="cuda") + 3
+    gb.cache4_append(cache, K, -K, slots)
+    k, v, ks, vs = codes_and_scales(cache.pool, slots, "e2m1")
+    assert int(((k == 0) & torch.signbit(k)).sum()) > 100
+    for code, scale, want in ((k, ks, K), (v, vs, -K)):
+        live = (scale > 0).repeat_interleave(GROUP, -1)
+        assert torch.equal(torch.signbit(code), torch.signbit(want) & live)
+
+
+@pytest.mark.parametrize("d", [64, 128])
 def test_the_sign_of_what_becomes_zero(d):
     # e2m1 has a zero of either sign: that of the number, however small it is beside the group's largest
     small = [0.0, 2.0 ** -130, 2.0 ** -40, 2.0 ** -18, 2.0 ** -17, 2.0 ** -16, 2.0 ** -15, 2.0 ** -8, 0.125, 0.2421875, 0.25, 0.2578125]
